@@ -369,6 +369,116 @@ QW3_API int qw3_q8_0_gemm(const void *W_dev, int32_t rows, int32_t cols, const f
                           int32_t M, float *y_dev, void *workspace_dev, int64_t workspace_bytes,
                           void *stream);
 
+/* ---- The 4-bit KV cache ---------------------------------------------------
+ * A cache on a caller's buffer, for callers that run their own layers: rows
+ * are written with the per-head norm and the rotation in the same pass, read
+ * back, and attended over ("A transformer from scratch", 12.3.4, 12.3.5 and
+ * 12.4; minfer 2.2).
+ *
+ * Layout, in bytes: [slot][K|V][kv head]{codes [capacity][head_dim / 2],
+ * scales [capacity][head_dim / 32] f16}: 4.5 bits per value. A row is
+ * head_dim / 32 blocks of 32 values, value i = scale * (code_i - 8). A block's
+ * codes, in order with the even value in the low nibble, are 16 bytes; a K row
+ * interleaves its blocks' 4-byte words ([word 0..3][block]), a V row their
+ * 2-byte halfwords ([halfword 0..7][block]).
+ * Encoder: P = max x, N = max -x over the block, m = P if P >= N else -N,
+ * d = -m / 8, code = clamp(floor(x / d + 8.5), 0, 15) (8 where m = 0), scale =
+ * f16(d) to nearest even, x and d being the exact values (of normalised and
+ * rotated keys too), so that codes do not depend on the order of any sum. A
+ * block that holds NaN, an infinity or a magnitude of 524160 or more is
+ * written as zeros and, if status_dev is not NULL, *status_dev is set to
+ * QW3_ERR_NONFINITE.
+ *
+ * data: 16-byte aligned device memory of qw3_kv_q4_bytes(). slots >= 1;
+ * capacity a multiple of 32; n_kv_heads 1..64; head_dim 64 or 128. The buffer
+ * needs no initialisation: what lies past a sequence's length is not used. */
+typedef struct qw3_kv_q4 {
+    void *data;
+    int32_t slots;
+    int32_t capacity;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+} qw3_kv_q4;
+
+/* Bytes of a cache of these sizes, or -1 if one of them cannot be taken. */
+QW3_API int64_t qw3_kv_q4_bytes(int32_t slots, int32_t capacity, int32_t n_kv_heads, int32_t head_dim);
+
+/* Append M rows. qkv_dev: f32 [M][qkv_stride] (qkv_stride in floats), each row
+ * the raw projections of n_heads query heads, then the key heads, then the
+ * value heads. Queries and keys take x / sqrt(mean(x^2) + eps) * w per head
+ * (q_norm_dev, k_norm_dev: f32 [head_dim]) and the NeoX rotation of their
+ * position with rope_dev (f32 [capacity][head_dim / 2][2]: cos, sin); the
+ * queries go to q_out_dev (f32 [M][q_stride]; may be qkv_dev itself with its
+ * stride), keys and values into the cache.
+ * Row i goes to slot slots_dev[i] (slot0 where slots_dev is NULL) and position
+ * pos_dev[i] (pos0 + i where pos_dev is NULL). A row whose slot or position
+ * from a device array lies outside the cache (a padding row, say -1) is
+ * skipped, its q_out row left as it was; positions given as pos0 must fit
+ * (QW3_ERR_KV_OVERFLOW). No two rows of a call may name the same place.
+ * n_heads a multiple of n_kv_heads. Asynchronous on `stream`. */
+QW3_API int qw3_kv_q4_append(const qw3_kv_q4 *cache, const float *qkv_dev, int32_t M, int64_t qkv_stride,
+                             int32_t n_heads, const float *q_norm_dev, const float *k_norm_dev, float eps,
+                             const float *rope_dev, const int32_t *slots_dev, int32_t slot0, const int32_t *pos_dev,
+                             int32_t pos0, float *q_out_dev, int64_t q_stride, int32_t *status_dev, void *stream);
+
+/* Read M cached rows back as f32: k_out_dev and v_out_dev [M][n_kv_heads]
+ * [head_dim]. Rows are named, and left out, as in qw3_kv_q4_append; here a
+ * place may be named twice. */
+QW3_API int qw3_kv_q4_read(const qw3_kv_q4 *cache, int32_t M, const int32_t *slots_dev, int32_t slot0,
+                           const int32_t *pos_dev, int32_t pos0, float *k_out_dev, float *v_out_dev, void *stream);
+
+/* Workspace bytes of qw3_kv_q4_attn for these sizes (may be 0), or -1 if one
+ * of them cannot be taken. */
+QW3_API int64_t qw3_kv_q4_attn_workspace_bytes(int32_t B, int32_t rows, int32_t n_heads, int32_t n_kv_heads,
+                                               int32_t head_dim, int32_t max_len);
+
+/* Grouped-query causal attention of `rows` query rows (1..16) of each of B
+ * sequences over the cache: q_dev f32 [B * rows][q_stride] (normalised and
+ * rotated), out_dev f32 [B * rows][out_stride], n_heads * head_dim values
+ * each; query head h reads kv head h / (n_heads / n_kv_heads), a group of at
+ * most 16. Sequence b lies in slot slots_dev[b] (slot b where slots_dev is
+ * NULL) and holds lens_dev[b] positions, its `rows` newest among them: row t
+ * is at position p = lens_dev[b] - rows + t and attends positions 0..p,
+ *     out = sum_j softmax_j(scale * q . K[j]) V[j].
+ * A row with p < 0, and every row of a sequence whose slot lies outside the
+ * cache, is written as zeros. Lengths are read on the device and taken as at
+ * most max_len (<= capacity), which decides how the work is split: an upper
+ * bound close to the longest sequence is best. The sums are f32; results are
+ * within f32 reassociation error of the exact ones and the same in every call.
+ * workspace_dev: 16-byte aligned, qw3_kv_q4_attn_workspace_bytes() or more, of
+ * any content, not used by another call until this one has completed (two
+ * graphs that may run at once need a workspace each). Asynchronous on
+ * `stream`. */
+QW3_API int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride, int32_t n_heads,
+                           const int32_t *slots_dev, const int32_t *lens_dev, int32_t B, int32_t rows,
+                           int32_t max_len, float scale, float *out_dev, int64_t out_stride, void *workspace_dev,
+                           int64_t workspace_bytes, void *stream);
+
+/* ---- Sampling --------------------------------------------------------------
+ * One token from each of B rows of logits (f32 [B][stride], V values used,
+ * 1 <= V <= 4194304), beside the greedy argmax of "A transformer from
+ * scratch", 12.6. With w_i = exp((l_i - max l) / temperature) and the tokens
+ * ordered by (l descending, index ascending), in this order:
+ *   top-k  keeps the first top_k tokens (all if top_k <= 0);
+ *   top-p  keeps the shortest prefix whose w reach top_p times their sum, one
+ *          token at least (all if top_p >= 1);
+ *   min-p  keeps the tokens with w >= min(min_p, 1).
+ * The token is the first, in index order, whose running sum of kept w exceeds
+ * u times their total; prob_dev (nullable) takes its w over that total. The
+ * four settings are device arrays [B], each nullable: temperature 1, no top-k,
+ * no top-p, no min-p. A temperature <= 0 is greedy (lowest index among equal
+ * maxima, probability 1). u_dev: [B] in [0, 1), values outside taken as the
+ * nearest inside. A -inf logit is never drawn.
+ * Weights are summed in 64-bit fixed point (2^-40 of the largest), so equal
+ * inputs give equal tokens; a token whose weight is below 2^-41 of the largest
+ * is not drawn. A row with a NaN, with no logit above -inf, with a +inf
+ * (unless greedy) or with a temperature that is NaN or infinite gets token -1
+ * and probability 0 and, if status_dev is not NULL, sets *status_dev to
+ * QW3_ERR_NONFINITE. Asynchronous on `stream`. */
+QW3_API int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, const float *temperature_dev,
+                       const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+                       int32_t *token_dev, float *prob_dev, int32_t *status_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

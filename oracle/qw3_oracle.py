@@ -427,6 +427,86 @@ def argmax_lowest(logits: np.ndarray) -> int:
 
 
 # ---------------------------------------------------------------------------
+# The 4-bit KV cache rows
+# ---------------------------------------------------------------------------
+
+def kv_q4_encode(x: np.ndarray):
+    """(codes [..., d] int, scales [..., d/32] f16) of rows x [..., d] taken in
+    f64: per block of 32, m the value of largest magnitude (the positive one of
+    two opposite equals), d = -m / 8, code = clamp(floor(x / d + 8.5), 0, 15),
+    8 throughout where m = 0; the scale is d rounded once to f16."""
+    b = np.asarray(x, np.float64).reshape(*np.shape(x)[:-1], -1, 32)
+    hi, lo = b.max(-1), b.min(-1)
+    m = np.where(hi >= -lo, hi, lo)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        code = np.where(m[..., None] == 0, 8.0, np.clip(np.floor(-8.0 * b / m[..., None] + 8.5), 0, 15))
+    return code.astype(np.int32).reshape(np.shape(x)), (m / -8.0).astype(np.float16)
+
+
+def kv_q4_decode(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """scale * (code - 8), exact in f32."""
+    return (np.repeat(scales.astype(np.float32), 32, axis=-1) * (np.asarray(codes) - 8).astype(np.float32))
+
+
+def kv_q4_row_bytes(codes: np.ndarray, value_row: bool) -> np.ndarray:
+    """Code bytes [..., d/2] of rows of codes [..., d]: byte j of block b holds
+    values 2j (low nibble) and 2j + 1; a K row lists the blocks' words of 4
+    bytes word by word, a V row their halfwords of 2."""
+    u = 2 if value_row else 4
+    c = np.asarray(codes).reshape(*np.shape(codes)[:-1], -1, 16, 2)
+    byte = (c[..., 0] | (c[..., 1] << 4)).astype(np.uint8)          # [..., nb, 16]
+    nb = byte.shape[-2]
+    out = np.empty(byte.shape[:-2] + (16 * nb,), np.uint8)
+    for b in range(nb):
+        for j in range(16):
+            out[..., (j // u * nb + b) * u + j % u] = byte[..., b, j]
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Sampling
+# ---------------------------------------------------------------------------
+
+def sample_token(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, probability, margin) of one row, in f64: w = exp((l - max) / T);
+    tokens ordered by (l descending, index ascending); the first top_k; the
+    shortest prefix whose sum reaches top_p times theirs (one at least); those
+    with w >= min_p; the first index whose running sum of kept w exceeds u times
+    their total. margin: how near, relative to a total, any of these decisions
+    comes to going the other way."""
+    lg = np.asarray(logits, np.float64)
+    if np.isnan(lg).any() or not (lg > -np.inf).any():
+        raise NonFiniteValue("no token to draw")
+    if temperature <= 0:
+        return argmax_lowest(lg), 1.0, 1.0
+    if np.isposinf(lg).any():
+        raise NonFiniteValue("+inf logit")
+    margin = 1.0
+    order = np.argsort(-lg, kind="stable")
+    if 0 < top_k < lg.size:
+        order = order[:top_k]
+    w = np.exp((lg[order] - lg[order[0]]) / float(temperature))
+    if top_p < 1.0:
+        c, goal = np.cumsum(w), float(top_p) * w.sum()
+        n = int(np.argmax(c >= goal)) + 1
+        margin = min(margin, abs(c[n - 1] - goal) / w.sum(), abs(c[n - 1] - w[n - 1] - goal) / w.sum() if n > 1 else 1.0)
+        order, w = order[:n], w[:n]
+    if min_p > 0:
+        edge = np.abs(w[1:] / min(float(min_p), 1.0) - 1.0)
+        margin = min(margin, float(edge.min()) if edge.size and min_p < 1 else 1.0)
+        keep = (w >= min(float(min_p), 1.0)) | (np.arange(w.size) == 0)
+        order, w = order[keep], w[keep]
+    by = np.argsort(order)
+    order, w = order[by], w[by]
+    c = np.cumsum(w)
+    goal = min(max(float(u), 0.0), 1.0) * c[-1]
+    i = min(int(np.searchsorted(c, goal, side="right")), int(np.flatnonzero(w)[-1]))
+    margin = min(margin, abs(c[i] - goal) / c[-1] if goal < c[-1] else 1.0,
+                 abs(c[i] - w[i] - goal) / c[-1] if goal > 0 else 1.0)
+    return int(order[i]), float(w[i] / c[-1]), float(margin)
+
+
+# ---------------------------------------------------------------------------
 # Linear layers over dequantised Q8_0 weights
 # ---------------------------------------------------------------------------
 
@@ -543,14 +623,15 @@ class KvCache:
     LLM stack", 13.4; 12.4): each (position, kv head) row is stored as
     head_dim/32 Q8_0 blocks by the 11.7 encoder (codes in kq/vq, f16 scales
     in kd/vd; k and v hold the dequantised rows f32(d) * q that every reader
-    sees). head_dim must be a multiple of 32.
+    sees); or "q4": rows of 4-bit blocks (kv_q4_encode), k and v holding the
+    dequantised rows. head_dim must be a multiple of 32.
     """
 
     def __init__(self, n_layers: int, n_kv_heads: int, head_dim: int, capacity: int, dtype: str = "f32"):
-        if dtype not in ("f32", "f16", "q8_0"):
+        if dtype not in ("f32", "f16", "q8_0", "q4"):
             raise InvalidShape(f"KV cache dtype {dtype!r}")
-        if dtype == "q8_0" and head_dim % QK8_0:
-            raise InvalidShape(f"a q8_0 KV cache needs head_dim % {QK8_0} == 0, got {head_dim}")
+        if dtype in ("q8_0", "q4") and head_dim % QK8_0:
+            raise InvalidShape(f"a {dtype} KV cache needs head_dim % {QK8_0} == 0, got {head_dim}")
         self.capacity = capacity
         self.dtype = dtype
         np_t = np.float16 if dtype == "f16" else np.float32
@@ -582,6 +663,8 @@ class KvCache:
             self._store_q8(self.kq, self.kd, self.k, layer, k_rows)
             self._store_q8(self.vq, self.vd, self.v, layer, v_rows)
             return
+        if self.dtype == "q4":
+            k_rows, v_rows = (kv_q4_decode(*kv_q4_encode(np.asarray(r, np.float32))) for r in (k_rows, v_rows))
         # numpy's f32 -> f16 conversion rounds to nearest even
         self.k[layer, self.len:self.len + m] = np.asarray(k_rows, np.float32).astype(self.k.dtype)
         self.v[layer, self.len:self.len + m] = np.asarray(v_rows, np.float32).astype(self.v.dtype)

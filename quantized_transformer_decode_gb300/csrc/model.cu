@@ -1274,4 +1274,140 @@ int qw3_q8_0_gemv_q8act(const void *W_dev, int32_t rows, int32_t cols, const flo
     return QW3_OK;
 }
 
+namespace {
+
+constexpr int kQ4MaxRows = 16, kQ4MaxGroup = 16;
+
+// Checks of a 4-bit cache and of a head count over it.
+int check_kv_q4(const qw3_kv_q4 *c, int n_heads) {
+    if (!c || !c->data) return fail(nullptr, QW3_ERR_INVALID_ARG, "null cache");
+    if (qw3_kv_q4_bytes(c->slots, c->capacity, c->n_kv_heads, c->head_dim) < 0)
+        return fail(nullptr, QW3_ERR_SHAPE,
+                    "a cache needs slots >= 1, capacity % 32 == 0, 1 to 64 kv heads and head_dim 64 or 128");
+    if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads / c->n_kv_heads > kQ4MaxGroup)
+        return fail(nullptr, QW3_ERR_SHAPE, "n_heads must be 1 to 16 times n_kv_heads");
+    if (misaligned(c->data, 16)) return fail(nullptr, QW3_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
+    return QW3_OK;
+}
+
+// Checks of the rows that a call names; the host-given places must fit.
+int check_kv_q4_rows(const qw3_kv_q4 *c, int32_t M, const int32_t *slots_dev, int32_t slot0, const int32_t *pos_dev,
+                     int32_t pos0) {
+    if (M < 0) return fail(nullptr, QW3_ERR_INVALID_ARG, "a negative row count");
+    if (misaligned(slots_dev, 4) || misaligned(pos_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "slots and positions must be 4-byte aligned");
+    if (!slots_dev && (slot0 < 0 || slot0 >= c->slots)) return fail(nullptr, QW3_ERR_INVALID_ARG, "slot out of range");
+    if (!pos_dev && pos0 < 0) return fail(nullptr, QW3_ERR_INVALID_ARG, "a negative position");
+    if (!pos_dev && static_cast<int64_t>(pos0) + M > c->capacity)
+        return fail(nullptr, QW3_ERR_KV_OVERFLOW, "rows past the cache's capacity");
+    return QW3_OK;
+}
+
+KvQ4 kv_q4_view(const qw3_kv_q4 *c) {
+    KvQ4 v;
+    v.data = static_cast<uint8_t *>(c->data);
+    v.slots = c->slots;
+    v.cap = c->capacity;
+    v.nkv = c->n_kv_heads;
+    return v;
+}
+
+}  // namespace
+
+int64_t qw3_kv_q4_bytes(int32_t slots, int32_t capacity, int32_t n_kv_heads, int32_t head_dim) {
+    if (slots < 1 || capacity < 32 || capacity % 32 || n_kv_heads < 1 || n_kv_heads > 64 ||
+        (head_dim != 64 && head_dim != 128))
+        return -1;
+    // at most 2^31 slots * 2 * 64 heads * 2^31 positions * 72 bytes: check that it fits
+    const double total = 2.0 * slots * n_kv_heads * static_cast<double>(kv_q4_head_bytes(capacity, head_dim));
+    if (total > 9.0e18) return -1;
+    return static_cast<int64_t>(2 * static_cast<size_t>(slots) * n_kv_heads * kv_q4_head_bytes(capacity, head_dim));
+}
+
+int qw3_kv_q4_append(const qw3_kv_q4 *cache, const float *qkv_dev, int32_t M, int64_t qkv_stride, int32_t n_heads,
+                     const float *q_norm_dev, const float *k_norm_dev, float eps, const float *rope_dev,
+                     const int32_t *slots_dev, int32_t slot0, const int32_t *pos_dev, int32_t pos0, float *q_out_dev,
+                     int64_t q_stride, int32_t *status_dev, void *stream) {
+    if (int rc = check_kv_q4(cache, n_heads)) return rc;
+    if (int rc = check_kv_q4_rows(cache, M, slots_dev, slot0, pos_dev, pos0)) return rc;
+    if (!q_norm_dev || !k_norm_dev || !rope_dev || (M > 0 && (!qkv_dev || !q_out_dev)))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "null append arguments");
+    if (!(eps >= 0.0f)) return fail(nullptr, QW3_ERR_INVALID_ARG, "eps must be >= 0");
+    const int64_t qw = static_cast<int64_t>(n_heads) * cache->head_dim;
+    if (qkv_stride < qw + 2ll * cache->n_kv_heads * cache->head_dim || q_stride < qw)
+        return fail(nullptr, QW3_ERR_SHAPE, "a row stride is shorter than its heads");
+    if (misaligned(qkv_dev, 4) || misaligned(q_norm_dev, 4) || misaligned(k_norm_dev, 4) || misaligned(rope_dev, 8) ||
+        misaligned(q_out_dev, 4) || misaligned(status_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "rope must be 8-byte, the other buffers 4-byte aligned");
+    KvQ4Rows rows{slots_dev, slot0, pos_dev, pos0};
+    QW3_CUDA_TRY(launch_kv_q4_append(qkv_dev, M, qkv_stride, q_norm_dev, k_norm_dev, eps,
+                                     reinterpret_cast<const float2 *>(rope_dev), kv_q4_view(cache), cache->head_dim,
+                                     rows, n_heads, q_out_dev, q_stride, status_dev, static_cast<cudaStream_t>(stream)));
+    return QW3_OK;
+}
+
+int qw3_kv_q4_read(const qw3_kv_q4 *cache, int32_t M, const int32_t *slots_dev, int32_t slot0, const int32_t *pos_dev,
+                   int32_t pos0, float *k_out_dev, float *v_out_dev, void *stream) {
+    if (int rc = check_kv_q4(cache, cache ? cache->n_kv_heads : 1)) return rc;
+    if (int rc = check_kv_q4_rows(cache, M, slots_dev, slot0, pos_dev, pos0)) return rc;
+    if (M > 0 && (!k_out_dev || !v_out_dev)) return fail(nullptr, QW3_ERR_INVALID_ARG, "null read arguments");
+    if (misaligned(k_out_dev, 4) || misaligned(v_out_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "outputs must be 4-byte aligned");
+    KvQ4Rows rows{slots_dev, slot0, pos_dev, pos0};
+    QW3_CUDA_TRY(launch_kv_q4_read(kv_q4_view(cache), cache->head_dim, rows, M, k_out_dev, v_out_dev,
+                                   static_cast<cudaStream_t>(stream)));
+    return QW3_OK;
+}
+
+int64_t qw3_kv_q4_attn_workspace_bytes(int32_t B, int32_t rows, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                       int32_t max_len) {
+    if (B < 0 || rows < 1 || rows > kQ4MaxRows || n_kv_heads < 1 || n_kv_heads > 64 || n_heads < 1 ||
+        n_heads % n_kv_heads || n_heads / n_kv_heads > kQ4MaxGroup || (head_dim != 64 && head_dim != 128) || max_len < 0)
+        return -1;
+    return static_cast<int64_t>(kv_q4_attn_workspace_bytes(B, rows, n_heads, n_kv_heads, head_dim, max_len));
+}
+
+int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride, int32_t n_heads,
+                   const int32_t *slots_dev, const int32_t *lens_dev, int32_t B, int32_t rows, int32_t max_len,
+                   float scale, float *out_dev, int64_t out_stride, void *workspace_dev, int64_t workspace_bytes,
+                   void *stream) {
+    if (int rc = check_kv_q4(cache, n_heads)) return rc;
+    if (B < 0 || rows < 1 || rows > kQ4MaxRows) return fail(nullptr, QW3_ERR_INVALID_ARG, "1 to 16 rows per sequence");
+    if (max_len < 0) return fail(nullptr, QW3_ERR_INVALID_ARG, "a negative max_len");
+    if (max_len > cache->capacity) return fail(nullptr, QW3_ERR_KV_OVERFLOW, "max_len past the cache's capacity");
+    if (B > 0 && (!q_dev || !lens_dev || !out_dev)) return fail(nullptr, QW3_ERR_INVALID_ARG, "null attention arguments");
+    const int64_t qw = static_cast<int64_t>(n_heads) * cache->head_dim;
+    if (q_stride < qw || out_stride < qw) return fail(nullptr, QW3_ERR_SHAPE, "a row stride is shorter than its heads");
+    if (misaligned(q_dev, 4) || misaligned(out_dev, 4) || misaligned(slots_dev, 4) || misaligned(lens_dev, 4) ||
+        misaligned(workspace_dev, 16))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "the workspace must be 16-byte, the other buffers 4-byte aligned");
+    if (!(scale - scale == 0.0f)) return fail(nullptr, QW3_ERR_INVALID_ARG, "scale must be finite");
+    if (B == 0) return QW3_OK;
+    const int64_t need = qw3_kv_q4_attn_workspace_bytes(B, rows, n_heads, cache->n_kv_heads, cache->head_dim, max_len);
+    if (need > 0 && (!workspace_dev || workspace_bytes < need))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "workspace too small");
+    KvQ4AttnArgs a{};
+    a.q = q_dev; a.q_stride = q_stride; a.c = kv_q4_view(cache); a.slots = slots_dev; a.lens = lens_dev;
+    a.B = B; a.rows = rows; a.max_len = max_len; a.nh = n_heads; a.scale = scale;
+    a.out = out_dev; a.out_stride = out_stride; a.ws = static_cast<float *>(workspace_dev);
+    QW3_CUDA_TRY(launch_kv_q4_attn(a, cache->head_dim, static_cast<cudaStream_t>(stream)));
+    return QW3_OK;
+}
+
+int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, const float *temperature_dev,
+               const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+               int32_t *token_dev, float *prob_dev, int32_t *status_dev, void *stream) {
+    if (B < 0 || (B > 0 && (!logits_dev || !u_dev || !token_dev)))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "bad sample arguments");
+    if (V < 1 || V > (1 << 22) || stride < V) return fail(nullptr, QW3_ERR_SHAPE, "1 <= V <= 4194304, V <= stride");
+    if (misaligned(logits_dev, 4) || misaligned(temperature_dev, 4) || misaligned(top_k_dev, 4) ||
+        misaligned(top_p_dev, 4) || misaligned(min_p_dev, 4) || misaligned(u_dev, 4) || misaligned(token_dev, 4) ||
+        misaligned(prob_dev, 4) || misaligned(status_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "device buffers must be 4-byte aligned");
+    SampleArgs a{logits_dev, stride, V, temperature_dev, top_k_dev, top_p_dev, min_p_dev, u_dev, token_dev, prob_dev,
+                 status_dev};
+    QW3_CUDA_TRY(launch_sample(a, B, static_cast<cudaStream_t>(stream)));
+    return QW3_OK;
+}
+
 }  // extern "C"

@@ -255,6 +255,62 @@ cudaError_t launch_copy_kv_rows(const void *kv_layer_seq, size_t kvsel_stride, s
                                 int pos0, int n, int nkv, int hd, float *k_out, float *v_out, int kvtype,
                                 cudaStream_t s);
 
+// ---- the 4-bit KV cache (kv_q4.cu holds its layout)
+struct KvQ4 {
+    uint8_t *data = nullptr;
+    int slots = 0, cap = 0, nkv = 0;
+};
+
+// Bytes of one head's positions, codes and scales; cap a multiple of 32.
+__host__ __device__ inline size_t kv_q4_head_bytes(int cap, int hd) {
+    return static_cast<size_t>(cap) * (hd / 2 + hd / 16);
+}
+
+// (slot, position) of each row of a call: from device arrays where they are
+// given, else slot0 and pos0 + row. A row outside the cache is left out.
+struct KvQ4Rows {
+    const int32_t *slots = nullptr;
+    int slot0 = 0;
+    const int32_t *pos = nullptr;
+    int pos0 = 0;
+};
+
+cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, const float *q_norm, const float *k_norm,
+                                float eps, const float2 *rope, const KvQ4 &c, int hd, const KvQ4Rows &rows, int nh,
+                                float *q_out, int64_t q_stride, int32_t *status, cudaStream_t s);
+cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M, float *k_out, float *v_out,
+                              cudaStream_t s);
+
+struct KvQ4AttnArgs {
+    const float *q;   // [B * rows][q_stride], nh heads of hd
+    int64_t q_stride;
+    KvQ4 c;
+    const int32_t *slots;   // nullable: sequence b in slot b
+    const int32_t *lens;    // [B] positions in the cache, the rows' own among them
+    int B, rows, max_len, nh;
+    float scale;
+    float *out;
+    int64_t out_stride;
+    float *ws;
+};
+size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len);
+cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, cudaStream_t s);
+
+// ---- sampling (sample.cu)
+struct SampleArgs {
+    const float *logits;   // [B][stride]
+    int64_t stride;
+    int V;
+    const float *temperature;   // the four nullable, [B]
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    const float *u;   // [B]
+    int32_t *token;   // [B]
+    float *prob;      // nullable [B]
+    int32_t *status;
+};
+cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s);
+
 }  // namespace qw3
 
 // ------------------------------------------------------------ device PTX
@@ -440,6 +496,21 @@ __device__ __forceinline__ float kv_elem(const kvq8 *row, int d) {
     const uint8_t *blk = &row->b + (d >> 5) * 34;
     const float sc = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(blk)));
     return sc * static_cast<float>(static_cast<int8_t>(blk[2 + (d & 31)]));
+}
+
+// ---- the 4-bit KV cache: a head's code plane and scale plane
+template <int HD>
+__device__ __forceinline__ uint8_t *kv_q4_codes(const KvQ4 &c, int slot, int sel, int g) {
+    return c.data + ((static_cast<size_t>(slot) * 2 + sel) * c.nkv + g) * kv_q4_head_bytes(c.cap, HD);
+}
+template <int HD>
+__device__ __forceinline__ __half *kv_q4_scales(const KvQ4 &c, int slot, int sel, int g) {
+    return reinterpret_cast<__half *>(kv_q4_codes<HD>(c, slot, sel, g) + static_cast<size_t>(c.cap) * (HD / 2));
+}
+__device__ __forceinline__ bool kv_q4_row(const KvQ4 &c, const KvQ4Rows &r, int row, int &slot, int &pos) {
+    slot = r.slots ? r.slots[row] : r.slot0;
+    pos = r.pos ? r.pos[row] : r.pos0 + row;
+    return slot >= 0 && slot < c.slots && pos >= 0 && pos < c.cap;
 }
 
 // ---- Q4_K block decode ("Model files and quantization", 11.8; layout in q4k.cu)

@@ -46,6 +46,8 @@ EXPORTS = (
     "qw3_q8_0_quantize", "qw3_q8_0_dequantize", "qw3_q8_0_gemv", "qw3_q8_0_gemv_q8act",
     "qw3_q4_k_quantize", "qw3_q4_k_dequantize", "qw3_q4_k_gemv", "qw3_q8_0_gemv_splitk_noalloc",
     "qw3_q8_0_gemm_workspace_bytes", "qw3_q8_0_gemm",
+    "qw3_kv_q4_bytes", "qw3_kv_q4_append", "qw3_kv_q4_read", "qw3_kv_q4_attn_workspace_bytes", "qw3_kv_q4_attn",
+    "qw3_sample",
 )
 
 
@@ -72,6 +74,12 @@ class Qw3Weights(ctypes.Structure):
     ]
 
 
+class Qw3KvQ4(ctypes.Structure):
+    """A 4-bit KV cache on a device buffer."""
+    _fields_ = [("data", ctypes.c_void_p), ("slots", ctypes.c_int32), ("capacity", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 class Qw3Error(RuntimeError):
     """A libqw3 call returned a non-zero status."""
 
@@ -85,6 +93,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -123,6 +132,14 @@ def lib() -> ctypes.CDLL:
         "qw3_q8_0_gemv_splitk_noalloc": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _P]),
         "qw3_q8_0_gemm_workspace_bytes": (_I64, [_I32, _I32, _I32]),
         "qw3_q8_0_gemm": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _P, _I64, _P]),
+        "qw3_kv_q4_bytes": (_I64, [_I32, _I32, _I32, _I32]),
+        "qw3_kv_q4_append": (ctypes.c_int, [ctypes.POINTER(Qw3KvQ4), _P, _I32, _I64, _I32, _P, _P, _F32, _P, _P, _I32,
+                                            _P, _I32, _P, _I64, _P, _P]),
+        "qw3_kv_q4_read": (ctypes.c_int, [ctypes.POINTER(Qw3KvQ4), _I32, _P, _I32, _P, _I32, _P, _P, _P]),
+        "qw3_kv_q4_attn_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32, _I32]),
+        "qw3_kv_q4_attn": (ctypes.c_int, [ctypes.POINTER(Qw3KvQ4), _P, _I64, _I32, _P, _P, _I32, _I32, _I32, _F32, _P,
+                                          _I64, _P, _I64, _P]),
+        "qw3_sample": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -268,6 +285,44 @@ def qw3_q8_0_gemm(W_ptr: int, rows: int, cols: int, x_ptr: int, M: int, y_ptr: i
     _check(lib().qw3_q8_0_gemm(W_ptr, rows, cols, x_ptr, M, y_ptr, ws_ptr or None, ws_bytes, stream or None))
 
 
+def qw3_kv_q4_bytes(slots: int, capacity: int, n_kv_heads: int, head_dim: int) -> int:
+    return lib().qw3_kv_q4_bytes(slots, capacity, n_kv_heads, head_dim)
+
+
+def qw3_kv_q4_append(cache: Qw3KvQ4, qkv_ptr: int, M: int, qkv_stride: int, n_heads: int, q_norm_ptr: int,
+                     k_norm_ptr: int, eps: float, rope_ptr: int, slots_ptr: int, slot0: int, pos_ptr: int, pos0: int,
+                     q_out_ptr: int, q_stride: int, status_ptr: int = 0, stream: int = 0) -> None:
+    _check(lib().qw3_kv_q4_append(cache, qkv_ptr or None, M, qkv_stride, n_heads, q_norm_ptr or None,
+                                  k_norm_ptr or None, eps, rope_ptr or None, slots_ptr or None, slot0, pos_ptr or None,
+                                  pos0, q_out_ptr or None, q_stride, status_ptr or None, stream or None))
+
+
+def qw3_kv_q4_read(cache: Qw3KvQ4, M: int, slots_ptr: int, slot0: int, pos_ptr: int, pos0: int, k_ptr: int, v_ptr: int,
+                   stream: int = 0) -> None:
+    _check(lib().qw3_kv_q4_read(cache, M, slots_ptr or None, slot0, pos_ptr or None, pos0, k_ptr or None, v_ptr or None,
+                                stream or None))
+
+
+def qw3_kv_q4_attn_workspace_bytes(B: int, rows: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                   max_len: int) -> int:
+    return lib().qw3_kv_q4_attn_workspace_bytes(B, rows, n_heads, n_kv_heads, head_dim, max_len)
+
+
+def qw3_kv_q4_attn(cache: Qw3KvQ4, q_ptr: int, q_stride: int, n_heads: int, slots_ptr: int, lens_ptr: int, B: int,
+                   rows: int, max_len: int, scale: float, out_ptr: int, out_stride: int, ws_ptr: int, ws_bytes: int,
+                   stream: int = 0) -> None:
+    _check(lib().qw3_kv_q4_attn(cache, q_ptr or None, q_stride, n_heads, slots_ptr or None, lens_ptr or None, B, rows,
+                                max_len, scale, out_ptr or None, out_stride, ws_ptr or None, ws_bytes, stream or None))
+
+
+def qw3_sample(logits_ptr: int, stride: int, B: int, V: int, temperature_ptr: int, top_k_ptr: int, top_p_ptr: int,
+               min_p_ptr: int, u_ptr: int, token_ptr: int, prob_ptr: int = 0, status_ptr: int = 0,
+               stream: int = 0) -> None:
+    _check(lib().qw3_sample(logits_ptr or None, stride, B, V, temperature_ptr or None, top_k_ptr or None,
+                            top_p_ptr or None, min_p_ptr or None, u_ptr or None, token_ptr or None, prob_ptr or None,
+                            status_ptr or None, stream or None))
+
+
 # ---------------------------------------------------------- torch wrapper
 
 def _torch():
@@ -356,6 +411,143 @@ def q4_k_gemv(W, rows: int, cols: int, x):
     y = torch.empty((B, rows), dtype=torch.float32, device=x.device)
     qw3_q4_k_gemv(W.data_ptr(), rows, cols, x.data_ptr(), B, y.data_ptr(), _stream_ptr())
     return y
+
+
+def _on(device, dtype, **tensors):
+    """Check that each given tensor lies on `device` as contiguous values of `dtype`."""
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous()):
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a contiguous {dtype} tensor on {device} is wanted")
+
+
+def _rows_of(t, name: str):
+    """(rows, stride) of a 2-d tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a 2-d tensor with contiguous rows is wanted")
+    return t.shape[0], t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+class KVCacheQ4:
+    """A 4-bit KV cache of `slots` sequences (qw3_kv_q4): rows appended from
+    raw q/k/v projections, read back, attended over. Every call runs on torch's
+    current stream of the cache's device."""
+
+    def __init__(self, slots: int, capacity: int, n_kv_heads: int, head_dim: int, data=None, device="cuda"):
+        torch = _torch()
+        n = qw3_kv_q4_bytes(slots, capacity, n_kv_heads, head_dim)
+        if n < 0:
+            raise Qw3Error(QW3_ERR_SHAPE, "slots >= 1, capacity % 32 == 0, 1 to 64 kv heads, head_dim 64 or 128")
+        if data is None:
+            data = torch.empty(n, dtype=torch.uint8, device=device)
+        elif data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous() or data.numel() < n:
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"data: a contiguous CUDA uint8 tensor of {n} bytes is wanted")
+        self.data, self.device = data, data.device
+        self.slots, self.capacity, self.n_kv_heads, self.head_dim = slots, capacity, n_kv_heads, head_dim
+        self.c = Qw3KvQ4(data.data_ptr(), slots, capacity, n_kv_heads, head_dim)
+
+    def _places(self, M, slots, pos, slot, first):
+        _on(self.device, _torch().int32, slots=slots, pos=pos)
+        for t in (slots, pos):
+            if t is not None and t.numel() != M:
+                raise Qw3Error(QW3_ERR_SHAPE, f"slots and pos hold one place for each of {M} rows")
+        return slots.data_ptr() if slots is not None else 0, slot, pos.data_ptr() if pos is not None else 0, first
+
+    def append(self, qkv, q_norm, k_norm, eps: float, rope, slots=None, pos=None, slot: int = 0, first: int = 0,
+               status=None):
+        """Norm, rotate and append M rows; returns the rotated queries
+        [M, n_heads, head_dim]. qkv: f32 [M, (n_heads + 2 n_kv_heads) * head_dim]
+        (rows may be strided); rope: f32 [capacity, head_dim / 2, 2]. Row i goes
+        to (slots[i], pos[i]), int32 tensors, or to (slot, first + i). A row
+        outside the cache is skipped and its queries are zero."""
+        torch = _torch()
+        M, stride = _rows_of(qkv, "qkv")
+        hd = self.head_dim
+        n_heads = qkv.shape[1] // hd - 2 * self.n_kv_heads
+        if qkv.dtype != torch.float32 or qkv.device != self.device or qkv.shape[1] % hd or n_heads < 1:
+            raise Qw3Error(QW3_ERR_SHAPE, "qkv: f32 rows of n_heads + 2 n_kv_heads heads on the cache's device")
+        _on(self.device, torch.float32, q_norm=q_norm, k_norm=k_norm, rope=rope)
+        _on(self.device, torch.int32, status=status)
+        if q_norm.numel() != hd or k_norm.numel() != hd or rope.numel() != self.capacity * hd:
+            raise Qw3Error(QW3_ERR_SHAPE, "q_norm and k_norm hold head_dim values, rope capacity * head_dim")
+        places = self._places(M, slots, pos, slot, first)
+        new = torch.zeros if slots is not None or pos is not None else torch.empty
+        with torch.cuda.device(self.device):
+            q = new((M, n_heads, hd), dtype=torch.float32, device=self.device)
+            qw3_kv_q4_append(self.c, qkv.data_ptr(), M, stride, n_heads, q_norm.data_ptr(), k_norm.data_ptr(), eps,
+                             rope.data_ptr(), *places, q.data_ptr(), n_heads * hd,
+                             status.data_ptr() if status is not None else 0, _stream_ptr())
+        return q
+
+    def read(self, slots=None, pos=None, slot: int = 0, first: int = 0, n: Optional[int] = None):
+        """Rows back as f32: (k, v), each [M, n_kv_heads, head_dim]; the places
+        as in append, M from slots or pos, else n. Rows outside the cache are
+        zero."""
+        torch = _torch()
+        M = n if n is not None else next((t.numel() for t in (slots, pos) if t is not None), None)
+        if M is None or M < 0:
+            raise Qw3Error(QW3_ERR_INVALID_ARG, "read needs slots, pos or n")
+        places = self._places(M, slots, pos, slot, first)
+        new = torch.zeros if slots is not None or pos is not None else torch.empty
+        with torch.cuda.device(self.device):
+            k, v = new((2, M, self.n_kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
+            qw3_kv_q4_read(self.c, M, *places, k.data_ptr(), v.data_ptr(), _stream_ptr())
+        return k, v
+
+    def attention(self, q, lens, rows: int = 1, slots=None, max_len: Optional[int] = None,
+                  scale: Optional[float] = None, out=None, workspace=None):
+        """Attention of q [B * rows, n_heads, head_dim] (f32, contiguous) over
+        the first lens[b] positions (int32 [B]) of slot slots[b] (int32 [B],
+        else slot b); returns the same shape. max_len: an upper bound of lens
+        (the capacity where it is not given). scale: 1 / sqrt(head_dim) where it
+        is not given. workspace: a uint8 tensor to use in place of a new one."""
+        torch = _torch()
+        B = lens.numel()
+        _on(self.device, torch.float32, q=q, out=out)
+        _on(self.device, torch.int32, lens=lens, slots=slots)
+        if q.dim() != 3 or q.shape[0] != B * rows or q.shape[2] != self.head_dim:
+            raise Qw3Error(QW3_ERR_SHAPE, f"q: [{B * rows}, n_heads, {self.head_dim}] is wanted")
+        if (slots is not None and slots.numel() != B) or (out is not None and out.shape != q.shape):
+            raise Qw3Error(QW3_ERR_SHAPE, "slots holds one slot per sequence, out has q's shape")
+        if slots is None and B > self.slots:
+            raise Qw3Error(QW3_ERR_SHAPE, "more sequences than slots")
+        n_heads, w = q.shape[1], q.shape[1] * self.head_dim
+        max_len = self.capacity if max_len is None else max_len
+        need = qw3_kv_q4_attn_workspace_bytes(B, rows, n_heads, self.n_kv_heads, self.head_dim, max_len)
+        with torch.cuda.device(self.device):
+            out = torch.empty_like(q) if out is None else out
+            if workspace is None and need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            _on(self.device, torch.uint8, workspace=workspace)
+            qw3_kv_q4_attn(self.c, q.data_ptr(), w, n_heads, slots.data_ptr() if slots is not None else 0,
+                           lens.data_ptr(), B, rows, max_len,
+                           self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), w,
+                           workspace.data_ptr() if workspace is not None else 0,
+                           workspace.numel() if workspace is not None else 0, _stream_ptr())
+        return out
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, status=None):
+    """One token per row of CUDA f32 logits [B, V] (rows may be strided) from
+    uniform numbers u [B] (qw3_sample): (tokens int32 [B], probabilities f32
+    [B]). temperature, top_p, min_p: f32 [B]; top_k: int32 [B]; each may be
+    left out."""
+    torch = _torch()
+    B, stride = _rows_of(logits, "logits")
+    dev = logits.device
+    if logits.dtype != torch.float32 or not logits.is_cuda:
+        raise Qw3Error(QW3_ERR_INVALID_ARG, "logits: a CUDA f32 tensor is wanted")
+    _on(dev, torch.float32, u=u, temperature=temperature, top_p=top_p, min_p=min_p)
+    _on(dev, torch.int32, top_k=top_k, status=status)
+    for t in (u, temperature, top_k, top_p, min_p):
+        if t is not None and t.numel() != B:
+            raise Qw3Error(QW3_ERR_SHAPE, f"one setting and one number for each of {B} rows are wanted")
+    ptr = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
+    with torch.cuda.device(dev):
+        token = torch.empty(B, dtype=torch.int32, device=dev)
+        prob = torch.empty(B, dtype=torch.float32, device=dev)
+        qw3_sample(logits.data_ptr(), stride, B, logits.shape[1], ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p),
+                   u.data_ptr(), token.data_ptr(), prob.data_ptr(), ptr(status), _stream_ptr())
+    return token, prob
 
 
 class _Ordered:

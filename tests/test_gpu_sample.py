@@ -1,0 +1,199 @@
+"""qw3_sample against the oracle's sampler (f64).
+
+Tokens have to be equal wherever no decision of the row is a near one: the f32
+weights are within 4e-6 of exact (exp 2^-22 for an argument of up to 28 rounded
+twice at 2^-24), so a row whose oracle margin is below 4e-6 may go either way
+and is left out. Probabilities: within 8e-6 (a weight and a total)."""
+import numpy as np
+import pytest
+
+from oracle import qw3_oracle as orc
+
+pytestmark = pytest.mark.gpu
+
+NEAR = 4e-6
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as t
+    if not t.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from quantized_transformer_decode_gb300 import build
+    build.build()
+    return t
+
+
+def run(torch, logits, u, pad=0, **kw):
+    from quantized_transformer_decode_gb300 import qw3
+    cu = lambda x, d: torch.from_numpy(np.asarray(x, d)).cuda()  # noqa: E731
+    buf = cu(np.pad(np.asarray(logits, np.float32), ((0, 0), (pad, pad)), constant_values=1e30), np.float32)
+    view = buf[:, pad:buf.shape[1] - pad] if pad else buf
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = {k: cu(v, np.int32 if k == "top_k" else np.float32) for k, v in kw.items() if v is not None}
+    token, prob = qw3.sample(view, cu(u, np.float32), status=status, **args)
+    return token.cpu().numpy(), prob.cpu().numpy(), int(status)
+
+
+def check(torch, logits, u, least=0.9, pad=0, **kw):
+    """Compare every row; at least `least` of them must not be near ones."""
+    token, prob, status = run(torch, logits, u, pad, **kw)
+    assert status == 0
+    clear = 0
+    for i, row in enumerate(np.asarray(logits, np.float32)):
+        t, p, margin = orc.sample_token(row, np.float32(u[i]), **{k: np.asarray(v)[i] if k == "top_k" else np.float32(v[i])
+                                                                 for k, v in kw.items() if v is not None})
+        if margin > NEAR:
+            clear += 1
+            assert token[i] == t, (i, int(token[i]), t, margin)
+            assert abs(prob[i] - p) <= 8e-6 * p, (i, float(prob[i]), p)
+    assert clear >= least * len(u)
+
+
+def settings(rng, B):
+    return dict(temperature=rng.choice([0.0, 0.3, 0.7, 1.0, 1.7], B), top_k=rng.choice([0, 1, 2, 20, 999, 10 ** 6], B),
+                top_p=rng.choice([0.0, 0.1, 0.5, 0.9, 0.999, 1.0], B), min_p=rng.choice([0.0, 0.02, 0.3, 1.0], B))
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 31, 33, 255, 1000, 4099, 32768, 50257, 151936, 262145])
+def test_random_rows_and_settings(torch, V):
+    rng = np.random.default_rng(V)
+    B = 60 if V < 60000 else 24
+    # settings whose edges lie on exact values (a lone token, top-p of equal weights) are not near in f64: none is skipped
+    # for rows of one token
+    logits = rng.standard_normal((B, V)) * rng.choice([0.5, 2.0, 6.0], (B, 1))
+    check(torch, logits, rng.random(B), least=0.6 if V < 40 else 0.8, **settings(rng, B))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=[50]), dict(top_p=[0.9]), dict(min_p=[0.05]), dict(temperature=[0.6]),
+                                dict(temperature=[0.8], top_k=[40], top_p=[0.95], min_p=[0.05])])
+def test_each_setting_alone(torch, kw):
+    rng = np.random.default_rng(7)
+    B, V = 64, 20011
+    check(torch, rng.standard_normal((B, V)) * 3, rng.random(B), **{k: v * B for k, v in kw.items()})
+
+
+def test_equal_logits(torch):
+    """Ties go to the lowest indices, across any split of the row."""
+    V = 70001
+    rows = np.zeros((6, V), np.float32)
+    u = [0.0, 0.5, 0.99999, 0.3, 0.7, 0.5]
+    token, prob, _ = run(torch, rows, u, top_k=[5, 40000, 5, 0, V, 1], top_p=[1.0, 1.0, 1.0, 0.25, 1.0, 1.0])
+    f = lambda n, x: int(np.floor(np.float64(np.float32(x)) * n))  # noqa: E731
+    n_p = int(np.ceil(0.25 * V))
+    assert token.tolist() == [0, f(40000, 0.5), 4, f(n_p, 0.3), f(V, 0.7), 0]
+    assert np.allclose(prob, [1 / 5, 1 / 40000, 1 / 5, 1 / n_p, 1 / V, 1], rtol=1e-6)
+
+
+def test_signed_zeros_are_one_value(torch):
+    row = np.array([[-0.0, 0.0, -0.0, 0.0]], np.float32)
+    assert [run(torch, row, [u], top_k=[2])[0][0] for u in (0.0, 0.49, 0.51, 0.99)] == [0, 0, 1, 1]
+    assert run(torch, row, [0.5], temperature=[0.0])[0][0] == 0
+
+
+def test_plateaus_inside_a_row(torch):
+    """Cuts that fall inside runs of equal logits spread over the row."""
+    rng = np.random.default_rng(12)
+    B, V = 40, 9001
+    logits = np.round(rng.standard_normal((B, V)) * 2)
+    check(torch, logits, rng.random(B), least=0.7, top_k=rng.integers(1, V, B), top_p=rng.uniform(0.2, 1.0, B))
+
+
+def test_masked_rows(torch):
+    rng = np.random.default_rng(13)
+    B, V = 24, 30011
+    logits = (rng.standard_normal((B, V)) * 2).astype(np.float32)
+    logits[rng.random((B, V)) < 0.999] = -np.inf
+    logits[:, 17] = 0.5
+    logits[0] = -np.inf
+    logits[0, V - 1] = -3e38                            # one token left, far from any other number
+    logits[1, :] = np.finfo(np.float32).min              # a mask of the type's lowest value everywhere
+    check(torch, logits, rng.random(B), least=0.7, **settings(rng, B))
+
+
+def test_large_and_tiny_scales(torch):
+    rng = np.random.default_rng(14)
+    B, V = 32, 5003
+    logits = rng.standard_normal((B, V)).astype(np.float32)
+    logits[::4] *= 1e4
+    logits[1::4] *= 1e-6
+    logits[2::4] += 1e5
+    logits[3::4] = logits[3::4] * 2 - 200
+    check(torch, logits, rng.random(B), least=0.7, temperature=rng.choice([1e-3, 0.5, 1.0, 100.0], B))
+
+
+def test_ends_of_u(torch):
+    V = 40009
+    rng = np.random.default_rng(15)
+    row = rng.standard_normal((4, V)).astype(np.float32)
+    token, _, _ = run(torch, row, [0.0, -1.0, 1.0, np.nan])
+    assert token[0] == 0 and token[1] == 0 and token[2] == V - 1 and token[3] == 0
+    row[:, 0] = row[:, V - 1] = -np.inf
+    token, _, _ = run(torch, row, [0.0, 0.0, 1.0, 1.0 - 2.0 ** -24])
+    assert token[0] == 1 and token[2] == V - 2
+
+
+def test_rows_without_an_answer(torch):
+    V = 3001
+    rows = np.zeros((7, V), np.float32)
+    rows[0, 5] = np.nan
+    rows[1] = -np.inf
+    rows[2, 9] = np.inf
+    rows[3, 9] = np.inf                                  # greedy: the answer is 9
+    rows[4, 100] = 3.0
+    token, prob, status = run(torch, rows, [0.5] * 7, temperature=[1, 1, 1, 0, 0, np.nan, np.inf])
+    assert status == 5
+    assert token.tolist() == [-1, -1, -1, 9, 100, -1, -1] and prob.tolist() == [0, 0, 0, 1, 1, 0, 0]
+    token, _, status = run(torch, rows[4:5], [0.5], temperature=[0])
+    assert status == 0 and token.tolist() == [100]
+
+
+def test_strided_rows_and_no_settings(torch):
+    rng = np.random.default_rng(16)
+    B, V = 12, 4097
+    for pad in (1, 3, 8):
+        check(torch, rng.standard_normal((B, V)), rng.random(B), pad=pad, top_k=[100] * B)
+
+
+def test_many_rows(torch):
+    rng = np.random.default_rng(17)
+    B, V = 300, 2003
+    check(torch, rng.standard_normal((B, V)) * 2, rng.random(B), **settings(rng, B), least=0.8)
+
+
+def test_largest_vocabulary(torch):
+    rng = np.random.default_rng(18)
+    V = 4194304
+    check(torch, rng.standard_normal((2, V)), [0.3, 0.9], least=0.5, top_k=[0, 100000], top_p=[0.9, 1.0])
+
+
+def test_same_tokens_every_time_and_captured(torch):
+    from quantized_transformer_decode_gb300 import qw3
+    rng = np.random.default_rng(19)
+    B, V = 16, 151936
+    x = torch.from_numpy((rng.standard_normal((B, V)) * 2).astype(np.float32)).cuda()
+    u = torch.from_numpy(rng.random(B, np.float32)).cuda()
+    kw = dict(temperature=torch.full((B,), 0.9, device="cuda"), top_p=torch.full((B,), 0.95, device="cuda"))
+    want, wp = qw3.sample(x, u, **kw)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got, gp = qw3.sample(x, u, **kw)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(gp, wp)
+    u.copy_(torch.from_numpy(rng.random(B, np.float32)).cuda())
+    g.replay()
+    assert torch.equal(got, qw3.sample(x, u, **kw)[0])
+
+
+def test_wrapper_refusals(torch):
+    from quantized_transformer_decode_gb300 import qw3
+    x, u = torch.zeros(2, 10, device="cuda"), torch.zeros(2, device="cuda")
+    for bad in (lambda: qw3.sample(x.half(), u), lambda: qw3.sample(x.t(), torch.zeros(10, device="cuda")),
+                lambda: qw3.sample(x, u[:1]), lambda: qw3.sample(x, u, temperature=u.double()),
+                lambda: qw3.sample(x, u, top_k=u), lambda: qw3.sample(x[0], u), lambda: qw3.sample(x[:, :0], u),
+                lambda: qw3.sample(x, u.cpu())):
+        with pytest.raises(qw3.Qw3Error):
+            bad()
+    assert qw3.sample(x[:0], u[:0])[0].numel() == 0
