@@ -412,8 +412,8 @@ QW3_API int64_t qw3_kv_q4_bytes(int32_t slots, int32_t capacity, int32_t n_kv_he
  * stride), keys and values into the cache.
  * Row i goes to slot slots_dev[i] (slot0 where slots_dev is NULL) and position
  * pos_dev[i] (pos0 + i where pos_dev is NULL). A row whose slot or position
- * from a device array lies outside the cache (a padding row, say -1) is
- * skipped, its q_out row left as it was; positions given as pos0 must fit
+ * from a device array lies outside the cache (a padding row, say -1) is not
+ * cached, and its q_out row is zeros; positions given as pos0 must fit
  * (QW3_ERR_KV_OVERFLOW). No two rows of a call may name the same place.
  * n_heads a multiple of n_kv_heads. Asynchronous on `stream`. */
 QW3_API int qw3_kv_q4_append(const qw3_kv_q4 *cache, const float *qkv_dev, int32_t M, int64_t qkv_stride,
@@ -422,8 +422,8 @@ QW3_API int qw3_kv_q4_append(const qw3_kv_q4 *cache, const float *qkv_dev, int32
                              int32_t pos0, float *q_out_dev, int64_t q_stride, int32_t *status_dev, void *stream);
 
 /* Read M cached rows back as f32: k_out_dev and v_out_dev [M][n_kv_heads]
- * [head_dim]. Rows are named, and left out, as in qw3_kv_q4_append; here a
- * place may be named twice. */
+ * [head_dim]. Rows are named as in qw3_kv_q4_append, those outside the cache
+ * read as zeros; here a place may be named twice. */
 QW3_API int qw3_kv_q4_read(const qw3_kv_q4 *cache, int32_t M, const int32_t *slots_dev, int32_t slot0,
                            const int32_t *pos_dev, int32_t pos0, float *k_out_dev, float *v_out_dev, void *stream);
 

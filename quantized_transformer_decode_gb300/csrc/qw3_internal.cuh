@@ -267,7 +267,8 @@ __host__ __device__ inline size_t kv_q4_head_bytes(int cap, int hd) {
 }
 
 // (slot, position) of each row of a call: from device arrays where they are
-// given, else slot0 and pos0 + row. A row outside the cache is left out.
+// given, else slot0 and pos0 + row. A row outside the cache is not cached and
+// reads as zeros.
 struct KvQ4Rows {
     const int32_t *slots = nullptr;
     int slot0 = 0;

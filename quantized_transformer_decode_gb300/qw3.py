@@ -413,11 +413,15 @@ def q4_k_gemv(W, rows: int, cols: int, x):
     return y
 
 
-def _on(device, dtype, **tensors):
-    """Check that each given tensor lies on `device` as contiguous values of `dtype`."""
+def _on(index: int, dtype, **tensors):
+    """Check that each given tensor lies on CUDA device `index` as contiguous values of `dtype`."""
     for name, t in tensors.items():
-        if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous()):
-            raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a contiguous {dtype} tensor on {device} is wanted")
+        if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a contiguous {dtype} tensor on cuda:{index} is wanted")
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _rows_of(t, name: str):
@@ -425,6 +429,25 @@ def _rows_of(t, name: str):
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a 2-d tensor with contiguous rows is wanted")
     return t.shape[0], t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+class _Here:
+    """Makes a CUDA device current for a call, at no cost where it is already."""
+
+    def __init__(self, index: int):
+        self.index, self.guard = index, None
+
+    def __enter__(self):
+        torch = _torch()
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        return torch.cuda.current_stream(self.index).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
 
 
 class KVCacheQ4:
@@ -439,18 +462,16 @@ class KVCacheQ4:
             raise Qw3Error(QW3_ERR_SHAPE, "slots >= 1, capacity % 32 == 0, 1 to 64 kv heads, head_dim 64 or 128")
         if data is None:
             data = torch.empty(n, dtype=torch.uint8, device=device)
-        elif data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous() or data.numel() < n:
+        elif data.dtype is not torch.uint8 or not data.is_cuda or not data.is_contiguous() or data.numel() < n:
             raise Qw3Error(QW3_ERR_INVALID_ARG, f"data: a contiguous CUDA uint8 tensor of {n} bytes is wanted")
-        self.data, self.device = data, data.device
+        self.data, self.device, self.index = data, data.device, data.get_device()
         self.slots, self.capacity, self.n_kv_heads, self.head_dim = slots, capacity, n_kv_heads, head_dim
         self.c = Qw3KvQ4(data.data_ptr(), slots, capacity, n_kv_heads, head_dim)
 
-    def _places(self, M, slots, pos, slot, first):
-        _on(self.device, _torch().int32, slots=slots, pos=pos)
-        for t in (slots, pos):
-            if t is not None and t.numel() != M:
-                raise Qw3Error(QW3_ERR_SHAPE, f"slots and pos hold one place for each of {M} rows")
-        return slots.data_ptr() if slots is not None else 0, slot, pos.data_ptr() if pos is not None else 0, first
+    def _check_places(self, M, slots, pos):
+        _on(self.index, _torch().int32, slots=slots, pos=pos)
+        if (slots is not None and slots.numel() != M) or (pos is not None and pos.numel() != M):
+            raise Qw3Error(QW3_ERR_SHAPE, f"slots and pos hold one place for each of {M} rows")
 
     def append(self, qkv, q_norm, k_norm, eps: float, rope, slots=None, pos=None, slot: int = 0, first: int = 0,
                status=None):
@@ -458,24 +479,23 @@ class KVCacheQ4:
         [M, n_heads, head_dim]. qkv: f32 [M, (n_heads + 2 n_kv_heads) * head_dim]
         (rows may be strided); rope: f32 [capacity, head_dim / 2, 2]. Row i goes
         to (slots[i], pos[i]), int32 tensors, or to (slot, first + i). A row
-        outside the cache is skipped and its queries are zero."""
+        outside the cache is not cached and its queries are zero."""
         torch = _torch()
         M, stride = _rows_of(qkv, "qkv")
-        hd = self.head_dim
-        n_heads = qkv.shape[1] // hd - 2 * self.n_kv_heads
-        if qkv.dtype != torch.float32 or qkv.device != self.device or qkv.shape[1] % hd or n_heads < 1:
+        hd, width = self.head_dim, qkv.shape[1]
+        n_heads = width // hd - 2 * self.n_kv_heads
+        if qkv.dtype is not torch.float32 or qkv.get_device() != self.index or width % hd or n_heads < 1:
             raise Qw3Error(QW3_ERR_SHAPE, "qkv: f32 rows of n_heads + 2 n_kv_heads heads on the cache's device")
-        _on(self.device, torch.float32, q_norm=q_norm, k_norm=k_norm, rope=rope)
-        _on(self.device, torch.int32, status=status)
+        _on(self.index, torch.float32, q_norm=q_norm, k_norm=k_norm, rope=rope)
         if q_norm.numel() != hd or k_norm.numel() != hd or rope.numel() != self.capacity * hd:
             raise Qw3Error(QW3_ERR_SHAPE, "q_norm and k_norm hold head_dim values, rope capacity * head_dim")
-        places = self._places(M, slots, pos, slot, first)
-        new = torch.zeros if slots is not None or pos is not None else torch.empty
-        with torch.cuda.device(self.device):
-            q = new((M, n_heads, hd), dtype=torch.float32, device=self.device)
-            qw3_kv_q4_append(self.c, qkv.data_ptr(), M, stride, n_heads, q_norm.data_ptr(), k_norm.data_ptr(), eps,
-                             rope.data_ptr(), *places, q.data_ptr(), n_heads * hd,
-                             status.data_ptr() if status is not None else 0, _stream_ptr())
+        _on(self.index, torch.int32, status=status)
+        self._check_places(M, slots, pos)
+        q = torch.empty((M, n_heads, hd), dtype=torch.float32, device=self.device)
+        with _Here(self.index) as stream:
+            _check(lib().qw3_kv_q4_append(self.c, qkv.data_ptr(), M, stride, n_heads, q_norm.data_ptr(),
+                                          k_norm.data_ptr(), eps, rope.data_ptr(), _ptr(slots), slot, _ptr(pos), first,
+                                          q.data_ptr(), n_heads * hd, _ptr(status), stream))
         return q
 
     def read(self, slots=None, pos=None, slot: int = 0, first: int = 0, n: Optional[int] = None):
@@ -483,14 +503,15 @@ class KVCacheQ4:
         as in append, M from slots or pos, else n. Rows outside the cache are
         zero."""
         torch = _torch()
-        M = n if n is not None else next((t.numel() for t in (slots, pos) if t is not None), None)
-        if M is None or M < 0:
+        M = n if n is not None else slots.numel() if slots is not None else pos.numel() if pos is not None else -1
+        if M < 0:
             raise Qw3Error(QW3_ERR_INVALID_ARG, "read needs slots, pos or n")
-        places = self._places(M, slots, pos, slot, first)
-        new = torch.zeros if slots is not None or pos is not None else torch.empty
-        with torch.cuda.device(self.device):
-            k, v = new((2, M, self.n_kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
-            qw3_kv_q4_read(self.c, M, *places, k.data_ptr(), v.data_ptr(), _stream_ptr())
+        self._check_places(M, slots, pos)
+        shape = (M, self.n_kv_heads, self.head_dim)
+        k = torch.empty(shape, dtype=torch.float32, device=self.device)
+        v = torch.empty(shape, dtype=torch.float32, device=self.device)
+        with _Here(self.index) as stream:
+            _check(lib().qw3_kv_q4_read(self.c, M, _ptr(slots), slot, _ptr(pos), first, k.data_ptr(), v.data_ptr(), stream))
         return k, v
 
     def attention(self, q, lens, rows: int = 1, slots=None, max_len: Optional[int] = None,
@@ -501,28 +522,30 @@ class KVCacheQ4:
         (the capacity where it is not given). scale: 1 / sqrt(head_dim) where it
         is not given. workspace: a uint8 tensor to use in place of a new one."""
         torch = _torch()
-        B = lens.numel()
-        _on(self.device, torch.float32, q=q, out=out)
-        _on(self.device, torch.int32, lens=lens, slots=slots)
-        if q.dim() != 3 or q.shape[0] != B * rows or q.shape[2] != self.head_dim:
-            raise Qw3Error(QW3_ERR_SHAPE, f"q: [{B * rows}, n_heads, {self.head_dim}] is wanted")
+        B, hd, n_heads = lens.numel(), self.head_dim, q.shape[1] if q.dim() == 3 else 0
+        _on(self.index, torch.float32, q=q, out=out)
+        _on(self.index, torch.int32, lens=lens, slots=slots)
+        if n_heads < 1 or q.shape[0] != B * rows or q.shape[2] != hd:
+            raise Qw3Error(QW3_ERR_SHAPE, f"q: [{B * rows}, n_heads, {hd}] is wanted")
         if (slots is not None and slots.numel() != B) or (out is not None and out.shape != q.shape):
             raise Qw3Error(QW3_ERR_SHAPE, "slots holds one slot per sequence, out has q's shape")
         if slots is None and B > self.slots:
             raise Qw3Error(QW3_ERR_SHAPE, "more sequences than slots")
-        n_heads, w = q.shape[1], q.shape[1] * self.head_dim
         max_len = self.capacity if max_len is None else max_len
-        need = qw3_kv_q4_attn_workspace_bytes(B, rows, n_heads, self.n_kv_heads, self.head_dim, max_len)
-        with torch.cuda.device(self.device):
-            out = torch.empty_like(q) if out is None else out
-            if workspace is None and need > 0:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32, device=self.device)
+        L = lib()
+        if workspace is None:
+            need = L.qw3_kv_q4_attn_workspace_bytes(B, rows, n_heads, self.n_kv_heads, hd, max_len)
+            if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            _on(self.device, torch.uint8, workspace=workspace)
-            qw3_kv_q4_attn(self.c, q.data_ptr(), w, n_heads, slots.data_ptr() if slots is not None else 0,
-                           lens.data_ptr(), B, rows, max_len,
-                           self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), w,
-                           workspace.data_ptr() if workspace is not None else 0,
-                           workspace.numel() if workspace is not None else 0, _stream_ptr())
+        else:
+            _on(self.index, torch.uint8, workspace=workspace)
+            need = workspace.numel()
+        with _Here(self.index) as stream:
+            _check(L.qw3_kv_q4_attn(self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots), lens.data_ptr(), B, rows,
+                                    max_len, hd ** -0.5 if scale is None else scale, out.data_ptr(), n_heads * hd,
+                                    _ptr(workspace), need, stream))
         return out
 
 
@@ -533,20 +556,20 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stat
     left out."""
     torch = _torch()
     B, stride = _rows_of(logits, "logits")
-    dev = logits.device
-    if logits.dtype != torch.float32 or not logits.is_cuda:
+    dev = logits.get_device()
+    if logits.dtype is not torch.float32 or dev < 0:
         raise Qw3Error(QW3_ERR_INVALID_ARG, "logits: a CUDA f32 tensor is wanted")
     _on(dev, torch.float32, u=u, temperature=temperature, top_p=top_p, min_p=min_p)
     _on(dev, torch.int32, top_k=top_k, status=status)
     for t in (u, temperature, top_k, top_p, min_p):
         if t is not None and t.numel() != B:
             raise Qw3Error(QW3_ERR_SHAPE, f"one setting and one number for each of {B} rows are wanted")
-    ptr = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
-    with torch.cuda.device(dev):
-        token = torch.empty(B, dtype=torch.int32, device=dev)
-        prob = torch.empty(B, dtype=torch.float32, device=dev)
-        qw3_sample(logits.data_ptr(), stride, B, logits.shape[1], ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p),
-                   u.data_ptr(), token.data_ptr(), prob.data_ptr(), ptr(status), _stream_ptr())
+    token = torch.empty(B, dtype=torch.int32, device=logits.device)
+    prob = torch.empty(B, dtype=torch.float32, device=logits.device)
+    with _Here(dev) as stream:
+        _check(lib().qw3_sample(logits.data_ptr(), stride, B, logits.shape[1], _ptr(temperature), _ptr(top_k),
+                                _ptr(top_p), _ptr(min_p), u.data_ptr(), token.data_ptr(), prob.data_ptr(), _ptr(status),
+                                stream))
     return token, prob
 
 

@@ -11,7 +11,12 @@ rounded or truncated once (2^-23): within ds = scale * sum|q k| * (2^-22 +
 (head_dim / 16 + 4) * 2^-23); an output moves by at most 2 ds times sum p |v|,
 plus the P V products (p kept to 22 bits, exp within 2^-22 of its value for an
 argument rounded at 2^-24 of up to 128, chains of 2^-23 roundings: 64 of them
-in all), so |error| <= (2 ds + 64 * 2^-23) sum p |v|.
+in all), so |error| <= (2 ds + 64 * 2^-23) sum p |v|. To that comes a floor: p
+times a V scale enters the tensor core as two f16 parts, cut at 2^-24 where the
+largest such product may be anything from 2^12 to 2^15 (the unit follows the
+largest scale s in steps that leave up to 3 bits free); times a code of at most
+8 that is 2^-36 * 8 s for each of n positions, and 8 s is the largest |v|:
+n * 2^-36 * max |v|.
 """
 import numpy as np
 import pytest
@@ -269,7 +274,7 @@ def plain_attention(q, k, v, lens, rows, scale):
                 p /= p.sum()
                 out[b * rows + t, h] = p @ vv
                 ds = abs(scale) * (np.abs(kk) @ np.abs(qq)).max() * (2.0 ** -22 + (hd / 16 + 4) * 2.0 ** -23)
-                tol[b * rows + t, h] = (2 * ds + 64 * 2.0 ** -23) * (p @ np.abs(vv)) + 1e-30
+                tol[b * rows + t, h] = (2 * ds + 64 * 2.0 ** -23) * (p @ np.abs(vv)) + n * 2.0 ** -36 * np.abs(vv).max() + 1e-30
     return out, tol
 
 
