@@ -69,6 +69,7 @@ cudaError_t configure_all() {
         if (e == cudaSuccess) e = configure_gemm_tc();
         if (e == cudaSuccess) e = configure_q4k();
         if (e == cudaSuccess) e = configure_attn_prefill_tc();
+        if (e == cudaSuccess) e = configure_sample();
         g_cfg_err = e;
     });
     return g_cfg_err;
@@ -1406,6 +1407,7 @@ int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, co
         return fail(nullptr, QW3_ERR_INVALID_ARG, "device buffers must be 4-byte aligned");
     SampleArgs a{logits_dev, stride, V, temperature_dev, top_k_dev, top_p_dev, min_p_dev, u_dev, token_dev, prob_dev,
                  status_dev};
+    QW3_CUDA_TRY(configure_all());   // the kernel's shared-memory limit
     QW3_CUDA_TRY(launch_sample(a, B, static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }

@@ -310,6 +310,7 @@ struct SampleArgs {
     float *prob;      // nullable [B]
     int32_t *status;
 };
+cudaError_t configure_sample();
 cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s);
 
 }  // namespace qw3
