@@ -120,6 +120,13 @@ typedef struct qw3_config {
                                   forward read the dequantised rows. Not with
                                   QW3_FLAG_KV_F16. Batch-1 decode runs the
                                   per-kernel chain.                           */
+#define QW3_FLAG_KV_Q4  0x200    /* KV cache in 4 bits (4.5 with the scales;
+                                  the layout and encoder of qw3_kv_q4 below).
+                                  Decode and forwards of up to 16 rows attend
+                                  over the codes; longer chunks over the rows
+                                  read back as f32. Not with QW3_FLAG_KV_F16 or
+                                  QW3_FLAG_KV_Q8. Batch-1 decode runs the
+                                  per-kernel chain.                           */
 #define QW3_FLAG_WEIGHTS_Q4_K 0x100 /* every linear weight (the embedding and
                                   output included) is given as Q4_K blocks
                                   ("Model files and quantization", 11.8:
@@ -209,6 +216,21 @@ QW3_API int qw3_decode(qw3_model *m, int32_t B, const int32_t *seqs_host,
 QW3_API int qw3_generate_greedy(qw3_model *m, int32_t B, const int32_t *seqs_host,
                         int32_t n_steps, const int32_t *first_tokens_dev,
                         int32_t *out_tokens_dev);
+
+/* n_steps sampled decode steps for B sequences without host round trips:
+ * qw3_generate_greedy with each step's token drawn by qw3_sample (below) from
+ * that step's logits. temperature_dev, top_k_dev, top_p_dev, min_p_dev: [B],
+ * one setting per sequence for all steps, each nullable; u_dev: f32
+ * [n_steps][B] in [0, 1). logits_dev: f32 [B][V], written by every step, the
+ * last step's on return. out_tokens_dev: int32 [n_steps][B]; prob_dev:
+ * nullable f32 [n_steps][B]. A row without an answer (NaN logits) gets token
+ * -1, goes on from token 0 and sets the device status. Errors as
+ * qw3_generate_greedy; QW3_ERR_SHAPE for a vocabulary above 4194304. */
+QW3_API int qw3_generate_sample(qw3_model *m, int32_t B, const int32_t *seqs_host,
+                        int32_t n_steps, const int32_t *first_tokens_dev,
+                        const float *temperature_dev, const int32_t *top_k_dev,
+                        const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+                        float *logits_dev, int32_t *out_tokens_dev, float *prob_dev);
 
 /* Sequence bookkeeping (course 12.4): reset sets the length to 0, truncate
  * to min(len, keep_len); neither touches device memory. */

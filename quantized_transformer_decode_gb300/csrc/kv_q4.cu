@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(128) k_kv_q4_append(Q4AppendArgs a) {
 // Four values of one (row, head) of K and of V per thread.
 template <int HD>
 __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M, float *__restrict__ k_out,
-                                                    float *__restrict__ v_out) {
+                                                    float *__restrict__ v_out, size_t out_row, size_t out_head) {
     constexpr int NB = HD / 32, Q = HD / 4;
     const int64_t total = static_cast<int64_t>(M) * c.nkv * Q;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
             y.y = s * static_cast<float>(static_cast<int>((w >> 4) & 15u) - 8);
             y.z = s * static_cast<float>(static_cast<int>((w >> 8) & 15u) - 8);
             y.w = s * static_cast<float>(static_cast<int>(w >> 12) - 8);
-            float *out = (sel ? v_out : k_out) + rg * HD + 4 * j;
+            float *out = (sel ? v_out : k_out) + row * out_row + g * out_head + 4 * j;
             out[0] = y.x; out[1] = y.y; out[2] = y.z; out[3] = y.w;
         }
     }
@@ -348,6 +348,11 @@ __device__ __forceinline__ float half_of(uint32_t w, int i) {
 
 constexpr int kQ4Warps = 4, kQ4Tile = 32;
 
+// Positions of sequence b, within what the call allows.
+__device__ __forceinline__ int q4_len(const KvQ4AttnArgs &a, int b) {
+    return min(max(a.lens ? a.lens[b] : 0, -a.len_add) + a.len_add, a.max_len);
+}
+
 // Columns that one CTA of width class W takes, and its 8-column operands: W =
 // 1, 2, 4 with hi and lo in one operand; 8 and 16 with operands of their own.
 __host__ __device__ constexpr int q4_ops(int W) { return W <= 4 ? 1 : W / 4; }
@@ -392,9 +397,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int split = blockIdx.x, g = blockIdx.y / cgroups, cg = blockIdx.y % cgroups, b = blockIdx.z;
     const int G = a.nh / a.c.nkv, cols = G * a.rows, col0 = cg * W, ncol = min(W, cols - col0);
-    const int slot = a.slots ? a.slots[b] : b;
+    const int slot = a.slots ? a.slots[b] : a.slot0 + b;
     const bool there = slot >= 0 && slot < a.c.slots;
-    const int len = there ? min(max(a.lens[b], 0), a.max_len) : 0;
+    const int len = there ? q4_len(a, b) : 0;
     // positions that this group's last column sees
     const int seen = len - a.rows + (col0 + ncol - 1) / G + 1;
     const int start = split * chunk, end = min(seen, start + chunk);
@@ -765,8 +770,8 @@ __global__ void __launch_bounds__(128) k_kv_q4_merge(KvQ4AttnArgs a, int chunk, 
     if (unit >= static_cast<int64_t>(a.B) * a.c.nkv * cols) return;
     const int cc = static_cast<int>(unit % cols), g = static_cast<int>(unit / cols % a.c.nkv);
     const int b = static_cast<int>(unit / cols / a.c.nkv);
-    const int slot = a.slots ? a.slots[b] : b;
-    const int len = slot >= 0 && slot < a.c.slots ? min(max(a.lens[b], 0), a.max_len) : 0;
+    const int slot = a.slots ? a.slots[b] : a.slot0 + b;
+    const int len = slot >= 0 && slot < a.c.slots ? q4_len(a, b) : 0;
     const int col0 = cc / W * W, ncol = min(W, cols - col0);
     const int seen = len - a.rows + (col0 + ncol - 1) / G + 1;   // as in the kernel above
     const int runs = seen > 0 ? min(nsplit, (seen + chunk - 1) / chunk) : 0;
@@ -804,12 +809,12 @@ cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, con
 }
 
 cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M, float *k_out, float *v_out,
-                              cudaStream_t s) {
+                              size_t out_row, size_t out_head, cudaStream_t s) {
     if (M <= 0) return cudaSuccess;
     const int64_t total = static_cast<int64_t>(M) * c.nkv * (hd / 4);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + 255) / 256, 152 * 16));
-    if (hd == 128) k_kv_q4_read<128><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out);
-    else if (hd == 64) k_kv_q4_read<64><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out);
+    if (hd == 128) k_kv_q4_read<128><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    else if (hd == 64) k_kv_q4_read<64><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
     else return cudaErrorInvalidValue;
     return cudaGetLastError();
 }
@@ -865,6 +870,10 @@ cudaError_t launch_q4_attn_hd(const KvQ4AttnArgs &a, const Q4Plan &p, cudaStream
 }
 
 }  // namespace
+
+int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len) {
+    return q4_plan(B, rows, nh, nkv, max_len).nsplit > 1 ? 2 : 1;
+}
 
 size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len) {
     const Q4Plan p = q4_plan(B, rows, nh, nkv, max_len);

@@ -111,13 +111,16 @@ struct qw3_model {
     float *out_norm = nullptr;
     float2 *rope = nullptr;
 
-    void *kv = nullptr;    // f32, IEEE half or q8_0 rows (kvtype)
+    void *kv = nullptr;    // f32, IEEE half, q8_0 rows or the 4-bit layout (kvtype)
     int kvtype = KV_F32;
     bool act_q8 = false;   // linear inputs through a Q8_0 round trip
     bool q4k = false;      // Q4_K weights: raw rows per matrix (QMat::q4), tensor-core tiles, no Q8_0 tiles
     uint8_t *emb4 = nullptr, *out4 = nullptr;
     size_t head_stride = 0, kvsel_stride = 0, seq_stride = 0, layer_stride = 0;
     std::vector<int32_t> seq_len;
+    int kv_cap = 0;            // allocated positions per sequence
+    float *q4_ws = nullptr;    // 4-bit cache: attention workspace
+    float *q4_rows = nullptr;  // 4-bit cache: one sequence's rows of a layer as f32 [K|V][kv_head][max_seq_len][hd]
 
     // decode scratch
     int qkv_w = 0;
@@ -154,6 +157,16 @@ namespace {
 void *kv_at(const qw3_model *m, int layer, int seq) {
     const size_t e = static_cast<size_t>(layer) * m->layer_stride + static_cast<size_t>(seq) * m->seq_stride;
     return static_cast<uint8_t *>(m->kv) + e * kv_unit_bytes(m->kvtype);
+}
+
+// Layer l of the 4-bit cache.
+KvQ4 kv_q4_layer(const qw3_model *m, int layer) {
+    KvQ4 v;
+    v.data = static_cast<uint8_t *>(kv_at(m, layer, 0));
+    v.slots = m->cfg.max_seqs;
+    v.cap = m->kv_cap;
+    v.nkv = m->cfg.n_kv_heads;
+    return v;
 }
 
 // A linear layer through the GEMM; in the q8_0 activation mode its input
@@ -295,7 +308,9 @@ int validate_config(const qw3_config *c, std::string &why) {
         return bad("max_seqs, max_seq_len and max_prefill must be positive");
     if (!(c->rms_eps >= 0.0f) || !(c->rope_theta > 0.0f)) return bad("rms_eps must be >= 0 and rope_theta > 0");
     if (c->hidden > 16384 || c->intermediate > 65536) return bad("hidden or intermediate too large");
-    if ((c->flags & QW3_FLAG_KV_F16) && (c->flags & QW3_FLAG_KV_Q8)) return bad("one KV cache type at most");
+    const int cache_types = ((c->flags & QW3_FLAG_KV_F16) != 0) + ((c->flags & QW3_FLAG_KV_Q8) != 0) +
+                            ((c->flags & QW3_FLAG_KV_Q4) != 0);
+    if (cache_types > 1) return bad("one KV cache type at most");
     if (c->flags & QW3_FLAG_WEIGHTS_Q4_K) {
         if (c->hidden % 256 || c->intermediate % 256 || (c->n_heads * c->head_dim) % 256)
             return bad("Q4_K weights need hidden, intermediate and n_heads*head_dim multiples of 256");
@@ -340,6 +355,41 @@ AttnDecodeArgs attn_args(qw3_model *m, int l) {
     return at;
 }
 
+// Attention of `rows` query rows per sequence (already in q, normalised and
+// rotated) over layer l of the 4-bit cache.
+KvQ4AttnArgs q4_attn_args(qw3_model *m, int l, const float *q, int B, int rows, float *out) {
+    const qw3_config &c = m->cfg;
+    KvQ4AttnArgs a{};
+    a.q = q; a.q_stride = m->qkv_w; a.c = kv_q4_layer(m, l); a.B = B; a.rows = rows; a.nh = c.n_heads;
+    a.max_len = c.max_seq_len;
+    a.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.head_dim)));
+    a.out = out; a.out_stride = static_cast<int64_t>(c.n_heads) * c.head_dim; a.ws = m->q4_ws;
+    return a;
+}
+
+// Norm, rotation, append and attention of a decode step's layer: one kernel
+// for the f32, half and q8_0 caches, the 4-bit cache's own kernels for that.
+int decode_attention(qw3_model *m, int l, int B, int nsplit, int csize, bool pdl, unsigned long long *trace,
+                     cudaStream_t s) {
+    if (m->kvtype != KV_Q4) {
+        AttnDecodeArgs at = attn_args(m, l);
+        at.trace = trace;
+        M_TRY(m, launch_attn_decode(at, B, nsplit, csize, pdl, s));
+        return QW3_OK;
+    }
+    const qw3_config &c = m->cfg;
+    const LayerDev &L = m->layers[l];
+    const KvQ4Rows rows{m->d_seq, 0, m->d_pos, 0};
+    M_TRY(m, launch_kv_q4_append(m->qkv, B, m->qkv_w, L.q_norm, L.k_norm, c.rms_eps, m->rope, kv_q4_layer(m, l),
+                                 c.head_dim, rows, c.n_heads, m->qkv, m->qkv_w, m->d_status, s));
+    KvQ4AttnArgs a = q4_attn_args(m, l, m->qkv, B, 1, m->o);
+    a.slots = m->d_seq;
+    a.lens = m->d_pos;
+    a.len_add = 1;
+    M_TRY(m, launch_kv_q4_attn(a, c.head_dim, s));
+    return QW3_OK;
+}
+
 // One decode step of a Q4_K model for B rows the Q4_K GEMV takes: every
 // projection streams the raw Q4_K rows (norms fused as prologues, SwiGLU over
 // the interleaved gate/up pairs), the lm_head keeps packed argmax keys that
@@ -356,7 +406,7 @@ int enqueue_decode_q4k(qw3_model *m, int B, int nsplit, int csize, cudaStream_t 
         const LayerDev &L = m->layers[l];
         M_TRY(m, launch_gemv_q4k(L.qkv.q4, m->qkv_w, H, B, m->x, L.attn_norm, eps, m->qkv, GEMV_STORE, nullptr,
                                  nullptr, pdl, s));
-        M_TRY(m, launch_attn_decode(attn_args(m, l), B, nsplit, csize, pdl, s));
+        if (int rc = decode_attention(m, l, B, nsplit, csize, pdl, nullptr, s)) return rc;
         M_TRY(m, launch_gemv_q4k(L.o.q4, H, qw, B, m->o, nullptr, eps, m->x, GEMV_RESID, nullptr, nullptr, pdl, s));
         M_TRY(m, launch_gemv_q4k(L.gu.q4, 2 * I, H, B, m->x, L.ffn_norm, eps, m->act, GEMV_SWIGLU, nullptr, nullptr,
                                  pdl, s));
@@ -374,8 +424,8 @@ int enqueue_decode_q4k(qw3_model *m, int B, int nsplit, int csize, cudaStream_t 
 int enqueue_decode(qw3_model *m, int B, cudaStream_t s) {
     const qw3_config &c = m->cfg;
     const bool pdl = !(c.flags & QW3_FLAG_NO_PDL);
-    const int H = c.hidden, hd = c.head_dim, nh = c.n_heads, nkv = c.n_kv_heads, I = c.intermediate;
-    const int qw = nh * hd;
+    const int H = c.hidden, nkv = c.n_kv_heads, I = c.intermediate;
+    const int qw = c.n_heads * c.head_dim;
     int nsplit = pick_nsplit(B, nkv, m->attn_max_split), csize = nsplit;
     if (B == 1 && m->attn_long_c > 0) {
         // long contexts at batch 1: kAttnLongClusters clusters per kv head,
@@ -407,15 +457,7 @@ int enqueue_decode(qw3_model *m, int B, cudaStream_t s) {
             M_TRY(m, launch_rmsnorm_rows(m->x, B, H, L.attn_norm, c.rms_eps, m->h, s));
             M_TRY(m, lin_gemm(m, m->h, B, H, L.qkv, m->qkv, GEMV_STORE, nullptr, nullptr, s));
         }
-        AttnDecodeArgs at{};
-        at.qkv = m->qkv; at.qkv_stride = m->qkv_w; at.q_norm = L.q_norm; at.k_norm = L.k_norm; at.eps = c.rms_eps;
-        at.rope = m->rope; at.kv = kv_at(m, l, 0); at.kvtype = m->kvtype;
-        at.seq_stride = m->seq_stride; at.kvsel_stride = m->kvsel_stride; at.head_stride = m->head_stride;
-        at.seq_ids = m->d_seq; at.pos = m->d_pos; at.nh = nh; at.nkv = nkv; at.hd = hd;
-        at.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(hd)));
-        at.out = m->o; at.status = m->d_status; at.cpart = m->attn_cpart; at.ccnt = m->attn_ccnt;
-        at.trace = tr();
-        M_TRY(m, launch_attn_decode(at, B, nsplit, csize, pdl && gv, s));
+        if (int rc = decode_attention(m, l, B, nsplit, csize, pdl && gv, tr(), s)) return rc;
         if (gv) {
             GemvArgs a{};
             a.act_q8 = m->act_q8;
@@ -694,7 +736,7 @@ int qw3_create(const qw3_config *cfg, const qw3_weights *w, void *cuda_stream, q
 
     qw3_model *m = new qw3_model();
     m->cfg = *cfg;
-    m->kvtype = (cfg->flags & QW3_FLAG_KV_Q8) ? KV_Q8 : ((cfg->flags & QW3_FLAG_KV_F16) ? KV_F16 : KV_F32);
+    m->kvtype = (cfg->flags & QW3_FLAG_KV_Q4) ? KV_Q4 : (cfg->flags & QW3_FLAG_KV_Q8) ? KV_Q8 : ((cfg->flags & QW3_FLAG_KV_F16) ? KV_F16 : KV_F32);
     m->act_q8 = (cfg->flags & QW3_FLAG_ACT_Q8) != 0;
     m->q4k = (cfg->flags & QW3_FLAG_WEIGHTS_Q4_K) != 0;
     auto bail = [&](int rc) {
@@ -851,9 +893,11 @@ int qw3_create(const qw3_config *cfg, const qw3_weights *w, void *cuda_stream, q
     // half values, or of q8_0 rows (hd/32 blocks of 34 bytes; the capacity
     // rounded up to 32 positions so every head and every 32-position tile
     // starts 16-byte aligned, and 64 bytes of tail for the last bulk copy's
-    // rounding to 16 bytes)
-    const size_t cap = m->kvtype == KV_Q8 ? (static_cast<size_t>(c.max_seq_len) + 31) / 32 * 32
-                                          : static_cast<size_t>(c.max_seq_len);
+    // rounding to 16 bytes); the 4-bit layout of kv_q4.cu takes the same
+    // strides, its capacity a multiple of 32 too
+    const size_t cap = m->kvtype == KV_Q8 || m->kvtype == KV_Q4 ? (static_cast<size_t>(c.max_seq_len) + 31) / 32 * 32
+                                                                : static_cast<size_t>(c.max_seq_len);
+    m->kv_cap = static_cast<int>(cap);
     m->head_stride = cap * kv_row_units(m->kvtype, hd);
     m->kvsel_stride = m->head_stride * nkv;
     m->seq_stride = 2 * m->kvsel_stride;
@@ -884,6 +928,16 @@ int qw3_create(const qw3_config *cfg, const qw3_weights *w, void *cuda_stream, q
         e = A(reinterpret_cast<void **>(&m->attn_cpart),
               static_cast<size_t>(nkv) * kAttnLongClusters * (nh / nkv) * (hd + 4) * 4);
     if (e == cudaSuccess && m->attn_long_c > 0) e = A(reinterpret_cast<void **>(&m->attn_ccnt), 64 * 4);
+    if (e == cudaSuccess && m->kvtype == KV_Q4) {
+        // the attention's runs: the largest of what any batch or a short forward needs
+        size_t ws = 0;
+        for (int B = 1; B <= Bm; ++B) ws = std::max(ws, kv_q4_attn_workspace_bytes(B, 1, nh, nkv, hd, c.max_seq_len));
+        for (int r = 1; r <= kQ4MaxRows; ++r)
+            ws = std::max(ws, kv_q4_attn_workspace_bytes(1, r, nh, nkv, hd, c.max_seq_len));
+        e = A(reinterpret_cast<void **>(&m->q4_ws), ws);
+        if (e == cudaSuccess && c.max_prefill > kQ4MaxRows)
+            e = A(reinterpret_cast<void **>(&m->q4_rows), static_cast<size_t>(2) * nkv * c.max_seq_len * hd * 4);
+    }
     if (e == cudaSuccess) e = A(reinterpret_cast<void **>(&m->argmax_key), static_cast<size_t>(Bm) * 8);
     if (e == cudaSuccess) e = A(reinterpret_cast<void **>(&m->d_tok), static_cast<size_t>(Bm) * 4);
     if (e == cudaSuccess) e = A(reinterpret_cast<void **>(&m->d_pos), static_cast<size_t>(Bm) * 4);
@@ -962,16 +1016,39 @@ int forward_rows(qw3_model *m, int32_t seq, const int32_t *tokens_dev, int32_t n
             void *kvl = kv_at(m, l, 0);
             M_TRY(m, launch_rmsnorm_rows(m->px, M, H, L.attn_norm, c.rms_eps, m->ph, s));
             M_TRY(m, lin_gemm(m, m->ph, M, H, L.qkv, m->pqkv, GEMV_STORE, nullptr, nullptr, s));
-            M_TRY(m, launch_qk_rope_append(m->pqkv, M, m->qkv_w, L.q_norm, L.k_norm, c.rms_eps, m->rope, nullptr, seq,
-                                           nullptr, pos0, kvl, m->seq_stride, m->kvsel_stride, m->head_stride, nh,
-                                           nkv, hd, m->kvtype, s));
-            if (m->kvpack && M >= kAttnPrefillTcMinRows) {
-                M_TRY(m, launch_attn_prefill_tc(m->pqkv, M, m->qkv_w, kv_at(m, l, seq), m->kvsel_stride,
-                                                m->head_stride, pos0, nh, nkv, hd, scale, m->po, m->kvpack,
-                                                m->d_status, m->kvtype, s));
+            const void *kv_seq = kv_at(m, l, seq);
+            size_t kvsel = m->kvsel_stride, kvhead = m->head_stride;
+            int kvtype = m->kvtype;
+            if (m->kvtype == KV_Q4) {
+                const KvQ4 kq = kv_q4_layer(m, l);
+                const KvQ4Rows at{nullptr, seq, nullptr, pos0}, all{nullptr, seq, nullptr, 0};
+                M_TRY(m, launch_kv_q4_append(m->pqkv, M, m->qkv_w, L.q_norm, L.k_norm, c.rms_eps, m->rope, kq, hd, at,
+                                             nh, m->pqkv, m->qkv_w, m->d_status, s));
+                if (M > kQ4MaxRows) {
+                    // longer chunks attend over the rows read back as f32: one
+                    // pass over the context, small beside the chunk's attention
+                    kvhead = static_cast<size_t>(c.max_seq_len) * hd;
+                    kvsel = kvhead * nkv;
+                    M_TRY(m, launch_kv_q4_read(kq, hd, all, pos0 + M, m->q4_rows, m->q4_rows + kvsel, hd, kvhead, s));
+                    kv_seq = m->q4_rows;
+                    kvtype = KV_F32;
+                }
             } else {
-                M_TRY(m, launch_attn_prefill(m->pqkv, M, m->qkv_w, kv_at(m, l, seq), m->kvsel_stride, m->head_stride,
-                                             pos0, nh, nkv, hd, scale, m->po, m->kvtype, s));
+                M_TRY(m, launch_qk_rope_append(m->pqkv, M, m->qkv_w, L.q_norm, L.k_norm, c.rms_eps, m->rope, nullptr,
+                                               seq, nullptr, pos0, kvl, m->seq_stride, m->kvsel_stride, m->head_stride,
+                                               nh, nkv, hd, m->kvtype, s));
+            }
+            if (kvtype == KV_Q4) {
+                KvQ4AttnArgs a = q4_attn_args(m, l, m->pqkv, 1, M, m->po);
+                a.slot0 = seq;
+                a.len_add = pos0 + M;
+                M_TRY(m, launch_kv_q4_attn(a, hd, s));
+            } else if (m->kvpack && M >= kAttnPrefillTcMinRows) {
+                M_TRY(m, launch_attn_prefill_tc(m->pqkv, M, m->qkv_w, kv_seq, kvsel, kvhead, pos0, nh, nkv, hd, scale,
+                                                m->po, m->kvpack, m->d_status, kvtype, s));
+            } else {
+                M_TRY(m, launch_attn_prefill(m->pqkv, M, m->qkv_w, kv_seq, kvsel, kvhead, pos0, nh, nkv, hd, scale,
+                                             m->po, kvtype, s));
             }
             M_TRY(m, lin_gemm(m, m->po, M, qw, L.o, m->px, GEMV_RESID, nullptr, nullptr, s));
             M_TRY(m, launch_rmsnorm_rows(m->px, M, H, L.ffn_norm, c.rms_eps, m->ph, s));
@@ -1050,9 +1127,12 @@ int qw3_decode(qw3_model *m, int32_t B, const int32_t *seqs_host, const int32_t 
     return QW3_OK;
 }
 
-int qw3_generate_greedy(qw3_model *m, int32_t B, const int32_t *seqs_host, int32_t n_steps,
-                        const int32_t *first_tokens_dev, int32_t *out_tokens_dev) {
-    if (check_model(m)) return QW3_ERR_INVALID_ARG;
+namespace {
+
+// n_steps decode steps for B sequences from first_tokens_dev: the checks of a
+// generation, the device state it starts from.
+int begin_generate(qw3_model *m, int32_t B, const int32_t *seqs_host, int32_t n_steps, const int32_t *first_tokens_dev,
+                   const int32_t *out_tokens_dev, const DecodeIO &io, std::vector<int32_t> &seqs) {
     const qw3_config &c = m->cfg;
     if (B < 1 || B > c.max_seqs) return fail(m, QW3_ERR_INVALID_ARG, "batch must be in [1, max_seqs]");
     if (n_steps < 0 || !first_tokens_dev || (n_steps > 0 && !out_tokens_dev))
@@ -1060,7 +1140,8 @@ int qw3_generate_greedy(qw3_model *m, int32_t B, const int32_t *seqs_host, int32
     if (misaligned(first_tokens_dev, 4) || misaligned(out_tokens_dev, 4))
         return fail(m, QW3_ERR_INVALID_ARG, "device buffers must be 4-byte aligned");
     if (n_steps == 0) return QW3_OK;
-    std::vector<int32_t> seqs(B), pos(B);
+    seqs.resize(B);
+    std::vector<int32_t> pos(B);
     std::vector<char> seen(c.max_seqs, 0);
     for (int b = 0; b < B; ++b) {
         const int sq = seqs_host ? seqs_host[b] : b;
@@ -1072,21 +1153,60 @@ int qw3_generate_greedy(qw3_model *m, int32_t B, const int32_t *seqs_host, int32
         seqs[b] = sq;
         pos[b] = m->seq_len[sq];
     }
-    DecodeIO io{nullptr, nullptr, out_tokens_dev, nullptr};
     const int32_t zero = 0;
     M_TRY(m, cudaMemcpyAsync(m->d_seq, seqs.data(), B * 4, cudaMemcpyHostToDevice, m->stream));
     M_TRY(m, cudaMemcpyAsync(m->d_pos, pos.data(), B * 4, cudaMemcpyHostToDevice, m->stream));
     M_TRY(m, cudaMemcpyAsync(m->d_io, &io, sizeof io, cudaMemcpyHostToDevice, m->stream));
     M_TRY(m, cudaMemcpyAsync(m->d_step, &zero, 4, cudaMemcpyHostToDevice, m->stream));
     M_TRY(m, cudaMemcpyAsync(m->d_tok, first_tokens_dev, B * 4, cudaMemcpyDeviceToDevice, m->stream));
-    for (int sidx = 0; sidx < n_steps; ++sidx) {
-        if (m->step && B == 1) {
-            M_TRY(m, launch_step(m->sp, m->stream));
-        } else if (int rc = run_decode_step(m, B)) {
-            return rc;
-        }
+    return QW3_OK;
+}
+
+int one_step(qw3_model *m, int B) {
+    if (m->step && B == 1) {
+        M_TRY(m, launch_step(m->sp, m->stream));
+        return QW3_OK;
     }
-    for (int b = 0; b < B; ++b) m->seq_len[seqs[b]] += n_steps;
+    return run_decode_step(m, B);
+}
+
+}  // namespace
+
+int qw3_generate_greedy(qw3_model *m, int32_t B, const int32_t *seqs_host, int32_t n_steps,
+                        const int32_t *first_tokens_dev, int32_t *out_tokens_dev) {
+    if (check_model(m)) return QW3_ERR_INVALID_ARG;
+    std::vector<int32_t> seqs;
+    const DecodeIO io{nullptr, nullptr, out_tokens_dev, nullptr};
+    if (int rc = begin_generate(m, B, seqs_host, n_steps, first_tokens_dev, out_tokens_dev, io, seqs)) return rc;
+    for (int sidx = 0; sidx < n_steps; ++sidx)
+        if (int rc = one_step(m, B)) return rc;
+    for (const int sq : seqs) m->seq_len[sq] += n_steps;
+    return QW3_OK;
+}
+
+int qw3_generate_sample(qw3_model *m, int32_t B, const int32_t *seqs_host, int32_t n_steps,
+                        const int32_t *first_tokens_dev, const float *temperature_dev, const int32_t *top_k_dev,
+                        const float *top_p_dev, const float *min_p_dev, const float *u_dev, float *logits_dev,
+                        int32_t *out_tokens_dev, float *prob_dev) {
+    if (check_model(m)) return QW3_ERR_INVALID_ARG;
+    const int V = m->cfg.vocab;
+    if (n_steps > 0 && (!u_dev || !logits_dev))
+        return fail(m, QW3_ERR_INVALID_ARG, "sampling needs uniform numbers and a logits buffer");
+    if (misaligned(temperature_dev, 4) || misaligned(top_k_dev, 4) || misaligned(top_p_dev, 4) ||
+        misaligned(min_p_dev, 4) || misaligned(u_dev, 4) || misaligned(logits_dev, 4) || misaligned(prob_dev, 4))
+        return fail(m, QW3_ERR_INVALID_ARG, "device buffers must be 4-byte aligned");
+    if (V > kSampleMaxVocab) return fail(m, QW3_ERR_SHAPE, "sampling takes a vocabulary of up to 4194304");
+    std::vector<int32_t> seqs;
+    const DecodeIO io{logits_dev, nullptr, nullptr, nullptr};
+    if (int rc = begin_generate(m, B, seqs_host, n_steps, first_tokens_dev, out_tokens_dev, io, seqs)) return rc;
+    for (int sidx = 0; sidx < n_steps; ++sidx) {
+        if (int rc = one_step(m, B)) return rc;
+        const size_t at = static_cast<size_t>(sidx) * B;
+        const SampleArgs a{logits_dev, V, V, temperature_dev, top_k_dev, top_p_dev, min_p_dev, u_dev + at,
+                           out_tokens_dev + at, m->d_tok, prob_dev ? prob_dev + at : nullptr, m->d_status};
+        M_TRY(m, launch_sample(a, B, m->stream));
+    }
+    for (const int sq : seqs) m->seq_len[sq] += n_steps;
     return QW3_OK;
 }
 
@@ -1120,6 +1240,12 @@ int qw3_debug_read_kv(qw3_model *m, int32_t layer, int32_t seq, int32_t pos0, in
     if (layer < 0 || layer >= c.n_layers || pos0 < 0 || n < 0 || static_cast<int64_t>(pos0) + n > c.max_seq_len ||
         !k_out_dev || !v_out_dev || misaligned(k_out_dev, 4) || misaligned(v_out_dev, 4))
         return fail(m, QW3_ERR_INVALID_ARG, "bad KV read range");
+    if (m->kvtype == KV_Q4) {
+        const KvQ4Rows rows{nullptr, seq, nullptr, pos0};
+        M_TRY(m, launch_kv_q4_read(kv_q4_layer(m, layer), c.head_dim, rows, n, k_out_dev, v_out_dev,
+                                   static_cast<size_t>(c.n_kv_heads) * c.head_dim, c.head_dim, m->stream));
+        return QW3_OK;
+    }
     M_TRY(m, launch_copy_kv_rows(kv_at(m, layer, seq), m->kvsel_stride, m->head_stride, pos0, n, c.n_kv_heads,
                                  c.head_dim, k_out_dev, v_out_dev, m->kvtype, m->stream));
     return QW3_OK;
@@ -1152,6 +1278,9 @@ int qw3_decode_plan(const qw3_model *m, int32_t B, int32_t *persistent, int32_t 
     *persistent = 0;
     *launches_per_step = use_gemv(c, B) ? ((c.flags & QW3_FLAG_WEIGHTS_Q4_K) ? 3 : 2) + 5 * c.n_layers
                                         : 4 + 7 * c.n_layers;
+    // the 4-bit cache: the append and the attention's second kernel besides
+    if (m->kvtype == KV_Q4)
+        *launches_per_step += c.n_layers * kv_q4_attn_launches(B, 1, c.n_heads, c.n_kv_heads, c.max_seq_len);
     return QW3_OK;
 }
 
@@ -1277,8 +1406,6 @@ int qw3_q8_0_gemv_q8act(const void *W_dev, int32_t rows, int32_t cols, const flo
 
 namespace {
 
-constexpr int kQ4MaxRows = 16, kQ4MaxGroup = 16;
-
 // Checks of a 4-bit cache and of a head count over it.
 int check_kv_q4(const qw3_kv_q4 *c, int n_heads) {
     if (!c || !c->data) return fail(nullptr, QW3_ERR_INVALID_ARG, "null cache");
@@ -1356,6 +1483,7 @@ int qw3_kv_q4_read(const qw3_kv_q4 *cache, int32_t M, const int32_t *slots_dev, 
         return fail(nullptr, QW3_ERR_INVALID_ARG, "outputs must be 4-byte aligned");
     KvQ4Rows rows{slots_dev, slot0, pos_dev, pos0};
     QW3_CUDA_TRY(launch_kv_q4_read(kv_q4_view(cache), cache->head_dim, rows, M, k_out_dev, v_out_dev,
+                                   static_cast<size_t>(cache->n_kv_heads) * cache->head_dim, cache->head_dim,
                                    static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }
@@ -1400,13 +1528,14 @@ int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, co
                int32_t *token_dev, float *prob_dev, int32_t *status_dev, void *stream) {
     if (B < 0 || (B > 0 && (!logits_dev || !u_dev || !token_dev)))
         return fail(nullptr, QW3_ERR_INVALID_ARG, "bad sample arguments");
-    if (V < 1 || V > (1 << 22) || stride < V) return fail(nullptr, QW3_ERR_SHAPE, "1 <= V <= 4194304, V <= stride");
+    if (V < 1 || V > kSampleMaxVocab || stride < V) return fail(nullptr, QW3_ERR_SHAPE, "1 <= V <= 4194304, V <= stride");
     if (misaligned(logits_dev, 4) || misaligned(temperature_dev, 4) || misaligned(top_k_dev, 4) ||
         misaligned(top_p_dev, 4) || misaligned(min_p_dev, 4) || misaligned(u_dev, 4) || misaligned(token_dev, 4) ||
         misaligned(prob_dev, 4) || misaligned(status_dev, 4))
         return fail(nullptr, QW3_ERR_INVALID_ARG, "device buffers must be 4-byte aligned");
-    SampleArgs a{logits_dev, stride, V, temperature_dev, top_k_dev, top_p_dev, min_p_dev, u_dev, token_dev, prob_dev,
-                 status_dev};
+    SampleArgs a{logits_dev, stride, V, temperature_dev, top_k_dev, top_p_dev, min_p_dev, u_dev, token_dev, nullptr,
+                 prob_dev, status_dev};
+    if (B == 0) return QW3_OK;
     QW3_CUDA_TRY(configure_all());   // the kernel's shared-memory limit
     QW3_CUDA_TRY(launch_sample(a, B, static_cast<cudaStream_t>(stream)));
     return QW3_OK;

@@ -279,25 +279,31 @@ struct KvQ4Rows {
 cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, const float *q_norm, const float *k_norm,
                                 float eps, const float2 *rope, const KvQ4 &c, int hd, const KvQ4Rows &rows, int nh,
                                 float *q_out, int64_t q_stride, int32_t *status, cudaStream_t s);
+// Row i of head g lands at i * out_row + g * out_head floats.
 cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M, float *k_out, float *v_out,
-                              cudaStream_t s);
+                              size_t out_row, size_t out_head, cudaStream_t s);
 
 struct KvQ4AttnArgs {
     const float *q;   // [B * rows][q_stride], nh heads of hd
     int64_t q_stride;
     KvQ4 c;
-    const int32_t *slots;   // nullable: sequence b in slot b
-    const int32_t *lens;    // [B] positions in the cache, the rows' own among them
+    const int32_t *slots;   // nullable: sequence b in slot slot0 + b
+    int slot0;
+    const int32_t *lens;    // [B]: lens[b] + len_add positions in the cache, the
+    int len_add;            // rows' own among them (nullable: len_add alone)
     int B, rows, max_len, nh;
     float scale;
     float *out;
     int64_t out_stride;
     float *ws;
 };
+constexpr int kQ4MaxRows = 16, kQ4MaxGroup = 16;
+int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len);
 size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len);
 cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, cudaStream_t s);
 
 // ---- sampling (sample.cu)
+constexpr int kSampleMaxVocab = 1 << 22;   // sums of 2^40 each stay below 2^63
 struct SampleArgs {
     const float *logits;   // [B][stride]
     int64_t stride;
@@ -307,6 +313,7 @@ struct SampleArgs {
     const float *top_p, *min_p;
     const float *u;   // [B]
     int32_t *token;   // [B]
+    int32_t *next;    // nullable [B]: the token to feed next (0 for one that has none)
     float *prob;      // nullable [B]
     int32_t *status;
 };
@@ -473,7 +480,8 @@ __device__ __forceinline__ __half kv_cvt<__half>(float v) { return __float2half_
 struct kvq8 {
     uint8_t b;
 };
-enum KvType : int { KV_F32 = 0, KV_F16 = 1, KV_Q8 = 2 };
+// KV_Q4: the 4-bit cache of kv_q4.cu, which has kernels of its own.
+enum KvType : int { KV_F32 = 0, KV_F16 = 1, KV_Q8 = 2, KV_Q4 = 3 };
 template <typename KT>
 struct kv_is_q8 {
     static constexpr bool value = false;
@@ -485,7 +493,10 @@ struct kv_is_q8<kvq8> {
 // Elements of type KT in one cached row of head_dim HD.
 template <typename KT, int HD>
 __host__ __device__ constexpr int kv_row() { return kv_is_q8<KT>::value ? HD / 32 * 34 : HD; }
-inline size_t kv_row_units(int kvtype, int hd) { return kvtype == KV_Q8 ? static_cast<size_t>(hd) / 32 * 34 : hd; }
+inline size_t kv_row_units(int kvtype, int hd) {
+    if (kvtype == KV_Q4) return static_cast<size_t>(hd) / 16 * 9;   // codes and scales, in planes of their own
+    return kvtype == KV_Q8 ? static_cast<size_t>(hd) / 32 * 34 : hd;
+}
 inline size_t kv_unit_bytes(int kvtype) { return kvtype == KV_F32 ? 4 : (kvtype == KV_F16 ? 2 : 1); }
 
 // Value d of a cached row (any element type).

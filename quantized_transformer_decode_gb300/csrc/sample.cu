@@ -330,7 +330,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
     if (bad || greedy) {
         if (row.rank == 0 && tid == 0) {
             if (bad) record_status(a.status, QW3_ERR_NONFINITE);
-            a.token[b] = bad ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
+            const int arg = bad ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
+            a.token[b] = arg;
+            if (a.next) a.next[b] = max(arg, 0);
             if (a.prob) a.prob[b] = bad ? 0.0f : 1.0f;
         }
         return;
@@ -406,6 +408,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
             w += weight(i, seen);
             if (w > at) {
                 a.token[b] = row.base + i;
+                if (a.next) a.next[b] = row.base + i;
                 if (a.prob)
                     a.prob[b] = static_cast<float>(exp((static_cast<double>(row.l[i]) - row.top) / fmaxf(T, 1e-30f)) *
                                                    static_cast<double>(kOne) / static_cast<double>(total));
@@ -443,6 +446,7 @@ cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s) {
         if (x.min_p) x.min_p += b0;
         x.u += b0;
         x.token += b0;
+        if (x.next) x.next += b0;
         if (x.prob) x.prob += b0;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(size, std::min(65535, B - b0));

@@ -37,11 +37,12 @@ QW3_FLAG_KV_F16 = 0x20
 QW3_FLAG_ACT_Q8 = 0x40
 QW3_FLAG_KV_Q8 = 0x80
 QW3_FLAG_WEIGHTS_Q4_K = 0x100
+QW3_FLAG_KV_Q4 = 0x200
 
 # Every entry point of include/qw3.h, in declaration order.
 EXPORTS = (
     "qw3_create", "qw3_destroy", "qw3_prefill", "qw3_forward_all_logits", "qw3_decode", "qw3_generate_greedy",
-    "qw3_reset", "qw3_truncate", "qw3_seq_len", "qw3_debug_read_kv", "qw3_debug_read_trace",
+    "qw3_generate_sample", "qw3_reset", "qw3_truncate", "qw3_seq_len", "qw3_debug_read_kv", "qw3_debug_read_trace",
     "qw3_decode_plan", "qw3_sync", "qw3_stream", "qw3_status_string", "qw3_last_error",
     "qw3_q8_0_quantize", "qw3_q8_0_dequantize", "qw3_q8_0_gemv", "qw3_q8_0_gemv_q8act",
     "qw3_q4_k_quantize", "qw3_q4_k_dequantize", "qw3_q4_k_gemv", "qw3_q8_0_gemv_splitk_noalloc",
@@ -112,6 +113,7 @@ def lib() -> ctypes.CDLL:
         "qw3_forward_all_logits": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P]),
         "qw3_decode": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P]),
         "qw3_generate_greedy": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P]),
+        "qw3_generate_sample": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
         "qw3_reset": (ctypes.c_int, [_P, _I32]),
         "qw3_truncate": (ctypes.c_int, [_P, _I32, _I32]),
         "qw3_seq_len": (ctypes.c_int, [_P, _I32, ctypes.POINTER(_I32)]),
@@ -193,6 +195,14 @@ def qw3_decode(h: int, B: int, seqs: Optional[Sequence[int]], tokens_ptr: int, p
 def qw3_generate_greedy(h: int, B: int, seqs: Optional[Sequence[int]], n_steps: int, first_ptr: int,
                         out_ptr: int) -> None:
     _check(lib().qw3_generate_greedy(h, B, _i32_array(seqs), n_steps, first_ptr, out_ptr or None), h)
+
+
+def qw3_generate_sample(h: int, B: int, seqs: Optional[Sequence[int]], n_steps: int, first_ptr: int,
+                        temperature_ptr: int, top_k_ptr: int, top_p_ptr: int, min_p_ptr: int, u_ptr: int,
+                        logits_ptr: int, out_ptr: int, prob_ptr: int = 0) -> None:
+    _check(lib().qw3_generate_sample(h, B, _i32_array(seqs), n_steps, first_ptr, temperature_ptr or None,
+                                     top_k_ptr or None, top_p_ptr or None, min_p_ptr or None, u_ptr or None,
+                                     logits_ptr or None, out_ptr or None, prob_ptr or None), h)
 
 
 def qw3_reset(h: int, seq: int) -> None:
@@ -698,6 +708,28 @@ class Qw3Model:
         with _Ordered(self):
             qw3_generate_greedy(self.h, B, seqs, n_steps, first_tokens.data_ptr(), out.data_ptr())
         return out
+
+    def generate_sample(self, first_tokens, n_steps: int, u, temperature=None, top_k=None, top_p=None, min_p=None,
+                        seqs: Optional[Sequence[int]] = None):
+        """n_steps sampled steps (qw3_generate_sample) from CUDA tensors:
+        first_tokens [B], u f32 [n_steps, B] in [0, 1), the settings [B] each
+        (f32; top_k int32) or left out. Returns (tokens int32 [n_steps, B],
+        probabilities f32 [n_steps, B])."""
+        torch = _torch()
+        first_tokens = first_tokens.to(torch.int32).contiguous()
+        B, dev = first_tokens.numel(), first_tokens.get_device()
+        _on(dev, torch.float32, u=u, temperature=temperature, top_p=top_p, min_p=min_p)
+        _on(dev, torch.int32, top_k=top_k)
+        if u.numel() != n_steps * B or any(t is not None and t.numel() != B for t in (temperature, top_k, top_p, min_p)):
+            raise Qw3Error(QW3_ERR_SHAPE, "u holds n_steps * B numbers, a setting B")
+        logits = torch.empty((B, self.shape.vocab), dtype=torch.float32, device=first_tokens.device)
+        out = torch.empty((n_steps, B), dtype=torch.int32, device=first_tokens.device)
+        prob = torch.empty((n_steps, B), dtype=torch.float32, device=first_tokens.device)
+        with _Ordered(self):
+            qw3_generate_sample(self.h, B, seqs, n_steps, first_tokens.data_ptr(), _ptr(temperature), _ptr(top_k),
+                                _ptr(top_p), _ptr(min_p), u.data_ptr(), logits.data_ptr(), out.data_ptr(),
+                                prob.data_ptr())
+        return out, prob
 
     def reset(self, seq: int) -> None:
         qw3_reset(self.h, seq)
