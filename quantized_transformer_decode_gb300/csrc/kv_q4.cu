@@ -277,10 +277,14 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 //
 // out = sum_j softmax_j(scale q.K_j) V_j over the 4-bit rows. The columns of
 // one kv head (its group's heads times the query rows) share every cached
-// byte, so a CTA takes up to 16 columns of one kv head and sequence over a run
-// of positions; runs merge in a second small kernel. A warp takes tiles of 32
-// positions and multiplies with mma.m16n8k16 (f16 in, f32 out), positions
-// along m for S = K Q^T, dimensions along m for O = V^T P^T:
+// byte: a unit of work is up to 8 columns of one kv head and sequence, a block
+// of it 128 positions. The blocks of all units in one row are dealt to the
+// CTAs in equal contiguous shares (the lengths are on the device: each CTA sums
+// them), so that sequences of any lengths keep every SM busy to the end; a unit
+// that a share's end cuts leaves partial results, which a second small kernel
+// joins. A warp takes tiles of 32 positions and multiplies with mma.m16n8k16
+// (f16 in, f32 out), positions along m for S = K Q^T, dimensions along m for O
+// = V^T P^T:
 //  - codes are exact in f16 (-8..7): a word of 8 codes becomes 4 half2
 //    operands with 9 instructions and no scale. K scales multiply the f32 sums
 //    of a 32-value block, V scales the probabilities of their position.
@@ -295,15 +299,23 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 //    again with positions along k: one 8x8 transpose in registers each.
 // A chain of products in the tensor core is 2 instructions long; the sums over
 // blocks and tiles are f32 with rounding to nearest. mma.sync rather than
-// tcgen05: with 8 or 16 columns the product is bound by what the operands
-// cost (bytes, then the unpacking), and registers to registers saves writing
-// the unpacked codes to shared memory and reading them back.
+// tcgen05: with at most 8 columns the product is bound by what the codes cost
+// (bytes, then the unpacking), and registers to registers saves writing the
+// unpacked codes to shared memory and reading them back.
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// The first of a chain: d = a b.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -346,16 +358,16 @@ __device__ __forceinline__ float half_of(uint32_t w, int i) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(i ? w >> 16 : w)));
 }
 
-constexpr int kQ4Warps = 4, kQ4Tile = 32;
+constexpr int kQ4Warps = 4, kQ4Tile = 32, kQ4Block = kQ4Warps * kQ4Tile;
 
 // Positions of sequence b, within what the call allows.
 __device__ __forceinline__ int q4_len(const KvQ4AttnArgs &a, int b) {
     return min(max(a.lens ? a.lens[b] : 0, -a.len_add) + a.len_add, a.max_len);
 }
 
-// Columns that one CTA of width class W takes, and its 8-column operands: W =
-// 1, 2, 4 with hi and lo in one operand; 8 and 16 with operands of their own.
-__host__ __device__ constexpr int q4_ops(int W) { return W <= 4 ? 1 : W / 4; }
+// A CTA of width class W takes W columns in q4_ops(W) operands of 8: W = 1, 2,
+// 4 with hi and lo in one operand, 8 with one for each.
+__host__ __device__ constexpr int q4_ops(int W) { return W <= 4 ? 1 : 2; }
 
 template <int HD>
 struct Q4Words {   // words of a thread's share of a row
@@ -375,126 +387,205 @@ __device__ __forceinline__ void ld_words(uint32_t (&d)[N], const void *p) {
     }
 }
 
-// Partial results of a CTA: per column acc[HD], then log2 of their unit and
-// the sum of weights.
+// Partial results: per column acc[HD], then log2 of their unit and the sum of
+// weights.
 template <int HD>
 __host__ __device__ constexpr int q4_part() { return HD + 2; }
 
-template <int HD, int W>
-__global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(KvQ4AttnArgs a, int chunk, int nsplit,
-                                                                             int cgroups) {
-    constexpr int NB = HD / 32, NT = q4_ops(W), SC = W <= 8 ? 1 : W / 8;
-    constexpr int DUP = W <= 4 ? 4 / W : 1;          // blocks that share an operand
-    constexpr int NI = (NB + DUP - 1) / DUP;         // P operands per 16 positions
-    constexpr int MT = W <= 8 ? 2 : 1;               // 16-position halves held at once
-    constexpr int TILE = 16 * MT;
-    using Wd = Q4Words<HD>;
-    extern __shared__ __align__(16) float q4_smem[];
-    // [warp][W][q4_part]: the warps' results; before that the q operands
-    uint2 *qfrag = reinterpret_cast<uint2 *>(q4_smem);   // [NB * 2][NT][32]
-    __shared__ float s_exp[W];
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-    const int split = blockIdx.x, g = blockIdx.y / cgroups, cg = blockIdx.y % cgroups, b = blockIdx.z;
-    const int G = a.nh / a.c.nkv, cols = G * a.rows, col0 = cg * W, ncol = min(W, cols - col0);
-    const int slot = a.slots ? a.slots[b] : a.slot0 + b;
+// Blocks of sequence b (one at least: a sequence without positions still has
+// outputs to write) and, if asked, its length and slot.
+__device__ __forceinline__ int q4_blocks(const KvQ4AttnArgs &a, int b, int *len_out = nullptr, int *slot_out = nullptr) {
+    const int slot = a.slots ? __ldg(a.slots + b) : a.slot0 + b;
     const bool there = slot >= 0 && slot < a.c.slots;
     const int len = there ? q4_len(a, b) : 0;
+    if (len_out) *len_out = len;
+    if (slot_out) *slot_out = there ? slot : 0;
+    return max(1, (len + kQ4Block - 1) / kQ4Block);
+}
+
+// Sum over the block's threads; red: kQ4Warps values.
+__device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kQ4Warps; ++w) v += red[w];
+    return v;
+}
+
+// Workspace: two partial results of W columns for each CTA (of the unit that
+// its share begins inside, and of the one that it ends inside), then the first
+// and the last CTA of each unit.
+template <int HD, int W>
+__global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
+    constexpr int NB = HD / 32, NT = q4_ops(W);
+    constexpr int DUP = W <= 4 ? 4 / W : 1;          // blocks that share an operand
+    constexpr int NI = (NB + DUP - 1) / DUP;         // P operands per 16 positions
+    constexpr int MT = kQ4Tile / 16;
+    constexpr int PS = q4_part<HD>();
+    constexpr int QS = HD + 8;                       // a q row in shared memory, padded
+    using Wd = Q4Words<HD>;
+    extern __shared__ __align__(16) float q4_smem[];   // [warp][W][PS]: the warps' results
+    __shared__ __align__(16) __half s_q[W][2][QS];      // hi and lo; see below for the order of a row
+    __shared__ float s_exp[W];
+    __shared__ int64_t s_red[kQ4Warps];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    const int G = a.nh / a.c.nkv, cols = G * a.rows, U = a.c.nkv * cgroups;
+
+    // ---- this CTA's share [at, stop) of the blocks
+    int64_t mine = 0;
+    for (int i = tid; i < a.B; i += kQ4Warps * 32) mine += q4_blocks(a, i);
+    const int64_t all = q4_sum(mine, s_red);
+    // no share is empty: the join counts on every CTA between a unit's first and last
+    const int64_t total = all * U, P = min(static_cast<int64_t>(gridDim.x), total);
+    if (blockIdx.x >= P) return;
+    int64_t at = total * blockIdx.x / P;
+    const int64_t stop = total * (blockIdx.x + 1) / P;
+    // its first sequence: sums of 128 sequences at a time, then one by one
+    int b = 0;
+    int64_t before = 0;   // blocks of the sequences below b (of one unit)
+    if (a.B > 1) {
+        const int64_t want = at / U;
+        for (int b0 = 0; b0 < a.B; b0 += kQ4Warps * 32) {
+            const int64_t n = b0 + tid < a.B ? q4_blocks(a, b0 + tid) : 0;
+            int64_t run = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += x;
+            }
+            __syncthreads();
+            if (lane == 31) s_red[warp] = run;
+            __syncthreads();
+            int64_t lead = before, sum = 0;
+#pragma unroll
+            for (int w = 0; w < kQ4Warps; ++w) {
+                if (w < warp) lead += s_red[w];
+                sum += s_red[w];
+            }
+            if (want < before + sum) {
+                __syncthreads();
+                if (n > 0 && lead + run - n <= want && want < lead + run) {
+                    s_red[0] = b0 + tid;
+                    s_red[1] = lead + run - n;
+                }
+                __syncthreads();
+                b = static_cast<int>(s_red[0]);
+                before = s_red[1];
+                break;
+            }
+            before += sum;
+        }
+    }
+
+    for (; at < stop; ) {
+    // ---- the next piece: blocks [blk0, blk1) of unit (b, g, cg)
+    int len, slot;
+    const int blocks = q4_blocks(a, b, &len, &slot);
+    const int64_t in_b = at - before * U;
+    const int unit = static_cast<int>(in_b / blocks), g = unit / cgroups, cg = unit % cgroups;
+    const int blk0 = static_cast<int>(in_b - static_cast<int64_t>(unit) * blocks);
+    const int blk1 = static_cast<int>(min(static_cast<int64_t>(blocks), blk0 + (stop - at)));
+    const int col0 = cg * W, ncol = min(W, cols - col0);
     // positions that this group's last column sees
     const int seen = len - a.rows + (col0 + ncol - 1) / G + 1;
-    const int start = split * chunk, end = min(seen, start + chunk);
-    if (start >= end && nsplit > 1) return;   // the merge leaves empty runs out by the same rule
+    const int start = blk0 * kQ4Block, end = min(seen, blk1 * kQ4Block);
+    at += blk1 - blk0;
 
-    // ---- q columns: scaled by a power of two, split into hi and lo
-    for (int j = warp; j < W; j += kQ4Warps) {
-        float amax = 0.0f;
-        if (j < ncol) {
-            const int cc = col0 + j;
-            const float *qp = a.q + (static_cast<int64_t>(b) * a.rows + cc / G) * a.q_stride +
-                              static_cast<int64_t>(g * G + cc % G) * HD;
-            for (int d = lane; d < HD; d += 32) amax = fmaxf(amax, fabsf(qp[d]));
-            amax = warp_max(amax);
-        }
-        if (lane == 0) s_exp[j] = static_cast<float>(f16_row_exp(amax));
-    }
-    __syncthreads();
-    for (int i = tid; i < NB * 2 * NT * 32; i += kQ4Warps * 32) {
-        const int l = i & 31, nt = (i >> 5) % NT, ks = (i >> 5) / NT, blk = ks >> 1, st = ks & 1;
-        const int n = l >> 2, cq = l & 3;
-        const int j = W <= 4 ? (n & 3) % W : (nt % SC) * 8 + n;
-        const bool low = W <= 4 ? n >= 4 : nt >= SC;
-        uint32_t o[2] = {0u, 0u};
-        if (j < ncol) {
-            const int cc = col0 + j;
-            const float *qp = a.q + (static_cast<int64_t>(b) * a.rows + cc / G) * a.q_stride +
-                              static_cast<int64_t>(g * G + cc % G) * HD + blk * 32 + cq * 8;
-            const float f = pow2_f32(static_cast<int>(s_exp[j]));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float x0 = qp[2 * st + h] * f, x1 = qp[2 * st + h + 4] * f;
-                __half2 v = __floats2half2_rn(x0, x1);
-                if (low) {
-                    const float2 t = __half22float2(v);
-                    v = __floats2half2_rn(x0 - t.x, x1 - t.y);
-                }
-                o[h] = *reinterpret_cast<const uint32_t *>(&v);
-            }
-        }
-        qfrag[i] = make_uint2(o[0], o[1]);
-    }
-    __syncthreads();
-    constexpr bool kQRegs = W <= 8;
-    uint32_t qf[kQRegs ? NB * 2 : 1][kQRegs ? NT : 1][2];
-    if constexpr (kQRegs) {
-#pragma unroll
-        for (int ks = 0; ks < NB * 2; ++ks)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint2 t = qfrag[(ks * NT + nt) * 32 + lane];
-                qf[ks][nt][0] = t.x;
-                qf[ks][nt][1] = t.y;
-            }
-    }
-    // this thread's score columns: 2c and 2c + 1 of each set
-    float cscale[SC][2];
-    int lim[SC][2];
-#pragma unroll
-    for (int s = 0; s < SC; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int j = W <= 4 ? (2 * c + e) % 4 % W : 8 * s + 2 * c + e;
-            cscale[s][e] = a.scale * 1.4426950408889634f * pow2_f32(-static_cast<int>(s_exp[j]));
-            lim[s][e] = j < ncol ? len - a.rows + (col0 + j) / G + 1 : 0;
-        }
-    int low_lim = len - a.rows + col0 / G + 1;   // positions that every column sees
-
-    const uint8_t *kc = kv_q4_codes<HD>(a.c, there ? slot : 0, 0, g), *vc = kv_q4_codes<HD>(a.c, there ? slot : 0, 1, g);
-    const __half *ksc = kv_q4_scales<HD>(a.c, there ? slot : 0, 0, g), *vsc = kv_q4_scales<HD>(a.c, there ? slot : 0, 1, g);
+    // Row i of an operand along m holds position i/2 or 4 + i/2 of its eight
+    // (even, odd), so that the four positions that a load of V takes lie next
+    // to each other.
+    const int pr = (r >> 1) | ((r & 1) << 2);
+    const size_t first = static_cast<size_t>(start) + warp * kQ4Tile;
+    const uint8_t *kp = kv_q4_codes<HD>(a.c, slot, 0, g) + (first + pr) * (HD / 2) + c * (HD / 8);
+    const uint8_t *vp = kv_q4_codes<HD>(a.c, slot, 1, g) + (first + c) * (HD / 2) + r * (HD / 16);
+    const __half *ksp = kv_q4_scales<HD>(a.c, slot, 0, g) + (first + pr) * NB;
+    const __half *vsp = kv_q4_scales<HD>(a.c, slot, 1, g) + (first + pr) * NB;
 
     uint32_t kw[MT][2][Wd::K], kd[MT][2][Wd::S], vw[MT][4][Wd::V], vd[MT][2][Wd::S];
-    auto load_k = [&](int k0) {
+    auto load_k = [&]() {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const size_t j = static_cast<size_t>(k0) + 16 * m + 8 * h + r;
-                ld_words(kw[m][h], kc + j * (HD / 2) + c * (HD / 8));
-                ld_words(kd[m][h], ksc + j * NB);
+                ld_words(kw[m][h], kp + (16 * m + 8 * h) * (HD / 2));
+                ld_words(kd[m][h], ksp + (16 * m + 8 * h) * NB);
             }
+        kp += kQ4Warps * kQ4Tile * (HD / 2);
+        ksp += kQ4Warps * kQ4Tile * NB;
     };
-    auto load_v = [&](int k0) {
+    auto load_v = [&]() {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-                ld_words(vw[m][h], vc + (static_cast<size_t>(k0) + 16 * m + 2 * c + (h & 1) + 8 * (h >> 1)) * (HD / 2) +
-                                       r * (HD / 16));
+            for (int h = 0; h < 4; ++h) ld_words(vw[m][h], vp + (16 * m + 4 * h) * (HD / 2));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) ld_words(vd[m][h], vsc + (static_cast<size_t>(k0) + 16 * m + 8 * h + r) * NB);
+            for (int h = 0; h < 2; ++h) ld_words(vd[m][h], vsp + (16 * m + 8 * h) * NB);
         }
+        vp += kQ4Warps * kQ4Tile * (HD / 2);
+        vsp += kQ4Warps * kQ4Tile * NB;
     };
 
-    float acc[NB][2][NT][4], mx[SC][2], sum[SC][2];
+    int k0 = start + warp * kQ4Tile;
+    if (k0 < end) {
+        load_k();
+        load_v();
+    }
+
+    // ---- q columns, while the first rows are on their way: scaled by a power
+    // of two, split into hi and lo. Value 8 i + p of a row lies at 8 i + 2 (p &
+    // 3) + (p >> 2), so that the pairs (p, p + 4) of an operand lie together.
+    for (int j = warp; j < W; j += kQ4Warps) {
+        constexpr int E = HD / 32;
+        float x[E], amax = 0.0f;
+        const int cc = col0 + j;
+        const float *qp = a.q + (static_cast<int64_t>(b) * a.rows + cc / G) * a.q_stride +
+                          static_cast<int64_t>(g * G + cc % G) * HD;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] = j < ncol ? qp[lane + 32 * e] : 0.0f;
+            amax = fmaxf(amax, fabsf(x[e]));
+        }
+        const int t = f16_row_exp(warp_max(amax));
+        const float f = pow2_f32(t);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int d = lane + 32 * e, to = (d & ~7) | 2 * (d & 3) | ((d >> 2) & 1);
+            const float v = x[e] * f;
+            const __half hi = __float2half_rn(v);
+            s_q[j][0][to] = hi;
+            s_q[j][1][to] = __float2half_rn(v - __half2float(hi));
+        }
+        if (lane == 0) s_exp[j] = static_cast<float>(t);
+    }
+    __syncthreads();
+    uint32_t qf[NB * 2][NT][2];
+#pragma unroll
+    for (int ks = 0; ks < NB * 2; ++ks)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // column r of operand nt, words c of block ks / 2
+            const __half *row = W <= 4 ? s_q[(r & 3) % W][r >> 2] : s_q[r % W][nt];
+            const uint2 t = *reinterpret_cast<const uint2 *>(row + (ks >> 1) * 32 + c * 8 + (ks & 1) * 4);
+            qf[ks][nt][0] = t.x;
+            qf[ks][nt][1] = t.y;
+        }
+    // this thread's score columns: 2c and 2c + 1
+    float cscale[2];
+    int lim[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int j = W <= 4 ? (2 * c + e) % 4 % W : 2 * c + e;
+        cscale[e] = a.scale * 1.4426950408889634f * pow2_f32(-static_cast<int>(s_exp[j]));
+        lim[e] = j < ncol ? len - a.rows + (col0 + j) / G + 1 : 0;
+    }
+    const int low_lim = len - a.rows + col0 / G + 1;   // positions that every column sees
+
+    float acc[NB][2][NT][4], mx[2], sum[2];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -504,12 +595,10 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][m][n][e] = 0.0f;
 #pragma unroll
-    for (int s = 0; s < SC; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            mx[s][e] = -INFINITY;
-            sum[s][e] = 0.0f;
-        }
+    for (int e = 0; e < 2; ++e) {
+        mx[e] = -INFINITY;
+        sum[e] = 0.0f;
+    }
     // 2^kf brings P times the largest V scale so far to 2^15 at most; vlim:
     // the largest scale (f16 bits) that the present kf takes
     int kf = 0;
@@ -517,22 +606,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
     // hi lanes keep x (cut to f16 below), lo lanes what the cut leaves
     const uint32_t cut = (W <= 4 && c < 2) ? 0u : 0xFFFFE000u;
 
-    int k0 = start + warp * TILE;
-    if (k0 < end) {
-        load_k(k0);
-        load_v(k0);
-    }
-    for (; k0 < end; k0 += kQ4Warps * TILE) {
-        const int kn = k0 + kQ4Warps * TILE;
+    for (; k0 < end; k0 += kQ4Warps * kQ4Tile) {
+        const bool more = k0 + kQ4Warps * kQ4Tile < end;
         // ---- scores
-        float s[MT][SC][4];
+        float s[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             float t[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) t[n][e] = 0.0f;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 uint32_t x0[4], x1[4];
@@ -542,43 +622,30 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
                 const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if constexpr (kQRegs) {
-                        mma_f16(u, a0, qf[2 * i][n]);
-                        mma_f16(u, a1, qf[2 * i + 1][n]);
-                    } else {
-                        const uint2 q0 = qfrag[(2 * i * NT + n) * 32 + lane], q1 = qfrag[((2 * i + 1) * NT + n) * 32 + lane];
-                        const uint32_t b0[2] = {q0.x, q0.y}, b1[2] = {q1.x, q1.y};
-                        mma_f16(u, a0, b0);
-                        mma_f16(u, a1, b1);
-                    }
-                    t[n][0] = fmaf(u[0], d0, t[n][0]);
-                    t[n][1] = fmaf(u[1], d0, t[n][1]);
-                    t[n][2] = fmaf(u[2], d1, t[n][2]);
-                    t[n][3] = fmaf(u[3], d1, t[n][3]);
+                    float u[4];
+                    mma_f16_first(u, a0, qf[2 * i][n]);
+                    mma_f16(u, a1, qf[2 * i + 1][n]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[n][e] = i ? fmaf(u[e], e < 2 ? d0 : d1, t[n][e]) : u[e] * (e < 2 ? d0 : d1);
                 }
             }
 #pragma unroll
-            for (int q = 0; q < SC; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = W <= 4 ? t[0][e] + __shfl_xor_sync(0xffffffffu, t[0][e], 2) : t[q][e] + t[q + NT - SC][e];
-                    s[m][q][e] = v * cscale[q][e & 1];
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float v = W <= 4 ? t[0][e] + __shfl_xor_sync(0xffffffffu, t[0][e], 2) : t[0][e] + t[NT - 1][e];
+                s[m][e] = v * cscale[e & 1];
+            }
         }
-        if (kn < end) load_k(kn);
-        if (k0 + TILE > low_lim) {
+        if (more) load_k();
+        if (k0 + kQ4Tile > low_lim) {
             // the tile that a column's range ends in: what lies past it may be anything
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                for (int q = 0; q < SC; ++q)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (k0 + 16 * m + 8 * (e >> 1) + r >= lim[q][e & 1]) s[m][q][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e)
+                    if (k0 + 16 * m + 8 * (e >> 1) + pr >= lim[e & 1]) s[m][e] = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (k0 + 16 * m + 8 * h + r >= len)
+                    if (k0 + 16 * m + 8 * h + pr >= len)
 #pragma unroll
                         for (int w = 0; w < Wd::S; ++w) vd[m][h][w] = 0u;
             }
@@ -606,28 +673,26 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
             }
         }
         // ---- softmax: running maximum, weights in units of 2^-kf
-        float corr[SC][2];
+        float corr[2];
+        const float unit = pow2_f32(kf);
 #pragma unroll
-        for (int q = 0; q < SC; ++q)
+        for (int e = 0; e < 2; ++e) {
+            float t = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float t = fmaxf(s[0][q][e], s[0][q][e + 2]);
-                if constexpr (MT == 2) t = fmaxf(t, fmaxf(s[1][q][e], s[1][q][e + 2]));
+            for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+            const float mn = fmaxf(mx[e], t), base = mn == -INFINITY ? 0.0f : mn;
+            corr[e] = exp2_f32(mx[e] - base) * refit;
+            mx[e] = mn;
+            sum[e] *= corr[e];
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                const float mn = fmaxf(mx[q][e], t), base = mn == -INFINITY ? 0.0f : mn;
-                corr[q][e] = exp2_f32(mx[q][e] - base) * refit;
-                mx[q][e] = mn;
-                sum[q][e] *= corr[q][e];
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float p = exp2_f32(s[m][q][e + 2 * h] - base) * pow2_f32(kf);
-                        s[m][q][e + 2 * h] = p;
-                        sum[q][e] += p;
-                    }
-            }
+                for (int h = 0; h < 2; ++h) {
+                    const float p = exp2_f32(s[m][e + 2 * h] - base) * unit;
+                    s[m][e + 2 * h] = p;
+                    sum[e] += p;
+                }
+        }
         // ---- P operands: p times the block's V scale, hi and lo, transposed
         uint32_t pf[NI][MT][NT][2];
 #pragma unroll
@@ -647,29 +712,16 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
                     } else {
                         d0 = d1 = half_of(vd[m][h][i >> 1], i & 1);
                     }
-#pragma unroll
-                    for (int q = 0; q < SC; ++q) {
-                        const float x0 = s[m][q][2 * h] * d0, x1 = s[m][q][2 * h + 1] * d1;
-                        const float y0 = x0 - __uint_as_float(__float_as_uint(x0) & cut);
-                        const float y1 = x1 - __uint_as_float(__float_as_uint(x1) & cut);
-                        if constexpr (W <= 4) {
-                            pf[i][m][0][h] = transpose8x8(pack_rz(y0, y1));
-                        } else {
-                            pf[i][m][q][h] = transpose8x8(pack_rz(x0, x1));
-                            pf[i][m][q + SC][h] = transpose8x8(pack_rz(y0, y1));
-                        }
-                    }
+                    const float x0 = s[m][2 * h] * d0, x1 = s[m][2 * h + 1] * d1;
+                    const float y0 = x0 - __uint_as_float(__float_as_uint(x0) & cut);
+                    const float y1 = x1 - __uint_as_float(__float_as_uint(x1) & cut);
+                    if constexpr (W > 4) pf[i][m][0][h] = transpose8x8(pack_rz(x0, x1));
+                    pf[i][m][NT - 1][h] = transpose8x8(pack_rz(y0, y1));
                 }
         // ---- O: two positions' halfwords of a block make the pairs along k
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             float u[2][NT][4];
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) u[d][n][e] = 0.0f;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 uint32_t x0[4], x1[4];
@@ -679,8 +731,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
                 const uint32_t a0[4] = {x0[0], x0[1], x1[0], x1[1]}, a1[4] = {x0[2], x0[3], x1[2], x1[3]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    mma_f16(u[0][n], a0, pf[i / DUP][m][n]);
-                    mma_f16(u[1][n], a1, pf[i / DUP][m][n]);
+                    if (m == 0) {
+                        mma_f16_first(u[0][n], a0, pf[i / DUP][m][n]);
+                        mma_f16_first(u[1][n], a1, pf[i / DUP][m][n]);
+                    } else {
+                        mma_f16(u[0][n], a0, pf[i / DUP][m][n]);
+                        mma_f16(u[1][n], a1, pf[i / DUP][m][n]);
+                    }
                 }
             }
 #pragma unroll
@@ -688,110 +745,108 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][d][n][e] = fmaf(acc[i][d][n][e], corr[n % SC][e & 1], u[d][n][e]);
+                    for (int e = 0; e < 4; ++e) acc[i][d][n][e] = fmaf(acc[i][d][n][e], corr[e & 1], u[d][n][e]);
         }
-        if (kn < end) load_v(kn);
+        if (more) load_v();
     }
 
     // ---- the warps' results meet in shared memory
-    constexpr int PS = q4_part<HD>();
-    __syncthreads();   // the q operands are done with
-    float *mine = q4_smem + warp * W * PS;
+    float *res = q4_smem + warp * W * PS;
 #pragma unroll
-    for (int q = 0; q < SC; ++q)
+    for (int e = 0; e < 2; ++e) {
+        float t = sum[e];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float t = sum[q][e];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            const int n = 2 * c + e, j = W <= 4 ? n : 8 * q + n;
-            if (r == 0 && j < W) {
-                mine[j * PS + HD] = mx[q][e] - static_cast<float>(kf);
-                mine[j * PS + HD + 1] = t;
-            }
+        for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        const int j = 2 * c + e;
+        if (r == 0 && j < W) {
+            res[j * PS + HD] = mx[e] - static_cast<float>(kf);
+            res[j * PS + HD + 1] = t;
         }
+    }
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int q = 0; q < SC; ++q)
+        for (int e = 0; e < 2; ++e) {
+            float o[4];   // dimensions 4 r .. 4 r + 3 of the block
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float o[4];   // dimensions 4 r .. 4 r + 3 of the block
+            for (int d = 0; d < 2; ++d)
 #pragma unroll
-                for (int d = 0; d < 2; ++d)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        o[2 * d + h] = W <= 4 ? acc[i][d][0][e + 2 * h] + __shfl_xor_sync(0xffffffffu, acc[i][d][0][e + 2 * h], 2)
-                                              : acc[i][d][q][e + 2 * h] + acc[i][d][q + NT - SC][e + 2 * h];
-                const int n = 2 * c + e, j = W <= 4 ? n % W : 8 * q + n;
-                if (W > 4 || (n < 4 && n / W == i % DUP)) {
-                    float2 *dst = reinterpret_cast<float2 *>(mine + j * PS + i * 32 + 4 * r);
-                    dst[0] = make_float2(o[0], o[1]);
-                    dst[1] = make_float2(o[2], o[3]);
-                }
+                for (int h = 0; h < 2; ++h)
+                    o[2 * d + h] = W <= 4 ? acc[i][d][0][e + 2 * h] + __shfl_xor_sync(0xffffffffu, acc[i][d][0][e + 2 * h], 2)
+                                          : acc[i][d][0][e + 2 * h] + acc[i][d][NT - 1][e + 2 * h];
+            const int n = 2 * c + e, j = W <= 4 ? n % W : n;
+            if (W > 4 || (n < 4 && n / W == i % DUP)) {
+                float2 *dst = reinterpret_cast<float2 *>(res + j * PS + i * 32 + 4 * r);
+                dst[0] = make_float2(o[0], o[1]);
+                dst[1] = make_float2(o[2], o[3]);
             }
+        }
     __syncthreads();
+    const bool begins = blk0 == 0, ends = blk1 == blocks;
+    float *ws = a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * W * PS;
     for (int x = tid; x < ncol * HD; x += kQ4Warps * 32) {
         const int j = x / HD, d = x % HD;
-        float M = -INFINITY;
+        float M = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll
         for (int w = 0; w < kQ4Warps; ++w) M = fmaxf(M, q4_smem[(w * W + j) * PS + HD]);
-        float l = 0.0f, o = 0.0f;
         if (M != -INFINITY)
 #pragma unroll
             for (int w = 0; w < kQ4Warps; ++w) {
-                const float *pw = q4_smem + (w * W + j) * PS;
-                const float f = exp2_f32(pw[HD] - M);
-                l = fmaf(pw[HD + 1], f, l);
-                o = fmaf(pw[d], f, o);
+                const float *p = q4_smem + (w * W + j) * PS;
+                const float f = exp2_f32(p[HD] - M);
+                l = fmaf(p[HD + 1], f, l);
+                o = fmaf(p[d], f, o);
             }
-        if (nsplit == 1) {
+        if (begins && ends) {
             const int cc = col0 + j;
             a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
                 l > 0.0f ? o / l : 0.0f;
         } else {
-            float *ws = a.ws + (((static_cast<size_t>(b) * a.c.nkv + g) * cols + col0 + j) * nsplit + split) * PS;
-            ws[d] = o;
+            ws[j * PS + d] = o;
             if (d == 0) {
-                ws[HD] = M;
-                ws[HD + 1] = l;
+                ws[j * PS + HD] = M;
+                ws[j * PS + HD + 1] = l;
             }
         }
     }
+    if (tid == 0 && owners) {
+        int2 *own = owners + static_cast<size_t>(b) * U + unit;
+        if (begins) own->x = static_cast<int>(blockIdx.x);
+        if (ends) own->y = static_cast<int>(blockIdx.x);
+    }
+    __syncthreads();   // results and q rows are read: the next piece may write its own
+    if (ends && unit == U - 1) {
+        before += blocks;
+        ++b;
+    }
+    }
 }
 
-// Joins the runs of one column: a warp per (sequence, kv head, column).
+// Joins the partial results of the columns whose unit more than one CTA worked
+// on: a CTA per (sequence, kv head, column), a thread per dimension.
 template <int HD>
-__global__ void __launch_bounds__(128) k_kv_q4_merge(KvQ4AttnArgs a, int chunk, int nsplit, int W) {
-    constexpr int E = HD / 32, PS = q4_part<HD>();
-    const int lane = threadIdx.x & 31, G = a.nh / a.c.nkv, cols = G * a.rows;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (unit >= static_cast<int64_t>(a.B) * a.c.nkv * cols) return;
-    const int cc = static_cast<int>(unit % cols), g = static_cast<int>(unit / cols % a.c.nkv);
-    const int b = static_cast<int>(unit / cols / a.c.nkv);
-    const int slot = a.slots ? a.slots[b] : a.slot0 + b;
-    const int len = slot >= 0 && slot < a.c.slots ? q4_len(a, b) : 0;
-    const int col0 = cc / W * W, ncol = min(W, cols - col0);
-    const int seen = len - a.rows + (col0 + ncol - 1) / G + 1;   // as in the kernel above
-    const int runs = seen > 0 ? min(nsplit, (seen + chunk - 1) / chunk) : 0;
-    const float *ws = a.ws + static_cast<size_t>(unit) * nsplit * PS;
-    float M = -INFINITY;
-    for (int i = lane; i < runs; i += 32) M = fmaxf(M, ws[i * PS + HD]);
-    M = warp_max(M);
-    float l = 0.0f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+__global__ void __launch_bounds__(HD) k_kv_q4_join(KvQ4AttnArgs a, int cgroups, int W, const int2 *owners) {
+    constexpr int PS = q4_part<HD>();
+    pdl_wait();
+    const int G = a.nh / a.c.nkv, cols = G * a.rows, U = a.c.nkv * cgroups;
+    const int cc = blockIdx.x % cols, g = blockIdx.x / cols % a.c.nkv, b = blockIdx.x / (cols * a.c.nkv), d = threadIdx.x;
+    const int2 own = owners[static_cast<size_t>(b) * U + g * cgroups + cc / W];
+    if (own.x == own.y) return;
+    // the first CTA ended inside the unit (its second result), the others began inside it
+    const auto part = [&](int i) { return a.ws + (static_cast<size_t>(i) * 2 + (i == own.x ? 1 : 0)) * W * PS + cc % W * PS; };
+    float M = -INFINITY, l = 0.0f, o = 0.0f;
+#pragma unroll 8
+    for (int i = own.x; i <= own.y; ++i) M = fmaxf(M, part(i)[HD]);
     if (M != -INFINITY)
-        for (int i = 0; i < runs; ++i) {
-            const float f = exp2_f32(ws[i * PS + HD] - M);
-            l = fmaf(ws[i * PS + HD + 1], f, l);
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(ws[i * PS + e * 32 + lane], f, o[e]);
+#pragma unroll 8
+        for (int i = own.x; i <= own.y; ++i) {
+            const float *p = part(i);
+            const float f = exp2_f32(p[HD] - M);
+            l = fmaf(p[HD + 1], f, l);
+            o = fmaf(p[d], f, o);
         }
-    float *out = a.out + (static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e * 32 + lane] = l > 0.0f ? o[e] / l : 0.0f;
+    a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
+        l > 0.0f ? o / l : 0.0f;
 }
 
 }  // namespace
@@ -821,63 +876,71 @@ cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M
 
 namespace {
 
-// How a call is split: width class of the columns, column groups, and runs of
-// `chunk` positions.
+// How a call is split: width class of the columns, column groups, CTAs.
 struct Q4Plan {
-    int W, cgroups, chunk, nsplit;
+    int W, cgroups, ctas;
+    bool whole;   // units of one block: none is cut
 };
 
 Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
     const int cols = nh / nkv * rows;
     Q4Plan p;
-    p.W = cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : cols <= 8 ? 8 : 16;
+    p.W = cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : 8;
     p.cgroups = (cols + p.W - 1) / p.W;
-    const int64_t units = static_cast<int64_t>(B) * nkv * p.cgroups;
-    // about four runs for every CTA that fits at once, so that sequences of
-    // different lengths even out; no run shorter than one tile per warp
-    const int64_t want = (4 * 3 * 152 + units - 1) / std::max<int64_t>(units, 1);
-    const int quantum = kQ4Warps * kQ4Tile;
-    const int64_t most = std::max<int64_t>(1, (max_len + quantum - 1) / quantum);
-    const int64_t n = std::max<int64_t>(1, std::min<int64_t>(want, most));
-    p.chunk = static_cast<int>(std::max<int64_t>(1, (max_len + n * quantum - 1) / (n * quantum)) * quantum);
-    p.nsplit = std::max(1, (max_len + p.chunk - 1) / p.chunk);
+    // the CTAs that fit at once; for little work two blocks to each, below which
+    // the joining costs more than the wait for a second block
+    const int fit = 152 * (p.W <= 4 ? 3 : 2);
+    const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
+    const int64_t units = static_cast<int64_t>(std::max(B, 1)) * nkv * p.cgroups;
+    p.ctas = static_cast<int>(std::min<int64_t>(fit, std::max(units, units * ((most + 1) / 2))));
+    p.whole = most == 1;
     return p;
 }
 
+size_t q4_parts_bytes(const Q4Plan &p, int hd) {
+    return (static_cast<size_t>(p.ctas) * 2 * p.W * (hd + 2) * 4 + 15) / 16 * 16;
+}
+
 template <int HD, int W>
-cudaError_t launch_q4_attn_w(const KvQ4AttnArgs &a, const Q4Plan &p, cudaStream_t s) {
-    constexpr size_t smem = std::max<size_t>(static_cast<size_t>(kQ4Warps) * W * q4_part<HD>() * 4,
-                                             static_cast<size_t>(HD / 32) * 2 * q4_ops(W) * 32 * 8);
-    static_assert(smem <= 48 * 1024, "fits without an opt-in");
-    k_kv_q4_attn<HD, W><<<dim3(p.nsplit, a.c.nkv * p.cgroups, a.B), kQ4Warps * 32, smem, s>>>(a, p.chunk, p.nsplit, p.cgroups);
+cudaError_t launch_q4_attn_w(const KvQ4AttnArgs &a, const Q4Plan &p, int2 *owners, cudaStream_t s) {
+    constexpr size_t smem = static_cast<size_t>(kQ4Warps) * W * q4_part<HD>() * 4;
+    static_assert(smem <= 40 * 1024, "fits without an opt-in");
+    k_kv_q4_attn<HD, W><<<p.ctas, kQ4Warps * 32, smem, s>>>(a, p.cgroups, owners);
     return cudaGetLastError();
 }
 
 template <int HD>
 cudaError_t launch_q4_attn_hd(const KvQ4AttnArgs &a, const Q4Plan &p, cudaStream_t s) {
+    int2 *owners = p.whole ? nullptr : reinterpret_cast<int2 *>(reinterpret_cast<uint8_t *>(a.ws) + q4_parts_bytes(p, HD));
     cudaError_t e = cudaErrorInvalidValue;
     switch (p.W) {
-        case 1: e = launch_q4_attn_w<HD, 1>(a, p, s); break;
-        case 2: e = launch_q4_attn_w<HD, 2>(a, p, s); break;
-        case 4: e = launch_q4_attn_w<HD, 4>(a, p, s); break;
-        case 8: e = launch_q4_attn_w<HD, 8>(a, p, s); break;
-        case 16: e = launch_q4_attn_w<HD, 16>(a, p, s); break;
+        case 1: e = launch_q4_attn_w<HD, 1>(a, p, owners, s); break;
+        case 2: e = launch_q4_attn_w<HD, 2>(a, p, owners, s); break;
+        case 4: e = launch_q4_attn_w<HD, 4>(a, p, owners, s); break;
+        case 8: e = launch_q4_attn_w<HD, 8>(a, p, owners, s); break;
     }
-    if (e != cudaSuccess || p.nsplit == 1) return e;
-    const int64_t units = static_cast<int64_t>(a.B) * a.nh * a.rows;
-    k_kv_q4_merge<HD><<<static_cast<unsigned>((units + 3) / 4), 128, 0, s>>>(a, p.chunk, p.nsplit, p.W);
-    return cudaGetLastError();
+    if (e != cudaSuccess || p.whole) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.nh) * a.rows * a.B);
+    cfg.blockDim = dim3(HD);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_kv_q4_join<HD>, a, p.cgroups, p.W, static_cast<const int2 *>(owners));
 }
 
 }  // namespace
 
 int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len) {
-    return q4_plan(B, rows, nh, nkv, max_len).nsplit > 1 ? 2 : 1;
+    return q4_plan(B, rows, nh, nkv, max_len).whole ? 1 : 2;
 }
 
 size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len) {
     const Q4Plan p = q4_plan(B, rows, nh, nkv, max_len);
-    return p.nsplit > 1 ? static_cast<size_t>(B) * nh * rows * p.nsplit * (hd + 2) * 4 : 0;
+    return p.whole ? 0 : q4_parts_bytes(p, hd) + static_cast<size_t>(B) * nkv * p.cgroups * sizeof(int2);
 }
 
 cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, cudaStream_t s) {

@@ -1510,6 +1510,8 @@ int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride,
     if (misaligned(q_dev, 4) || misaligned(out_dev, 4) || misaligned(slots_dev, 4) || misaligned(lens_dev, 4) ||
         misaligned(workspace_dev, 16))
         return fail(nullptr, QW3_ERR_INVALID_ARG, "the workspace must be 16-byte, the other buffers 4-byte aligned");
+    if (static_cast<int64_t>(B) * rows * n_heads > INT32_MAX)
+        return fail(nullptr, QW3_ERR_SHAPE, "B * rows * n_heads must fit in 31 bits");
     if (!(scale - scale == 0.0f)) return fail(nullptr, QW3_ERR_INVALID_ARG, "scale must be finite");
     if (B == 0) return QW3_OK;
     const int64_t need = qw3_kv_q4_attn_workspace_bytes(B, rows, n_heads, cache->n_kv_heads, cache->head_dim, max_len);

@@ -37,7 +37,14 @@ constexpr float kOne = 1099511627776.0f;   // 2^40
 // Order of logits as unsigned keys; the two zeros are one value.
 __device__ __forceinline__ uint32_t logit_key(float v) { return float_order_key(v + 0.0f); }
 
-__device__ __forceinline__ u64 fixed_weight(float e) { return static_cast<u64>(__float2ull_rn(e * kOne)); }
+// e in [0, 1] times 2^40, cut to an integer, from its bits (a conversion of
+// f32 to 64 bits runs on the f64 units, which are few).
+__device__ __forceinline__ u64 fixed_weight(float e) {
+    const uint32_t x = __float_as_uint(e);
+    const int shift = static_cast<int>(x >> 23) - 110;   // 2^40 e = mantissa * 2^shift
+    const u64 m = (x & 0x7fffffu) | 0x800000u;
+    return shift >= 0 ? m << shift : (shift > -24 ? m >> -shift : 0ull);
+}
 
 __device__ __forceinline__ void remote_st(uint32_t addr, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
