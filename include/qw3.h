@@ -469,12 +469,13 @@ QW3_API int64_t qw3_kv_q4_attn_workspace_bytes(int32_t B, int32_t rows, int32_t 
  * within f32 reassociation error of the exact ones and the same in every call.
  * workspace_dev: 16-byte aligned, qw3_kv_q4_attn_workspace_bytes() or more, of
  * any content, not used by another call until this one has completed (two
- * graphs that may run at once need a workspace each). Asynchronous on
- * `stream`. */
+ * graphs that may run at once need a workspace each). If a bounded wait in the
+ * kernel runs out and status_dev is not NULL, *status_dev becomes
+ * QW3_ERR_TIMEOUT and the outputs are not valid. Asynchronous on `stream`. */
 QW3_API int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride, int32_t n_heads,
                            const int32_t *slots_dev, const int32_t *lens_dev, int32_t B, int32_t rows,
                            int32_t max_len, float scale, float *out_dev, int64_t out_stride, void *workspace_dev,
-                           int64_t workspace_bytes, void *stream);
+                           int64_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /* ---- Sampling --------------------------------------------------------------
  * One token from each of B rows of logits (f32 [B][stride], V values used,

@@ -375,17 +375,26 @@ struct Q4Words {   // words of a thread's share of a row
 };
 
 template <int N>
-__device__ __forceinline__ void ld_words(uint32_t (&d)[N], const void *p) {
+__device__ __forceinline__ void ld_words(uint32_t (&d)[N], const uint8_t *p) {
     if constexpr (N == 4) {
-        const uint4 t = __ldg(static_cast<const uint4 *>(p));
+        const uint4 t = *reinterpret_cast<const uint4 *>(p);
         d[0] = t.x; d[1] = t.y; d[2] = t.z; d[3] = t.w;
     } else if constexpr (N == 2) {
-        const uint2 t = __ldg(static_cast<const uint2 *>(p));
+        const uint2 t = *reinterpret_cast<const uint2 *>(p);
         d[0] = t.x; d[1] = t.y;
     } else {
-        d[0] = __ldg(static_cast<const uint32_t *>(p));
+        d[0] = *reinterpret_cast<const uint32_t *>(p);
     }
 }
+
+// A warp's tile in shared memory: codes of K, of V, scales of K, of V. Each
+// warp has a ring of kQ4Stages of them, filled by bulk copies.
+constexpr int kQ4Stages = 2;
+template <int HD>
+struct Q4Stage {
+    static constexpr int kCodes = kQ4Tile * HD / 2, kScales = kQ4Tile * HD / 16;
+    static constexpr int V = kCodes, KS = 2 * kCodes, VS = KS + kScales, bytes = VS + kScales;
+};
 
 // Partial results: per column acc[HD], then log2 of their unit and the sum of
 // weights.
@@ -420,7 +429,7 @@ __device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
 // its share begins inside, and of the one that it ends inside), then the first
 // and the last CTA of each unit.
 template <int HD, int W>
-__global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
+__global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
     constexpr int NB = HD / 32, NT = q4_ops(W);
     constexpr int DUP = W <= 4 ? 4 / W : 1;          // blocks that share an operand
     constexpr int NI = (NB + DUP - 1) / DUP;         // P operands per 16 positions
@@ -428,13 +437,26 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
     constexpr int PS = q4_part<HD>();
     constexpr int QS = HD + 8;                       // a q row in shared memory, padded
     using Wd = Q4Words<HD>;
-    extern __shared__ __align__(16) float q4_smem[];   // [warp][W][PS]: the warps' results
+    using St = Q4Stage<HD>;
+    static_assert(W * PS * 4 <= kQ4Stages * St::bytes, "a warp's results fit its ring");
+    extern __shared__ __align__(128) uint8_t q4_ring[];   // [warp][kQ4Stages] tiles; a piece's results after it
+    __shared__ uint64_t s_bar[kQ4Warps][kQ4Stages];
     __shared__ __align__(16) __half s_q[W][2][QS];      // hi and lo; see below for the order of a row
     __shared__ float s_exp[W];
     __shared__ int64_t s_red[kQ4Warps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int G = a.nh / a.c.nkv, cols = G * a.rows, U = a.c.nkv * cgroups;
+    uint8_t *ring = q4_ring + warp * kQ4Stages * St::bytes;
+    const auto results = [&](int w) { return reinterpret_cast<float *>(q4_ring + w * kQ4Stages * St::bytes); };
+    if (lane == 0) {
+        for (int i = 0; i < kQ4Stages; ++i) mbar_init(&s_bar[warp][i], 1);
+        fence_mbar_init();
+    }
+    uint32_t taken = 0;     // tiles this warp has taken from its ring
+    bool lost = false;      // a copy did not arrive in time, the lost_at-th tile's
+    uint32_t lost_at = 0;
+    const uint64_t policy = policy_evict_first();
 
     // ---- this CTA's share [at, stop) of the blocks
     int64_t mine = 0;
@@ -496,45 +518,31 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
     const int start = blk0 * kQ4Block, end = min(seen, blk1 * kQ4Block);
     at += blk1 - blk0;
 
-    // Row i of an operand along m holds position i/2 or 4 + i/2 of its eight
-    // (even, odd), so that the four positions that a load of V takes lie next
-    // to each other.
-    const int pr = (r >> 1) | ((r & 1) << 2);
-    const size_t first = static_cast<size_t>(start) + warp * kQ4Tile;
-    const uint8_t *kp = kv_q4_codes<HD>(a.c, slot, 0, g) + (first + pr) * (HD / 2) + c * (HD / 8);
-    const uint8_t *vp = kv_q4_codes<HD>(a.c, slot, 1, g) + (first + c) * (HD / 2) + r * (HD / 16);
-    const __half *ksp = kv_q4_scales<HD>(a.c, slot, 0, g) + (first + pr) * NB;
-    const __half *vsp = kv_q4_scales<HD>(a.c, slot, 1, g) + (first + pr) * NB;
-
-    uint32_t kw[MT][2][Wd::K], kd[MT][2][Wd::S], vw[MT][4][Wd::V], vd[MT][2][Wd::S];
-    auto load_k = [&]() {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ld_words(kw[m][h], kp + (16 * m + 8 * h) * (HD / 2));
-                ld_words(kd[m][h], ksp + (16 * m + 8 * h) * NB);
-            }
-        kp += kQ4Warps * kQ4Tile * (HD / 2);
-        ksp += kQ4Warps * kQ4Tile * NB;
-    };
-    auto load_v = [&]() {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) ld_words(vw[m][h], vp + (16 * m + 4 * h) * (HD / 2));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) ld_words(vd[m][h], vsp + (16 * m + 8 * h) * NB);
-        }
-        vp += kQ4Warps * kQ4Tile * (HD / 2);
-        vsp += kQ4Warps * kQ4Tile * NB;
-    };
-
+    // ---- tiles of this warp: every kQ4Warps-th of the piece, the first ones on
+    // their way before anything else
     int k0 = start + warp * kQ4Tile;
-    if (k0 < end) {
-        load_k();
-        load_v();
+    const uint8_t *kc = kv_q4_codes<HD>(a.c, slot, 0, g), *vc = kv_q4_codes<HD>(a.c, slot, 1, g);
+    const __half *ksc = kv_q4_scales<HD>(a.c, slot, 0, g), *vsc = kv_q4_scales<HD>(a.c, slot, 1, g);
+    const auto fetch = [&](int j0, uint32_t n) {   // the tile at position j0 as the warp's n-th
+        uint8_t *st = ring + n % kQ4Stages * St::bytes;
+        uint64_t *bar = &s_bar[warp][n % kQ4Stages];
+        mbar_arrive_expect_tx(bar, St::bytes);
+        bulk_g2s(st, kc + static_cast<size_t>(j0) * (HD / 2), St::kCodes, bar, policy);
+        bulk_g2s(st + St::KS, ksc + static_cast<size_t>(j0) * NB, St::kScales, bar, policy);
+        bulk_g2s(st + St::V, vc + static_cast<size_t>(j0) * (HD / 2), St::kCodes, bar, policy);
+        bulk_g2s(st + St::VS, vsc + static_cast<size_t>(j0) * NB, St::kScales, bar, policy);
+    };
+    if (lane == 0 && !lost) {
+        // the last piece's results lay in the ring
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < kQ4Stages; ++i)
+            if (k0 + i * kQ4Block < end) fetch(k0 + i * kQ4Block, taken + i);
     }
+    // Rows i of an operand along m hold positions of its eight in this order, so
+    // that the four positions of one load of V lie together and no load of K
+    // meets a bank twice.
+    const int pr = (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1;
 
     // ---- q columns, while the first rows are on their way: scaled by a power
     // of two, split into hi and lo. Value 8 i + p of a row lies at 8 i + 2 (p &
@@ -606,19 +614,31 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
     // hi lanes keep x (cut to f16 below), lo lanes what the cut leaves
     const uint32_t cut = (W <= 4 && c < 2) ? 0u : 0xFFFFE000u;
 
-    for (; k0 < end; k0 += kQ4Warps * kQ4Tile) {
-        const bool more = k0 + kQ4Warps * kQ4Tile < end;
+    for (; k0 < end; k0 += kQ4Block) {
+        const uint8_t *st = ring + taken % kQ4Stages * St::bytes;
+        if (!lost && !mbar_wait_bounded(&s_bar[warp][taken % kQ4Stages], (taken / kQ4Stages) & 1u)) {
+            lost = true;   // no further copy is started
+            lost_at = taken;
+            record_status(a.status, QW3_ERR_TIMEOUT);
+        }
+        lost = __any_sync(0xffffffffu, lost);
         // ---- scores
         float s[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             float t[NT][4];
+            uint32_t kw[2][Wd::K], kd[2][Wd::S];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ld_words(kw[h], st + (16 * m + 8 * h + pr) * (HD / 2) + c * (HD / 8));
+                ld_words(kd[h], st + St::KS + (16 * m + 8 * h + pr) * (HD / 16));
+            }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 uint32_t x0[4], x1[4];
-                unpack8(kw[m][0][i], x0);
-                unpack8(kw[m][1][i], x1);
-                const float d0 = half_of(kd[m][0][i >> 1], i & 1), d1 = half_of(kd[m][1][i >> 1], i & 1);
+                unpack8(kw[0][i], x0);
+                unpack8(kw[1][i], x1);
+                const float d0 = half_of(kd[0][i >> 1], i & 1), d1 = half_of(kd[1][i >> 1], i & 1);
                 const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -635,7 +655,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
                 s[m][e] = v * cscale[e & 1];
             }
         }
-        if (more) load_k();
+        uint32_t vd[MT][2][Wd::S];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ld_words(vd[m][h], st + St::VS + (16 * m + 8 * h + pr) * (HD / 16));
         if (k0 + kQ4Tile > low_lim) {
             // the tile that a column's range ends in: what lies past it may be anything
 #pragma unroll
@@ -719,6 +743,12 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
                     pf[i][m][NT - 1][h] = transpose8x8(pack_rz(y0, y1));
                 }
         // ---- O: two positions' halfwords of a block make the pairs along k
+        uint32_t vw[MT][4][Wd::V];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                ld_words(vw[m][h], st + St::V + (16 * m + 8 * (h >> 1) + ((h & 1) ? 4 + (c ^ 1) : c)) * (HD / 2) + r * (HD / 16));
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             float u[2][NT][4];
@@ -747,11 +777,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[i][d][n][e] = fmaf(acc[i][d][n][e], corr[e & 1], u[d][n][e]);
         }
-        if (more) load_v();
+        ++taken;
+        __syncwarp();   // the tile is in registers: its place may be filled again
+        if (lane == 0 && !lost && k0 + kQ4Stages * kQ4Block < end) fetch(k0 + kQ4Stages * kQ4Block, taken + kQ4Stages - 1);
     }
 
     // ---- the warps' results meet in shared memory
-    float *res = q4_smem + warp * W * PS;
+    float *res = results(warp);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         float t = sum[e];
@@ -788,11 +820,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
         const int j = x / HD, d = x % HD;
         float M = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kQ4Warps; ++w) M = fmaxf(M, q4_smem[(w * W + j) * PS + HD]);
+        for (int w = 0; w < kQ4Warps; ++w) M = fmaxf(M, results(w)[j * PS + HD]);
         if (M != -INFINITY)
 #pragma unroll
             for (int w = 0; w < kQ4Warps; ++w) {
-                const float *p = q4_smem + (w * W + j) * PS;
+                const float *p = results(w) + j * PS;
                 const float f = exp2_f32(p[HD] - M);
                 l = fmaf(p[HD + 1], f, l);
                 o = fmaf(p[d], f, o);
@@ -820,6 +852,10 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 3 : 2) k_kv_q4_attn(Kv
         ++b;
     }
     }
+    // a warp that gave up leaves no copy in flight behind it
+    if (lost)
+        for (uint32_t n = lost_at; n < lost_at + kQ4Stages; ++n)
+            (void)mbar_wait_bounded(&s_bar[warp][n % kQ4Stages], (n / kQ4Stages) & 1u);
 }
 
 // Joins the partial results of the columns whose unit more than one CTA worked
@@ -889,7 +925,7 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
     p.cgroups = (cols + p.W - 1) / p.W;
     // the CTAs that fit at once; for little work two blocks to each, below which
     // the joining costs more than the wait for a second block
-    const int fit = 152 * (p.W <= 4 ? 3 : 2);
+    const int fit = 152 * (p.W <= 4 ? 4 : 3);
     const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
     const int64_t units = static_cast<int64_t>(std::max(B, 1)) * nkv * p.cgroups;
     p.ctas = static_cast<int>(std::min<int64_t>(fit, std::max(units, units * ((most + 1) / 2))));
@@ -903,7 +939,7 @@ size_t q4_parts_bytes(const Q4Plan &p, int hd) {
 
 template <int HD, int W>
 cudaError_t launch_q4_attn_w(const KvQ4AttnArgs &a, const Q4Plan &p, int2 *owners, cudaStream_t s) {
-    constexpr size_t smem = static_cast<size_t>(kQ4Warps) * W * q4_part<HD>() * 4;
+    constexpr size_t smem = static_cast<size_t>(kQ4Warps) * kQ4Stages * Q4Stage<HD>::bytes;
     static_assert(smem <= 40 * 1024, "fits without an opt-in");
     k_kv_q4_attn<HD, W><<<p.ctas, kQ4Warps * 32, smem, s>>>(a, p.cgroups, owners);
     return cudaGetLastError();

@@ -364,6 +364,7 @@ KvQ4AttnArgs q4_attn_args(qw3_model *m, int l, const float *q, int B, int rows, 
     a.max_len = c.max_seq_len;
     a.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.head_dim)));
     a.out = out; a.out_stride = static_cast<int64_t>(c.n_heads) * c.head_dim; a.ws = m->q4_ws;
+    a.status = m->d_status;
     return a;
 }
 
@@ -1499,7 +1500,7 @@ int64_t qw3_kv_q4_attn_workspace_bytes(int32_t B, int32_t rows, int32_t n_heads,
 int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride, int32_t n_heads,
                    const int32_t *slots_dev, const int32_t *lens_dev, int32_t B, int32_t rows, int32_t max_len,
                    float scale, float *out_dev, int64_t out_stride, void *workspace_dev, int64_t workspace_bytes,
-                   void *stream) {
+                   int32_t *status_dev, void *stream) {
     if (int rc = check_kv_q4(cache, n_heads)) return rc;
     if (B < 0 || rows < 1 || rows > kQ4MaxRows) return fail(nullptr, QW3_ERR_INVALID_ARG, "1 to 16 rows per sequence");
     if (max_len < 0) return fail(nullptr, QW3_ERR_INVALID_ARG, "a negative max_len");
@@ -1508,7 +1509,7 @@ int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride,
     const int64_t qw = static_cast<int64_t>(n_heads) * cache->head_dim;
     if (q_stride < qw || out_stride < qw) return fail(nullptr, QW3_ERR_SHAPE, "a row stride is shorter than its heads");
     if (misaligned(q_dev, 4) || misaligned(out_dev, 4) || misaligned(slots_dev, 4) || misaligned(lens_dev, 4) ||
-        misaligned(workspace_dev, 16))
+        misaligned(workspace_dev, 16) || misaligned(status_dev, 4))
         return fail(nullptr, QW3_ERR_INVALID_ARG, "the workspace must be 16-byte, the other buffers 4-byte aligned");
     if (static_cast<int64_t>(B) * rows * n_heads > INT32_MAX)
         return fail(nullptr, QW3_ERR_SHAPE, "B * rows * n_heads must fit in 31 bits");
@@ -1521,6 +1522,7 @@ int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride,
     a.q = q_dev; a.q_stride = q_stride; a.c = kv_q4_view(cache); a.slots = slots_dev; a.lens = lens_dev;
     a.B = B; a.rows = rows; a.max_len = max_len; a.nh = n_heads; a.scale = scale;
     a.out = out_dev; a.out_stride = out_stride; a.ws = static_cast<float *>(workspace_dev);
+    a.status = status_dev;
     QW3_CUDA_TRY(launch_kv_q4_attn(a, cache->head_dim, static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }

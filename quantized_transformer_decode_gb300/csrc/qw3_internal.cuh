@@ -296,6 +296,7 @@ struct KvQ4AttnArgs {
     float *out;
     int64_t out_stride;
     float *ws;
+    int32_t *status;   // nullable
 };
 constexpr int kQ4MaxRows = 16, kQ4MaxGroup = 16;
 int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len);

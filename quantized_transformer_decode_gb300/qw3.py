@@ -140,7 +140,7 @@ def lib() -> ctypes.CDLL:
         "qw3_kv_q4_read": (ctypes.c_int, [ctypes.POINTER(Qw3KvQ4), _I32, _P, _I32, _P, _I32, _P, _P, _P]),
         "qw3_kv_q4_attn_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32, _I32]),
         "qw3_kv_q4_attn": (ctypes.c_int, [ctypes.POINTER(Qw3KvQ4), _P, _I64, _I32, _P, _P, _I32, _I32, _I32, _F32, _P,
-                                          _I64, _P, _I64, _P]),
+                                          _I64, _P, _I64, _P, _P]),
         "qw3_sample": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
@@ -320,9 +320,10 @@ def qw3_kv_q4_attn_workspace_bytes(B: int, rows: int, n_heads: int, n_kv_heads: 
 
 def qw3_kv_q4_attn(cache: Qw3KvQ4, q_ptr: int, q_stride: int, n_heads: int, slots_ptr: int, lens_ptr: int, B: int,
                    rows: int, max_len: int, scale: float, out_ptr: int, out_stride: int, ws_ptr: int, ws_bytes: int,
-                   stream: int = 0) -> None:
+                   status_ptr: int = 0, stream: int = 0) -> None:
     _check(lib().qw3_kv_q4_attn(cache, q_ptr or None, q_stride, n_heads, slots_ptr or None, lens_ptr or None, B, rows,
-                                max_len, scale, out_ptr or None, out_stride, ws_ptr or None, ws_bytes, stream or None))
+                                max_len, scale, out_ptr or None, out_stride, ws_ptr or None, ws_bytes, status_ptr or None,
+                                stream or None))
 
 
 def qw3_sample(logits_ptr: int, stride: int, B: int, V: int, temperature_ptr: int, top_k_ptr: int, top_p_ptr: int,
@@ -525,7 +526,7 @@ class KVCacheQ4:
         return k, v
 
     def attention(self, q, lens, rows: int = 1, slots=None, max_len: Optional[int] = None,
-                  scale: Optional[float] = None, out=None, workspace=None):
+                  scale: Optional[float] = None, out=None, workspace=None, status=None):
         """Attention of q [B * rows, n_heads, head_dim] (f32, contiguous) over
         the first lens[b] positions (int32 [B]) of slot slots[b] (int32 [B],
         else slot b); returns the same shape. max_len: an upper bound of lens
@@ -534,7 +535,7 @@ class KVCacheQ4:
         torch = _torch()
         B, hd, n_heads = lens.numel(), self.head_dim, q.shape[1] if q.dim() == 3 else 0
         _on(self.index, torch.float32, q=q, out=out)
-        _on(self.index, torch.int32, lens=lens, slots=slots)
+        _on(self.index, torch.int32, lens=lens, slots=slots, status=status)
         if n_heads < 1 or q.shape[0] != B * rows or q.shape[2] != hd:
             raise Qw3Error(QW3_ERR_SHAPE, f"q: [{B * rows}, n_heads, {hd}] is wanted")
         if (slots is not None and slots.numel() != B) or (out is not None and out.shape != q.shape):
@@ -555,7 +556,7 @@ class KVCacheQ4:
         with _Here(self.index) as stream:
             _check(L.qw3_kv_q4_attn(self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots), lens.data_ptr(), B, rows,
                                     max_len, hd ** -0.5 if scale is None else scale, out.data_ptr(), n_heads * hd,
-                                    _ptr(workspace), need, stream))
+                                    _ptr(workspace), need, _ptr(status), stream))
         return out
 
 

@@ -406,7 +406,8 @@ def test_attention_strides_output_and_repeat(torch):
     ws = torch.full((n + 16,), 0xAB, dtype=torch.uint8, device="cuda")
     for _ in range(2):
         qw3.qw3_kv_q4_attn(cache.c, q[:, 1:].data_ptr(), nh * hd + 5, nh, 0, lens.data_ptr(), B, rows, 1000, hd ** -0.5,
-                           out[:, 3:].data_ptr(), nh * hd + 7, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+                           out[:, 3:].data_ptr(), nh * hd + 7, ws.data_ptr(), n, 0,
+                           torch.cuda.current_stream().cuda_stream)
         assert torch.equal(out[:, 3:3 + nh * hd].reshape(B * rows, nh, hd), want)
     assert bool((out[:, :3] == 77).all()) and bool((out[:, 3 + nh * hd:] == 77).all())
     assert bool((ws[n:] == 0xAB).all())

@@ -67,7 +67,7 @@ def test_every_entry_checks_the_cache(L, c, want):
     c = cache(**c)
     assert append(L, c) == want
     assert L.qw3_kv_q4_read(c, 1, 16, 0, 16, 0, 16, 16, None) == want
-    assert L.qw3_kv_q4_attn(c, 16, 256, 4, None, 16, 1, 1, 32, 0.1, 16, 256, 16, 1 << 30, None) == want
+    assert L.qw3_kv_q4_attn(c, 16, 256, 4, None, 16, 1, 1, 32, 0.1, 16, 256, 16, 1 << 30, None, None) == want
 
 
 def test_null_cache(L):
@@ -85,14 +85,14 @@ def test_read_refusals(L, args, want):
 
 def attn(L, **kw):
     a = {**dict(q=16, qs=256, nh=4, slots=16, lens=16, B=2, rows=1, max_len=64, scale=0.1, out=16, os=256, ws=16,
-                wb=1 << 30), **kw}
+                wb=1 << 30, status=None), **kw}
     return L.qw3_kv_q4_attn(cache(), a["q"], a["qs"], a["nh"], a["slots"], a["lens"], a["B"], a["rows"], a["max_len"],
-                            a["scale"], a["out"], a["os"], a["ws"], a["wb"], None)
+                            a["scale"], a["out"], a["os"], a["ws"], a["wb"], a["status"], None)
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), ARG), (dict(lens=None), ARG), (dict(out=None), ARG), (dict(q=18), ARG), (dict(out=18), ARG),
-    (dict(lens=18), ARG), (dict(slots=18), ARG), (dict(ws=24), ARG), (dict(qs=255), SHAPE), (dict(os=255), SHAPE),
+    (dict(lens=18), ARG), (dict(slots=18), ARG), (dict(ws=24), ARG), (dict(status=18), ARG), (dict(qs=255), SHAPE), (dict(os=255), SHAPE),
     (dict(rows=0), ARG), (dict(rows=17), ARG), (dict(B=-1), ARG), (dict(max_len=-1), ARG), (dict(max_len=65), OVERFLOW),
     (dict(nh=3), SHAPE), (dict(nh=34), SHAPE), (dict(scale=float("inf")), ARG), (dict(scale=float("nan")), ARG),
     (dict(B=0, q=None, lens=None, out=None, ws=None, wb=0), OK),
@@ -110,7 +110,7 @@ def test_attention_workspace(L):
     need = w(1, 1, 32, 8, 128, 8192)
     if need:
         c = cache(slots=1, capacity=8192, n_kv_heads=8, head_dim=128)
-        call = lambda ws, n: L.qw3_kv_q4_attn(c, 16, 4096, 32, None, 16, 1, 1, 8192, 0.1, 16, 4096, ws, n, None)  # noqa: E731
+        call = lambda ws, n: L.qw3_kv_q4_attn(c, 16, 4096, 32, None, 16, 1, 1, 8192, 0.1, 16, 4096, ws, n, None, None)  # noqa: E731
         assert call(None, need) == ARG and call(16, need - 1) == ARG
 
 
