@@ -355,7 +355,8 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&h)[4]) {
 }
 
 __device__ __forceinline__ float half_of(uint32_t w, int i) {
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(i ? w >> 16 : w)));
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+    return i ? __high2float(h) : __low2float(h);
 }
 
 constexpr int kQ4Warps = 4, kQ4Tile = 32, kQ4Block = kQ4Warps * kQ4Tile;
@@ -400,6 +401,11 @@ struct Q4Stage {
 // weights.
 template <int HD>
 __host__ __device__ constexpr int q4_part() { return HD + 2; }
+
+// What a unit costs besides its blocks (its queries, the joining of its warps),
+// in blocks: 1 measured against 0, 2 and 3 at 64 sequences of 1 to 4101
+// positions.
+constexpr int kQ4UnitCost = 1;
 
 // Blocks of sequence b (one at least: a sequence without positions still has
 // outputs to write) and, if asked, its length and slot.
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
 
     // ---- this CTA's share [at, stop) of the blocks
     int64_t mine = 0;
-    for (int i = tid; i < a.B; i += kQ4Warps * 32) mine += q4_blocks(a, i);
+    for (int i = tid; i < a.B; i += kQ4Warps * 32) mine += q4_blocks(a, i) + kQ4UnitCost;
     const int64_t all = q4_sum(mine, s_red);
     // no share is empty: the join counts on every CTA between a unit's first and last
     const int64_t total = all * U, P = min(static_cast<int64_t>(gridDim.x), total);
@@ -469,11 +475,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     const int64_t stop = total * (blockIdx.x + 1) / P;
     // its first sequence: sums of 128 sequences at a time, then one by one
     int b = 0;
-    int64_t before = 0;   // blocks of the sequences below b (of one unit)
+    int64_t before = 0;   // cost of the sequences below b (of one unit)
     if (a.B > 1) {
         const int64_t want = at / U;
         for (int b0 = 0; b0 < a.B; b0 += kQ4Warps * 32) {
-            const int64_t n = b0 + tid < a.B ? q4_blocks(a, b0 + tid) : 0;
+            const int64_t n = b0 + tid < a.B ? q4_blocks(a, b0 + tid) + kQ4UnitCost : 0;
             int64_t run = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -508,36 +514,44 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     // ---- the next piece: blocks [blk0, blk1) of unit (b, g, cg)
     int len, slot;
     const int blocks = q4_blocks(a, b, &len, &slot);
+    // a unit's cost: kQ4UnitCost, then its blocks
     const int64_t in_b = at - before * U;
-    const int unit = static_cast<int>(in_b / blocks), g = unit / cgroups, cg = unit % cgroups;
-    const int blk0 = static_cast<int>(in_b - static_cast<int64_t>(unit) * blocks);
-    const int blk1 = static_cast<int>(min(static_cast<int64_t>(blocks), blk0 + (stop - at)));
+    const int cost = blocks + kQ4UnitCost;
+    const int unit = static_cast<int>(in_b / cost), g = unit / cgroups, cg = unit % cgroups;
+    const int off0 = static_cast<int>(in_b - static_cast<int64_t>(unit) * cost);
+    const int off1 = static_cast<int>(min(static_cast<int64_t>(cost), off0 + (stop - at)));
+    const int blk0 = max(0, off0 - kQ4UnitCost), blk1 = max(0, off1 - kQ4UnitCost);
+    at += off1 - off0;
+    if (blk0 == blk1) continue;   // the share ends before the unit's first block
     const int col0 = cg * W, ncol = min(W, cols - col0);
     // positions that this group's last column sees
     const int seen = len - a.rows + (col0 + ncol - 1) / G + 1;
     const int start = blk0 * kQ4Block, end = min(seen, blk1 * kQ4Block);
-    at += blk1 - blk0;
 
     // ---- tiles of this warp: every kQ4Warps-th of the piece, the first ones on
     // their way before anything else
     int k0 = start + warp * kQ4Tile;
-    const uint8_t *kc = kv_q4_codes<HD>(a.c, slot, 0, g), *vc = kv_q4_codes<HD>(a.c, slot, 1, g);
-    const __half *ksc = kv_q4_scales<HD>(a.c, slot, 0, g), *vsc = kv_q4_scales<HD>(a.c, slot, 1, g);
-    const auto fetch = [&](int j0, uint32_t n) {   // the tile at position j0 as the warp's n-th
-        uint8_t *st = ring + n % kQ4Stages * St::bytes;
+    // (lane 0's) next tile: codes and scales of K; V's lie a fixed distance behind
+    const uint8_t *codes = kv_q4_codes<HD>(a.c, slot, 0, g) + static_cast<size_t>(k0) * (HD / 2);
+    const uint8_t *scales = reinterpret_cast<const uint8_t *>(kv_q4_scales<HD>(a.c, slot, 0, g)) + static_cast<size_t>(k0) * (HD / 16);
+    const size_t to_v = static_cast<size_t>(a.c.nkv) * kv_q4_head_bytes(a.c.cap, HD);
+    const auto fetch = [&](uint32_t n) {   // the tile that is the warp's n-th
+        uint8_t *to = ring + n % kQ4Stages * St::bytes;
         uint64_t *bar = &s_bar[warp][n % kQ4Stages];
         mbar_arrive_expect_tx(bar, St::bytes);
-        bulk_g2s(st, kc + static_cast<size_t>(j0) * (HD / 2), St::kCodes, bar, policy);
-        bulk_g2s(st + St::KS, ksc + static_cast<size_t>(j0) * NB, St::kScales, bar, policy);
-        bulk_g2s(st + St::V, vc + static_cast<size_t>(j0) * (HD / 2), St::kCodes, bar, policy);
-        bulk_g2s(st + St::VS, vsc + static_cast<size_t>(j0) * NB, St::kScales, bar, policy);
+        bulk_g2s(to, codes, St::kCodes, bar, policy);
+        bulk_g2s(to + St::KS, scales, St::kScales, bar, policy);
+        bulk_g2s(to + St::V, codes + to_v, St::kCodes, bar, policy);
+        bulk_g2s(to + St::VS, scales + to_v, St::kScales, bar, policy);
+        codes += kQ4Block * (HD / 2);
+        scales += kQ4Block * (HD / 16);
     };
     if (lane == 0 && !lost) {
         // the last piece's results lay in the ring
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < kQ4Stages; ++i)
-            if (k0 + i * kQ4Block < end) fetch(k0 + i * kQ4Block, taken + i);
+            if (k0 + i * kQ4Block < end) fetch(taken + i);
     }
     // Rows i of an operand along m hold positions of its eight in this order, so
     // that the four positions of one load of V lie together and no load of K
@@ -593,7 +607,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     }
     const int low_lim = len - a.rows + col0 / G + 1;   // positions that every column sees
 
-    float acc[NB][2][NT][4], mx[2], sum[2];
+    float acc[NB][2][NT][4], mx[2], ref[2], sum[2];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -605,12 +619,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         mx[e] = -INFINITY;
+        ref[e] = -INFINITY;
         sum[e] = 0.0f;
     }
     // 2^kf brings P times the largest V scale so far to 2^15 at most; vlim:
-    // the largest scale (f16 bits) that the present kf takes
-    int kf = 0;
-    uint32_t vlim = 0u;
+    // the largest scale that the present kf takes
+    float kf = 37.0f;
+    __half2 vlim = __float2half2_rn(0.0f);
     // hi lanes keep x (cut to f16 below), lo lanes what the cut leaves
     const uint32_t cut = (W <= 4 && c < 2) ? 0u : 0xFFFFE000u;
 
@@ -675,44 +690,42 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
             }
         }
         // ---- the unit of P: does a V scale pass what kf takes?
-        float refit = 1.0f;
         {
-            uint32_t big = 0u;
+            __half2 big = __float2half2_rn(0.0f);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int w = 0; w < Wd::S; ++w) big = __vmaxu2(big, vd[m][h][w] & 0x7FFF7FFFu);
-            const uint32_t top = max(big & 0xFFFFu, big >> 16);
-            if (__any_sync(0xffffffffu, top > vlim || vlim == 0u)) {
-                const uint32_t t = __reduce_max_sync(0xffffffffu, top);
+                    for (int w = 0; w < Wd::S; ++w) big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&vd[m][h][w])));
+            if (!__all_sync(0xffffffffu, __hble2(big, vlim))) {
+                const uint32_t t = __reduce_max_sync(0xffffffffu, max(static_cast<uint32_t>(__half_as_ushort(__low2half(big))),
+                                                                      static_cast<uint32_t>(__half_as_ushort(__high2half(big)))));
                 // 2^e > the largest scale; two more bits so that a rise is rare
                 const int e = t ? static_cast<int>(__float_as_uint(half_of(t, 0)) >> 23) - 126 : -24;
-                const int lim2 = min(e + 2, 16), kn2 = 15 - lim2;
-                // f16 bits of 2^lim2 (of the largest finite value from 2^16 on)
-                vlim = lim2 >= 16 ? 0x7BFFu : __half_as_ushort(__float2half_rn(pow2_f32(lim2)));
-                refit = pow2_f32(max(-100, min(100, kn2 - kf)));
-                kf = kn2;
+                const int lim2 = min(e + 2, 16);
+                vlim = lim2 >= 16 ? __half2half2(__ushort_as_half(0x7BFF)) : __float2half2_rn(pow2_f32(lim2));
+                kf = static_cast<float>(15 - lim2);
             }
         }
-        // ---- softmax: running maximum, weights in units of 2^-kf
+        // ---- softmax: weights 2^(s - ref), ref the running maximum less kf (any
+        // reference serves as long as one is used throughout)
         float corr[2];
-        const float unit = pow2_f32(kf);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float t = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-            const float mn = fmaxf(mx[e], t), base = mn == -INFINITY ? 0.0f : mn;
-            corr[e] = exp2_f32(mx[e] - base) * refit;
-            mx[e] = mn;
+            mx[e] = fmaxf(mx[e], t);
+            const float to = mx[e] - kf, now = to == -INFINITY ? 0.0f : to;
+            corr[e] = exp2_f32(ref[e] - now);
+            ref[e] = to;
             sum[e] *= corr[e];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float p = exp2_f32(s[m][e + 2 * h] - base) * unit;
+                    const float p = exp2_f32(s[m][e + 2 * h] - now);
                     s[m][e + 2 * h] = p;
                     sum[e] += p;
                 }
@@ -779,7 +792,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
         }
         ++taken;
         __syncwarp();   // the tile is in registers: its place may be filled again
-        if (lane == 0 && !lost && k0 + kQ4Stages * kQ4Block < end) fetch(k0 + kQ4Stages * kQ4Block, taken + kQ4Stages - 1);
+        if (lane == 0 && !lost && k0 + kQ4Stages * kQ4Block < end) fetch(taken + kQ4Stages - 1);
     }
 
     // ---- the warps' results meet in shared memory
@@ -791,7 +804,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
         for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
         const int j = 2 * c + e;
         if (r == 0 && j < W) {
-            res[j * PS + HD] = mx[e] - static_cast<float>(kf);
+            res[j * PS + HD] = ref[e];
             res[j * PS + HD + 1] = t;
         }
     }
@@ -848,7 +861,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     }
     __syncthreads();   // results and q rows are read: the next piece may write its own
     if (ends && unit == U - 1) {
-        before += blocks;
+        before += cost;
         ++b;
     }
     }
