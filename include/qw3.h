@@ -492,8 +492,8 @@ QW3_API int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q
  * no top-p, no min-p. A temperature <= 0 is greedy (lowest index among equal
  * maxima, probability 1). u_dev: [B] in [0, 1), values outside taken as the
  * nearest inside. A -inf logit is never drawn.
- * Weights are summed in 64-bit fixed point (2^-40 of the largest), so equal
- * inputs give equal tokens; a token whose weight is below 2^-41 of the largest
+ * Weights are summed in 64-bit fixed point (cut to 2^-40 of the largest), so equal
+ * inputs give equal tokens; a token whose weight is below 2^-40 of the largest
  * is not drawn. A row with a NaN, with no logit above -inf, with a +inf
  * (unless greedy) or with a temperature that is NaN or infinite gets token -1
  * and probability 0 and, if status_dev is not NULL, sets *status_dev to

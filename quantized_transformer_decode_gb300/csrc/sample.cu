@@ -11,10 +11,13 @@
 //
 // One thread-block cluster takes a row: its CTAs hold a slice each in shared
 // memory, so the logits are read from memory once, and histograms and totals
-// meet through distributed shared memory. A cut is found by histograms over
-// ranges of keys (1024 bins, counts and weights), each level inside the bin of
-// the one before, until the bin holds at most kList tokens; these are ranked
-// directly. A row with few distinct logits ends at a bin of one key instead.
+// meet through distributed shared memory. A cut is found by a histogram over
+// equal steps of (max l - l) / T (1024 of them down to weights of 2^-41),
+// whose bins a vocabulary's logits fill evenly, so that few of a warp's
+// additions meet in one word. Where the top-k bin and all above it hold at most
+// kList tokens, the first CTA takes these and finishes the row by itself; else
+// the cut's bin alone is ranked, or cut further by histograms over its keys
+// until it holds at most kList tokens or equal logits only.
 //
 // Sums are taken in 64-bit fixed point (2^40 for the largest weight): they are
 // the same whatever the order of the additions, so one input gives one token.
@@ -29,7 +32,7 @@ namespace {
 using u64 = unsigned long long;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024;
+constexpr int kBins = 2 * kThreads;   // two to a thread
 constexpr int kList = 256;
 constexpr int kMaxCluster = 8;
 constexpr float kOne = 1099511627776.0f;   // 2^40
@@ -119,12 +122,19 @@ __device__ __forceinline__ void scan2(u64 &a, u64 &b, u64 &ta, u64 &tb, Shared &
     b = by + y - b;
 }
 
+constexpr float kNats = 29.0f;   // exp(-29) < 2^-41: weights that round to zero
+
 struct Row {
     const float *l;   // this CTA's slice, in shared or global memory
     int n, base;      // its length, and its first token
-    float top, inv_t;
-    uint32_t rank, size;   // in the cluster
-    __device__ __forceinline__ float weight(float v) const { return expf((v - top) * inv_t); }
+    float top, inv_t, step;   // step: bins per unit of logit
+    uint32_t rank, size;      // in the cluster
+    __device__ __forceinline__ float weight(float v) const { return exp2f((v - top) * inv_t * 1.4426950408889634f); }
+    // Bin of a logit, kBins or more for one that has no weight: the float
+    // operations are monotone, so the bins follow the order of the logits.
+    __device__ __forceinline__ int bin(float v) const {
+        return static_cast<int>(fminf((top - v) * step, static_cast<float>(kBins)));
+    }
 };
 
 // Shares a word of this CTA with its cluster: afterwards slot[r] holds CTA r's.
@@ -133,20 +143,23 @@ __device__ __forceinline__ void share(const Row &row, u64 *slot, u64 v) {
     sync_cluster();
 }
 
-// Histogram of the row's keys in [lo, hi], the highest keys in bin 0.
-__device__ void histogram(const Row &row, uint32_t lo, uint32_t hi, int shift, Shared &s) {
+// Histogram of the row: bin_of(logit) gives a bin or a negative number for a
+// token left out; weights only where `weigh`.
+template <typename F>
+__device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s, F bin_of) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.cnt[i] = s.wlo[i] = s.whi[i] = 0u;
     __syncthreads();
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
         const float v = row.l[i];
-        const uint32_t k = logit_key(v);
-        if (k < lo || k > hi) continue;
-        const uint32_t bin = (hi - k) >> shift;
-        const u64 w = fixed_weight(row.weight(v));
+        const int bin = bin_of(v);
+        if (bin < 0) continue;
         atomicAdd(&s.cnt[bin], 1u);
-        const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&s.wlo[bin], wl);
-        const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
-        if (wh) atomicAdd(&s.whi[bin], wh);
+        if (weigh) {
+            const u64 w = fixed_weight(row.weight(v));
+            const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&s.wlo[bin], wl);
+            const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
+            if (wh) atomicAdd(&s.whi[bin], wh);
+        }
     }
     if (row.size == 1) {
         __syncthreads();
@@ -164,10 +177,13 @@ __device__ void histogram(const Row &row, uint32_t lo, uint32_t hi, int shift, S
         const int bin = static_cast<int>(row.rank) * share_n + i;
         uint32_t c = 0;
         u64 w = 0;
+#pragma unroll 4
         for (uint32_t p = 0; p < row.size; ++p) {
             c += remote_ld32(dsmem_map(&s.cnt[bin], p));
-            w += static_cast<u64>(remote_ld32(dsmem_map(&s.whi[bin], p))) << 32;
-            w += remote_ld32(dsmem_map(&s.wlo[bin], p));
+            if (weigh) {
+                w += static_cast<u64>(remote_ld32(dsmem_map(&s.whi[bin], p))) << 32;
+                w += remote_ld32(dsmem_map(&s.wlo[bin], p));
+            }
         }
         for (uint32_t p = 0; p < row.size; ++p) {
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_map(&s.tcnt[bin], p)), "r"(c) : "memory");
@@ -177,83 +193,110 @@ __device__ void histogram(const Row &row, uint32_t lo, uint32_t hi, int shift, S
     sync_cluster();
 }
 
+// The bin in which the running sum (of counts, or of weights) of the row's
+// histogram, over above_c and above_w, reaches target.
+struct Found {
+    bool some;
+    int bin;
+    uint32_t n;                    // tokens in the bin
+    u64 w, above_c, above_w;       // its weight; counts and weight before it
+    u64 total_c, total_w;          // of all bins
+};
+
+__device__ __forceinline__ Found find(bool by_weight, u64 target, u64 above_c, u64 above_w, Shared &s) {
+    // thread t looks at bins 2 t and 2 t + 1
+    const int b0 = 2 * threadIdx.x;
+    u64 c = static_cast<u64>(s.tcnt[b0]) + s.tcnt[b0 + 1], w = s.tw[b0] + s.tw[b0 + 1];
+    Found f;
+    scan2(c, w, f.total_c, f.total_w, s);
+    if (threadIdx.x == 0) s.found = 0u;
+    __syncthreads();
+    c += above_c;
+    w += above_w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const u64 nc = c + s.tcnt[b0 + h], nw = w + s.tw[b0 + h];
+        if (by_weight ? (w < target && nw >= target) : (c < target && nc >= target)) {
+            s.found = 1u;
+            s.bin = b0 + h;
+            s.above_cnt = c;
+            s.above_w = w;
+        }
+        c = nc;
+        w = nw;
+    }
+    __syncthreads();
+    f.some = s.found != 0u;
+    f.bin = f.some ? static_cast<int>(s.bin) : 0;
+    f.n = s.tcnt[f.bin];
+    f.w = s.tw[f.bin];
+    f.above_c = s.above_cnt;
+    f.above_w = s.above_w;
+    return f;
+}
+
+// The tokens that `in` picks, at most kList in the row, into the first CTA's
+// list; the list's length there is s.n_list. All CTAs leave together.
+template <typename F>
+__device__ __forceinline__ void gather(const Row &row, Shared &s, F in) {
+    const uint32_t n_at = dsmem_map(&s.n_list, 0u), list_at = dsmem_map(s.list, 0u);
+    for (int i = threadIdx.x; i < row.n; i += kThreads) {
+        const float v = row.l[i];
+        if (in(v)) {
+            const uint32_t at = remote_add(n_at, 1u);
+            if (at < kList)
+                remote_st(list_at + 8u * at,
+                          static_cast<u64>(logit_key(v)) << 32 | (0xffffffffu - static_cast<uint32_t>(row.base + i)));
+        }
+    }
+    if (row.size > 1) sync_cluster();
+    else __syncthreads();
+}
+
 struct Cut {
     uint32_t key;      // kept: keys above, and the first `ties` equal to it
     u64 ties;
-    u64 w;             // weight of what is kept
+    u64 w;             // weight of what is kept (by_weight cuts only)
     bool some;         // equals of the key are left out
 };
 
-// The shortest prefix of the row's order, among keys in [lo, hi], that holds
-// `target` tokens or (by_weight) reaches `target` weight. Where the whole range
-// does not, all of it. target >= 1.
-__device__ Cut prefix(const Row &row, uint32_t lo, uint32_t hi, bool by_weight, u64 target, Shared &s) {
-    u64 above_c = 0, above_w = 0;
-    const uint32_t floor_key = lo;
-    while (true) {
-        const uint32_t range = hi - lo;
-        const int bits = 32 - __clz(range), shift = bits > 10 ? bits - 10 : 0;
-        histogram(row, lo, hi, shift, s);
-        // thread t looks at bins 2 t and 2 t + 1
-        const int b0 = 2 * threadIdx.x;
-        u64 c = static_cast<u64>(s.tcnt[b0]) + s.tcnt[b0 + 1], w = s.tw[b0] + s.tw[b0 + 1], tc, tw;
-        scan2(c, w, tc, tw, s);
-        if (threadIdx.x == 0) s.found = 0u;
-        __syncthreads();
-        c += above_c;
-        w += above_w;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const u64 nc = c + s.tcnt[b0 + h], nw = w + s.tw[b0 + h];
-            if (by_weight ? (w < target && nw >= target) : (c < target && nc >= target)) {
-                s.found = 1u;
-                s.bin = b0 + h;
-                s.above_cnt = c;
-                s.above_w = w;
-            }
-            c = nc;
-            w = nw;
-        }
-        __syncthreads();
-        if (!s.found) return Cut{floor_key, ~0ull, above_w + tw, false};
-        const uint32_t bin = s.bin, n = s.tcnt[bin];
-        above_c = s.above_cnt;
-        above_w = s.above_w;
-        const u64 bw = s.tw[bin];
-        hi = hi - (bin << shift);
-        lo = (shift == 0) ? hi : (hi - lo >= (1u << shift) - 1u ? hi - ((1u << shift) - 1u) : lo);
-        if (n <= kList) break;
+// The shortest prefix of the row's order that holds `target` tokens or
+// (by_weight) reaches `target` weight, its end known to lie in the bin f of the
+// first histogram; keys below floor_key are out.
+__device__ Cut cut_in_bin(const Row &row, Found f, bool by_weight, u64 target, uint32_t floor_key, Shared &s) {
+    const int bin0 = f.bin;
+    // keys that the bin can hold, with room for the rounding of its float operations
+    const float slack = 4.0f * 1.2e-7f * (fabsf(row.top) + (bin0 + 2.0f) / row.step);
+    uint32_t hi = logit_key(row.top - static_cast<float>(bin0) / row.step + slack);
+    uint32_t lo = logit_key(row.top - (static_cast<float>(bin0) + 1.0f) / row.step - slack);
+    hi = min(hi, logit_key(row.top));
+    lo = min(max(lo, floor_key), hi);
+    while (f.n > kList) {
         if (lo == hi) {
-            // n equal logits
-            const u64 one = bw / n;
-            const u64 m = by_weight ? (target - above_w + one - 1) / one : target - above_c;
-            __syncthreads();
-            return Cut{lo, m, above_w + m * one, m < n};
+            // equal logits
+            const u64 one = f.w / f.n;
+            const u64 m = by_weight ? (target - f.above_w + one - 1) / one : target - f.above_c;
+            return Cut{lo, m, f.above_w + m * one, m < f.n};
         }
-        __syncthreads();
+        const int bits = 32 - __clz(hi - lo), shift = bits > 10 ? bits - 10 : 0;
+        histogram(row, by_weight, s, [&](float v) {
+            const uint32_t k = logit_key(v);
+            return row.bin(v) == bin0 && k >= lo && k <= hi ? static_cast<int>((hi - k) >> shift) : -1;
+        });
+        f = find(by_weight, target, f.above_c, f.above_w, s);
+        hi -= static_cast<uint32_t>(f.bin) << shift;
+        const uint32_t width = (1u << shift) - 1u;
+        lo = hi - lo >= width ? hi - width : lo;
     }
-    // ---- rank the bin's tokens in the first CTA
-    if (threadIdx.x == 0) {
-        s.n_list = 0u;
-        s.last_rank = 0u;
-    }
-    if (row.size > 1) sync_cluster();
-    else __syncthreads();
-    const uint32_t n_at = dsmem_map(&s.n_list, 0u), list_at = dsmem_map(s.list, 0u);
-    for (int i = threadIdx.x; i < row.n; i += kThreads) {
-        const uint32_t k = logit_key(row.l[i]);
-        if (k >= lo && k <= hi) {
-            const uint32_t at = remote_add(n_at, 1u);
-            if (at < kList)
-                remote_st(list_at + 8u * at, static_cast<u64>(k) << 32 | (0xffffffffu - static_cast<uint32_t>(row.base + i)));
-        }
-    }
-    if (row.size > 1) sync_cluster();
-    else __syncthreads();
+    gather(row, s, [&](float v) {
+        const uint32_t k = logit_key(v);
+        return row.bin(v) == bin0 && k >= lo && k <= hi;
+    });
     if (row.rank == 0) {
         const int n = static_cast<int>(min(s.n_list, static_cast<uint32_t>(kList)));
+        if (threadIdx.x == 0) s.last_rank = 0u;
         bool kept = false;
-        u64 before_w = above_w, same = 0, left = 0, mine = 0;
+        u64 before_w = f.above_w, same = 0, left = 0, mine = 0;
         uint32_t rank = 0;
         if (static_cast<int>(threadIdx.x) < n) {
             mine = s.list[threadIdx.x];
@@ -271,17 +314,17 @@ __device__ Cut prefix(const Row &row, uint32_t lo, uint32_t hi, bool by_weight, 
                     left += (x >> 32) == (mine >> 32);
                 }
             }
-            kept = by_weight ? before_w < target : above_c + rank < target;
+            kept = by_weight ? before_w < target : f.above_c + rank < target;
             if (kept) atomicMax(&s.last_rank, rank);
         }
         __syncthreads();
         if (kept && rank == s.last_rank) {
-            const uint32_t k = static_cast<uint32_t>(mine >> 32);
-            s.res[0] = k;
+            s.res[0] = mine >> 32;
             s.res[1] = same + 1;
             s.res[2] = before_w + s.list_w[threadIdx.x];
             s.res[3] = left;
         }
+        if (threadIdx.x == 0) s.n_list = 0u;
         __syncthreads();
         if (threadIdx.x < row.size * 4u && threadIdx.x >= 4u)
             remote_st(dsmem_map(&s.res[threadIdx.x & 3], threadIdx.x >> 2), s.res[threadIdx.x & 3]);
@@ -291,6 +334,63 @@ __device__ Cut prefix(const Row &row, uint32_t lo, uint32_t hi, bool by_weight, 
     const Cut cut{static_cast<uint32_t>(s.res[0]), s.res[1], s.res[2], s.res[3] != 0};
     __syncthreads();
     return cut;
+}
+
+// The answer: token, and its weight's share of the total. (v - top) / T in two
+// parts, so that the probability is good to a few f32 roundings.
+__device__ __forceinline__ void answer(const SampleArgs &a, int b, int token, float v, const Row &row, u64 total) {
+    a.token[b] = token;
+    if (a.next) a.next[b] = token;
+    if (a.prob) {
+        const float T = a.temperature ? fmaxf(a.temperature[b], 1e-30f) : 1.0f;
+        const float d = v - row.top, q = d / T, r = fmaf(-q, T, d) / T;
+        const float e = expf(q);
+        a.prob[b] = fmaf(e, r, e) * (kOne / static_cast<float>(total));
+    }
+}
+
+// The row from its list alone (the first CTA): the top-k tokens are all in it.
+__device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, float p, float mp, Shared &s) {
+    const int n = static_cast<int>(min(s.n_list, static_cast<uint32_t>(kList))), i = threadIdx.x;
+    u64 mine = 0, w = 0;
+    float v = 0.0f, e = 0.0f;
+    if (i < n) {
+        mine = s.list[i];
+        v = float_from_order_key(static_cast<uint32_t>(mine >> 32));
+        e = row.weight(v);
+        w = fixed_weight(e);
+        s.list_w[i] = w;
+    }
+    __syncthreads();
+    u64 before = 0;
+    uint32_t rank = 0;
+    if (i < n)
+        for (int j = 0; j < n; ++j)
+            if (s.list[j] > mine) {
+                ++rank;
+                before += s.list_w[j];
+            }
+    bool kept = i < n && rank < k;
+    if (p < 1.0f) {
+        u64 x = kept ? w : 0, y = 0, total, none;
+        scan2(x, y, total, none, s);
+        const u64 target = static_cast<u64>(ceil(static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(total)));
+        kept = kept && (rank == 0 || before < target);
+    }
+    kept = kept && e >= mp;
+    __syncthreads();
+    if (i < n) s.list_w[i] = kept ? w : 0;
+    u64 x = kept ? w : 0, y = 0, total, none;
+    scan2(x, y, total, none, s);   // its barriers also show everyone the kept weights
+    if (!kept) return;
+    const uint32_t idx = static_cast<uint32_t>(mine);   // ~index: the larger, the earlier
+    u64 first = 0;
+    for (int j = 0; j < n; ++j)
+        if (static_cast<uint32_t>(s.list[j]) > idx) first += s.list_w[j];
+    const float u = a.u[b];
+    u64 at = static_cast<u64>(static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(total));
+    if (at >= total) at = total - 1;
+    if (first <= at && at < first + w) answer(a, b, static_cast<int>(0xffffffffu - idx), v, row, total);
 }
 
 template <bool kHeld>
@@ -323,6 +423,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
         best = k > best ? k : best;
     }
     if (lane == 0) s.red[warp] = best;
+    if (tid == 0) s.n_list = 0u;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) best = s.red[w] > best ? s.red[w] : best;
@@ -345,28 +446,53 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
         return;
     }
     row.inv_t = 1.0f / fmaxf(T, 1e-30f);
+    row.step = row.inv_t * (kBins / kNats);
     const int k = a.top_k ? a.top_k[b] : 0;
     const float p = a.top_p ? a.top_p[b] : 1.0f, mp = a.min_p ? fminf(a.min_p[b], 1.0f) : 0.0f;
-    // below: weights that round to zero (exp(-29) < 2^-41)
-    const uint32_t hi = logit_key(row.top), lo = logit_key(row.top - 29.0f * fmaxf(T, 1e-30f));
-    Cut cut{lo, ~0ull, 0, false};
-    if (k > 0 && k < a.V) cut = prefix(row, lo, hi, false, static_cast<u64>(k), s);
-    if (p < 1.0f) {
-        u64 total = cut.w;
-        if (total == 0) {
-            // no top-k: the whole row's weight
-            u64 w = 0, none = 0, t0, t1;
-            for (int i = tid; i < row.n; i += kThreads) w += fixed_weight(row.weight(row.l[i]));
-            scan2(w, none, t0, t1, s);
-            total = t0;
-            if (size > 1) {
-                share(row, s.peer2, t0);
-                total = 0;
-                for (int q = 0; q < size; ++q) total += s.peer2[q];
+    // kept: every token with a weight, until a cut says otherwise
+    Cut cut{0u, ~0ull, 0, false};
+    if (k > 0 && k < a.V) {
+        histogram(row, false, s, [&](float v) {
+            const int i = row.bin(v);
+            return i < kBins ? i : -1;
+        });
+        const Found f = find(false, static_cast<u64>(k), 0, 0, s);
+        if (f.some) {
+            if (f.above_c + f.n <= kList) {
+                gather(row, s, [&](float v) { return row.bin(v) <= f.bin; });
+                if (row.rank == 0) finish_list(a, b, row, static_cast<u64>(k), p, mp, s);
+                return;
             }
+            cut = cut_in_bin(row, f, false, static_cast<u64>(k), 0u, s);
         }
-        const u64 target = static_cast<u64>(ceil(static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(total)));
-        const Cut c = prefix(row, cut.key, hi, true, target > 0 ? (target < total ? target : total) : 1ull, s);
+    }
+    if (p < 1.0f) {
+        // weights of what top-k left; of the equals of its last logit all are
+        // counted, which matters only where the cut falls among them
+        histogram(row, true, s, [&](float v) {
+            const int i = row.bin(v);
+            return i < kBins && logit_key(v) >= cut.key ? i : -1;
+        });
+        u64 x = s.tw[2 * tid] + s.tw[2 * tid + 1], y = 0, total, none;
+        scan2(x, y, total, none, s);
+        if (cut.some) {
+            const u64 one = fixed_weight(row.weight(float_from_order_key(cut.key)));
+            u64 equals = 0;
+            for (int i = tid; i < row.n; i += kThreads) equals += logit_key(row.l[i]) == cut.key;
+            u64 z = 0, all;
+            scan2(equals, z, all, none, s);
+            if (size > 1) {
+                share(row, s.peer2, all);
+                all = 0;
+                for (int q = 0; q < size; ++q) all += s.peer2[q];
+            }
+            total -= (all - cut.ties) * one;
+        }
+        u64 target = static_cast<u64>(ceil(static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(total)));
+        target = target < 1 ? 1 : (target < total ? target : total);
+        __syncthreads();
+        const Found f = find(true, target, 0, 0, s);
+        const Cut c = cut_in_bin(row, f, true, target, cut.key, s);
         if (c.key > cut.key) cut = c;
         else if (c.ties < cut.ties) cut = Cut{c.key, c.ties, 0, true};
     }
@@ -414,11 +540,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
         for (int i = i0; i < i1; ++i) {
             w += weight(i, seen);
             if (w > at) {
-                a.token[b] = row.base + i;
-                if (a.next) a.next[b] = row.base + i;
-                if (a.prob)
-                    a.prob[b] = static_cast<float>(exp((static_cast<double>(row.l[i]) - row.top) / fmaxf(T, 1e-30f)) *
-                                                   static_cast<double>(kOne) / static_cast<double>(total));
+                answer(a, b, row.base + i, row.l[i], row, total);
                 break;
             }
         }
