@@ -34,7 +34,7 @@ using u64 = unsigned long long;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2 * kThreads;   // two to a thread
 constexpr int kList = 256;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr float kOne = 1099511627776.0f;   // 2^40
 
 // Order of logits as unsigned keys; the two zeros are one value.
@@ -81,6 +81,8 @@ struct Shared {
     u64 peer2[kMaxCluster];
     u64 red[2 * kWarps + 2];
     uint32_t n_list;
+    uint64_t bar;      // the slice has arrived
+    uint32_t lost;     // it did not in time
     // what a search found
     uint32_t bin, found, last_rank;
     u64 above_cnt, above_w;
@@ -123,6 +125,17 @@ __device__ __forceinline__ void scan2(u64 &a, u64 &b, u64 &ta, u64 &tb, Shared &
 }
 
 constexpr float kNats = 29.0f;   // exp(-29) < 2^-41: weights that round to zero
+
+// Largest word of the block.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, Shared &s) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v = max(v, static_cast<uint32_t>(s.red[w]));
+    return v;
+}
 
 struct Row {
     const float *l;   // this CTA's slice, in shared or global memory
@@ -395,9 +408,9 @@ __device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, f
 
 template <bool kHeld>
 __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
-    extern __shared__ float held[];
+    extern __shared__ __align__(16) float held[];
     __shared__ Shared s;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int size = static_cast<int>(gridDim.x);   // one cluster along x
     Row row;
     row.rank = size > 1 ? cluster_rank() : 0u;
@@ -406,41 +419,74 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
     row.base = static_cast<int>(row.rank) * slice;
     row.n = max(0, min(slice, a.V - row.base));
     const float *src = a.logits + b * a.stride + row.base;
-    row.l = kHeld ? held : src;
+    row.l = src;
 
-    // ---- the largest logit, the lowest index among equals; a NaN above all
-    u64 best = 0;
-#pragma unroll 8
-    for (int i = tid; i < row.n; i += kThreads) {
-        const float v = src[i];
-        if (kHeld) held[i] = v;
-        const u64 k = v != v ? ~0ull : argmax_pack(v + 0.0f, row.base + i);
-        best = k > best ? k : best;
+    // ---- the slice into shared memory: the 16-byte aligned middle as one bulk
+    // copy, the ends by themselves, each value as far from a 16-byte boundary as in memory
+    if constexpr (kHeld) {
+        const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(src) / 4) & 3);
+        float *to = held + shift;
+        row.l = to;
+        const int head = min(row.n, (4 - shift) & 3), mid = (row.n - head) / 4 * 4;
+        if (tid == 0) {
+            mbar_init(&s.bar, 1);
+            fence_mbar_init();
+            if (mid > 0) {
+                mbar_arrive_expect_tx(&s.bar, static_cast<uint32_t>(mid) * 4u);
+                bulk_g2s(to + head, src + head, static_cast<uint32_t>(mid) * 4u, &s.bar, policy_evict_first());
+            }
+        }
+        for (int i = tid; i < head; i += kThreads) to[i] = src[i];
+        for (int i = head + mid + tid; i < row.n; i += kThreads) to[i] = src[i];
+        if (tid == 0) s.lost = 0u;
+        __syncthreads();
+        if (mid > 0 && !mbar_wait_bounded(&s.bar, 0u)) {
+            // the copy did not arrive in a second: what there is of it is taken
+            // (every thread saw the wait run out, or sees the data now)
+            s.lost = 1u;
+        }
+        __syncthreads();
+        if (s.lost && tid == 0) {
+            record_status(a.status, QW3_ERR_TIMEOUT);
+            (void)mbar_wait_bounded(&s.bar, 0u);
+        }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const u64 k = __shfl_xor_sync(0xffffffffu, best, o);
-        best = k > best ? k : best;
-    }
-    if (lane == 0) s.red[warp] = best;
+
+    // ---- the largest logit; a NaN counts above all
+    float top = -INFINITY;
+    bool nan = false;
     if (tid == 0) s.n_list = 0u;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) best = s.red[w] > best ? s.red[w] : best;
+#pragma unroll 4
+    for (int i = tid; i < row.n; i += kThreads) {
+        const float v = row.l[i];
+        nan |= v != v;
+        top = fmaxf(top, v);
+    }
+    u64 best = block_max(nan ? ~0u : logit_key(top), s);
     if (size > 1) {
         share(row, s.peer, best);
         for (int p = 0; p < size; ++p) best = s.peer[p] > best ? s.peer[p] : best;
     }
-    row.top = float_from_order_key(static_cast<uint32_t>(best >> 32));
+    row.top = float_from_order_key(static_cast<uint32_t>(best));
     const float T = a.temperature ? a.temperature[b] : 1.0f;
     const bool greedy = T <= 0.0f;
-    const bool bad = best == ~0ull || row.top == -INFINITY || !(T < INFINITY) || (!greedy && row.top == INFINITY);
+    const bool bad = best == ~0u || row.top == -INFINITY || !(T < INFINITY) || (!greedy && row.top == INFINITY);
     if (bad || greedy) {
+        u64 first = ~0ull;   // the lowest index of the largest logit
+        if (!bad) {
+            uint32_t at = ~0u;
+            for (int i = tid; i < row.n; i += kThreads)
+                if (row.l[i] == row.top) at = min(at, static_cast<uint32_t>(row.base + i));
+            first = ~0u - block_max(~0u - at, s);
+            if (size > 1) {
+                share(row, s.peer2, first);
+                for (int p = 0; p < size; ++p) first = s.peer2[p] < first ? s.peer2[p] : first;
+            }
+        }
         if (row.rank == 0 && tid == 0) {
             if (bad) record_status(a.status, QW3_ERR_NONFINITE);
-            const int arg = bad ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
-            a.token[b] = arg;
-            if (a.next) a.next[b] = max(arg, 0);
+            a.token[b] = bad ? -1 : static_cast<int>(first);
+            if (a.next) a.next[b] = bad ? 0 : static_cast<int>(first);
             if (a.prob) a.prob[b] = bad ? 0.0f : 1.0f;
         }
         return;
@@ -549,21 +595,27 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
 
 // CTAs per row and the tokens of one: a small vocabulary stays in one CTA, a
 // large one is cut into slices of which two fit an SM (up to 20480 tokens, 80
-// KB); beyond 8 slices of what one SM holds the row is read again from memory
-// (L2) at every pass.
+// KB), or finer, to 16 CTAs, while the rows together leave SMs free; beyond 16
+// slices of what one SM holds the row is read again from memory (L2) at every
+// pass.
 constexpr int kOneCta = 8192, kSlice = 20480, kMaxHeld = 45056;
 
 }  // namespace
 
 cudaError_t configure_sample() {
-    return cudaFuncSetAttribute(k_sample<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 4);
+    cudaError_t e = cudaFuncSetAttribute(k_sample<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 4 + 16);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sample<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sample<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
 }
 
 cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s) {
     if (B <= 0) return cudaSuccess;
     int size = 1;
     if (a.V > kOneCta)
-        while (size < kMaxCluster && (a.V + size - 1) / size > kSlice) size *= 2;
+        while (size < kMaxCluster && ((a.V + size - 1) / size > (size < 8 ? kSlice : kMaxHeld) ||
+                                      (static_cast<int64_t>(B) * size * 2 <= 152 && a.V / size > kOneCta)))
+            size *= 2;
     const int slice = (a.V + size - 1) / size;
     const bool is_held = slice <= kMaxHeld;
     for (int b0 = 0; b0 < B; b0 += 65535) {
@@ -580,7 +632,7 @@ cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(size, std::min(65535, B - b0));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = is_held ? static_cast<size_t>(slice) * 4 : 0;
+        cfg.dynamicSmemBytes = is_held ? static_cast<size_t>(slice) * 4 + 16 : 0;
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
