@@ -15,6 +15,7 @@
 // d = -m / 8, code = clamp(floor(x / d + 8.5), 0, 15) (8 where m = 0), scale
 // = f16(d), with x and d taken without rounding. 4.5 bits per value.
 #include <algorithm>
+#include <type_traits>
 #include <cstdint>
 
 #include "qw3_internal.cuh"
@@ -40,31 +41,92 @@ __device__ __forceinline__ int q4_lane_byte(int lane, bool v_row) {
     return v_row ? 2 * ((j >> 1) * NB + b) + (j & 1) : 4 * ((j >> 2) * NB + b) + (j & 3);
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
-
-// The row in f64 from its inputs: normalised and rotated (K; w and cs given)
-// or as it is (V), then encoded. Called by a whole warp for the few rows whose
-// f32 values leave a code or a scale undecided.
-template <int HD>
-__device__ __noinline__ void q4_encode_f64(const float *raw, const float *w, const float2 *cs, float eps, int lane,
-                                           int *code, __half *scale) {
-    constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L;
-    double x[E];
+// Loads and stores of a lane's E values; VEC where everything is aligned for one
+// access.
+template <int E, bool VEC>
+__device__ __forceinline__ void q4_ld(float (&v)[E], const float *p) {
+    if constexpr (VEC && E == 4) {
+        const float4 t = *reinterpret_cast<const float4 *>(p);
+        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else if constexpr (VEC && E == 2) {
+        const float2 t = *reinterpret_cast<const float2 *>(p);
+        v[0] = t.x; v[1] = t.y;
+    } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = raw[e];
-    if (w) {
+        for (int e = 0; e < E; ++e) v[e] = p[e];
+    }
+}
+
+template <int E, bool VEC>
+__device__ __forceinline__ void q4_st(float *p, const float (&v)[E]) {
+    if constexpr (VEC && E == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if constexpr (VEC && E == 2) {
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) p[e] = v[e];
+    }
+}
+
+// A number as the unevaluated sum of two floats, |lo| <= ulp(hi) / 2 (about 48
+// bits): products by fma, sums by Knuth's two-sum.
+struct F2 {
+    float hi, lo;
+};
+__device__ __forceinline__ F2 f2_norm(float h, float l) {
+    const float s = __fadd_rn(h, l);
+    return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ F2 f2_mul(float a, float b) {
+    const float h = __fmul_rn(a, b);
+    return {h, __fmaf_rn(a, b, -h)};
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, float b) {
+    const float h = __fmul_rn(a.hi, b);
+    return f2_norm(h, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -h)));
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+    return f2_norm(s, __fadd_rn(e, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ F2 f2_neg(F2 a) { return {-a.hi, -a.lo}; }
+__device__ __forceinline__ bool f2_less(F2 a, F2 b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ F2 f2_shfl(F2 a, int o) {
+    return {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
+}
+
+// One row of the cache from a warp: E values to a lane. raw: the inputs; for a
+// key its norm weights w and rotation cs too.
+template <int HD>
+struct Q4Src {
+    float raw[HD / 32], w[HD / 32];
+    float2 cs[HD / 32];
+    bool key;
+    float eps;
+};
+
+// The row encoded in f64: for the values that two floats do not hold or decide
+// (outside their range, or on a border to the last bit).
+template <int HD>
+__device__ __noinline__ void q4_encode_f64(const Q4Src<HD> &in, int lane, int *code, __half *scale) {
+    constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L;
+    double x[E], r = 1.0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = in.raw[e];
+    if (in.key) {
         double ss = 0.0;
 #pragma unroll
         for (int e = 0; e < E; ++e) ss += x[e] * x[e];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += shfl_xor_f64(ss, o);
-        const double r = 1.0 / sqrt(ss / HD + static_cast<double>(eps));
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        r = 1.0 / sqrt(ss / HD + static_cast<double>(in.eps));
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = x[e] * r * w[e];
+        for (int e = 0; e < E; ++e) x[e] *= in.w[e];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const double o = shfl_xor_f64(x[e], 16);
-            const double c = cs[e].x, s = cs[e].y;
+            const double o = __shfl_xor_sync(0xffffffffu, x[e], 16), c = in.cs[e].x, s = in.cs[e].y;
             x[e] = lane < 16 ? x[e] * c - o * s : x[e] * c + o * s;
         }
     }
@@ -76,8 +138,8 @@ __device__ __noinline__ void q4_encode_f64(const float *raw, const float *w, con
     }
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) {
-        P = fmax(P, shfl_xor_f64(P, o));
-        N = fmax(N, shfl_xor_f64(N, o));
+        P = fmax(P, __shfl_xor_sync(0xffffffffu, P, o));
+        N = fmax(N, __shfl_xor_sync(0xffffffffu, N, o));
     }
     const double m = P >= N ? P : -N;
 #pragma unroll
@@ -85,28 +147,111 @@ __device__ __noinline__ void q4_encode_f64(const float *raw, const float *w, con
         const double f = floor(-8.0 * x[e] / m + 8.5);
         code[e] = m == 0.0 ? 8 : static_cast<int>(fmin(fmax(f, 0.0), 15.0));
     }
-    *scale = m == 0.0 ? __float2half_rn(0.0f) : __double2half(-m / 8.0);
+    *scale = m == 0.0 ? __float2half_rn(0.0f) : __double2half(-m * r / 8.0);
 }
 
-// Encode a warp's row x, each value within err of the exact one (0 for a row
-// taken as it is). f32 decides every code and scale that lies further from a
-// border than err can carry it; where one does not, the whole row goes through
-// f64 (about one K row in thirty, hardly ever a V row), so the codes are those
-// of the exact values whatever the order of the f32 sums. Returns false for a
-// lane whose block holds a value that is not finite or too large for an f16
-// scale: it is written as zeros.
+// The row encoded with two floats to a number. The norm's factor r > 0 is
+// common to the row, so codes come from the rotated values without it: code k
+// or k - 1 by the sign of -8 y / m - (k - 8.5). The scale's rounding compares
+// squares, (m / 8)^2 against (midpoint)^2 (mean + eps), without a root. Returns
+// false (for the whole warp) where that decides nothing.
 template <int HD>
-__device__ __forceinline__ bool q4_encode(const float (&x)[HD / 32], float err, const float (&raw)[HD / 32],
-                                          const float *w, const float2 *cs, float eps, int lane,
+__device__ __noinline__ bool q4_encode_f2(const Q4Src<HD> &in, int lane, int *code, __half *scale) {
+    constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L;
+    constexpr float kSure = 0x1p-42f;
+    F2 y[E], S{0.0f, 0.0f};
+    if (in.key) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            S = f2_add(S, f2_mul(in.raw[e], in.raw[e]));
+            y[e] = f2_mul(in.raw[e], in.w[e]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) S = f2_add(S, f2_shfl(S, o));
+        S = f2_add({S.hi / HD, S.lo / HD}, {in.eps, 0.0f});
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const F2 o = f2_shfl(y[e], 16);
+            y[e] = f2_add(f2_mul(y[e], in.cs[e].x), f2_mul(o, lane < 16 ? -in.cs[e].y : in.cs[e].y));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = {in.raw[e], 0.0f};
+    }
+    F2 P = y[0], N = f2_neg(y[0]);
+#pragma unroll
+    for (int e = 1; e < E; ++e) {
+        if (f2_less(P, y[e])) P = y[e];
+        if (f2_less(N, f2_neg(y[e]))) N = f2_neg(y[e]);
+    }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+        const F2 p = f2_shfl(P, o), n = f2_shfl(N, o);
+        if (f2_less(P, p)) P = p;
+        if (f2_less(N, n)) N = n;
+    }
+    const F2 m = f2_less(P, N) ? f2_neg(N) : P;
+    const float am = fabsf(m.hi);
+    // products' low parts stay normal in this range
+    bool sure = am == 0.0f || (am > 0x1p-30f && am < 0x1p30f);
+    if (am == 0.0f) {
+        // exactly zero where the inputs are; a key's sum may have lost what f64 keeps
+        sure = !in.key || S.hi == in.eps;
+#pragma unroll
+        for (int e = 0; e < E; ++e) code[e] = 8;
+        *scale = __float2half_rn(0.0f);
+    } else {
+        const float inv = -8.0f / m.hi;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float k = rintf(fmaf(y[e].hi, inv, 8.5f));
+            // sign of -8 y - (k - 8.5) m, for m > 0
+            const F2 d = f2_add({-8.0f * y[e].hi, -8.0f * y[e].lo}, f2_neg(f2_mul(m, k - 8.5f)));
+            const float side = m.hi > 0.0f ? d.hi : -d.hi;
+            // a value's two floats are exact for V, and a tie goes up; a key's are not
+            if (in.key && fabsf(side) < kSure * am) sure = false;
+            code[e] = static_cast<int>(fminf(fmaxf(side >= 0.0f ? k : k - 1.0f, 0.0f), 15.0f));
+        }
+        if (!in.key) {
+            *scale = __float2half_rn(m.hi * -0.125f);   // m is exact
+        } else {
+            const float a32 = am * 0.125f, d32 = a32 / sqrtf(S.hi);
+            const __half h = __float2half_rn(d32);
+            const unsigned bits = __half_as_ushort(h);
+            const float hf = __half2float(h);
+            // midpoints to the f16 neighbours: 12 bits, their squares exact
+            const float up = 0.5f * (hf + __half2float(__ushort_as_half(static_cast<unsigned short>(bits + 1))));
+            const float dn = 0.5f * (hf + __half2float(__ushort_as_half(static_cast<unsigned short>(bits - 1))));
+            const F2 a{a32, (m.hi > 0.0f ? m.lo : -m.lo) * 0.125f};
+            const F2 aa = f2_add(f2_mul(a, a.hi), f2_mul(a, a.lo));
+            const F2 over = f2_add(aa, f2_neg(f2_mul(S, up * up))), under = f2_add(aa, f2_neg(f2_mul(S, dn * dn)));
+            if (!(d32 > 0x1p-13f && d32 < 65000.0f) || fabsf(over.hi) < kSure * aa.hi || fabsf(under.hi) < kSure * aa.hi) sure = false;
+            const unsigned c = over.hi > 0.0f ? bits + 1 : (under.hi < 0.0f ? bits - 1 : bits);
+            *scale = __ushort_as_half(static_cast<unsigned short>(c | (m.hi > 0.0f ? 0x8000u : 0u)));
+        }
+    }
+    return __all_sync(0xffffffffu, sure);
+}
+
+// Encode a warp's row: y are its values in f32 (a key's rotated, without the
+// norm's factor r), each within err of the exact one. f32 decides every code
+// and scale that lies further from a border than err can carry it; where one
+// does not, the whole row goes through two floats to a number (about one key
+// row in eighty, hardly ever a value row), so the codes are those of the exact
+// values whatever the order of the f32 sums. Returns false for a lane whose
+// block holds a value that is not finite or too large for an f16 scale: it is
+// written as zeros.
+template <int HD>
+__device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, float r, const Q4Src<HD> &in, int lane,
                                           int (&code)[HD / 32], __half &scale) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L;
-    float P = x[0], N = -x[0];
-    bool bad = false;
+    float P = y[0], N = -y[0];
+    bool bad = !(r < INFINITY);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        P = fmaxf(P, x[e]);
-        N = fmaxf(N, -x[e]);
-        bad |= !(fabsf(x[e]) < 524160.0f);   // 8 * 65520, where the scale rounds to infinity
+        P = fmaxf(P, y[e]);
+        N = fmaxf(N, -y[e]);
+        bad |= !(fabsf(y[e] * r) < 524160.0f);   // 8 * 65520, where the scale rounds to infinity
     }
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) {
@@ -121,17 +266,20 @@ __device__ __forceinline__ bool q4_encode(const float (&x)[HD / 32], float err, 
     if (fine && am > 0.0f) {
         // under 1e-30 the quotient leaves f32's range
         near = am < 1e-30f || (err > 0.0f && fabsf(P - N) <= 2.0f * err);
-        const float inv = -8.0f / m, tol = fmaf(16.0f * err, fabsf(inv) * 0.125f, 4e-6f);
+        const float inv = -8.0f / m, tol = fmaf(2.0f * err, fabsf(inv), 2e-6f);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float f = fmaf(x[e], inv, 8.5f);
+            const float f = fmaf(y[e], inv, 8.5f);
             near |= fabsf(f - rintf(f)) <= tol;
             code[e] = static_cast<int>(fminf(fmaxf(floorf(f), 0.0f), 15.0f));
         }
-        const float d = am * 0.125f, de = err * 0.126f;
-        scale = __float2half_rn(-m * 0.125f);
-        if (err > 0.0f)
+        const float d = am * 0.125f * r;
+        scale = __float2half_rn(m > 0.0f ? -d : d);
+        if (err > 0.0f) {
+            // r is within 8 roundings, d within one more and m's err
+            const float de = fmaf(d, 9.0f * 5.97e-8f, err * 0.126f * r);
             near |= __half_as_ushort(__float2half_rn(d - de)) != __half_as_ushort(__float2half_rn(d + de));
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) code[e] = 8;
@@ -140,13 +288,13 @@ __device__ __forceinline__ bool q4_encode(const float (&x)[HD / 32], float err, 
         near = fine && err > 0.0f;
     }
     if (__any_sync(0xffffffffu, near)) {
-        int c64[E];
-        __half s64;
-        q4_encode_f64<HD>(raw, w, cs, eps, lane, c64, &s64);
+        int c2[E];
+        __half s2;
+        if (!q4_encode_f2<HD>(in, lane, c2, &s2)) q4_encode_f64<HD>(in, lane, c2, &s2);
         if (fine) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) code[e] = c64[e];
-            scale = s64;
+            for (int e = 0; e < E; ++e) code[e] = c2[e];
+            scale = s2;
         }
     }
     return fine;
@@ -167,80 +315,92 @@ struct Q4AppendArgs {
     int32_t *status;
 };
 
-// One warp per (row, head).
-template <int HD>
+// A warp takes TPW heads of a row, one after another, their loads first: one
+// for a few rows (every warp of the GPU has something to do), four for many
+// (four loads in flight for each warp). Bound by memory: a row is read once and
+// its queries written once.
+template <int HD, int TPW, bool VEC>
 __global__ void __launch_bounds__(128) k_kv_q4_append(Q4AppendArgs a) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L, NB = Q4Row<HD>::NB;
     const int lane = threadIdx.x & 31;
-    const int task = blockIdx.y * 4 + (threadIdx.x >> 5), row = blockIdx.x;
-    const int nkv = a.c.nkv;
-    if (task >= a.nh + 2 * nkv) return;
+    const int task0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * TPW, row = blockIdx.x;
+    const int nkv = a.c.nkv, tasks = a.nh + 2 * nkv;
+    if (task0 >= tasks) return;
     int slot, pos;
-    if (!kv_q4_row(a.c, a.rows, row, slot, pos)) {
-        if (task < a.nh) {
-            float *dst = a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD;
-            for (int e = 0; e < E; ++e) dst[lane * E + e] = 0.0f;
-        }
-        return;
+    const bool there = kv_q4_row(a.c, a.rows, row, slot, pos);
+    const float *src = a.qkv + row * a.qkv_stride + lane * E;
+    Q4Src<HD> in;
+    float raw[TPW][E];
+    in.eps = a.eps;
+#pragma unroll
+    for (int t = 0; t < TPW; ++t)
+        if (task0 + t < tasks) q4_ld<E, VEC>(raw[t], src + static_cast<int64_t>(task0 + t) * HD);
+    if (there && task0 < a.nh + nkv) {
+        float cs[2 * E];
+        q4_ld<E, VEC>(*reinterpret_cast<float(*)[E]>(&cs[0]), reinterpret_cast<const float *>(a.rope + static_cast<size_t>(pos) * (HD / 2) + (lane & 15) * E));
+        q4_ld<E, VEC>(*reinterpret_cast<float(*)[E]>(&cs[E]), reinterpret_cast<const float *>(a.rope + static_cast<size_t>(pos) * (HD / 2) + (lane & 15) * E) + E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) in.cs[e] = make_float2(cs[2 * e], cs[2 * e + 1]);
     }
-    const float *src = a.qkv + row * a.qkv_stride + static_cast<int64_t>(task) * HD;
-    float raw[E], v[E], w[E];
-    float2 cs[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = raw[e] = src[lane * E + e];
-    const bool normed = task < a.nh + nkv;
-    float err = 0.0f;
-    if (normed) {
-        const float *wp = task < a.nh ? a.q_norm : a.k_norm;
-        const float2 *rr = a.rope + static_cast<size_t>(pos) * (HD / 2) + (lane & 15) * E;
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            w[e] = wp[lane * E + e];
-            cs[e] = rr[e];
-            ss = fmaf(v[e], v[e], ss);
+    for (int t = 0; t < TPW; ++t) {
+        const int task = task0 + t;
+        if (task >= tasks) return;
+        const bool query = task < a.nh;
+        if (!there) {
+            const float zero[E] = {};
+            if (query) q4_st<E, VEC>(a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD + lane * E, zero);
+            continue;
         }
-        ss = warp_sum(ss);
-        const float r = 1.0f / sqrtf(ss / static_cast<float>(HD) + a.eps);
-        float top = 0.0f;
+        in.key = task < a.nh + nkv;
+        float y[E], err = 0.0f, r = 1.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            v[e] = v[e] * r * w[e];
-            top = fmaxf(top, fabsf(v[e]));
+        for (int e = 0; e < E; ++e) y[e] = in.raw[e] = raw[t][e];
+        if (in.key) {
+            q4_ld<E, VEC>(in.w, (query ? a.q_norm : a.k_norm) + lane * E);
+            float ss = 0.0f, top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                ss = fmaf(y[e], y[e], ss);
+                y[e] *= in.w[e];
+                top = fmaxf(top, fabsf(y[e]));
+            }
+            ss = warp_sum(ss);
+            r = 1.0f / sqrtf(ss / static_cast<float>(HD) + a.eps);
+            // a rotated value is within 4 roundings of sqrt 2 times the row's
+            // largest: one for each product with w, with cos and with sin, one sum
+            if (!query) err = 6.0f * 5.97e-8f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float o = __shfl_xor_sync(0xffffffffu, y[e], 16);
+                y[e] = lane < 16 ? y[e] * in.cs[e].x - o * in.cs[e].y : o * in.cs[e].y + y[e] * in.cs[e].x;
+            }
         }
-        // every rotated value is within 20 f32 roundings of the row's largest
-        // normalised one: 9 of the sum of squares and its root, 3 products, a
-        // sum, times sqrt 2
-        err = 20.0f * 5.97e-8f * warp_max(top);
+        if (query) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float o = __shfl_xor_sync(0xffffffffu, v[e], 16);
-            v[e] = lane < 16 ? v[e] * cs[e].x - o * cs[e].y : o * cs[e].y + v[e] * cs[e].x;
+            for (int e = 0; e < E; ++e) y[e] *= r;
+            q4_st<E, VEC>(a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD + lane * E, y);
+            continue;
         }
+        const int sel = in.key ? 0 : 1, g = task - a.nh - sel * nkv;
+        int code[E];
+        __half scale;
+        const bool fine = q4_encode<HD>(y, err, r, in, lane, code, scale);
+        if (!fine) record_status(a.status, QW3_ERR_NONFINITE);
+        uint8_t *codes = kv_q4_codes<HD>(a.c, slot, sel, g) + static_cast<size_t>(pos) * (HD / 2) + q4_lane_byte<HD>(lane, sel);
+        if constexpr (E == 4) {
+            *reinterpret_cast<uint16_t *>(codes) =
+                static_cast<uint16_t>(code[0] | (code[1] << 4) | (code[2] << 8) | (code[3] << 12));
+        } else {
+            *codes = static_cast<uint8_t>(code[0] | (code[1] << 4));
+        }
+        if (lane % L == 0) kv_q4_scales<HD>(a.c, slot, sel, g)[static_cast<size_t>(pos) * NB + lane / L] = scale;
     }
-    if (task < a.nh) {
-        float *dst = a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dst[lane * E + e] = v[e];
-        return;
-    }
-    const int sel = task < a.nh + nkv ? 0 : 1, g = task - a.nh - sel * nkv;
-    int code[E];
-    __half scale;
-    const bool fine = q4_encode<HD>(v, err, raw, normed ? w : nullptr, cs, a.eps, lane, code, scale);
-    if (!fine) record_status(a.status, QW3_ERR_NONFINITE);
-    uint8_t *codes = kv_q4_codes<HD>(a.c, slot, sel, g) + static_cast<size_t>(pos) * (HD / 2) + q4_lane_byte<HD>(lane, sel);
-    if constexpr (E == 4) {
-        *reinterpret_cast<uint16_t *>(codes) =
-            static_cast<uint16_t>(code[0] | (code[1] << 4) | (code[2] << 8) | (code[3] << 12));
-    } else {
-        *codes = static_cast<uint8_t>(code[0] | (code[1] << 4));
-    }
-    if (lane % L == 0) kv_q4_scales<HD>(a.c, slot, sel, g)[static_cast<size_t>(pos) * NB + lane / L] = scale;
 }
 
-// Four values of one (row, head) of K and of V per thread.
-template <int HD>
+// Four values of one (row, head) of K and of V per thread: a warp writes whole
+// rows. Bound by the f32 values written.
+template <int HD, bool VEC>
 __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M, float *__restrict__ k_out,
                                                     float *__restrict__ v_out, size_t out_row, size_t out_head) {
     constexpr int NB = HD / 32, Q = HD / 4;
@@ -262,13 +422,10 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
                                                         static_cast<size_t>(pos) * (HD / 2) + at);
                 s = __half2float(kv_q4_scales<HD>(c, slot, sel, g)[static_cast<size_t>(pos) * NB + b]);
             }
-            float4 y;
-            y.x = s * static_cast<float>(static_cast<int>(w & 15u) - 8);
-            y.y = s * static_cast<float>(static_cast<int>((w >> 4) & 15u) - 8);
-            y.z = s * static_cast<float>(static_cast<int>((w >> 8) & 15u) - 8);
-            y.w = s * static_cast<float>(static_cast<int>(w >> 12) - 8);
-            float *out = (sel ? v_out : k_out) + row * out_row + g * out_head + 4 * j;
-            out[0] = y.x; out[1] = y.y; out[2] = y.z; out[3] = y.w;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = s * static_cast<float>(static_cast<int>((w >> (4 * e)) & 15u) - 8);
+            q4_st<4, VEC>((sel ? v_out : k_out) + row * out_row + g * out_head + 4 * j, y);
         }
     }
 }
@@ -900,14 +1057,34 @@ __global__ void __launch_bounds__(HD) k_kv_q4_join(KvQ4AttnArgs a, int cgroups, 
 
 }  // namespace
 
+namespace {
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+}  // namespace
+
 cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, const float *q_norm, const float *k_norm,
                                 float eps, const float2 *rope, const KvQ4 &c, int hd, const KvQ4Rows &rows, int nh,
                                 float *q_out, int64_t q_stride, int32_t *status, cudaStream_t s) {
     if (M <= 0) return cudaSuccess;
     const Q4AppendArgs a{qkv, M, qkv_stride, q_norm, k_norm, eps, rope, c, rows, nh, q_out, q_stride, status};
-    const dim3 grid(M, (nh + 2 * c.nkv + 3) / 4);
-    if (hd == 128) k_kv_q4_append<128><<<grid, 128, 0, s>>>(a);
-    else if (hd == 64) k_kv_q4_append<64><<<grid, 128, 0, s>>>(a);
+    const int tasks = nh + 2 * c.nkv;
+    const bool vec = aligned16(qkv) && aligned16(q_norm) && aligned16(k_norm) && aligned16(rope) && aligned16(q_out) &&
+                     qkv_stride % 4 == 0 && q_stride % 4 == 0;
+    // four heads to a warp once one to a warp would fill the GPU's 64 warps per
+    // SM: 4096 rows of 48 heads 41 us, 53 with one (64 rows 5.7 and 5.1)
+    const bool four = static_cast<int64_t>(M) * tasks >= 4ll * 64 * 152;
+    const auto go = [&](auto hd_, auto tpw_, auto vec_) {
+        constexpr int T = decltype(tpw_)::value;
+        const dim3 grid(M, (tasks + 4 * T - 1) / (4 * T));
+        k_kv_q4_append<decltype(hd_)::value, T, decltype(vec_)::value><<<grid, 128, 0, s>>>(a);
+    };
+    const auto pick = [&](auto hd_) {
+        if (four && vec) go(hd_, std::integral_constant<int, 4>{}, std::true_type{});
+        else if (four) go(hd_, std::integral_constant<int, 4>{}, std::false_type{});
+        else if (vec) go(hd_, std::integral_constant<int, 1>{}, std::true_type{});
+        else go(hd_, std::integral_constant<int, 1>{}, std::false_type{});
+    };
+    if (hd == 128) pick(std::integral_constant<int, 128>{});
+    else if (hd == 64) pick(std::integral_constant<int, 64>{});
     else return cudaErrorInvalidValue;
     return cudaGetLastError();
 }
@@ -916,9 +1093,12 @@ cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M
                               size_t out_row, size_t out_head, cudaStream_t s) {
     if (M <= 0) return cudaSuccess;
     const int64_t total = static_cast<int64_t>(M) * c.nkv * (hd / 4);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + 255) / 256, 152 * 16));
-    if (hd == 128) k_kv_q4_read<128><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else if (hd == 64) k_kv_q4_read<64><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + 255) / 256, 1 << 20));
+    const bool vec = aligned16(k_out) && aligned16(v_out) && out_row % 4 == 0 && out_head % 4 == 0;
+    if (hd == 128 && vec) k_kv_q4_read<128, true><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    else if (hd == 128) k_kv_q4_read<128, false><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    else if (hd == 64 && vec) k_kv_q4_read<64, true><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    else if (hd == 64) k_kv_q4_read<64, false><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
     else return cudaErrorInvalidValue;
     return cudaGetLastError();
 }
