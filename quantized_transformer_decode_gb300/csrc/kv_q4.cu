@@ -276,8 +276,9 @@ __device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, 
         const float d = am * 0.125f * r;
         scale = __float2half_rn(m > 0.0f ? -d : d);
         if (err > 0.0f) {
-            // r is within 8 roundings, d within one more and m's err
-            const float de = fmaf(d, 9.0f * 5.97e-8f, err * 0.126f * r);
+            // r is within 9 roundings (4.5 for half of a sum of 9, the mean, 4 for the
+            // root), d within one more and m's err
+            const float de = fmaf(d, 10.0f * 5.97e-8f, err * 0.126f * r);
             near |= __half_as_ushort(__float2half_rn(d - de)) != __half_as_ushort(__float2half_rn(d + de));
         }
     } else {
@@ -320,7 +321,7 @@ struct Q4AppendArgs {
 // (four loads in flight for each warp). Bound by memory: a row is read once and
 // its queries written once.
 template <int HD, int TPW, bool VEC>
-__global__ void __launch_bounds__(128) k_kv_q4_append(Q4AppendArgs a) {
+__global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L, NB = Q4Row<HD>::NB;
     const int lane = threadIdx.x & 31;
     const int task0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * TPW, row = blockIdx.x;
@@ -341,6 +342,36 @@ __global__ void __launch_bounds__(128) k_kv_q4_append(Q4AppendArgs a) {
         q4_ld<E, VEC>(*reinterpret_cast<float(*)[E]>(&cs[E]), reinterpret_cast<const float *>(a.rope + static_cast<size_t>(pos) * (HD / 2) + (lane & 15) * E) + E);
 #pragma unroll
         for (int e = 0; e < E; ++e) in.cs[e] = make_float2(cs[2 * e], cs[2 * e + 1]);
+    }
+    if (TPW > 1 && there && task0 + TPW <= a.nh) {
+        // queries only, as most heads are: side by side, their shuffles in flight together
+        float w[E], ss[TPW];
+        q4_ld<E, VEC>(w, a.q_norm + lane * E);
+#pragma unroll
+        for (int t = 0; t < TPW; ++t) {
+            ss[t] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                ss[t] = fmaf(raw[t][e], raw[t][e], ss[t]);
+                raw[t][e] *= w[e];
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int t = 0; t < TPW; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
+#pragma unroll
+        for (int t = 0; t < TPW; ++t) {
+            const float r = rsqrtf(ss[t] / static_cast<float>(HD) + a.eps);
+            float y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float o = __shfl_xor_sync(0xffffffffu, raw[t][e], 16);
+                y[e] = r * (lane < 16 ? raw[t][e] * in.cs[e].x - o * in.cs[e].y : o * in.cs[e].y + raw[t][e] * in.cs[e].x);
+            }
+            q4_st<E, VEC>(a.q_out + row * a.q_stride + static_cast<int64_t>(task0 + t) * HD + lane * E, y);
+        }
+        return;
     }
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
@@ -366,7 +397,7 @@ __global__ void __launch_bounds__(128) k_kv_q4_append(Q4AppendArgs a) {
                 top = fmaxf(top, fabsf(y[e]));
             }
             ss = warp_sum(ss);
-            r = 1.0f / sqrtf(ss / static_cast<float>(HD) + a.eps);
+            r = rsqrtf(ss / static_cast<float>(HD) + a.eps);
             // a rotated value is within 4 roundings of sqrt 2 times the row's
             // largest: one for each product with w, with cos and with sin, one sum
             if (!query) err = 6.0f * 5.97e-8f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
@@ -398,33 +429,34 @@ __global__ void __launch_bounds__(128) k_kv_q4_append(Q4AppendArgs a) {
     }
 }
 
-// Four values of one (row, head) of K and of V per thread: a warp writes whole
-// rows. Bound by the f32 values written.
+// A block per row, four values of one head of K and of V to a thread: a warp
+// writes whole rows. Bound by the f32 values written.
 template <int HD, bool VEC>
 __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M, float *__restrict__ k_out,
                                                     float *__restrict__ v_out, size_t out_row, size_t out_head) {
     constexpr int NB = HD / 32, Q = HD / 4;
-    const int64_t total = static_cast<int64_t>(M) * c.nkv * Q;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const int j = static_cast<int>(i % Q);
-        const int64_t rg = i / Q;
-        const int g = static_cast<int>(rg % c.nkv), row = static_cast<int>(rg / c.nkv);
-        int slot, pos;
-        const bool there = kv_q4_row(c, rows, row, slot, pos);
+    const int row = blockIdx.x;
+    int slot, pos;
+    const bool there = kv_q4_row(c, rows, row, slot, pos);
+    for (int i = threadIdx.x; i < c.nkv * Q; i += blockDim.x) {
+        const int j = i % Q, g = i / Q;
         const int b = j / 8, q = j % 8;   // block, quadruple of the block
+        unsigned w[2] = {0x8888u, 0x8888u};
+        float s[2] = {0.0f, 0.0f};
+        if (there) {
+#pragma unroll
+            for (int sel = 0; sel < 2; ++sel) {
+                const int at = sel ? 2 * (q * NB + b) : 4 * ((q >> 1) * NB + b) + 2 * (q & 1);
+                w[sel] = *reinterpret_cast<const uint16_t *>(kv_q4_codes<HD>(c, slot, sel, g) +
+                                                             static_cast<size_t>(pos) * (HD / 2) + at);
+                s[sel] = __half2float(kv_q4_scales<HD>(c, slot, sel, g)[static_cast<size_t>(pos) * NB + b]);
+            }
+        }
 #pragma unroll
         for (int sel = 0; sel < 2; ++sel) {
-            const int at = sel ? 2 * (q * NB + b) : 4 * ((q >> 1) * NB + b) + 2 * (q & 1);
-            unsigned w = 0x8888u;
-            float s = 0.0f;
-            if (there) {
-                w = *reinterpret_cast<const uint16_t *>(kv_q4_codes<HD>(c, slot, sel, g) +
-                                                        static_cast<size_t>(pos) * (HD / 2) + at);
-                s = __half2float(kv_q4_scales<HD>(c, slot, sel, g)[static_cast<size_t>(pos) * NB + b]);
-            }
             float y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = s * static_cast<float>(static_cast<int>((w >> (4 * e)) & 15u) - 8);
+            for (int e = 0; e < 4; ++e) y[e] = s[sel] * static_cast<float>(static_cast<int>((w[sel] >> (4 * e)) & 15u) - 8);
             q4_st<4, VEC>((sel ? v_out : k_out) + row * out_row + g * out_head + 4 * j, y);
         }
     }
@@ -1092,13 +1124,12 @@ cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, con
 cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M, float *k_out, float *v_out,
                               size_t out_row, size_t out_head, cudaStream_t s) {
     if (M <= 0) return cudaSuccess;
-    const int64_t total = static_cast<int64_t>(M) * c.nkv * (hd / 4);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + 255) / 256, 1 << 20));
+    const unsigned threads = static_cast<unsigned>(std::min(256, (c.nkv * (hd / 4) + 31) / 32 * 32));
     const bool vec = aligned16(k_out) && aligned16(v_out) && out_row % 4 == 0 && out_head % 4 == 0;
-    if (hd == 128 && vec) k_kv_q4_read<128, true><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else if (hd == 128) k_kv_q4_read<128, false><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else if (hd == 64 && vec) k_kv_q4_read<64, true><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else if (hd == 64) k_kv_q4_read<64, false><<<grid, 256, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    if (hd == 128 && vec) k_kv_q4_read<128, true><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    else if (hd == 128) k_kv_q4_read<128, false><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    else if (hd == 64 && vec) k_kv_q4_read<64, true><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
+    else if (hd == 64) k_kv_q4_read<64, false><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
     else return cudaErrorInvalidValue;
     return cudaGetLastError();
 }
