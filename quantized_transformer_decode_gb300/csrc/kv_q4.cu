@@ -327,15 +327,18 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
     const int task0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * TPW, row = blockIdx.x;
     const int nkv = a.c.nkv, tasks = a.nh + 2 * nkv;
     if (task0 >= tasks) return;
-    int slot, pos;
-    const bool there = kv_q4_row(a.c, a.rows, row, slot, pos);
     const float *src = a.qkv + row * a.qkv_stride + lane * E;
     Q4Src<HD> in;
     float raw[TPW][E];
     in.eps = a.eps;
+    pdl_wait();
+    // every load that waits for no other first
 #pragma unroll
     for (int t = 0; t < TPW; ++t)
         if (task0 + t < tasks) q4_ld<E, VEC>(raw[t], src + static_cast<int64_t>(task0 + t) * HD);
+    if (TPW == 1) q4_ld<E, VEC>(in.w, (task0 < a.nh ? a.q_norm : a.k_norm) + lane * E);
+    int slot, pos;
+    const bool there = kv_q4_row(a.c, a.rows, row, slot, pos);
     if (there && task0 < a.nh + nkv) {
         float cs[2 * E];
         q4_ld<E, VEC>(*reinterpret_cast<float(*)[E]>(&cs[0]), reinterpret_cast<const float *>(a.rope + static_cast<size_t>(pos) * (HD / 2) + (lane & 15) * E));
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = in.raw[e] = raw[t][e];
         if (in.key) {
-            q4_ld<E, VEC>(in.w, (query ? a.q_norm : a.k_norm) + lane * E);
+            if (TPW > 1) q4_ld<E, VEC>(in.w, (query ? a.q_norm : a.k_norm) + lane * E);
             float ss = 0.0f, top = 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -430,13 +433,15 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
 }
 
 // A block per row, four values of one head of K and of V to a thread: a warp
-// writes whole rows. Bound by the f32 values written.
+// writes whole rows. Bound by the f32 values written, which leave L2 first
+// (8192 rows of 8 heads, 67 MB: 17.5 us a call, 22.2 with plain stores).
 template <int HD, bool VEC>
 __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M, float *__restrict__ k_out,
                                                     float *__restrict__ v_out, size_t out_row, size_t out_head) {
     constexpr int NB = HD / 32, Q = HD / 4;
     const int row = blockIdx.x;
     int slot, pos;
+    pdl_wait();
     const bool there = kv_q4_row(c, rows, row, slot, pos);
     for (int i = threadIdx.x; i < c.nkv * Q; i += blockDim.x) {
         const int j = i % Q, g = i / Q;
@@ -457,7 +462,9 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
             float y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = s[sel] * static_cast<float>(static_cast<int>((w[sel] >> (4 * e)) & 15u) - 8);
-            q4_st<4, VEC>((sel ? v_out : k_out) + row * out_row + g * out_head + 4 * j, y);
+            float *to = (sel ? v_out : k_out) + row * out_row + g * out_head + 4 * j;
+            if constexpr (VEC) __stcs(reinterpret_cast<float4 *>(to), make_float4(y[0], y[1], y[2], y[3]));
+            else q4_st<4, false>(to, y);
         }
     }
 }
@@ -467,11 +474,12 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 // out = sum_j softmax_j(scale q.K_j) V_j over the 4-bit rows. The columns of
 // one kv head (its group's heads times the query rows) share every cached
 // byte: a unit of work is up to 8 columns of one kv head and sequence, a block
-// of it 128 positions. The blocks of all units in one row are dealt to the
-// CTAs in equal contiguous shares (the lengths are on the device: each CTA sums
-// them), so that sequences of any lengths keep every SM busy to the end; a unit
-// that a share's end cuts leaves partial results, which a second small kernel
-// joins. A warp takes tiles of 32 positions and multiplies with mma.m16n8k16
+// of it 128 positions. Few units: a cluster of CTAs takes each and joins its
+// results through distributed shared memory, in one launch. Many: the blocks of
+// all units in one row are dealt to the CTAs in equal contiguous shares (the
+// lengths are on the device: each CTA sums them), so that sequences of any
+// lengths keep every SM busy to the end; a unit that a share's end cuts leaves
+// partial results, which a second small kernel joins. A warp takes tiles of 32 positions and multiplies with mma.m16n8k16
 // (f16 in, f32 out), positions along m for S = K Q^T, dimensions along m for O
 // = V^T P^T:
 //  - codes are exact in f16 (-8..7): a word of 8 codes becomes 4 half2
@@ -548,7 +556,9 @@ __device__ __forceinline__ float half_of(uint32_t w, int i) {
     return i ? __high2float(h) : __low2float(h);
 }
 
-constexpr int kQ4Warps = 4, kQ4Tile = 32, kQ4Block = kQ4Warps * kQ4Tile;
+// Warps of a CTA: kQ4Warps where units are dealt out in blocks, kQ4ClusterWarps
+// where a cluster takes a unit.
+constexpr int kQ4Warps = 4, kQ4ClusterWarps = 8, kQ4Tile = 32, kQ4Block = kQ4Warps * kQ4Tile, kQ4MaxCluster = 16;
 
 // Positions of sequence b, within what the call allows.
 __device__ __forceinline__ int q4_len(const KvQ4AttnArgs &a, int b) {
@@ -623,8 +633,11 @@ __device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
 // Workspace: two partial results of W columns for each CTA (of the unit that
 // its share begins inside, and of the one that it ends inside), then the first
 // and the last CTA of each unit.
-template <int HD, int W>
-__global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
+// CLUSTER: no workspace; grid (csize, units), clusters along x.
+template <int HD, int W, bool CLUSTER>
+__global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, CLUSTER ? (W <= 4 ? 2 : 1) : (W <= 4 ? 4 : 3))
+    k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
+    constexpr int NW = CLUSTER ? kQ4ClusterWarps : kQ4Warps, kStep = NW * kQ4Tile;
     constexpr int NB = HD / 32, NT = q4_ops(W);
     constexpr int DUP = W <= 4 ? 4 / W : 1;          // blocks that share an operand
     constexpr int NI = (NB + DUP - 1) / DUP;         // P operands per 16 positions
@@ -635,10 +648,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     using St = Q4Stage<HD>;
     static_assert(W * PS * 4 <= kQ4Stages * St::bytes, "a warp's results fit its ring");
     extern __shared__ __align__(128) uint8_t q4_ring[];   // [warp][kQ4Stages] tiles; a piece's results after it
-    __shared__ uint64_t s_bar[kQ4Warps][kQ4Stages];
+    __shared__ uint64_t s_bar[NW][kQ4Stages];
+    __shared__ float s_joined[CLUSTER ? W * PS : 1];   // this CTA's result, for its cluster
     __shared__ __align__(16) __half s_q[W][2][QS];      // hi and lo; see below for the order of a row
     __shared__ float s_exp[W];
-    __shared__ int64_t s_red[kQ4Warps];
+    __shared__ int64_t s_red[NW];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int G = a.nh / a.c.nkv, cols = G * a.rows, U = a.c.nkv * cgroups;
@@ -652,22 +666,26 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     bool lost = false;      // a copy did not arrive in time, the lost_at-th tile's
     uint32_t lost_at = 0;
     const uint64_t policy = policy_evict_first();
+    pdl_wait();
 
     // ---- this CTA's share [at, stop) of the blocks
-    int64_t mine = 0;
-    for (int i = tid; i < a.B; i += kQ4Warps * 32) mine += q4_blocks(a, i) + kQ4UnitCost;
-    const int64_t all = q4_sum(mine, s_red);
-    // no share is empty: the join counts on every CTA between a unit's first and last
-    const int64_t total = all * U, P = min(static_cast<int64_t>(gridDim.x), total);
-    if (blockIdx.x >= P) return;
-    int64_t at = total * blockIdx.x / P;
-    const int64_t stop = total * (blockIdx.x + 1) / P;
+    int64_t at = 0, stop = 1;
+    if constexpr (!CLUSTER) {
+        int64_t mine = 0;
+        for (int i = tid; i < a.B; i += NW * 32) mine += q4_blocks(a, i) + kQ4UnitCost;
+        const int64_t all = a.B > 1 ? q4_sum(mine, s_red) : q4_blocks(a, 0) + kQ4UnitCost;
+        // no share is empty: the join counts on every CTA between a unit's first and last
+        const int64_t total = all * U, P = min(static_cast<int64_t>(gridDim.x), total);
+        if (blockIdx.x >= P) return;
+        at = total * blockIdx.x / P;
+        stop = total * (blockIdx.x + 1) / P;
+    }
     // its first sequence: sums of 128 sequences at a time, then one by one
-    int b = 0;
+    int b = CLUSTER ? static_cast<int>(blockIdx.y) / U : 0;
     int64_t before = 0;   // cost of the sequences below b (of one unit)
-    if (a.B > 1) {
+    if (!CLUSTER && a.B > 1) {
         const int64_t want = at / U;
-        for (int b0 = 0; b0 < a.B; b0 += kQ4Warps * 32) {
+        for (int b0 = 0; b0 < a.B; b0 += NW * 32) {
             const int64_t n = b0 + tid < a.B ? q4_blocks(a, b0 + tid) + kQ4UnitCost : 0;
             int64_t run = n;
 #pragma unroll
@@ -680,7 +698,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
             __syncthreads();
             int64_t lead = before, sum = 0;
 #pragma unroll
-            for (int w = 0; w < kQ4Warps; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 if (w < warp) lead += s_red[w];
                 sum += s_red[w];
             }
@@ -703,21 +721,37 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     // ---- the next piece: blocks [blk0, blk1) of unit (b, g, cg)
     int len, slot;
     const int blocks = q4_blocks(a, b, &len, &slot);
-    // a unit's cost: kQ4UnitCost, then its blocks
-    const int64_t in_b = at - before * U;
-    const int cost = blocks + kQ4UnitCost;
-    const int unit = static_cast<int>(in_b / cost), g = unit / cgroups, cg = unit % cgroups;
-    const int off0 = static_cast<int>(in_b - static_cast<int64_t>(unit) * cost);
-    const int off1 = static_cast<int>(min(static_cast<int64_t>(cost), off0 + (stop - at)));
-    const int blk0 = max(0, off0 - kQ4UnitCost), blk1 = max(0, off1 - kQ4UnitCost);
-    at += off1 - off0;
-    if (blk0 == blk1) continue;   // the share ends before the unit's first block
+    int unit, blk0 = 0, blk1 = 1, start, end, cost = 0;
+    if constexpr (CLUSTER) {
+        unit = static_cast<int>(blockIdx.y) % U;
+    } else {
+        // a unit's cost: kQ4UnitCost, then its blocks
+        const int64_t in_b = at - before * U;
+        cost = blocks + kQ4UnitCost;
+        unit = static_cast<int>(in_b / cost);
+        const int off0 = static_cast<int>(in_b - static_cast<int64_t>(unit) * cost);
+        const int off1 = static_cast<int>(min(static_cast<int64_t>(cost), off0 + (stop - at)));
+        blk0 = max(0, off0 - kQ4UnitCost);
+        blk1 = max(0, off1 - kQ4UnitCost);
+        at += off1 - off0;
+        if (blk0 == blk1) continue;   // the share ends before the unit's first block
+    }
+    const int g = unit / cgroups, cg = unit % cgroups;
     const int col0 = cg * W, ncol = min(W, cols - col0);
     // positions that this group's last column sees
     const int seen = len - a.rows + (col0 + ncol - 1) / G + 1;
-    const int start = blk0 * kQ4Block, end = min(seen, blk1 * kQ4Block);
+    if constexpr (CLUSTER) {
+        // an even share of the unit's tiles
+        const int64_t tiles = max(0, (seen + kQ4Tile - 1) / kQ4Tile);
+        start = static_cast<int>(tiles * blockIdx.x / gridDim.x) * kQ4Tile;
+        end = min(seen, static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x) * kQ4Tile);
+        at = stop;
+    } else {
+        start = blk0 * kQ4Block;
+        end = min(seen, blk1 * kQ4Block);
+    }
 
-    // ---- tiles of this warp: every kQ4Warps-th of the piece, the first ones on
+    // ---- tiles of this warp: every NW-th of the piece, the first ones on
     // their way before anything else
     int k0 = start + warp * kQ4Tile;
     // (lane 0's) next tile: codes and scales of K; V's lie a fixed distance behind
@@ -732,15 +766,15 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
         bulk_g2s(to + St::KS, scales, St::kScales, bar, policy);
         bulk_g2s(to + St::V, codes + to_v, St::kCodes, bar, policy);
         bulk_g2s(to + St::VS, scales + to_v, St::kScales, bar, policy);
-        codes += kQ4Block * (HD / 2);
-        scales += kQ4Block * (HD / 16);
+        codes += kStep * (HD / 2);
+        scales += kStep * (HD / 16);
     };
     if (lane == 0 && !lost) {
         // the last piece's results lay in the ring
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < kQ4Stages; ++i)
-            if (k0 + i * kQ4Block < end) fetch(taken + i);
+            if (k0 + i * kStep < end) fetch(taken + i);
     }
     // Rows i of an operand along m hold positions of its eight in this order, so
     // that the four positions of one load of V lie together and no load of K
@@ -750,7 +784,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     // ---- q columns, while the first rows are on their way: scaled by a power
     // of two, split into hi and lo. Value 8 i + p of a row lies at 8 i + 2 (p &
     // 3) + (p >> 2), so that the pairs (p, p + 4) of an operand lie together.
-    for (int j = warp; j < W; j += kQ4Warps) {
+    for (int j = warp; j < W; j += NW) {
         constexpr int E = HD / 32;
         float x[E], amax = 0.0f;
         const int cc = col0 + j;
@@ -818,7 +852,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     // hi lanes keep x (cut to f16 below), lo lanes what the cut leaves
     const uint32_t cut = (W <= 4 && c < 2) ? 0u : 0xFFFFE000u;
 
-    for (; k0 < end; k0 += kQ4Block) {
+    for (; k0 < end; k0 += kStep) {
         const uint8_t *st = ring + taken % kQ4Stages * St::bytes;
         if (!lost && !mbar_wait_bounded(&s_bar[warp][taken % kQ4Stages], (taken / kQ4Stages) & 1u)) {
             lost = true;   // no further copy is started
@@ -981,7 +1015,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
         }
         ++taken;
         __syncwarp();   // the tile is in registers: its place may be filled again
-        if (lane == 0 && !lost && k0 + kQ4Stages * kQ4Block < end) fetch(taken + kQ4Stages - 1);
+        if (lane == 0 && !lost && k0 + kQ4Stages * kStep < end) fetch(taken + kQ4Stages - 1);
     }
 
     // ---- the warps' results meet in shared memory
@@ -1018,20 +1052,26 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
     __syncthreads();
     const bool begins = blk0 == 0, ends = blk1 == blocks;
     float *ws = a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * W * PS;
-    for (int x = tid; x < ncol * HD; x += kQ4Warps * 32) {
+    for (int x = tid; x < ncol * HD; x += NW * 32) {
         const int j = x / HD, d = x % HD;
         float M = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kQ4Warps; ++w) M = fmaxf(M, results(w)[j * PS + HD]);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, results(w)[j * PS + HD]);
         if (M != -INFINITY)
 #pragma unroll
-            for (int w = 0; w < kQ4Warps; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const float *p = results(w) + j * PS;
                 const float f = exp2_f32(p[HD] - M);
                 l = fmaf(p[HD + 1], f, l);
                 o = fmaf(p[d], f, o);
             }
-        if (begins && ends) {
+        if constexpr (CLUSTER) {
+            s_joined[j * PS + d] = o;
+            if (d == 0) {
+                s_joined[j * PS + HD] = M;
+                s_joined[j * PS + HD + 1] = l;
+            }
+        } else if (begins && ends) {
             const int cc = col0 + j;
             a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
                 l > 0.0f ? o / l : 0.0f;
@@ -1043,13 +1083,37 @@ __global__ void __launch_bounds__(kQ4Warps * 32, W <= 4 ? 4 : 3) k_kv_q4_attn(Kv
             }
         }
     }
-    if (tid == 0 && owners) {
+    if constexpr (CLUSTER) {
+        // each CTA joins its share of the outputs over the cluster
+        const int peers = static_cast<int>(gridDim.x);
+        __syncwarp();
+        hw_cluster_sync();
+        for (int x = static_cast<int>(blockIdx.x) * NW * 32 + tid; x < ncol * HD; x += peers * NW * 32) {
+            const int j = x / HD, d = x % HD;
+            float M = -INFINITY, l = 0.0f, o = 0.0f;
+#pragma unroll 4
+            for (int p = 0; p < peers; ++p) M = fmaxf(M, dsmem_ld(dsmem_map(&s_joined[j * PS + HD], p)));
+            if (M != -INFINITY)
+#pragma unroll 4
+                for (int p = 0; p < peers; ++p) {
+                    const float f = exp2_f32(dsmem_ld(dsmem_map(&s_joined[j * PS + HD], p)) - M);
+                    l = fmaf(dsmem_ld(dsmem_map(&s_joined[j * PS + HD + 1], p)), f, l);
+                    o = fmaf(dsmem_ld(dsmem_map(&s_joined[j * PS + d], p)), f, o);
+                }
+            const int cc = col0 + j;
+            a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
+                l > 0.0f ? o / l : 0.0f;
+        }
+        __syncwarp();
+        hw_cluster_sync();   // nobody leaves while its result is read
+    }
+    if (!CLUSTER && tid == 0 && owners) {
         int2 *own = owners + static_cast<size_t>(b) * U + unit;
         if (begins) own->x = static_cast<int>(blockIdx.x);
         if (ends) own->y = static_cast<int>(blockIdx.x);
     }
     __syncthreads();   // results and q rows are read: the next piece may write its own
-    if (ends && unit == U - 1) {
+    if (!CLUSTER && ends && unit == U - 1) {
         before += cost;
         ++b;
     }
@@ -1107,18 +1171,17 @@ cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, con
     const auto go = [&](auto hd_, auto tpw_, auto vec_) {
         constexpr int T = decltype(tpw_)::value;
         const dim3 grid(M, (tasks + 4 * T - 1) / (4 * T));
-        k_kv_q4_append<decltype(hd_)::value, T, decltype(vec_)::value><<<grid, 128, 0, s>>>(a);
+        return launch_pdl(k_kv_q4_append<decltype(hd_)::value, T, decltype(vec_)::value>, grid, 128, 0, 1, s, a);
     };
     const auto pick = [&](auto hd_) {
-        if (four && vec) go(hd_, std::integral_constant<int, 4>{}, std::true_type{});
-        else if (four) go(hd_, std::integral_constant<int, 4>{}, std::false_type{});
-        else if (vec) go(hd_, std::integral_constant<int, 1>{}, std::true_type{});
-        else go(hd_, std::integral_constant<int, 1>{}, std::false_type{});
+        if (four && vec) return go(hd_, std::integral_constant<int, 4>{}, std::true_type{});
+        if (four) return go(hd_, std::integral_constant<int, 4>{}, std::false_type{});
+        if (vec) return go(hd_, std::integral_constant<int, 1>{}, std::true_type{});
+        return go(hd_, std::integral_constant<int, 1>{}, std::false_type{});
     };
-    if (hd == 128) pick(std::integral_constant<int, 128>{});
-    else if (hd == 64) pick(std::integral_constant<int, 64>{});
-    else return cudaErrorInvalidValue;
-    return cudaGetLastError();
+    if (hd == 128) return pick(std::integral_constant<int, 128>{});
+    if (hd == 64) return pick(std::integral_constant<int, 64>{});
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M, float *k_out, float *v_out,
@@ -1126,20 +1189,19 @@ cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M
     if (M <= 0) return cudaSuccess;
     const unsigned threads = static_cast<unsigned>(std::min(256, (c.nkv * (hd / 4) + 31) / 32 * 32));
     const bool vec = aligned16(k_out) && aligned16(v_out) && out_row % 4 == 0 && out_head % 4 == 0;
-    if (hd == 128 && vec) k_kv_q4_read<128, true><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else if (hd == 128) k_kv_q4_read<128, false><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else if (hd == 64 && vec) k_kv_q4_read<64, true><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else if (hd == 64) k_kv_q4_read<64, false><<<M, threads, 0, s>>>(c, rows, M, k_out, v_out, out_row, out_head);
-    else return cudaErrorInvalidValue;
-    return cudaGetLastError();
+    const auto kernel = hd == 128 ? (vec ? k_kv_q4_read<128, true> : k_kv_q4_read<128, false>)
+                                  : (vec ? k_kv_q4_read<64, true> : k_kv_q4_read<64, false>);
+    if (hd != 128 && hd != 64) return cudaErrorInvalidValue;
+    return launch_pdl(kernel, dim3(M), threads, 0, 1, s, c, rows, M, k_out, v_out, out_row, out_head);
 }
 
 namespace {
 
-// How a call is split: width class of the columns, column groups, CTAs.
+// How a call is split: width class of the columns, column groups; CTAs to a
+// unit's cluster, or (0) CTAs to deal the blocks to.
 struct Q4Plan {
-    int W, cgroups, ctas;
-    bool whole;   // units of one block: none is cut
+    int W, cgroups, csize, ctas;
+    bool whole;   // no unit is cut: no workspace, no second kernel
 };
 
 Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
@@ -1147,13 +1209,20 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
     Q4Plan p;
     p.W = cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : 8;
     p.cgroups = (cols + p.W - 1) / p.W;
-    // the CTAs that fit at once; for little work two blocks to each, below which
-    // the joining costs more than the wait for a second block
-    const int fit = 152 * (p.W <= 4 ? 4 : 3);
-    const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
     const int64_t units = static_cast<int64_t>(std::max(B, 1)) * nkv * p.cgroups;
+    const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
+    // Clusters while all of them fit at once (two CTAs to an SM, one at W = 8)
+    // and a warp has eight tiles at most: beyond, dealing out blocks uses the
+    // SMs better than saving the second launch does.
+    const int64_t fit_cluster = p.W <= 4 ? 304 : 152;
+    const int64_t need = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4ClusterWarps * kQ4Tile - 1) / (kQ4ClusterWarps * kQ4Tile));
+    int csize = 1;
+    while (csize < kQ4MaxCluster && csize < need && units * csize * 2 <= fit_cluster) csize *= 2;
+    p.csize = units * csize <= fit_cluster && need <= 8ll * csize ? csize : 0;
+    // the CTAs that fit at once; for little work two blocks to each
+    const int fit = 152 * (p.W <= 4 ? 4 : 3);
     p.ctas = static_cast<int>(std::min<int64_t>(fit, std::max(units, units * ((most + 1) / 2))));
-    p.whole = most == 1;
+    p.whole = p.csize > 0 || most == 1;
     return p;
 }
 
@@ -1162,11 +1231,24 @@ size_t q4_parts_bytes(const Q4Plan &p, int hd) {
 }
 
 template <int HD, int W>
+constexpr size_t q4_attn_smem(int warps) { return static_cast<size_t>(warps) * kQ4Stages * Q4Stage<HD>::bytes; }
+
+template <int HD, int W>
+cudaError_t configure_q4_attn() {
+    cudaError_t e = cudaFuncSetAttribute(k_kv_q4_attn<HD, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(q4_attn_smem<HD, W>(kQ4ClusterWarps)));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_q4_attn<HD, W, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+}
+
+template <int HD, int W>
 cudaError_t launch_q4_attn_w(const KvQ4AttnArgs &a, const Q4Plan &p, int2 *owners, cudaStream_t s) {
-    constexpr size_t smem = static_cast<size_t>(kQ4Warps) * kQ4Stages * Q4Stage<HD>::bytes;
-    static_assert(smem <= 40 * 1024, "fits without an opt-in");
-    k_kv_q4_attn<HD, W><<<p.ctas, kQ4Warps * 32, smem, s>>>(a, p.cgroups, owners);
-    return cudaGetLastError();
+    static_assert(q4_attn_smem<HD, W>(kQ4Warps) <= 40 * 1024, "fits without an opt-in");
+    if (p.csize)
+        return launch_pdl(k_kv_q4_attn<HD, W, true>, dim3(p.csize, static_cast<unsigned>(a.B) * a.c.nkv * p.cgroups),
+                          kQ4ClusterWarps * 32, q4_attn_smem<HD, W>(kQ4ClusterWarps), p.csize, s, a, p.cgroups, owners);
+    return launch_pdl(k_kv_q4_attn<HD, W, false>, dim3(p.ctas), kQ4Warps * 32, q4_attn_smem<HD, W>(kQ4Warps), 1, s, a,
+                      p.cgroups, owners);
 }
 
 template <int HD>
@@ -1180,19 +1262,23 @@ cudaError_t launch_q4_attn_hd(const KvQ4AttnArgs &a, const Q4Plan &p, cudaStream
         case 8: e = launch_q4_attn_w<HD, 8>(a, p, owners, s); break;
     }
     if (e != cudaSuccess || p.whole) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.nh) * a.rows * a.B);
-    cfg.blockDim = dim3(HD);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_kv_q4_join<HD>, a, p.cgroups, p.W, static_cast<const int2 *>(owners));
+    return launch_pdl(k_kv_q4_join<HD>, dim3(static_cast<unsigned>(a.nh) * a.rows * a.B), HD, 0, 1, s, a, p.cgroups, p.W,
+                      static_cast<const int2 *>(owners));
 }
 
 }  // namespace
+
+cudaError_t configure_kv_q4() {
+    cudaError_t e = configure_q4_attn<128, 1>();
+    if (e == cudaSuccess) e = configure_q4_attn<128, 2>();
+    if (e == cudaSuccess) e = configure_q4_attn<128, 4>();
+    if (e == cudaSuccess) e = configure_q4_attn<128, 8>();
+    if (e == cudaSuccess) e = configure_q4_attn<64, 1>();
+    if (e == cudaSuccess) e = configure_q4_attn<64, 2>();
+    if (e == cudaSuccess) e = configure_q4_attn<64, 4>();
+    if (e == cudaSuccess) e = configure_q4_attn<64, 8>();
+    return e;
+}
 
 int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len) {
     return q4_plan(B, rows, nh, nkv, max_len).whole ? 1 : 2;

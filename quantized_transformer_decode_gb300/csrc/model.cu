@@ -70,6 +70,7 @@ cudaError_t configure_all() {
         if (e == cudaSuccess) e = configure_q4k();
         if (e == cudaSuccess) e = configure_attn_prefill_tc();
         if (e == cudaSuccess) e = configure_sample();
+        if (e == cudaSuccess) e = configure_kv_q4();
         g_cfg_err = e;
     });
     return g_cfg_err;
@@ -1523,6 +1524,7 @@ int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride,
     a.B = B; a.rows = rows; a.max_len = max_len; a.nh = n_heads; a.scale = scale;
     a.out = out_dev; a.out_stride = out_stride; a.ws = static_cast<float *>(workspace_dev);
     a.status = status_dev;
+    QW3_CUDA_TRY(configure_all());   // the kernels' shared-memory limits
     QW3_CUDA_TRY(launch_kv_q4_attn(a, cache->head_dim, static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/qw3.h"
@@ -255,6 +256,28 @@ cudaError_t launch_copy_kv_rows(const void *kv_layer_seq, size_t kvsel_stride, s
                                 int pos0, int n, int nkv, int hd, float *k_out, float *v_out, int kvtype,
                                 cudaStream_t s);
 
+// Launch that may start while the kernel before it in the stream ends
+// (programmatic dependent launch); the kernel calls pdl_wait() before it
+// touches memory that others write or read. cluster > 1: clusters along x.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, int cluster, cudaStream_t s,
+                       A &&...args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 // ---- the 4-bit KV cache (kv_q4.cu holds its layout)
 struct KvQ4 {
     uint8_t *data = nullptr;
@@ -301,6 +324,7 @@ struct KvQ4AttnArgs {
 constexpr int kQ4MaxRows = 16, kQ4MaxGroup = 16;
 int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len);
 size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len);
+cudaError_t configure_kv_q4();
 cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, cudaStream_t s);
 
 // ---- sampling (sample.cu)

@@ -410,6 +410,7 @@ template <bool kHeld>
 __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
     extern __shared__ __align__(16) float held[];
     __shared__ Shared s;
+    pdl_wait();
     const int tid = threadIdx.x;
     const int size = static_cast<int>(gridDim.x);   // one cluster along x
     Row row;
@@ -629,19 +630,8 @@ cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s) {
         x.token += b0;
         if (x.next) x.next += b0;
         if (x.prob) x.prob += b0;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(size, std::min(65535, B - b0));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = is_held ? static_cast<size_t>(slice) * 4 + 16 : 0;
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(size);
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        const cudaError_t e = is_held ? cudaLaunchKernelEx(&cfg, k_sample<true>, x, slice)
-                                      : cudaLaunchKernelEx(&cfg, k_sample<false>, x, slice);
+        const cudaError_t e = launch_pdl(is_held ? k_sample<true> : k_sample<false>, dim3(size, std::min(65535, B - b0)),
+                                         kThreads, is_held ? static_cast<size_t>(slice) * 4 + 16 : 0, size, s, x, slice);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

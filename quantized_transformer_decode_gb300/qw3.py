@@ -424,11 +424,11 @@ def q4_k_gemv(W, rows: int, cols: int, x):
     return y
 
 
-def _on(index: int, dtype, **tensors):
+def _on(index: int, dtype, name: str, *tensors):
     """Check that each given tensor lies on CUDA device `index` as contiguous values of `dtype`."""
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
-            raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a contiguous {dtype} tensor on cuda:{index} is wanted")
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: contiguous {dtype} tensors on cuda:{index} are wanted")
 
 
 def _ptr(t):
@@ -442,23 +442,16 @@ def _rows_of(t, name: str):
     return t.shape[0], t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
 
 
-class _Here:
-    """Makes a CUDA device current for a call, at no cost where it is already."""
-
-    def __init__(self, index: int):
-        self.index, self.guard = index, None
-
-    def __enter__(self):
-        torch = _torch()
-        if torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _on_current_stream(index: int, call, *args) -> None:
+    """call(*args, stream) with device `index` current and torch's current stream on it."""
+    torch = _torch()
+    if torch.cuda.current_device() == index:
+        rc = call(*args, torch.cuda.current_stream(index).cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args, torch.cuda.current_stream(index).cuda_stream)
+    if rc:
+        _check(rc)
 
 
 class KVCacheQ4:
@@ -480,7 +473,7 @@ class KVCacheQ4:
         self.c = Qw3KvQ4(data.data_ptr(), slots, capacity, n_kv_heads, head_dim)
 
     def _check_places(self, M, slots, pos):
-        _on(self.index, _torch().int32, slots=slots, pos=pos)
+        _on(self.index, _torch().int32, "slots and pos", slots, pos)
         if (slots is not None and slots.numel() != M) or (pos is not None and pos.numel() != M):
             raise Qw3Error(QW3_ERR_SHAPE, f"slots and pos hold one place for each of {M} rows")
 
@@ -497,16 +490,16 @@ class KVCacheQ4:
         n_heads = width // hd - 2 * self.n_kv_heads
         if qkv.dtype is not torch.float32 or qkv.get_device() != self.index or width % hd or n_heads < 1:
             raise Qw3Error(QW3_ERR_SHAPE, "qkv: f32 rows of n_heads + 2 n_kv_heads heads on the cache's device")
-        _on(self.index, torch.float32, q_norm=q_norm, k_norm=k_norm, rope=rope)
+        _on(self.index, torch.float32, "q_norm, k_norm and rope", q_norm, k_norm, rope)
         if q_norm.numel() != hd or k_norm.numel() != hd or rope.numel() != self.capacity * hd:
             raise Qw3Error(QW3_ERR_SHAPE, "q_norm and k_norm hold head_dim values, rope capacity * head_dim")
-        _on(self.index, torch.int32, status=status)
+        if status is not None:
+            _on(self.index, torch.int32, "status", status)
         self._check_places(M, slots, pos)
         q = torch.empty((M, n_heads, hd), dtype=torch.float32, device=self.device)
-        with _Here(self.index) as stream:
-            _check(lib().qw3_kv_q4_append(self.c, qkv.data_ptr(), M, stride, n_heads, q_norm.data_ptr(),
-                                          k_norm.data_ptr(), eps, rope.data_ptr(), _ptr(slots), slot, _ptr(pos), first,
-                                          q.data_ptr(), n_heads * hd, _ptr(status), stream))
+        _on_current_stream(self.index, lib().qw3_kv_q4_append, self.c, qkv.data_ptr(), M, stride, n_heads,
+                           q_norm.data_ptr(), k_norm.data_ptr(), eps, rope.data_ptr(), _ptr(slots), slot, _ptr(pos),
+                           first, q.data_ptr(), n_heads * hd, _ptr(status))
         return q
 
     def read(self, slots=None, pos=None, slot: int = 0, first: int = 0, n: Optional[int] = None):
@@ -521,8 +514,8 @@ class KVCacheQ4:
         shape = (M, self.n_kv_heads, self.head_dim)
         k = torch.empty(shape, dtype=torch.float32, device=self.device)
         v = torch.empty(shape, dtype=torch.float32, device=self.device)
-        with _Here(self.index) as stream:
-            _check(lib().qw3_kv_q4_read(self.c, M, _ptr(slots), slot, _ptr(pos), first, k.data_ptr(), v.data_ptr(), stream))
+        _on_current_stream(self.index, lib().qw3_kv_q4_read, self.c, M, _ptr(slots), slot, _ptr(pos), first,
+                           k.data_ptr(), v.data_ptr())
         return k, v
 
     def attention(self, q, lens, rows: int = 1, slots=None, max_len: Optional[int] = None,
@@ -534,8 +527,8 @@ class KVCacheQ4:
         is not given. workspace: a uint8 tensor to use in place of a new one."""
         torch = _torch()
         B, hd, n_heads = lens.numel(), self.head_dim, q.shape[1] if q.dim() == 3 else 0
-        _on(self.index, torch.float32, q=q, out=out)
-        _on(self.index, torch.int32, lens=lens, slots=slots, status=status)
+        _on(self.index, torch.float32, "q and out", q, out)
+        _on(self.index, torch.int32, "lens, slots and status", lens, slots, status)
         if n_heads < 1 or q.shape[0] != B * rows or q.shape[2] != hd:
             raise Qw3Error(QW3_ERR_SHAPE, f"q: [{B * rows}, n_heads, {hd}] is wanted")
         if (slots is not None and slots.numel() != B) or (out is not None and out.shape != q.shape):
@@ -551,12 +544,11 @@ class KVCacheQ4:
             if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         else:
-            _on(self.index, torch.uint8, workspace=workspace)
+            _on(self.index, torch.uint8, "workspace", workspace)
             need = workspace.numel()
-        with _Here(self.index) as stream:
-            _check(L.qw3_kv_q4_attn(self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots), lens.data_ptr(), B, rows,
-                                    max_len, hd ** -0.5 if scale is None else scale, out.data_ptr(), n_heads * hd,
-                                    _ptr(workspace), need, _ptr(status), stream))
+        _on_current_stream(self.index, L.qw3_kv_q4_attn, self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots),
+                           lens.data_ptr(), B, rows, max_len, hd ** -0.5 if scale is None else scale, out.data_ptr(),
+                           n_heads * hd, _ptr(workspace), need, _ptr(status))
         return out
 
 
@@ -570,17 +562,16 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stat
     dev = logits.get_device()
     if logits.dtype is not torch.float32 or dev < 0:
         raise Qw3Error(QW3_ERR_INVALID_ARG, "logits: a CUDA f32 tensor is wanted")
-    _on(dev, torch.float32, u=u, temperature=temperature, top_p=top_p, min_p=min_p)
-    _on(dev, torch.int32, top_k=top_k, status=status)
+    _on(dev, torch.float32, "u, temperature, top_p and min_p", u, temperature, top_p, min_p)
+    _on(dev, torch.int32, "top_k and status", top_k, status)
     for t in (u, temperature, top_k, top_p, min_p):
         if t is not None and t.numel() != B:
             raise Qw3Error(QW3_ERR_SHAPE, f"one setting and one number for each of {B} rows are wanted")
     token = torch.empty(B, dtype=torch.int32, device=logits.device)
     prob = torch.empty(B, dtype=torch.float32, device=logits.device)
-    with _Here(dev) as stream:
-        _check(lib().qw3_sample(logits.data_ptr(), stride, B, logits.shape[1], _ptr(temperature), _ptr(top_k),
-                                _ptr(top_p), _ptr(min_p), u.data_ptr(), token.data_ptr(), prob.data_ptr(), _ptr(status),
-                                stream))
+    _on_current_stream(dev, lib().qw3_sample, logits.data_ptr(), stride, B, logits.shape[1], _ptr(temperature),
+                       _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(), token.data_ptr(), prob.data_ptr(),
+                       _ptr(status))
     return token, prob
 
 
@@ -719,8 +710,8 @@ class Qw3Model:
         torch = _torch()
         first_tokens = first_tokens.to(torch.int32).contiguous()
         B, dev = first_tokens.numel(), first_tokens.get_device()
-        _on(dev, torch.float32, u=u, temperature=temperature, top_p=top_p, min_p=min_p)
-        _on(dev, torch.int32, top_k=top_k)
+        _on(dev, torch.float32, "u, temperature, top_p and min_p", u, temperature, top_p, min_p)
+        _on(dev, torch.int32, "top_k", top_k)
         if u.numel() != n_steps * B or any(t is not None and t.numel() != B for t in (temperature, top_k, top_p, min_p)):
             raise Qw3Error(QW3_ERR_SHAPE, "u holds n_steps * B numbers, a setting B")
         logits = torch.empty((B, self.shape.vocab), dtype=torch.float32, device=first_tokens.device)
