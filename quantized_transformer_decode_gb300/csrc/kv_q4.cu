@@ -617,6 +617,11 @@ __device__ __forceinline__ int q4_blocks(const KvQ4AttnArgs &a, int b, int *len_
     return max(1, (len + kQ4Block - 1) / kQ4Block);
 }
 
+// a / b for a >= 0, in 32 bits where that is enough.
+__device__ __forceinline__ int64_t q4_div(int64_t a, unsigned b) {
+    return a >> 32 ? a / b : static_cast<int64_t>(static_cast<unsigned>(a) / b);
+}
+
 // Sum over the block's threads; red: kQ4Warps values.
 __device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
 #pragma unroll
@@ -675,16 +680,18 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         for (int i = tid; i < a.B; i += NW * 32) mine += q4_blocks(a, i) + kQ4UnitCost;
         const int64_t all = a.B > 1 ? q4_sum(mine, s_red) : q4_blocks(a, 0) + kQ4UnitCost;
         // no share is empty: the join counts on every CTA between a unit's first and last
-        const int64_t total = all * U, P = min(static_cast<int64_t>(gridDim.x), total);
+        const int64_t total = all * U;
+        const unsigned P = static_cast<unsigned>(min(static_cast<int64_t>(gridDim.x), total));
         if (blockIdx.x >= P) return;
-        at = total * blockIdx.x / P;
-        stop = total * (blockIdx.x + 1) / P;
+        const int64_t each = q4_div(total, P), more = total - each * P;
+        at = each * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), more);
+        stop = at + each + (blockIdx.x < more ? 1 : 0);
     }
     // its first sequence: sums of 128 sequences at a time, then one by one
     int b = CLUSTER ? static_cast<int>(blockIdx.y) / U : 0;
     int64_t before = 0;   // cost of the sequences below b (of one unit)
     if (!CLUSTER && a.B > 1) {
-        const int64_t want = at / U;
+        const int64_t want = q4_div(at, static_cast<unsigned>(U));
         for (int b0 = 0; b0 < a.B; b0 += NW * 32) {
             const int64_t n = b0 + tid < a.B ? q4_blocks(a, b0 + tid) + kQ4UnitCost : 0;
             int64_t run = n;
@@ -728,7 +735,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         // a unit's cost: kQ4UnitCost, then its blocks
         const int64_t in_b = at - before * U;
         cost = blocks + kQ4UnitCost;
-        unit = static_cast<int>(in_b / cost);
+        unit = static_cast<int>(q4_div(in_b, static_cast<unsigned>(cost)));
         const int off0 = static_cast<int>(in_b - static_cast<int64_t>(unit) * cost);
         const int off1 = static_cast<int>(min(static_cast<int64_t>(cost), off0 + (stop - at)));
         blk0 = max(0, off0 - kQ4UnitCost);
@@ -852,14 +859,14 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
     // hi lanes keep x (cut to f16 below), lo lanes what the cut leaves
     const uint32_t cut = (W <= 4 && c < 2) ? 0u : 0xFFFFE000u;
 
-    for (; k0 < end; k0 += kStep) {
+    // one tile; tail: a column's range ends in it, and what lies past that may be anything
+    const auto tile = [&](auto tail) {
         const uint8_t *st = ring + taken % kQ4Stages * St::bytes;
         if (!lost && !mbar_wait_bounded(&s_bar[warp][taken % kQ4Stages], (taken / kQ4Stages) & 1u)) {
             lost = true;   // no further copy is started
             lost_at = taken;
             record_status(a.status, QW3_ERR_TIMEOUT);
         }
-        lost = __any_sync(0xffffffffu, lost);
         // ---- scores
         float s[MT][4];
 #pragma unroll
@@ -898,8 +905,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) ld_words(vd[m][h], st + St::VS + (16 * m + 8 * h + pr) * (HD / 16));
-        if (k0 + kQ4Tile > low_lim) {
-            // the tile that a column's range ends in: what lies past it may be anything
+        if constexpr (decltype(tail)::value) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -1016,6 +1022,10 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         ++taken;
         __syncwarp();   // the tile is in registers: its place may be filled again
         if (lane == 0 && !lost && k0 + kQ4Stages * kStep < end) fetch(taken + kQ4Stages - 1);
+    };
+    for (; k0 < end; k0 += kStep) {
+        if (k0 + kQ4Tile <= low_lim) tile(std::false_type{});
+        else tile(std::true_type{});
     }
 
     // ---- the warps' results meet in shared memory

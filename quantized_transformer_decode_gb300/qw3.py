@@ -336,9 +336,15 @@ def qw3_sample(logits_ptr: int, stride: int, B: int, V: int, temperature_ptr: in
 
 # ---------------------------------------------------------- torch wrapper
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr() -> int:
@@ -444,12 +450,13 @@ def _rows_of(t, name: str):
 
 def _on_current_stream(index: int, call, *args) -> None:
     """call(*args, stream) with device `index` current and torch's current stream on it."""
-    torch = _torch()
-    if torch.cuda.current_device() == index:
-        rc = call(*args, torch.cuda.current_stream(index).cuda_stream)
+    cuda = _torch().cuda
+    stream = cuda.current_stream(index).cuda_stream
+    if cuda.current_device() == index:
+        rc = call(*args, stream)
     else:
-        with torch.cuda.device(index):
-            rc = call(*args, torch.cuda.current_stream(index).cuda_stream)
+        with cuda.device(index):
+            rc = call(*args, stream)
     if rc:
         _check(rc)
 
