@@ -536,14 +536,27 @@ __device__ __forceinline__ uint32_t pack_rz(float a, float b) {
 
 // Codes less 8 of a word's nibbles as half2: h[p] = (nibble p, nibble p + 4).
 // 0x6400 | n is 1024 + n in f16, 0x6400 | n << 4 is 1024 + 16 n.
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&h)[4]) {
+// `magic` is 0x64006400 in a register (q4_magic), so that mask and or are one
+// three-operand instruction.
+__device__ __forceinline__ uint32_t q4_magic() {
+    uint32_t r;
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(r));
+    return r;
+}
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "n"(MASK), "r"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t magic, uint32_t (&h)[4]) {
     const __half2 c1032 = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));
     const __half2 c16 = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));     // 1 / 16
     const __half2 c72 = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));     // -72
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t x = i ? w >> 8 : w;
-        const uint32_t lo = (x & 0x000F000Fu) | 0x64006400u, hi = (x & 0x00F000F0u) | 0x64006400u;
+        const uint32_t lo = and_or<0x000F000Fu>(x, magic), hi = and_or<0x00F000F0u>(x, magic);
         const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&lo), c1032);
         const __half2 g = __hfma2(*reinterpret_cast<const __half2 *>(&hi), c16, c72);
         h[2 * i] = *reinterpret_cast<const uint32_t *>(&l);
@@ -667,6 +680,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         for (int i = 0; i < kQ4Stages; ++i) mbar_init(&s_bar[warp][i], 1);
         fence_mbar_init();
     }
+    const uint32_t magic = q4_magic();
     uint32_t taken = 0;     // tiles this warp has taken from its ring
     bool lost = false;      // a copy did not arrive in time, the lost_at-th tile's
     uint32_t lost_at = 0;
@@ -881,8 +895,8 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 uint32_t x0[4], x1[4];
-                unpack8(kw[0][i], x0);
-                unpack8(kw[1][i], x1);
+                unpack8(kw[0][i], magic, x0);
+                unpack8(kw[1][i], magic, x1);
                 const float d0 = half_of(kd[0][i >> 1], i & 1), d1 = half_of(kd[1][i >> 1], i & 1);
                 const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
 #pragma unroll
@@ -998,8 +1012,8 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
             for (int m = 0; m < MT; ++m) {
                 uint32_t x0[4], x1[4];
                 const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
-                unpack8(__byte_perm(vw[m][0][i >> 1], vw[m][1][i >> 1], sel), x0);
-                unpack8(__byte_perm(vw[m][2][i >> 1], vw[m][3][i >> 1], sel), x1);
+                unpack8(__byte_perm(vw[m][0][i >> 1], vw[m][1][i >> 1], sel), magic, x0);
+                unpack8(__byte_perm(vw[m][2][i >> 1], vw[m][3][i >> 1], sel), magic, x1);
                 const uint32_t a0[4] = {x0[0], x0[1], x1[0], x1[1]}, a1[4] = {x0[2], x0[3], x1[2], x1[3]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
