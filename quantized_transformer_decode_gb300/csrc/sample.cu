@@ -70,8 +70,9 @@ __device__ __forceinline__ void sync_cluster() {
 }
 
 struct Shared {
-    // this CTA's histogram: counts, and weights as 32-bit halves with carries
-    uint32_t cnt[kBins], wlo[kBins], whi[kBins];
+    // this CTA's histogram: counts, and weights as sums of their 14-bit digits (up
+    // to 2^18 tokens to a slice: no sum passes 32 bits)
+    uint32_t cnt[kBins], digit[3][kBins];
     // the row's
     uint32_t tcnt[kBins];
     u64 tw[kBins];
@@ -160,8 +161,12 @@ __device__ __forceinline__ void share(const Row &row, u64 *slot, u64 v) {
 // token left out; weights only where `weigh`.
 template <typename F>
 __device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s, F bin_of) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.cnt[i] = s.wlo[i] = s.whi[i] = 0u;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        s.cnt[i] = 0u;
+        if (weigh) s.digit[0][i] = s.digit[1][i] = s.digit[2][i] = 0u;
+    }
     __syncthreads();
+#pragma unroll 4
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
         const float v = row.l[i];
         const int bin = bin_of(v);
@@ -169,16 +174,18 @@ __device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s,
         atomicAdd(&s.cnt[bin], 1u);
         if (weigh) {
             const u64 w = fixed_weight(row.weight(v));
-            const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&s.wlo[bin], wl);
-            const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u);
-            if (wh) atomicAdd(&s.whi[bin], wh);
+            const uint32_t d0 = static_cast<uint32_t>(w) & 0x3fffu, d1 = static_cast<uint32_t>(w >> 14) & 0x3fffu;
+            const uint32_t d2 = static_cast<uint32_t>(w >> 28);
+            if (d0) atomicAdd(&s.digit[0][bin], d0);
+            if (d1) atomicAdd(&s.digit[1][bin], d1);
+            if (d2) atomicAdd(&s.digit[2][bin], d2);
         }
     }
     if (row.size == 1) {
         __syncthreads();
         for (int i = threadIdx.x; i < kBins; i += kThreads) {
             s.tcnt[i] = s.cnt[i];
-            s.tw[i] = static_cast<u64>(s.whi[i]) << 32 | s.wlo[i];
+            s.tw[i] = weigh ? (static_cast<u64>(s.digit[2][i]) << 28) + (static_cast<u64>(s.digit[1][i]) << 14) + s.digit[0][i] : 0;
         }
         __syncthreads();
         return;
@@ -194,8 +201,9 @@ __device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s,
         for (uint32_t p = 0; p < row.size; ++p) {
             c += remote_ld32(dsmem_map(&s.cnt[bin], p));
             if (weigh) {
-                w += static_cast<u64>(remote_ld32(dsmem_map(&s.whi[bin], p))) << 32;
-                w += remote_ld32(dsmem_map(&s.wlo[bin], p));
+                w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[2][bin], p))) << 28;
+                w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[1][bin], p))) << 14;
+                w += remote_ld32(dsmem_map(&s.digit[0][bin], p));
             }
         }
         for (uint32_t p = 0; p < row.size; ++p) {
@@ -557,15 +565,24 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
             for (uint32_t q = 0; q < row.rank; ++q) n0 += s.peer[q];
         }
     }
-    auto weight = [&](int i, u64 &seen) -> u64 {
-        const float v = row.l[i];
+    // kept weight of token i; nth: its number among the equals of the cut key
+    const auto weight = [&](float v, u64 nth) -> u64 {
         const uint32_t key = logit_key(v);
-        if (key < cut.key || (key == cut.key && cut.some && seen++ >= cut.ties)) return 0ull;
         const float e = row.weight(v);
-        return e >= mp ? fixed_weight(e) : 0ull;
+        return key > cut.key || (key == cut.key && nth < cut.ties) ? (e >= mp ? fixed_weight(e) : 0ull) : 0ull;
     };
-    u64 w = 0, seen = n0, none = 0, t0, t1;
-    for (int i = i0; i < i1; ++i) w += weight(i, seen);
+    u64 w = 0, none = 0, t0, t1;
+    if (cut.some) {
+        u64 seen = n0;
+        for (int i = i0; i < i1; ++i) {
+            const float v = row.l[i];
+            w += weight(v, seen);
+            seen += logit_key(v) == cut.key;
+        }
+    } else {
+#pragma unroll 4
+        for (int i = i0; i < i1; ++i) w += weight(row.l[i], 0);
+    }
     const u64 mine = w;
     scan2(w, none, t0, t1, s);
     u64 total = t0, before = 0;
@@ -582,15 +599,30 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
     u64 at = static_cast<u64>(static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(total));
     if (at >= total) at = total - 1;
     w += before;
-    if (w <= at && at < w + mine) {
-        seen = n0;
-        for (int i = i0; i < i1; ++i) {
-            w += weight(i, seen);
-            if (w > at) {
-                answer(a, b, row.base + i, row.l[i], row, total);
-                break;
-            }
+    // the warp whose lane holds the place looks through that lane's run, 32 tokens at a time
+    const unsigned holder = __ballot_sync(0xffffffffu, w <= at && at < w + mine);
+    if (!holder) return;
+    const int from = __ffs(static_cast<int>(holder)) - 1, lane = tid & 31;
+    const int first = __shfl_sync(0xffffffffu, i0, from), last = __shfl_sync(0xffffffffu, i1, from);
+    u64 sum = __shfl_sync(0xffffffffu, w, from), nth = __shfl_sync(0xffffffffu, n0, from);
+    for (int i = first; i < last; i += 32) {
+        const bool in = i + lane < last;
+        const float v = in ? row.l[i + lane] : -INFINITY;
+        const unsigned equals = __ballot_sync(0xffffffffu, in && logit_key(v) == cut.key);
+        const u64 x = in ? weight(v, cut.some ? nth + __popc(equals & ((1u << lane) - 1u)) : 0) : 0;
+        u64 run = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += y;
         }
+        const unsigned past = __ballot_sync(0xffffffffu, sum + run > at);
+        if (past) {
+            if (lane == __ffs(static_cast<int>(past)) - 1) answer(a, b, row.base + i + lane, v, row, total);
+            return;
+        }
+        sum += __shfl_sync(0xffffffffu, run, 31);
+        nth += __popc(equals);
     }
 }
 
