@@ -11,13 +11,20 @@
 //
 // One thread-block cluster takes a row: its CTAs hold a slice each in shared
 // memory, so the logits are read from memory once, and histograms and totals
-// meet through distributed shared memory. A cut is found by a histogram over
-// equal steps of (max l - l) / T (1024 of them down to weights of 2^-41),
-// whose bins a vocabulary's logits fill evenly, so that few of a warp's
-// additions meet in one word. Where the top-k bin and all above it hold at most
-// kList tokens, the first CTA takes these and finishes the row by itself; else
-// the cut's bin alone is ranked, or cut further by histograms over its keys
-// until it holds at most kList tokens or equal logits only.
+// meet through distributed shared memory.
+//
+// Mostly a short list settles a row: a histogram of the threads' largest logits
+// (one addition to a thread) gives a bound that the k-th largest token cannot
+// lie below; the few tokens above it go to the first CTA, which ranks them and
+// finishes the row by itself. With top-p alone the list is taken for k = 192 and
+// serves if it holds p of the row's weight. Else a cut is found by a histogram
+// of all tokens over equal steps of (max l - l) / T (1024 of them, down to
+// weights of 2^-41), whose bins a vocabulary's logits fill evenly, so that few
+// of a warp's additions meet in one word; the cut's bin alone is ranked, or cut
+// further by histograms over its keys until it holds at most kList tokens or
+// equal logits only. What bounds it: the passes over the slices in shared
+// memory (some 20 instructions a token where weights are summed) and, for one
+// row, the barriers between them.
 //
 // Sums are taken in 64-bit fixed point (2^40 for the largest weight): they are
 // the same whatever the order of the additions, so one input gives one token.
@@ -33,7 +40,8 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2 * kThreads;   // two to a thread
-constexpr int kList = 256;
+constexpr int kList = 256;      // tokens that the first CTA ranks
+constexpr int kListP = 192;     // of them, asked for with top-p alone
 constexpr int kMaxCluster = 16;
 constexpr float kOne = 1099511627776.0f;   // 2^40
 
@@ -79,7 +87,7 @@ struct Shared {
     // tokens of a small bin, in the first CTA: key and ~index, weight
     u64 list[kList], list_w[kList];
     u64 peer[kMaxCluster];    // a word from each CTA
-    u64 peer2[kMaxCluster];
+    u64 peer2[kMaxCluster], peer3[kMaxCluster];
     u64 red[2 * kWarps + 2];
     uint32_t n_list;
     uint64_t bar;      // the slice has arrived
@@ -141,9 +149,13 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, Shared &s) {
 struct Row {
     const float *l;   // this CTA's slice, in shared or global memory
     int n, base;      // its length, and its first token
-    float top, inv_t, step;   // step: bins per unit of logit
+    float top, inv_t2, step;  // log2(e) / T; bins per unit of logit
     uint32_t rank, size;      // in the cluster
-    __device__ __forceinline__ float weight(float v) const { return exp2f((v - top) * inv_t * 1.4426950408889634f); }
+    __device__ __forceinline__ float weight(float v) const {
+        float r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((v - top) * inv_t2));
+        return r;
+    }
     // Bin of a logit, kBins or more for one that has no weight: the float
     // operations are monotone, so the bins follow the order of the logits.
     __device__ __forceinline__ int bin(float v) const {
@@ -157,15 +169,60 @@ __device__ __forceinline__ void share(const Row &row, u64 *slot, u64 v) {
     sync_cluster();
 }
 
-// Histogram of the row: bin_of(logit) gives a bin or a negative number for a
-// token left out; weights only where `weigh`.
-template <typename F>
-__device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s, F bin_of) {
+__device__ __forceinline__ void clear_histogram(bool weigh, Shared &s) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
         s.cnt[i] = 0u;
         if (weigh) s.digit[0][i] = s.digit[1][i] = s.digit[2][i] = 0u;
     }
     __syncthreads();
+}
+
+// The cluster's histograms added up, in every CTA's tcnt and tw.
+__device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Shared &s) {
+    if (row.size == 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+            s.tcnt[i] = s.cnt[i];
+            s.tw[i] = weigh ? (static_cast<u64>(s.digit[2][i]) << 28) + (static_cast<u64>(s.digit[1][i]) << 14) + s.digit[0][i] : 0;
+        }
+        __syncthreads();
+        return;
+    }
+    sync_cluster();
+    // each CTA adds its share of the bins over the cluster and hands it to all:
+    // size / 2 neighbouring threads to a bin, two CTAs to each
+    const int parts = static_cast<int>(row.size) / 2, part = static_cast<int>(threadIdx.x) % parts;
+    const int bin = static_cast<int>(row.rank) * (kBins / static_cast<int>(row.size)) + static_cast<int>(threadIdx.x) / parts;
+    uint32_t c = 0;
+    u64 w = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t p = 2 * part + h;
+        c += remote_ld32(dsmem_map(&s.cnt[bin], p));
+        if (weigh) {
+            w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[2][bin], p))) << 28;
+            w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[1][bin], p))) << 14;
+            w += remote_ld32(dsmem_map(&s.digit[0][bin], p));
+        }
+    }
+    for (int o = 1; o < parts; o <<= 1) {
+        c += __shfl_xor_sync(0xffffffffu, c, o);
+        if (weigh) w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t p = 2 * part + h;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_map(&s.tcnt[bin], p)), "r"(c) : "memory");
+        remote_st(dsmem_map(&s.tw[bin], p), w);
+    }
+    sync_cluster();
+}
+
+// Histogram of the row: bin_of(logit) gives a bin or a negative number for a
+// token left out; weights only where `weigh`.
+template <typename F>
+__device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s, F bin_of) {
+    clear_histogram(weigh, s);
 #pragma unroll 4
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
         const float v = row.l[i];
@@ -181,37 +238,7 @@ __device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s,
             if (d2) atomicAdd(&s.digit[2][bin], d2);
         }
     }
-    if (row.size == 1) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBins; i += kThreads) {
-            s.tcnt[i] = s.cnt[i];
-            s.tw[i] = weigh ? (static_cast<u64>(s.digit[2][i]) << 28) + (static_cast<u64>(s.digit[1][i]) << 14) + s.digit[0][i] : 0;
-        }
-        __syncthreads();
-        return;
-    }
-    sync_cluster();
-    // each CTA adds its share of the bins over the cluster and hands it to all
-    const int share_n = kBins / static_cast<int>(row.size);
-    for (int i = threadIdx.x; i < share_n; i += kThreads) {
-        const int bin = static_cast<int>(row.rank) * share_n + i;
-        uint32_t c = 0;
-        u64 w = 0;
-#pragma unroll 4
-        for (uint32_t p = 0; p < row.size; ++p) {
-            c += remote_ld32(dsmem_map(&s.cnt[bin], p));
-            if (weigh) {
-                w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[2][bin], p))) << 28;
-                w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[1][bin], p))) << 14;
-                w += remote_ld32(dsmem_map(&s.digit[0][bin], p));
-            }
-        }
-        for (uint32_t p = 0; p < row.size; ++p) {
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_map(&s.tcnt[bin], p)), "r"(c) : "memory");
-            remote_st(dsmem_map(&s.tw[bin], p), w);
-        }
-    }
-    sync_cluster();
+    add_histograms(row, weigh, s);
 }
 
 // The bin in which the running sum (of counts, or of weights) of the row's
@@ -370,9 +397,11 @@ __device__ __forceinline__ void answer(const SampleArgs &a, int b, int token, fl
     }
 }
 
-// The row from its list alone (the first CTA): the top-k tokens are all in it.
-__device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, float p, float mp, Shared &s) {
-    const int n = static_cast<int>(min(s.n_list, static_cast<uint32_t>(kList))), i = threadIdx.x;
+// The row from its list alone (the first CTA): the top-k tokens are all in it,
+// or (k = 0) the tokens of weight p of the row's total `all`. Two threads to a
+// token, each looking at every other one.
+__device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, float p, float mp, u64 all, Shared &s) {
+    const int n = static_cast<int>(min(s.n_list, static_cast<uint32_t>(kList))), i = threadIdx.x >> 1, half = threadIdx.x & 1;
     u64 mine = 0, w = 0;
     float v = 0.0f, e = 0.0f;
     if (i < n) {
@@ -386,32 +415,95 @@ __device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, f
     u64 before = 0;
     uint32_t rank = 0;
     if (i < n)
-        for (int j = 0; j < n; ++j)
+        for (int j = half; j < n; j += 2)
             if (s.list[j] > mine) {
                 ++rank;
                 before += s.list_w[j];
             }
-    bool kept = i < n && rank < k;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    before += __shfl_xor_sync(0xffffffffu, before, 1);
+    bool kept = i < n && (k == 0 || rank < k);
     if (p < 1.0f) {
-        u64 x = kept ? w : 0, y = 0, total, none;
-        scan2(x, y, total, none, s);
-        const u64 target = static_cast<u64>(ceil(static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(total)));
+        if (k > 0) {
+            u64 x = kept && !half ? w : 0, y = 0, none;
+            scan2(x, y, all, none, s);
+        }
+        const u64 target = static_cast<u64>(ceil(static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(all)));
         kept = kept && (rank == 0 || before < target);
     }
     kept = kept && e >= mp;
     __syncthreads();
     if (i < n) s.list_w[i] = kept ? w : 0;
-    u64 x = kept ? w : 0, y = 0, total, none;
+    u64 x = kept && !half ? w : 0, y = 0, total, none;
     scan2(x, y, total, none, s);   // its barriers also show everyone the kept weights
-    if (!kept) return;
     const uint32_t idx = static_cast<uint32_t>(mine);   // ~index: the larger, the earlier
     u64 first = 0;
-    for (int j = 0; j < n; ++j)
-        if (static_cast<uint32_t>(s.list[j]) > idx) first += s.list_w[j];
+    if (kept)
+        for (int j = half; j < n; j += 2)
+            if (static_cast<uint32_t>(s.list[j]) > idx) first += s.list_w[j];
+    first += __shfl_xor_sync(0xffffffffu, first, 1);
     const float u = a.u[b];
     u64 at = static_cast<u64>(static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(total));
     if (at >= total) at = total - 1;
-    if (first <= at && at < first + w) answer(a, b, static_cast<int>(0xffffffffu - idx), v, row, total);
+    if (kept && !half && first <= at && at < first + w) answer(a, b, static_cast<int>(0xffffffffu - idx), v, row, total);
+}
+
+// Lists the row's largest tokens in the first CTA, the `want` largest among
+// them, where that takes at most kList: a bin that `want` of the threads' largest
+// logits (thread_top) reach holds, with those above it, at least so many tokens.
+// With `weigh`, *all is the row's weight and *listed the list's. Every CTA
+// returns the same.
+__device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 want, bool weigh, u64 *all, u64 *listed,
+                                         Shared &s) {
+    clear_histogram(false, s);
+    const int mine = row.bin(thread_top);
+    if (mine < kBins) atomicAdd(&s.cnt[mine], 1u);
+    add_histograms(row, false, s);
+    const Found f = find(false, want, 0, 0, s);
+    if (!f.some) return false;
+    const uint32_t n_at = dsmem_map(&s.n_list, 0u), list_at = dsmem_map(s.list, 0u);
+    u64 count = 0, sum = 0, in_list = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < row.n; i += kThreads) {
+        const float v = row.l[i];
+        const bool in = row.bin(v) <= f.bin;
+        if (weigh) {
+            const u64 w = fixed_weight(row.weight(v));
+            sum += w;
+            in_list += in ? w : 0;
+        }
+        if (in) {
+            const uint32_t at = remote_add(n_at, 1u);
+            if (at < kList)
+                remote_st(list_at + 8u * at,
+                          static_cast<u64>(logit_key(v)) << 32 | (0xffffffffu - static_cast<uint32_t>(row.base + i)));
+            ++count;
+        }
+    }
+    u64 c = count, x = 0, ct, xt, st = 0, lt = 0;
+    scan2(c, x, ct, xt, s);
+    if (weigh) scan2(sum, in_list, st, lt, s);
+    if (row.size > 1) {
+        if (threadIdx.x < row.size) {
+            if (weigh) {
+                remote_st(dsmem_map(&s.peer2[row.rank], threadIdx.x), st);
+                remote_st(dsmem_map(&s.peer3[row.rank], threadIdx.x), lt);
+            }
+        }
+        share(row, s.peer, ct);   // the list has arrived too
+        ct = st = lt = 0;
+        for (uint32_t p = 0; p < row.size; ++p) {
+            ct += s.peer[p];
+            st += weigh ? s.peer2[p] : 0;
+            lt += weigh ? s.peer3[p] : 0;
+        }
+    }
+    *all = st;
+    *listed = lt;
+    const bool fits = ct <= kList;
+    __syncthreads();
+    if (!fits && threadIdx.x == 0) s.n_list = 0u;   // a later gather starts over
+    return fits;
 }
 
 template <bool kHeld>
@@ -500,26 +592,29 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
         }
         return;
     }
-    row.inv_t = 1.0f / fmaxf(T, 1e-30f);
-    row.step = row.inv_t * (kBins / kNats);
+    row.inv_t2 = 1.4426950408889634f / fmaxf(T, 1e-30f);
+    row.step = kBins / kNats / fmaxf(T, 1e-30f);
     const int k = a.top_k ? a.top_k[b] : 0;
     const float p = a.top_p ? a.top_p[b] : 1.0f, mp = a.min_p ? fminf(a.min_p[b], 1.0f) : 0.0f;
     // kept: every token with a weight, until a cut says otherwise
     Cut cut{0u, ~0ull, 0, false};
-    if (k > 0 && k < a.V) {
+    const bool has_k = k > 0 && k < a.V;
+    if (has_k ? k <= kList : p < 1.0f) {
+        u64 all, listed;
+        const bool fits = try_list(row, top, has_k ? static_cast<u64>(k) : kListP, !has_k, &all, &listed, s);
+        if (fits && (has_k || static_cast<double>(listed) >= static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(all))) {
+            if (row.rank == 0) finish_list(a, b, row, has_k ? static_cast<u64>(k) : 0ull, p, mp, all, s);
+            return;
+        }
+        if (fits && row.rank == 0 && tid == 0) s.n_list = 0u;   // not enough of the weight
+    }
+    if (has_k) {
         histogram(row, false, s, [&](float v) {
             const int i = row.bin(v);
             return i < kBins ? i : -1;
         });
         const Found f = find(false, static_cast<u64>(k), 0, 0, s);
-        if (f.some) {
-            if (f.above_c + f.n <= kList) {
-                gather(row, s, [&](float v) { return row.bin(v) <= f.bin; });
-                if (row.rank == 0) finish_list(a, b, row, static_cast<u64>(k), p, mp, s);
-                return;
-            }
-            cut = cut_in_bin(row, f, false, static_cast<u64>(k), 0u, s);
-        }
+        if (f.some) cut = cut_in_bin(row, f, false, static_cast<u64>(k), 0u, s);
     }
     if (p < 1.0f) {
         // weights of what top-k left; of the equals of its last logit all are
@@ -565,11 +660,11 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
             for (uint32_t q = 0; q < row.rank; ++q) n0 += s.peer[q];
         }
     }
-    // kept weight of token i; nth: its number among the equals of the cut key
+    // kept weight of a token; nth: its number among the equals of the cut's logit
+    const float edge = cut.key ? float_from_order_key(cut.key) : -INFINITY;
     const auto weight = [&](float v, u64 nth) -> u64 {
-        const uint32_t key = logit_key(v);
         const float e = row.weight(v);
-        return key > cut.key || (key == cut.key && nth < cut.ties) ? (e >= mp ? fixed_weight(e) : 0ull) : 0ull;
+        return (v > edge || (v == edge && nth < cut.ties)) && e >= mp ? fixed_weight(e) : 0ull;
     };
     u64 w = 0, none = 0, t0, t1;
     if (cut.some) {
@@ -581,7 +676,10 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
         }
     } else {
 #pragma unroll 4
-        for (int i = i0; i < i1; ++i) w += weight(row.l[i], 0);
+        for (int i = i0; i < i1; ++i) {
+            const float v = row.l[i], e = row.weight(v);
+            w += v >= edge && e >= mp ? fixed_weight(e) : 0ull;
+        }
     }
     const u64 mine = w;
     scan2(w, none, t0, t1, s);
