@@ -615,9 +615,9 @@ template <int HD>
 __host__ __device__ constexpr int q4_part() { return HD + 2; }
 
 // What a unit costs besides its blocks (its queries, the joining of its warps),
-// in blocks: 1 measured against 0, 2 and 3 at 64 sequences of 1 to 4101
-// positions.
-constexpr int kQ4UnitCost = 1;
+// in blocks (64 sequences of 1 to 4101 positions, 16/8 heads: 47 us at 2, 51 at
+// 1, 62 at 0).
+constexpr int kQ4UnitCost = 2;
 
 // Blocks of sequence b (one at least: a sequence without positions still has
 // outputs to write) and, if asked, its length and slot.
@@ -653,7 +653,7 @@ __device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
 // and the last CTA of each unit.
 // CLUSTER: no workspace; grid (csize, units), clusters along x.
 template <int HD, int W, bool CLUSTER>
-__global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, CLUSTER ? (W <= 4 ? 2 : 1) : (W <= 4 ? 4 : 3))
+__global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, CLUSTER ? (W <= 4 ? 2 : 1) : (W <= 4 ? 3 : 2))
     k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
     constexpr int NW = CLUSTER ? kQ4ClusterWarps : kQ4Warps, kStep = NW * kQ4Tile;
     constexpr int NB = HD / 32, NT = q4_ops(W);
@@ -1244,7 +1244,7 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
     while (csize < kQ4MaxCluster && csize < need && units * csize * 2 <= fit_cluster) csize *= 2;
     p.csize = units * csize <= fit_cluster && need <= 8ll * csize ? csize : 0;
     // the CTAs that fit at once; for little work two blocks to each
-    const int fit = 152 * (p.W <= 4 ? 4 : 3);
+    const int fit = 152 * (p.W <= 4 ? 3 : 2);
     p.ctas = static_cast<int>(std::min<int64_t>(fit, std::max(units, units * ((most + 1) / 2))));
     p.whole = p.csize > 0 || most == 1;
     return p;
