@@ -479,9 +479,9 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 // all units in one row are dealt to the CTAs in equal contiguous shares (the
 // lengths are on the device: each CTA sums them), so that sequences of any
 // lengths keep every SM busy to the end; a unit that a share's end cuts leaves
-// partial results, which a second small kernel joins. A warp takes tiles of 32 positions and multiplies with mma.m16n8k16
-// (f16 in, f32 out), positions along m for S = K Q^T, dimensions along m for O
-// = V^T P^T:
+// partial results, which a second small kernel joins. A warp takes tiles of 32
+// positions and multiplies with mma.m16n8k16 (f16 in, f32 out), positions along
+// m for S = K Q^T, dimensions along m for O = V^T P^T:
 //  - codes are exact in f16 (-8..7): a word of 8 codes becomes 4 half2
 //    operands with 9 instructions and no scale. K scales multiply the f32 sums
 //    of a 32-value block, V scales the probabilities of their position.
@@ -499,6 +499,10 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 // tcgen05: with at most 8 columns the product is bound by what the codes cost
 // (bytes, then the unpacking), and registers to registers saves writing the
 // unpacked codes to shared memory and reading them back.
+// What bounds it: instructions. A warp's tile of 4.6 KB takes some 900 of them
+// (unpacking, the split of P, the softmax), half on the pipe that issues every
+// second cycle; 64 sequences of 2048 positions (32/8 heads, 151 MB) take 47 us,
+// 3.2 TB/s, 0.48 of the measured copy rate.
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
@@ -622,7 +626,7 @@ constexpr int kQ4UnitCost = 2;
 // Blocks of sequence b (one at least: a sequence without positions still has
 // outputs to write) and, if asked, its length and slot.
 __device__ __forceinline__ int q4_blocks(const KvQ4AttnArgs &a, int b, int *len_out = nullptr, int *slot_out = nullptr) {
-    const int slot = a.slots ? __ldg(a.slots + b) : a.slot0 + b;
+    const int slot = a.slots ? a.slots[b] : a.slot0 + b;
     const bool there = slot >= 0 && slot < a.c.slots;
     const int len = there ? q4_len(a, b) : 0;
     if (len_out) *len_out = len;
@@ -691,6 +695,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
     int64_t at = 0, stop = 1;
     if constexpr (!CLUSTER) {
         int64_t mine = 0;
+#pragma unroll 4
         for (int i = tid; i < a.B; i += NW * 32) mine += q4_blocks(a, i) + kQ4UnitCost;
         const int64_t all = a.B > 1 ? q4_sum(mine, s_red) : q4_blocks(a, 0) + kQ4UnitCost;
         // no share is empty: the join counts on every CTA between a unit's first and last
@@ -1051,7 +1056,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
         const int j = 2 * c + e;
         if (r == 0 && j < W) {
-            res[j * PS + HD] = ref[e];
+            res[j * PS + HD] = t != t ? 0.0f : ref[e];   // a NaN is not taken for an empty range
             res[j * PS + HD + 1] = t;
         }
     }
@@ -1098,7 +1103,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         } else if (begins && ends) {
             const int cc = col0 + j;
             a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
-                l > 0.0f ? o / l : 0.0f;
+                l == 0.0f ? 0.0f : o / l;
         } else {
             ws[j * PS + d] = o;
             if (d == 0) {
@@ -1126,7 +1131,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
                 }
             const int cc = col0 + j;
             a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
-                l > 0.0f ? o / l : 0.0f;
+                l == 0.0f ? 0.0f : o / l;
         }
         __syncwarp();
         hw_cluster_sync();   // nobody leaves while its result is read
@@ -1172,7 +1177,7 @@ __global__ void __launch_bounds__(HD) k_kv_q4_join(KvQ4AttnArgs a, int cgroups, 
             o = fmaf(p[d], f, o);
         }
     a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
-        l > 0.0f ? o / l : 0.0f;
+        l == 0.0f ? 0.0f : o / l;
 }
 
 }  // namespace
@@ -1183,19 +1188,20 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, const float *q_norm, const float *k_norm,
                                 float eps, const float2 *rope, const KvQ4 &c, int hd, const KvQ4Rows &rows, int nh,
-                                float *q_out, int64_t q_stride, int32_t *status, cudaStream_t s) {
+                                float *q_out, int64_t q_stride, int32_t *status, bool pdl, cudaStream_t s) {
     if (M <= 0) return cudaSuccess;
     const Q4AppendArgs a{qkv, M, qkv_stride, q_norm, k_norm, eps, rope, c, rows, nh, q_out, q_stride, status};
     const int tasks = nh + 2 * c.nkv;
     const bool vec = aligned16(qkv) && aligned16(q_norm) && aligned16(k_norm) && aligned16(rope) && aligned16(q_out) &&
                      qkv_stride % 4 == 0 && q_stride % 4 == 0;
     // four heads to a warp once one to a warp would fill the GPU's 64 warps per
-    // SM: 4096 rows of 48 heads 41 us, 53 with one (64 rows 5.7 and 5.1)
+    // SM four times (a call with the rows' reading back: 4096 rows of 48 heads 59
+    // us against 93, 2048 of 20 16.6 against 18.7; 128 of 32 12.1 against 10.3)
     const bool four = static_cast<int64_t>(M) * tasks >= 4ll * 64 * 152;
     const auto go = [&](auto hd_, auto tpw_, auto vec_) {
         constexpr int T = decltype(tpw_)::value;
         const dim3 grid(M, (tasks + 4 * T - 1) / (4 * T));
-        return launch_pdl(k_kv_q4_append<decltype(hd_)::value, T, decltype(vec_)::value>, grid, 128, 0, 1, s, a);
+        return launch_pdl(pdl, k_kv_q4_append<decltype(hd_)::value, T, decltype(vec_)::value>, grid, 128, 0, 1, s, a);
     };
     const auto pick = [&](auto hd_) {
         if (four && vec) return go(hd_, std::integral_constant<int, 4>{}, std::true_type{});
@@ -1209,14 +1215,14 @@ cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, con
 }
 
 cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M, float *k_out, float *v_out,
-                              size_t out_row, size_t out_head, cudaStream_t s) {
+                              size_t out_row, size_t out_head, bool pdl, cudaStream_t s) {
     if (M <= 0) return cudaSuccess;
     const unsigned threads = static_cast<unsigned>(std::min(256, (c.nkv * (hd / 4) + 31) / 32 * 32));
     const bool vec = aligned16(k_out) && aligned16(v_out) && out_row % 4 == 0 && out_head % 4 == 0;
     const auto kernel = hd == 128 ? (vec ? k_kv_q4_read<128, true> : k_kv_q4_read<128, false>)
                                   : (vec ? k_kv_q4_read<64, true> : k_kv_q4_read<64, false>);
     if (hd != 128 && hd != 64) return cudaErrorInvalidValue;
-    return launch_pdl(kernel, dim3(M), threads, 0, 1, s, c, rows, M, k_out, v_out, out_row, out_head);
+    return launch_pdl(pdl, kernel, dim3(M), threads, 0, 1, s, c, rows, M, k_out, v_out, out_row, out_head);
 }
 
 namespace {
@@ -1236,14 +1242,17 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
     const int64_t units = static_cast<int64_t>(std::max(B, 1)) * nkv * p.cgroups;
     const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
     // Clusters while all of them fit at once (two CTAs to an SM, one at W = 8)
-    // and a warp has eight tiles at most: beyond, dealing out blocks uses the
-    // SMs better than saving the second launch does.
+    // and a warp has eight tiles at most (against dealing out blocks, with its
+    // second kernel: 1 x 517 8.3 us and 12.4, 1 x 8317 15.4 and 20.6, 16 x 2000
+    // 18.5 and 21.8, 1 x 32000 28.7 and 35.6).
     const int64_t fit_cluster = p.W <= 4 ? 304 : 152;
     const int64_t need = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4ClusterWarps * kQ4Tile - 1) / (kQ4ClusterWarps * kQ4Tile));
     int csize = 1;
     while (csize < kQ4MaxCluster && csize < need && units * csize * 2 <= fit_cluster) csize *= 2;
     p.csize = units * csize <= fit_cluster && need <= 8ll * csize ? csize : 0;
-    // the CTAs that fit at once; for little work two blocks to each
+    // the CTAs that fit at once (three to an SM in 168 registers, two at W = 8;
+    // four in 128 spill: 213 us against 196 at 24 x 8192 with 5 rows); for little
+    // work two blocks to each
     const int fit = 152 * (p.W <= 4 ? 3 : 2);
     p.ctas = static_cast<int>(std::min<int64_t>(fit, std::max(units, units * ((most + 1) / 2))));
     p.whole = p.csize > 0 || most == 1;
@@ -1266,27 +1275,27 @@ cudaError_t configure_q4_attn() {
 }
 
 template <int HD, int W>
-cudaError_t launch_q4_attn_w(const KvQ4AttnArgs &a, const Q4Plan &p, int2 *owners, cudaStream_t s) {
+cudaError_t launch_q4_attn_w(const KvQ4AttnArgs &a, const Q4Plan &p, int2 *owners, bool pdl, cudaStream_t s) {
     static_assert(q4_attn_smem<HD, W>(kQ4Warps) <= 40 * 1024, "fits without an opt-in");
     if (p.csize)
-        return launch_pdl(k_kv_q4_attn<HD, W, true>, dim3(p.csize, static_cast<unsigned>(a.B) * a.c.nkv * p.cgroups),
+        return launch_pdl(pdl, k_kv_q4_attn<HD, W, true>, dim3(p.csize, static_cast<unsigned>(a.B) * a.c.nkv * p.cgroups),
                           kQ4ClusterWarps * 32, q4_attn_smem<HD, W>(kQ4ClusterWarps), p.csize, s, a, p.cgroups, owners);
-    return launch_pdl(k_kv_q4_attn<HD, W, false>, dim3(p.ctas), kQ4Warps * 32, q4_attn_smem<HD, W>(kQ4Warps), 1, s, a,
+    return launch_pdl(pdl, k_kv_q4_attn<HD, W, false>, dim3(p.ctas), kQ4Warps * 32, q4_attn_smem<HD, W>(kQ4Warps), 1, s, a,
                       p.cgroups, owners);
 }
 
 template <int HD>
-cudaError_t launch_q4_attn_hd(const KvQ4AttnArgs &a, const Q4Plan &p, cudaStream_t s) {
+cudaError_t launch_q4_attn_hd(const KvQ4AttnArgs &a, const Q4Plan &p, bool pdl, cudaStream_t s) {
     int2 *owners = p.whole ? nullptr : reinterpret_cast<int2 *>(reinterpret_cast<uint8_t *>(a.ws) + q4_parts_bytes(p, HD));
     cudaError_t e = cudaErrorInvalidValue;
     switch (p.W) {
-        case 1: e = launch_q4_attn_w<HD, 1>(a, p, owners, s); break;
-        case 2: e = launch_q4_attn_w<HD, 2>(a, p, owners, s); break;
-        case 4: e = launch_q4_attn_w<HD, 4>(a, p, owners, s); break;
-        case 8: e = launch_q4_attn_w<HD, 8>(a, p, owners, s); break;
+        case 1: e = launch_q4_attn_w<HD, 1>(a, p, owners, pdl, s); break;
+        case 2: e = launch_q4_attn_w<HD, 2>(a, p, owners, pdl, s); break;
+        case 4: e = launch_q4_attn_w<HD, 4>(a, p, owners, pdl, s); break;
+        case 8: e = launch_q4_attn_w<HD, 8>(a, p, owners, pdl, s); break;
     }
     if (e != cudaSuccess || p.whole) return e;
-    return launch_pdl(k_kv_q4_join<HD>, dim3(static_cast<unsigned>(a.nh) * a.rows * a.B), HD, 0, 1, s, a, p.cgroups, p.W,
+    return launch_pdl(pdl, k_kv_q4_join<HD>, dim3(static_cast<unsigned>(a.nh) * a.rows * a.B), HD, 0, 1, s, a, p.cgroups, p.W,
                       static_cast<const int2 *>(owners));
 }
 
@@ -1313,11 +1322,11 @@ size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int 
     return p.whole ? 0 : q4_parts_bytes(p, hd) + static_cast<size_t>(B) * nkv * p.cgroups * sizeof(int2);
 }
 
-cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, cudaStream_t s) {
+cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, bool pdl, cudaStream_t s) {
     if (a.B <= 0) return cudaSuccess;
     const Q4Plan p = q4_plan(a.B, a.rows, a.nh, a.c.nkv, a.max_len);
-    if (hd == 128) return launch_q4_attn_hd<128>(a, p, s);
-    if (hd == 64) return launch_q4_attn_hd<64>(a, p, s);
+    if (hd == 128) return launch_q4_attn_hd<128>(a, p, pdl, s);
+    if (hd == 64) return launch_q4_attn_hd<64>(a, p, pdl, s);
     return cudaErrorInvalidValue;
 }
 

@@ -381,14 +381,15 @@ int decode_attention(qw3_model *m, int l, int B, int nsplit, int csize, bool pdl
     }
     const qw3_config &c = m->cfg;
     const LayerDev &L = m->layers[l];
+    const bool dep = !(c.flags & QW3_FLAG_NO_PDL);
     const KvQ4Rows rows{m->d_seq, 0, m->d_pos, 0};
     M_TRY(m, launch_kv_q4_append(m->qkv, B, m->qkv_w, L.q_norm, L.k_norm, c.rms_eps, m->rope, kv_q4_layer(m, l),
-                                 c.head_dim, rows, c.n_heads, m->qkv, m->qkv_w, m->d_status, s));
+                                 c.head_dim, rows, c.n_heads, m->qkv, m->qkv_w, m->d_status, dep, s));
     KvQ4AttnArgs a = q4_attn_args(m, l, m->qkv, B, 1, m->o);
     a.slots = m->d_seq;
     a.lens = m->d_pos;
     a.len_add = 1;
-    M_TRY(m, launch_kv_q4_attn(a, c.head_dim, s));
+    M_TRY(m, launch_kv_q4_attn(a, c.head_dim, dep, s));
     return QW3_OK;
 }
 
@@ -1025,13 +1026,13 @@ int forward_rows(qw3_model *m, int32_t seq, const int32_t *tokens_dev, int32_t n
                 const KvQ4 kq = kv_q4_layer(m, l);
                 const KvQ4Rows at{nullptr, seq, nullptr, pos0}, all{nullptr, seq, nullptr, 0};
                 M_TRY(m, launch_kv_q4_append(m->pqkv, M, m->qkv_w, L.q_norm, L.k_norm, c.rms_eps, m->rope, kq, hd, at,
-                                             nh, m->pqkv, m->qkv_w, m->d_status, s));
+                                             nh, m->pqkv, m->qkv_w, m->d_status, false, s));
                 if (M > kQ4MaxRows) {
                     // longer chunks attend over the rows read back as f32: one
                     // pass over the context, small beside the chunk's attention
                     kvhead = static_cast<size_t>(c.max_seq_len) * hd;
                     kvsel = kvhead * nkv;
-                    M_TRY(m, launch_kv_q4_read(kq, hd, all, pos0 + M, m->q4_rows, m->q4_rows + kvsel, hd, kvhead, s));
+                    M_TRY(m, launch_kv_q4_read(kq, hd, all, pos0 + M, m->q4_rows, m->q4_rows + kvsel, hd, kvhead, false, s));
                     kv_seq = m->q4_rows;
                     kvtype = KV_F32;
                 }
@@ -1044,7 +1045,7 @@ int forward_rows(qw3_model *m, int32_t seq, const int32_t *tokens_dev, int32_t n
                 KvQ4AttnArgs a = q4_attn_args(m, l, m->pqkv, 1, M, m->po);
                 a.slot0 = seq;
                 a.len_add = pos0 + M;
-                M_TRY(m, launch_kv_q4_attn(a, hd, s));
+                M_TRY(m, launch_kv_q4_attn(a, hd, false, s));
             } else if (m->kvpack && M >= kAttnPrefillTcMinRows) {
                 M_TRY(m, launch_attn_prefill_tc(m->pqkv, M, m->qkv_w, kv_seq, kvsel, kvhead, pos0, nh, nkv, hd, scale,
                                                 m->po, m->kvpack, m->d_status, kvtype, s));
@@ -1206,7 +1207,7 @@ int qw3_generate_sample(qw3_model *m, int32_t B, const int32_t *seqs_host, int32
         const size_t at = static_cast<size_t>(sidx) * B;
         const SampleArgs a{logits_dev, V, V, temperature_dev, top_k_dev, top_p_dev, min_p_dev, u_dev + at,
                            out_tokens_dev + at, m->d_tok, prob_dev ? prob_dev + at : nullptr, m->d_status};
-        M_TRY(m, launch_sample(a, B, m->stream));
+        M_TRY(m, launch_sample(a, B, !(m->cfg.flags & QW3_FLAG_NO_PDL), m->stream));
     }
     for (const int sq : seqs) m->seq_len[sq] += n_steps;
     return QW3_OK;
@@ -1245,7 +1246,7 @@ int qw3_debug_read_kv(qw3_model *m, int32_t layer, int32_t seq, int32_t pos0, in
     if (m->kvtype == KV_Q4) {
         const KvQ4Rows rows{nullptr, seq, nullptr, pos0};
         M_TRY(m, launch_kv_q4_read(kv_q4_layer(m, layer), c.head_dim, rows, n, k_out_dev, v_out_dev,
-                                   static_cast<size_t>(c.n_kv_heads) * c.head_dim, c.head_dim, m->stream));
+                                   static_cast<size_t>(c.n_kv_heads) * c.head_dim, c.head_dim, false, m->stream));
         return QW3_OK;
     }
     M_TRY(m, launch_copy_kv_rows(kv_at(m, layer, seq), m->kvsel_stride, m->head_stride, pos0, n, c.n_kv_heads,
@@ -1472,7 +1473,8 @@ int qw3_kv_q4_append(const qw3_kv_q4 *cache, const float *qkv_dev, int32_t M, in
     KvQ4Rows rows{slots_dev, slot0, pos_dev, pos0};
     QW3_CUDA_TRY(launch_kv_q4_append(qkv_dev, M, qkv_stride, q_norm_dev, k_norm_dev, eps,
                                      reinterpret_cast<const float2 *>(rope_dev), kv_q4_view(cache), cache->head_dim,
-                                     rows, n_heads, q_out_dev, q_stride, status_dev, static_cast<cudaStream_t>(stream)));
+                                     rows, n_heads, q_out_dev, q_stride, status_dev, true,
+                                     static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }
 
@@ -1485,7 +1487,7 @@ int qw3_kv_q4_read(const qw3_kv_q4 *cache, int32_t M, const int32_t *slots_dev, 
         return fail(nullptr, QW3_ERR_INVALID_ARG, "outputs must be 4-byte aligned");
     KvQ4Rows rows{slots_dev, slot0, pos_dev, pos0};
     QW3_CUDA_TRY(launch_kv_q4_read(kv_q4_view(cache), cache->head_dim, rows, M, k_out_dev, v_out_dev,
-                                   static_cast<size_t>(cache->n_kv_heads) * cache->head_dim, cache->head_dim,
+                                   static_cast<size_t>(cache->n_kv_heads) * cache->head_dim, cache->head_dim, true,
                                    static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }
@@ -1525,7 +1527,7 @@ int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q_stride,
     a.out = out_dev; a.out_stride = out_stride; a.ws = static_cast<float *>(workspace_dev);
     a.status = status_dev;
     QW3_CUDA_TRY(configure_all());   // the kernels' shared-memory limits
-    QW3_CUDA_TRY(launch_kv_q4_attn(a, cache->head_dim, static_cast<cudaStream_t>(stream)));
+    QW3_CUDA_TRY(launch_kv_q4_attn(a, cache->head_dim, true, static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }
 
@@ -1543,7 +1545,7 @@ int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, co
                  prob_dev, status_dev};
     if (B == 0) return QW3_OK;
     QW3_CUDA_TRY(configure_all());   // the kernel's shared-memory limit
-    QW3_CUDA_TRY(launch_sample(a, B, static_cast<cudaStream_t>(stream)));
+    QW3_CUDA_TRY(launch_sample(a, B, true, static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }
 

@@ -256,25 +256,31 @@ cudaError_t launch_copy_kv_rows(const void *kv_layer_seq, size_t kvsel_stride, s
                                 int pos0, int n, int nkv, int hd, float *k_out, float *v_out, int kvtype,
                                 cudaStream_t s);
 
-// Launch that may start while the kernel before it in the stream ends
-// (programmatic dependent launch); the kernel calls pdl_wait() before it
+// Launch that, where `pdl`, may start while the kernel before it in the stream
+// ends (programmatic dependent launch): the kernel calls pdl_wait() before it
 // touches memory that others write or read. cluster > 1: clusters along x.
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, int cluster, cudaStream_t s,
-                       A &&...args) {
+cudaError_t launch_pdl(bool pdl, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, int cluster,
+                       cudaStream_t s, A &&...args) {
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    unsigned n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
@@ -301,10 +307,10 @@ struct KvQ4Rows {
 
 cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, const float *q_norm, const float *k_norm,
                                 float eps, const float2 *rope, const KvQ4 &c, int hd, const KvQ4Rows &rows, int nh,
-                                float *q_out, int64_t q_stride, int32_t *status, cudaStream_t s);
+                                float *q_out, int64_t q_stride, int32_t *status, bool pdl, cudaStream_t s);
 // Row i of head g lands at i * out_row + g * out_head floats.
 cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M, float *k_out, float *v_out,
-                              size_t out_row, size_t out_head, cudaStream_t s);
+                              size_t out_row, size_t out_head, bool pdl, cudaStream_t s);
 
 struct KvQ4AttnArgs {
     const float *q;   // [B * rows][q_stride], nh heads of hd
@@ -325,7 +331,7 @@ constexpr int kQ4MaxRows = 16, kQ4MaxGroup = 16;
 int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len);
 size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len);
 cudaError_t configure_kv_q4();
-cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, cudaStream_t s);
+cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, bool pdl, cudaStream_t s);
 
 // ---- sampling (sample.cu)
 constexpr int kSampleMaxVocab = 1 << 22;   // sums of 2^40 each stay below 2^63
@@ -343,7 +349,7 @@ struct SampleArgs {
     int32_t *status;
 };
 cudaError_t configure_sample();
-cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s);
+cudaError_t launch_sample(const SampleArgs &a, int B, bool pdl, cudaStream_t s);
 
 }  // namespace qw3
 

@@ -93,7 +93,7 @@ struct Shared {
     uint64_t bar;      // the slice has arrived
     uint32_t lost;     // it did not in time
     // what a search found
-    uint32_t bin, found, last_rank;
+    uint32_t bin, found, last_rank, sent;
     u64 above_cnt, above_w;
     u64 res[4];   // cut, ties, weight of the prefix, ties left out
 };
@@ -455,6 +455,7 @@ __device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, f
 // returns the same.
 __device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 want, bool weigh, u64 *all, u64 *listed,
                                          Shared &s) {
+    if (threadIdx.x == 0) s.sent = 0u;
     clear_histogram(false, s);
     const int mine = row.bin(thread_top);
     if (mine < kBins) atomicAdd(&s.cnt[mine], 1u);
@@ -473,11 +474,14 @@ __device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 w
             in_list += in ? w : 0;
         }
         if (in) {
-            const uint32_t at = remote_add(n_at, 1u);
-            if (at < kList)
-                remote_st(list_at + 8u * at,
-                          static_cast<u64>(logit_key(v)) << 32 | (0xffffffffu - static_cast<uint32_t>(row.base + i)));
             ++count;
+            // a CTA with more than the list holds (equal logits, say) need not send them
+            if (atomicAdd(&s.sent, 1u) < kList) {
+                const uint32_t at = remote_add(n_at, 1u);
+                if (at < kList)
+                    remote_st(list_at + 8u * at,
+                              static_cast<u64>(logit_key(v)) << 32 | (0xffffffffu - static_cast<uint32_t>(row.base + i)));
+            }
         }
     }
     u64 c = count, x = 0, ct, xt, st = 0, lt = 0;
@@ -740,7 +744,7 @@ cudaError_t configure_sample() {
     return e;
 }
 
-cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s) {
+cudaError_t launch_sample(const SampleArgs &a, int B, bool pdl, cudaStream_t s) {
     if (B <= 0) return cudaSuccess;
     int size = 1;
     if (a.V > kOneCta)
@@ -760,7 +764,7 @@ cudaError_t launch_sample(const SampleArgs &a, int B, cudaStream_t s) {
         x.token += b0;
         if (x.next) x.next += b0;
         if (x.prob) x.prob += b0;
-        const cudaError_t e = launch_pdl(is_held ? k_sample<true> : k_sample<false>, dim3(size, std::min(65535, B - b0)),
+        const cudaError_t e = launch_pdl(pdl, is_held ? k_sample<true> : k_sample<false>, dim3(size, std::min(65535, B - b0)),
                                          kThreads, is_held ? static_cast<size_t>(slice) * 4 + 16 : 0, size, s, x, slice);
         if (e != cudaSuccess) return e;
     }

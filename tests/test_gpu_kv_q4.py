@@ -253,6 +253,54 @@ def test_append_in_place_and_strided(torch):
     assert torch.equal(a.data, b.data)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_append_many_unaligned_rows_and_unaligned_outputs(torch, hd):
+    """Several heads to a warp without wide accesses: rows at odd strides and
+    starts in, queries and read-back values at odd starts out."""
+    from quantized_transformer_decode_gb300 import qw3
+    nh, nkv, M = 12, 2, 2500
+    rng = np.random.default_rng([hd, 4])
+    w = (nh + 2 * nkv) * hd
+    x = rng.standard_normal((M, w)).astype(np.float32)
+    buf = cu(torch, np.pad(x, ((0, 0), (1, 2))))
+    qw, kw = (1 + 0.1 * rng.standard_normal((2, hd))).astype(np.float32)
+    rope = rope_table(2528, hd)
+    cache = new_cache(torch, 1, 2528, nkv, hd)
+    q = torch.full((M * nh * hd + 1,), 5.0, device="cuda")
+    kv = torch.full((2, M * nkv * hd + 1), 5.0, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    dq, dk, dr = cu(torch, qw), cu(torch, kw), cu(torch, rope)
+    qw3.qw3_kv_q4_append(cache.c, buf[:, 1:].data_ptr(), M, w + 3, nh, dq.data_ptr(), dk.data_ptr(), EPS, dr.data_ptr(), 0,
+                         0, 0, 28, q[1:].data_ptr(), nh * hd, 0, s)
+    qw3.qw3_kv_q4_read(cache.c, M, 0, 0, 0, 28, kv[0, 1:].data_ptr(), kv[1, 1:].data_ptr(), s)
+    x = x.reshape(M, nh + 2 * nkv, hd)
+    qn, want_q = norm_rope(x[:, :nh], qw, rope[28:])
+    got = q.cpu().numpy()
+    assert got[0] == 5 and np.all(np.abs(got[1:].reshape(M, nh, hd) - want_q) <= 20 * 2.0 ** -24 * np.abs(qn).max(-1, keepdims=True))
+    _, want_k = norm_rope(x[:, nh:nh + nkv], kw, rope[28:])
+    for got, rows in zip(kv.cpu().numpy(), (want_k, x[:, nh + nkv:])):
+        assert got[0] == 5
+        assert np.array_equal(got[1:].reshape(M, nkv, hd), orc.kv_q4_decode(*orc.kv_q4_encode(rows)))
+
+
+@pytest.mark.parametrize("scale", [1e-25, 1e-12, 1e12, 1e17])
+def test_append_extreme_sizes(torch, scale):
+    """Inputs whose squares or products leave two floats' range."""
+    hd, M, nkv = 128, 600, 2
+    rng = np.random.default_rng(3)
+    x = (rng.standard_normal((M, 3 * nkv, hd)) * scale).astype(np.float32)
+    x[:, 2 * nkv:] = np.clip(x[:, 2 * nkv:], -5e5, 5e5)
+    w = (1 + 0.1 * rng.standard_normal(hd)).astype(np.float32)
+    w[5] = 1e-20
+    rope = rope_table(608, hd)
+    cache = new_cache(torch, 1, 608, nkv, hd)
+    cache.append(cu(torch, x.reshape(M, -1)), cu(torch, w), cu(torch, w), EPS, cu(torch, rope))
+    k, v = cache.read(n=M)
+    _, want = norm_rope(x[:, nkv:2 * nkv], w, rope[:M])
+    assert np.array_equal(k.cpu().numpy(), orc.kv_q4_decode(*orc.kv_q4_encode(want)))
+    assert np.array_equal(v.cpu().numpy(), orc.kv_q4_decode(*orc.kv_q4_encode(x[:, 2 * nkv:])))
+
+
 # ---------------------------------------------------------------- attention
 
 def plain_attention(q, k, v, lens, rows, scale):
@@ -353,7 +401,23 @@ def test_attention_max_len_is_a_bound(torch):
     q = cu(torch, rng.standard_normal((1, 2, 64)).astype(np.float32))
     ask = lambda n, m: cache.attention(q, cu(torch, [n], np.int32), max_len=m)  # noqa: E731
     assert torch.equal(ask(64, 40), ask(40, 40)) and torch.equal(ask(2147483647, 64), ask(64, 64))
-    assert not ask(-5, 64).any()
+    assert not ask(-5, 64).any() and not ask(64, 0).any()
+
+
+@pytest.mark.parametrize("B", [1, 150])
+def test_attention_nan_query_stays_in_its_head(torch, B):
+    """A NaN query gives a NaN output, and no other head or sequence one."""
+    rng = np.random.default_rng(8)
+    cache = new_cache(torch, B, 64, 2, 64)
+    put_rows(cache, torch, rng.standard_normal((B, 64, 2, 64)), rng.standard_normal((B, 64, 2, 64)))
+    q = rng.standard_normal((B, 8, 64)).astype(np.float32)
+    lens = cu(torch, np.full(B, 50), np.int32)
+    want = cache.attention(cu(torch, q), lens)
+    q[0, 5, 3] = np.nan
+    got = cache.attention(cu(torch, q), lens)
+    bad = torch.isnan(got)
+    assert bool(bad[0, 5].all()) and int(bad.sum()) == 64
+    assert torch.equal(got[~bad], want[~bad])
 
 
 def test_attention_slots_outside_and_named_twice(torch):

@@ -161,6 +161,38 @@ def test_many_rows(torch):
     check(torch, rng.standard_normal((B, V)) * 2, rng.random(B), **settings(rng, B), least=0.8)
 
 
+def test_more_rows_than_a_grid_holds(torch):
+    rng = np.random.default_rng(20)
+    B, V = 66000, 6
+    x = rng.standard_normal((B, V)).astype(np.float32)
+    u = rng.random(B).astype(np.float32)
+    token, _, _ = run(torch, x, u, temperature=np.where(np.arange(B) % 2, 1.0, 0.0))
+    c = np.cumsum(np.exp(x.astype(np.float64) - x.max(1, keepdims=True)), 1)
+    goal = u.astype(np.float64) * c[:, -1]
+    want = np.where(np.arange(B) % 2, (c <= goal[:, None]).sum(1), x.argmax(1))
+    near = (np.abs(c - goal[:, None]) < NEAR * c[:, -1:]).any(1)
+    assert np.array_equal(token[~near], want[~near]) and near.sum() < 20
+
+
+def test_lists_that_nearly_or_just_overflow(torch):
+    """More than the short list's 256 tokens tie with, or lie just above, the
+    top-k bound; top-p whose tokens fill, or overfill, the list."""
+    rng = np.random.default_rng(21)
+    V = 40000
+    rows, k, p = [], [], []
+    for n in (255, 256, 257, 300, 5000, V):
+        for kk in (1, 200, 256, 257):
+            r = rng.standard_normal(V) - 30
+            at = rng.permutation(V)[:n]
+            r[at] = 2.0 + (rng.random(n) * 1e-3 if kk % 2 else 0.0)
+            rows.append(r), k.append(kk), p.append(1.0)
+        for pp in (0.3, 0.9, 0.9999):
+            r = rng.standard_normal(V) - 30
+            r[rng.permutation(V)[:n]] = 2.0 + rng.random(n)
+            rows.append(r), k.append(0), p.append(pp)
+    check(torch, np.array(rows), rng.random(len(rows)), least=0.7, top_k=k, top_p=p)
+
+
 def test_largest_vocabulary(torch):
     rng = np.random.default_rng(18)
     V = 4194304
