@@ -171,8 +171,8 @@ __device__ __forceinline__ void share(const Row &row, u64 *slot, u64 v) {
 
 __device__ __forceinline__ void clear_histogram(bool weigh, Shared &s) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        s.cnt[i] = 0u;
         if (weigh) s.digit[0][i] = s.digit[1][i] = s.digit[2][i] = 0u;
+        else s.cnt[i] = 0u;
     }
     __syncthreads();
 }
@@ -182,7 +182,7 @@ __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Share
     if (row.size == 1) {
         __syncthreads();
         for (int i = threadIdx.x; i < kBins; i += kThreads) {
-            s.tcnt[i] = s.cnt[i];
+            s.tcnt[i] = weigh ? 0u : s.cnt[i];
             s.tw[i] = weigh ? (static_cast<u64>(s.digit[2][i]) << 28) + (static_cast<u64>(s.digit[1][i]) << 14) + s.digit[0][i] : 0;
         }
         __syncthreads();
@@ -198,16 +198,17 @@ __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Share
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t p = 2 * part + h;
-        c += remote_ld32(dsmem_map(&s.cnt[bin], p));
-        if (weigh) {
+        if (!weigh) {
+            c += remote_ld32(dsmem_map(&s.cnt[bin], p));
+        } else {
             w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[2][bin], p))) << 28;
             w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[1][bin], p))) << 14;
             w += remote_ld32(dsmem_map(&s.digit[0][bin], p));
         }
     }
     for (int o = 1; o < parts; o <<= 1) {
-        c += __shfl_xor_sync(0xffffffffu, c, o);
-        if (weigh) w += __shfl_xor_sync(0xffffffffu, w, o);
+        if (!weigh) c += __shfl_xor_sync(0xffffffffu, c, o);
+        else w += __shfl_xor_sync(0xffffffffu, w, o);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -218,8 +219,8 @@ __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Share
     sync_cluster();
 }
 
-// Histogram of the row: bin_of(logit) gives a bin or a negative number for a
-// token left out; weights only where `weigh`.
+// Histogram of the row, of counts or (weigh) of weights: bin_of(logit) gives a
+// bin or a negative number for a token left out.
 template <typename F>
 __device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s, F bin_of) {
     clear_histogram(weigh, s);
@@ -228,8 +229,9 @@ __device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s,
         const float v = row.l[i];
         const int bin = bin_of(v);
         if (bin < 0) continue;
-        atomicAdd(&s.cnt[bin], 1u);
-        if (weigh) {
+        if (!weigh) {
+            atomicAdd(&s.cnt[bin], 1u);
+        } else {
             const u64 w = fixed_weight(row.weight(v));
             const uint32_t d0 = static_cast<uint32_t>(w) & 0x3fffu, d1 = static_cast<uint32_t>(w >> 14) & 0x3fffu;
             const uint32_t d2 = static_cast<uint32_t>(w >> 28);
@@ -246,7 +248,7 @@ __device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s,
 struct Found {
     bool some;
     int bin;
-    uint32_t n;                    // tokens in the bin
+    u64 n;                         // tokens in the bin (of weights: as many at most)
     u64 w, above_c, above_w;       // its weight; counts and weight before it
     u64 total_c, total_w;          // of all bins
 };
@@ -308,6 +310,13 @@ struct Cut {
     bool some;         // equals of the key are left out
 };
 
+// The tokens of a bin of weight w in which no token's exact weight lies below
+// `least`: as many at most (with room for that weight's roundings).
+__device__ __forceinline__ u64 most_tokens(u64 w, float least) {
+    const u64 one = fixed_weight(least), low = one - (one >> 14) - 1;
+    return one > 1 ? w / low + 1 : ~0ull;
+}
+
 // The shortest prefix of the row's order that holds `target` tokens or
 // (by_weight) reaches `target` weight, its end known to lie in the bin f of the
 // first histogram; keys below floor_key are out.
@@ -319,12 +328,13 @@ __device__ Cut cut_in_bin(const Row &row, Found f, bool by_weight, u64 target, u
     uint32_t lo = logit_key(row.top - (static_cast<float>(bin0) + 1.0f) / row.step - slack);
     hi = min(hi, logit_key(row.top));
     lo = min(max(lo, floor_key), hi);
+    if (by_weight) f.n = most_tokens(f.w, exp2f(-kNats / kBins * 1.4426950408889634f * (bin0 + 1.0f)));
     while (f.n > kList) {
         if (lo == hi) {
-            // equal logits
-            const u64 one = f.w / f.n;
+            // equal logits, each of weight `one`
+            const u64 one = fixed_weight(row.weight(float_from_order_key(lo)));
             const u64 m = by_weight ? (target - f.above_w + one - 1) / one : target - f.above_c;
-            return Cut{lo, m, f.above_w + m * one, m < f.n};
+            return Cut{lo, m, f.above_w + m * one, by_weight ? m * one < f.w : m < f.n};
         }
         const int bits = 32 - __clz(hi - lo), shift = bits > 10 ? bits - 10 : 0;
         histogram(row, by_weight, s, [&](float v) {
@@ -335,6 +345,7 @@ __device__ Cut cut_in_bin(const Row &row, Found f, bool by_weight, u64 target, u
         hi -= static_cast<uint32_t>(f.bin) << shift;
         const uint32_t width = (1u << shift) - 1u;
         lo = hi - lo >= width ? hi - width : lo;
+        if (by_weight) f.n = most_tokens(f.w, row.weight(float_from_order_key(lo)));
     }
     gather(row, s, [&](float v) {
         const uint32_t k = logit_key(v);
