@@ -161,6 +161,8 @@ struct Row {
     __device__ __forceinline__ int bin(float v) const {
         return static_cast<int>(fminf((top - v) * step, static_cast<float>(kBins)));
     }
+    // bin(v) <= b, for b < kBins
+    __device__ __forceinline__ bool within(float v, int b) const { return (top - v) * step < static_cast<float>(b + 1); }
 };
 
 // Shares a word of this CTA with its cluster: afterwards slot[r] holds CTA r's.
@@ -353,35 +355,41 @@ __device__ Cut cut_in_bin(const Row &row, Found f, bool by_weight, u64 target, u
     });
     if (row.rank == 0) {
         const int n = static_cast<int>(min(s.n_list, static_cast<uint32_t>(kList)));
+        // two threads to a token, each looking at every other one
+        const int i = static_cast<int>(threadIdx.x) >> 1, half = static_cast<int>(threadIdx.x) & 1;
         if (threadIdx.x == 0) s.last_rank = 0u;
-        bool kept = false;
-        u64 before_w = f.above_w, same = 0, left = 0, mine = 0;
-        uint32_t rank = 0;
-        if (static_cast<int>(threadIdx.x) < n) {
-            mine = s.list[threadIdx.x];
-            s.list_w[threadIdx.x] = fixed_weight(row.weight(float_from_order_key(static_cast<uint32_t>(mine >> 32))));
+        u64 before_w = 0, mine = 0, w = 0;
+        if (i < n) {
+            mine = s.list[i];
+            w = fixed_weight(row.weight(float_from_order_key(static_cast<uint32_t>(mine >> 32))));
+            s.list_w[i] = w;
         }
         __syncthreads();
-        if (static_cast<int>(threadIdx.x) < n) {
-            for (int j = 0; j < n; ++j) {
-                const u64 x = s.list[j];
-                if (x > mine) {
-                    ++rank;
-                    before_w += s.list_w[j];
-                    same += (x >> 32) == (mine >> 32);
-                } else if (x < mine) {
-                    left += (x >> 32) == (mine >> 32);
-                }
+        uint32_t rank = 0, same = 0, equal = 0;
+        if (i < n) {
+            const uint32_t key = static_cast<uint32_t>(mine >> 32);
+#pragma unroll 4
+            for (int j = half; j < n; j += 2) {
+                const u64 x = s.list[j], xw = s.list_w[j];
+                const bool above = x > mine, eq = static_cast<uint32_t>(x >> 32) == key;
+                rank += above;
+                before_w += above ? xw : 0;
+                same += above && eq;
+                equal += eq;
             }
-            kept = by_weight ? before_w < target : f.above_c + rank < target;
-            if (kept) atomicMax(&s.last_rank, rank);
         }
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        same += __shfl_xor_sync(0xffffffffu, same, 1);
+        equal += __shfl_xor_sync(0xffffffffu, equal, 1);
+        before_w += __shfl_xor_sync(0xffffffffu, before_w, 1) + f.above_w;
+        const bool kept = i < n && (by_weight ? before_w < target : f.above_c + rank < target);
+        if (kept) atomicMax(&s.last_rank, rank);
         __syncthreads();
-        if (kept && rank == s.last_rank) {
+        if (kept && !half && rank == s.last_rank) {
             s.res[0] = mine >> 32;
             s.res[1] = same + 1;
-            s.res[2] = before_w + s.list_w[threadIdx.x];
-            s.res[3] = left;
+            s.res[2] = before_w + w;
+            s.res[3] = equal - same - 1;
         }
         if (threadIdx.x == 0) s.n_list = 0u;
         __syncthreads();
@@ -478,7 +486,7 @@ __device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 w
 #pragma unroll 4
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
         const float v = row.l[i];
-        const bool in = row.bin(v) <= f.bin;
+        const bool in = row.within(v, f.bin);
         if (weigh) {
             const u64 w = fixed_weight(row.weight(v));
             sum += w;
