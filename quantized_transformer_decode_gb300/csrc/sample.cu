@@ -90,6 +90,7 @@ struct Shared {
     u64 peer2[kMaxCluster], peer3[kMaxCluster];
     u64 red[2 * kWarps + 2];
     uint32_t n_list;
+    int row;           // which row this cluster takes
     uint64_t bar;      // the slice has arrived
     uint32_t lost;     // it did not in time
     // what a search found
@@ -529,8 +530,43 @@ __device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 w
     return fits;
 }
 
+// The row of the cluster that starts as the c-th of n: rows that take longest
+// first, so that no such row is begun last (cuts over the whole vocabulary, then
+// long lists, then the rest).
+__device__ int row_of(const SampleArgs &a, int n, int c, Shared &s) {
+    const auto kind = [&](int i) {
+        const int k = a.top_k ? a.top_k[i] : 0;
+        const bool has_k = k > 0 && k < a.V, greedy = a.temperature && a.temperature[i] <= 0.0f;
+        if (greedy) return 0;
+        if (has_k ? k > kList : a.top_p && a.top_p[i] < 1.0f) return 2;
+        return has_k && k > 64 ? 1 : 0;
+    };
+    // places in the order, a block of rows after another: the first pass counts
+    u64 t2 = 0, t1 = 0, p2 = 0, p1 = 0;
+    for (int pass = n <= kThreads ? 1 : 0; pass < 2; ++pass)
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+            const int i = i0 + static_cast<int>(threadIdx.x), q = i < n ? kind(i) : -1;
+            u64 x2 = q == 2, x1 = q == 1, n2, n1;
+            scan2(x2, x1, n2, n1, s);
+            if (pass == 0 || n <= kThreads) {
+                t2 += n2;
+                t1 += n1;
+            }
+            if (pass == 1) {
+                x2 += p2;
+                x1 += p1;
+                const u64 at = q == 2 ? x2 : q == 1 ? t2 + x1 : t2 + t1 + static_cast<u64>(i) - x2 - x1;
+                if (q >= 0 && at == static_cast<u64>(c)) s.row = i;
+                p2 += n2;
+                p1 += n1;
+            }
+        }
+    __syncthreads();
+    return s.row;
+}
+
 template <bool kHeld>
-__global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bool reorder) {
     extern __shared__ __align__(16) float held[];
     __shared__ Shared s;
     pdl_wait();
@@ -539,7 +575,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice) {
     Row row;
     row.rank = size > 1 ? cluster_rank() : 0u;
     row.size = static_cast<uint32_t>(size);
-    const int b = blockIdx.y;
+    const int b = reorder ? row_of(a, static_cast<int>(gridDim.y), static_cast<int>(blockIdx.y), s) : static_cast<int>(blockIdx.y);
     row.base = static_cast<int>(row.rank) * slice;
     row.n = max(0, min(slice, a.V - row.base));
     const float *src = a.logits + b * a.stride + row.base;
@@ -772,6 +808,8 @@ cudaError_t launch_sample(const SampleArgs &a, int B, bool pdl, cudaStream_t s) 
             size *= 2;
     const int slice = (a.V + size - 1) / size;
     const bool is_held = slice <= kMaxHeld;
+    // rows in more than one wave (two CTAs to an SM) with settings of their own
+    const bool reorder = static_cast<int64_t>(B) * size > 2 * 152 && (a.top_p || a.top_k);
     for (int b0 = 0; b0 < B; b0 += 65535) {
         SampleArgs x = a;
         x.logits += b0 * a.stride;
@@ -784,7 +822,7 @@ cudaError_t launch_sample(const SampleArgs &a, int B, bool pdl, cudaStream_t s) 
         if (x.next) x.next += b0;
         if (x.prob) x.prob += b0;
         const cudaError_t e = launch_pdl(pdl, is_held ? k_sample<true> : k_sample<false>, dim3(size, std::min(65535, B - b0)),
-                                         kThreads, is_held ? static_cast<size_t>(slice) * 4 + 16 : 0, size, s, x, slice);
+                                         kThreads, is_held ? static_cast<size_t>(slice) * 4 + 16 : 0, size, s, x, slice, reorder);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

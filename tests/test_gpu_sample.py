@@ -174,6 +174,14 @@ def test_more_rows_than_a_grid_holds(torch):
     assert np.array_equal(token[~near], want[~near]) and near.sum() < 20
 
 
+@pytest.mark.parametrize("B,V", [(512, 301), (1400, 300), (40, 151936)])
+def test_rows_of_every_kind_in_several_waves(torch, B, V):
+    """More rows than run at once, each with settings of its own: the order in
+    which they are taken must not show."""
+    rng = np.random.default_rng([B, V])
+    check(torch, rng.standard_normal((B, V)) * 2.5, rng.random(B), least=0.8, **settings(rng, B))
+
+
 def test_lists_that_nearly_or_just_overflow(torch):
     """More than the short list's 256 tokens tie with, or lie just above, the
     top-k bound; top-p whose tokens fill, or overfill, the list."""
