@@ -530,37 +530,22 @@ __device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 w
     return fits;
 }
 
-// The row of the cluster that starts as the c-th of n: rows that take longest
-// first, so that no such row is begun last (cuts over the whole vocabulary, then
-// long lists, then the rest).
+// The row of the cluster that starts as the c-th of n <= kThreads: rows that take
+// longest first, so that no such row is begun last (cuts over the whole
+// vocabulary, then long lists, then the rest).
 __device__ int row_of(const SampleArgs &a, int n, int c, Shared &s) {
-    const auto kind = [&](int i) {
+    const int i = static_cast<int>(threadIdx.x);
+    int kind = -1;
+    if (i < n) {
         const int k = a.top_k ? a.top_k[i] : 0;
         const bool has_k = k > 0 && k < a.V, greedy = a.temperature && a.temperature[i] <= 0.0f;
-        if (greedy) return 0;
-        if (has_k ? k > kList : a.top_p && a.top_p[i] < 1.0f) return 2;
-        return has_k && k > 64 ? 1 : 0;
-    };
-    // places in the order, a block of rows after another: the first pass counts
-    u64 t2 = 0, t1 = 0, p2 = 0, p1 = 0;
-    for (int pass = n <= kThreads ? 1 : 0; pass < 2; ++pass)
-        for (int i0 = 0; i0 < n; i0 += kThreads) {
-            const int i = i0 + static_cast<int>(threadIdx.x), q = i < n ? kind(i) : -1;
-            u64 x2 = q == 2, x1 = q == 1, n2, n1;
-            scan2(x2, x1, n2, n1, s);
-            if (pass == 0 || n <= kThreads) {
-                t2 += n2;
-                t1 += n1;
-            }
-            if (pass == 1) {
-                x2 += p2;
-                x1 += p1;
-                const u64 at = q == 2 ? x2 : q == 1 ? t2 + x1 : t2 + t1 + static_cast<u64>(i) - x2 - x1;
-                if (q >= 0 && at == static_cast<u64>(c)) s.row = i;
-                p2 += n2;
-                p1 += n1;
-            }
-        }
+        const bool whole = has_k ? k > kList : a.top_p && a.top_p[i] < 1.0f;
+        kind = greedy ? 0 : whole ? 2 : has_k && k > 64 ? 1 : 0;
+    }
+    u64 x2 = kind == 2, x1 = kind == 1, n2, n1;
+    scan2(x2, x1, n2, n1, s);
+    const u64 at = kind == 2 ? x2 : kind == 1 ? n2 + x1 : n2 + n1 + static_cast<u64>(i) - x2 - x1;
+    if (kind >= 0 && at == static_cast<u64>(c)) s.row = i;
     __syncthreads();
     return s.row;
 }
@@ -808,8 +793,12 @@ cudaError_t launch_sample(const SampleArgs &a, int B, bool pdl, cudaStream_t s) 
             size *= 2;
     const int slice = (a.V + size - 1) / size;
     const bool is_held = slice <= kMaxHeld;
-    // rows in more than one wave (two CTAs to an SM) with settings of their own
-    const bool reorder = static_cast<int64_t>(B) * size > 2 * 152 && (a.top_p || a.top_k);
+    // Settings that differ from row to row, in more than one wave (two CTAs to an
+    // SM): 64 rows of 151936 54 us against 65, 400 of 32000 64 against 77, 512 of
+    // 8192 32 against 37. Finding its row costs a CTA two microseconds, which rows
+    // of the same settings pay for nothing: 33 us against 30, 46 against 42, 24
+    // against 21.
+    const bool reorder = static_cast<int64_t>(B) * size > 2 * 152 && B <= kThreads && (a.top_p || a.top_k);
     for (int b0 = 0; b0 < B; b0 += 65535) {
         SampleArgs x = a;
         x.logits += b0 * a.stride;
