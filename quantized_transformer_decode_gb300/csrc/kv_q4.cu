@@ -494,8 +494,10 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 //    that hi and lo stay clear of f16's subnormals; both undone in f32.
 //  - the scores leave the tensor core with positions along rows and enter it
 //    again with positions along k: one 8x8 transpose in registers each.
-// A chain of products in the tensor core is 2 instructions long; the sums over
-// blocks and tiles are f32 with rounding to nearest. mma.sync rather than
+// A chain of products in the tensor core is 2 instructions long (4 where hi and
+// lo take an operand each: the small lo products first, so that they add no
+// rounding to speak of); the sums over blocks and tiles are f32 with rounding to
+// nearest. mma.sync rather than
 // tcgen05: with at most 8 columns the product is bound by what the codes cost
 // (bytes, then the unpacking), and registers to registers saves writing the
 // unpacked codes to shared memory and reading them back.
@@ -603,6 +605,11 @@ __device__ __forceinline__ void ld_words(uint32_t (&d)[N], const uint8_t *p) {
         d[0] = *reinterpret_cast<const uint32_t *>(p);
     }
 }
+
+// How far (log2) a score may pass the highest at the last change of the
+// weights' unit: P keeps 2^-39 of its largest possible value, so 2^-33 of the
+// highest weight.
+constexpr float kRoom = 6.0f;
 
 // A warp's tile in shared memory: codes of K, of V, scales of K, of V. Each
 // warp has a ring of kQ4Stages of them, filled by bulk copies.
@@ -856,22 +863,19 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
     }
     const int low_lim = len - a.rows + col0 / G + 1;   // positions that every column sees
 
-    float acc[NB][2][NT][4], mx[2], ref[2], sum[2];
+    float acc[NB][2][4], mx[2], ref[2], sum[2];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][m][n][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[i][m][e] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         mx[e] = -INFINITY;
         ref[e] = -INFINITY;
         sum[e] = 0.0f;
     }
-    // 2^kf brings P times the largest V scale so far to 2^15 at most; vlim:
+    // 2^(kf + kRoom) brings P times the largest V scale so far to 2^15 at most; vlim:
     // the largest scale that the present kf takes
     float kf = 37.0f;
     __half2 vlim = __float2half2_rn(0.0f);
@@ -890,7 +894,7 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
         float s[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            float t[NT][4];
+            float t[4];
             uint32_t kw[2][Wd::K], kd[2][Wd::S];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -904,18 +908,19 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
                 unpack8(kw[1][i], magic, x1);
                 const float d0 = half_of(kd[0][i >> 1], i & 1), d1 = half_of(kd[1][i >> 1], i & 1);
                 const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float u[4];
-                    mma_f16_first(u, a0, qf[2 * i][n]);
-                    mma_f16(u, a1, qf[2 * i + 1][n]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) t[n][e] = i ? fmaf(u[e], e < 2 ? d0 : d1, t[n][e]) : u[e] * (e < 2 ? d0 : d1);
+                float u[4];
+                mma_f16_first(u, a0, qf[2 * i][NT - 1]);
+                mma_f16(u, a1, qf[2 * i + 1][NT - 1]);
+                if constexpr (NT == 2) {
+                    mma_f16(u, a0, qf[2 * i][0]);
+                    mma_f16(u, a1, qf[2 * i + 1][0]);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[e] = i ? fmaf(u[e], e < 2 ? d0 : d1, t[e]) : u[e] * (e < 2 ? d0 : d1);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float v = W <= 4 ? t[0][e] + __shfl_xor_sync(0xffffffffu, t[0][e], 2) : t[0][e] + t[NT - 1][e];
+                const float v = W <= 4 ? t[e] + __shfl_xor_sync(0xffffffffu, t[e], 2) : t[e];
                 s[m][e] = v * cscale[e & 1];
             }
         }
@@ -937,38 +942,50 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
                         for (int w = 0; w < Wd::S; ++w) vd[m][h][w] = 0u;
             }
         }
-        // ---- the unit of P: does a V scale pass what kf takes?
-        {
-            __half2 big = __float2half2_rn(0.0f);
+        // ---- weights 2^(s - ref) (any reference serves as long as one is used
+        // throughout): a new one where a score passes the highest so far by more
+        // than kRoom, or a V scale what kf takes
+        __half2 big = __float2half2_rn(0.0f);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int w = 0; w < Wd::S; ++w) big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&vd[m][h][w])));
-            if (!__all_sync(0xffffffffu, __hble2(big, vlim))) {
-                const uint32_t t = __reduce_max_sync(0xffffffffu, max(static_cast<uint32_t>(__half_as_ushort(__low2half(big))),
-                                                                      static_cast<uint32_t>(__half_as_ushort(__high2half(big)))));
+                for (int w = 0; w < Wd::S; ++w) big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&vd[m][h][w])));
+        bool stays = __hble2(big, vlim);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) stays &= s[m][e] <= mx[e & 1] + kRoom;
+        if (!__all_sync(0xffffffffu, stays)) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(static_cast<uint32_t>(__half_as_ushort(__low2half(big))),
+                                                                    static_cast<uint32_t>(__half_as_ushort(__high2half(big)))));
+            if (half_of(top, 0) > __low2float(vlim)) {
                 // 2^e > the largest scale; two more bits so that a rise is rare
-                const int e = t ? static_cast<int>(__float_as_uint(half_of(t, 0)) >> 23) - 126 : -24;
-                const int lim2 = min(e + 2, 16);
+                const int e = static_cast<int>(__float_as_uint(half_of(top, 0)) >> 23) - 126, lim2 = min(e + 2, 16);
                 vlim = lim2 >= 16 ? __half2half2(__ushort_as_half(0x7BFF)) : __float2half2_rn(pow2_f32(lim2));
-                kf = static_cast<float>(15 - lim2);
+                kf = 15.0f - kRoom - static_cast<float>(lim2);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float t = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                mx[e] = fmaxf(mx[e], t);
+                const float to = mx[e] - kf, now = to == -INFINITY ? 0.0f : to, corr = exp2_f32(ref[e] - now);
+                ref[e] = to;
+                sum[e] *= corr;
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int d = 0; d < 2; ++d)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) acc[i][d][e + 2 * h] *= corr;
             }
         }
-        // ---- softmax: weights 2^(s - ref), ref the running maximum less kf (any
-        // reference serves as long as one is used throughout)
-        float corr[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-            mx[e] = fmaxf(mx[e], t);
-            const float to = mx[e] - kf, now = to == -INFINITY ? 0.0f : to;
-            corr[e] = exp2_f32(ref[e] - now);
-            ref[e] = to;
-            sum[e] *= corr[e];
+            const float now = ref[e] == -INFINITY ? 0.0f : ref[e];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -1012,31 +1029,38 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
                 ld_words(vw[m][h], st + St::V + (16 * m + 8 * (h >> 1) + ((h & 1) ? 4 + (c ^ 1) : c)) * (HD / 2) + r * (HD / 16));
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            float u[2][NT][4];
+            float u[2][4];
+            uint32_t a0[MT][4], a1[MT][4];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 uint32_t x0[4], x1[4];
                 const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
                 unpack8(__byte_perm(vw[m][0][i >> 1], vw[m][1][i >> 1], sel), magic, x0);
                 unpack8(__byte_perm(vw[m][2][i >> 1], vw[m][3][i >> 1], sel), magic, x1);
-                const uint32_t a0[4] = {x0[0], x0[1], x1[0], x1[1]}, a1[4] = {x0[2], x0[3], x1[2], x1[3]};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (m == 0) {
-                        mma_f16_first(u[0][n], a0, pf[i / DUP][m][n]);
-                        mma_f16_first(u[1][n], a1, pf[i / DUP][m][n]);
-                    } else {
-                        mma_f16(u[0][n], a0, pf[i / DUP][m][n]);
-                        mma_f16(u[1][n], a1, pf[i / DUP][m][n]);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    a0[m][e] = x0[e];
+                    a0[m][2 + e] = x1[e];
+                    a1[m][e] = x0[2 + e];
+                    a1[m][2 + e] = x1[2 + e];
                 }
             }
 #pragma unroll
+            for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (m == 0 && n == NT - 1) {
+                        mma_f16_first(u[0], a0[m], pf[i / DUP][m][n]);
+                        mma_f16_first(u[1], a1[m], pf[i / DUP][m][n]);
+                    } else {
+                        mma_f16(u[0], a0[m], pf[i / DUP][m][n]);
+                        mma_f16(u[1], a1[m], pf[i / DUP][m][n]);
+                    }
+                }
+#pragma unroll
             for (int d = 0; d < 2; ++d)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][d][n][e] = fmaf(acc[i][d][n][e], corr[e & 1], u[d][n][e]);
+                for (int e = 0; e < 4; ++e) acc[i][d][e] += u[d][e];
         }
         ++taken;
         __syncwarp();   // the tile is in registers: its place may be filled again
@@ -1069,8 +1093,8 @@ __global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, C
             for (int d = 0; d < 2; ++d)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    o[2 * d + h] = W <= 4 ? acc[i][d][0][e + 2 * h] + __shfl_xor_sync(0xffffffffu, acc[i][d][0][e + 2 * h], 2)
-                                          : acc[i][d][0][e + 2 * h] + acc[i][d][NT - 1][e + 2 * h];
+                    o[2 * d + h] = W <= 4 ? acc[i][d][e + 2 * h] + __shfl_xor_sync(0xffffffffu, acc[i][d][e + 2 * h], 2)
+                                          : acc[i][d][e + 2 * h];
             const int n = 2 * c + e, j = W <= 4 ? n % W : n;
             if (W > 4 || (n < 4 && n / W == i % DUP)) {
                 float2 *dst = reinterpret_cast<float2 *>(res + j * PS + i * 32 + 4 * r);
