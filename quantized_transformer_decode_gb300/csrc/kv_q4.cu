@@ -588,6 +588,12 @@ __device__ __forceinline__ int q4_len(const KvQ4AttnArgs &a, int b) {
 // 4 with hi and lo in one operand, 8 with one for each.
 __host__ __device__ constexpr int q4_ops(int W) { return W <= 4 ? 1 : 2; }
 
+// CTAs of kQ4Warps warps that share an SM: three in 168 registers, two where 8
+// columns of 128 dimensions want 254 (three spill: 4 x 5000 with 16 rows 66 us
+// against 64; at 64 dimensions three are faster, 30 x 4000 with 4 rows 27 against
+// 29). Four in 128 spill too: 64 x 2048 with 32/8 heads 51 us against 47.
+__host__ __device__ constexpr int q4_per_sm(int hd, int W) { return W <= 4 || hd <= 64 ? 3 : 2; }
+
 template <int HD>
 struct Q4Words {   // words of a thread's share of a row
     static constexpr int K = HD / 32, V = HD / 64, S = HD / 64;
@@ -664,7 +670,7 @@ __device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
 // and the last CTA of each unit.
 // CLUSTER: no workspace; grid (csize, units), clusters along x.
 template <int HD, int W, bool CLUSTER>
-__global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, CLUSTER ? (W <= 4 ? 2 : 1) : (W <= 4 ? 3 : 2))
+__global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, CLUSTER ? (W <= 4 ? 2 : 1) : q4_per_sm(HD, W))
     k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
     constexpr int NW = CLUSTER ? kQ4ClusterWarps : kQ4Warps, kStep = NW * kQ4Tile;
     constexpr int NB = HD / 32, NT = q4_ops(W);
@@ -1258,7 +1264,7 @@ struct Q4Plan {
     bool whole;   // no unit is cut: no workspace, no second kernel
 };
 
-Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
+Q4Plan q4_plan(int B, int rows, int nh, int nkv, int hd, int max_len) {
     const int cols = nh / nkv * rows;
     Q4Plan p;
     p.W = cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : 8;
@@ -1274,10 +1280,8 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int max_len) {
     int csize = 1;
     while (csize < kQ4MaxCluster && csize < need && units * csize * 2 <= fit_cluster) csize *= 2;
     p.csize = units * csize <= fit_cluster && need <= 8ll * csize ? csize : 0;
-    // the CTAs that fit at once (three to an SM in 168 registers, two at W = 8;
-    // four in 128 spill: 213 us against 196 at 24 x 8192 with 5 rows); for little
-    // work two blocks to each
-    const int fit = 152 * (p.W <= 4 ? 3 : 2);
+    // the CTAs that fit at once; for little work two blocks to each
+    const int fit = 152 * q4_per_sm(hd, p.W);
     p.ctas = static_cast<int>(std::min<int64_t>(fit, std::max(units, units * ((most + 1) / 2))));
     p.whole = p.csize > 0 || most == 1;
     return p;
@@ -1337,18 +1341,18 @@ cudaError_t configure_kv_q4() {
     return e;
 }
 
-int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int max_len) {
-    return q4_plan(B, rows, nh, nkv, max_len).whole ? 1 : 2;
+int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int hd, int max_len) {
+    return q4_plan(B, rows, nh, nkv, hd, max_len).whole ? 1 : 2;
 }
 
 size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len) {
-    const Q4Plan p = q4_plan(B, rows, nh, nkv, max_len);
+    const Q4Plan p = q4_plan(B, rows, nh, nkv, hd, max_len);
     return p.whole ? 0 : q4_parts_bytes(p, hd) + static_cast<size_t>(B) * nkv * p.cgroups * sizeof(int2);
 }
 
 cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, bool pdl, cudaStream_t s) {
     if (a.B <= 0) return cudaSuccess;
-    const Q4Plan p = q4_plan(a.B, a.rows, a.nh, a.c.nkv, a.max_len);
+    const Q4Plan p = q4_plan(a.B, a.rows, a.nh, a.c.nkv, hd, a.max_len);
     if (hd == 128) return launch_q4_attn_hd<128>(a, p, pdl, s);
     if (hd == 64) return launch_q4_attn_hd<64>(a, p, pdl, s);
     return cudaErrorInvalidValue;

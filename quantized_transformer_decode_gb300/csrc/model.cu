@@ -1283,7 +1283,7 @@ int qw3_decode_plan(const qw3_model *m, int32_t B, int32_t *persistent, int32_t 
                                         : 4 + 7 * c.n_layers;
     // the 4-bit cache: the append and the attention's second kernel besides
     if (m->kvtype == KV_Q4)
-        *launches_per_step += c.n_layers * kv_q4_attn_launches(B, 1, c.n_heads, c.n_kv_heads, c.max_seq_len);
+        *launches_per_step += c.n_layers * kv_q4_attn_launches(B, 1, c.n_heads, c.n_kv_heads, c.head_dim, c.max_seq_len);
     return QW3_OK;
 }
 
