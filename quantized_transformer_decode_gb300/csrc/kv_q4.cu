@@ -42,14 +42,16 @@ __device__ __forceinline__ int q4_lane_byte(int lane, bool v_row) {
 }
 
 // Loads and stores of a lane's E values; VEC where everything is aligned for one
-// access.
-template <int E, bool VEC>
+// access. CS: what leaves L2 first.
+template <int E, bool VEC, bool CS = false>
 __device__ __forceinline__ void q4_ld(float (&v)[E], const float *p) {
     if constexpr (VEC && E == 4) {
-        const float4 t = *reinterpret_cast<const float4 *>(p);
+        const float4 *from = reinterpret_cast<const float4 *>(p);
+        const float4 t = CS ? __ldcs(from) : *from;
         v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
     } else if constexpr (VEC && E == 2) {
-        const float2 t = *reinterpret_cast<const float2 *>(p);
+        const float2 *from = reinterpret_cast<const float2 *>(p);
+        const float2 t = CS ? __ldcs(from) : *from;
         v[0] = t.x; v[1] = t.y;
     } else {
 #pragma unroll
@@ -57,12 +59,16 @@ __device__ __forceinline__ void q4_ld(float (&v)[E], const float *p) {
     }
 }
 
-template <int E, bool VEC>
+template <int E, bool VEC, bool CS = false>
 __device__ __forceinline__ void q4_st(float *p, const float (&v)[E]) {
     if constexpr (VEC && E == 4) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        const float4 t = make_float4(v[0], v[1], v[2], v[3]);
+        if constexpr (CS) __stcs(reinterpret_cast<float4 *>(p), t);
+        else *reinterpret_cast<float4 *>(p) = t;
     } else if constexpr (VEC && E == 2) {
-        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+        const float2 t = make_float2(v[0], v[1]);
+        if constexpr (CS) __stcs(reinterpret_cast<float2 *>(p), t);
+        else *reinterpret_cast<float2 *>(p) = t;
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) p[e] = v[e];
@@ -318,11 +324,18 @@ struct Q4AppendArgs {
 
 // A warp takes TPW heads of a row, one after another, their loads first: one
 // for a few rows (every warp of the GPU has something to do), four for many
-// (four loads in flight for each warp). Bound by memory: a row is read once and
-// its queries written once.
+// (four loads in flight for each warp). A row is read once and its queries
+// written once: 4096 rows of 48 heads of 128 (172 MB, a floor of 25 us) take 44
+// us, 0.58 of the measured copy rate. What bounds it there: waiting for loads (the
+// rotation's depends on the position's) at 32 warps to an SM, a third of the
+// issue slots; more warps in fewer registers (40 to 56 a thread) or two heads to
+// a warp are no faster. Few rows: the launch and two loads in a row.
 template <int HD, int TPW, bool VEC>
 __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L, NB = Q4Row<HD>::NB;
+    // many rows pass through L2 once and leave it first (with the rows' reading back
+    // 55.4 us against 58.6 with plain accesses)
+    constexpr bool kMany = TPW > 1;
     const int lane = threadIdx.x & 31;
     const int task0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * TPW, row = blockIdx.x;
     const int nkv = a.c.nkv, tasks = a.nh + 2 * nkv;
@@ -335,7 +348,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
     // every load that waits for no other first
 #pragma unroll
     for (int t = 0; t < TPW; ++t)
-        if (task0 + t < tasks) q4_ld<E, VEC>(raw[t], src + static_cast<int64_t>(task0 + t) * HD);
+        if (task0 + t < tasks) q4_ld<E, VEC, kMany>(raw[t], src + static_cast<int64_t>(task0 + t) * HD);
     if (TPW == 1) q4_ld<E, VEC>(in.w, (task0 < a.nh ? a.q_norm : a.k_norm) + lane * E);
     int slot, pos;
     const bool there = kv_q4_row(a.c, a.rows, row, slot, pos);
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
                 const float o = __shfl_xor_sync(0xffffffffu, raw[t][e], 16);
                 y[e] = r * (lane < 16 ? raw[t][e] * in.cs[e].x - o * in.cs[e].y : o * in.cs[e].y + raw[t][e] * in.cs[e].x);
             }
-            q4_st<E, VEC>(a.q_out + row * a.q_stride + static_cast<int64_t>(task0 + t) * HD + lane * E, y);
+            q4_st<E, VEC, kMany>(a.q_out + row * a.q_stride + static_cast<int64_t>(task0 + t) * HD + lane * E, y);
         }
         return;
     }
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
         const bool query = task < a.nh;
         if (!there) {
             const float zero[E] = {};
-            if (query) q4_st<E, VEC>(a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD + lane * E, zero);
+            if (query) q4_st<E, VEC, kMany>(a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD + lane * E, zero);
             continue;
         }
         in.key = task < a.nh + nkv;
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
         if (query) {
 #pragma unroll
             for (int e = 0; e < E; ++e) y[e] *= r;
-            q4_st<E, VEC>(a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD + lane * E, y);
+            q4_st<E, VEC, kMany>(a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD + lane * E, y);
             continue;
         }
         const int sel = in.key ? 0 : 1, g = task - a.nh - sel * nkv;
@@ -463,8 +476,7 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = s[sel] * static_cast<float>(static_cast<int>((w[sel] >> (4 * e)) & 15u) - 8);
             float *to = (sel ? v_out : k_out) + row * out_row + g * out_head + 4 * j;
-            if constexpr (VEC) __stcs(reinterpret_cast<float4 *>(to), make_float4(y[0], y[1], y[2], y[3]));
-            else q4_st<4, false>(to, y);
+            q4_st<4, VEC, true>(to, y);
         }
     }
 }
@@ -501,10 +513,12 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 // tcgen05: with at most 8 columns the product is bound by what the codes cost
 // (bytes, then the unpacking), and registers to registers saves writing the
 // unpacked codes to shared memory and reading them back.
-// What bounds it: instructions. A warp's tile of 4.6 KB takes some 900 of them
-// (unpacking, the split of P, the softmax), half on the pipe that issues every
-// second cycle; 64 sequences of 2048 positions (32/8 heads, 151 MB) take 47 us,
-// 3.2 TB/s, 0.48 of the measured copy rate.
+// What bounds it: instructions, and the register file's ports, for which mma and
+// FMA compete (8 mma and 64 FMA take the sum of their times, not the longer). A
+// warp's tile of 4.6 KB takes some 700 instructions (830 at 8 columns: unpacking,
+// the split of P, the softmax); the copies alone would take 29 of the 43 us of 64
+// sequences of 2048 positions (32/8 heads, 151 MB; 3.5 TB/s, 0.52 of the measured
+// copy rate), the instructions alone 38.
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
