@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 // unpacked codes to shared memory and reading them back.
 // What bounds it: instructions, and the register file's ports, for which mma and
 // FMA compete (8 mma and 64 FMA take the sum of their times, not the longer). A
-// warp's tile of 4.6 KB takes some 700 instructions (830 at 8 columns: unpacking,
+// warp's tile of 4.6 KB takes some 750 instructions (830 at 8 columns: unpacking,
 // the split of P, the softmax); the copies alone would take 29 of the 43 us of 64
 // sequences of 2048 positions (32/8 heads, 151 MB; 3.5 TB/s, 0.52 of the measured
 // copy rate), the instructions alone 38.

@@ -24,7 +24,9 @@
 // further by histograms over its keys until it holds at most kList tokens or
 // equal logits only. What bounds it: the passes over the slices in shared
 // memory (some 20 instructions a token where weights are summed) and, for one
-// row, the barriers between them.
+// row, the barriers between them. Measured: one row of 151936 with temperature,
+// top-k 20, top-p 0.95 and min-p 12 us; 64 such rows 32 us, without a cut 32 us
+// (39 MB, 1.2 TB/s), with top-p 0.92 alone, which keeps most of the row, 102 us.
 //
 // Sums are taken in 64-bit fixed point (2^40 for the largest weight): they are
 // the same whatever the order of the additions, so one input gives one token.
@@ -768,11 +770,13 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     }
 }
 
-// CTAs per row and the tokens of one: a small vocabulary stays in one CTA, a
-// large one is cut into slices of which two fit an SM (up to 20480 tokens, 80
-// KB), or finer, to 16 CTAs, while the rows together leave SMs free; beyond 16
-// slices of what one SM holds the row is read again from memory (L2) at every
-// pass.
+// CTAs per row and the tokens of one: a small vocabulary stays in one CTA (64
+// rows of 8192 with top-k and top-p 10.5 us, 12.5 in two CTAs), a large one is
+// cut into slices of which two fit an SM (up to 20480 tokens, 80 KB: 64 rows of
+// 151936 with settings of their own 51 us in 8 CTAs each, 65 in 4 that take an SM
+// each), or finer, to 16 CTAs, while the rows together leave SMs free (one row
+// without a cut 7.9 us in 16 CTAs, 9.6 in 8; 64 rows 53 and 32); beyond 16 slices
+// of what one SM holds the row is read again from memory (L2) at every pass.
 constexpr int kOneCta = 8192, kSlice = 20480, kMaxHeld = 45056;
 
 }  // namespace
