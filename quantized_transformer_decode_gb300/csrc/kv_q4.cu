@@ -325,8 +325,8 @@ struct Q4AppendArgs {
 // A warp takes TPW heads of a row, one after another, their loads first: one
 // for a few rows (every warp of the GPU has something to do), four for many
 // (four loads in flight for each warp). A row is read once and its queries
-// written once: 4096 rows of 48 heads of 128 (172 MB, a floor of 25 us) take 44
-// us, 0.58 of the measured copy rate. What bounds it there: waiting for loads (the
+// written once: 4096 rows of 48 heads of 128 (172 MB, a floor of 25 us) take 46
+// us, 0.55 of the measured copy rate. What bounds it there: waiting for loads (the
 // rotation's depends on the position's) at 32 warps to an SM, a third of the
 // issue slots; more warps in fewer registers (40 to 56 a thread) or two heads to
 // a warp are no faster. Few rows: the launch and two loads in a row.
