@@ -466,7 +466,8 @@ QW3_API int64_t qw3_kv_q4_attn_workspace_bytes(int32_t B, int32_t rows, int32_t 
  * cache, is written as zeros. Lengths are read on the device and taken as at
  * most max_len (<= capacity), which decides how the work is split: an upper
  * bound close to the longest sequence is best. The sums are f32; results are
- * within f32 reassociation error of the exact ones and the same in every call.
+ * within f32 reassociation error of the exact ones, and within 2^-36 of the
+ * sequence's largest |V| for each position, and the same in every call.
  * workspace_dev: 16-byte aligned, qw3_kv_q4_attn_workspace_bytes() or more, of
  * any content, not used by another call until this one has completed (two
  * graphs that may run at once need a workspace each). If a bounded wait in the

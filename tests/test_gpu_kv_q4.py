@@ -438,6 +438,29 @@ def test_attention_ranges(torch, kw):
         check_attention(torch, nh, 2, hd, [300, 45], rows=2, **kw)
 
 
+@pytest.mark.parametrize("hd,rows,n", [(128, 1, 700), (64, 5, 700), (128, 8, 6000)])
+@pytest.mark.parametrize("way", ["up", "down", "late", "steps"])
+def test_attention_scores_that_drift(torch, hd, rows, n, way):
+    """Scores that rise or fall along the sequence by a fraction of a bit a
+    position, that jump in the last tile, or rise in steps; V grows with them."""
+    rng = np.random.default_rng([hd, rows, n])
+    at = np.arange(n)
+    ramp = {"up": at * 0.06, "down": -at * 0.06, "late": np.where(at >= n - 3, 30.0, 0.0),
+            "steps": at // 100 * 3.0}[way]
+    q = rng.standard_normal((rows, 4, hd)).astype(np.float32)
+    k, v = rng.standard_normal((1, n, 2, hd)), rng.standard_normal((1, n, 2, hd)) * 2.0 ** (np.clip(ramp, -20, 20) / 4)[:, None, None]
+    for g in range(2):
+        # along the first query of the group, in units of its scores
+        k[0, :, g] += np.outer(ramp, q[0, 2 * g]) * hd ** 0.5 / (q[0, 2 * g] @ q[0, 2 * g])
+    cap = (n + 31) // 32 * 32
+    cache = new_cache(torch, 1, cap, 2, hd)
+    pad = ((0, 0), (0, cap - n), (0, 0), (0, 0))
+    k, v = put_rows(cache, torch, np.pad(k, pad), np.pad(v, pad))
+    got = cache.attention(cu(torch, q), cu(torch, [n], np.int32), rows=rows).cpu().numpy()
+    want, tol = plain_attention(q, k, v, [n], rows, hd ** -0.5)
+    assert np.all(np.abs(got - want) <= tol)
+
+
 def test_attention_values_of_very_different_sizes(torch):
     """A token with values 10^4 times the others' and a small weight must not
     cost the others their precision."""
