@@ -13,16 +13,15 @@
 // memory, so the logits are read from memory once, and histograms and totals
 // meet through distributed shared memory.
 //
-// Mostly a short list settles a row: a histogram of the threads' largest logits
-// (one addition to a thread) gives a bound that the k-th largest token cannot
-// lie below; the few tokens above it go to the first CTA, which ranks them and
-// finishes the row by itself. With top-p alone the list is taken for k = 192 and
-// serves if it holds p of the row's weight. Else a cut is found by a histogram
-// of all tokens over equal steps of (max l - l) / T (1024 of them, down to
-// weights of 2^-41), whose bins a vocabulary's logits fill evenly, so that few
-// of a warp's additions meet in one word; the cut's bin alone is ranked, or cut
-// further by histograms over its keys until it holds at most kList tokens or
-// equal logits only. What bounds it: the passes over the slices in shared
+// Mostly a short list settles a row, which the first CTA ranks and finishes by
+// itself. For a small top-k a histogram of the threads' largest logits (one
+// addition to a thread) gives a bound that the k-th largest token cannot lie
+// below. Else a cut is found by a histogram of all tokens over equal steps of
+// (max l - l) / T (1024 of them, down to weights of 2^-41), whose bins a
+// vocabulary's logits fill evenly, so that few of a warp's additions meet in one
+// word; if what top-p keeps fits the list, it is listed, else the cut's bin alone
+// is ranked, or cut further by histograms over its keys until it holds at most
+// kList tokens or equal logits only. What bounds it: the passes over the slices in shared
 // memory (some 20 instructions a token where weights are summed) and, for one
 // row, the barriers between them. Measured: one row of 151936 with temperature,
 // top-k 20, top-p 0.95 and min-p 12 us; 64 such rows 32 us, without a cut 32 us
@@ -43,7 +42,6 @@ using u64 = unsigned long long;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2 * kThreads;   // two to a thread
 constexpr int kList = 256;      // tokens that the first CTA ranks
-constexpr int kListP = 192;     // of them, asked for with top-p alone
 constexpr int kMaxCluster = 16;
 constexpr float kOne = 1099511627776.0f;   // 2^40
 
@@ -89,7 +87,7 @@ struct Shared {
     // tokens of a small bin, in the first CTA: key and ~index, weight
     u64 list[kList], list_w[kList];
     u64 peer[kMaxCluster];    // a word from each CTA
-    u64 peer2[kMaxCluster], peer3[kMaxCluster];
+    u64 peer2[kMaxCluster];
     u64 red[2 * kWarps + 2];
     uint32_t n_list;
     int row;           // which row this cluster takes
@@ -182,13 +180,24 @@ __device__ __forceinline__ void clear_histogram(bool weigh, Shared &s) {
     __syncthreads();
 }
 
-// The cluster's histograms added up, in every CTA's tcnt and tw.
+// As many tokens at most as bin b of the first histogram holds, if they weigh w
+// together: its weights lie within 3 percent of each other, and 0.1 percent
+// covers the roundings of bins and weights. (2^20 where weights are so small that
+// being cut to integers counts.)
+__device__ __forceinline__ uint32_t most_in_bin(u64 w, int b) {
+    const float least = exp2f(-kNats / kBins * 1.4426950408889634f * (b + 1.0f)) * (kOne * 0.999f);
+    return w == 0 ? 0u : least < 4096.0f ? 1u << 20 : static_cast<uint32_t>(fminf(static_cast<float>(w) / least, 1048576.0f));
+}
+
+// The cluster's histograms added up, in every CTA's tcnt and tw; with weights
+// tcnt is what most_in_bin says.
 __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Shared &s) {
     if (row.size == 1) {
         __syncthreads();
         for (int i = threadIdx.x; i < kBins; i += kThreads) {
-            s.tcnt[i] = weigh ? 0u : s.cnt[i];
-            s.tw[i] = weigh ? (static_cast<u64>(s.digit[2][i]) << 28) + (static_cast<u64>(s.digit[1][i]) << 14) + s.digit[0][i] : 0;
+            const u64 w = weigh ? (static_cast<u64>(s.digit[2][i]) << 28) + (static_cast<u64>(s.digit[1][i]) << 14) + s.digit[0][i] : 0;
+            s.tcnt[i] = weigh ? most_in_bin(w, i) : s.cnt[i];
+            s.tw[i] = w;
         }
         __syncthreads();
         return;
@@ -215,6 +224,7 @@ __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Share
         if (!weigh) c += __shfl_xor_sync(0xffffffffu, c, o);
         else w += __shfl_xor_sync(0xffffffffu, w, o);
     }
+    if (weigh) c = most_in_bin(w, bin);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t p = 2 * part + h;
@@ -473,10 +483,8 @@ __device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, f
 // Lists the row's largest tokens in the first CTA, the `want` largest among
 // them, where that takes at most kList: a bin that `want` of the threads' largest
 // logits (thread_top) reach holds, with those above it, at least so many tokens.
-// With `weigh`, *all is the row's weight and *listed the list's. Every CTA
-// returns the same.
-__device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 want, bool weigh, u64 *all, u64 *listed,
-                                         Shared &s) {
+// Every CTA returns the same.
+__device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 want, Shared &s) {
     if (threadIdx.x == 0) s.sent = 0u;
     clear_histogram(false, s);
     const int mine = row.bin(thread_top);
@@ -485,17 +493,11 @@ __device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 w
     const Found f = find(false, want, 0, 0, s);
     if (!f.some) return false;
     const uint32_t n_at = dsmem_map(&s.n_list, 0u), list_at = dsmem_map(s.list, 0u);
-    u64 count = 0, sum = 0, in_list = 0;
+    u64 count = 0;
 #pragma unroll 4
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
         const float v = row.l[i];
-        const bool in = row.within(v, f.bin);
-        if (weigh) {
-            const u64 w = fixed_weight(row.weight(v));
-            sum += w;
-            in_list += in ? w : 0;
-        }
-        if (in) {
+        if (row.within(v, f.bin)) {
             ++count;
             // a CTA with more than the list holds (equal logits, say) need not send them
             if (atomicAdd(&s.sent, 1u) < kList) {
@@ -506,27 +508,14 @@ __device__ __forceinline__ bool try_list(const Row &row, float thread_top, u64 w
             }
         }
     }
-    u64 c = count, x = 0, ct, xt, st = 0, lt = 0;
-    scan2(c, x, ct, xt, s);
-    if (weigh) scan2(sum, in_list, st, lt, s);
+    u64 none = 0, total, zero;
+    scan2(count, none, total, zero, s);
     if (row.size > 1) {
-        if (threadIdx.x < row.size) {
-            if (weigh) {
-                remote_st(dsmem_map(&s.peer2[row.rank], threadIdx.x), st);
-                remote_st(dsmem_map(&s.peer3[row.rank], threadIdx.x), lt);
-            }
-        }
-        share(row, s.peer, ct);   // the list has arrived too
-        ct = st = lt = 0;
-        for (uint32_t p = 0; p < row.size; ++p) {
-            ct += s.peer[p];
-            st += weigh ? s.peer2[p] : 0;
-            lt += weigh ? s.peer3[p] : 0;
-        }
+        share(row, s.peer, total);   // the list has arrived too
+        total = 0;
+        for (uint32_t p = 0; p < row.size; ++p) total += s.peer[p];
     }
-    *all = st;
-    *listed = lt;
-    const bool fits = ct <= kList;
+    const bool fits = total <= kList;
     __syncthreads();
     if (!fits && threadIdx.x == 0) s.n_list = 0u;   // a later gather starts over
     return fits;
@@ -645,14 +634,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     // kept: every token with a weight, until a cut says otherwise
     Cut cut{0u, ~0ull, 0, false};
     const bool has_k = k > 0 && k < a.V;
-    if (has_k ? k <= kList : p < 1.0f) {
-        u64 all, listed;
-        const bool fits = try_list(row, top, has_k ? static_cast<u64>(k) : kListP, !has_k, &all, &listed, s);
-        if (fits && (has_k || static_cast<double>(listed) >= static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(all))) {
-            if (row.rank == 0) finish_list(a, b, row, has_k ? static_cast<u64>(k) : 0ull, p, mp, all, s);
-            return;
-        }
-        if (fits && row.rank == 0 && tid == 0) s.n_list = 0u;   // not enough of the weight
+    if (has_k && k <= kList && try_list(row, top, static_cast<u64>(k), s)) {
+        if (row.rank == 0) finish_list(a, b, row, static_cast<u64>(k), p, mp, 0, s);
+        return;
     }
     if (has_k) {
         histogram(row, false, s, [&](float v) {
@@ -688,6 +672,11 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
         target = target < 1 ? 1 : (target < total ? target : total);
         __syncthreads();
         const Found f = find(true, target, 0, 0, s);
+        if (f.above_c + f.n <= kList) {
+            gather(row, s, [&](float v) { return row.within(v, f.bin) && logit_key(v) >= cut.key; });
+            if (row.rank == 0) finish_list(a, b, row, 0, p, mp, total, s);
+            return;
+        }
         const Cut c = cut_in_bin(row, f, true, target, cut.key, s);
         if (c.key > cut.key) cut = c;
         else if (c.ties < cut.ties) cut = Cut{c.key, c.ties, 0, true};
