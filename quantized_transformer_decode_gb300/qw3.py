@@ -9,6 +9,7 @@ libqw3.so, and a missing library is an error, never a fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from pathlib import Path
 from typing import Iterable, Optional, Sequence
@@ -442,10 +443,14 @@ def _ptr(t):
 
 
 def _rows_of(t, name: str):
-    """(rows, stride) of a 2-d tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    """(rows, width, stride) of a 2-d tensor whose rows are contiguous."""
+    if t.dim() != 2:
         raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a 2-d tensor with contiguous rows is wanted")
-    return t.shape[0], t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    rows, width = t.shape
+    stride, step = t.stride()
+    if width > 1 and step != 1:
+        raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a 2-d tensor with contiguous rows is wanted")
+    return rows, width, stride if rows > 1 else max(width, stride)
 
 
 def _on_current_stream(index: int, call, *args) -> None:
@@ -463,6 +468,11 @@ def _on_current_stream(index: int, call, *args) -> None:
         _check(rc)
 
 
+# functions of their sizes alone, asked for in every call
+_kv_q4_bytes = functools.lru_cache(maxsize=256)(qw3_kv_q4_bytes)
+_kv_q4_attn_workspace_bytes = functools.lru_cache(maxsize=1024)(qw3_kv_q4_attn_workspace_bytes)
+
+
 class KVCacheQ4:
     """A 4-bit KV cache of `slots` sequences (qw3_kv_q4): rows appended from
     raw q/k/v projections, read back, attended over. Every call runs on torch's
@@ -470,7 +480,7 @@ class KVCacheQ4:
 
     def __init__(self, slots: int, capacity: int, n_kv_heads: int, head_dim: int, data=None, device="cuda"):
         torch = _torch()
-        n = qw3_kv_q4_bytes(slots, capacity, n_kv_heads, head_dim)
+        n = _kv_q4_bytes(slots, capacity, n_kv_heads, head_dim)
         if n < 0:
             raise Qw3Error(QW3_ERR_SHAPE, "slots >= 1, capacity % 32 == 0, 1 to 64 kv heads, head_dim 64 or 128")
         if data is None:
@@ -481,8 +491,8 @@ class KVCacheQ4:
         self.slots, self.capacity, self.n_kv_heads, self.head_dim = slots, capacity, n_kv_heads, head_dim
         self.c = Qw3KvQ4(data.data_ptr(), slots, capacity, n_kv_heads, head_dim)
 
-    def _check_places(self, M, slots, pos):
-        _on(self.index, _torch().int32, "slots and pos", slots, pos)
+    def _check_places(self, torch, M, slots, pos):
+        _on(self.index, torch.int32, "slots and pos", slots, pos)
         if (slots is not None and slots.numel() != M) or (pos is not None and pos.numel() != M):
             raise Qw3Error(QW3_ERR_SHAPE, f"slots and pos hold one place for each of {M} rows")
 
@@ -494,8 +504,8 @@ class KVCacheQ4:
         to (slots[i], pos[i]), int32 tensors, or to (slot, first + i). A row
         outside the cache is not cached and its queries are zero."""
         torch = _torch()
-        M, stride = _rows_of(qkv, "qkv")
-        hd, width = self.head_dim, qkv.shape[1]
+        M, width, stride = _rows_of(qkv, "qkv")
+        hd = self.head_dim
         n_heads = width // hd - 2 * self.n_kv_heads
         if qkv.dtype is not torch.float32 or qkv.get_device() != self.index or width % hd or n_heads < 1:
             raise Qw3Error(QW3_ERR_SHAPE, "qkv: f32 rows of n_heads + 2 n_kv_heads heads on the cache's device")
@@ -504,7 +514,7 @@ class KVCacheQ4:
             raise Qw3Error(QW3_ERR_SHAPE, "q_norm and k_norm hold head_dim values, rope capacity * head_dim")
         if status is not None:
             _on(self.index, torch.int32, "status", status)
-        self._check_places(M, slots, pos)
+        self._check_places(torch, M, slots, pos)
         q = torch.empty((M, n_heads, hd), dtype=torch.float32, device=self.device)
         _on_current_stream(self.index, lib().qw3_kv_q4_append, self.c, qkv.data_ptr(), M, stride, n_heads,
                            q_norm.data_ptr(), k_norm.data_ptr(), eps, rope.data_ptr(), _ptr(slots), slot, _ptr(pos),
@@ -519,7 +529,7 @@ class KVCacheQ4:
         M = n if n is not None else slots.numel() if slots is not None else pos.numel() if pos is not None else -1
         if M < 0:
             raise Qw3Error(QW3_ERR_INVALID_ARG, "read needs slots, pos or n")
-        self._check_places(M, slots, pos)
+        self._check_places(torch, M, slots, pos)
         shape = (M, self.n_kv_heads, self.head_dim)
         k = torch.empty(shape, dtype=torch.float32, device=self.device)
         v = torch.empty(shape, dtype=torch.float32, device=self.device)
@@ -546,16 +556,15 @@ class KVCacheQ4:
             raise Qw3Error(QW3_ERR_SHAPE, "more sequences than slots")
         max_len = self.capacity if max_len is None else max_len
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=self.device)
-        L = lib()
+            out = torch.empty_like(q)
         if workspace is None:
-            need = L.qw3_kv_q4_attn_workspace_bytes(B, rows, n_heads, self.n_kv_heads, hd, max_len)
+            need = _kv_q4_attn_workspace_bytes(B, rows, n_heads, self.n_kv_heads, hd, max_len)
             if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         else:
             _on(self.index, torch.uint8, "workspace", workspace)
             need = workspace.numel()
-        _on_current_stream(self.index, L.qw3_kv_q4_attn, self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots),
+        _on_current_stream(self.index, lib().qw3_kv_q4_attn, self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots),
                            lens.data_ptr(), B, rows, max_len, hd ** -0.5 if scale is None else scale, out.data_ptr(),
                            n_heads * hd, _ptr(workspace), need, _ptr(status))
         return out
@@ -567,7 +576,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stat
     [B]). temperature, top_p, min_p: f32 [B]; top_k: int32 [B]; each may be
     left out."""
     torch = _torch()
-    B, stride = _rows_of(logits, "logits")
+    B, V, stride = _rows_of(logits, "logits")
     dev = logits.get_device()
     if logits.dtype is not torch.float32 or dev < 0:
         raise Qw3Error(QW3_ERR_INVALID_ARG, "logits: a CUDA f32 tensor is wanted")
@@ -578,7 +587,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stat
             raise Qw3Error(QW3_ERR_SHAPE, f"one setting and one number for each of {B} rows are wanted")
     token = torch.empty(B, dtype=torch.int32, device=logits.device)
     prob = torch.empty(B, dtype=torch.float32, device=logits.device)
-    _on_current_stream(dev, lib().qw3_sample, logits.data_ptr(), stride, B, logits.shape[1], _ptr(temperature),
+    _on_current_stream(dev, lib().qw3_sample, logits.data_ptr(), stride, B, V, _ptr(temperature),
                        _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(), token.data_ptr(), prob.data_ptr(),
                        _ptr(status))
     return token, prob
