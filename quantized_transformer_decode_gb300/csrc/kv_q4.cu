@@ -684,10 +684,12 @@ __device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
 // Workspace: two partial results of W columns for each CTA (of the unit that
 // its share begins inside, and of the one that it ends inside), then the first
 // and the last CTA of each unit.
-// CLUSTER: no workspace; grid (csize, units), clusters along x.
-template <int HD, int W, bool CLUSTER>
-__global__ void __launch_bounds__((CLUSTER ? kQ4ClusterWarps : kQ4Warps) * 32, CLUSTER ? (W <= 4 ? 2 : 1) : q4_per_sm(HD, W))
+// CL: clusters of CTAs, CL to an SM (0: blocks dealt out); no workspace; grid
+// (csize, units), clusters along x.
+template <int HD, int W, int CL>
+__global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? CL : q4_per_sm(HD, W))
     k_kv_q4_attn(KvQ4AttnArgs a, int cgroups, int2 *owners) {
+    constexpr bool CLUSTER = CL > 0;
     constexpr int NW = CLUSTER ? kQ4ClusterWarps : kQ4Warps, kStep = NW * kQ4Tile;
     constexpr int NB = HD / 32, NT = q4_ops(W);
     constexpr int DUP = W <= 4 ? 4 / W : 1;          // blocks that share an operand
@@ -1274,9 +1276,9 @@ cudaError_t launch_kv_q4_read(const KvQ4 &c, int hd, const KvQ4Rows &rows, int M
 namespace {
 
 // How a call is split: width class of the columns, column groups; CTAs to a
-// unit's cluster, or (0) CTAs to deal the blocks to.
+// unit's cluster and to an SM, or (0) CTAs to deal the blocks to.
 struct Q4Plan {
-    int W, cgroups, csize, ctas;
+    int W, cgroups, csize = 0, per_sm = 0, ctas;
     bool whole;   // no unit is cut: no workspace, no second kernel
 };
 
@@ -1287,15 +1289,22 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int hd, int max_len) {
     p.cgroups = (cols + p.W - 1) / p.W;
     const int64_t units = static_cast<int64_t>(std::max(B, 1)) * nkv * p.cgroups;
     const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
-    // Clusters while all of them fit at once (two CTAs to an SM, one at W = 8)
-    // and a warp has eight tiles at most (against dealing out blocks, with its
-    // second kernel: 1 x 517 8.3 us and 12.4, 1 x 8317 15.4 and 20.6, 16 x 2000
-    // 18.5 and 21.8, 1 x 32000 28.7 and 35.6).
-    const int64_t fit_cluster = p.W <= 4 ? 304 : 152;
+    // Clusters while all of them fit at once and a warp has eight tiles at most
+    // (against dealing out blocks, with its second kernel: 1 x 517 8.3 us and 12.4,
+    // 1 x 8317 14.7 and 20.6, 1 x 32000 28.7 and 35.6): with an SM to each CTA, whose
+    // threads then have 255 registers, else two CTAs to an SM in 128 (16 x 2000 16.4
+    // us against 18.5). The sizes are powers of two; a GPC of 18 or 20 SMs holds one
+    // or two clusters of 8 and one of 16 at most.
+    constexpr int kFit[2][5] = {{152, 76, 36, 15, 0}, {304, 152, 74, 36, 14}};
     const int64_t need = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4ClusterWarps * kQ4Tile - 1) / (kQ4ClusterWarps * kQ4Tile));
-    int csize = 1;
-    while (csize < kQ4MaxCluster && csize < need && units * csize * 2 <= fit_cluster) csize *= 2;
-    p.csize = units * csize <= fit_cluster && need <= 8ll * csize ? csize : 0;
+    for (int per_sm = 1; per_sm <= (p.W <= 4 ? 2 : 1) && !p.csize; ++per_sm) {
+        int log2 = 0;
+        while (log2 < 4 && (1 << log2) < need && units <= kFit[per_sm - 1][log2 + 1]) ++log2;
+        if (units <= kFit[per_sm - 1][log2] && need <= 8ll << log2) {
+            p.csize = 1 << log2;
+            p.per_sm = per_sm;
+        }
+    }
     // the CTAs that fit at once; for little work two blocks to each
     const int fit = 152 * q4_per_sm(hd, p.W);
     p.ctas = static_cast<int>(std::min<int64_t>(fit, std::max(units, units * ((most + 1) / 2))));
@@ -1310,21 +1319,36 @@ size_t q4_parts_bytes(const Q4Plan &p, int hd) {
 template <int HD, int W>
 constexpr size_t q4_attn_smem(int warps) { return static_cast<size_t>(warps) * kQ4Stages * Q4Stage<HD>::bytes; }
 
+template <int HD, int W, int CL>
+cudaError_t configure_q4_clusters() {
+    cudaError_t e = cudaFuncSetAttribute(k_kv_q4_attn<HD, W, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(q4_attn_smem<HD, W>(kQ4ClusterWarps)));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_q4_attn<HD, W, CL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+}
+
 template <int HD, int W>
 cudaError_t configure_q4_attn() {
-    cudaError_t e = cudaFuncSetAttribute(k_kv_q4_attn<HD, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(q4_attn_smem<HD, W>(kQ4ClusterWarps)));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_q4_attn<HD, W, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = configure_q4_clusters<HD, W, 1>();
+    if constexpr (W <= 4)
+        if (e == cudaSuccess) e = configure_q4_clusters<HD, W, 2>();
     return e;
+}
+
+template <int HD, int W, int CL>
+cudaError_t launch_q4_clusters(const KvQ4AttnArgs &a, const Q4Plan &p, bool pdl, cudaStream_t s) {
+    return launch_pdl(pdl, k_kv_q4_attn<HD, W, CL>, dim3(p.csize, static_cast<unsigned>(a.B) * a.c.nkv * p.cgroups),
+                      kQ4ClusterWarps * 32, q4_attn_smem<HD, W>(kQ4ClusterWarps), p.csize, s, a, p.cgroups,
+                      static_cast<int2 *>(nullptr));
 }
 
 template <int HD, int W>
 cudaError_t launch_q4_attn_w(const KvQ4AttnArgs &a, const Q4Plan &p, int2 *owners, bool pdl, cudaStream_t s) {
     static_assert(q4_attn_smem<HD, W>(kQ4Warps) <= 40 * 1024, "fits without an opt-in");
-    if (p.csize)
-        return launch_pdl(pdl, k_kv_q4_attn<HD, W, true>, dim3(p.csize, static_cast<unsigned>(a.B) * a.c.nkv * p.cgroups),
-                          kQ4ClusterWarps * 32, q4_attn_smem<HD, W>(kQ4ClusterWarps), p.csize, s, a, p.cgroups, owners);
-    return launch_pdl(pdl, k_kv_q4_attn<HD, W, false>, dim3(p.ctas), kQ4Warps * 32, q4_attn_smem<HD, W>(kQ4Warps), 1, s, a,
+    if (p.per_sm == 1) return launch_q4_clusters<HD, W, 1>(a, p, pdl, s);
+    if constexpr (W <= 4)
+        if (p.per_sm == 2) return launch_q4_clusters<HD, W, 2>(a, p, pdl, s);
+    return launch_pdl(pdl, k_kv_q4_attn<HD, W, 0>, dim3(p.ctas), kQ4Warps * 32, q4_attn_smem<HD, W>(kQ4Warps), 1, s, a,
                       p.cgroups, owners);
 }
 
