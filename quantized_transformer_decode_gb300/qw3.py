@@ -453,19 +453,15 @@ def _rows_of(t, name: str):
     return rows, width, stride if rows > 1 else max(width, stride)
 
 
-def _on_current_stream(index: int, call, *args) -> None:
-    """call(*args, stream) with device `index` current and torch's current stream on it."""
-    torch = _torch()
-    # the stream's handle itself: a Stream object around it costs a short call
-    # 2 of its 13 us
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
-        rc = call(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            rc = call(*args, stream)
-    if rc:
-        _check(rc)
+def _stream_on(torch, index: int) -> int:
+    """The handle of torch's current stream on device `index` (a Stream object
+    around it costs a short call 2 of its 13 us)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _elsewhere(torch, index: int) -> bool:
+    """Whether another device than `index` is current: a call launches on the current one."""
+    return torch._C._cuda_getDevice() != index
 
 
 # functions of their sizes alone, asked for in every call
@@ -504,6 +500,9 @@ class KVCacheQ4:
         to (slots[i], pos[i]), int32 tensors, or to (slot, first + i). A row
         outside the cache is not cached and its queries are zero."""
         torch = _torch()
+        if _elsewhere(torch, self.index):
+            with torch.cuda.device(self.index):
+                return self.append(qkv, q_norm, k_norm, eps, rope, slots, pos, slot, first, status)
         M, width, stride = _rows_of(qkv, "qkv")
         hd = self.head_dim
         n_heads = width // hd - 2 * self.n_kv_heads
@@ -516,9 +515,11 @@ class KVCacheQ4:
             _on(self.index, torch.int32, "status", status)
         self._check_places(torch, M, slots, pos)
         q = torch.empty((M, n_heads, hd), dtype=torch.float32, device=self.device)
-        _on_current_stream(self.index, lib().qw3_kv_q4_append, self.c, qkv.data_ptr(), M, stride, n_heads,
-                           q_norm.data_ptr(), k_norm.data_ptr(), eps, rope.data_ptr(), _ptr(slots), slot, _ptr(pos),
-                           first, q.data_ptr(), n_heads * hd, _ptr(status))
+        rc = lib().qw3_kv_q4_append(self.c, qkv.data_ptr(), M, stride, n_heads, q_norm.data_ptr(), k_norm.data_ptr(),
+                                    eps, rope.data_ptr(), _ptr(slots), slot, _ptr(pos), first, q.data_ptr(),
+                                    n_heads * hd, _ptr(status), _stream_on(torch, self.index))
+        if rc:
+            _check(rc)
         return q
 
     def read(self, slots=None, pos=None, slot: int = 0, first: int = 0, n: Optional[int] = None):
@@ -526,6 +527,9 @@ class KVCacheQ4:
         as in append, M from slots or pos, else n. Rows outside the cache are
         zero."""
         torch = _torch()
+        if _elsewhere(torch, self.index):
+            with torch.cuda.device(self.index):
+                return self.read(slots, pos, slot, first, n)
         M = n if n is not None else slots.numel() if slots is not None else pos.numel() if pos is not None else -1
         if M < 0:
             raise Qw3Error(QW3_ERR_INVALID_ARG, "read needs slots, pos or n")
@@ -533,8 +537,10 @@ class KVCacheQ4:
         shape = (M, self.n_kv_heads, self.head_dim)
         k = torch.empty(shape, dtype=torch.float32, device=self.device)
         v = torch.empty(shape, dtype=torch.float32, device=self.device)
-        _on_current_stream(self.index, lib().qw3_kv_q4_read, self.c, M, _ptr(slots), slot, _ptr(pos), first,
-                           k.data_ptr(), v.data_ptr())
+        rc = lib().qw3_kv_q4_read(self.c, M, _ptr(slots), slot, _ptr(pos), first, k.data_ptr(), v.data_ptr(),
+                                  _stream_on(torch, self.index))
+        if rc:
+            _check(rc)
         return k, v
 
     def attention(self, q, lens, rows: int = 1, slots=None, max_len: Optional[int] = None,
@@ -545,6 +551,9 @@ class KVCacheQ4:
         (the capacity where it is not given). scale: 1 / sqrt(head_dim) where it
         is not given. workspace: a uint8 tensor to use in place of a new one."""
         torch = _torch()
+        if _elsewhere(torch, self.index):
+            with torch.cuda.device(self.index):
+                return self.attention(q, lens, rows, slots, max_len, scale, out, workspace, status)
         B, hd, n_heads = lens.numel(), self.head_dim, q.shape[1] if q.dim() == 3 else 0
         _on(self.index, torch.float32, "q and out", q, out)
         _on(self.index, torch.int32, "lens, slots and status", lens, slots, status)
@@ -564,9 +573,11 @@ class KVCacheQ4:
         else:
             _on(self.index, torch.uint8, "workspace", workspace)
             need = workspace.numel()
-        _on_current_stream(self.index, lib().qw3_kv_q4_attn, self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots),
-                           lens.data_ptr(), B, rows, max_len, hd ** -0.5 if scale is None else scale, out.data_ptr(),
-                           n_heads * hd, _ptr(workspace), need, _ptr(status))
+        rc = lib().qw3_kv_q4_attn(self.c, q.data_ptr(), n_heads * hd, n_heads, _ptr(slots), lens.data_ptr(), B, rows,
+                                  max_len, hd ** -0.5 if scale is None else scale, out.data_ptr(), n_heads * hd,
+                                  _ptr(workspace), need, _ptr(status), _stream_on(torch, self.index))
+        if rc:
+            _check(rc)
         return out
 
 
@@ -585,11 +596,15 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stat
     for t in (u, temperature, top_k, top_p, min_p):
         if t is not None and t.numel() != B:
             raise Qw3Error(QW3_ERR_SHAPE, f"one setting and one number for each of {B} rows are wanted")
+    if _elsewhere(torch, dev):
+        with torch.cuda.device(dev):
+            return sample(logits, u, temperature, top_k, top_p, min_p, status)
     token = torch.empty(B, dtype=torch.int32, device=logits.device)
     prob = torch.empty(B, dtype=torch.float32, device=logits.device)
-    _on_current_stream(dev, lib().qw3_sample, logits.data_ptr(), stride, B, V, _ptr(temperature),
-                       _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(), token.data_ptr(), prob.data_ptr(),
-                       _ptr(status))
+    rc = lib().qw3_sample(logits.data_ptr(), stride, B, V, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                          u.data_ptr(), token.data_ptr(), prob.data_ptr(), _ptr(status), _stream_on(torch, dev))
+    if rc:
+        _check(rc)
     return token, prob
 
 

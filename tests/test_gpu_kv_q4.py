@@ -590,6 +590,45 @@ def test_captured_and_replayed(torch):
         assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+def test_calls_while_another_device_is_current(torch, monkeypatch):
+    """The calls go through a switch to the cache's device with all they were
+    given (the switch stands in for a second device)."""
+    from quantized_transformer_decode_gb300 import qw3
+    rng = np.random.default_rng(41)
+    nh, nkv, hd, cap = 4, 2, 64, 96
+    w = [cu(torch, (1 + 0.1 * rng.standard_normal(hd)).astype(np.float32)) for _ in range(2)]
+    rope = cu(torch, rope_table(cap, hd))
+    x = cu(torch, rng.standard_normal((5, (nh + 2 * nkv) * hd)).astype(np.float32))
+    lens, slots = cu(torch, [7], np.int32), cu(torch, [1], np.int32)
+    logits = cu(torch, rng.standard_normal((3, 500)).astype(np.float32))
+    one = lambda v, d=np.float32: cu(torch, np.full(3, v), d)  # noqa: E731
+
+    def calls():
+        status = cu(torch, [0], np.int32)
+        cache = new_cache(torch, 2, cap, nkv, hd)
+        q = cache.append(x, *w, EPS, rope, slot=1, first=2, status=status)
+        cache.append(x[:2], *w, EPS, rope, slots=cu(torch, [1, 1], np.int32), pos=cu(torch, [0, 1], np.int32))
+        rows = cache.read(slot=1, first=3, n=4) + cache.read(cu(torch, [1, 0], np.int32), cu(torch, [2, 95], np.int32))
+        out = torch.empty_like(q[:2])
+        ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+        got = cache.attention(q[3:], lens, 2, slots, 64, 0.3, out, ws, status)
+        token, prob = qw3.sample(logits, one(0.7), one(0.8), one(50, np.int32), one(0.9), one(0.01), status)
+        assert got is out and int(status) == 0
+        return (q, *rows, out, token, prob)
+
+    want = calls()
+    seen = []
+
+    def elsewhere(torch, index):
+        seen.append(index)
+        return len(seen) % 2 == 1   # asked again after the switch
+
+    monkeypatch.setattr(qw3, "_elsewhere", elsewhere)
+    for a, b in zip(want, calls()):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))   # the unwritten row read is NaN
+    assert seen == [0] * 12
+
+
 def test_wrapper_refusals(torch):
     from quantized_transformer_decode_gb300.qw3 import KVCacheQ4, Qw3Error
     cache = KVCacheQ4(2, 64, 2, 64)
