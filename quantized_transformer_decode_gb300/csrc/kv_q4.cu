@@ -668,19 +668,6 @@ __device__ __forceinline__ int64_t q4_div(int64_t a, unsigned b) {
     return a >> 32 ? a / b : static_cast<int64_t>(static_cast<unsigned>(a) / b);
 }
 
-// Sum over the block's threads; red: kQ4Warps values.
-__device__ __forceinline__ int64_t q4_sum(int64_t v, int64_t *red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int w = 0; w < kQ4Warps; ++w) v += red[w];
-    return v;
-}
-
 // Workspace: two partial results of W columns for each CTA (of the unit that
 // its share begins inside, and of the one that it ends inside), then the first
 // and the last CTA of each unit.
@@ -722,29 +709,17 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
     const uint64_t policy = policy_evict_first();
     pdl_wait();
 
-    // ---- this CTA's share [at, stop) of the blocks
-    int64_t at = 0, stop = 1;
-    if constexpr (!CLUSTER) {
-        int64_t mine = 0;
-#pragma unroll 4
-        for (int i = tid; i < a.B; i += NW * 32) mine += q4_blocks(a, i) + kQ4UnitCost;
-        const int64_t all = a.B > 1 ? q4_sum(mine, s_red) : q4_blocks(a, 0) + kQ4UnitCost;
-        // no share is empty: the join counts on every CTA between a unit's first and last
-        const int64_t total = all * U;
-        const unsigned P = static_cast<unsigned>(min(static_cast<int64_t>(gridDim.x), total));
-        if (blockIdx.x >= P) return;
-        const int64_t each = q4_div(total, P), more = total - each * P;
-        at = each * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), more);
-        stop = at + each + (blockIdx.x < more ? 1 : 0);
-    }
-    // its first sequence: sums of 128 sequences at a time, then one by one
+    // ---- this CTA's share [at, stop) of the blocks, its first sequence b and the
+    // cost (of one unit) of the sequences below that
+    int64_t at = 0, stop = 1, before = 0;
     int b = CLUSTER ? static_cast<int>(blockIdx.y) / U : 0;
-    int64_t before = 0;   // cost of the sequences below b (of one unit)
-    if (!CLUSTER && a.B > 1) {
-        const int64_t want = q4_div(at, static_cast<unsigned>(U));
-        for (int b0 = 0; b0 < a.B; b0 += NW * 32) {
-            const int64_t n = b0 + tid < a.B ? q4_blocks(a, b0 + tid) + kQ4UnitCost : 0;
-            int64_t run = n;
+    if constexpr (!CLUSTER) {
+        // costs of kQ4Warps * 32 sequences from b0 on: this thread's, their sum up to
+        // and with it, and all of them
+        int64_t n = 0, run = 0, sum = 0;
+        const auto scan = [&](int b0) {
+            n = b0 + tid < a.B ? q4_blocks(a, b0 + tid) + kQ4UnitCost : 0;
+            run = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t x = __shfl_up_sync(0xffffffffu, run, o);
@@ -753,17 +728,34 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
             __syncthreads();
             if (lane == 31) s_red[warp] = run;
             __syncthreads();
-            int64_t lead = before, sum = 0;
+            sum = 0;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                if (w < warp) lead += s_red[w];
+                if (w < warp) run += s_red[w];
                 sum += s_red[w];
             }
+        };
+        constexpr int kAtOnce = NW * 32;
+        int64_t all = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kAtOnce) {
+            scan(b0);
+            all += sum;
+        }
+        // no share is empty: the join counts on every CTA between a unit's first and last
+        const int64_t total = all * U;
+        const unsigned P = static_cast<unsigned>(min(static_cast<int64_t>(gridDim.x), total));
+        if (blockIdx.x >= P) return;
+        const int64_t each = q4_div(total, P), more = total - each * P;
+        at = each * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), more);
+        stop = at + each + (blockIdx.x < more ? 1 : 0);
+        const int64_t want = q4_div(at, static_cast<unsigned>(U));
+        for (int b0 = 0; b0 < a.B; b0 += kAtOnce) {
+            if (a.B > kAtOnce) scan(b0);
             if (want < before + sum) {
                 __syncthreads();
-                if (n > 0 && lead + run - n <= want && want < lead + run) {
+                if (n > 0 && before + run - n <= want && want < before + run) {
                     s_red[0] = b0 + tid;
-                    s_red[1] = lead + run - n;
+                    s_red[1] = before + run - n;
                 }
                 __syncthreads();
                 b = static_cast<int>(s_red[0]);
