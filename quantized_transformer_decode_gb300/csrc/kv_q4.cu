@@ -1194,28 +1194,50 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
 }
 
 // Joins the partial results of the columns whose unit more than one CTA worked
-// on: a CTA per (sequence, kv head, column), a thread per dimension.
-template <int HD>
-__global__ void __launch_bounds__(HD) k_kv_q4_join(KvQ4AttnArgs a, int cgroups, int W, const int2 *owners) {
+// on: a CTA per (sequence, kv head, column), a thread per dimension; Y rows of
+// threads where a unit's results are many, each taking every Y-th.
+template <int HD, int Y>
+__global__ void __launch_bounds__(HD * Y) k_kv_q4_join(KvQ4AttnArgs a, int cgroups, int W, const int2 *owners) {
     constexpr int PS = q4_part<HD>();
+    __shared__ float s_part[Y][PS];
     pdl_wait();
     const int G = a.nh / a.c.nkv, cols = G * a.rows, U = a.c.nkv * cgroups;
-    const int cc = blockIdx.x % cols, g = blockIdx.x / cols % a.c.nkv, b = blockIdx.x / (cols * a.c.nkv), d = threadIdx.x;
+    const int cc = blockIdx.x % cols, g = blockIdx.x / cols % a.c.nkv, b = blockIdx.x / (cols * a.c.nkv);
+    const int d = threadIdx.x % HD, y = threadIdx.x / HD;
     const int2 own = owners[static_cast<size_t>(b) * U + g * cgroups + cc / W];
     if (own.x == own.y) return;
     // the first CTA ended inside the unit (its second result), the others began inside it
     const auto part = [&](int i) { return a.ws + (static_cast<size_t>(i) * 2 + (i == own.x ? 1 : 0)) * W * PS + cc % W * PS; };
     float M = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll 8
-    for (int i = own.x; i <= own.y; ++i) M = fmaxf(M, part(i)[HD]);
+    for (int i = own.x + y; i <= own.y; i += Y) M = fmaxf(M, part(i)[HD]);
     if (M != -INFINITY)
 #pragma unroll 8
-        for (int i = own.x; i <= own.y; ++i) {
+        for (int i = own.x + y; i <= own.y; i += Y) {
             const float *p = part(i);
             const float f = exp2_f32(p[HD] - M);
             l = fmaf(p[HD + 1], f, l);
             o = fmaf(p[d], f, o);
         }
+    if constexpr (Y > 1) {
+        s_part[y][d] = o;
+        if (d == 0) {
+            s_part[y][HD] = M;
+            s_part[y][HD + 1] = l;
+        }
+        __syncthreads();
+        if (y > 0) return;
+#pragma unroll
+        for (int k = 1; k < Y; ++k) M = fmaxf(M, s_part[k][HD]);
+        l = o = 0.0f;
+        if (M != -INFINITY)
+#pragma unroll
+            for (int k = 0; k < Y; ++k) {
+                const float f = exp2_f32(s_part[k][HD] - M);
+                l = fmaf(s_part[k][HD + 1], f, l);
+                o = fmaf(s_part[k][d], f, o);
+            }
+    }
     a.out[(static_cast<int64_t>(b) * a.rows + cc / G) * a.out_stride + static_cast<int64_t>(g * G + cc % G) * HD + d] =
         l == 0.0f ? 0.0f : o / l;
 }
@@ -1355,8 +1377,13 @@ cudaError_t launch_q4_attn_hd(const KvQ4AttnArgs &a, const Q4Plan &p, bool pdl, 
         case 8: e = launch_q4_attn_w<HD, 8>(a, p, owners, pdl, s); break;
     }
     if (e != cudaSuccess || p.whole) return e;
-    return launch_pdl(pdl, k_kv_q4_join<HD>, dim3(static_cast<unsigned>(a.nh) * a.rows * a.B), HD, 0, 1, s, a, p.cgroups, p.W,
-                      static_cast<const int2 *>(owners));
+    // a unit's results, eight at a time where there are many: 1 x 100000 with 8/1
+    // heads 31 us against 90, 4 x 20000 with 32/8 (14 results) 33 against 37, but 1 x
+    // 8000 with 16 rows (5 results) 37 against 35
+    const unsigned joins = static_cast<unsigned>(a.nh) * a.rows * a.B;
+    const bool many = p.ctas >= 8ll * a.B * a.c.nkv * p.cgroups;
+    return launch_pdl(pdl, many ? k_kv_q4_join<HD, 8> : k_kv_q4_join<HD, 1>, dim3(joins), many ? HD * 8 : HD, 0, 1, s, a,
+                      p.cgroups, p.W, static_cast<const int2 *>(owners));
 }
 
 }  // namespace

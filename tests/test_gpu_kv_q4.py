@@ -383,6 +383,15 @@ def test_attention_long_split(torch, rows):
     check_attention(torch, 2, 1, 64, [9000, 17, 4096], rows=rows)
 
 
+@pytest.mark.parametrize("nh,nkv,hd,lens,rows", [(8, 1, 128, [40000], 1), (4, 1, 64, [36001], 3), (2, 2, 64, [33333, 0, 1], 1),
+                                                 (4, 1, 128, [34000, 20000], 8)])
+def test_attention_results_of_many_ctas(torch, nh, nkv, hd, lens, rows):
+    """A few long sequences, whose units more CTAs work on than join in one go."""
+    check_attention(torch, nh, nkv, hd, lens, rows=rows)
+    if rows == 1:
+        check_attention(torch, nh, nkv, hd, lens, rows=rows, spread=6.0)
+
+
 def test_attention_batch_of_many_lengths(torch):
     rng = np.random.default_rng(5)
     lens = [int(n) for n in rng.integers(0, 400, 40)]
