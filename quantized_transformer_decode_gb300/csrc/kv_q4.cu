@@ -1303,18 +1303,20 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int hd, int max_len) {
     p.cgroups = (cols + p.W - 1) / p.W;
     const int64_t units = static_cast<int64_t>(std::max(B, 1)) * nkv * p.cgroups;
     const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
-    // Clusters while all of them fit at once and a warp has eight tiles at most
-    // (against dealing out blocks, with its second kernel: 1 x 517 8.3 us and 12.4,
-    // 1 x 8317 14.7 and 20.6, 1 x 32000 28.7 and 35.6): with an SM to each CTA, whose
-    // threads then have 255 registers, else two CTAs to an SM in 128 (16 x 2000 16.4
-    // us against 18.5). The sizes are powers of two; a GPC of 18 or 20 SMs holds one
-    // or two clusters of 8 and one of 16 at most.
+    // Clusters while all of them fit at once (against dealing out blocks, with its
+    // second kernel: 1 x 517 8.3 us and 12.4, 4 x 8000 19.2 and 22.5): with an SM to
+    // each CTA, whose threads then have 255 registers, else two CTAs to an SM in 128
+    // (16 x 2000 16.4 us against 18.5). A warp takes eight tiles at most, five where
+    // the clusters leave room for more CTAs (1 x 8317 14.4 us against 16.4; but
+    // 1 x 32000 27.6 in clusters, 22.6 dealt out). The sizes are powers of two; a GPC of 18 or 20
+    // SMs holds one or two clusters of 8 and one of 16 at most.
     constexpr int kFit[2][5] = {{152, 76, 36, 15, 0}, {304, 152, 74, 36, 14}};
     const int64_t need = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4ClusterWarps * kQ4Tile - 1) / (kQ4ClusterWarps * kQ4Tile));
     for (int per_sm = 1; per_sm <= (p.W <= 4 ? 2 : 1) && !p.csize; ++per_sm) {
         int log2 = 0;
         while (log2 < 4 && (1 << log2) < need && units <= kFit[per_sm - 1][log2 + 1]) ++log2;
-        if (units <= kFit[per_sm - 1][log2] && need <= 8ll << log2) {
+        const int64_t tiles = units << log2 >= (per_sm == 1 ? 96 : 240) ? 8 : 5;
+        if (units <= kFit[per_sm - 1][log2] && need <= tiles << log2) {
             p.csize = 1 << log2;
             p.per_sm = per_sm;
         }
