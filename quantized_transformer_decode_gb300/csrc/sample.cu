@@ -551,6 +551,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     const int size = static_cast<int>(gridDim.x);   // one cluster along x
     Row row;
     row.rank = size > 1 ? cluster_rank() : 0u;
+    // a CTA's shared memory may be written by its peers once it has started: waited
+    // for at the first share below, behind the slice's load
+    if (size > 1) cluster_arrive_release();
     row.size = static_cast<uint32_t>(size);
     const int b = reorder ? row_of(a, static_cast<int>(gridDim.y), static_cast<int>(blockIdx.y), s) : static_cast<int>(blockIdx.y);
     row.base = static_cast<int>(row.rank) * slice;
@@ -601,6 +604,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     }
     u64 best = block_max(nan ? ~0u : logit_key(top), s);
     if (size > 1) {
+        __syncwarp();
+        cluster_wait_acquire();   // every CTA of the cluster runs
         share(row, s.peer, best);
         for (int p = 0; p < size; ++p) best = s.peer[p] > best ? s.peer[p] : best;
     }

@@ -201,6 +201,24 @@ def test_lists_that_nearly_or_just_overflow(torch):
     check(torch, np.array(rows), rng.random(len(rows)), least=0.7, top_k=k, top_p=p)
 
 
+@pytest.mark.parametrize("V", [8193, 40003, 151936])
+def test_the_largest_logit_in_any_slice(torch, V):
+    """Many clusters in several waves, whose CTAs start at different times: each
+    CTA's largest logit reaches its peers, wherever the row's largest lies."""
+    rng = np.random.default_rng(V)
+    B = 600
+    at = np.concatenate([[0, V - 1], rng.integers(0, V, B - 2)])
+    x = torch.randn(B, V, device="cuda", generator=torch.Generator("cuda").manual_seed(V))
+    rows = torch.arange(B, device="cuda")
+    x[rows, torch.from_numpy(at).cuda()] = 50.0
+    from quantized_transformer_decode_gb300 import qw3
+    u = torch.rand(B, device="cuda")
+    temperature = torch.from_numpy((np.arange(B) % 2).astype(np.float32)).cuda()   # greedy and drawn: exp(-40) is left out
+    for _ in range(20):
+        token, prob = qw3.sample(x, u, temperature=temperature)
+        assert np.array_equal(token.cpu().numpy(), at) and bool((prob > 0.999).all())
+
+
 def test_largest_vocabulary(torch):
     rng = np.random.default_rng(18)
     V = 4194304
