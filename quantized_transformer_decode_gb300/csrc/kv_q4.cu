@@ -114,9 +114,10 @@ struct Q4Src {
 };
 
 // The row encoded in f64: for the values that two floats do not hold or decide
-// (outside their range, or on a border to the last bit).
+// (outside their range, or on a border to the last bit). Returns whether one of
+// the lane's values cannot be held.
 template <int HD>
-__device__ __noinline__ void q4_encode_f64(const Q4Src<HD> &in, int lane, int *code, __half *scale) {
+__device__ __noinline__ bool q4_encode_f64(const Q4Src<HD> &in, int lane, int *code, __half *scale) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L;
     double x[E], r = 1.0;
 #pragma unroll
@@ -137,10 +138,12 @@ __device__ __noinline__ void q4_encode_f64(const Q4Src<HD> &in, int lane, int *c
         }
     }
     double P = x[0], N = -x[0];
+    bool bad = false;
 #pragma unroll
-    for (int e = 1; e < E; ++e) {
+    for (int e = 0; e < E; ++e) {
         P = fmax(P, x[e]);
         N = fmax(N, -x[e]);
+        bad |= !(fabs(x[e] * r) < 524160.0);
     }
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) {
@@ -154,6 +157,7 @@ __device__ __noinline__ void q4_encode_f64(const Q4Src<HD> &in, int lane, int *c
         code[e] = m == 0.0 ? 8 : static_cast<int>(fmin(fmax(f, 0.0), 15.0));
     }
     *scale = m == 0.0 ? __float2half_rn(0.0f) : __double2half(-m * r / 8.0);
+    return bad || __hisinf(*scale);   // a value at the limit to the last bit goes by its scale
 }
 
 // The row encoded with two floats to a number. The norm's factor r > 0 is
@@ -248,16 +252,19 @@ __device__ __noinline__ bool q4_encode_f2(const Q4Src<HD> &in, int lane, int *co
 // block holds a value that is not finite or too large for an f16 scale: it is
 // written as zeros.
 template <int HD>
-__device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, float r, const Q4Src<HD> &in, int lane,
-                                          int (&code)[HD / 32], __half &scale) {
+__device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, float r, const Q4Src<HD> &in,
+                                          int lane, int (&code)[HD / 32], __half &scale) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L;
     float P = y[0], N = -y[0];
     bool bad = !(r < INFINITY);
+    // 8 * 65520, where the scale rounds to infinity; a key's value is within `room` of the exact one there
+    constexpr float kLimit = 524160.0f;
+    const float room = in.key ? fmaf(err * 1.01f, r, kLimit * 12.0f * 5.97e-8f) : 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         P = fmaxf(P, y[e]);
         N = fmaxf(N, -y[e]);
-        bad |= !(fabsf(y[e] * r) < 524160.0f);   // 8 * 65520, where the scale rounds to infinity
+        bad |= !(fabsf(y[e] * r) < kLimit + room);
     }
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) {
@@ -266,12 +273,12 @@ __device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, 
     }
     const unsigned badmask = __ballot_sync(0xffffffffu, bad);
     const unsigned block = (L == 32 ? 0xffffffffu : ((1u << L) - 1u)) << (lane / L * L);
-    const bool fine = (badmask & block) == 0u;
+    bool fine = (badmask & block) == 0u;
     const float m = P >= N ? P : -N, am = fabsf(m);
     bool near = false;
     if (fine && am > 0.0f) {
         // under 1e-30 the quotient leaves f32's range
-        near = am < 1e-30f || (err > 0.0f && fabsf(P - N) <= 2.0f * err);
+        near |= am < 1e-30f || (err > 0.0f && (fabsf(P - N) <= 2.0f * err || am * r >= kLimit - room));
         const float inv = -8.0f / m, tol = fmaf(2.0f * err, fabsf(inv), 2e-6f);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -292,17 +299,17 @@ __device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, 
         for (int e = 0; e < E; ++e) code[e] = 8;
         scale = __float2half_rn(0.0f);
         // an exact value may be tiny where its f32 value is zero
-        near = fine && err > 0.0f;
+        near |= fine && err > 0.0f;
     }
     if (__any_sync(0xffffffffu, near)) {
         int c2[E];
         __half s2;
-        if (!q4_encode_f2<HD>(in, lane, c2, &s2)) q4_encode_f64<HD>(in, lane, c2, &s2);
-        if (fine) {
+        // (a value at the limit is beyond the scales that two floats decide)
+        if (!q4_encode_f2<HD>(in, lane, c2, &s2))
+            fine = (__ballot_sync(0xffffffffu, q4_encode_f64<HD>(in, lane, c2, &s2)) & block) == 0u;
 #pragma unroll
-            for (int e = 0; e < E; ++e) code[e] = c2[e];
-            scale = s2;
-        }
+        for (int e = 0; e < E; ++e) code[e] = fine ? c2[e] : 8;
+        scale = fine ? s2 : __float2half_rn(0.0f);
     }
     return fine;
 }
