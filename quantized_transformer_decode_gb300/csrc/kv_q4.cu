@@ -113,6 +113,29 @@ struct Q4Src {
     float eps;
 };
 
+// Whether a head's mean square (with eps) may be had in f32: beyond these the
+// squares, or their sum, leave its range, and f64 takes the head (so 1e30 in an
+// input is as good as 1).
+__device__ __forceinline__ bool q4_norm_fits(float mean) { return mean > 0x1p-100f && mean < 0x1p120f; }
+
+// A query head normalised and rotated in f64: for those whose squares leave f32.
+template <int HD>
+__device__ __noinline__ void q4_query_f64(const Q4Src<HD> &in, int lane, float *y) {
+    constexpr int E = Q4Row<HD>::E;
+    double ss = 0.0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss += static_cast<double>(in.raw[e]) * in.raw[e];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const double r = 1.0 / sqrt(ss / HD + static_cast<double>(in.eps));
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const double x = static_cast<double>(in.raw[e]) * in.w[e] * r;
+        const double o = __shfl_xor_sync(0xffffffffu, x, 16), c = in.cs[e].x, s = in.cs[e].y;
+        y[e] = static_cast<float>(lane < 16 ? x * c - o * s : o * s + x * c);
+    }
+}
+
 // The row encoded in f64: for the values that two floats do not hold or decide
 // (outside their range, or on a border to the last bit). Returns whether one of
 // the lane's values cannot be held.
@@ -248,15 +271,15 @@ __device__ __noinline__ bool q4_encode_f2(const Q4Src<HD> &in, int lane, int *co
 // and scale that lies further from a border than err can carry it; where one
 // does not, the whole row goes through two floats to a number (about one key
 // row in eighty, hardly ever a value row), so the codes are those of the exact
-// values whatever the order of the f32 sums. Returns false for a lane whose
-// block holds a value that is not finite or too large for an f16 scale: it is
-// written as zeros.
+// values whatever the order of the f32 sums. far: a key whose norm f32 does not
+// hold, for f64 from the start. Returns false for a lane whose block holds a value
+// that is not finite or too large for an f16 scale: it is written as zeros.
 template <int HD>
-__device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, float r, const Q4Src<HD> &in,
+__device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, float r, bool far, const Q4Src<HD> &in,
                                           int lane, int (&code)[HD / 32], __half &scale) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L;
     float P = y[0], N = -y[0];
-    bool bad = !(r < INFINITY);
+    bool bad = false;
     // 8 * 65520, where the scale rounds to infinity; a key's value is within `room` of the exact one there
     constexpr float kLimit = 524160.0f;
     const float room = in.key ? fmaf(err * 1.01f, r, kLimit * 12.0f * 5.97e-8f) : 0.0f;
@@ -275,7 +298,7 @@ __device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, 
     const unsigned block = (L == 32 ? 0xffffffffu : ((1u << L) - 1u)) << (lane / L * L);
     bool fine = (badmask & block) == 0u;
     const float m = P >= N ? P : -N, am = fabsf(m);
-    bool near = false;
+    bool near = far;
     if (fine && am > 0.0f) {
         // under 1e-30 the quotient leaves f32's range
         near |= am < 1e-30f || (err > 0.0f && (fabsf(P - N) <= 2.0f * err || am * r >= kLimit - room));
@@ -305,7 +328,7 @@ __device__ __forceinline__ bool q4_encode(const float (&y)[HD / 32], float err, 
         int c2[E];
         __half s2;
         // (a value at the limit is beyond the scales that two floats decide)
-        if (!q4_encode_f2<HD>(in, lane, c2, &s2))
+        if (far || !q4_encode_f2<HD>(in, lane, c2, &s2))
             fine = (__ballot_sync(0xffffffffu, q4_encode_f64<HD>(in, lane, c2, &s2)) & block) == 0u;
 #pragma unroll
         for (int e = 0; e < E; ++e) code[e] = fine ? c2[e] : 8;
@@ -383,18 +406,29 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
             for (int t = 0; t < TPW; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
+        bool fits = true;
 #pragma unroll
         for (int t = 0; t < TPW; ++t) {
-            const float r = rsqrtf(ss[t] / static_cast<float>(HD) + a.eps);
-            float y[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float o = __shfl_xor_sync(0xffffffffu, raw[t][e], 16);
-                y[e] = r * (lane < 16 ? raw[t][e] * in.cs[e].x - o * in.cs[e].y : o * in.cs[e].y + raw[t][e] * in.cs[e].x);
-            }
-            q4_st<E, VEC, kMany>(a.q_out + row * a.q_stride + static_cast<int64_t>(task0 + t) * HD + lane * E, y);
+            ss[t] = ss[t] / static_cast<float>(HD) + a.eps;
+            fits &= q4_norm_fits(ss[t]);
         }
-        return;
+        if (fits) {
+#pragma unroll
+            for (int t = 0; t < TPW; ++t) {
+                const float r = rsqrtf(ss[t]);
+                float y[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float o = __shfl_xor_sync(0xffffffffu, raw[t][e], 16);
+                    y[e] = r * (lane < 16 ? raw[t][e] * in.cs[e].x - o * in.cs[e].y : o * in.cs[e].y + raw[t][e] * in.cs[e].x);
+                }
+                q4_st<E, VEC, kMany>(a.q_out + row * a.q_stride + static_cast<int64_t>(task0 + t) * HD + lane * E, y);
+            }
+            return;
+        }
+        // one by one below, from the inputs again
+#pragma unroll
+        for (int t = 0; t < TPW; ++t) q4_ld<E, VEC, kMany>(raw[t], src + static_cast<int64_t>(task0 + t) * HD);
     }
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
@@ -408,6 +442,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
         }
         in.key = task < a.nh + nkv;
         float y[E], err = 0.0f, r = 1.0f;
+        bool far = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = in.raw[e] = raw[t][e];
         if (in.key) {
@@ -419,8 +454,9 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
                 y[e] *= in.w[e];
                 top = fmaxf(top, fabsf(y[e]));
             }
-            ss = warp_sum(ss);
-            r = rsqrtf(ss / static_cast<float>(HD) + a.eps);
+            const float mean = warp_sum(ss) / static_cast<float>(HD) + a.eps;
+            far = !q4_norm_fits(mean);
+            r = rsqrtf(mean);
             // a rotated value is within 4 roundings of sqrt 2 times the row's
             // largest: one for each product with w, with cos and with sin, one sum
             if (!query) err = 6.0f * 5.97e-8f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
@@ -433,13 +469,14 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
         if (query) {
 #pragma unroll
             for (int e = 0; e < E; ++e) y[e] *= r;
+            if (far) q4_query_f64<HD>(in, lane, y);
             q4_st<E, VEC, kMany>(a.q_out + row * a.q_stride + static_cast<int64_t>(task) * HD + lane * E, y);
             continue;
         }
         const int sel = in.key ? 0 : 1, g = task - a.nh - sel * nkv;
         int code[E];
         __half scale;
-        const bool fine = q4_encode<HD>(y, err, r, in, lane, code, scale);
+        const bool fine = q4_encode<HD>(y, err, r, far, in, lane, code, scale);
         if (!fine) record_status(a.status, QW3_ERR_NONFINITE);
         uint8_t *codes = kv_q4_codes<HD>(a.c, slot, sel, g) + static_cast<size_t>(pos) * (HD / 2) + q4_lane_byte<HD>(lane, sel);
         if constexpr (E == 4) {

@@ -9,6 +9,43 @@ from test_gpu_kv_q4 import EPS, cu, new_cache, planes, rope_table, torch  # noqa
 pytestmark = pytest.mark.gpu
 
 
+def normed(x, w, cs, eps):
+    """norm_rope for any eps."""
+    x, w, cs = (np.asarray(v, np.float64) for v in (x, w, cs))
+    n = x / np.sqrt(np.mean(x * x, -1, keepdims=True) + np.float64(np.float32(eps))) * w
+    h = x.shape[-1] // 2
+    a, b, c, s = n[..., :h], n[..., h:], cs[:, None, :, 0], cs[:, None, :, 1]
+    return n, np.concatenate((a * c - b * s, b * c + a * s), -1)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("M", [5, 2600])
+@pytest.mark.parametrize("scale,eps", [(3e17, EPS), (2e18, EPS), (1e19, EPS), (1e30, EPS), (1e38, EPS), (1e-12, 0.0), (1e-20, 0.0),
+                                       (1e-25, 0.0), (1e-38, 0.0), (1e-43, 0.0), (1e-19, 1e-38)])
+def test_append_norms_whose_squares_leave_f32(torch, hd, M, scale, eps):  # noqa: F811
+    """Finite heads of any size have finite norms: queries within their bound, exact
+    codes, no status. (M: one head to a warp, and four.)"""
+    nh, nkv = 6, 2
+    rng = np.random.default_rng([hd, M])
+    x = (np.clip(rng.standard_normal((M, nh + 2 * nkv, hd)), -3.3, 3.3) * scale).astype(np.float32)
+    x[:, nh + nkv:] = rng.standard_normal((M, nkv, hd))
+    if eps == 0:
+        x[:, :, 0] = scale                                    # no head of zeros
+    qw, kw = (1 + 0.2 * rng.standard_normal((2, hd))).astype(np.float32)
+    cap = (M + 31) // 32 * 32
+    rope = rope_table(cap, hd)
+    cache = new_cache(torch, 1, cap, nkv, hd)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = cache.append(cu(torch, x.reshape(M, -1)), cu(torch, qw), cu(torch, kw), eps, cu(torch, rope), status=status)
+    k, v = cache.read(n=M)
+    assert int(status) == 0
+    qn, want_q = normed(x[:, :nh], qw, rope[:M], eps)
+    assert np.all(np.abs(q.cpu().numpy() - want_q) <= 20 * 2.0 ** -24 * np.abs(qn).max(-1, keepdims=True))
+    _, want_k = normed(x[:, nh:nh + nkv], kw, rope[:M], eps)
+    assert np.array_equal(k.cpu().numpy(), orc.kv_q4_decode(*orc.kv_q4_encode(want_k)))
+    assert np.array_equal(v.cpu().numpy(), orc.kv_q4_decode(*orc.kv_q4_encode(x[:, nh + nkv:])))
+
+
 @pytest.mark.parametrize("big,fits", [(524159.96875, True), (524160.0, None), (524160.03125, False)])
 def test_append_keys_at_the_largest_scale(torch, big, fits):  # noqa: F811
     """Heads of one value c have norm 1 exactly whatever c: a key value just under
