@@ -13,6 +13,7 @@
 // are chained with programmatic dependent launch. Larger batches and prefill
 // use the tiled GEMM path.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -57,12 +58,22 @@ int num_sms() {
 
 namespace {
 
-std::once_flag g_cfg_once;
-cudaError_t g_cfg_err = cudaSuccess;
+// The kernels' attributes (shared memory, cluster sizes) on the current device:
+// they belong to a device, so each one that a call runs on is configured once.
+constexpr int kMaxDevices = 64;
+std::mutex g_cfg_mutex;
+std::atomic<bool> g_cfg_done[kMaxDevices];
+cudaError_t g_cfg_err[kMaxDevices];
 
 cudaError_t configure_all() {
-    std::call_once(g_cfg_once, [] {
-        cudaError_t e = configure_gemv();
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (g_cfg_done[dev].load(std::memory_order_acquire)) return g_cfg_err[dev];
+    std::lock_guard<std::mutex> lock(g_cfg_mutex);
+    if (!g_cfg_done[dev].load(std::memory_order_relaxed)) {
+        e = configure_gemv();
         if (e == cudaSuccess) e = configure_attention();
         if (e == cudaSuccess) e = configure_misc();
         if (e == cudaSuccess) e = configure_step();
@@ -71,9 +82,10 @@ cudaError_t configure_all() {
         if (e == cudaSuccess) e = configure_attn_prefill_tc();
         if (e == cudaSuccess) e = configure_sample();
         if (e == cudaSuccess) e = configure_kv_q4();
-        g_cfg_err = e;
-    });
-    return g_cfg_err;
+        g_cfg_err[dev] = e;
+        g_cfg_done[dev].store(true, std::memory_order_release);
+    }
+    return g_cfg_err[dev];
 }
 
 // Device allocations go through here so that tests can make the n-th one

@@ -85,3 +85,23 @@ def test_append_subnormal_scales(torch):  # noqa: F811
     cache.append(cu(torch, x.reshape(M, -1)), one, one, EPS, cu(torch, rope_table(M, hd)))
     assert np.array_equal(cache.read(n=M)[1].cpu().numpy()[:, 0], orc.kv_q4_decode(*orc.kv_q4_encode(x[:, 2])))
     assert np.array_equal(planes(cache)[1][0, 1, 0].view(np.uint16) & 0x7fff, orc.kv_q4_encode(x[:, 2])[1].view(np.uint16) & 0x7fff)
+
+
+def test_every_entry_on_another_device(torch):  # noqa: F811
+    """The kernels' limits are set on each device that a call runs on."""
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one device")
+    from quantized_transformer_decode_gb300 import qw3
+    rng = np.random.default_rng(7)
+    got = []
+    for d in ("cuda:0", "cuda:1"):
+        dev = lambda x, t=np.float32: torch.from_numpy(np.asarray(x, t)).to(d)  # noqa: B023, E731
+        cache = qw3.KVCacheQ4(1, 1024, 2, 128, device=d)
+        rng = np.random.default_rng(7)
+        one = dev(np.ones(128))
+        q = cache.append(dev(rng.standard_normal((900, 8 * 128))), one, one, EPS, dev(rope_table(1024, 128)))
+        out = cache.attention(q[-1:].contiguous(), dev([900], np.int32))
+        token, prob = qw3.sample(dev(rng.standard_normal((2, 151936))), dev([0.3, 0.6]))
+        got.append([t.cpu() for t in (q, out, token, prob)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
