@@ -495,10 +495,10 @@ QW3_API int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q
  * nearest inside. A -inf logit is never drawn.
  * Weights are summed in 64-bit fixed point (cut to 2^-40 of the largest), so equal
  * inputs give equal tokens; a token whose weight is below 2^-40 of the largest
- * is not drawn. A row with a NaN, with no logit above -inf, with a +inf
- * (unless greedy) or with a temperature that is NaN or infinite gets token -1
- * and probability 0 and, if status_dev is not NULL, sets *status_dev to
- * QW3_ERR_NONFINITE. Asynchronous on `stream`. */
+ * is not drawn. A row with a NaN, with no logit above -inf, with a +inf or a
+ * NaN top_p or min_p (unless greedy), or with a temperature that is NaN or
+ * infinite of either sign gets token -1 and probability 0 and, if status_dev is
+ * not NULL, sets *status_dev to QW3_ERR_NONFINITE. Asynchronous on `stream`. */
 QW3_API int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, const float *temperature_dev,
                        const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
                        int32_t *token_dev, float *prob_dev, int32_t *status_dev, void *stream);

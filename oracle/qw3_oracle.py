@@ -477,10 +477,14 @@ def sample_token(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     lg = np.asarray(logits, np.float64)
     if np.isnan(lg).any() or not (lg > -np.inf).any():
         raise NonFiniteValue("no token to draw")
+    if not np.isfinite(temperature):
+        raise NonFiniteValue("a temperature that is not finite")
     if temperature <= 0:
         return argmax_lowest(lg), 1.0, 1.0
     if np.isposinf(lg).any():
         raise NonFiniteValue("+inf logit")
+    if np.isnan(top_p) or np.isnan(min_p):
+        raise NonFiniteValue("a cut that is not a number")
     margin = 1.0
     order = np.argsort(-lg, kind="stable")
     if 0 < top_k < lg.size:

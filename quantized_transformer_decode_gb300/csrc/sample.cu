@@ -611,8 +611,11 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     }
     row.top = float_from_order_key(static_cast<uint32_t>(best));
     const float T = a.temperature ? a.temperature[b] : 1.0f;
+    const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f, mp = fminf(min_p, 1.0f);
     const bool greedy = T <= 0.0f;
-    const bool bad = best == ~0u || row.top == -INFINITY || !(T < INFINITY) || (!greedy && row.top == INFINITY);
+    // a setting that is not a number has no answer
+    const bool bad = best == ~0u || row.top == -INFINITY || !(fabsf(T) < INFINITY) ||
+                     (!greedy && (row.top == INFINITY || p != p || min_p != min_p));
     if (bad || greedy) {
         u64 first = ~0ull;   // the lowest index of the largest logit
         if (!bad) {
@@ -636,7 +639,6 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     row.inv_t2 = 1.4426950408889634f / fmaxf(T, 1e-30f);
     row.step = kBins / kNats / fmaxf(T, 1e-30f);
     const int k = a.top_k ? a.top_k[b] : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.0f, mp = a.min_p ? fminf(a.min_p[b], 1.0f) : 0.0f;
     // kept: every token with a weight, until a cut says otherwise
     Cut cut{0u, ~0ull, 0, false};
     const bool has_k = k > 0 && k < a.V;

@@ -255,3 +255,16 @@ def test_wrapper_refusals(torch):
         with pytest.raises(qw3.Qw3Error):
             bad()
     assert qw3.sample(x[:0], u[:0])[0].numel() == 0
+
+
+def test_settings_that_are_not_numbers(torch):
+    """A temperature that is not finite, or a top-p or min-p that is NaN, has no
+    answer; a greedy row does not look at its cuts."""
+    V, nan, inf = 9001, np.nan, np.inf
+    rows = np.zeros((9, V), np.float32)
+    rows[:, 77] = 3.0
+    token, prob, status = run(torch, rows, [0.5] * 9, temperature=[1, 1, 1, -inf, nan, inf, 0, 0, -2.0],
+                              top_p=[nan, 1, 0.9, 1, 1, 1, nan, 1, 1], min_p=[0, nan, 1, 0, 0, 0, 0, nan, 0], top_k=[0, 5] + [0] * 7)
+    assert status == 5
+    assert token.tolist() == [-1, -1, 77, -1, -1, -1, 77, 77, 77] and prob.tolist() == [0, 0, 1, 0, 0, 0, 1, 1, 1]
+    assert run(torch, rows[6:], [0.5] * 3, temperature=[0, 0, -2.0], top_p=[nan, 1, 1], min_p=[0, nan, 0])[2] == 0

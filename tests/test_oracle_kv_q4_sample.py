@@ -94,3 +94,11 @@ def test_sample_skips_minus_inf_and_refuses_what_has_no_answer():
     for bad in (np.full(3, -np.inf), np.array([0.0, np.nan]), np.array([0.0, np.inf])):
         with pytest.raises(orc.NonFiniteValue):
             orc.sample_token(bad, 0.5)
+
+
+def test_sample_refuses_settings_that_are_not_numbers():
+    for kw in (dict(temperature=np.nan), dict(temperature=np.inf), dict(temperature=-np.inf), dict(top_p=np.nan),
+               dict(min_p=np.nan)):
+        with pytest.raises(orc.NonFiniteValue):
+            orc.sample_token(LOGITS, 0.5, **kw)
+    assert orc.sample_token(LOGITS, 0.5, temperature=0.0, top_p=np.nan, min_p=np.nan)[0] == 1
