@@ -712,6 +712,69 @@ __device__ __forceinline__ int64_t q4_div(int64_t a, unsigned b) {
     return a >> 32 ? a / b : static_cast<int64_t>(static_cast<unsigned>(a) / b);
 }
 
+// A warp's part of one column, plainly in f32, for far scores: from kFar on (log2
+// units) the reference of the weights, the highest score less the unit's power of
+// two, is rounded in one f32 number by 2^-3 and more, soon by more than P's spare
+// bits, to weights of several times f16's largest or next to nothing. Here the
+// reference is the highest score. The positions are first .. first + 31 and every
+// step-th tile from there, below lim; k: the head's K codes, its scales `plane`
+// bytes on, V to_v bytes on; a lane to a position for the scores, to HD / 32
+// dimensions for the output. (Inside the tiles the same cost every call 1 to 3
+// percent; what such scores cost here does not matter.)
+constexpr float kFar = 2097152.0f;
+template <int HD>
+__device__ __noinline__ void q4_far_column(const float *q, float scale, const uint8_t *k, size_t plane, size_t to_v,
+                                           int first, int step, int lim, float *res) {
+    constexpr int E = HD / 32, NB = HD / 32;
+    const int lane = threadIdx.x & 31;
+    float amax = 0.0f;
+    for (int d = lane; d < HD; d += 32) amax = fmaxf(amax, fabsf(q[d]));
+    const int t = f16_row_exp(warp_max(amax));
+    const float f = pow2_f32(t), c = scale * 1.4426950408889634f * pow2_f32(-t);
+    float mx = -INFINITY, sum = 0.0f, o[E] = {};
+    for (int k0 = first; k0 < lim; k0 += step) {
+        const int n = min(32, lim - k0);
+        float s = -INFINITY;
+        if (lane < n) {
+            const uint8_t *row = k + static_cast<size_t>(k0 + lane) * (HD / 2);
+            const __half *sc = reinterpret_cast<const __half *>(k + plane) + static_cast<size_t>(k0 + lane) * NB;
+            s = 0.0f;
+            for (int b = 0; b < NB; ++b) {
+                float x = 0.0f;
+                for (int j = 0; j < 16; ++j) {
+                    const int w = row[4 * ((j >> 2) * NB + b) + (j & 3)];
+                    x = fmaf(q[32 * b + 2 * j] * f, static_cast<float>((w & 15) - 8), x);
+                    x = fmaf(q[32 * b + 2 * j + 1] * f, static_cast<float>((w >> 4) - 8), x);
+                }
+                s = fmaf(x, __half2float(sc[b]), s);
+            }
+            s *= c;
+        }
+        const float top = fmaxf(mx, warp_max(s)), now = top == -INFINITY ? 0.0f : top;
+        const float corr = exp2_f32(mx - now), p = exp2_f32(s - now);
+        mx = top;
+        sum = fmaf(sum, corr, warp_sum(p));
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= corr;
+        const uint8_t *v = k + to_v + static_cast<size_t>(k0) * (HD / 2);
+        const __half *sv = reinterpret_cast<const __half *>(k + to_v + plane) + static_cast<size_t>(k0) * NB;
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, p, i) * __half2float(sv[i * NB + lane * E / 32]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int code = v[i * (HD / 2) + q4_lane_byte<HD>(lane, true) + e / 2] >> (4 * (e & 1)) & 15;
+                o[e] = fmaf(w, static_cast<float>(code - 8), o[e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) res[lane * E + e] = o[e];
+    if (lane == 0) {
+        res[HD] = sum != sum ? 0.0f : mx;
+        res[HD + 1] = sum;
+    }
+}
+
 // Workspace: two partial results of W columns for each CTA (of the unit that
 // its share begins inside, and of the one that it ends inside), then the first
 // and the last CTA of each unit.
@@ -737,6 +800,7 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
     __shared__ __align__(16) __half s_q[W][2][QS];      // hi and lo; see below for the order of a row
     __shared__ float s_exp[W];
     __shared__ int64_t s_red[NW];
+    __shared__ int s_from[NW];      // each warp's first position of the piece
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int G = a.nh / a.c.nkv, cols = G * a.rows, U = a.c.nkv * cgroups;
@@ -847,6 +911,7 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
     // ---- tiles of this warp: every NW-th of the piece, the first ones on
     // their way before anything else
     int k0 = start + warp * kQ4Tile;
+    if (lane == 0) s_from[warp] = k0;   // read again for far scores: a register for it costs every tile
     // (lane 0's) next tile: codes and scales of K; V's lie a fixed distance behind
     const uint8_t *codes = kv_q4_codes<HD>(a.c, slot, 0, g) + static_cast<size_t>(k0) * (HD / 2);
     const uint8_t *scales = reinterpret_cast<const uint8_t *>(kv_q4_scales<HD>(a.c, slot, 0, g)) + static_cast<size_t>(k0) * (HD / 16);
@@ -1131,6 +1196,8 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
         else tile(std::true_type{});
     }
 
+    const auto far = [](float v) { return fabsf(v) >= kFar && fabsf(v) < INFINITY; };
+    const bool any_far = __any_sync(0xffffffffu, !lost && (far(mx[0]) || far(mx[1])));
     // ---- the warps' results meet in shared memory
     float *res = results(warp);
 #pragma unroll
@@ -1162,6 +1229,20 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
                 dst[1] = make_float2(o[2], o[3]);
             }
         }
+    if (__builtin_expect(any_far, 0)) {
+        __syncwarp();   // over what the lanes have just written
+        int n, sl;
+        q4_blocks(a, b, &n, &sl);
+        const int from = s_from[warp];
+        for (int j = 0; j < ncol; ++j) {
+            const int cc = col0 + j;
+            q4_far_column<HD>(a.q + (static_cast<int64_t>(b) * a.rows + cc / G) * a.q_stride +
+                                  static_cast<int64_t>(g * G + cc % G) * HD,
+                              a.scale, kv_q4_codes<HD>(a.c, sl, 0, g), static_cast<size_t>(a.c.cap) * (HD / 2),
+                              static_cast<size_t>(a.c.nkv) * kv_q4_head_bytes(a.c.cap, HD),
+                              from, kStep, min(end, n - a.rows + cc / G + 1), res + j * PS);
+        }
+    }
     __syncthreads();
     const bool begins = blk0 == 0, ends = blk1 == blocks;
     float *ws = a.ws + (static_cast<size_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * W * PS;

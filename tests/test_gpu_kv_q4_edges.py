@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import qw3_oracle as orc
-from test_gpu_kv_q4 import EPS, cu, new_cache, planes, rope_table, torch  # noqa: F401
+from test_gpu_kv_q4 import EPS, cu, new_cache, planes, put_rows, rope_table, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -85,6 +85,62 @@ def test_append_subnormal_scales(torch):  # noqa: F811
     cache.append(cu(torch, x.reshape(M, -1)), one, one, EPS, cu(torch, rope_table(M, hd)))
     assert np.array_equal(cache.read(n=M)[1].cpu().numpy()[:, 0], orc.kv_q4_decode(*orc.kv_q4_encode(x[:, 2])))
     assert np.array_equal(planes(cache)[1][0, 1, 0].view(np.uint16) & 0x7fff, orc.kv_q4_encode(x[:, 2])[1].view(np.uint16) & 0x7fff)
+
+
+# ---------------------------------------------------------------- attention
+
+SHAPES = [(2, 2, 64, 1, 1), (2, 1, 128, 1, 45), (8, 2, 128, 1, 700), (4, 1, 64, 8, 300), (8, 1, 128, 5, 2000), (8, 1, 128, 1, 40000),
+          (4, 2, 64, 3, 36001)]
+
+
+@pytest.mark.parametrize("nh,nkv,hd,rows,n", SHAPES)
+@pytest.mark.parametrize("gain", [1.0, -1e6, 3e7, 1e8, -1e9, 1e12, 1e30])
+def test_attention_equal_scores_of_any_size(torch, nh, nkv, hd, rows, n, gain):  # noqa: F811
+    """One key throughout: every score of a row is the same number, so the output is
+    the mean of V however large that number is (the score's own error drops out of
+    the tolerance), V of sizes that differ from tile to tile."""
+    rng = np.random.default_rng([nh, hd, rows, n])
+    cap = (n + 31) // 32 * 32
+    cache = new_cache(torch, 1, cap, nkv, hd)
+    k = np.broadcast_to(rng.standard_normal((1, 1, nkv, hd)), (1, cap, nkv, hd))
+    v = rng.standard_normal((1, cap, nkv, hd)) * 2.0 ** np.array([3.0, -10.0, 0.0, 4.0, -4.0])[np.arange(cap) // 96 % 5][:, None, None]
+    k, v = put_rows(cache, torch, k, v)
+    q = rng.standard_normal((rows, nh, hd)).astype(np.float32)
+    kk = np.repeat(k[0, 0], nh // nkv, 0)                     # [nh, hd]
+    q *= (gain / np.einsum("thd,hd->th", q, kk))[..., None]   # q . k = gain
+    got = cache.attention(cu(torch, q.astype(np.float32)), cu(torch, [n], np.int32), rows=rows, scale=1.0).cpu().numpy()
+    for t in range(rows):
+        m = max(0, n - rows + t + 1)
+        vv = np.repeat(v[0, :m], nh // nkv, 1).astype(np.float64)
+        want = vv.mean(0) if m else np.zeros((nh, hd))
+        tol = 64 * 2.0 ** -23 * np.abs(vv).mean(0) + m * 2.0 ** -36 * np.abs(vv).max() if m else 0.0
+        assert np.all(np.abs(got[t] - want) <= tol), (t, float(np.abs(got[t] - want).max()))
+
+
+@pytest.mark.parametrize("nh,nkv,hd,rows,n", SHAPES[1:])
+@pytest.mark.parametrize("gain", [1e7, 1e9, 1e20])
+def test_attention_a_winner_by_far(torch, nh, nkv, hd, rows, n, gain):  # noqa: F811
+    """Scores so large that only the highest counts: its V, wherever the score's error
+    cannot have made another the highest."""
+    rng = np.random.default_rng([nh, hd, rows, n, 1])
+    cap = (n + 31) // 32 * 32
+    cache = new_cache(torch, 1, cap, nkv, hd)
+    k, v = put_rows(cache, torch, rng.standard_normal((1, cap, nkv, hd)), rng.standard_normal((1, cap, nkv, hd)) * 0.003)
+    q = (rng.standard_normal((rows, nh, hd)) * gain).astype(np.float32)
+    got = cache.attention(cu(torch, q), cu(torch, [n], np.int32), rows=rows).cpu().numpy()
+    clear = 0
+    for t in range(rows):
+        for h in range(nh):
+            m = n - rows + t + 1
+            kk, vv = (x[0, :m, h // (nh // nkv)].astype(np.float64) for x in (k, v))
+            s = kk @ q[t, h].astype(np.float64) * hd ** -0.5
+            ds = hd ** -0.5 * (np.abs(kk) @ np.abs(q[t, h].astype(np.float64))).max() * (2.0 ** -22 + (hd / 16 + 4) * 2.0 ** -23)
+            a, b = np.sort(s)[-2:]
+            if b - a > 2 * ds + 40:
+                clear += 1
+                want = vv[int(np.argmax(s))]
+                assert np.all(np.abs(got[t, h] - want) <= 64 * 2.0 ** -23 * np.abs(want) + m * 2.0 ** -36 * np.abs(vv).max())
+    assert clear >= 0.7 * rows * nh
 
 
 def test_every_entry_on_another_device(torch):  # noqa: F811
