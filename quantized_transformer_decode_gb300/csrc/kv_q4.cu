@@ -670,6 +670,14 @@ __device__ __forceinline__ void ld_words(uint32_t (&d)[N], const uint8_t *p) {
     }
 }
 
+// The power of two that brings a query's largest magnitude into [2^14, 2^15), over
+// all of f32 (f16_row_exp stops at 2^100, short of the largest and smallest
+// queries): both it and its inverse are normal. 0, NaN and infinities as they are.
+__device__ __forceinline__ int q4_query_exp(float amax) {
+    if (!(amax > 0.0f && amax < INFINITY)) return 0;
+    return min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23));
+}
+
 // How far (log2) a score may pass the highest at the last change of the
 // weights' unit. P is cut at 2^-24 where its largest product lies in [2^12,
 // 2^15]: these 2 bits and one of the V scale's rounding up to a power of two.
@@ -729,7 +737,7 @@ __device__ __noinline__ void q4_far_column(const float *q, float scale, const ui
     const int lane = threadIdx.x & 31;
     float amax = 0.0f;
     for (int d = lane; d < HD; d += 32) amax = fmaxf(amax, fabsf(q[d]));
-    const int t = f16_row_exp(warp_max(amax));
+    const int t = q4_query_exp(warp_max(amax));
     const float f = pow2_f32(t), c = scale * 1.4426950408889634f * pow2_f32(-t);
     float mx = -INFINITY, sum = 0.0f, o[E] = {};
     for (int k0 = first; k0 < lim; k0 += step) {
@@ -953,7 +961,7 @@ __global__ void __launch_bounds__((CL ? kQ4ClusterWarps : kQ4Warps) * 32, CL ? C
             x[e] = j < ncol ? qp[lane + 32 * e] : 0.0f;
             amax = fmaxf(amax, fabsf(x[e]));
         }
-        const int t = f16_row_exp(warp_max(amax));
+        const int t = q4_query_exp(warp_max(amax));
         const float f = pow2_f32(t);
 #pragma unroll
         for (int e = 0; e < E; ++e) {

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import qw3_oracle as orc
-from test_gpu_kv_q4 import EPS, cu, new_cache, planes, put_rows, rope_table, torch  # noqa: F401
+from test_gpu_kv_q4 import EPS, check_attention, cu, new_cache, planes, put_rows, rope_table, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -141,6 +141,12 @@ def test_attention_a_winner_by_far(torch, nh, nkv, hd, rows, n, gain):  # noqa: 
                 want = vv[int(np.argmax(s))]
                 assert np.all(np.abs(got[t, h] - want) <= 64 * 2.0 ** -23 * np.abs(want) + m * 2.0 ** -36 * np.abs(vv).max())
     assert clear >= 0.7 * rows * nh
+
+
+@pytest.mark.parametrize("qgain,scale", [(1e36, 1e-36), (6e37, 2e-38), (1e-34, 1e34), (1e-37, 1e37), (3e-39, 1e38)])
+def test_attention_the_largest_and_smallest_queries(torch, qgain, scale):  # noqa: F811
+    for nh, nkv, hd, rows, lens in ((4, 2, 128, 2, [300, 45]), (2, 2, 64, 1, [77]), (8, 1, 128, 5, [6000, 1])):
+        check_attention(torch, nh, nkv, hd, lens, rows=rows, qgain=qgain, scale=scale)
 
 
 def test_every_entry_on_another_device(torch):  # noqa: F811
