@@ -431,6 +431,9 @@ def q4_k_gemv(W, rows: int, cols: int, x):
     return y
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
 def _on(index: int, dtype, name: str, *tensors):
     """Check that each given tensor lies on CUDA device `index` as contiguous values of `dtype`."""
     for t in tensors:
@@ -450,6 +453,8 @@ def _rows_of(t, name: str):
     stride, step = t.stride()
     if width > 1 and step != 1:
         raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a 2-d tensor with contiguous rows is wanted")
+    if rows > _INT32_MAX or width > _INT32_MAX:
+        raise Qw3Error(QW3_ERR_SHAPE, f"{name}: more rows or columns than 31 bits count")
     return rows, width, stride if rows > 1 else max(width, stride)
 
 
@@ -476,7 +481,9 @@ class KVCacheQ4:
 
     def __init__(self, slots: int, capacity: int, n_kv_heads: int, head_dim: int, data=None, device="cuda"):
         torch = _torch()
-        n = _kv_q4_bytes(slots, capacity, n_kv_heads, head_dim)
+        # (ctypes would take a larger number modulo 2^32)
+        sizes = (slots, capacity, n_kv_heads, head_dim)
+        n = _kv_q4_bytes(*sizes) if 0 < min(sizes) and max(sizes) <= _INT32_MAX else -1
         if n < 0:
             raise Qw3Error(QW3_ERR_SHAPE, "slots >= 1, capacity % 32 == 0, 1 to 64 kv heads, head_dim 64 or 128")
         if data is None:
@@ -487,8 +494,10 @@ class KVCacheQ4:
         self.slots, self.capacity, self.n_kv_heads, self.head_dim = slots, capacity, n_kv_heads, head_dim
         self.c = Qw3KvQ4(data.data_ptr(), slots, capacity, n_kv_heads, head_dim)
 
-    def _check_places(self, torch, M, slots, pos):
+    def _check_places(self, torch, M, slots, pos, slot, first):
         _on(self.index, torch.int32, "slots and pos", slots, pos)
+        if not (-_INT32_MAX <= slot <= _INT32_MAX and -_INT32_MAX <= first <= _INT32_MAX and M <= _INT32_MAX):
+            raise Qw3Error(QW3_ERR_INVALID_ARG, "a slot, position or row count past 31 bits")
         if (slots is not None and slots.numel() != M) or (pos is not None and pos.numel() != M):
             raise Qw3Error(QW3_ERR_SHAPE, f"slots and pos hold one place for each of {M} rows")
 
@@ -513,7 +522,7 @@ class KVCacheQ4:
             raise Qw3Error(QW3_ERR_SHAPE, "q_norm and k_norm hold head_dim values, rope capacity * head_dim")
         if status is not None:
             _on(self.index, torch.int32, "status", status)
-        self._check_places(torch, M, slots, pos)
+        self._check_places(torch, M, slots, pos, slot, first)
         q = torch.empty((M, n_heads, hd), dtype=torch.float32, device=self.device)
         rc = lib().qw3_kv_q4_append(self.c, qkv.data_ptr(), M, stride, n_heads, q_norm.data_ptr(), k_norm.data_ptr(),
                                     eps, rope.data_ptr(), _ptr(slots), slot, _ptr(pos), first, q.data_ptr(),
@@ -533,7 +542,7 @@ class KVCacheQ4:
         M = n if n is not None else slots.numel() if slots is not None else pos.numel() if pos is not None else -1
         if M < 0:
             raise Qw3Error(QW3_ERR_INVALID_ARG, "read needs slots, pos or n")
-        self._check_places(torch, M, slots, pos)
+        self._check_places(torch, M, slots, pos, slot, first)
         shape = (M, self.n_kv_heads, self.head_dim)
         k = torch.empty(shape, dtype=torch.float32, device=self.device)
         v = torch.empty(shape, dtype=torch.float32, device=self.device)
@@ -564,6 +573,8 @@ class KVCacheQ4:
         if slots is None and B > self.slots:
             raise Qw3Error(QW3_ERR_SHAPE, "more sequences than slots")
         max_len = self.capacity if max_len is None else max_len
+        if not 0 <= max_len <= self.capacity:
+            raise Qw3Error(QW3_ERR_KV_OVERFLOW if max_len > 0 else QW3_ERR_INVALID_ARG, "max_len past the cache's capacity")
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:

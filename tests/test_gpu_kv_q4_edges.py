@@ -149,6 +149,24 @@ def test_attention_the_largest_and_smallest_queries(torch, qgain, scale):  # noq
         check_attention(torch, nh, nkv, hd, lens, rows=rows, qgain=qgain, scale=scale)
 
 
+def test_places_past_31_bits_are_refused(torch):  # noqa: F811
+    """A slot, position or length is not taken modulo 2^32."""
+    from quantized_transformer_decode_gb300.qw3 import KVCacheQ4, Qw3Error
+    cache = KVCacheQ4(2, 64, 1, 64)
+    cache.data.zero_()
+    f = lambda *s: torch.ones(s, device="cuda")  # noqa: E731
+    good = (f(64), f(64), EPS, f(64, 32, 2))
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    for bad in (lambda: cache.append(f(1, 192), *good, first=2 ** 32), lambda: cache.append(f(1, 192), *good, slot=2 ** 32),
+                lambda: cache.read(n=1, first=2 ** 32), lambda: cache.read(n=1, slot=2 ** 32 + 1),
+                lambda: cache.attention(f(1, 1, 64), lens, max_len=2 ** 32 + 32),
+                lambda: cache.attention(f(1, 1, 64), lens, max_len=-2 ** 32),
+                lambda: cache.append(f(1, 192), *good, first=-2 ** 32)):
+        with pytest.raises(Qw3Error):
+            bad()
+    assert not cache.data.any()
+
+
 def test_every_entry_on_another_device(torch):  # noqa: F811
     """The kernels' limits are set on each device that a call runs on."""
     if torch.cuda.device_count() < 2:

@@ -130,3 +130,16 @@ def test_wrappers_check_before_they_allocate():
     with pytest.raises(qw3.Qw3Error) as e:
         qw3.KVCacheQ4(1, 33, 1, 64)
     assert e.value.status == SHAPE
+
+
+def test_sizes_past_31_bits_are_refused():
+    """ctypes would pass them on modulo 2^32."""
+    import torch
+    for sizes in ((2 ** 32 + 1, 32, 1, 64), (1 - 2 ** 32, 32, 1, 64), (1, 2 ** 32 + 32, 1, 64), (1, 32, 2 ** 32 + 1, 64), (1, 32, 1, 2 ** 32 + 64)):
+        with pytest.raises(qw3.Qw3Error) as e:
+            qw3.KVCacheQ4(*sizes)
+        assert e.value.status == SHAPE
+    for shape in ((1, 2 ** 32 + 5), (2 ** 32 + 1, 8)):
+        with pytest.raises(qw3.Qw3Error) as e:
+            qw3._rows_of(torch.empty(shape, device="meta"), "logits")
+        assert e.value.status == SHAPE
