@@ -487,6 +487,8 @@ class KVCacheQ4:
         if n < 0:
             raise Qw3Error(QW3_ERR_SHAPE, "slots >= 1, capacity % 32 == 0, 1 to 64 kv heads, head_dim 64 or 128")
         if data is None:
+            if torch.device(device).type != "cuda":
+                raise Qw3Error(QW3_ERR_INVALID_ARG, "device: a cache lies on a CUDA device")
             data = torch.empty(n, dtype=torch.uint8, device=device)
         elif data.dtype is not torch.uint8 or not data.is_cuda or not data.is_contiguous() or data.numel() < n:
             raise Qw3Error(QW3_ERR_INVALID_ARG, f"data: a contiguous CUDA uint8 tensor of {n} bytes is wanted")

@@ -143,3 +143,11 @@ def test_sizes_past_31_bits_are_refused():
         with pytest.raises(qw3.Qw3Error) as e:
             qw3._rows_of(torch.empty(shape, device="meta"), "logits")
         assert e.value.status == SHAPE
+
+
+def test_a_cache_lies_on_a_gpu():
+    """A cache in host memory is refused where it is made, not by its calls."""
+    for kw in (dict(device="cpu"), dict(device="meta")):
+        with pytest.raises(qw3.Qw3Error) as e:
+            qw3.KVCacheQ4(1, 32, 1, 64, **kw)
+        assert e.value.status == ARG
