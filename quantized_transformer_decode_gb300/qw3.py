@@ -749,17 +749,20 @@ class Qw3Model:
 
     def generate_sample(self, first_tokens, n_steps: int, u, temperature=None, top_k=None, top_p=None, min_p=None,
                         seqs: Optional[Sequence[int]] = None):
-        """n_steps sampled steps (qw3_generate_sample) from CUDA tensors:
-        first_tokens [B], u f32 [n_steps, B] in [0, 1), the settings [B] each
-        (f32; top_k int32) or left out. Returns (tokens int32 [n_steps, B],
+        """n_steps sampled steps (qw3_generate_sample) from tensors on the model's
+        device: first_tokens [B], u f32 [n_steps, B] in [0, 1), the settings [B]
+        each (f32; top_k int32) or left out. Returns (tokens int32 [n_steps, B],
         probabilities f32 [n_steps, B])."""
         torch = _torch()
         first_tokens = first_tokens.to(torch.int32).contiguous()
-        B, dev = first_tokens.numel(), first_tokens.get_device()
+        B, dev = first_tokens.numel(), self.stream.device.index
+        _on(dev, torch.int32, "first_tokens", first_tokens)
         _on(dev, torch.float32, "u, temperature, top_p and min_p", u, temperature, top_p, min_p)
         _on(dev, torch.int32, "top_k", top_k)
         if u.numel() != n_steps * B or any(t is not None and t.numel() != B for t in (temperature, top_k, top_p, min_p)):
             raise Qw3Error(QW3_ERR_SHAPE, "u holds n_steps * B numbers, a setting B")
+        if seqs is not None and len(seqs) != B:
+            raise Qw3Error(QW3_ERR_SHAPE, "seqs names one sequence for each first token")
         logits = torch.empty((B, self.shape.vocab), dtype=torch.float32, device=first_tokens.device)
         out = torch.empty((n_steps, B), dtype=torch.int32, device=first_tokens.device)
         prob = torch.empty((n_steps, B), dtype=torch.float32, device=first_tokens.device)

@@ -151,3 +151,39 @@ def test_a_cache_lies_on_a_gpu():
         with pytest.raises(qw3.Qw3Error) as e:
             qw3.KVCacheQ4(1, 32, 1, 64, **kw)
         assert e.value.status == ARG
+
+
+@pytest.mark.parametrize("kw", [dict(first=[1, 2]), dict(u=True), dict(temperature=True), dict(seqs=[0]), dict(seqs=[0, 1, 0])])
+def test_sampled_generation_takes_tensors_of_its_device(monkeypatch, kw):
+    """A host pointer, or a list of another length than the batch, never reaches the
+    library."""
+    import types
+
+    import torch
+    m = object.__new__(qw3.Qw3Model)
+    m.h, m.shape, m.stream = None, types.SimpleNamespace(vocab=8), types.SimpleNamespace(device=torch.device("cuda", 0))
+
+    class Gpu(torch.Tensor):
+        """A host tensor that says it lies on cuda:0."""
+        def get_device(self):
+            return 0
+
+        @property
+        def device(self):
+            return torch.device("cuda", 0)
+
+    def reached(*a, **k):
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(qw3, "qw3_generate_sample", reached)
+    monkeypatch.setattr(qw3, "_Ordered", reached)
+    # what is allocated once the checks have passed
+    monkeypatch.setattr(torch, "empty", reached)
+    g = lambda x, d=torch.float32: torch.tensor(x, dtype=d).as_subclass(Gpu)  # noqa: E731
+    args = dict(first_tokens=g([1, 2], torch.int32), n_steps=3, u=g([[0.5, 0.5]] * 3), temperature=g([1.0, 1.0]))
+    with pytest.raises(AssertionError):                       # the arguments themselves are good
+        m.generate_sample(**args)
+    host = {"first": dict(first_tokens=torch.tensor([1, 2], dtype=torch.int32), u=torch.full((3, 2), 0.5), temperature=torch.ones(2)),
+            "u": dict(u=torch.full((3, 2), 0.5)), "temperature": dict(temperature=torch.ones(2)), "seqs": dict(seqs=kw.get("seqs"))}
+    with pytest.raises(qw3.Qw3Error):
+        m.generate_sample(**{**args, **host[next(iter(kw))]})
