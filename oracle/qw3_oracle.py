@@ -434,8 +434,10 @@ def kv_q4_encode(x: np.ndarray):
     """(codes [..., d] int, scales [..., d/32] f16) of rows x [..., d] taken in
     f64: per block of 32, m the value of largest magnitude (the positive one of
     two opposite equals), d = -m / 8, code = clamp(floor(x / d + 8.5), 0, 15),
-    8 throughout where m = 0; the scale is d rounded once to f16."""
+    8 throughout where m = 0; the scale is d rounded once to f16. A block with a
+    NaN, an infinity or a magnitude of 524160 or more is one of zeros."""
     b = np.asarray(x, np.float64).reshape(*np.shape(x)[:-1], -1, 32)
+    b = np.where(np.all(np.abs(b) < 524160.0, axis=-1, keepdims=True), b, 0.0)
     hi, lo = b.max(-1), b.min(-1)
     m = np.where(hi >= -lo, hi, lo)
     with np.errstate(divide="ignore", invalid="ignore"):

@@ -38,6 +38,24 @@ def test_kv_q4_error_bound():
     assert np.all(err <= np.where(end, d[..., None], d[..., None] / 2) + slack[..., None] + 1e-12)
 
 
+def test_kv_q4_blocks_that_cannot_be_held_are_zeros():
+    x = np.ones((6, 64))
+    x[0, 3], x[1, 3], x[2, 3], x[3, 3], x[4, 3], x[5, 3] = np.nan, np.inf, -np.inf, 524160.0, -524160.0, 524159.0
+    codes, scales = orc.kv_q4_encode(x)
+    assert not scales[:5, 0].any() and np.all(codes[:5, :32] == 8)
+    assert scales[5, 0] == np.float16(-65504)              # under 65520: still the largest f16
+    assert np.all(scales[:, 1] == np.float16(-0.125)) and np.all(orc.kv_q4_decode(codes, scales)[:, 32:] == 1.0)
+
+
+def test_kv_q4_scales_round_to_nearest_even():
+    """d at the middle between two f16 values, normal and subnormal."""
+    for d, want in ((1 + 2.0 ** -11, 1.0), (1 + 3 * 2.0 ** -11, 1 + 2.0 ** -9), (2.5 * 2.0 ** -24, 2 * 2.0 ** -24),
+                    (3.5 * 2.0 ** -24, 4 * 2.0 ** -24), (0.5 * 2.0 ** -24, 0.0), (0.75 * 2.0 ** -24, 2.0 ** -24)):
+        x = np.zeros(32)
+        x[7] = -8 * d
+        assert orc.kv_q4_encode(x)[1].tolist() == [want]
+
+
 def test_kv_q4_row_bytes_places():
     """Two blocks: K bytes go word by word, V bytes halfword by halfword."""
     codes = np.concatenate([np.arange(32) % 16, (np.arange(32) + 5) % 16])
