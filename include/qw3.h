@@ -457,7 +457,7 @@ QW3_API int64_t qw3_kv_q4_attn_workspace_bytes(int32_t B, int32_t rows, int32_t 
 /* Grouped-query causal attention of `rows` query rows (1..16) of each of B
  * sequences over the cache: q_dev f32 [B * rows][q_stride] (normalised and
  * rotated), out_dev f32 [B * rows][out_stride], n_heads * head_dim values
- * each; query head h reads kv head h / (n_heads / n_kv_heads), a group of at
+ * each (out_dev may be q_dev itself with its stride, no other overlap); query head h reads kv head h / (n_heads / n_kv_heads), a group of at
  * most 16. Sequence b lies in slot slots_dev[b] (slot b where slots_dev is
  * NULL) and holds lens_dev[b] positions, its `rows` newest among them: row t
  * is at position p = lens_dev[b] - rows + t and attends positions 0..p,
@@ -493,9 +493,11 @@ QW3_API int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q
  * no top-p, no min-p. A temperature <= 0 is greedy (lowest index among equal
  * maxima, probability 1). u_dev: [B] in [0, 1), values outside taken as the
  * nearest inside. A -inf logit is never drawn.
- * Weights are summed in 64-bit fixed point (cut to 2^-40 of the largest), so equal
- * inputs give equal tokens; a token whose weight is below 2^-40 of the largest
- * is not drawn. A row with a NaN, with no logit above -inf, with a +inf or a
+ * Weights are f32, within 4e-6 of exact, and summed in 64-bit fixed point (cut
+ * to 2^-40 of the largest), so equal inputs give equal tokens; where a cut or the
+ * draw comes nearer than that to a border it may fall on either side. A token
+ * whose weight is below 2^-40 of the largest is not drawn. A positive temperature
+ * below 1e-30 is taken as 1e-30. A row with a NaN, with no logit above -inf, with a +inf or a
  * NaN top_p or min_p (unless greedy), or with a temperature that is NaN or
  * infinite of either sign gets token -1 and probability 0 and, if status_dev is
  * not NULL, sets *status_dev to QW3_ERR_NONFINITE. Asynchronous on `stream`. */

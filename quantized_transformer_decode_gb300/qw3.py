@@ -560,7 +560,8 @@ class KVCacheQ4:
         the first lens[b] positions (int32 [B]) of slot slots[b] (int32 [B],
         else slot b); returns the same shape. max_len: an upper bound of lens
         (the capacity where it is not given). scale: 1 / sqrt(head_dim) where it
-        is not given. workspace: a uint8 tensor to use in place of a new one."""
+        is not given. out: where the result goes (q itself, or apart from it).
+        workspace: a uint8 tensor to use in place of a new one."""
         torch = _torch()
         if _elsewhere(torch, self.index):
             with torch.cuda.device(self.index):

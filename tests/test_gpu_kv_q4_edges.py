@@ -149,6 +149,47 @@ def test_attention_the_largest_and_smallest_queries(torch, qgain, scale):  # noq
         check_attention(torch, nh, nkv, hd, lens, rows=rows, qgain=qgain, scale=scale)
 
 
+def test_attention_past_32_bits(torch):  # noqa: F811
+    """A cache of 4.9 GB: the last slot's rows lie past 2^32 bytes, its last ones past
+    2^31 from its start."""
+    slots, cap, nkv, hd, nh, n = 2, 2097152, 8, 128, 16, 300
+    from quantized_transformer_decode_gb300.qw3 import KVCacheQ4
+    cache = KVCacheQ4(slots, cap, nkv, hd)
+    cache.data.zero_()                                        # scores 0, V 0 up to the last rows
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((n, nh + 2 * nkv, hd)).astype(np.float32)
+    one = cu(torch, np.ones(hd, np.float32))
+    rope = torch.zeros(cap, hd // 2, 2, device="cuda")
+    rope[..., 0] = 1
+    q = cache.append(cu(torch, x.reshape(n, -1)), one, one, EPS, rope, slots=cu(torch, np.full(n, slots - 1, np.int32)),
+                     pos=cu(torch, np.arange(cap - n, cap, dtype=np.int32)))[-1:] * 4
+    got = cache.attention(q, cu(torch, [cap], np.int32), slots=cu(torch, [slots - 1], np.int32)).cpu().numpy()
+    k, v = (t.cpu().numpy().astype(np.float64) for t in cache.read(slot=slots - 1, first=cap - n, n=n))
+    for h in range(nh):
+        s = k[:, h // 2] @ q[0, h].cpu().numpy().astype(np.float64) * hd ** -0.5
+        top = max(s.max(), 0.0)
+        p, rest = np.exp(s - top), (cap - n) * np.exp(-top)
+        p /= p.sum() + rest
+        ds = hd ** -0.5 * (np.abs(k[:, h // 2]) @ np.abs(q[0, h].cpu().numpy())).max() * (2.0 ** -22 + (hd / 16 + 4) * 2.0 ** -23)
+        # the sum of 2^21 weights: 65536 tiles of 8 heads over 456 CTAs of 4 warps, 4 roundings of 2^-24 to a
+        # thread in each: some 1150 of 2^-24
+        tol = (2 * ds + (64 + 600) * 2.0 ** -23) * (p @ np.abs(v[:, h // 2])) + n * 2.0 ** -36 * np.abs(v).max()
+        assert np.all(np.abs(got[0, h] - p @ v[:, h // 2]) <= tol)
+
+
+@pytest.mark.parametrize("nh,nkv,hd,rows,lens", [(4, 2, 128, 1, [70]), (4, 2, 64, 3, [5, 0, 2100]), (8, 1, 128, 5, [30000, 400]),
+                                                 (2, 1, 64, 1, [130] * 400)])
+def test_attention_in_place_of_its_queries(torch, nh, nkv, hd, rows, lens):  # noqa: F811
+    rng = np.random.default_rng(4)
+    B, cap = len(lens), (max(lens) + 31) // 32 * 32
+    cache = new_cache(torch, B, cap, nkv, hd)
+    put_rows(cache, torch, rng.standard_normal((B, cap, nkv, hd)), rng.standard_normal((B, cap, nkv, hd)))
+    q = cu(torch, rng.standard_normal((B * rows, nh, hd)).astype(np.float32))
+    n = cu(torch, lens, np.int32)
+    want = cache.attention(q, n, rows=rows)
+    assert cache.attention(q, n, rows=rows, out=q) is q and torch.equal(q, want)
+
+
 def test_places_past_31_bits_are_refused(torch):  # noqa: F811
     """A slot, position or length is not taken modulo 2^32."""
     from quantized_transformer_decode_gb300.qw3 import KVCacheQ4, Qw3Error

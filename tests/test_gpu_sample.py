@@ -268,3 +268,15 @@ def test_settings_that_are_not_numbers(torch):
     assert status == 5
     assert token.tolist() == [-1, -1, 77, -1, -1, -1, 77, 77, 77] and prob.tolist() == [0, 0, 1, 0, 0, 0, 1, 1, 1]
     assert run(torch, rows[6:], [0.5] * 3, temperature=[0, 0, -2.0], top_p=[nan, 1, 1], min_p=[0, nan, 0])[2] == 0
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-20, 1e30, 1e37])
+@pytest.mark.parametrize("V", [5003, 40009])
+def test_scales_at_the_ends_of_f32(torch, scale, V):
+    """Logits and temperatures of any size: what counts is their ratio."""
+    rng = np.random.default_rng(V)
+    B = 24
+    logits = (rng.standard_normal((B, V)) * 2).astype(np.float32) * np.float32(scale)
+    kw = settings(rng, B)
+    kw["temperature"] = np.float32(rng.choice([1.0, 1.7], B)) * np.float32(scale)
+    check(torch, logits, rng.random(B), least=0.8, **kw)
