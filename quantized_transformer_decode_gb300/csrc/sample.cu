@@ -424,7 +424,10 @@ __device__ __forceinline__ void answer(const SampleArgs &a, int b, int token, fl
     if (a.next) a.next[b] = token;
     if (a.prob) {
         const float T = a.temperature ? fmaxf(a.temperature[b], 1e-30f) : 1.0f;
-        const float d = v - row.top, q = d / T, r = fmaf(-q, T, d) / T;
+        // v - top as two floats (Knuth's two-sum): rounded, 20 below the largest costs 6e-7
+        const float d = __fsub_rn(v, row.top), z = __fsub_rn(d, v);
+        const float lo = __fsub_rn(__fsub_rn(v, __fsub_rn(d, z)), __fadd_rn(row.top, z));
+        const float q = __fdiv_rn(d, T), r = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, T, d), lo), T);
         const float e = expf(q);
         a.prob[b] = fmaf(e, r, e) * (kOne / static_cast<float>(total));
     }

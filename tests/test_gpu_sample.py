@@ -280,3 +280,18 @@ def test_scales_at_the_ends_of_f32(torch, scale, V):
     kw = settings(rng, B)
     kw["temperature"] = np.float32(rng.choice([1.0, 1.7], B)) * np.float32(scale)
     check(torch, logits, rng.random(B), least=0.8, **kw)
+
+
+def test_probabilities_of_small_weights(torch):
+    """A token far below the largest: its probability is good to 8 roundings (expf 4, a
+    correction, the total, a quotient, a product of 2^-24 each)."""
+    rng = np.random.default_rng(23)
+    B = 4000
+    x = np.stack([rng.uniform(-30, 30, B), np.zeros(B)], 1).astype(np.float32)
+    temp = rng.uniform(0.3, 3, B).astype(np.float32)
+    x[:, 1] = x[:, 0] - rng.uniform(2, 12, B) * temp
+    w = np.exp((x[:, 1].astype(np.float64) - x[:, 0]) / temp)
+    p = w / (1 + w)
+    token, prob, status = run(torch, x, 1 - p / 2, temperature=temp)
+    assert status == 0 and np.all(token == 1)
+    assert np.all(np.abs(prob - p) <= 8 * 2.0 ** -24 * p)
