@@ -493,11 +493,12 @@ QW3_API int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q
  * no top-p, no min-p. A temperature <= 0 is greedy (lowest index among equal
  * maxima, probability 1). u_dev: [B] in [0, 1), values outside taken as the
  * nearest inside. A -inf logit is never drawn.
- * Weights are f32, within 4e-6 of exact, and summed in 64-bit fixed point (cut
- * to 2^-40 of the largest), so equal inputs give equal tokens; where a cut or the
- * draw comes nearer than that to a border it may fall on either side. A token
- * whose weight is below 2^-40 of the largest is not drawn. A positive temperature
- * below 1e-30 is taken as 1e-30. A row with a NaN, with no logit above -inf, with a +inf or a
+ * Weights are within 2^-29 of exact and summed in 64-bit fixed point (in units of
+ * 2^-46 of the largest, 2^-40 for V >= 2^18), so equal inputs give equal tokens;
+ * where a cut or the draw comes nearer to a border than these roundings it may
+ * fall on either side (one row of a large vocabulary in 100,000). A token whose
+ * weight is below that unit is not drawn. A positive temperature below 1e-30 is
+ * taken as 1e-30. A row with a NaN, with no logit above -inf, with a +inf or a
  * NaN top_p or min_p (unless greedy), or with a temperature that is NaN or
  * infinite of either sign gets token -1 and probability 0 and, if status_dev is
  * not NULL, sets *status_dev to QW3_ERR_NONFINITE. Asynchronous on `stream`. */

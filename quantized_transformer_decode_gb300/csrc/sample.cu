@@ -17,7 +17,7 @@
 // itself. For a small top-k a histogram of the threads' largest logits (one
 // addition to a thread) gives a bound that the k-th largest token cannot lie
 // below. Else a cut is found by a histogram of all tokens over equal steps of
-// (max l - l) / T (1024 of them, down to weights of 2^-41), whose bins a
+// (max l - l) / T (1024 of them, down to weights of 2^-46), whose bins a
 // vocabulary's logits fill evenly, so that few of a warp's additions meet in one
 // word; if what top-p keeps fits the list, it is listed, else the cut's bin alone
 // is ranked, or cut further by histograms over its keys until it holds at most
@@ -28,9 +28,10 @@
 // (39 MB, 1.2 TB/s), with top-p alone 53 us where that keeps few tokens and 80 us
 // where it keeps much of the row.
 //
-// Sums are taken in 64-bit fixed point (2^40 for the largest weight): they are
+// Sums are taken in 64-bit fixed point (2^46 for the largest weight): they are
 // the same whatever the order of the additions, so one input gives one token.
 #include <algorithm>
+#include <type_traits>
 
 #include "qw3_internal.cuh"
 
@@ -44,19 +45,58 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2 * kThreads;   // two to a thread
 constexpr int kList = 256;      // tokens that the first CTA ranks
 constexpr int kMaxCluster = 16;
-constexpr float kOne = 1099511627776.0f;   // 2^40
+
+// The largest weight in fixed point: 2^46 while 64 bits hold the sum of a vocabulary of
+// them (and 32 bits the digit sums of a slice), else 2^40. Weights are odd: cut to a
+// multiple of 2, and half of that added, so that the sums lean to neither side (what
+// cutting alone takes from 150,000 small weights moves the draw of one row in 40,000
+// at 2^46, and of one in 500 at 2^40).
+constexpr int kFineVocab = 1 << 18, kFineBits = 46, kCoarseBits = 40;
 
 // Order of logits as unsigned keys; the two zeros are one value.
 __device__ __forceinline__ uint32_t logit_key(float v) { return float_order_key(v + 0.0f); }
 
-// e in [0, 1] times 2^40, cut to an integer, from its bits (a conversion of
-// f32 to 64 bits runs on the f64 units, which are few).
-__device__ __forceinline__ u64 fixed_weight(float e) {
+// e in [0, 1] times 2^bits, cut to an integer, or (up) the next one where that cuts
+// something off: from its bits (a conversion of f32 to 64 bits runs on the f64 units,
+// which are few).
+__device__ __forceinline__ u64 fixed_point(float e, int bits, bool up = false) {
     const uint32_t x = __float_as_uint(e);
-    const int shift = static_cast<int>(x >> 23) - 110;   // 2^40 e = mantissa * 2^shift
-    const u64 m = (x & 0x7fffffu) | 0x800000u;
-    return shift >= 0 ? m << shift : (shift > -24 ? m >> -shift : 0ull);
+    if (!(e > 0.0f)) return 0ull;
+    const int shift = static_cast<int>(x >> 23) - 150 + bits;   // e = mantissa * 2^(shift - bits)
+    const u64 m = (x & 0x7fffffu) | (x >> 23 ? 0x800000u : 0u);
+    const u64 v = shift >= 0 ? m << shift : (shift > -24 ? m >> -shift : 0ull);
+    return v + (up && shift < 0 && (shift <= -24 || (m & ((1ull << -shift) - 1ull)) != 0ull));
 }
+
+// f x for f in [0, 1], to the integer below or (up) above, exactly: equal weights are
+// parted where f says, which a product in f64 would miss by what it rounds off.
+__device__ __forceinline__ u64 share_of(float f, u64 x, bool up) {
+    if (!(f > 0.0f)) return 0ull;
+    if (f >= 1.0f) return x;
+    const uint32_t b = __float_as_uint(f);
+    const u64 m = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
+    const int e = 150 - max(static_cast<int>(b >> 23), 1);   // f = m 2^-e, e >= 24
+    const u64 hi = __umul64hi(m, x), lo = m * x;
+    if (e >= 64) return (e < 128 ? hi >> (e - 64) : 0ull) + (up && x > 0 && (e >= 128 || lo || (hi & ((1ull << (e - 64)) - 1ull))));
+    return (lo >> e | hi << (64 - e)) + (up && (lo & ((1ull << e) - 1ull)));
+}
+
+// 2^30 * 2^(j / 256), rounded: made when this file is compiled, by the series of exp.
+struct Powers {
+    uint32_t v[256];
+    constexpr Powers() : v() {
+        for (int j = 0; j < 256; ++j) {
+            const double x = j * (0.69314718055994530942 / 256);
+            double term = 1.0, sum = 1.0;
+            for (int i = 1; i < 24; ++i) {
+                term *= x / i;
+                sum += term;
+            }
+            v[j] = static_cast<uint32_t>(sum * 1073741824.0 + 0.5);
+        }
+    }
+};
+__device__ const Powers kPowers{};
 
 __device__ __forceinline__ void remote_st(uint32_t addr, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -79,8 +119,9 @@ __device__ __forceinline__ void sync_cluster() {
 }
 
 struct Shared {
-    // this CTA's histogram: counts, and weights as sums of their 14-bit digits (up
-    // to 2^18 tokens to a slice: no sum passes 32 bits)
+    // this CTA's histogram: counts, and weights as sums of their digits (16 bits at
+    // 2^46 with up to 45056 tokens to a slice, 14 at 2^40 with up to 2^18: no sum
+    // passes 32 bits)
     uint32_t cnt[kBins], digit[3][kBins];
     // the row's
     uint32_t tcnt[kBins];
@@ -98,6 +139,7 @@ struct Shared {
     uint32_t bin, found, last_rank, sent;
     u64 above_cnt, above_w;
     u64 res[4];   // cut, ties, weight of the prefix, ties left out
+    uint32_t pow2[256];   // kPowers
 };
 
 // Sums over the threads below this one, of a and b at once, and in ta and tb
@@ -135,7 +177,7 @@ __device__ __forceinline__ void scan2(u64 &a, u64 &b, u64 &ta, u64 &tb, Shared &
     b = by + y - b;
 }
 
-constexpr float kNats = 29.0f;   // exp(-29) < 2^-41: weights that round to zero
+constexpr float kNats = 32.0f, kCoarseNats = 28.0f;   // exp(-32) < 2^-46, exp(-28) < 2^-40: beyond, no weight
 
 // Largest word of the block.
 __device__ __forceinline__ uint32_t block_max(uint32_t v, Shared &s) {
@@ -148,15 +190,75 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, Shared &s) {
     return v;
 }
 
+// Weights: 2^(x / 256) with x = (l - max l) 256 log2(e) / T, the 256 powers of a table
+// and a polynomial between them (a published way to exp: P. Tang, "Table-driven
+// implementation of the exponential function in IEEE floating-point arithmetic",
+// 1989). l c - max c, c = 256 log2(e) / T, is had with c in two floats, its whole part
+// taken off within the fma, so that what is left, at most 1, keeps an error of some
+// 2^-24; the weight is then within 2^-29 of exact, besides its rounding to an odd
+// integer. It takes some 25 instructions. A single f32 weight (ex2.approx of an argument
+// rounded twice: 10 instructions, 4e-6 off at most) gave another token than 64 bits in
+// one row of 600 over a whole vocabulary; its times: 64 rows of 151936 with mixed
+// settings 45 us against 47.5, without a cut 32 against 37.
 struct Row {
     const float *l;   // this CTA's slice, in shared or global memory
     int n, base;      // its length, and its first token
-    float top, inv_t2, step;  // log2(e) / T; bins per unit of logit
+    float top, step;  // the largest logit; bins per unit of logit
     uint32_t rank, size;      // in the cluster
-    __device__ __forceinline__ float weight(float v) const {
-        float r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((v - top) * inv_t2));
-        return r;
+    float c, c_lo;            // c in two floats
+    float x;                  // less the fraction of max c; its whole part
+    int whole;
+    float least;              // logits below have no weight
+    bool wide;                // max c is too large for that: the difference first
+    int bits;                 // the largest weight is 2^bits
+    const uint32_t *pow2;
+
+    // the temperature's part, while the slice is on its way, and the largest logit's
+    __device__ __forceinline__ void set_temperature(float T) {
+        constexpr float kL = 369.32993f;   // 256 log2(e) in two floats
+        constexpr float kLlo = static_cast<float>(256.0 * 1.4426950408889634074 - static_cast<double>(kL));
+        c = __fdiv_rn(kL, T);
+        c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c, T, kL), kLlo), T);
+        step = kBins / kNats / T;
+    }
+    __device__ __forceinline__ void set_top(float highest, float T) {
+        top = highest;
+        wide = !(fabsf(__fmul_rn(top, c)) < 2097152.0f);
+        const float m = __fmaf_rn(top, c, kMagic);
+        whole = __float_as_int(m);
+        x = -__fmaf_rn(top, c_lo, __fmaf_rn(top, c, -__fsub_rn(m, kMagic)));
+        least = fmaxf(top - (bits == kFineBits ? kNats : kCoarseNats) * T, -3.4028235e38f);
+    }
+    static constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: a number added to it is rounded to an integer
+    // The weight of a logit (of the row's: at most top, or -inf) in fixed point.
+    __device__ __forceinline__ u64 weight(float v) const { return wide ? weight<true>(v) : weight<false>(v); }
+    template <bool WIDE>
+    __device__ __forceinline__ u64 weight(float v) const {
+        float f;
+        int k;
+        if constexpr (!WIDE) {
+            const float m = __fmaf_rn(v, c, kMagic);
+            f = __fadd_rn(__fmaf_rn(v, c_lo, __fmaf_rn(v, c, -__fsub_rn(m, kMagic))), x);
+            k = __float_as_int(m) - whole;
+        } else {
+            // v - top as two floats (Knuth's two-sum), then its product with c
+            const float s = __fsub_rn(v, top), b = __fsub_rn(s, v);
+            const float e = __fsub_rn(__fsub_rn(v, __fsub_rn(s, b)), __fadd_rn(top, b));
+            const float m = __fmaf_rn(s, c, kMagic);
+            f = __fmaf_rn(e, c, __fmaf_rn(s, c_lo, __fmaf_rn(s, c, -__fsub_rn(m, kMagic))));
+            k = __float_as_int(m) - __float_as_int(kMagic);
+        }
+        // 2^(f / 256) - 1, |f| <= 1, as a multiple of 2^-30: what the sum with a number of 2^-7 keeps
+        constexpr double kG = 0.69314718055994530942 / 256;
+        constexpr float kA1 = static_cast<float>(kG), kA2 = static_cast<float>(kG * kG / 2);
+        constexpr float kA3 = static_cast<float>(kG * kG * kG / 6), kSplit = 1.5f / 128.0f;
+        constexpr uint32_t kSplitBits = 0x3c400000u;   // kSplit's
+        const float y = __fmul_rn(f, __fmaf_rn(f, __fmaf_rn(f, kA3, kA2), kA1));
+        const uint32_t one_y = __float_as_uint(__fadd_rn(y, kSplit)) + ((1u << 30) - kSplitBits);
+        // 2^60 times the weight less its power of two (where `least` was rounded down, k
+        // may be past the last bit)
+        const u64 m = static_cast<u64>(pow2[k & 255]) * one_y;
+        return v >= least ? m >> min(60 - bits - (k >> 8), 63) | 1ull : 0ull;
     }
     // Bin of a logit, kBins or more for one that has no weight: the float
     // operations are monotone, so the bins follow the order of the logits.
@@ -173,6 +275,8 @@ __device__ __forceinline__ void share(const Row &row, u64 *slot, u64 v) {
     sync_cluster();
 }
 
+__device__ __forceinline__ int digit_bits(const Row &row) { return row.bits == kFineBits ? 16 : 14; }
+
 __device__ __forceinline__ void clear_histogram(bool weigh, Shared &s) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
         if (weigh) s.digit[0][i] = s.digit[1][i] = s.digit[2][i] = 0u;
@@ -182,22 +286,23 @@ __device__ __forceinline__ void clear_histogram(bool weigh, Shared &s) {
 }
 
 // As many tokens at most as bin b of the first histogram holds, if they weigh w
-// together: its weights lie within 3 percent of each other, and 0.1 percent
+// together: its weights lie within 3.2 percent of each other, and 0.1 percent
 // covers the roundings of bins and weights. (2^20 where weights are so small that
-// being cut to integers counts.)
-__device__ __forceinline__ uint32_t most_in_bin(u64 w, int b) {
-    const float least = exp2f(-kNats / kBins * 1.4426950408889634f * (b + 1.0f)) * (kOne * 0.999f);
+// being rounded to integers counts.)
+__device__ __forceinline__ uint32_t most_in_bin(u64 w, int b, int bits) {
+    const float least = exp2f(static_cast<float>(bits) - kNats / kBins * 1.4426950408889634f * (b + 1.0f)) * 0.999f;
     return w == 0 ? 0u : least < 4096.0f ? 1u << 20 : static_cast<uint32_t>(fminf(static_cast<float>(w) / least, 1048576.0f));
 }
 
 // The cluster's histograms added up, in every CTA's tcnt and tw; with weights
 // tcnt is what most_in_bin says.
 __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Shared &s) {
+    const int d = digit_bits(row);
     if (row.size == 1) {
         __syncthreads();
         for (int i = threadIdx.x; i < kBins; i += kThreads) {
-            const u64 w = weigh ? (static_cast<u64>(s.digit[2][i]) << 28) + (static_cast<u64>(s.digit[1][i]) << 14) + s.digit[0][i] : 0;
-            s.tcnt[i] = weigh ? most_in_bin(w, i) : s.cnt[i];
+            const u64 w = weigh ? (static_cast<u64>(s.digit[2][i]) << (2 * d)) + (static_cast<u64>(s.digit[1][i]) << d) + s.digit[0][i] : 0;
+            s.tcnt[i] = weigh ? most_in_bin(w, i, row.bits) : s.cnt[i];
             s.tw[i] = w;
         }
         __syncthreads();
@@ -216,8 +321,8 @@ __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Share
         if (!weigh) {
             c += remote_ld32(dsmem_map(&s.cnt[bin], p));
         } else {
-            w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[2][bin], p))) << 28;
-            w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[1][bin], p))) << 14;
+            w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[2][bin], p))) << (2 * d);
+            w += static_cast<u64>(remote_ld32(dsmem_map(&s.digit[1][bin], p))) << d;
             w += remote_ld32(dsmem_map(&s.digit[0][bin], p));
         }
     }
@@ -225,7 +330,7 @@ __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Share
         if (!weigh) c += __shfl_xor_sync(0xffffffffu, c, o);
         else w += __shfl_xor_sync(0xffffffffu, w, o);
     }
-    if (weigh) c = most_in_bin(w, bin);
+    if (weigh) c = most_in_bin(w, bin, row.bits);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t p = 2 * part + h;
@@ -237,23 +342,34 @@ __device__ __forceinline__ void add_histograms(const Row &row, bool weigh, Share
 
 // Histogram of the row, of counts or (weigh) of weights: bin_of(logit) gives a
 // bin or a negative number for a token left out.
-template <typename F>
-__device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s, F bin_of) {
-    clear_histogram(weigh, s);
+template <bool WIDE, typename F>
+__device__ __forceinline__ void weigh_slice(const Row &row, Shared &s, F bin_of) {
+    const int d = digit_bits(row);
+    const uint32_t mask = (1u << d) - 1u;
 #pragma unroll 4
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
         const float v = row.l[i];
         const int bin = bin_of(v);
         if (bin < 0) continue;
-        if (!weigh) {
-            atomicAdd(&s.cnt[bin], 1u);
-        } else {
-            const u64 w = fixed_weight(row.weight(v));
-            const uint32_t d0 = static_cast<uint32_t>(w) & 0x3fffu, d1 = static_cast<uint32_t>(w >> 14) & 0x3fffu;
-            const uint32_t d2 = static_cast<uint32_t>(w >> 28);
-            if (d0) atomicAdd(&s.digit[0][bin], d0);
-            if (d1) atomicAdd(&s.digit[1][bin], d1);
-            if (d2) atomicAdd(&s.digit[2][bin], d2);
+        const u64 w = row.weight<WIDE>(v);
+        const uint32_t d0 = static_cast<uint32_t>(w) & mask, d1 = static_cast<uint32_t>(w >> d) & mask;
+        const uint32_t d2 = static_cast<uint32_t>(w >> (2 * d));
+        if (d0) atomicAdd(&s.digit[0][bin], d0);
+        if (d1) atomicAdd(&s.digit[1][bin], d1);
+        if (d2) atomicAdd(&s.digit[2][bin], d2);
+    }
+}
+template <typename F>
+__device__ __forceinline__ void histogram(const Row &row, bool weigh, Shared &s, F bin_of) {
+    clear_histogram(weigh, s);
+    if (weigh) {
+        if (row.wide) weigh_slice<true>(row, s, bin_of);
+        else weigh_slice<false>(row, s, bin_of);
+    } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < row.n; i += kThreads) {
+            const int bin = bin_of(row.l[i]);
+            if (bin >= 0) atomicAdd(&s.cnt[bin], 1u);
         }
     }
     add_histograms(row, weigh, s);
@@ -326,10 +442,10 @@ struct Cut {
     bool some;         // equals of the key are left out
 };
 
-// The tokens of a bin of weight w in which no token's exact weight lies below
-// `least`: as many at most (with room for that weight's roundings).
-__device__ __forceinline__ u64 most_tokens(u64 w, float least) {
-    const u64 one = fixed_weight(least), low = one - (one >> 14) - 1;
+// The tokens of a bin of weight w in which no token's exact weight lies below that
+// of `one`: as many at most (with room for that weight's roundings).
+__device__ __forceinline__ u64 most_tokens(u64 w, u64 one) {
+    const u64 low = one - (one >> 14) - 1;
     return one > 1 ? w / low + 1 : ~0ull;
 }
 
@@ -344,12 +460,12 @@ __device__ Cut cut_in_bin(const Row &row, Found f, bool by_weight, u64 target, u
     uint32_t lo = logit_key(row.top - (static_cast<float>(bin0) + 1.0f) / row.step - slack);
     hi = min(hi, logit_key(row.top));
     lo = min(max(lo, floor_key), hi);
-    if (by_weight) f.n = most_tokens(f.w, exp2f(-kNats / kBins * 1.4426950408889634f * (bin0 + 1.0f)));
+    if (by_weight) f.n = most_tokens(f.w, fixed_point(exp2f(-kNats / kBins * 1.4426950408889634f * (bin0 + 1.0f)), row.bits));
     while (f.n > kList) {
         if (lo == hi) {
             // equal logits, each of weight `one`
-            const u64 one = fixed_weight(row.weight(float_from_order_key(lo)));
-            const u64 m = by_weight ? (target - f.above_w + one - 1) / one : target - f.above_c;
+            const u64 one = row.weight(float_from_order_key(lo));
+            const u64 m = by_weight ? (target - f.above_w - 1) / one + 1 : target - f.above_c;
             return Cut{lo, m, f.above_w + m * one, by_weight ? m * one < f.w : m < f.n};
         }
         const int bits = 32 - __clz(hi - lo), shift = bits > 10 ? bits - 10 : 0;
@@ -375,7 +491,7 @@ __device__ Cut cut_in_bin(const Row &row, Found f, bool by_weight, u64 target, u
         u64 before_w = 0, mine = 0, w = 0;
         if (i < n) {
             mine = s.list[i];
-            w = fixed_weight(row.weight(float_from_order_key(static_cast<uint32_t>(mine >> 32))));
+            w = row.weight(float_from_order_key(static_cast<uint32_t>(mine >> 32)));
             s.list_w[i] = w;
         }
         __syncthreads();
@@ -429,22 +545,21 @@ __device__ __forceinline__ void answer(const SampleArgs &a, int b, int token, fl
         const float lo = __fsub_rn(__fsub_rn(v, __fsub_rn(d, z)), __fadd_rn(row.top, z));
         const float q = __fdiv_rn(d, T), r = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, T, d), lo), T);
         const float e = expf(q);
-        a.prob[b] = fmaf(e, r, e) * (kOne / static_cast<float>(total));
+        a.prob[b] = fmaf(e, r, e) * (exp2f(static_cast<float>(row.bits)) / static_cast<float>(total));
     }
 }
 
 // The row from its list alone (the first CTA): the top-k tokens are all in it,
 // or (k = 0) the tokens of weight p of the row's total `all`. Two threads to a
 // token, each looking at every other one.
-__device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, float p, float mp, u64 all, Shared &s) {
+__device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, float p, u64 mp, u64 all, Shared &s) {
     const int n = static_cast<int>(min(s.n_list, static_cast<uint32_t>(kList))), i = threadIdx.x >> 1, half = threadIdx.x & 1;
     u64 mine = 0, w = 0;
-    float v = 0.0f, e = 0.0f;
+    float v = 0.0f;
     if (i < n) {
         mine = s.list[i];
         v = float_from_order_key(static_cast<uint32_t>(mine >> 32));
-        e = row.weight(v);
-        w = fixed_weight(e);
+        w = row.weight(v);
         s.list_w[i] = w;
     }
     __syncthreads();
@@ -464,10 +579,10 @@ __device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, f
             u64 x = kept && !half ? w : 0, y = 0, none;
             scan2(x, y, all, none, s);
         }
-        const u64 target = static_cast<u64>(ceil(static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(all)));
+        const u64 target = share_of(p, all, true);
         kept = kept && (rank == 0 || before < target);
     }
-    kept = kept && e >= mp;
+    kept = kept && w >= mp;
     __syncthreads();
     if (i < n) s.list_w[i] = kept ? w : 0;
     u64 x = kept && !half ? w : 0, y = 0, total, none;
@@ -479,7 +594,7 @@ __device__ void finish_list(const SampleArgs &a, int b, const Row &row, u64 k, f
             if (static_cast<uint32_t>(s.list[j]) > idx) first += s.list_w[j];
     first += __shfl_xor_sync(0xffffffffu, first, 1);
     const float u = a.u[b];
-    u64 at = static_cast<u64>(static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(total));
+    u64 at = share_of(u, total, false);
     if (at >= total) at = total - 1;
     if (kept && !half && first <= at && at < first + w) answer(a, b, static_cast<int>(0xffffffffu - idx), v, row, total);
 }
@@ -549,8 +664,9 @@ template <bool kHeld>
 __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bool reorder) {
     extern __shared__ __align__(16) float held[];
     __shared__ Shared s;
-    pdl_wait();
     const int tid = threadIdx.x;
+    const uint32_t power = kPowers.v[tid & 255];
+    pdl_wait();
     const int size = static_cast<int>(gridDim.x);   // one cluster along x
     Row row;
     row.rank = size > 1 ? cluster_rank() : 0u;
@@ -563,6 +679,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     row.n = max(0, min(slice, a.V - row.base));
     const float *src = a.logits + b * a.stride + row.base;
     row.l = src;
+    row.bits = a.V < kFineVocab ? kFineBits : kCoarseBits;
+    row.pow2 = s.pow2;
+    const float T = a.temperature ? a.temperature[b] : 1.0f;
 
     // ---- the slice into shared memory: the 16-byte aligned middle as one bulk
     // copy, the ends by themselves, each value as far from a 16-byte boundary as in memory
@@ -582,6 +701,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
         for (int i = tid; i < head; i += kThreads) to[i] = src[i];
         for (int i = head + mid + tid; i < row.n; i += kThreads) to[i] = src[i];
         if (tid == 0) s.lost = 0u;
+        row.set_temperature(fmaxf(T, 1e-30f));
         __syncthreads();
         if (mid > 0 && !mbar_wait_bounded(&s.bar, 0u)) {
             // the copy did not arrive in a second: what there is of it is taken
@@ -595,6 +715,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
         }
     }
 
+    if constexpr (!kHeld) row.set_temperature(fmaxf(T, 1e-30f));
+    if (tid < 256) s.pow2[tid] = power;   // (barriers follow before its first use)
     // ---- the largest logit; a NaN counts above all
     float top = -INFINITY;
     bool nan = false;
@@ -613,8 +735,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
         for (int p = 0; p < size; ++p) best = s.peer[p] > best ? s.peer[p] : best;
     }
     row.top = float_from_order_key(static_cast<uint32_t>(best));
-    const float T = a.temperature ? a.temperature[b] : 1.0f;
-    const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f, mp = fminf(min_p, 1.0f);
+    const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f;
     const bool greedy = T <= 0.0f;
     // a setting that is not a number has no answer
     const bool bad = best == ~0u || row.top == -INFINITY || !(fabsf(T) < INFINITY) ||
@@ -639,9 +760,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
         }
         return;
     }
-    row.inv_t2 = 1.4426950408889634f / fmaxf(T, 1e-30f);
-    row.step = kBins / kNats / fmaxf(T, 1e-30f);
+    row.set_top(row.top, fmaxf(T, 1e-30f));
     const int k = a.top_k ? a.top_k[b] : 0;
+    const u64 mp = fixed_point(fminf(min_p, 1.0f), row.bits, true);
     // kept: every token with a weight, until a cut says otherwise
     Cut cut{0u, ~0ull, 0, false};
     const bool has_k = k > 0 && k < a.V;
@@ -667,7 +788,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
         u64 x = s.tw[2 * tid] + s.tw[2 * tid + 1], y = 0, total, none;
         scan2(x, y, total, none, s);
         if (cut.some) {
-            const u64 one = fixed_weight(row.weight(float_from_order_key(cut.key)));
+            const u64 one = row.weight(float_from_order_key(cut.key));
             u64 equals = 0;
             for (int i = tid; i < row.n; i += kThreads) equals += logit_key(row.l[i]) == cut.key;
             u64 z = 0, all;
@@ -679,7 +800,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
             }
             total -= (all - cut.ties) * one;
         }
-        u64 target = static_cast<u64>(ceil(static_cast<double>(fmaxf(p, 0.0f)) * static_cast<double>(total)));
+        u64 target = share_of(p, total, true);
         target = target < 1 ? 1 : (target < total ? target : total);
         __syncthreads();
         const Found f = find(true, target, 0, 0, s);
@@ -708,9 +829,10 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
     }
     // kept weight of a token; nth: its number among the equals of the cut's logit
     const float edge = cut.key ? float_from_order_key(cut.key) : -INFINITY;
+    row.least = fmaxf(row.least, edge);
     const auto weight = [&](float v, u64 nth) -> u64 {
-        const float e = row.weight(v);
-        return (v > edge || (v == edge && nth < cut.ties)) && e >= mp ? fixed_weight(e) : 0ull;
+        const u64 e = row.weight(v);
+        return (v > edge || (v == edge && nth < cut.ties)) && e >= mp ? e : 0ull;
     };
     u64 w = 0, none = 0, t0, t1;
     if (cut.some) {
@@ -721,11 +843,16 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
             seen += logit_key(v) == cut.key;
         }
     } else {
+        const auto sum = [&](auto wide) {
 #pragma unroll 4
-        for (int i = i0; i < i1; ++i) {
-            const float v = row.l[i], e = row.weight(v);
-            w += v >= edge && e >= mp ? fixed_weight(e) : 0ull;
-        }
+            for (int i = i0; i < i1; ++i) {
+                const float v = row.l[i];
+                const u64 e = row.weight<decltype(wide)::value>(v);
+                w += e >= mp ? e : 0ull;
+            }
+        };
+        if (row.wide) sum(std::true_type{});
+        else sum(std::false_type{});
     }
     const u64 mine = w;
     scan2(w, none, t0, t1, s);
@@ -740,7 +867,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
         }
     }
     const float u = a.u[b];
-    u64 at = static_cast<u64>(static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(total));
+    u64 at = share_of(u, total, false);
     if (at >= total) at = total - 1;
     w += before;
     // the warp whose lane holds the place looks through that lane's run, 32 tokens at a time
@@ -777,7 +904,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
 // each), or finer, to 16 CTAs, while the rows together leave SMs free (one row
 // without a cut 7.9 us in 16 CTAs, 9.6 in 8; 64 rows 53 and 32); beyond 16 slices
 // of what one SM holds the row is read again from memory (L2) at every pass.
-constexpr int kOneCta = 8192, kSlice = 20480, kMaxHeld = 45056;
+constexpr int kOneCta = 8192, kSlice = 20224, kMaxHeld = 45056;
 
 }  // namespace
 

@@ -295,3 +295,81 @@ def test_probabilities_of_small_weights(torch):
     token, prob, status = run(torch, x, 1 - p / 2, temperature=temp)
     assert status == 0 and np.all(token == 1)
     assert np.all(np.abs(prob - p) <= 8 * 2.0 ** -24 * p)
+
+
+def bound(V):
+    """How near a border a decision may lie and still be the f64 one: weights within
+    2^-29 of exact and rounded at 2^-46 of the largest (2^-40 from 2^18 tokens on), summed
+    on both sides of it."""
+    return 2 * (2.0 ** -29 + V * 2.0 ** (-46 if V < 2 ** 18 else -40))
+
+
+def model_rows(rng, B, V):
+    x = (rng.standard_normal((B, V)) * 2.2).astype(np.float32)
+    for row in x:
+        row[rng.integers(0, V, 400)] += (-2.5 * np.log(rng.random(400).clip(1e-6))).astype(np.float32)
+    return x
+
+
+def check_near(torch, logits, u, **kw):
+    """Tokens as in f64, probabilities within 8 f32 roundings, in all rows beyond the
+    bound; how many those are."""
+    token, prob, status = run(torch, logits, u, **kw)
+    clear = 0
+    for i, row in enumerate(logits):
+        t, p, margin = orc.sample_token(row, np.float32(u[i]), **{k: np.float32(v[i]) for k, v in kw.items()})
+        if margin > bound(len(row)):
+            clear += 1
+            assert token[i] == t, (i, int(token[i]), t, margin)
+            assert abs(prob[i] - p) <= (8 * 2.0 ** -24 + bound(len(row))) * p, (i, float(prob[i]), p)
+    assert status == 0
+    return clear
+
+
+@pytest.mark.parametrize("V", [20011, 151936, 300007])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 1.3])
+def test_draws_beside_a_border(torch, V, temperature):
+    """u a few 10^-8 of the total from where one token ends and the next begins."""
+    rng = np.random.default_rng([V, int(temperature * 10)])
+    B = 48
+    x = model_rows(rng, B, V)
+    u = np.empty(B, np.float32)
+    for i, row in enumerate(x.astype(np.float64)):
+        c = np.cumsum(np.exp((row - row.max()) / np.float64(np.float32(temperature))))
+        at = int(np.argmin(np.abs(c / c[-1] - 10.0 ** rng.uniform(-4, -0.5))))
+        u[i] = c[at] / c[-1] + rng.choice([-1, 1]) * rng.uniform(1, 4) * max(bound(V), 1e-9)
+    assert check_near(torch, x, u, temperature=[temperature] * B) >= 0.5 * B
+
+
+@pytest.mark.parametrize("V", [20011, 151936])
+@pytest.mark.parametrize("temperature", [0.9, 1.7])
+def test_top_p_beside_a_border(torch, V, temperature):
+    """top_p a few 10^-8 of the sum from where one more token is kept."""
+    rng = np.random.default_rng([V, int(temperature * 10), 1])
+    B = 48
+    x = model_rows(rng, B, V)
+    p = np.empty(B, np.float32)
+    for i, row in enumerate(x.astype(np.float64)):
+        c = np.cumsum(np.sort(np.exp((row - row.max()) / np.float64(np.float32(temperature))))[::-1])
+        at = int(np.argmin(np.abs(c / c[-1] - rng.uniform(0.3, 0.97))))
+        p[i] = c[at] / c[-1] + rng.choice([-1, 1]) * rng.uniform(1, 4) * bound(V)
+    # (p has 2^-25 to itself: some fall within the bound, or beyond the next border)
+    assert check_near(torch, x, rng.random(B).astype(np.float32), temperature=[temperature] * B, top_p=p) >= 0.5 * B
+
+
+def test_draws_at_large(torch):
+    """Rows over a whole vocabulary, drawn as they come: no token but f64's."""
+    from quantized_transformer_decode_gb300 import qw3
+    V, B = 151936, 64
+    x = torch.from_numpy(model_rows(np.random.default_rng(5), B, V)).cuda()
+    temp = torch.from_numpy(np.resize(np.float32([1.0, 0.7, 1.1, 2.0]), B)).cuda()
+    w = torch.exp((x.double() - x.double().amax(1, keepdim=True)) / temp.double()[:, None])
+    c = torch.cumsum(w, 1)
+    for seed in range(100):
+        u = torch.from_numpy(np.random.default_rng(seed).random(B).astype(np.float32)).cuda()
+        goal = u.double()[:, None] * c[:, -1:]
+        want = (c <= goal).sum(1)
+        near = ((c - goal).abs() < bound(V) * c[:, -1:]).any(1)
+        got = qw3.sample(x, u, temperature=temp)[0].long()
+        assert torch.equal(got[~near], want[~near])
+        assert int((got != want).sum()) == 0 or bool(near.any())
