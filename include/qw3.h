@@ -412,7 +412,7 @@ QW3_API int qw3_q8_0_gemm(const void *W_dev, int32_t rows, int32_t cols, const f
  * QW3_ERR_NONFINITE.
  *
  * data: 16-byte aligned device memory of qw3_kv_q4_bytes(). slots >= 1;
- * capacity a multiple of 32; n_kv_heads 1..64; head_dim 64 or 128. The buffer
+ * capacity a multiple of 32 up to 2^30; n_kv_heads 1..64; head_dim 64 or 128. The buffer
  * needs no initialisation: what lies past a sequence's length is not used. */
 typedef struct qw3_kv_q4 {
     void *data;

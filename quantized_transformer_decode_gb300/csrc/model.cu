@@ -1426,7 +1426,7 @@ int check_kv_q4(const qw3_kv_q4 *c, int n_heads) {
     if (!c || !c->data) return fail(nullptr, QW3_ERR_INVALID_ARG, "null cache");
     if (qw3_kv_q4_bytes(c->slots, c->capacity, c->n_kv_heads, c->head_dim) < 0)
         return fail(nullptr, QW3_ERR_SHAPE,
-                    "a cache needs slots >= 1, capacity % 32 == 0, 1 to 64 kv heads and head_dim 64 or 128");
+                    "a cache needs slots >= 1, capacity % 32 == 0 (up to 2^30), 1 to 64 kv heads and head_dim 64 or 128");
     if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads / c->n_kv_heads > kQ4MaxGroup)
         return fail(nullptr, QW3_ERR_SHAPE, "n_heads must be 1 to 16 times n_kv_heads");
     if (misaligned(c->data, 16)) return fail(nullptr, QW3_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
@@ -1458,7 +1458,7 @@ KvQ4 kv_q4_view(const qw3_kv_q4 *c) {
 }  // namespace
 
 int64_t qw3_kv_q4_bytes(int32_t slots, int32_t capacity, int32_t n_kv_heads, int32_t head_dim) {
-    if (slots < 1 || capacity < 32 || capacity % 32 || n_kv_heads < 1 || n_kv_heads > 64 ||
+    if (slots < 1 || capacity < 32 || capacity % 32 || capacity > kQ4MaxCapacity || n_kv_heads < 1 || n_kv_heads > 64 ||
         (head_dim != 64 && head_dim != 128))
         return -1;
     // at most 2^31 slots * 2 * 64 heads * 2^31 positions * 72 bytes: check that it fits

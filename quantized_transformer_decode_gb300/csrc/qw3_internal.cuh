@@ -328,6 +328,7 @@ struct KvQ4AttnArgs {
     int32_t *status;   // nullable
 };
 constexpr int kQ4MaxRows = 16, kQ4MaxGroup = 16;
+constexpr int kQ4MaxCapacity = 1 << 30;   // positions and the steps past their end stay within 31 bits
 int kv_q4_attn_launches(int B, int rows, int nh, int nkv, int hd, int max_len);
 size_t kv_q4_attn_workspace_bytes(int B, int rows, int nh, int nkv, int hd, int max_len);
 cudaError_t configure_kv_q4();

@@ -35,6 +35,15 @@ def test_cache_bytes(L):
         assert b(*bad) == -1, bad
 
 
+def test_the_longest_capacity(L):
+    """Positions are counted in 31 bits, with room for the last step past the end."""
+    assert L.qw3_kv_q4_bytes(1, 1 << 30, 1, 64) == 2 * (1 << 30) * 36
+    assert L.qw3_kv_q4_bytes(1, (1 << 30) + 32, 1, 64) == -1 and L.qw3_kv_q4_bytes(1, 2147483616, 1, 64) == -1
+    c = cache(capacity=2147483616, slots=1, n_kv_heads=1)
+    assert append(L, c) == SHAPE and L.qw3_kv_q4_read(c, 1, 16, 0, 16, 0, 16, 16, None) == SHAPE
+    assert L.qw3_kv_q4_attn(c, 16, 256, 1, None, 16, 1, 1, 2147483616, 0.1, 16, 256, 16, 1 << 40, None, None) == SHAPE
+
+
 APPEND = dict(qkv=16, M=4, stride=512, nh=4, qn=16, kn=16, eps=1e-6, rope=16, slots=16, slot0=0, pos=16, pos0=0,
               out=16, ostride=256, status=None)
 
