@@ -479,7 +479,7 @@ QW3_API int qw3_kv_q4_attn(const qw3_kv_q4 *cache, const float *q_dev, int64_t q
                            int64_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /* ---- Sampling --------------------------------------------------------------
- * One token from each of B rows of logits (f32 [B][stride], V values used,
+ * One token from each of B <= 2^30 rows of logits (f32 [B][stride], V values used,
  * 1 <= V <= 4194304), beside the greedy argmax of "A transformer from
  * scratch", 12.6. With w_i = exp((l_i - max l) / temperature) and the tokens
  * ordered by (l descending, index ascending), in this order:

@@ -1548,6 +1548,7 @@ int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, co
                int32_t *token_dev, float *prob_dev, int32_t *status_dev, void *stream) {
     if (B < 0 || (B > 0 && (!logits_dev || !u_dev || !token_dev)))
         return fail(nullptr, QW3_ERR_INVALID_ARG, "bad sample arguments");
+    if (B > kSampleMaxRows) return fail(nullptr, QW3_ERR_SHAPE, "sampling takes up to 2^30 rows");
     if (V < 1 || V > kSampleMaxVocab || stride < V) return fail(nullptr, QW3_ERR_SHAPE, "1 <= V <= 4194304, V <= stride");
     if (misaligned(logits_dev, 4) || misaligned(temperature_dev, 4) || misaligned(top_k_dev, 4) ||
         misaligned(top_p_dev, 4) || misaligned(min_p_dev, 4) || misaligned(u_dev, 4) || misaligned(token_dev, 4) ||

@@ -336,6 +336,7 @@ cudaError_t launch_kv_q4_attn(const KvQ4AttnArgs &a, int hd, bool pdl, cudaStrea
 
 // ---- sampling (sample.cu)
 constexpr int kSampleMaxVocab = 1 << 22;   // sums of 2^40 each stay below 2^63
+constexpr int kSampleMaxRows = 1 << 30;    // rows are taken 65535 at a time: the count past the last stays within 31 bits
 struct SampleArgs {
     const float *logits;   // [B][stride]
     int64_t stride;

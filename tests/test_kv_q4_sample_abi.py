@@ -135,6 +135,11 @@ def test_sample_refusals(L, kw, want):
                         a["token"], a["prob"], a["status"], None) == want
 
 
+def test_sample_takes_up_to_two_to_the_thirty_rows(L):
+    for B in ((1 << 30) + 1, 2147483647):
+        assert L.qw3_sample(16, 100, B, 100, None, None, None, None, 16, 16, None, None, None) == SHAPE
+
+
 def test_wrappers_check_before_they_allocate():
     with pytest.raises(qw3.Qw3Error) as e:
         qw3.KVCacheQ4(1, 33, 1, 64)
