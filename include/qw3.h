@@ -457,8 +457,9 @@ QW3_API int64_t qw3_kv_q4_attn_workspace_bytes(int32_t B, int32_t rows, int32_t 
 /* Grouped-query causal attention of `rows` query rows (1..16) of each of B
  * sequences over the cache: q_dev f32 [B * rows][q_stride] (normalised and
  * rotated), out_dev f32 [B * rows][out_stride], n_heads * head_dim values
- * each (out_dev may be q_dev itself with its stride, no other overlap); query head h reads kv head h / (n_heads / n_kv_heads), a group of at
- * most 16. Sequence b lies in slot slots_dev[b] (slot b where slots_dev is
+ * each (out_dev may be q_dev itself with its stride, no other overlap); query
+ * head h reads kv head h / (n_heads / n_kv_heads), a group of at most 16.
+ * Sequence b lies in slot slots_dev[b] (slot b where slots_dev is
  * NULL) and holds lens_dev[b] positions, its `rows` newest among them: row t
  * is at position p = lens_dev[b] - rows + t and attends positions 0..p,
  *     out = sum_j softmax_j(scale * q . K[j]) V[j].

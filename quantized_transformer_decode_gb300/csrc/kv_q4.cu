@@ -355,8 +355,8 @@ struct Q4AppendArgs {
 // A warp takes TPW heads of a row, one after another, their loads first: one
 // for a few rows (every warp of the GPU has something to do), four for many
 // (four loads in flight for each warp). A row is read once and its queries
-// written once: 4096 rows of 48 heads of 128 (172 MB, a floor of 25 us) take 46
-// us, 0.55 of the measured copy rate. What bounds it there: waiting for loads (the
+// written once: 4096 rows of 48 heads of 128 (172 MB, a floor of 25 us) take 47
+// us, 0.54 of the measured copy rate. What bounds it there: waiting for loads (the
 // rotation's depends on the position's) at 32 warps to an SM, a third of the
 // issue slots; more warps in fewer registers (40 to 56 a thread) or two heads to
 // a warp are no faster. Few rows: the launch and two loads in a row.
@@ -364,7 +364,7 @@ template <int HD, int TPW, bool VEC>
 __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
     constexpr int E = Q4Row<HD>::E, L = Q4Row<HD>::L, NB = Q4Row<HD>::NB;
     // many rows pass through L2 once and leave it first (with the rows' reading back
-    // 55.4 us against 58.6 with plain accesses)
+    // 55.5 us against 58.6 with plain accesses)
     constexpr bool kMany = TPW > 1;
     const int lane = threadIdx.x & 31;
     const int task0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * TPW, row = blockIdx.x;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
         if (fits) {
 #pragma unroll
             for (int t = 0; t < TPW; ++t) {
-                const float r = rsqrtf(ss[t]);
+                const float r = rsqrtf(ss[t]);   // within 2 roundings: queries are f32 sums anyway
                 float y[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(128, 8) k_kv_q4_append(Q4AppendArgs a) {
 
 // A block per row, four values of one head of K and of V to a thread: a warp
 // writes whole rows. Bound by the f32 values written, which leave L2 first
-// (8192 rows of 8 heads, 67 MB: 17.5 us a call, 22.2 with plain stores).
+// (8192 rows of 8 heads, 67 MB: 17.2 us a call, 22.2 with plain stores).
 template <int HD, bool VEC>
 __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M, float *__restrict__ k_out,
                                                     float *__restrict__ v_out, size_t out_row, size_t out_head) {
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 //    operands with 9 instructions and no scale. K scales multiply the f32 sums
 //    of a 32-value block, V scales the probabilities of their position.
 //  - f16 keeps 11 bits, so q and p v_scale go in as two parts, hi + lo (22
-//    bits), in columns of their own: of the 8 columns of an operand 4 are hi
+//    bits: less than f32, and below its sums' own error), in columns of their own: of the 8 columns of an operand 4 are hi
 //    and 4 lo where that is enough; else hi and lo take an operand each. With
 //    2 columns or 1 the spare columns hold P times the scales of other blocks.
 //  - q columns are scaled by a power of two (largest value in [2^14, 2^15)),
@@ -561,8 +561,8 @@ __global__ void __launch_bounds__(256) k_kv_q4_read(KvQ4 c, KvQ4Rows rows, int M
 // FMA compete (8 mma and 64 FMA take the sum of their times, not the longer). A
 // warp's tile of 4.6 KB takes some 750 instructions (830 at 8 columns: unpacking,
 // the split of P, the softmax); the copies alone would take 29 of the 43 us of 64
-// sequences of 2048 positions (32/8 heads, 151 MB; 3.5 TB/s, 0.52 of the measured
-// copy rate), the instructions alone 38.
+// sequences of 2048 positions (47 with a graph's launch, as all times below; 32/8
+// heads, 151 MB; 3.5 TB/s, 0.52 of the measured copy rate), the instructions alone 38.
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
@@ -598,7 +598,8 @@ __device__ __forceinline__ uint32_t pack_rz(float a, float b) {
     return r;
 }
 
-// Codes less 8 of a word's nibbles as half2: h[p] = (nibble p, nibble p + 4).
+// Codes less 8 of a word's nibbles as half2: h[p] = (nibble p, nibble p + 4), by the
+// widely published way to turn nibbles into halves: under the exponent of 1024.
 // 0x6400 | n is 1024 + n in f16, 0x6400 | n << 4 is 1024 + 16 n.
 // `magic` is 0x64006400 in a register (q4_magic), so that mask and or are one
 // three-operand instruction.
@@ -647,9 +648,9 @@ __device__ __forceinline__ int q4_len(const KvQ4AttnArgs &a, int b) {
 __host__ __device__ constexpr int q4_ops(int W) { return W <= 4 ? 1 : 2; }
 
 // CTAs of kQ4Warps warps that share an SM: three in 168 registers, two where 8
-// columns of 128 dimensions want 254 (three spill: 4 x 5000 with 16 rows 66 us
-// against 64; at 64 dimensions three are faster, 30 x 4000 with 4 rows 27 against
-// 29). Four in 128 spill too: 64 x 2048 with 32/8 heads 51 us against 47.
+// columns of 128 dimensions want 254 (three spill: 4 x 5000 with 16 rows and 32/8
+// heads 68 us against 64; at 64 dimensions three are faster, 30 x 4000 with 4 rows
+// 57 against 64). Four in 128 spill too: 64 x 2048 with 32/8 heads 51 us against 47.
 __host__ __device__ constexpr int q4_per_sm(int hd, int W) { return W <= 4 || hd <= 64 ? 3 : 2; }
 
 template <int HD>
@@ -682,7 +683,7 @@ __device__ __forceinline__ int q4_query_exp(float amax) {
 // weights' unit. P is cut at 2^-24 where its largest product lies in [2^12,
 // 2^15]: these 2 bits and one of the V scale's rounding up to a power of two.
 // More room costs precision beside tokens with far larger values and gains
-// little: 24 x 8192 with 5 rows 197 us with none, 193 with 2 bits, 191 with 6.
+// little: 24 x 8192 with 5 rows 197 us with none, 192 with 2 bits, 190 with 6.
 constexpr float kRoom = 2.0f;
 
 // A warp's tile in shared memory: codes of K, of V, scales of K, of V. Each
@@ -700,7 +701,7 @@ template <int HD>
 __host__ __device__ constexpr int q4_part() { return HD + 2; }
 
 // What a unit costs besides its blocks (its queries, the joining of its warps),
-// in blocks (64 sequences of 1 to 4101 positions, 16/8 heads: 47 us at 2, 51 at
+// in blocks (64 sequences of 1 to 4101 positions, 16/8 heads: 45 us at 2, 51 at
 // 1, 62 at 0).
 constexpr int kQ4UnitCost = 2;
 
@@ -1390,8 +1391,8 @@ cudaError_t launch_kv_q4_append(const float *qkv, int M, int64_t qkv_stride, con
     const bool vec = aligned16(qkv) && aligned16(q_norm) && aligned16(k_norm) && aligned16(rope) && aligned16(q_out) &&
                      qkv_stride % 4 == 0 && q_stride % 4 == 0;
     // four heads to a warp once one to a warp would fill the GPU's 64 warps per
-    // SM four times (a call with the rows' reading back: 4096 rows of 48 heads 59
-    // us against 93, 2048 of 20 16.6 against 18.7; 128 of 32 12.1 against 10.3)
+    // SM four times (a call with the rows' reading back: 4096 rows of 48 heads 56
+    // us against 100, 2048 of 20 of 64 16.1 against 20.5; 128 of 32 10.3 against 8.9)
     const bool four = static_cast<int64_t>(M) * tasks >= 4ll * 64 * 152;
     const auto go = [&](auto hd_, auto tpw_, auto vec_) {
         constexpr int T = decltype(tpw_)::value;
@@ -1437,12 +1438,14 @@ Q4Plan q4_plan(int B, int rows, int nh, int nkv, int hd, int max_len) {
     const int64_t units = static_cast<int64_t>(std::max(B, 1)) * nkv * p.cgroups;
     const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4Block - 1) / kQ4Block);
     // Clusters while all of them fit at once (against dealing out blocks, with its
-    // second kernel: 1 x 517 8.3 us and 12.4, 4 x 8000 19.2 and 22.5): with an SM to
-    // each CTA, whose threads then have 255 registers, else two CTAs to an SM in 128
-    // (16 x 2000 16.4 us against 18.5). A warp takes eight tiles at most, five where
-    // the clusters leave room for more CTAs (1 x 8317 14.4 us against 16.4; but
-    // 1 x 32000 27.6 in clusters, 22.6 dealt out). The sizes are powers of two; a GPC of 18 or 20
-    // SMs holds one or two clusters of 8 and one of 16 at most.
+    // second kernel: 1 x 517 with 16/8 heads 8.3 us and 13.7, 4 x 8000 with 32/8 19.2
+    // and 21.3): with an SM to each CTA, whose threads then have 255 registers (16 x
+    // 2000 with 16/8 16.5 us, 18.5 in two CTAs to an SM), else two CTAs to an SM in 128
+    // (24 x 500 with 16/8 12.3 us, dealt out 16.4; 36 x 1000 with 32/8 18.9 and 24.4). A
+    // warp takes eight tiles at most, five where the clusters leave room for more CTAs
+    // (1 x 8317 with 32/8 14.4 us, dealt out 16.4; but 1 x 32000 with 16/8 26.8 in
+    // clusters, 22.6 dealt out). The sizes are powers of two; a GPC of 18 or 20 SMs
+    // holds one or two clusters of 8 and one of 16 at most.
     constexpr int kFit[2][5] = {{152, 76, 36, 15, 0}, {304, 152, 74, 36, 14}};
     const int64_t need = std::max<int64_t>(1, (static_cast<int64_t>(max_len) + kQ4ClusterWarps * kQ4Tile - 1) / (kQ4ClusterWarps * kQ4Tile));
     for (int per_sm = 1; per_sm <= (p.W <= 4 ? 2 : 1) && !p.csize; ++per_sm) {
@@ -1513,7 +1516,7 @@ cudaError_t launch_q4_attn_hd(const KvQ4AttnArgs &a, const Q4Plan &p, bool pdl, 
     }
     if (e != cudaSuccess || p.whole) return e;
     // a unit's results, eight at a time where there are many: 1 x 100000 with 8/1
-    // heads 31 us against 90, 4 x 20000 with 32/8 (14 results) 33 against 37, but 1 x
+    // heads 31 us against 90, 4 x 20000 with 32/8 (14 results) 33 against 36, but 1 x
     // 8000 with 16 rows (5 results) 37 against 35
     const unsigned joins = static_cast<unsigned>(a.nh) * a.rows * a.B;
     const bool many = p.ctas >= 8ll * a.B * a.c.nkv * p.cgroups;

@@ -21,12 +21,12 @@
 // vocabulary's logits fill evenly, so that few of a warp's additions meet in one
 // word; if what top-p keeps fits the list, it is listed, else the cut's bin alone
 // is ranked, or cut further by histograms over its keys until it holds at most
-// kList tokens or equal logits only. What bounds it: the passes over the slices in shared
-// memory (some 20 instructions a token where weights are summed) and, for one
-// row, the barriers between them. Measured: one row of 151936 with temperature,
-// top-k 20, top-p 0.95 and min-p 12 us; 64 such rows 32 us, without a cut 32 us
-// (39 MB, 1.2 TB/s), with top-p alone 53 us where that keeps few tokens and 80 us
-// where it keeps much of the row.
+// kList tokens or equal logits only. What bounds it: the passes over the slices in
+// shared memory (some 35 instructions a token where weights are summed) and, for one
+// row, the barriers between them. Measured (a graph's launch included): one row of
+// 151936 with temperature, top-k 20, top-p 0.95 and min-p 14.4 us; 64 such rows 37 us,
+// without a cut 37 us (39 MB, 1.1 TB/s), with top-p alone 55 us where that keeps few
+// tokens, 92 us at 0.92 of a spread-out row and 111 us at 0.92 of a flat one.
 //
 // Sums are taken in 64-bit fixed point (2^46 for the largest weight): they are
 // the same whatever the order of the additions, so one input gives one token.
@@ -898,11 +898,11 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a, int slice, bo
 }
 
 // CTAs per row and the tokens of one: a small vocabulary stays in one CTA (64
-// rows of 8192 with top-k and top-p 10.5 us, 12.5 in two CTAs), a large one is
-// cut into slices of which two fit an SM (up to 20480 tokens, 80 KB: 64 rows of
-// 151936 with settings of their own 51 us, 65 in 4 CTAs each that take an SM
+// rows of 8192 with top-k and top-p 10.3 us, 12.3 in two CTAs), a large one is
+// cut into slices of which two fit an SM (up to 20224 tokens, 79 KB: 64 rows of
+// 151936 with settings of their own 47 us, 71 in 4 CTAs each that take an SM
 // each), or finer, to 16 CTAs, while the rows together leave SMs free (one row
-// without a cut 7.9 us in 16 CTAs, 9.6 in 8; 64 rows 53 and 32); beyond 16 slices
+// without a cut 12.3 us in 16 CTAs, 13.9 in 8; 64 rows 52 and 37); beyond 16 slices
 // of what one SM holds the row is read again from memory (L2) at every pass.
 constexpr int kOneCta = 8192, kSlice = 20224, kMaxHeld = 45056;
 
@@ -925,10 +925,10 @@ cudaError_t launch_sample(const SampleArgs &a, int B, bool pdl, cudaStream_t s) 
     const int slice = (a.V + size - 1) / size;
     const bool is_held = slice <= kMaxHeld;
     // Settings that differ from row to row, in more than one wave (two CTAs to an
-    // SM): 64 rows of 151936 45 us against 53, 400 of 32000 58 against 67, 512 of
-    // 8192 28 against 33. Finding its row costs a CTA two microseconds, which rows
-    // of the same settings pay for nothing: 31 us against 29, 43 against 39, 22
-    // against 19.
+    // SM): 64 rows of 151936 47 us against 62, 400 of 32000 58 against 61, 512 of
+    // 8192 29 against 32. Finding its row costs a CTA two microseconds, which rows
+    // of the same settings pay for nothing: 37 us against 34, 51 against 46, 27
+    // against 24.
     const bool reorder = static_cast<int64_t>(B) * size > 2 * 152 && B <= kThreads && (a.top_p || a.top_k);
     for (int b0 = 0; b0 < B; b0 += 65535) {
         SampleArgs x = a;
