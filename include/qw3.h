@@ -507,6 +507,130 @@ QW3_API int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32
                        const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
                        int32_t *token_dev, float *prob_dev, int32_t *status_dev, void *stream);
 
+/* ---- The paged KV cache -----------------------------------------------------
+ * A cache of f16 rows (the default cache type of "A transformer from scratch",
+ * 12.4) in pages of a pool that many sequences share, for callers that run
+ * their own layers over ragged batches: prompts, chunks of prompts and single
+ * tokens in one call.
+ *
+ * Layout: f16 [page][K|V][kv head][page_size][head_dim]: the positions of a
+ * page that one head reads are contiguous. data: 16-byte aligned device memory
+ * of qw3_kv_paged_bytes(); page_size 16, 32, 64, 128 or 256; n_kv_heads 1..64;
+ * head_dim 64 or 128; n_pages * 2 * n_kv_heads * page_size below 2^31. The pool
+ * needs no initialisation: what no sequence holds is not used. */
+typedef struct qw3_kv_paged {
+    void *data;
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+} qw3_kv_paged;
+
+/* A ragged batch of B sequences, on the device. Rows starts_dev[b] ..
+ * starts_dev[b + 1] - 1 of a call's activations (starts_dev: int32 [B + 1], not
+ * decreasing; values outside 0..M are taken as the nearest inside) are the n_b
+ * newest tokens of sequence b, which holds lens_dev[b] positions with them: row
+ * t of its rows is at position lens_dev[b] - n_b + t. Position p lies in page
+ * table_dev[b * table_stride + p / page_size] (int32; pages_per_seq entries for
+ * each sequence, those that no position needs are not read). A position whose
+ * entry lies outside the pool (-1, say), or past pages_per_seq pages, is not in
+ * the cache. Rows before starts_dev[0] and from starts_dev[B] on belong to no
+ * sequence, and what a call would write for them is left as it was. */
+typedef struct qw3_kv_batch {
+    const int32_t *starts_dev;
+    const int32_t *lens_dev;
+    const int32_t *table_dev;
+    int64_t table_stride;
+    int32_t B;
+    int32_t pages_per_seq;
+} qw3_kv_batch;
+
+/* The type of a call's activations; what is computed from them is f32. */
+enum qw3_type { QW3_F32 = 0, QW3_F16 = 1 };
+
+/* Bytes of a pool of these sizes, or -1 if one of them cannot be taken. */
+QW3_API int64_t qw3_kv_paged_bytes(int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim);
+
+/* Append the batch's rows. qkv_dev: `type` [M][qkv_stride] (strides in values),
+ * each row the raw projections of n_heads query heads, then the key heads, then
+ * the value heads. Queries and keys take x / sqrt(mean(x^2) + eps) * w per head
+ * ("Qwen3 Support Plan (dense)", 2.2; q_norm_dev, k_norm_dev: f32 [head_dim],
+ * each nullable: no norm), then the NeoX rotation of their position ("A
+ * transformer from scratch", 12.3.4) with rope_dev (f32 [rope_len][head_dim /
+ * 2][2]: cos, sin). The queries go to q_out_dev (`type` [M][q_stride]; may be
+ * qkv_dev itself with its stride, no other overlap), keys and values to the
+ * cache, each rounded once, to nearest even. A row whose position is not in the
+ * cache (above), is negative or is not below rope_len is not cached, and its
+ * q_out row is zeros. A key or value head that holds NaN, an infinity or a
+ * magnitude that f16 does not hold (65520 or more) is written as zeros and, if
+ * status_dev is not NULL, *status_dev is set to QW3_ERR_NONFINITE. Norms are
+ * f32; a head whose squares leave f32 is normalised in f64.
+ * No two rows of a call may name the same place (two sequences may share pages
+ * that hold only older positions of both). n_heads 1 to 16 times n_kv_heads.
+ * qkv_dev, q_out_dev 16-byte aligned, their strides multiples of 16 bytes.
+ * Asynchronous on `stream`. */
+QW3_API int qw3_kv_paged_append(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int32_t type,
+                                const void *qkv_dev, int32_t M, int64_t qkv_stride, int32_t n_heads,
+                                const float *q_norm_dev, const float *k_norm_dev, float eps, const float *rope_dev,
+                                int32_t rope_len, void *q_out_dev, int64_t q_stride, int32_t *status_dev,
+                                void *stream);
+
+/* Workspace bytes of qw3_kv_paged_attn for these sizes (may be 0), or -1 if one
+ * of them cannot be taken. */
+QW3_API int64_t qw3_kv_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t type, int32_t n_heads,
+                                                  int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
+                                                  int32_t max_len, int32_t window, int32_t sinks);
+
+/* Grouped-query causal attention ("A transformer from scratch", 12.3.5) of the
+ * batch's rows over the cache, their own positions among it: q_dev `type`
+ * [M][q_stride] (normalised and rotated), out_dev `type` [M][out_stride],
+ * n_heads * head_dim values each (out_dev may be q_dev itself with its stride,
+ * no other overlap); query head h reads kv head h / (n_heads / n_kv_heads), a
+ * group of at most 16. A row at position p attends the positions j <= p that are
+ * in the cache and, where window > 0, that lie in its window (j > p - window) or
+ * among the first `sinks` positions (j < sinks):
+ *     out = sum_j softmax_j(scale * q . K[j]) V[j].
+ * A row that attends to nothing (p < 0 among them) is zeros. Nothing that a row
+ * does not attend to has a part in it, be it NaN or infinite.
+ * Row counts and lengths are read on the device, and taken as at most max_rows
+ * (a sequence's rows past it are left as they were) and max_len (at most
+ * pages_per_seq * page_size; QW3_ERR_KV_OVERFLOW), which decide how the work is
+ * split: upper bounds close to the largest are best. max_rows <= M.
+ * With f32 activations queries and weights enter the tensor cores in two f16
+ * parts (22 bits) and the sums are f32; with f16 the weights are rounded to f16
+ * (11 bits), the sums are f32 and the output is rounded once.
+ * workspace_dev: 16-byte aligned, qw3_kv_paged_attn_workspace_bytes() or more, of
+ * any content, not used by another call until this one has completed (two graphs
+ * that may run at once need a workspace each). Equal calls give equal results.
+ * If a bounded wait in a kernel runs out and status_dev is not NULL, *status_dev
+ * becomes QW3_ERR_TIMEOUT and the outputs are not valid. q_dev, out_dev 16-byte
+ * aligned, their strides multiples of 16 bytes. Asynchronous on `stream`. */
+QW3_API int qw3_kv_paged_attn(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int32_t type, const void *q_dev,
+                              int32_t M, int64_t q_stride, int32_t n_heads, int32_t max_rows, int32_t max_len,
+                              int32_t window, int32_t sinks, float scale, void *out_dev, int64_t out_stride,
+                              void *workspace_dev, int64_t workspace_bytes, int32_t *status_dev, void *stream);
+
+/* ---- Log probabilities -------------------------------------------------------
+ * What B <= 2^30 rows of logits (f32 [B][stride], V values used, 1 <= V <=
+ * 4194304) say about given tokens: with log Z = log sum_i exp(l_i),
+ *   logprob_dev [B][T]   l_t - log Z of the T given tokens of the row (tokens_dev
+ *                        int32 [B][T]; T = 0: none); a token outside 0..V-1 (-1,
+ *                        say) has none: -inf;
+ *   entropy_dev [B]      -sum_i p_i log p_i in nats, p_i = exp(l_i - log Z);
+ *                        nullable;
+ *   top_id_dev, top_logprob_dev [B][top]   the `top` (0..64) most likely tokens,
+ *                        largest logit first, the lower index among equal ones;
+ *                        places past the tokens with a logit above -inf hold
+ *                        id -1 and -inf.
+ * Sums are f32 with the largest logit's own term apart, so that log p of a token
+ * of almost all the probability keeps its digits. A row with a NaN or +inf, or
+ * without a logit above -inf, has no answer: NaN, ids -1 and, if status_dev is
+ * not NULL, *status_dev = QW3_ERR_NONFINITE. Buffers 4-byte aligned. Equal
+ * calls give equal results. Asynchronous on `stream`. */
+QW3_API int qw3_logprobs(const float *logits_dev, int64_t stride, int32_t B, int32_t V, const int32_t *tokens_dev,
+                         int32_t T, int32_t top, float *logprob_dev, float *entropy_dev, int32_t *top_id_dev,
+                         float *top_logprob_dev, int32_t *status_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -82,6 +82,8 @@ cudaError_t configure_all() {
         if (e == cudaSuccess) e = configure_attn_prefill_tc();
         if (e == cudaSuccess) e = configure_sample();
         if (e == cudaSuccess) e = configure_kv_q4();
+        if (e == cudaSuccess) e = configure_kv_paged();
+        if (e == cudaSuccess) e = configure_logprobs();
         g_cfg_err[dev] = e;
         g_cfg_done[dev].store(true, std::memory_order_release);
     }
@@ -1559,6 +1561,152 @@ int qw3_sample(const float *logits_dev, int64_t stride, int32_t B, int32_t V, co
     if (B == 0) return QW3_OK;
     QW3_CUDA_TRY(configure_all());   // the kernel's shared-memory limit
     QW3_CUDA_TRY(launch_sample(a, B, true, static_cast<cudaStream_t>(stream)));
+    return QW3_OK;
+}
+
+namespace {
+
+// Checks of a paged cache, a ragged batch and a head count over them.
+int check_kv_paged(const qw3_kv_paged *c, const qw3_kv_batch *b, int type, int M, int n_heads) {
+    if (!c || !c->data || !b) return fail(nullptr, QW3_ERR_INVALID_ARG, "null cache or batch");
+    if (type != QW3_F32 && type != QW3_F16) return fail(nullptr, QW3_ERR_INVALID_ARG, "activations are QW3_F32 or QW3_F16");
+    if (qw3_kv_paged_bytes(c->n_pages, c->page_size, c->n_kv_heads, c->head_dim) < 0)
+        return fail(nullptr, QW3_ERR_SHAPE,
+                    "a pool needs n_pages >= 1, page_size 16 to 256 (a power of two), 1 to 64 kv heads, head_dim 64 or 128, "
+                    "and fewer than 2^31 rows");
+    if (n_heads < 1 || n_heads % c->n_kv_heads || n_heads / c->n_kv_heads > kPagedMaxGroup)
+        return fail(nullptr, QW3_ERR_SHAPE, "n_heads must be 1 to 16 times n_kv_heads");
+    if (misaligned(c->data, 16)) return fail(nullptr, QW3_ERR_INVALID_ARG, "the pool must be 16-byte aligned");
+    if (M < 0 || b->B < 0 || b->pages_per_seq < 0) return fail(nullptr, QW3_ERR_INVALID_ARG, "a negative count");
+    if (b->B > 0 && (!b->starts_dev || !b->lens_dev || (b->pages_per_seq > 0 && !b->table_dev)))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "null batch arrays");
+    if (b->table_stride < b->pages_per_seq) return fail(nullptr, QW3_ERR_SHAPE, "table_stride is shorter than pages_per_seq");
+    if (misaligned(b->starts_dev, 4) || misaligned(b->lens_dev, 4) || misaligned(b->table_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "the batch's arrays must be 4-byte aligned");
+    if (static_cast<int64_t>(b->pages_per_seq) * c->page_size > kPagedMaxLen)
+        return fail(nullptr, QW3_ERR_SHAPE, "a sequence holds at most 2^30 positions");
+    if (b->B > kPagedMaxBatch) return fail(nullptr, QW3_ERR_SHAPE, "a batch holds at most 2^20 sequences");
+    if (static_cast<int64_t>(M) * (n_heads + 2 * c->n_kv_heads) > INT32_MAX)
+        return fail(nullptr, QW3_ERR_SHAPE, "M * (n_heads + 2 n_kv_heads) must fit in 31 bits");
+    return QW3_OK;
+}
+
+// Rows of activations: 16-byte aligned, the stride too, and no shorter than `width` values.
+int check_rows(const void *p, int64_t stride, int64_t width, int type) {
+    if (stride < width) return fail(nullptr, QW3_ERR_SHAPE, "a row stride is shorter than its heads");
+    if (misaligned(p, 16) || stride % (type == QW3_F32 ? 4 : 8))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "activations and their strides must be 16-byte aligned");
+    return QW3_OK;
+}
+
+KvPaged kv_paged_view(const qw3_kv_paged *c) {
+    KvPaged v;
+    v.data = static_cast<__half *>(c->data);
+    v.pages = c->n_pages;
+    while (1 << v.shift < c->page_size) ++v.shift;
+    v.nkv = c->n_kv_heads;
+    return v;
+}
+
+KvBatch kv_batch_view(const qw3_kv_batch *b, int M, int max_rows, int max_len) {
+    return {b->starts_dev, b->lens_dev, b->table_dev, b->table_stride, b->B, b->pages_per_seq, M, max_rows, max_len};
+}
+
+}  // namespace
+
+int64_t qw3_kv_paged_bytes(int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim) {
+    if (n_pages < 1 || page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) || n_kv_heads < 1 ||
+        n_kv_heads > 64 || (head_dim != 64 && head_dim != 128))
+        return -1;
+    const int64_t rows = static_cast<int64_t>(n_pages) * 2 * n_kv_heads * page_size;
+    return rows > INT32_MAX ? -1 : rows * head_dim * 2;
+}
+
+int qw3_kv_paged_append(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int32_t type, const void *qkv_dev,
+                        int32_t M, int64_t qkv_stride, int32_t n_heads, const float *q_norm_dev,
+                        const float *k_norm_dev, float eps, const float *rope_dev, int32_t rope_len, void *q_out_dev,
+                        int64_t q_stride, int32_t *status_dev, void *stream) {
+    if (int rc = check_kv_paged(cache, batch, type, M, n_heads)) return rc;
+    if (!rope_dev || (M > 0 && (!qkv_dev || !q_out_dev))) return fail(nullptr, QW3_ERR_INVALID_ARG, "null append arguments");
+    if (!(eps >= 0.0f)) return fail(nullptr, QW3_ERR_INVALID_ARG, "eps must be >= 0");
+    if (rope_len < 1) return fail(nullptr, QW3_ERR_INVALID_ARG, "rope_len must be >= 1");
+    const int64_t qw = static_cast<int64_t>(n_heads) * cache->head_dim;
+    if (int rc = check_rows(qkv_dev, qkv_stride, qw + 2ll * cache->n_kv_heads * cache->head_dim, type)) return rc;
+    if (int rc = check_rows(q_out_dev, q_stride, qw, type)) return rc;
+    if (misaligned(q_norm_dev, 4) || misaligned(k_norm_dev, 4) || misaligned(rope_dev, 16) || misaligned(status_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "rope must be 16-byte, the norm weights and the status 4-byte aligned");
+    if (M == 0 || batch->B == 0) return QW3_OK;
+    KvPagedAppendArgs a{};
+    a.c = kv_paged_view(cache);
+    a.b = kv_batch_view(batch, M, M, kPagedMaxLen);
+    a.qkv = qkv_dev; a.qkv_stride = qkv_stride; a.nh = n_heads; a.q_norm = q_norm_dev; a.k_norm = k_norm_dev;
+    a.eps = eps; a.rope = reinterpret_cast<const float2 *>(rope_dev); a.rope_len = rope_len;
+    a.q_out = q_out_dev; a.q_stride = q_stride; a.status = status_dev;
+    QW3_CUDA_TRY(launch_kv_paged_append(a, type, cache->head_dim, true, static_cast<cudaStream_t>(stream)));
+    return QW3_OK;
+}
+
+int64_t qw3_kv_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t type, int32_t n_heads, int32_t n_kv_heads,
+                                          int32_t head_dim, int32_t max_rows, int32_t max_len, int32_t window,
+                                          int32_t sinks) {
+    if (B < 0 || B > kPagedMaxBatch || M < 0 || (type != QW3_F32 && type != QW3_F16) || n_kv_heads < 1 ||
+        n_kv_heads > 64 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > kPagedMaxGroup ||
+        (head_dim != 64 && head_dim != 128) || max_rows < 0 || max_rows > M || max_len < 0 || max_len > kPagedMaxLen ||
+        window < 0 || sinks < 0 || static_cast<int64_t>(M) * (n_heads + 2 * n_kv_heads) > INT32_MAX)
+        return -1;
+    return static_cast<int64_t>(
+        kv_paged_attn_workspace_bytes(B, M, type, n_heads, n_kv_heads, head_dim, max_rows, max_len, window, sinks));
+}
+
+int qw3_kv_paged_attn(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int32_t type, const void *q_dev, int32_t M,
+                      int64_t q_stride, int32_t n_heads, int32_t max_rows, int32_t max_len, int32_t window,
+                      int32_t sinks, float scale, void *out_dev, int64_t out_stride, void *workspace_dev,
+                      int64_t workspace_bytes, int32_t *status_dev, void *stream) {
+    if (int rc = check_kv_paged(cache, batch, type, M, n_heads)) return rc;
+    if (M > 0 && (!q_dev || !out_dev)) return fail(nullptr, QW3_ERR_INVALID_ARG, "null attention arguments");
+    if (max_rows < 0 || max_rows > M) return fail(nullptr, QW3_ERR_INVALID_ARG, "max_rows must be 0 to M");
+    if (max_len < 0 || window < 0 || sinks < 0) return fail(nullptr, QW3_ERR_INVALID_ARG, "a negative max_len, window or sinks");
+    if (max_len > static_cast<int64_t>(batch->pages_per_seq) * cache->page_size)
+        return fail(nullptr, QW3_ERR_KV_OVERFLOW, "max_len past the positions that the table has pages for");
+    const int64_t qw = static_cast<int64_t>(n_heads) * cache->head_dim;
+    if (int rc = check_rows(q_dev, q_stride, qw, type)) return rc;
+    if (int rc = check_rows(out_dev, out_stride, qw, type)) return rc;
+    if (misaligned(workspace_dev, 16) || misaligned(status_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "the workspace must be 16-byte, the status 4-byte aligned");
+    if (!(scale - scale == 0.0f)) return fail(nullptr, QW3_ERR_INVALID_ARG, "scale must be finite");
+    if (M == 0 || batch->B == 0 || max_rows == 0) return QW3_OK;
+    const int64_t need = qw3_kv_paged_attn_workspace_bytes(batch->B, M, type, n_heads, cache->n_kv_heads, cache->head_dim,
+                                                           max_rows, max_len, window, sinks);
+    if (need > 0 && (!workspace_dev || workspace_bytes < need))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "workspace too small");
+    KvPagedAttnArgs a{};
+    a.c = kv_paged_view(cache);
+    a.b = kv_batch_view(batch, M, max_rows, max_len);
+    a.q = q_dev; a.q_stride = q_stride; a.nh = n_heads; a.window = window; a.sinks = sinks; a.scale = scale;
+    a.out = out_dev; a.out_stride = out_stride; a.ws = workspace_dev; a.status = status_dev;
+    QW3_CUDA_TRY(configure_all());   // the kernels' shared-memory limits
+    QW3_CUDA_TRY(launch_kv_paged_attn(a, type, cache->head_dim, true, static_cast<cudaStream_t>(stream)));
+    return QW3_OK;
+}
+
+int qw3_logprobs(const float *logits_dev, int64_t stride, int32_t B, int32_t V, const int32_t *tokens_dev, int32_t T,
+                 int32_t top, float *logprob_dev, float *entropy_dev, int32_t *top_id_dev, float *top_logprob_dev,
+                 int32_t *status_dev, void *stream) {
+    if (B < 0 || T < 0 || top < 0 || (B > 0 && !logits_dev) || (B > 0 && T > 0 && (!tokens_dev || !logprob_dev)) ||
+        (B > 0 && top > 0 && (!top_id_dev || !top_logprob_dev)))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "bad logprobs arguments");
+    if (B > kSampleMaxRows) return fail(nullptr, QW3_ERR_SHAPE, "log probabilities of up to 2^30 rows");
+    if (V < 1 || V > kSampleMaxVocab || stride < V) return fail(nullptr, QW3_ERR_SHAPE, "1 <= V <= 4194304, V <= stride");
+    if (top > kLogprobMaxTop) return fail(nullptr, QW3_ERR_SHAPE, "at most 64 alternatives");
+    if (misaligned(logits_dev, 4) || misaligned(tokens_dev, 4) || misaligned(logprob_dev, 4) ||
+        misaligned(entropy_dev, 4) || misaligned(top_id_dev, 4) || misaligned(top_logprob_dev, 4) ||
+        misaligned(status_dev, 4))
+        return fail(nullptr, QW3_ERR_INVALID_ARG, "device buffers must be 4-byte aligned");
+    if (B == 0) return QW3_OK;
+    LogprobArgs a{logits_dev, stride, V, tokens_dev, T, top, logprob_dev, entropy_dev, top_id_dev, top_logprob_dev,
+                  status_dev};
+    QW3_CUDA_TRY(configure_all());   // the kernel's cluster size
+    QW3_CUDA_TRY(launch_logprobs(a, B, true, static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }
 

@@ -353,6 +353,72 @@ struct SampleArgs {
 cudaError_t configure_sample();
 cudaError_t launch_sample(const SampleArgs &a, int B, bool pdl, cudaStream_t s);
 
+// ---- the paged KV cache (kv_paged.cu holds its layout)
+struct KvPaged {
+    __half *data = nullptr;   // [page][K|V][kv head][page_size][hd]
+    int pages = 0, shift = 0, nkv = 0;   // page_size = 1 << shift
+};
+
+// A ragged batch: what every kernel over it reads (qw3_kv_batch), with the rows
+// of the call's buffers and the bounds that the caller gave.
+struct KvBatch {
+    const int32_t *starts, *lens, *table;
+    int64_t tstride;
+    int B, pps;              // sequences, pages per sequence
+    int M, max_rows, max_len;
+};
+
+struct KvPagedAppendArgs {
+    KvPaged c;
+    KvBatch b;
+    const void *qkv;   // `type` [M][qkv_stride]
+    int64_t qkv_stride;
+    int nh;
+    const float *q_norm, *k_norm;   // nullable [hd]
+    float eps;
+    const float2 *rope;   // [rope_len][hd / 2]
+    int rope_len;
+    void *q_out;
+    int64_t q_stride;
+    int32_t *status;
+};
+constexpr int kPagedMaxGroup = 16, kPagedMaxBatch = 1 << 20;
+constexpr int kPagedMaxLen = 1 << 30;   // positions and the steps past their end stay within 31 bits
+cudaError_t launch_kv_paged_append(const KvPagedAppendArgs &a, int type, int hd, bool pdl, cudaStream_t s);
+
+struct KvPagedAttnArgs {
+    KvPaged c;
+    KvBatch b;
+    const void *q;   // `type` [M][q_stride]
+    int64_t q_stride;
+    int nh, window, sinks;
+    float scale;
+    void *out;
+    int64_t out_stride;
+    void *ws;
+    int32_t *status;
+};
+size_t kv_paged_attn_workspace_bytes(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len,
+                                     int window, int sinks);
+cudaError_t configure_kv_paged();
+cudaError_t launch_kv_paged_attn(const KvPagedAttnArgs &a, int type, int hd, bool pdl, cudaStream_t s);
+
+// ---- log probabilities (logprobs.cu)
+constexpr int kLogprobMaxTop = 64;
+struct LogprobArgs {
+    const float *logits;   // [B][stride]
+    int64_t stride;
+    int V;
+    const int32_t *tokens;   // [B][T]
+    int T, top;
+    float *logprob, *entropy;   // [B][T]; nullable [B]
+    int32_t *top_id;            // [B][top]
+    float *top_lp;
+    int32_t *status;
+};
+cudaError_t configure_logprobs();
+cudaError_t launch_logprobs(const LogprobArgs &a, int B, bool pdl, cudaStream_t s);
+
 }  // namespace qw3
 
 // ------------------------------------------------------------ device PTX
@@ -557,6 +623,47 @@ __device__ __forceinline__ bool kv_q4_row(const KvQ4 &c, const KvQ4Rows &r, int 
     slot = r.slots ? r.slots[row] : r.slot0;
     pos = r.pos ? r.pos[row] : r.pos0 + row;
     return slot >= 0 && slot < c.slots && pos >= 0 && pos < c.cap;
+}
+
+// ---- the paged KV cache: a sequence's rows and positions. n may be smaller
+// than its rows (max_rows); row t is at position p0 + t.
+struct KvSeq {
+    int start, n, p0;
+};
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch &b, int i) {
+    const int s = min(max(b.starts[i], 0), b.M), e = min(max(b.starts[i + 1], 0), b.M);
+    const int n = max(e - s, 0);
+    return {s, min(n, b.max_rows), min(max(b.lens[i], 0), b.max_len) - n};
+}
+// The page that holds position p >= 0 of sequence i, or -1.
+__device__ __forceinline__ int kv_page(const KvBatch &b, const KvPaged &c, int i, int p) {
+    const int at = p >> c.shift;
+    if (at >= b.pps) return -1;
+    const int page = b.table[i * b.tstride + at];
+    return page >= 0 && page < c.pages ? page : -1;
+}
+// Position p of head g of K (0) or V (1) of a page.
+template <int HD>
+__device__ __forceinline__ __half *kv_paged_row(const KvPaged &c, int page, int sel, int g, int p) {
+    return c.data + ((((static_cast<size_t>(page) * 2 + sel) * c.nkv + g) << c.shift) + (p & ((1 << c.shift) - 1))) * HD;
+}
+// Whether a row at position p attends position j (which is in the cache).
+__device__ __forceinline__ bool kv_sees(int p, int j, int window, int sinks) {
+    return j <= p && (window == 0 || p - j < window || j < sinks);
+}
+// The sequence that a row belongs to, or -1: a warp looks at 32 borders at a
+// time (the last start at or before the row). All lanes call it, with one row.
+__device__ __forceinline__ int kv_seq_of(const KvBatch &b, int row, int lane) {
+    int lo = 0, n = b.B + 1;   // borders lo .. lo + n - 1, the answer is the last one <= row
+    while (n > 0) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool in = lane * step < n && b.starts[at] <= row;
+        const int before = __popc(__ballot_sync(0xffffffffu, in));
+        if (before == 0) return lo - 1 < b.B ? lo - 1 : -1;
+        lo += (before - 1) * step + 1;
+        n = min(step - 1, n - (before - 1) * step - 1);
+    }
+    return lo - 1 < b.B ? lo - 1 : -1;
 }
 
 // ---- Q4_K block decode ("Model files and quantization", 11.8; layout in q4k.cu)

@@ -50,7 +50,13 @@ EXPORTS = (
     "qw3_q8_0_gemm_workspace_bytes", "qw3_q8_0_gemm",
     "qw3_kv_q4_bytes", "qw3_kv_q4_append", "qw3_kv_q4_read", "qw3_kv_q4_attn_workspace_bytes", "qw3_kv_q4_attn",
     "qw3_sample",
+    "qw3_kv_paged_bytes", "qw3_kv_paged_append", "qw3_kv_paged_attn_workspace_bytes", "qw3_kv_paged_attn",
+    "qw3_logprobs",
 )
+
+# enum qw3_type
+QW3_F32 = 0
+QW3_F16 = 1
 
 
 class Qw3Config(ctypes.Structure):
@@ -80,6 +86,18 @@ class Qw3KvQ4(ctypes.Structure):
     """A 4-bit KV cache on a device buffer."""
     _fields_ = [("data", ctypes.c_void_p), ("slots", ctypes.c_int32), ("capacity", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class Qw3KvPaged(ctypes.Structure):
+    """A pool of KV cache pages on a device buffer."""
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class Qw3KvBatch(ctypes.Structure):
+    """A ragged batch of sequences over a paged cache."""
+    _fields_ = [("starts_dev", ctypes.c_void_p), ("lens_dev", ctypes.c_void_p), ("table_dev", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("B", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32)]
 
 
 class Qw3Error(RuntimeError):
@@ -143,6 +161,13 @@ def lib() -> ctypes.CDLL:
         "qw3_kv_q4_attn": (ctypes.c_int, [ctypes.POINTER(Qw3KvQ4), _P, _I64, _I32, _P, _P, _I32, _I32, _I32, _F32, _P,
                                           _I64, _P, _I64, _P, _P]),
         "qw3_sample": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+        "qw3_kv_paged_bytes": (_I64, [_I32, _I32, _I32, _I32]),
+        "qw3_kv_paged_append": (ctypes.c_int, [ctypes.POINTER(Qw3KvPaged), ctypes.POINTER(Qw3KvBatch), _I32, _P, _I32,
+                                               _I64, _I32, _P, _P, _F32, _P, _I32, _P, _I64, _P, _P]),
+        "qw3_kv_paged_attn_workspace_bytes": (_I64, [_I32] * 10),
+        "qw3_kv_paged_attn": (ctypes.c_int, [ctypes.POINTER(Qw3KvPaged), ctypes.POINTER(Qw3KvBatch), _I32, _P, _I32,
+                                             _I64, _I32, _I32, _I32, _I32, _I32, _F32, _P, _I64, _P, _I64, _P, _P]),
+        "qw3_logprobs": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -333,6 +358,40 @@ def qw3_sample(logits_ptr: int, stride: int, B: int, V: int, temperature_ptr: in
     _check(lib().qw3_sample(logits_ptr or None, stride, B, V, temperature_ptr or None, top_k_ptr or None,
                             top_p_ptr or None, min_p_ptr or None, u_ptr or None, token_ptr or None, prob_ptr or None,
                             status_ptr or None, stream or None))
+
+
+def qw3_kv_paged_bytes(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    return lib().qw3_kv_paged_bytes(n_pages, page_size, n_kv_heads, head_dim)
+
+
+def qw3_kv_paged_append(cache: Qw3KvPaged, batch: Qw3KvBatch, type: int, qkv_ptr: int, M: int, qkv_stride: int,
+                        n_heads: int, q_norm_ptr: int, k_norm_ptr: int, eps: float, rope_ptr: int, rope_len: int,
+                        q_out_ptr: int, q_stride: int, status_ptr: int = 0, stream: int = 0) -> None:
+    _check(lib().qw3_kv_paged_append(cache, batch, type, qkv_ptr or None, M, qkv_stride, n_heads, q_norm_ptr or None,
+                                     k_norm_ptr or None, eps, rope_ptr or None, rope_len, q_out_ptr or None, q_stride,
+                                     status_ptr or None, stream or None))
+
+
+def qw3_kv_paged_attn_workspace_bytes(B: int, M: int, type: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                      max_rows: int, max_len: int, window: int = 0, sinks: int = 0) -> int:
+    return lib().qw3_kv_paged_attn_workspace_bytes(B, M, type, n_heads, n_kv_heads, head_dim, max_rows, max_len, window,
+                                                   sinks)
+
+
+def qw3_kv_paged_attn(cache: Qw3KvPaged, batch: Qw3KvBatch, type: int, q_ptr: int, M: int, q_stride: int, n_heads: int,
+                      max_rows: int, max_len: int, window: int, sinks: int, scale: float, out_ptr: int, out_stride: int,
+                      ws_ptr: int, ws_bytes: int, status_ptr: int = 0, stream: int = 0) -> None:
+    _check(lib().qw3_kv_paged_attn(cache, batch, type, q_ptr or None, M, q_stride, n_heads, max_rows, max_len, window,
+                                   sinks, scale, out_ptr or None, out_stride, ws_ptr or None, ws_bytes,
+                                   status_ptr or None, stream or None))
+
+
+def qw3_logprobs(logits_ptr: int, stride: int, B: int, V: int, tokens_ptr: int, T: int, top: int, logprob_ptr: int,
+                 entropy_ptr: int = 0, top_id_ptr: int = 0, top_logprob_ptr: int = 0, status_ptr: int = 0,
+                 stream: int = 0) -> None:
+    _check(lib().qw3_logprobs(logits_ptr or None, stride, B, V, tokens_ptr or None, T, top, logprob_ptr or None,
+                              entropy_ptr or None, top_id_ptr or None, top_logprob_ptr or None, status_ptr or None,
+                              stream or None))
 
 
 # ---------------------------------------------------------- torch wrapper
@@ -620,6 +679,163 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stat
     if rc:
         _check(rc)
     return token, prob
+
+
+_kv_paged_bytes = functools.lru_cache(maxsize=256)(qw3_kv_paged_bytes)
+_kv_paged_attn_workspace_bytes = functools.lru_cache(maxsize=1024)(qw3_kv_paged_attn_workspace_bytes)
+
+
+class KVCachePaged:
+    """A paged f16 KV cache (qw3_kv_paged): a pool of pages that many sequences
+    share. Its calls take ragged batches: rows starts[b] .. starts[b + 1] - 1 of
+    the activations are the newest tokens of sequence b, which holds lens[b]
+    positions with them, position p in page table[b, p // page_size] (starts int32
+    [B + 1], lens int32 [B], table int32 [B, pages]; -1 where there is no page).
+    Activations are f32 or f16. Every call runs on torch's current stream of the
+    cache's device."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, data=None, device="cuda"):
+        torch = _torch()
+        # (ctypes would take a larger number modulo 2^32)
+        sizes = (n_pages, page_size, n_kv_heads, head_dim)
+        n = _kv_paged_bytes(*sizes) if 0 < min(sizes) and max(sizes) <= _INT32_MAX else -1
+        if n < 0:
+            raise Qw3Error(QW3_ERR_SHAPE, "n_pages >= 1, page_size 16, 32, 64, 128 or 256, 1 to 64 kv heads, head_dim 64 "
+                                          "or 128, fewer than 2^31 rows")
+        if data is None:
+            if torch.device(device).type != "cuda":
+                raise Qw3Error(QW3_ERR_INVALID_ARG, "device: a cache lies on a CUDA device")
+            data = torch.empty((n_pages, 2, n_kv_heads, page_size, head_dim), dtype=torch.float16, device=device)
+        elif data.dtype is not torch.float16 or not data.is_cuda or not data.is_contiguous() or 2 * data.numel() < n:
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"data: a contiguous CUDA f16 tensor of {n // 2} values is wanted")
+        self.data, self.device, self.index = data, data.device, data.get_device()
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = sizes
+        self.c = Qw3KvPaged(data.data_ptr(), *sizes)
+
+    def _batch(self, torch, starts, lens, table):
+        _on(self.index, torch.int32, "starts and lens", starts, lens)
+        B = lens.numel()
+        if starts.numel() != B + 1 or table.dim() != 2 or table.shape[0] != B:
+            raise Qw3Error(QW3_ERR_SHAPE, "starts holds a border more than there are sequences, table a row for each")
+        _, width, stride = _rows_of(table, "table")
+        if table.dtype is not torch.int32 or table.get_device() != self.index:
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"table: an int32 tensor on cuda:{self.index} is wanted")
+        return Qw3KvBatch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), stride, B, width)
+
+    def _type(self, torch, t, name):
+        if t.get_device() != self.index or (t.dtype is not torch.float32 and t.dtype is not torch.float16):
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: an f32 or f16 tensor on cuda:{self.index} is wanted")
+        return QW3_F32 if t.dtype is torch.float32 else QW3_F16
+
+    def append(self, qkv, starts, lens, table, rope, q_norm=None, k_norm=None, eps: float = 1e-6, out=None, status=None):
+        """Norm (where q_norm, k_norm: f32 [head_dim] are given), rotate and
+        append the batch's rows; returns the rotated queries [M, n_heads,
+        head_dim] in qkv's type (in `out` where it is given). qkv: [M, (n_heads +
+        2 n_kv_heads) * head_dim], rows may be strided by multiples of 16 bytes;
+        rope: f32 [positions, head_dim / 2, 2]. The queries of a row that is not
+        in the cache are zero, those of rows outside the batch are not written."""
+        torch = _torch()
+        if _elsewhere(torch, self.index):
+            with torch.cuda.device(self.index):
+                return self.append(qkv, starts, lens, table, rope, q_norm, k_norm, eps, out, status)
+        kind = self._type(torch, qkv, "qkv")
+        M, width, stride = _rows_of(qkv, "qkv")
+        hd = self.head_dim
+        n_heads = width // hd - 2 * self.n_kv_heads
+        if width % hd or n_heads < 1:
+            raise Qw3Error(QW3_ERR_SHAPE, "qkv: rows of n_heads + 2 n_kv_heads heads are wanted")
+        _on(self.index, torch.float32, "q_norm, k_norm and rope", q_norm, k_norm, rope)
+        if any(w is not None and w.numel() != hd for w in (q_norm, k_norm)) or rope.dim() != 3 or rope.shape[1:] != (hd // 2, 2):
+            raise Qw3Error(QW3_ERR_SHAPE, "q_norm and k_norm hold head_dim values, rope [positions, head_dim / 2, 2]")
+        _on(self.index, torch.int32, "status", status)
+        batch = self._batch(torch, starts, lens, table)
+        if out is None:
+            out = torch.empty((M, n_heads, hd), dtype=qkv.dtype, device=self.device)
+        else:
+            _on(self.index, qkv.dtype, "out", out)
+            if out.numel() != M * n_heads * hd:
+                raise Qw3Error(QW3_ERR_SHAPE, f"out: [{M}, {n_heads}, {hd}] is wanted")
+        rc = lib().qw3_kv_paged_append(self.c, batch, kind, qkv.data_ptr(), M, stride, n_heads, _ptr(q_norm), _ptr(k_norm),
+                                       eps, rope.data_ptr(), min(rope.shape[0], _INT32_MAX), out.data_ptr(), n_heads * hd,
+                                       _ptr(status), _stream_on(torch, self.index))
+        if rc:
+            _check(rc)
+        return out
+
+    def attention(self, q, starts, lens, table, max_rows: Optional[int] = None, max_len: Optional[int] = None,
+                  window: int = 0, sinks: int = 0, scale: Optional[float] = None, out=None, workspace=None, status=None):
+        """Causal attention of the batch's rows q [M, n_heads, head_dim]
+        (contiguous) over the cache; returns the same shape and type. window > 0:
+        a row sees its `window` newest positions and the sequence's first `sinks`.
+        max_rows, max_len: upper bounds of a sequence's rows and length (M and
+        what the table has pages for where they are not given); rows past
+        max_rows are not written, nor are those outside the batch. scale:
+        1 / sqrt(head_dim) where it is not given. out: where the result goes (q
+        itself, or apart from it). workspace: a uint8 tensor to use in place of a
+        new one."""
+        torch = _torch()
+        if _elsewhere(torch, self.index):
+            with torch.cuda.device(self.index):
+                return self.attention(q, starts, lens, table, max_rows, max_len, window, sinks, scale, out, workspace, status)
+        kind = self._type(torch, q, "q")
+        if q.dim() != 3 or q.shape[2] != self.head_dim or q.shape[0] > _INT32_MAX or q.shape[1] < 1:
+            raise Qw3Error(QW3_ERR_SHAPE, f"q: [M, n_heads, {self.head_dim}] is wanted")
+        M, n_heads, hd = q.shape
+        _on(self.index, q.dtype, "q and out", q, out)
+        _on(self.index, torch.int32, "status", status)
+        if out is not None and out.shape != q.shape:
+            raise Qw3Error(QW3_ERR_SHAPE, "out has q's shape")
+        batch = self._batch(torch, starts, lens, table)
+        max_rows = M if max_rows is None else min(max_rows, M)
+        max_len = batch.pages_per_seq * self.page_size if max_len is None else max_len
+        if not (0 <= max_len <= _INT32_MAX and max_rows >= 0 and 0 <= window <= _INT32_MAX and 0 <= sinks <= _INT32_MAX):
+            raise Qw3Error(QW3_ERR_INVALID_ARG, "a negative bound, window or sinks, or one past 31 bits")
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            need = _kv_paged_attn_workspace_bytes(batch.B, M, kind, n_heads, self.n_kv_heads, hd, max_rows, max_len, window,
+                                                  sinks)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        else:
+            _on(self.index, torch.uint8, "workspace", workspace)
+            need = workspace.numel()
+        rc = lib().qw3_kv_paged_attn(self.c, batch, kind, q.data_ptr(), M, n_heads * hd, n_heads, max_rows, max_len, window,
+                                     sinks, hd ** -0.5 if scale is None else scale, out.data_ptr(), n_heads * hd,
+                                     _ptr(workspace), need, _ptr(status), _stream_on(torch, self.index))
+        if rc:
+            _check(rc)
+        return out
+
+
+def logprobs(logits, tokens, top: int = 0, status=None):
+    """What CUDA f32 logits [B, V] (rows may be strided) say about int32 tokens
+    [B] or [B, T] (qw3_logprobs): (log probabilities of the tokens in their shape,
+    entropies f32 [B], the `top` most likely tokens int32 [B, top], their log
+    probabilities f32 [B, top])."""
+    torch = _torch()
+    B, V, stride = _rows_of(logits, "logits")
+    dev = logits.get_device()
+    if logits.dtype is not torch.float32 or dev < 0:
+        raise Qw3Error(QW3_ERR_INVALID_ARG, "logits: a CUDA f32 tensor is wanted")
+    _on(dev, torch.int32, "tokens and status", tokens, status)
+    if tokens.dim() not in (1, 2) or tokens.shape[0] != B or tokens.numel() > B * _INT32_MAX:
+        raise Qw3Error(QW3_ERR_SHAPE, f"tokens: [{B}] or [{B}, T] is wanted")
+    if not 0 <= top <= 64:
+        raise Qw3Error(QW3_ERR_SHAPE, "0 to 64 alternatives")
+    if _elsewhere(torch, dev):
+        with torch.cuda.device(dev):
+            return logprobs(logits, tokens, top, status)
+    lp = torch.empty(tokens.shape, dtype=torch.float32, device=logits.device)
+    entropy = torch.empty(B, dtype=torch.float32, device=logits.device)
+    top_id = torch.empty((B, top), dtype=torch.int32, device=logits.device)
+    top_lp = torch.empty((B, top), dtype=torch.float32, device=logits.device)
+    T = 1 if tokens.dim() == 1 else tokens.shape[1]
+    rc = lib().qw3_logprobs(logits.data_ptr(), stride, B, V, tokens.data_ptr(), T, top, lp.data_ptr(), entropy.data_ptr(),
+                            top_id.data_ptr(), top_lp.data_ptr(), _ptr(status), _stream_on(torch, dev))
+    if rc:
+        _check(rc)
+    return lp, entropy, top_id, top_lp
 
 
 class _Ordered:

@@ -1,0 +1,552 @@
+"""The paged KV cache entries against plain 64-bit arithmetic (paged_f64.py):
+rows appended, attention over ragged batches, and both in a layer.
+
+Tolerances. A value before its last rounding is within 20 f32 roundings (2^-24
+each) of its row's largest normalised value: 9 for the sum of squares and its
+root, 3 products, one sum, times sqrt 2. Its last rounding is half a step: 2^-11
+of it in f16 (2^-25 where it is subnormal), 2^-24 in f32. Values of V are rounded
+once: exactly numpy's. Attention: paged_f64.bound.
+"""
+import numpy as np
+import pytest
+
+import paged_f64 as ref
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as t
+    if not t.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from quantized_transformer_decode_gb300 import build
+    build.build()
+    return t
+
+
+class Batch:
+    """A pool, and sequences of (new rows, length) in pages taken in no order."""
+
+    def __init__(self, torch, seqs, nkv=2, hd=64, page=16, dtype="f32", nh=4, seed=0, spare=3, lead=0, tail=0, extra=1):
+        from quantized_transformer_decode_gb300 import qw3
+        self.torch, self.rng = torch, np.random.default_rng(seed)
+        self.nh, self.nkv, self.hd, self.page = nh, nkv, hd, page
+        self.f16 = dtype == "f16"
+        self.np_type, self.dtype = (np.float16, torch.float16) if self.f16 else (np.float32, torch.float32)
+        rows, lens = [r for r, _ in seqs], [n for _, n in seqs]
+        self.M = lead + sum(rows) + tail
+        self.starts = np.concatenate(([0], np.cumsum(rows))).astype(np.int32) + lead
+        self.lens = np.array(lens, np.int32)
+        used = np.array([max(0, -(-n // page)) for n in lens], int)
+        self.n_pages = int(used.sum()) + spare
+        width = int(used.max()) + extra if len(used) else 1
+        self.table = np.full((len(seqs), width), -1, np.int32)
+        ids = self.rng.permutation(self.n_pages)[:int(used.sum())]
+        self.table[np.arange(width) < used[:, None]] = ids
+        gain = 1 + 0.5 * np.abs(self.rng.standard_normal((2, nkv, 1, hd)))
+        self.data = (self.rng.standard_normal((self.n_pages, 2, nkv, page, hd)) * gain).astype(np.float16)
+        # places behind a sequence's end hold anything
+        for b, n in enumerate(lens):
+            if n > 0 and n % page:
+                self.data[self.table[b, n // page], :, :, n % page:] = self.rng.choice([np.nan, np.inf, -np.inf, 3.0])
+        held = set(ids.tolist())
+        for p in range(self.n_pages):
+            if p not in held:
+                self.data[p] = np.nan
+        self.q = (self.rng.standard_normal((self.M, nh, hd)) * 1.5).astype(self.np_type)
+        self.qkv = (self.rng.standard_normal((self.M, (nh + 2 * nkv) * hd)) * 0.8).astype(self.np_type)
+        self.q_norm = (1 + 0.1 * self.rng.standard_normal(hd)).astype(np.float32)
+        self.k_norm = (1 + 0.1 * self.rng.standard_normal(hd)).astype(np.float32)
+        self.rope = ref.rope_table(max(1, max(lens, default=1)), hd)
+        self.qw3 = qw3
+
+    def dev(self, x):
+        return self.torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+    def cache(self):
+        return self.qw3.KVCachePaged(self.n_pages, self.page, self.nkv, self.hd, data=self.dev(self.data))
+
+    def where(self):
+        return self.dev(self.starts), self.dev(self.lens), self.dev(self.table)
+
+    def attend(self, cache=None, q=None, **kw):
+        return (cache or self.cache()).attention(self.dev(self.q) if q is None else q, *self.where(), **kw)
+
+    def check(self, got, **kw):
+        want, err, written = ref.attend(self.q, self.data.astype(np.float64), self.starts, self.lens, self.table, **kw)
+        got = got.cpu().numpy().astype(np.float64)
+        lim = ref.bound(err, want, self.hd, self.f16)
+        fine = np.isfinite(want)
+        assert np.array_equal(np.isfinite(got[written]), fine[written])
+        off = np.where(fine, np.abs(got - np.where(fine, want, 0)), 0)
+        over = (off > lim) & written[:, None, None]
+        assert not over.any(), (np.argwhere(over)[:4], off[over][:4], lim[over][:4], got[over][:4], want[over][:4])
+        return want, written
+
+
+# ---------------------------------------------------------------- append
+
+def check_append(b, norm=True, positions=None, qkv=None, got=None, cache=None, status=0):
+    """Every head of every row, the pages' other places bit for bit."""
+    want = b.data.copy()
+    nh, nkv, hd = b.nh, b.nkv, b.hd
+    x = (b.qkv if qkv is None else qkv).reshape(b.M, nh + 2 * nkv, hd)
+    data = cache.data.cpu().numpy()
+    q = got.cpu().numpy().astype(np.float64)
+    kerr = np.zeros(want.shape)
+    exact = want.astype(np.float64)
+    for row, (s, p, page) in enumerate(ref.places(b.starts, b.lens, b.table, b.page, b.n_pages, b.M)):
+        if s < 0:
+            continue
+        if page < 0 or p >= len(b.rope):
+            assert not q[row].any()
+            continue
+        n, y = ref.turned(x[row, :nh], b.q_norm if norm else None, b.rope[p], EPS)
+        lim = 20 * 2.0 ** -24 * np.abs(n).max(-1, keepdims=True) + np.abs(y) * (2.0 ** -11 if b.f16 else 2.0 ** -24) + (
+            2.0 ** -25 if b.f16 else 0)
+        assert (np.abs(q[row] - y) <= lim * (1 + 2.0 ** -10)).all(), (row, np.abs(q[row] - y).max())
+        n, y = ref.turned(x[row, nh:nh + nkv], b.k_norm if norm else None, b.rope[p], EPS)
+        exact[page, 0, :, p % b.page] = y
+        kerr[page, 0, :, p % b.page] = (20 * 2.0 ** -24 * np.abs(n).max(-1, keepdims=True) + 2.0 ** -11 * np.abs(y)) * (
+            1 + 2.0 ** -10) + 2.0 ** -25
+        v = x[row, nh + nkv:].astype(np.float16)
+        want[page, 1, :, p % b.page] = v
+        exact[page, 1, :, p % b.page] = v
+    touched = kerr > 0
+    assert np.array_equal(data.view(np.int16)[~touched], want.view(np.int16)[~touched])
+    assert (np.abs(data[touched].astype(np.float64) - exact[touched]) <= kerr[touched]).all()
+    return data
+
+
+SHAPES = [(4, 2, 64), (16, 8, 128), (8, 8, 128), (16, 2, 64), (5, 1, 128), (12, 4, 64), (48, 3, 128), (7, 7, 64)]
+APPENDS = [
+    [(1, 1)], [(1, 517)], [(3, 3), (1, 40), (0, 9), (2, 2)], [(70, 70)], [(33, 100), (1, 16), (17, 17)],
+    [(1, 5 + i) for i in range(70)],
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("nh,nkv,hd", SHAPES)
+@pytest.mark.parametrize("case", range(len(APPENDS)))
+def test_append(torch, case, nh, nkv, hd, dtype):
+    b = Batch(torch, APPENDS[case], nh=nh, nkv=nkv, hd=hd, page=(16, 32, 64, 128, 256)[(case + nh) % 5], dtype=dtype, seed=case)
+    c = b.cache()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = c.append(b.dev(b.qkv), *b.where(), b.dev(b.rope), b.dev(b.q_norm), b.dev(b.k_norm), EPS, status=status)
+    check_append(b, got=q, cache=c)
+    assert int(status) == 0
+
+
+def test_append_many_rows(torch):
+    """More than one pass of heads to a warp, and 32 x 32 sequences to look through."""
+    for dtype in ("f32", "f16"):
+        b = Batch(torch, [(1 + i % 3, 3 + i % 50) for i in range(1100)], nh=16, nkv=8, hd=128, dtype=dtype, seed=5)
+        c = b.cache()
+        q = c.append(b.dev(b.qkv), *b.where(), b.dev(b.rope), b.dev(b.q_norm), b.dev(b.k_norm), EPS)
+        check_append(b, got=q, cache=c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_append_without_norm_in_place_and_strided(torch, dtype):
+    b = Batch(torch, [(9, 30), (1, 1), (40, 44)], nh=4, nkv=2, hd=64, dtype=dtype, lead=2, tail=3)
+    c = b.cache()
+    wide = torch.full((b.M, b.qkv.shape[1] + 32), 7.0, dtype=b.dtype, device="cuda")
+    wide[:, 16:-16] = b.dev(b.qkv)
+    q = c.append(wide[:, 16:-16], *b.where(), b.dev(b.rope))
+    check_append(b, norm=False, got=q, cache=c)
+    # in place: through the C entry, rows outside the batch stay as they are
+    qw3 = b.qw3
+    c2, buf = b.cache(), b.dev(b.qkv)
+    starts, lens, table = b.where()
+    batch = qw3.Qw3KvBatch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], 3, table.shape[1])
+    rope = b.dev(b.rope)
+    qw3.qw3_kv_paged_append(c2.c, batch, int(b.f16), buf.data_ptr(), b.M, buf.shape[1], b.nh, 0, 0, EPS, rope.data_ptr(),
+                            len(b.rope), buf.data_ptr(), buf.shape[1], 0, torch.cuda.current_stream().cuda_stream)
+    heads = buf.view(b.M, -1, b.hd)
+    check_append(b, norm=False, got=heads[:, :b.nh], cache=c2)
+    keep = torch.ones(b.M, dtype=torch.bool)
+    keep[2:-3] = False
+    assert torch.equal(buf.cpu()[keep], torch.from_numpy(b.qkv)[keep])
+    assert torch.equal(heads.cpu()[:, b.nh:], torch.from_numpy(b.qkv).view(b.M, -1, b.hd)[:, b.nh:])
+
+
+def test_append_places_outside_the_cache(torch):
+    """Rows at negative positions, on pages outside the pool, past the table and
+    past the rotations are not cached; rows outside the batch are not written."""
+    b = Batch(torch, [(5, 3), (4, 20), (6, 40), (2, 30)], nh=4, nkv=2, hd=64, lead=3, tail=4)
+    b.table[1, 1] = b.n_pages          # positions 16..19 of sequence 1
+    b.table[2, 2] = -7                 # positions 32..39 of sequence 2
+    b.lens[3] = 3 * 16 + 1 + 16 * (b.table.shape[1] - 3)      # its last position is past the table's width
+    b.rope = b.rope[:38]
+    c = b.cache()
+    out = torch.full((b.M, b.nh, b.hd), 9.0, device="cuda")
+    q = c.append(b.dev(b.qkv), *b.where(), b.dev(b.rope), b.dev(b.q_norm), b.dev(b.k_norm), EPS, out=out)
+    assert q is out
+    check_append(b, got=q, cache=c)
+    assert (q[:3] == 9).all() and (q[-4:] == 9).all() and not (q[3:-4] == 9).any()
+
+
+def test_append_borders_beyond_the_rows(torch):
+    """Borders below 0 and past M are taken as the nearest inside."""
+    b = Batch(torch, [(4, 10), (4, 30)], nh=4, nkv=2, hd=64)
+    b.starts[0], b.starts[2] = -5, 1000
+    c = b.cache()
+    check_append(b, got=c.append(b.dev(b.qkv), *b.where(), b.dev(b.rope), b.dev(b.q_norm), b.dev(b.k_norm), EPS), cache=c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_append_values_that_f16_does_not_hold(torch, dtype):
+    """A head with NaN, an infinity or 65520 and more is zeros, others stay; the norm of huge and tiny heads."""
+    b = Batch(torch, [(8, 24)], nh=4, nkv=2, hd=64, dtype=dtype)
+    x = b.qkv.reshape(8, 8, 64)
+    x[0, 6, 5] = np.nan
+    x[1, 7, 63] = -np.inf
+    x[2, 4, 0] = np.nan
+    x[3, 5, 9] = np.inf
+    if dtype == "f32":
+        x[4, 6, 1] = 65520.0
+        x[5, 7, 2] = -65519.9          # the largest that rounds to what f16 holds
+        x[6, 4] *= 1e30                # squares leave f32
+        x[7, 5] *= 1e-30
+        x[6, 1] *= 1e30
+        x[7, 2] *= 1e-30
+    clean = x.copy()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c = b.cache()
+    q = c.append(b.dev(b.qkv), *b.where(), b.dev(b.rope), b.dev(b.q_norm), b.dev(b.k_norm), EPS, status=status)
+    assert int(status) == 5
+    data = c.data.cpu().numpy()
+    place = [(int(b.table[0, p // 16]), p % 16) for p in range(16, 24)]
+    dead = {(0, 1, 0), (1, 1, 1), (2, 0, 0), (3, 0, 1)} | ({(4, 1, 0)} if dtype == "f32" else set())
+    for r, (page, off) in enumerate(place):
+        for sel in (0, 1):
+            for g in (0, 1):
+                if (r, sel, g) in dead:
+                    assert not data[page, sel, g, off].any()
+                    continue
+                src = clean[r, 4 + 2 * sel + g]
+                if sel:
+                    assert np.array_equal(data[page, 1, g, off], src.astype(np.float16))
+                else:
+                    n, y = ref.turned(src[None], b.k_norm, b.rope[16 + r], EPS)
+                    lim = 20 * 2.0 ** -24 * np.abs(n).max() + 2.0 ** -11 * np.abs(y[0]) + 2.0 ** -25
+                    assert (np.abs(data[page, 0, g, off] - y[0]) <= lim * 1.001).all()
+    if dtype == "f32":
+        for r, h in ((6, 1), (7, 2)):
+            n, y = ref.turned(clean[r, h][None], b.q_norm, b.rope[16 + r], EPS)
+            assert (np.abs(q[r, h].cpu().numpy() - y[0]) <= 21 * 2.0 ** -24 * np.abs(n).max()).all()
+
+
+# ---------------------------------------------------------------- attention
+
+ATTNS = {
+    "one": [(1, 1)],
+    "short": [(1, 5), (1, 16), (1, 17), (1, 33)],
+    "long": [(1, 1000)],
+    "tokens": [(1, 1 + 37 * i % 400) for i in range(20)],
+    "verify": [(5, 77), (3, 3), (5, 130), (1, 64)],
+    "chunk": [(77, 77)],
+    "chunk_behind": [(100, 391)],
+    "mixed": [(1, 300), (0, 40), (65, 200), (2, 2), (129, 129), (1, 129)],
+    "odd": [(128, 128), (127, 255), (33, 257)],
+}
+HEADS = [(4, 2, 64), (16, 8, 128), (8, 8, 128), (16, 2, 64), (5, 1, 128), (16, 1, 128), (6, 2, 64), (3, 3, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("nh,nkv,hd", HEADS)
+@pytest.mark.parametrize("case", list(ATTNS))
+def test_attention(torch, case, nh, nkv, hd, dtype):
+    at = list(ATTNS).index(case)
+    b = Batch(torch, ATTNS[case], nh=nh, nkv=nkv, hd=hd, page=(16, 32, 64, 128, 256)[(at + nh) % 5], dtype=dtype, seed=at)
+    b.check(b.attend())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (50, 0), (64, 70), (128, 128), (129, 3), (300, 1), (1000, 5)])
+@pytest.mark.parametrize("case", ["tokens", "verify", "chunk_behind", "mixed", "odd"])
+def test_window_and_sinks(torch, case, window, sinks, dtype):
+    nh, nkv, hd = ((4, 2, 64), (16, 8, 128), (5, 1, 128))[(window + sinks) % 3]
+    b = Batch(torch, ATTNS[case], nh=nh, nkv=nkv, hd=hd, page=(16, 64)[sinks % 2], dtype=dtype, seed=window)
+    b.check(b.attend(window=window, sinks=sinks), window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_long_contexts(torch, dtype):
+    """Sums over thousands of positions, split over many CTAs and joined."""
+    for seqs, kw in (([(1, 20000)], {}), ([(4, 9001), (1, 50)], {}), ([(130, 6000)], {}), ([(300, 5000), (1, 7000)], {}),
+                     ([(200, 6000), (2, 6500)], dict(window=700, sinks=9))):
+        b = Batch(torch, seqs, nh=8, nkv=2, hd=128, page=64, dtype=dtype, seed=1)
+        b.check(b.attend(**kw), **kw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("seqs", [[(4, 2), (1, 0), (3, 0), (2, 20)], [(60, 20), (1, 40), (200, 100)]])
+def test_rows_that_see_nothing(torch, seqs, dtype):
+    """More rows than positions, lengths of zero and below: zeros."""
+    b = Batch(torch, seqs, dtype=dtype)
+    if len(seqs) == 4:
+        b.lens[2] = -3
+    got = b.attend()
+    want, _ = b.check(got)
+    assert not got.float().cpu().numpy()[(want == 0).all((1, 2))].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("rows", [1, 3, 90])
+def test_pages_outside_the_pool(torch, rows, dtype):
+    """Positions without a page are not attended, in whatever they lie between;
+    a row left with none is zeros."""
+    b = Batch(torch, [(rows, 400), (rows, 100), (rows, 300)], dtype=dtype, nh=4, nkv=2, hd=64)
+    b.table[0, [0, 3, 4, 20]] = [-1, b.n_pages, 2 ** 31 - 1, -2 ** 31]
+    b.table[1, :] = -1
+    b.table[2, 8:18] = -1
+    got = b.attend()
+    b.check(got)
+    assert not got[rows:2 * rows].any()
+    b.check(b.attend(window=30, sinks=2), window=30, sinks=2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("seqs", [[(1, 200), (1, 90)], [(6, 200), (3, 90)], [(150, 200), (40, 90)]])
+def test_what_is_not_seen_has_no_part(torch, seqs, dtype):
+    """NaN and infinities in places that some rows see and others do not."""
+    b = Batch(torch, seqs, dtype=dtype, nh=4, nkv=2, hd=64)
+    n = seqs[0][1]
+    for back, bad in ((1, np.nan), (2, np.inf), (60, -np.inf), (61, np.nan)):
+        p = n - back
+        b.data[b.table[0, p // 16], 1, 0, p % 16, back % 64] = bad
+    p = n - 3
+    b.data[b.table[0, p // 16], 0, 1, p % 16, 7] = np.nan
+    kw = dict(window=50, sinks=1)
+    want, err, written = ref.attend(b.q, np.where(np.isfinite(b.data), b.data, 0).astype(np.float64), b.starts, b.lens, b.table, **kw)
+    got = b.attend(**kw).float().cpu().numpy()
+    lim = ref.bound(err, want, b.hd, b.f16)
+    rows0 = seqs[0][0]
+    for i in range(b.M):
+        if i >= rows0:
+            assert (np.abs(got[i] - want[i]) <= lim[i]).all()
+            continue
+        p = n - rows0 + i
+        dims = {back % 64 for back in (1, 2, 60, 61) if p - 50 < n - back <= p}
+        for h in range(4):
+            if h < 2:
+                fine = np.array([d not in dims for d in range(64)])
+                assert (np.abs(got[i, h] - want[i, h]) <= lim[i, h])[fine].all(), (i, h)
+                assert not np.isfinite(got[i, h][~fine]).any()
+            elif p - 50 < n - 3 <= p:
+                assert np.isnan(got[i, h]).all()
+            else:
+                assert (np.abs(got[i, h] - want[i, h]) <= lim[i, h]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_rows_outside_the_batch_stay(torch, dtype):
+    b = Batch(torch, [(3, 40), (70, 90), (1, 5)], dtype=dtype, lead=2, tail=5)
+    out = torch.full((b.M, b.nh, b.hd), 9.0, dtype=b.dtype, device="cuda")
+    got = b.attend(out=out)
+    assert got is out
+    _, written = b.check(got)
+    assert (got[~torch.from_numpy(written).cuda()] == 9).all() and written.sum() == 74
+    # a bound below a sequence's rows: those past it stay
+    for cut in (2, 60):
+        out = torch.full_like(out, 9.0)
+        _, written = b.check(b.attend(out=out, max_rows=cut), max_rows=cut)
+        assert (out[~torch.from_numpy(written).cuda()] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("seqs", [[(1, 300), (2, 40)], [(90, 300), (2, 40)]])
+def test_bounds_scale_and_in_place(torch, seqs, dtype):
+    b = Batch(torch, seqs, dtype=dtype, nh=16, nkv=8, hd=128)
+    b.check(b.attend(max_len=100), max_len=100)
+    b.check(b.attend(scale=0.0), scale=0.0)
+    b.check(b.attend(scale=-0.3), scale=-0.3)
+    q = b.dev(b.q)
+    got = b.attend(q=q, out=q)
+    assert got is q
+    b.check(got)
+    assert not b.attend(max_len=0).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_large_scores(torch, rows, dtype):
+    """One position that takes everything, scores far apart, and queries at the type's ends."""
+    for size in (300.0, 60000.0) + ((1e30, 1e-30) if dtype == "f32" else ()):
+        b = Batch(torch, [(rows, 150), (rows, 80)], dtype=dtype, nh=4, nkv=2, hd=64)
+        b.q = np.clip(b.q.astype(np.float64) / 4 * size, -60000 if b.f16 else -3e38, 60000 if b.f16 else 3e38).astype(b.np_type)
+        scale = min(0.125, 40 / size)
+        b.check(b.attend(scale=scale), scale=np.float64(np.float32(scale)))
+
+
+def test_offsets_past_32_bits(torch):
+    """Pages beyond 2^32 bytes of the pool."""
+    from quantized_transformer_decode_gb300 import qw3
+    nkv, hd, page, n_pages = 8, 128, 64, 18000            # 4.7 GB
+    small = Batch(torch, [(1, 700), (90, 500)], nh=16, nkv=nkv, hd=hd, page=page, spare=0, dtype="f16")
+    pool = torch.empty((n_pages, 2, nkv, page, hd), dtype=torch.float16, device="cuda")
+    shift = n_pages - small.n_pages
+    pool[shift:] = small.dev(small.data)
+    c = qw3.KVCachePaged(n_pages, page, nkv, hd, data=pool)
+    starts, lens, table = small.where()
+    table = torch.where(table >= 0, table + shift, table)
+    small.check(c.attention(small.dev(small.q), starts, lens, table))
+    q = c.append(small.dev(small.qkv), starts, lens, table, small.dev(small.rope), small.dev(small.q_norm), small.dev(small.k_norm), EPS)
+    view = qw3.KVCachePaged(small.n_pages, page, nkv, hd, data=pool[shift:].clone())
+    check_append(small, got=q, cache=view)
+
+
+def test_many_sequences(torch):
+    b = Batch(torch, [(1 + (i % 97 == 0) * 40, 41 + i % 60) for i in range(700)], nh=4, nkv=2, hd=64, dtype="f16")
+    b.check(b.attend())
+
+
+@pytest.mark.parametrize("seqs", [[(1, 3000)], [(100, 900), (1, 2000)]])
+def test_streams_graphs_and_repeats(torch, seqs):
+    """The same bits each time, on another stream, and from a graph whose inputs change."""
+    b = Batch(torch, seqs, nh=16, nkv=8, hd=128, dtype="f32")
+    c, q = b.cache(), b.dev(b.q)
+    where = b.where()
+    kw = dict(max_rows=max(r for r, _ in seqs), max_len=max(n for _, n in seqs))
+    first = c.attention(q, *where, **kw)
+    b.check(first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = [c.attention(q, *where, **kw) for _ in range(3)]
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(first, t) for t in again)
+    g = torch.cuda.CUDAGraph()
+    out = torch.empty_like(q)
+    with torch.cuda.graph(g):
+        c.attention(q, *where, out=out, **kw)
+    for seed in (3, 4):
+        b.q = np.random.default_rng(seed).standard_normal(b.q.shape).astype(np.float32)
+        b.lens -= seed
+        q.copy_(b.dev(b.q))
+        where[1].copy_(b.dev(b.lens))
+        g.replay()
+        b.check(out)
+
+
+def test_two_at_once(torch):
+    """Calls on two streams, each with its own workspace."""
+    bs = [Batch(torch, [(1, 4000), (200, 1500)], nh=16, nkv=8, hd=128, dtype="f16", seed=i) for i in range(2)]
+    cs, qs, ws = [b.cache() for b in bs], [b.dev(b.q) for b in bs], [b.where() for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for c, q, w, s in zip(cs, qs, ws, streams):
+            with torch.cuda.stream(s):
+                outs.append(c.attention(q, *w))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, outs[i % 2])
+    for b, o in zip(bs, outs):
+        b.check(o)
+
+
+def test_a_table_wider_than_the_call_uses(torch):
+    """A strided view of a larger table."""
+    b = Batch(torch, [(1, 90), (20, 60)])
+    wide = torch.full((2, 40), 2 ** 30, dtype=torch.int32, device="cuda")
+    wide[:, 3:3 + b.table.shape[1]] = b.dev(b.table)
+    starts, lens, _ = b.where()
+    b.check(b.cache().attention(b.dev(b.q), starts, lens, wide[:, 3:3 + b.table.shape[1]]))
+
+
+def test_another_current_device(torch):
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one GPU")
+    b = Batch(torch, [(1, 90), (20, 60)])
+    c, q, w = b.cache(), b.dev(b.q), b.where()
+    with torch.cuda.device(1):
+        got = c.attention(q, *w)
+    b.check(got)
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_refusals(torch):
+    from quantized_transformer_decode_gb300 import qw3
+    b = Batch(torch, [(1, 90), (20, 60)])
+    c, q, (starts, lens, table) = b.cache(), b.dev(b.q), b.where()
+    rope, qkv = b.dev(b.rope), b.dev(b.qkv)
+    bad = qw3.Qw3Error
+    for args in ((0, 16, 2, 64), (1, 17, 2, 64), (1, 8, 2, 64), (1, 512, 2, 64), (1, 16, 0, 64), (1, 16, 65, 64),
+                 (1, 16, 2, 96), (2 ** 32 + 1, 16, 2, 64), (2 ** 31 - 1, 256, 64, 128)):
+        with pytest.raises(bad):
+            qw3.KVCachePaged(*args)
+    with pytest.raises(bad):
+        qw3.KVCachePaged(b.n_pages + 1, 16, 2, 64, data=c.data)
+    with pytest.raises(bad):
+        qw3.KVCachePaged(1, 16, 2, 64, data=torch.zeros(10000, dtype=torch.float16))
+    with pytest.raises(bad):
+        qw3.KVCachePaged(1, 16, 2, 64, device="cpu")
+    for call in (
+        lambda: c.attention(q.double(), starts, lens, table), lambda: c.attention(q.cpu(), starts, lens, table),
+        lambda: c.attention(q[:, :, :32], starts, lens, table), lambda: c.attention(q[:, :3], starts, lens, table),
+        lambda: c.attention(q[:, ::2], starts, lens, table), lambda: c.attention(q, starts[:-1], lens, table),
+        lambda: c.attention(q, starts.long(), lens, table), lambda: c.attention(q, starts, lens, table[:1]),
+        lambda: c.attention(q, starts, lens, table.t().contiguous().t()), lambda: c.attention(q, starts, lens, table, max_len=10000),
+        lambda: c.attention(q, starts, lens, table, window=-1), lambda: c.attention(q, starts, lens, table, sinks=-1),
+        lambda: c.attention(q, starts, lens, table, max_rows=-1), lambda: c.attention(q, starts, lens, table, scale=float("nan")),
+        lambda: c.attention(q, starts, lens, table, window=2 ** 31), lambda: c.attention(q, starts, lens, table, out=q.half()),
+        lambda: c.attention(q, starts, lens.cpu(), table),
+        lambda: c.append(qkv[:, :-1], starts, lens, table, rope), lambda: c.append(qkv[:, 1:-63], starts, lens, table, rope),
+        lambda: c.append(qkv.double(), starts, lens, table, rope), lambda: c.append(qkv, starts, lens, table, rope[:, :-1]),
+        lambda: c.append(qkv, starts, lens, table, rope, q_norm=rope.flatten()[:63]),
+        lambda: c.append(qkv, starts, lens, table, rope, eps=-1.0), lambda: c.append(qkv, starts, lens, table, rope[:0]),
+        lambda: c.append(qkv, starts, lens, table, rope, out=q.half()),
+    ):
+        with pytest.raises(bad):
+            call()
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    need = qw3.qw3_kv_paged_attn_workspace_bytes(2, b.M, 0, 4, 2, 64, b.M, 96)
+    if need > 16:
+        with pytest.raises(bad):
+            c.attention(q, starts, lens, table, workspace=small)
+    # nothing to do is no error
+    none = torch.zeros((0, 4, 64), device="cuda")
+    assert c.attention(none, starts, lens, table).shape == none.shape
+    empty = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert c.attention(q, empty, empty[:0], table[:0]).shape == q.shape
+    b.check(c.attention(q, starts, lens, table))
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_append_then_attention_over_steps(torch, dtype):
+    """A prompt in two chunks beside sequences that decode: every step appends and
+    attends, and each step's outputs are those of the whole history."""
+    from quantized_transformer_decode_gb300 import qw3
+    rng = np.random.default_rng(9)
+    nh, nkv, hd, page, n_pages = 8, 2, 64, 16, 40
+    kind = torch.float16 if dtype == "f16" else torch.float32
+    c = qw3.KVCachePaged(n_pages, page, nkv, hd)
+    c.data.fill_(float("nan"))
+    free = list(rng.permutation(n_pages))
+    table = np.full((3, 13), -1, np.int32)
+    lens = np.zeros(3, np.int32)
+    rope = ref.rope_table(256, hd)
+    for rows in ((70, 1, 0), (100, 1, 9), (1, 1, 1), (1, 4, 1)):
+        lens = lens + np.array(rows, np.int32)
+        for i in range(3):
+            for k in range(-(-int(lens[i]) // page)):
+                if table[i, k] < 0:
+                    table[i, k] = free.pop()
+        starts = np.concatenate(([0], np.cumsum(rows))).astype(np.int32)
+        m = int(starts[-1])
+        qkv = torch.from_numpy(rng.standard_normal((m, (nh + 2 * nkv) * hd)).astype(np.float32)).cuda().to(kind)
+        where = [torch.from_numpy(v).cuda() for v in (starts, lens, table)]
+        q = c.append(qkv, *where, torch.from_numpy(rope).cuda())
+        got = c.attention(q, *where).float().cpu().numpy()
+        data = c.data.cpu().numpy().astype(np.float64)
+        want, err, written = ref.attend(q.float().cpu().numpy(), data, starts, lens, table)
+        assert written.all() and (np.abs(got - want) <= ref.bound(err, want, hd, dtype == "f16")).all()
