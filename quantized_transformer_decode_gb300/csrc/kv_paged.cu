@@ -189,7 +189,557 @@ cudaError_t append_t(const KvPagedAppendArgs &a, bool pdl, cudaStream_t s) {
                : launch_pdl(pdl, k_paged_append<T, HD, 4>, grid, 128, 0, 1, s, a, passes, per_row, units);
 }
 
-// ---------------------------------------------------------------- attention
+// ---------------------------------------------------------------- attention of few rows
+//
+// Decoding, and verify blocks of a few rows: bound by the K and V that have to
+// be read. The rows of a sequence that share a kv head are columns j = t * G + h
+// (G query heads to a kv head); a unit is up to W columns of one kv head of one
+// sequence, a step 16 positions of it (they lie in one page). The steps of all
+// units are dealt to the CTAs in equal shares, so ragged lengths fill the GPU
+// evenly; a unit cut between CTAs leaves parts (maximum, sum, output) in the
+// workspace that a second kernel joins.
+//
+// A warp takes every eighth step of its CTA's share, through a ring of its own
+// in shared memory that cp.async fills three steps ahead, over the units' ends
+// too. Scores S = Q K^T and outputs O = P V are mma.sync.m16n8k16: 16 rows of A
+// are 8 columns in two f16 parts (f32 activations; hi + lo, 22 bits) or 16
+// columns (f16), K is B as it lies (8 positions x 16 dimensions, the dimensions
+// in an order that gives a thread 16 contiguous bytes), and so is V after
+// setting pairs of positions side by side (one byte permutation to a register).
+// tcgen05.mma has no part here: a tile of 128 rows would be filled by 2 to 16,
+// and reading K and V is what takes the time, not the products.
+
+constexpr int kTokWarps = 8, kTokStages = 3, kTokKeys = 16;
+constexpr int kTokCols = 32;      // columns of a sequence's kv head that these kernels take
+
+template <typename T, int HD>
+struct TokSizes {
+    static constexpr bool split = sizeof(T) == 4;
+    static constexpr int W = split ? 8 : 16;                    // columns of a unit
+    static constexpr int part = HD + 4;                         // floats of a column's part: output, maximum, sum
+    static constexpr uint32_t half = kTokKeys * HD * 2;         // bytes of a step's K, or V
+    static constexpr uint32_t ring = kTokStages * 2 * half;     // of a warp
+    static constexpr uint32_t smem = kTokWarps * (ring + 8 * part * 4);
+};
+
+// The steps of a sequence's units: its first `sinks` positions, then the
+// window's (or all). Rows 0 .. n - 1 are at p0 ..; where no row sees anything
+// there is one step, for the zeros.
+struct TokSeq {
+    int start, n, p0, cols, sink_steps, first, steps;
+    __device__ __forceinline__ int key_step(int k) const { return k < sink_steps ? k : k - sink_steps + first; }
+};
+__device__ __forceinline__ TokSeq tok_seq(const KvPagedAttnArgs &a, int i, int G) {
+    const KvSeq q = kv_seq(a.b, i);
+    TokSeq s;
+    s.start = q.start;
+    s.n = q.n;
+    s.p0 = q.p0;
+    s.cols = q.n * G;
+    if (s.cols > kTokCols) s.n = s.cols = 0;   // another kernel's
+    const int last = s.p0 + s.n - 1;
+    const int lo = a.window > 0 ? max(0, s.p0 - a.window + 1) : 0;
+    s.first = lo / kTokKeys;
+    s.sink_steps = a.window > 0 ? min((min(a.sinks, lo) + kTokKeys - 1) / kTokKeys, s.first) : 0;
+    s.steps = last < 0 ? 1 : s.sink_steps + last / kTokKeys - s.first + 1;
+    return s;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+__device__ __forceinline__ bool half2_nonfinite(uint32_t v) {
+    return (v & 0x7c00u) == 0x7c00u || (v & 0x7c000000u) == 0x7c000000u;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Where a CTA (or a warp's loads, ahead of it) is: unit `u` of sequence i, its
+// steps k .. end - 1 among them, and `left` steps of the share behind those.
+struct TokAt {
+    TokSeq s;
+    int i, u, units, k, end;
+    long long left;
+};
+// The units of sequence i, for all kv heads.
+template <int W>
+__device__ __forceinline__ int tok_units(const TokSeq &s, int nkv) { return (s.cols + W - 1) / W * nkv; }
+
+// The next unit of which the share has a step; i = -1 behind the last one.
+template <int W>
+__device__ __forceinline__ void tok_next(TokAt &t, const KvPagedAttnArgs &a, int G) {
+    while (t.left > 0) {
+        if (++t.u >= t.units) {
+            t.u = -1;
+            if (++t.i >= a.b.B) break;
+            t.s = tok_seq(a, t.i, G);
+            t.units = tok_units<W>(t.s, a.c.nkv);
+            continue;
+        }
+        t.k = 0;
+        t.end = static_cast<int>(min(static_cast<long long>(t.s.steps), t.left));
+        t.left -= t.end;
+        return;
+    }
+    t.left = 0;
+    t.i = -1;
+}
+
+// The CTAs that a unit is cut between: the first and the last, with bit 31 of
+// `last` where it begins in the first one's own first piece; first = -1 for a
+// unit that one CTA has whole.
+struct TokCut {
+    int first;
+    uint32_t last;
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPagedAttnArgs a, int G, int max_cb, int min_share) {
+    using Z = TokSizes<T, HD>;
+    constexpr int W = Z::W, KS = HD / 16, NT = HD / 8, CH = HD / 8;
+    constexpr float kOff = 12.0f, kLazy = 3.0f;   // a weight is 2^(s - ref + 12), at most 2^15
+    extern __shared__ __align__(128) uint8_t tok_smem[];
+    __shared__ long long s_sum[kTokWarps];
+    __shared__ int s_i, s_off_u, s_off_k;
+    __shared__ float s_m[kTokWarps][8], s_l[kTokWarps][8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
+    const int nkv = a.c.nkv;
+    pdl_wait();
+
+    // ---- the share of this CTA: steps x0 .. x1 - 1 of all
+    const int per = (a.b.B + kTokWarps * 32 - 1) / (kTokWarps * 32);
+    const int i0 = min(a.b.B, tid * per), i1 = min(a.b.B, i0 + per);
+    long long mine = 0;
+    for (int i = i0; i < i1; ++i) {
+        const TokSeq s = tok_seq(a, i, G);
+        mine += static_cast<long long>(tok_units<W>(s, nkv)) * s.steps;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    long long total = 0, before = upto - mine;
+    for (int w = 0; w < kTokWarps; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_share));
+    const long long x0 = share * blockIdx.x, x1 = min(total, x0 + share);
+    if (x0 >= before && x0 < before + mine) {
+        long long at = before;
+        for (int i = i0; i < i1; ++i) {
+            const TokSeq s = tok_seq(a, i, G);
+            const long long n = static_cast<long long>(tok_units<W>(s, nkv)) * s.steps;
+            if (x0 < at + n) {
+                s_i = i;
+                s_off_u = static_cast<int>((x0 - at) / s.steps);
+                s_off_k = static_cast<int>((x0 - at) % s.steps);
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    if (x0 >= total) return;
+
+    TokAt t;   // what the CTA computes
+    t.i = s_i;
+    t.s = tok_seq(a, t.i, G);
+    t.units = tok_units<W>(t.s, nkv);
+    t.u = s_off_u;
+    t.k = s_off_k;
+    t.end = static_cast<int>(min(static_cast<long long>(t.s.steps), t.k + (x1 - x0)));
+    t.left = x1 - x0 - (t.end - t.k);
+
+    // ---- this warp's loads: the next step to fetch, its page known one step ahead
+    const uint32_t ring = smem_u32(tok_smem) + warp * Z::ring;
+    TokAt f = t;
+    int fk = f.k + warp, fpage = -1;
+    uint32_t paged = 0;   // bit per stage: its step has a page
+    auto settle = [&]() {   // fk to a step of the share, if there is one
+        while (f.i >= 0 && fk >= f.end) {
+            tok_next<W>(f, a, G);
+            fk = f.k + warp;
+        }
+        fpage = f.i >= 0 ? kv_page(a.b, a.c, f.i, f.s.key_step(fk) * kTokKeys) : -1;
+    };
+    auto fetch = [&](int stage) {
+        if (f.i >= 0) {
+            const int j0 = f.s.key_step(fk) * kTokKeys, g = f.u / ((f.s.cols + W - 1) / W);
+            const bool there = fpage >= 0;
+            paged = (paged & ~(1u << stage)) | static_cast<uint32_t>(there) << stage;
+            const uint8_t *k = reinterpret_cast<const uint8_t *>(kv_paged_row<HD>(a.c, there ? fpage : 0, 0, g, j0));
+            const uint8_t *v = reinterpret_cast<const uint8_t *>(kv_paged_row<HD>(a.c, there ? fpage : 0, 1, g, j0));
+            const uint32_t to = ring + stage * 2 * Z::half;
+#pragma unroll
+            for (int n = 0; n < kTokKeys * CH / 32; ++n) {
+                const int c = n * 32 + lane, r = c / CH, ch = c % CH;
+                cp_async16(to + (r * CH + (ch ^ ((r & 1) << 2))) * 16, k + c * 16, there);
+                cp_async16(to + Z::half + (r * CH + (ch ^ ((r >> 1 & 3) << 1))) * 16, v + c * 16, there);
+            }
+            fk += kTokWarps;
+            settle();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    settle();
+#pragma unroll
+    for (int n = 0; n < kTokStages; ++n) fetch(n);
+    int stage = 0;
+
+    const float scale2 = a.scale * 1.4426950408889634f;   // softmax in base 2
+    float *slots = static_cast<float *>(a.ws);
+    TokCut *cuts = reinterpret_cast<TokCut *>(slots + static_cast<size_t>(gridDim.x) * 2 * W * Z::part);
+    long long x = x0;   // the first step of this piece
+    for (int piece = 0; t.i >= 0; ++piece) {
+        const int blocks = (t.s.cols + W - 1) / W, g = t.u / blocks, cb = t.u % blocks, col0 = cb * W;
+        const int pmin = t.s.p0 + col0 / G, pmax = t.s.p0 + (min(t.s.cols, col0 + W) - 1) / G;
+        // ---- the queries as A, and this thread's columns: gid (and gid + 8)
+        uint32_t qf[KS][4];
+        float cscale[2];
+        int p[2];
+#pragma unroll
+        for (int e = 0; e < (Z::split ? 1 : 2); ++e) {
+            const int col = col0 + gid + 8 * e;
+            const bool real = col < t.s.cols;
+            p[e] = real ? t.s.p0 + col / G : pmax;   // (a column that is none sees what the last one sees)
+            const T *src = static_cast<const T *>(a.q) + (t.s.start + (real ? col / G : 0)) * a.q_stride +
+                           static_cast<size_t>(g * G + (real ? col % G : 0)) * HD + 8 * tig;
+            if constexpr (Z::split) {
+                float v[HD / 32][8], amax = 0.0f;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    const float4 u0 = *reinterpret_cast<const float4 *>(src + 32 * c), u1 = *reinterpret_cast<const float4 *>(src + 32 * c + 4);
+                    v[c][0] = u0.x; v[c][1] = u0.y; v[c][2] = u0.z; v[c][3] = u0.w;
+                    v[c][4] = u1.x; v[c][5] = u1.y; v[c][6] = u1.z; v[c][7] = u1.w;
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) amax = fmaxf(amax, fabsf(v[c][d]));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // the power of two that takes the largest into [2^14, 2^15)
+                const int ex = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23 & 0xffu));
+                const float up = pow2_f32(ex);
+                cscale[0] = pow2_f32(-ex) * scale2;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    float w[8];
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) w[d] = real ? v[c][d] * up : 0.0f;
+                    uint4 hi, lo;
+                    split8_f16(w, hi, lo);
+                    qf[2 * c][0] = hi.x; qf[2 * c][1] = lo.x; qf[2 * c][2] = hi.y; qf[2 * c][3] = lo.y;
+                    qf[2 * c + 1][0] = hi.z; qf[2 * c + 1][1] = lo.z; qf[2 * c + 1][2] = hi.w; qf[2 * c + 1][3] = lo.w;
+                }
+            } else {
+                cscale[e] = scale2;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    const uint4 u = real ? *reinterpret_cast<const uint4 *>(src + 32 * c) : make_uint4(0, 0, 0, 0);
+                    qf[2 * c][e] = u.x; qf[2 * c][2 + e] = u.y;
+                    qf[2 * c + 1][e] = u.z; qf[2 * c + 1][2 + e] = u.w;
+                }
+            }
+        }
+
+        float acc[NT][4], ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+
+        for (int k = t.k + warp; k < t.end; k += kTokWarps) {
+            const int j0 = t.s.key_step(k) * kTokKeys;
+            const bool held = paged >> stage & 1;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kTokStages - 1) : "memory");
+            __syncwarp();
+            const uint32_t at = ring + stage * 2 * Z::half;
+            // ---- scores of 2 x 8 positions
+            float s[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    const int r = 8 * b + gid, ch = 4 * c + tig;
+                    const uint4 u = lds128(at + (r * CH + (ch ^ ((r & 1) << 2))) * 16);
+                    mma16816(s[b], qf[2 * c], u.x, u.y);
+                    mma16816(s[b], qf[2 * c + 1], u.z, u.w);
+                }
+            }
+            // every column sees all 16 positions?
+            const bool open = held && j0 + kTokKeys - 1 <= pmin && (a.window == 0 || pmax - j0 < a.window || j0 + kTokKeys <= a.sinks);
+            // s[b][2 h + e]: column gid + 8 h, position j0 + 8 b + 2 tig + e
+            constexpr int NC = Z::split ? 1 : 2;
+            float z[NC][4];
+#pragma unroll
+            for (int h = 0; h < NC; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float raw = Z::split ? s[e >> 1][e & 1] + s[e >> 1][2 + (e & 1)] : s[e >> 1][2 * h + (e & 1)];
+                    z[h][e] = raw * cscale[h];
+                    const int j = j0 + 8 * (e >> 1) + 2 * tig + (e & 1);
+                    if (!open && !(held && kv_sees(p[h], j, a.window, a.sinks))) z[h][e] = -INFINITY;
+                }
+            // ---- the reference follows the maximum when it is passed by more than 2^kLazy
+            bool far = false;
+            float mx[NC];
+#pragma unroll
+            for (int h = 0; h < NC; ++h) {
+                mx[h] = fmaxf(fmaxf(z[h][0], z[h][1]), fmaxf(z[h][2], z[h][3]));
+                far |= mx[h] > ref[h] + kLazy;
+            }
+            if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+                for (int h = 0; h < NC; ++h) {
+                    float m = mx[h];
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    if (m > ref[h] + kLazy) {
+                        const float c = ref[h] == -INFINITY ? 0.0f : ex2(ref[h] - m);
+                        ref[h] = m;
+                        sum[h] *= c;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            acc[n][2 * h] *= c;
+                            acc[n][2 * h + 1] *= c;
+                            if constexpr (Z::split) {
+                                acc[n][2] *= c;
+                                acc[n][3] *= c;
+                            }
+                        }
+                    }
+                }
+            }
+            uint32_t pf[4];
+#pragma unroll
+            for (int h = 0; h < NC; ++h) {
+                const float base = (ref[h] == -INFINITY ? 0.0f : ref[h]) - kOff;
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = ex2(z[h][e] - base);
+                    sum[h] += w[e];
+                }
+                if constexpr (Z::split) {
+                    pf[0] = pack_half2(w[0], w[1]);
+                    pf[2] = pack_half2(w[2], w[3]);
+                    const float2 h0 = unpack_half2(pf[0]), h1 = unpack_half2(pf[2]);
+                    pf[1] = pack_half2(w[0] - h0.x, w[1] - h0.y);
+                    pf[3] = pack_half2(w[2] - h1.x, w[3] - h1.y);
+                } else {
+                    pf[h] = pack_half2(w[0], w[1]);
+                    pf[2 + h] = pack_half2(w[2], w[3]);
+                }
+            }
+            // ---- O += P V
+#pragma unroll
+            for (int hh = 0; hh < HD / 64; ++hh) {
+                uint32_t v[4][4];   // positions 2 tig, + 1, + 8, + 9; dimensions 64 hh + 8 gid ..
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 2 * tig + (e & 1) + 8 * (e >> 1), ch = 8 * hh + gid;
+                    const uint4 u = lds128(at + Z::half + (r * CH + (ch ^ ((r >> 1 & 3) << 1))) * 16);
+                    v[e][0] = u.x; v[e][1] = u.y; v[e][2] = u.z; v[e][3] = u.w;
+                }
+                bool slow = false;
+                if (!open) {
+                    // what no column sees is zeros (its weights are 0, but 0 * NaN is not); what some do not
+                    // see has to be finite, or the columns are taken one by one
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + 2 * tig + (e & 1) + 8 * (e >> 1);
+                        const bool any = held && j <= pmax && kv_sees(max(j, pmin), j, a.window, a.sinks);
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            v[e][d] = any ? v[e][d] : 0u;
+                            slow |= half2_nonfinite(v[e][d]);
+                        }
+                    }
+                    slow = __any_sync(0xffffffffu, slow);
+                }
+                if (!slow) {
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) {
+                        const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
+                        mma16816(acc[8 * hh + d], pf, __byte_perm(v[0][d >> 1], v[1][d >> 1], sel),
+                                 __byte_perm(v[2][d >> 1], v[3][d >> 1], sel));
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < W; ++c) {   // column c alone, with the positions that it sees
+                        const int pc = col0 + c < t.s.cols ? t.s.p0 + (col0 + c) / G : pmax;
+                        uint32_t pc_f[4];
+                        const bool row = gid == (c & 7);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pc_f[e] = row && (Z::split || (e & 1) == c >> 3) ? pf[e] : 0u;
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) {
+                            const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
+                            uint32_t u[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                u[e] = kv_sees(pc, j0 + 2 * tig + (e & 1) + 8 * (e >> 1), a.window, a.sinks) ? v[e][d >> 1] : 0u;
+                            float o[4] = {acc[8 * hh + d][0], acc[8 * hh + d][1], acc[8 * hh + d][2], acc[8 * hh + d][3]};
+                            mma16816(o, pc_f, __byte_perm(u[0], u[1], sel), __byte_perm(u[2], u[3], sel));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (row && (Z::split || (e >> 1) == c >> 3)) acc[8 * hh + d][e] = o[e];
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            fetch(stage);
+            stage = stage + 1 == kTokStages ? 0 : stage + 1;
+        }
+
+        // ---- the warps' parts joined, 8 columns at a time
+        const bool whole = t.k == 0 && t.end == t.s.steps;
+        float *const dst = slots + (static_cast<size_t>(blockIdx.x) * 2 + (piece > 0)) * W * Z::part;
+        if (t.k == 0 && tid == 0) {
+            // the first of the unit's CTAs says where the others are
+            TokCut c{-1, 0u};
+            if (!whole) c = {static_cast<int>(blockIdx.x), static_cast<uint32_t>((x + t.s.steps - 1) / share) | (piece == 0 ? 0x80000000u : 0u)};
+            cuts[(static_cast<size_t>(t.i) * nkv + g) * max_cb + cb] = c;
+        }
+        float *const buf = reinterpret_cast<float *>(tok_smem + kTokWarps * Z::ring);
+#pragma unroll
+        for (int h = 0; h < (Z::split ? 1 : 2); ++h) {
+            if (8 * h >= t.s.cols - col0) break;
+            float l = sum[h];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if (tig == 0) {
+                s_m[warp][gid] = ref[h];
+                s_l[warp][gid] = l;
+            }
+            float *o = buf + (warp * 8 + gid) * Z::part + tig;   // [dimensions in the order of the registers][tig]
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    o[(((n >> 3) * 2 + e) * 8 + (n & 7)) * 4] = Z::split ? acc[n][e] + acc[n][2 + e] : acc[n][2 * h + e];
+            __syncthreads();
+            const int here = min(8, t.s.cols - col0 - 8 * h);
+            for (int n = tid; n < here * HD; n += kTokWarps * 32) {
+                const int c = n / HD, d = n % HD;
+                const int pos = (((d >> 6) * 2 + (d >> 3 & 1)) * 8 + (d & 7)) * 4 + (d >> 4 & 3);
+                float m = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kTokWarps; ++w) m = fmaxf(m, s_m[w][c]);
+                float lsum = 0.0f, v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kTokWarps; ++w) {
+                    const float fac = s_m[w][c] == m ? 1.0f : ex2(s_m[w][c] - m);
+                    lsum = fmaf(s_l[w][c], fac, lsum);
+                    v = fmaf(buf[(w * 8 + c) * Z::part + pos], fac, v);
+                }
+                const int col = col0 + 8 * h + c;
+                if (whole) {
+                    T *to = static_cast<T *>(a.out) + (t.s.start + col / G) * a.out_stride + static_cast<size_t>(g * G + col % G) * HD + d;
+                    *to = kv_cvt<T>(lsum == 0.0f ? 0.0f : v / lsum);
+                } else {
+                    float *to = dst + (8 * h + c) * Z::part;
+                    to[d] = v;
+                    if (d == 0) {
+                        to[HD] = m;
+                        to[HD + 1] = lsum;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        x += t.end - t.k;
+        tok_next<W>(t, a, G);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// One block to a column of a unit that was cut.
+template <typename T, int HD>
+__global__ void __launch_bounds__(HD) k_paged_tokens_join(const KvPagedAttnArgs a, int G, int max_cb, int grid) {
+    using Z = TokSizes<T, HD>;
+    constexpr int W = Z::W;
+    const int col = blockIdx.x, g = blockIdx.y, d = threadIdx.x;
+    pdl_wait();
+    for (int b = blockIdx.z; b < a.b.B; b += gridDim.z) {
+        const TokSeq s = tok_seq(a, b, G);
+        if (col >= s.cols) continue;
+        const float *slots = static_cast<const float *>(a.ws);
+        const TokCut *cuts = reinterpret_cast<const TokCut *>(slots + static_cast<size_t>(grid) * 2 * W * Z::part);
+        const TokCut cut = cuts[(static_cast<size_t>(b) * a.c.nkv + g) * max_cb + col / W];
+        if (cut.first < 0) continue;
+        const int last = static_cast<int>(cut.last & 0x7fffffffu), n = last - cut.first + 1;
+        float m = -INFINITY, l = 0.0f, v = 0.0f;
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) {
+            const int slot = c == 0 && !(cut.last & 0x80000000u) ? 1 : 0;
+            const float *q = slots + ((static_cast<size_t>(cut.first + c) * 2 + slot) * W + col % W) * Z::part;
+            const float mc = q[HD], lc = q[HD + 1], vc = q[d], top = fmaxf(m, mc);
+            const float f0 = m == top ? 1.0f : ex2(m - top), f1 = mc == top ? 1.0f : ex2(mc - top);
+            l = l * f0 + lc * f1;
+            v = v * f0 + vc * f1;
+            m = top;
+        }
+        T *to = static_cast<T *>(a.out) + (s.start + col / G) * a.out_stride + static_cast<size_t>(g * G + col % G) * HD + d;
+        *to = kv_cvt<T>(l == 0.0f ? 0.0f : v / l);
+    }
+}
+
+// How the token kernels are launched: the columns that a sequence can have, the
+// blocks of them, the CTAs.
+struct TokPlan {
+    int cols = 0, max_cb = 0, grid = 0;
+    size_t bytes = 0;
+};
+constexpr int kTokMinShare = kTokWarps;   // a step to a warp: fewer would only be more to join
+TokPlan tok_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
+    TokPlan p;
+    const int G = nh / nkv, W = type == QW3_F32 ? 8 : 16;
+    p.cols = static_cast<int>(std::min<long long>(static_cast<long long>(max_rows) * G, kTokCols));
+    p.max_cb = (p.cols + W - 1) / W;
+    long long len = max_len;
+    if (window > 0) len = std::min<long long>(len, static_cast<long long>(window) + max_rows + sinks + 3 * kTokKeys);
+    const long long steps = std::max<long long>(1, (len + kTokKeys - 1) / kTokKeys) * B * nkv * p.max_cb;
+    p.grid = static_cast<int>(std::max<long long>(1, std::min<long long>(num_sms(), (steps + kTokMinShare - 1) / kTokMinShare)));
+    p.bytes = static_cast<size_t>(p.grid) * 2 * W * (hd + 4) * 4 + static_cast<size_t>(B) * nkv * p.max_cb * sizeof(TokCut);
+    return p;
+}
+
+template <typename T, int HD>
+cudaError_t tokens_t(const KvPagedAttnArgs &a, const TokPlan &p, bool pdl, cudaStream_t s) {
+    using Z = TokSizes<T, HD>;
+    const int G = a.nh / a.c.nkv;
+    cudaError_t e = launch_pdl(pdl, k_paged_tokens<T, HD>, dim3(p.grid), kTokWarps * 32, Z::smem, 1, s, a, G, p.max_cb, kTokMinShare);
+    if (e != cudaSuccess || p.grid == 1) return e;
+    const dim3 grid(p.cols, a.c.nkv, std::min(a.b.B, 65535));
+    return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, HD, 0, 1, s, a, G, p.max_cb, p.grid);
+}
+
+// ---------------------------------------------------------------- attention of more rows
 
 // One warp to a (row, query head): an online softmax over the row's positions.
 template <typename T, int HD>
@@ -199,11 +749,11 @@ __global__ void __launch_bounds__(128) k_paged_attn(const KvPagedAttnArgs a) {
     const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     pdl_wait();
     if (unit >= static_cast<long long>(a.b.M) * a.nh) return;
-    const int row = static_cast<int>(unit / a.nh), h = static_cast<int>(unit % a.nh), g = h / (a.nh / a.c.nkv);
+    const int row = static_cast<int>(unit / a.nh), h = static_cast<int>(unit % a.nh), G = a.nh / a.c.nkv, g = h / G;
     const int i = kv_seq_of(a.b, row, lane);
     if (i < 0) return;
     const KvSeq q = kv_seq(a.b, i);
-    if (row < q.start || row >= q.start + q.n) return;
+    if (row < q.start || row >= q.start + q.n || q.n * G <= kTokCols) return;
     const int p = q.p0 + row - q.start;
     const T *src = static_cast<const T *>(a.q) + row * a.q_stride + static_cast<size_t>(h) * HD + lane * E;
     float x[E], o[E], m = -INFINITY, l = 0.0f;
@@ -233,25 +783,51 @@ __global__ void __launch_bounds__(128) k_paged_attn(const KvPagedAttnArgs a) {
     pdl_trigger();
 }
 
+template <typename T, int HD>
+cudaError_t rows_t(const KvPagedAttnArgs &a, bool pdl, cudaStream_t s) {
+    const long long units = static_cast<long long>(a.b.M) * a.nh;
+    return launch_pdl(pdl, k_paged_attn<T, HD>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0, 1, s, a);
+}
+
+template <typename T, int HD>
+cudaError_t attn_t(const KvPagedAttnArgs &a, int type, bool pdl, cudaStream_t s) {
+    const TokPlan p = tok_plan(a.b.B, type, a.nh, a.c.nkv, HD, a.b.max_rows, a.b.max_len, a.window, a.sinks);
+    cudaError_t e = tokens_t<T, HD>(a, p, pdl, s);
+    // sequences with more columns than the token kernels take
+    if (e == cudaSuccess && static_cast<long long>(a.b.max_rows) * (a.nh / a.c.nkv) > kTokCols) e = rows_t<T, HD>(a, pdl, s);
+    return e;
+}
+
+template <typename T, int HD>
+cudaError_t configure_t() {
+    return cudaFuncSetAttribute(k_paged_tokens<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(TokSizes<T, HD>::smem));
+}
+
 }  // namespace
 
-cudaError_t configure_kv_paged() { return cudaSuccess; }
+cudaError_t configure_kv_paged() {
+    cudaError_t e = configure_t<float, 128>();
+    if (e == cudaSuccess) e = configure_t<float, 64>();
+    if (e == cudaSuccess) e = configure_t<__half, 128>();
+    if (e == cudaSuccess) e = configure_t<__half, 64>();
+    return e;
+}
 
 cudaError_t launch_kv_paged_append(const KvPagedAppendArgs &a, int type, int hd, bool pdl, cudaStream_t s) {
     if (type == QW3_F32) return hd == 128 ? append_t<float, 128>(a, pdl, s) : append_t<float, 64>(a, pdl, s);
     return hd == 128 ? append_t<__half, 128>(a, pdl, s) : append_t<__half, 64>(a, pdl, s);
 }
 
-size_t kv_paged_attn_workspace_bytes(int, int, int, int, int, int, int, int, int, int) { return 0; }
+size_t kv_paged_attn_workspace_bytes(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len,
+                                     int window, int sinks) {
+    if (B == 0 || M == 0 || max_rows == 0) return 0;
+    return tok_plan(B, type, nh, nkv, hd, max_rows, max_len, window, sinks).bytes;
+}
 
 cudaError_t launch_kv_paged_attn(const KvPagedAttnArgs &a, int type, int hd, bool pdl, cudaStream_t s) {
-    const long long units = static_cast<long long>(a.b.M) * a.nh;
-    const dim3 grid(static_cast<unsigned>((units + 3) / 4));
-    if (type == QW3_F32)
-        return hd == 128 ? launch_pdl(pdl, k_paged_attn<float, 128>, grid, 128, 0, 1, s, a)
-                         : launch_pdl(pdl, k_paged_attn<float, 64>, grid, 128, 0, 1, s, a);
-    return hd == 128 ? launch_pdl(pdl, k_paged_attn<__half, 128>, grid, 128, 0, 1, s, a)
-                     : launch_pdl(pdl, k_paged_attn<__half, 64>, grid, 128, 0, 1, s, a);
+    if (type == QW3_F32) return hd == 128 ? attn_t<float, 128>(a, type, pdl, s) : attn_t<float, 64>(a, type, pdl, s);
+    return hd == 128 ? attn_t<__half, 128>(a, type, pdl, s) : attn_t<__half, 64>(a, type, pdl, s);
 }
 
 }  // namespace qw3

@@ -1655,7 +1655,8 @@ int64_t qw3_kv_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t type, in
         window < 0 || sinks < 0 || static_cast<int64_t>(M) * (n_heads + 2 * n_kv_heads) > INT32_MAX)
         return -1;
     return static_cast<int64_t>(
-        kv_paged_attn_workspace_bytes(B, M, type, n_heads, n_kv_heads, head_dim, max_rows, max_len, window, sinks));
+        kv_paged_attn_workspace_bytes(B, M, type, n_heads, n_kv_heads, head_dim, max_rows, max_len,
+                                     window > kPagedMaxLen ? 0 : window, std::min(sinks, kPagedMaxLen)));
 }
 
 int qw3_kv_paged_attn(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int32_t type, const void *q_dev, int32_t M,
@@ -1682,7 +1683,9 @@ int qw3_kv_paged_attn(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int3
     KvPagedAttnArgs a{};
     a.c = kv_paged_view(cache);
     a.b = kv_batch_view(batch, M, max_rows, max_len);
-    a.q = q_dev; a.q_stride = q_stride; a.nh = n_heads; a.window = window; a.sinks = sinks; a.scale = scale;
+    a.q = q_dev; a.q_stride = q_stride; a.nh = n_heads; a.scale = scale;
+    // (a window of more than any length is none)
+    a.window = window > kPagedMaxLen ? 0 : window; a.sinks = std::min(sinks, kPagedMaxLen);
     a.out = out_dev; a.out_stride = out_stride; a.ws = workspace_dev; a.status = status_dev;
     QW3_CUDA_TRY(configure_all());   // the kernels' shared-memory limits
     QW3_CUDA_TRY(launch_kv_paged_attn(a, type, cache->head_dim, true, static_cast<cudaStream_t>(stream)));
