@@ -1,0 +1,856 @@
+// Attention of many rows over the paged cache on the 5th-generation tensor
+// cores: prompts, and chunks of prompts behind a cached context.
+//
+// Rows are packed: the G query heads that read one kv head and consecutive
+// tokens of one sequence fill a tile of 128 rows (row r: token r / G, head
+// r % G), so that each K and V tile is used by all of them. A CTA takes a unit
+// (one kv head and f16: two row tiles, f32: one) and walks the key tiles of 128
+// positions that some row sees.
+//
+//   S = Q K^T   tcgen05.mma, both operands from shared memory (128-byte swizzle)
+//   P = 2^(S c - ref)   a thread to a row: S from tensor memory, P back over it
+//   O += P V    tcgen05.mma, P from tensor memory, V as it lies (MN-major)
+//
+// Roles: a warp loads K and V tiles by TMA (a box to a page) into a ring, a warp
+// issues the products, two warpgroups do the softmax, so that one is at work
+// while the tensor cores serve the other.
+//  * f16 activations: the warpgroups have a row tile each and share the key
+//    tiles. O stays in tensor memory; a row's reference maximum moves only when
+//    it is passed by 2^8, and the row is then rescaled in place. P is f16.
+//  * f32 activations: Q and P in two f16 parts (hi + lo), two products each. The
+//    warpgroups take alternate key tiles of the same rows, and each adds its
+//    tile's O to a master in registers (f32, round to nearest): the tensor core
+//    truncates its sums, a relative 1.6e-8 for every step of a chain, and a chain
+//    of one tile has 16. The two masters are joined at the end.
+//
+// What a row does not see must not reach it, and 0 * NaN would: in a tile that
+// is not seen whole, V rows that no row of the unit sees are set to zero, and if
+// one that only some rows see is not finite the unit is done again without
+// matrix products (k_rows' slow path).
+//
+// Bound by the tensor cores for long prompts. Few units are split along the keys
+// and joined by a second kernel.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda.h>
+
+#include "qw3_internal.cuh"
+
+namespace qw3 {
+
+namespace {
+
+constexpr int kRwThreads = 384;
+constexpr int kRwKeys = 128, kRwRows = 128;
+constexpr float kRwOff16 = 6.0f, kRwLazy = 8.0f, kRwOff32 = 14.0f;
+
+template <typename T, int HD>
+struct RwSizes {
+    static constexpr bool split = sizeof(T) == 4;
+    static constexpr int QT = split ? 1 : 2;                       // row tiles of a unit
+    static constexpr uint32_t tile = kRwRows * HD * 2;             // bytes of a row tile, a K tile, a V tile
+    static constexpr int stages = HD == 128 ? 5 : 8;
+    static constexpr uint32_t smem = 2 * tile + stages * tile + 1024;
+    static constexpr int part = HD + 4;                            // floats of a row's part: output, maximum, sum
+};
+
+struct RwUnit {
+    int seq, start, tok0, n, p0;   // token tok0 + k of the sequence's n rows is at p0 + tok0 + k
+};
+
+// What the join needs of a unit.
+struct RwCut {
+    int start, tokens, parts, unused;
+};
+
+struct RwArgs {
+    KvPagedAttnArgs a;
+    int G, TT;          // query heads of a kv head, tokens of a row tile
+    int min_cols;       // sequences with as many columns, or fewer, are others'
+    int split_tiles;    // key tiles of a part
+    int splits, units;  // parts and units that the workspace has room for
+    float *ws;
+};
+
+__device__ __forceinline__ float rw_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t rw_pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 rw_unpack(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+__device__ __forceinline__ void rw_ld32(uint32_t at, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void rw_st32(uint32_t at, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void rw_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void rw_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void rw_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void rw_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void rw_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Shared-memory operand with a 128-byte swizzle: K-major (rows of 128 bytes, 8-row
+// groups 1024 bytes apart) or MN-major (8-row groups along K 1024 bytes apart, 64
+// columns of N `lbo` bytes apart).
+__device__ __forceinline__ uint64_t rw_desc(uint32_t at, uint32_t lbo) {
+    return static_cast<uint64_t>((at & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16, f16 operands, f32 sums; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t rw_idesc(int N, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kRwRows >> 4) << 24);
+}
+__device__ __forceinline__ void rw_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+}
+__device__ __forceinline__ void rw_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+}
+__device__ __forceinline__ void rw_tma(uint32_t to, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void rw_bar(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+
+// The key tiles of rows at pmin .. pmax: tile i is key tile i < sink ? i : i - sink + first.
+struct RwTiles {
+    int sink, first, n;
+    __device__ __forceinline__ int key(int i) const { return (i < sink ? i : i - sink + first) * kRwKeys; }
+};
+__device__ __forceinline__ RwTiles rw_tiles(int pmin, int pmax, int window, int sinks) {
+    RwTiles t;
+    const int lo = window > 0 ? max(0, pmin - window + 1) : 0;
+    t.first = lo / kRwKeys;
+    t.sink = window > 0 ? min((min(sinks, lo) + kRwKeys - 1) / kRwKeys, t.first) : 0;
+    t.n = pmax < 0 ? 0 : t.sink + pmax / kRwKeys - t.first + 1;
+    return t;
+}
+
+// The unit without matrix products, for the tiles i0 .. i1 - 1: 8 warps, a row at
+// a time. dst: the part's rows, or null for the output.
+template <typename T, int HD>
+__device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwTiles &t, int i0, int i1, int g, int rows, float off,
+                                     float *dst) {
+    constexpr int E = HD / 32;
+    const int lane = threadIdx.x & 31;
+    const KvPagedAttnArgs &a = r.a;
+    for (int row = threadIdx.x >> 5; row < rows; row += 8) {
+        const int tok = row / kRwRows * r.TT + row % kRwRows / r.G, h = g * r.G + row % kRwRows % r.G;
+        if (row % kRwRows >= r.TT * r.G || u.tok0 + tok >= u.n) continue;
+        const int p = u.p0 + u.tok0 + tok;
+        const size_t at = static_cast<size_t>(u.start + u.tok0 + tok);
+        const T *q = static_cast<const T *>(a.q) + at * a.q_stride + static_cast<size_t>(h) * HD + lane * E;
+        float x[E], o[E], m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] = kv_f32(q[e]);
+            o[e] = 0.0f;
+        }
+        for (int i = i0; i < i1; ++i) {
+            const int j0 = t.key(i);
+            for (int j = j0; j < j0 + kRwKeys; ++j) {
+                if (!kv_sees(p, j, a.window, a.sinks)) continue;
+                const int page = kv_page(a.b, a.c, u.seq, j);
+                if (page < 0) continue;
+                const __half *k = kv_paged_row<HD>(a.c, page, 0, g, j) + lane * E, *v = kv_paged_row<HD>(a.c, page, 1, g, j) + lane * E;
+                float d = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) d = fmaf(x[e], kv_f32(k[e]), d);
+                d = warp_sum(d) * (a.scale * 1.4426950408889634f);
+                const float mn = d > m ? d : m, c = m == mn ? 1.0f : rw_ex2(m - mn), w = rw_ex2(d - mn + off);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(w, kv_f32(v[e]), o[e] * c);
+                l = fmaf(l, c, w);
+                m = mn;
+            }
+        }
+        if (dst) {
+            float *to = dst + static_cast<size_t>(row) * RwSizes<T, HD>::part;
+#pragma unroll
+            for (int e = 0; e < E; ++e) to[lane * E + e] = o[e];
+            if (lane == 0) {
+                to[HD] = m;
+                to[HD + 1] = l;
+            }
+        } else {
+            T *to = static_cast<T *>(a.out) + at * a.out_stride + static_cast<size_t>(h) * HD + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) to[e] = kv_cvt<T>(l == 0.0f ? 0.0f : o[e] / l);
+        }
+    }
+}
+
+// 16 bytes of output.
+__device__ __forceinline__ void rw_store(float *to, const float *v) {
+    *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void rw_store(__half *to, const float *v) {
+    *reinterpret_cast<uint4 *>(to) = make_uint4(rw_pack(v[0], v[1]), rw_pack(v[2], v[3]), rw_pack(v[4], v[5]), rw_pack(v[6], v[7]));
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, const __grid_constant__ CUtensorMap map) {
+    using Z = RwSizes<T, HD>;
+    constexpr int ST = Z::stages, QT = Z::QT;
+    extern __shared__ uint8_t rw_smem[];
+    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2], b_o[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_err, s_bad, s_found, s_sum[kRwThreads / 32];
+    __shared__ RwUnit s_unit;
+    __shared__ float s_c[kRwRows], s_ml[2][kRwRows];
+    const KvPagedAttnArgs &a = r.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = (smem_u32(rw_smem) + 1023) & ~1023u;
+    uint8_t *const smem = rw_smem + (base - smem_u32(rw_smem));
+    const int g = blockIdx.x % a.c.nkv, pair = blockIdx.x / a.c.nkv;
+    const int UT = r.TT * QT;   // tokens of a unit
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b_s[i], 1);
+            mbar_init(&b_p[i], 128);
+            mbar_init(&b_o[i], 1);
+        }
+        fence_mbar_init();
+        s_err = 0;
+        s_bad = 0;
+        s_found = 0;
+    }
+    __syncthreads();
+    pdl_wait();
+
+    // ---- the unit: number `pair` of the sequences' units, a sequence's last (longest) one first
+    {
+        int before = 0;
+        for (int b0 = 0; b0 < a.b.B; b0 += kRwThreads) {
+            const int b = b0 + tid;
+            KvSeq q{0, 0, 0};
+            int mine = 0;
+            if (b < a.b.B) {
+                q = kv_seq(a.b, b);
+                if (q.n * r.G > r.min_cols) mine = (q.n + UT - 1) / UT;
+            }
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (lane == 31) s_sum[warp] = upto;
+            __syncthreads();
+            int at = before + upto - mine, all = 0;
+            for (int w = 0; w < kRwThreads / 32; ++w) {
+                if (w < warp) at += s_sum[w];
+                all += s_sum[w];
+            }
+            if (pair >= at && pair < at + mine) {
+                s_unit = RwUnit{b, q.start, (mine - 1 - (pair - at)) * UT, q.n, q.p0};
+                s_found = 1;
+            }
+            before += all;
+            __syncthreads();
+            if (before > pair) break;
+        }
+    }
+    RwCut *const cuts = reinterpret_cast<RwCut *>(r.ws);
+    if (!s_found) {
+        if (blockIdx.y == 0 && tid == 0 && r.splits > 1) cuts[blockIdx.x] = RwCut{0, 0, 0, 0};
+        return;
+    }
+    const RwUnit u = s_unit;
+    const int tokens = min(UT, u.n - u.tok0);
+    const int pmin = u.p0 + u.tok0, pmax = pmin + tokens - 1;
+    const RwTiles tiles = rw_tiles(pmin, pmax, a.window, a.sinks);
+    const int parts = max(1, (tiles.n + r.split_tiles - 1) / r.split_tiles), part = blockIdx.y;
+    if (part == 0 && tid == 0 && r.splits > 1) cuts[blockIdx.x] = RwCut{u.start + u.tok0, tokens, parts, 0};
+    if (part >= parts) return;
+    const int i0 = part * r.split_tiles, i1 = min(tiles.n, i0 + r.split_tiles), NT = i1 - i0;
+    float *const dst = parts == 1 ? nullptr
+                                  : r.ws + static_cast<size_t>(r.units) * 4 +
+                                        (static_cast<size_t>(blockIdx.x) * r.splits + part) * (QT * kRwRows) * Z::part;
+    const int row_tiles = QT == 1 ? 1 : (tokens > r.TT ? 2 : 1);
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+
+    // ---- Q to shared memory. A negative scale goes into it, so that scores are scaled by c > 0
+    const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
+    const float c0 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
+    {
+        constexpr int L = HD / 8, RW = 32 / L;   // lanes to a row, rows to a warp
+        const int ch = lane % L;
+#pragma unroll 4
+        for (int row = warp * RW + lane / L; row < QT * kRwRows; row += kRwThreads / 32 * RW) {
+            const int rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;
+            const bool real = rr < r.TT * r.G && tok < tokens;
+            const T *q = static_cast<const T *>(a.q) + static_cast<size_t>(u.start + u.tok0 + (real ? tok : 0)) * a.q_stride +
+                         static_cast<size_t>(g * r.G + (real ? rr % r.G : 0)) * HD + ch * 8;
+            uint8_t *to = smem + (ch >> 3) * (kRwRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+            if constexpr (Z::split) {
+                float v[8];
+                const float4 x = *reinterpret_cast<const float4 *>(q), y = *reinterpret_cast<const float4 *>(q + 4);
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+                float amax = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+                const unsigned group = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << (lane / L * L);
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
+                // the power of two that takes the row's largest into [2^14, 2^15)
+                const int ex = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23 & 0xffu));
+                const float up = pow2_f32(ex) * sign;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = real ? v[e] * up : 0.0f;
+                uint4 hi, lo;
+                split8_f16(v, hi, lo);
+                *reinterpret_cast<uint4 *>(to) = hi;
+                *reinterpret_cast<uint4 *>(to + Z::tile) = lo;
+                if (ch == 0) s_c[rr] = pow2_f32(-ex) * c0;
+            } else {
+                uint4 x = real ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
+                if (sign != 1.0f) {
+                    const __half2 f = __float2half2_rn(sign);
+                    __half2 *h = reinterpret_cast<__half2 *>(&x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
+                }
+                *reinterpret_cast<uint4 *>(to + (row / kRwRows) * Z::tile) = x;
+            }
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    rw_before();
+    __syncthreads();
+    rw_after();
+    const uint32_t tmem = s_tmem;
+    const uint32_t ring = base + 2 * Z::tile;
+    volatile int *err = &s_err;
+    // fill n of the ring: its key tile, and whether it is V
+    auto fill = [&](int n, int &i, bool &v) {
+        if constexpr (!Z::split) {   // K0 V0 K1 V1 ..
+            v = n & 1;
+            i = n >> 1;
+        } else {                     // K0 K1 V0 K2 V1 .. (the order of the products)
+            v = n == 2 * NT - 1 || (n >= 2 && !(n & 1));
+            i = n == 2 * NT - 1 ? NT - 1 : v ? (n - 2) >> 1 : (n + 1) >> 1;
+        }
+    };
+    auto fill_of_k = [&](int i) { return Z::split ? max(0, 2 * i - 1) : 2 * i; };
+    auto fill_of_v = [&](int i) { return Z::split ? min(2 * i + 2, 2 * NT - 1) : 2 * i + 1; };
+    auto wait = [&](uint64_t *bar, int parity) {
+        if (*err || !mbar_wait_bounded(bar, static_cast<uint32_t>(parity & 1))) *err = 1;
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+            // ---- loads: a lane to a page of the tile
+            const int shift = min(a.c.shift, 7), boxes = kRwKeys >> shift;
+            const uint32_t bytes = static_cast<uint32_t>(HD * 2) << shift;
+            int n = 0;
+            for (; n < 2 * NT && !*err; ++n) {
+                int i;
+                bool v;
+                fill(n, i, v);
+                const int j = tiles.key(i0 + i) + (lane << shift);
+                const int page = lane < boxes && j <= pmax ? kv_page(a.b, a.c, u.seq, j) : -1;
+                const int st = n % ST;
+                if (n >= ST) wait(&b_empty[st], n / ST - 1);
+                if (__any_sync(0xffffffffu, *err != 0)) break;
+                const int held = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(&b_full[st], held * bytes);
+                __syncwarp();
+                if (page >= 0) {
+                    const int y = (((page * 2 + v) * a.c.nkv + g) << a.c.shift) + (j & ((1 << a.c.shift) - 1));
+                    const uint32_t to = ring + st * Z::tile + (static_cast<uint32_t>(lane) << shift) * 128;
+#pragma unroll
+                    for (int h = 0; h < HD / 64; ++h) rw_tma(to + h * (kRwKeys * 128), &map, h * 64, y, &b_full[st]);
+                }
+            }
+            // the CTA may end when every copy has landed, and every stage has been released
+            for (int k = max(0, n - ST); k < n; ++k) {
+                if (*err) (void)mbar_wait_bounded(&b_full[k % ST], static_cast<uint32_t>(k / ST & 1));
+                else wait(&b_empty[k % ST], k / ST);
+            }
+        } else if (warp == 9 && lane == 0 && NT > 0) {
+            // ---- products
+            auto qk = [&](int s, int i) {
+                const int n = fill_of_k(i), st = n % ST;
+                wait(&b_full[st], n / ST);
+                if (*err) return;
+                rw_after();
+                const uint32_t k = ring + st * Z::tile, q = base + (QT == 2 ? s * Z::tile : 0);
+#pragma unroll
+                for (int part_ = 0; part_ < (Z::split ? 2 : 1); ++part_)
+#pragma unroll
+                    for (int e = 0; e < HD / 16; ++e) {
+                        const uint32_t at = (e >> 2) * (kRwRows * 128) + (e & 3) * 32;
+                        rw_mma_ss(tmem + s * 128, rw_desc(q + part_ * Z::tile + at, 16), rw_desc(k + at, 16), rw_idesc(kRwKeys, false),
+                                  part_ + e > 0);
+                    }
+            };
+            auto pv = [&](int s, int i, bool add) {
+                const int n = fill_of_v(i), st = n % ST;
+                wait(&b_full[st], n / ST);
+                wait(&b_p[s], Z::split ? i >> 1 : i);
+                if (*err) return;
+                rw_after();
+                const uint32_t v = ring + st * Z::tile, p = tmem + s * 128;
+#pragma unroll
+                for (int e = 0; e < kRwKeys / 16; ++e) {
+                    const uint64_t d = rw_desc(v + e * 2048, kRwKeys * 128);
+                    // P: f16 [64 columns]; f32: hi and lo of 32 keys next to each other, 16 columns each
+                    const uint32_t at = p + (Z::split ? (e >> 1) * 32 + (e & 1) * 8 : e * 8);
+                    rw_mma_ts(tmem + 256 + s * HD, at, d, rw_idesc(HD, true), add || e > 0);
+                    if constexpr (Z::split) rw_mma_ts(tmem + 256 + s * HD, at + 16, d, rw_idesc(HD, true), true);
+                }
+            };
+            if constexpr (!Z::split) {
+                for (int s = 0; s < row_tiles; ++s) {
+                    qk(s, 0);
+                    rw_commit(&b_s[s]);
+                }
+                rw_commit(&b_empty[0]);
+                for (int i = 0; i < NT && !*err; ++i) {
+                    for (int s = 0; s < row_tiles; ++s) {
+                        pv(s, i, i > 0);
+                        if (i + 1 < NT) {
+                            qk(s, i + 1);
+                            rw_commit(&b_s[s]);
+                        } else {
+                            rw_commit(&b_o[s]);
+                        }
+                    }
+                    rw_commit(&b_empty[fill_of_v(i) % ST]);
+                    if (i + 1 < NT) rw_commit(&b_empty[fill_of_k(i + 1) % ST]);
+                }
+            } else {
+                for (int i = 0; i < min(2, NT); ++i) {
+                    qk(i, i);
+                    rw_commit(&b_s[i]);
+                    rw_commit(&b_empty[fill_of_k(i) % ST]);
+                }
+                for (int i = 0; i < NT && !*err; ++i) {
+                    pv(i & 1, i, false);
+                    rw_commit(&b_empty[fill_of_v(i) % ST]);
+                    if (i + 2 < NT) {
+                        qk(i & 1, i + 2);
+                        rw_commit(&b_s[i & 1]);
+                        rw_commit(&b_empty[fill_of_k(i + 2) % ST]);
+                    } else {
+                        rw_commit(&b_o[i & 1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---- softmax: warpgroup s, a thread to a row
+        const int s = warp >> 2, rr = tid & 127;
+        const int tok = (QT == 2 ? s * r.TT : 0) + rr / r.G;
+        const bool real = rr < r.TT * r.G && tok < tokens;
+        const int p = pmin + min(tok, tokens - 1);
+        // the rows of this warpgroup's tile
+        const int smin = QT == 2 ? min(pmin + s * r.TT, pmax) : pmin, smax = QT == 2 ? min(smin + r.TT - 1, pmax) : pmax;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + s * 128, tO = tmem + lanes + 256 + s * HD;
+        const float c = Z::split ? s_c[rr] : c0;
+        constexpr float kOff = Z::split ? kRwOff32 : kRwOff16;
+        float m = -INFINITY, l = 0.0f;   // reference (a score before c), sum of weights
+        float master[Z::split ? HD : 1];
+        if constexpr (Z::split) {
+#pragma unroll
+            for (int d = 0; d < HD; ++d) master[d] = 0.0f;
+        }
+        const bool active = QT == 1 || s < row_tiles;
+        int own = 0;   // tiles taken
+        for (int i = Z::split ? s : 0; active && i < NT; i += Z::split ? 2 : 1, ++own) {
+            const int j0 = tiles.key(i0 + i);
+            // which 16 positions have a page (lanes 0..7 look)
+            const int jl = j0 + 16 * (lane & 7);
+            const uint32_t pages = __ballot_sync(0xffffffffu, jl > pmax || kv_page(a.b, a.c, u.seq, jl) >= 0) & 0xffu;
+            const bool holes = pages != 0xffu;
+            // does every row of the tile see every position?
+            const bool open = !holes && j0 + kRwKeys - 1 <= smin && (a.window == 0 || smax - j0 < a.window || j0 + kRwKeys <= a.sinks);
+            if (!open) {
+                // V: this thread's position
+                const int n = fill_of_v(i), st = n % ST, j = j0 + rr;
+                const bool page = pages >> (rr >> 4) & 1;
+                const bool any = page && j <= pmax && kv_sees(max(j, pmin), j, a.window, a.sinks);
+                const bool all = page && j <= smin && kv_sees(smax, j, a.window, a.sinks);
+                wait(&b_full[st], n / ST);
+                uint8_t *v = smem + (2 + st) * Z::tile + rr * 128;
+                bool bad = false;
+                if (!all) {
+#pragma unroll
+                    for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint4 *at = reinterpret_cast<uint4 *>(v + h * (kRwKeys * 128) + ((e ^ (lane & 7)) << 4));
+                            if (!any) {
+                                *at = make_uint4(0, 0, 0, 0);
+                            } else {
+                                const uint4 x = *at;
+                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7c00u) == 0x7c00u || (w[k] & 0x7c000000u) == 0x7c000000u;
+                            }
+                        }
+                }
+                if (bad) s_bad = 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            wait(&b_s[s], own);
+            rw_after();
+            // the row's positions j0 + k, k in [k_lo, k_hi) or [0, k_sink), of pages that are there
+            const int k_hi = p - j0 + 1, k_lo = a.window > 0 ? p - a.window + 1 - j0 : 0, k_sink = a.window > 0 ? a.sinks - j0 : 0;
+            auto sees = [&](int k) { return k < k_hi && (k >= k_lo || k < k_sink) && (pages >> (k >> 4) & 1); };
+            if constexpr (!Z::split) {
+                uint32_t v[128];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) rw_ld32(tS + 32 * k, v + 32 * k);
+                rw_wait_ld();
+                if (!open) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        if (!sees(k)) v[k] = 0xff800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 128; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+                const bool far = m == -INFINITY ? mx > -INFINITY : (mx - m) * c > kRwLazy;
+                if (__any_sync(0xffffffffu, far)) {
+                    const float mn = far ? mx : m, f = m == mn ? 1.0f : m == -INFINITY ? 0.0f : rw_ex2((m - mn) * c);
+                    m = mn;
+                    l *= f;
+                    if (own > 0) {
+#pragma unroll 1
+                        for (int d = 0; d < HD; d += 32) {
+                            uint32_t o[32];
+                            rw_ld32(tO + d, o);
+                            rw_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            rw_st32(tO + d, o);
+                        }
+                    }
+                }
+                const float b = (m == -INFINITY ? 0.0f : m * c) - kOff;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < 128; k += 2) {
+                    const float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
+                    sum[k >> 1 & 1] += x;
+                    sum[2 + (k >> 1 & 1)] += y;
+                    v[k >> 1] = rw_pack(x, y);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                rw_st32(tS, v);
+                rw_st32(tS + 32, v + 32);
+            } else {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k0 = 0; k0 < 128; k0 += 32) {
+                    uint32_t v[32];
+                    rw_ld32(tS + k0, v);
+                    rw_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (open || sees(k0 + k)) mx = fmaxf(mx, __uint_as_float(v[k]));
+                }
+                const float mn = fmaxf(m, mx), f = m == mn ? 1.0f : rw_ex2((m - mn) * c);
+                // the O of this warpgroup's last tile, beside the old reference
+                if (own > 0) {
+#pragma unroll
+                    for (int d = 0; d < HD; d += 32) {
+                        uint32_t o[32];
+                        rw_ld32(tO + d, o);
+                        rw_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) master[d + e] = (master[d + e] + __uint_as_float(o[e])) * f;
+                    }
+                }
+                m = mn;
+                l *= f;
+                const float b = (m == -INFINITY ? 0.0f : m * c) - kOff;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int k0 = 0; k0 < 128; k0 += 32) {
+                    uint32_t v[32], w[32];
+                    rw_ld32(tS + k0, v);
+                    rw_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
+                        if (!open) {
+                            x = sees(k0 + k) ? x : 0.0f;
+                            y = sees(k0 + k + 1) ? y : 0.0f;
+                        }
+                        sum[0] += x;
+                        sum[1] += y;
+                        const uint32_t hi = rw_pack(x, y);
+                        const float2 h = rw_unpack(hi);
+                        w[k >> 1] = hi;
+                        w[16 + (k >> 1)] = rw_pack(x - h.x, y - h.y);
+                    }
+                    rw_st32(tS + k0, w);
+                }
+                l += sum[0] + sum[1];
+            }
+            rw_wait_st();
+            rw_before();
+            mbar_arrive(&b_p[s]);
+        }
+        if (active && own > 0) {
+            wait(&b_o[s], 0);
+            rw_after();
+        }
+        const float m2 = m == -INFINITY ? -INFINITY : m * c;   // the reference in base 2
+        const size_t at = static_cast<size_t>(u.start + u.tok0 + tok);
+        T *const out = static_cast<T *>(a.out) + at * a.out_stride + static_cast<size_t>(g * r.G + rr % r.G) * HD;
+        float *const to = dst ? dst + static_cast<size_t>((QT == 2 ? s * kRwRows : 0) + rr) * Z::part : nullptr;
+        if constexpr (!Z::split) {
+            rw_bar(1);
+            if (!s_bad) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if (active) {
+#pragma unroll
+                    for (int d = 0; d < HD; d += 32) {
+                        uint32_t o[32];
+                        if (own > 0) rw_ld32(tO + d, o);
+                        rw_wait_ld();
+                        float v[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = own > 0 ? __uint_as_float(o[e]) : 0.0f;
+                        if (real) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                if (to) {
+                                    rw_store(to + d + e, v + e);
+                                } else {
+                                    float w[8];
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) w[k] = v[e + k] * inv;
+                                    rw_store(out + d + e, w);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (to && real) {
+                        to[HD] = m2;
+                        to[HD + 1] = l;
+                    }
+                }
+            }
+        } else {
+            if (own > 0) {
+#pragma unroll
+                for (int d = 0; d < HD; d += 32) {
+                    uint32_t o[32];
+                    rw_ld32(tO + d, o);
+                    rw_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) master[d + e] += __uint_as_float(o[e]);
+                }
+            }
+            // the second warpgroup's part joins the first one's, through Q's place (every score is there: Q is done with)
+            float *x = reinterpret_cast<float *>(smem) + rr;
+            if (s == 1 && NT > 1) {
+#pragma unroll
+                for (int d = 0; d < HD; ++d) x[d * kRwRows] = master[d];
+                s_ml[0][rr] = m2;
+                s_ml[1][rr] = l;
+            }
+            rw_bar(1);
+            if (!s_bad && s == 0 && real) {
+                const bool two = NT > 1;
+                const float mo = two ? s_ml[0][rr] : m2, lo = two ? s_ml[1][rr] : 0.0f, top = fmaxf(m2, mo);
+                const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = mo == top ? 1.0f : rw_ex2(mo - top);
+                const float sum = l * f0 + lo * f1, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int d = 0; d < HD; d += 8) {
+                    float w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[k] = master[d + k] * f0 + (two ? x[(d + k) * kRwRows] * f1 : 0.0f);
+                    if (to) {
+                        rw_store(to + d, w);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] *= inv;
+                        rw_store(out + d, w);
+                    }
+                }
+                if (to) {
+                    to[HD] = top;
+                    to[HD + 1] = sum;
+                }
+            }
+        }
+        if (s_bad) rw_slow<T, HD>(r, u, tiles, i0, i1, g, QT * kRwRows, kOff, dst);
+        rw_before();
+    }
+    __syncthreads();
+    if (tid == 0 && s_err) record_status(a.status, QW3_ERR_TIMEOUT);
+    if (warp == 0) {
+        rw_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// A warp to a row of a unit that was split.
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) k_paged_rows_join(const RwArgs r) {
+    using Z = RwSizes<T, HD>;
+    constexpr int E = HD / 32;
+    const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5), unit = blockIdx.x;
+    pdl_wait();
+    const RwCut cut = reinterpret_cast<const RwCut *>(r.ws)[unit];
+    const int rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;
+    if (cut.parts < 2 || rr >= r.TT * r.G || tok >= cut.tokens) return;
+    const float *src = r.ws + static_cast<size_t>(r.units) * 4 + (static_cast<size_t>(unit) * r.splits * (Z::QT * kRwRows) + row) * Z::part;
+    float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < cut.parts; ++k) {
+        const float *q = src + static_cast<size_t>(k) * (Z::QT * kRwRows) * Z::part;
+        const float mc = q[HD], lc = q[HD + 1], top = fmaxf(m, mc);
+        const float f0 = m == top ? 1.0f : rw_ex2(m - top), f1 = mc == top ? 1.0f : rw_ex2(mc - top);
+        l = l * f0 + lc * f1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + q[lane * E + e] * f1;
+        m = top;
+    }
+    T *to = static_cast<T *>(r.a.out) + static_cast<size_t>(cut.start + tok) * r.a.out_stride +
+            static_cast<size_t>(unit % r.a.c.nkv * r.G + rr % r.G) * HD + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) to[e] = kv_cvt<T>(l == 0.0f ? 0.0f : o[e] / l);
+}
+
+// How the units are launched and split: `units` CTAs of one part each (an upper
+// bound: starts are on the device), times `splits`.
+struct RwPlan {
+    int TT = 0, units = 0, splits = 1, split_tiles = 0;
+    size_t bytes = 0;
+};
+RwPlan rw_plan(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
+    RwPlan p;
+    const int G = nh / nkv, QT = type == QW3_F32 ? 1 : 2;
+    p.TT = kRwRows / G;
+    const int UT = p.TT * QT;
+    const long long pairs = std::min(static_cast<long long>(B) * ((max_rows + UT - 1) / UT), (M - std::min(B, M)) / UT + static_cast<long long>(std::min(B, M)));
+    p.units = static_cast<int>(pairs * nkv);
+    long long len = max_len;
+    if (window > 0) len = std::min<long long>(len, static_cast<long long>(window) + UT + 2 * kRwKeys + sinks);
+    const int tiles = static_cast<int>(std::max<long long>(1, (len + kRwKeys - 1) / kRwKeys));
+    // the parts that take the fewest rounds of tiles, with three tiles' time for a part's ends and four for the join
+    const int sms = num_sms();
+    double best = 0.0;
+    for (int s = 1; s <= std::min(tiles, 32) && (s == 1 || static_cast<long long>(p.units) * s <= 4 * sms); ++s) {
+        const int per = (tiles + s - 1) / s;
+        const double cost = static_cast<double>((static_cast<long long>(p.units) * s + sms - 1) / sms) * (per + 3) + (s > 1 ? 4 : 0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.splits = s;
+            p.split_tiles = per;
+        }
+    }
+    if (p.splits > 1)
+        p.bytes = static_cast<size_t>(p.units) * sizeof(RwCut) +
+                  static_cast<size_t>(p.units) * p.splits * (QT * kRwRows) * (hd + 4) * sizeof(float);
+    return p;
+}
+
+// cuTensorMapEncodeTiled, found at run time: the library loads without a driver too.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+template <typename T, int HD>
+cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, float *ws, bool pdl, cudaStream_t s) {
+    using Z = RwSizes<T, HD>;
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    // the pool as rows of HD values; a box is 64 values of the rows of a page that lie in one key tile
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {HD, (static_cast<cuuint64_t>(a.c.pages) * 2 * a.c.nkv) << a.c.shift}, strides[1] = {HD * 2};
+    const cuuint32_t box[2] = {64, std::min<cuuint32_t>(1u << a.c.shift, kRwKeys)}, step[2] = {1, 1};
+    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.c.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const RwArgs r{a, a.nh / a.c.nkv, p.TT, min_cols, p.split_tiles, p.splits, p.units, ws};
+    cudaError_t e = launch_pdl(pdl, k_paged_rows<T, HD>, dim3(p.units, p.splits), kRwThreads, Z::smem, 1, s, r, map);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 4), 128, 0, 1, s, r);
+}
+
+template <typename T, int HD>
+cudaError_t configure_rows_t() {
+    return cudaFuncSetAttribute(k_paged_rows<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(RwSizes<T, HD>::smem));
+}
+
+}  // namespace
+
+cudaError_t configure_kv_paged_rows() {
+    cudaError_t e = configure_rows_t<float, 128>();
+    if (e == cudaSuccess) e = configure_rows_t<float, 64>();
+    if (e == cudaSuccess) e = configure_rows_t<__half, 128>();
+    if (e == cudaSuccess) e = configure_rows_t<__half, 64>();
+    return e;
+}
+
+size_t kv_paged_rows_workspace_bytes(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
+    return rw_plan(B, M, type, nh, nkv, hd, max_rows, max_len, window, sinks).bytes;
+}
+
+cudaError_t launch_kv_paged_rows(const KvPagedAttnArgs &a, int type, int hd, int min_cols, float *ws, bool pdl, cudaStream_t s) {
+    const RwPlan p = rw_plan(a.b.B, a.b.M, type, a.nh, a.c.nkv, hd, a.b.max_rows, a.b.max_len, a.window, a.sinks);
+    if (type == QW3_F32) return hd == 128 ? rows_t<float, 128>(a, min_cols, p, ws, pdl, s) : rows_t<float, 64>(a, min_cols, p, ws, pdl, s);
+    return hd == 128 ? rows_t<__half, 128>(a, min_cols, p, ws, pdl, s) : rows_t<__half, 64>(a, min_cols, p, ws, pdl, s);
+}
+
+}  // namespace qw3

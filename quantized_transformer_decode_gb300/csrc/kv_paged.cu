@@ -739,65 +739,6 @@ cudaError_t tokens_t(const KvPagedAttnArgs &a, const TokPlan &p, bool pdl, cudaS
     return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, HD, 0, 1, s, a, G, p.max_cb, p.grid);
 }
 
-// ---------------------------------------------------------------- attention of more rows
-
-// One warp to a (row, query head): an online softmax over the row's positions.
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) k_paged_attn(const KvPagedAttnArgs a) {
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    pdl_wait();
-    if (unit >= static_cast<long long>(a.b.M) * a.nh) return;
-    const int row = static_cast<int>(unit / a.nh), h = static_cast<int>(unit % a.nh), G = a.nh / a.c.nkv, g = h / G;
-    const int i = kv_seq_of(a.b, row, lane);
-    if (i < 0) return;
-    const KvSeq q = kv_seq(a.b, i);
-    if (row < q.start || row >= q.start + q.n || q.n * G <= kTokCols) return;
-    const int p = q.p0 + row - q.start;
-    const T *src = static_cast<const T *>(a.q) + row * a.q_stride + static_cast<size_t>(h) * HD + lane * E;
-    float x[E], o[E], m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        x[e] = kv_f32(src[e]);
-        o[e] = 0.0f;
-    }
-    for (int j = 0; j <= p; ++j) {
-        if (!kv_sees(p, j, a.window, a.sinks)) continue;
-        const int page = kv_page(a.b, a.c, i, j);
-        if (page < 0) continue;
-        const __half *k = kv_paged_row<HD>(a.c, page, 0, g, j) + lane * E, *v = kv_paged_row<HD>(a.c, page, 1, g, j) + lane * E;
-        float d = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) d = fmaf(x[e], kv_f32(k[e]), d);
-        d = warp_sum(d) * a.scale;
-        const float mn = d > m ? d : m, c = m == -INFINITY ? 0.0f : expf(m - mn), w = expf(d - mn);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, kv_f32(v[e]), o[e] * c);
-        l = fmaf(l, c, w);
-        m = mn;
-    }
-    T *dst = static_cast<T *>(a.out) + row * a.out_stride + static_cast<size_t>(h) * HD + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[e] = kv_cvt<T>(l == 0.0f ? 0.0f : o[e] / l);
-    pdl_trigger();
-}
-
-template <typename T, int HD>
-cudaError_t rows_t(const KvPagedAttnArgs &a, bool pdl, cudaStream_t s) {
-    const long long units = static_cast<long long>(a.b.M) * a.nh;
-    return launch_pdl(pdl, k_paged_attn<T, HD>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0, 1, s, a);
-}
-
-template <typename T, int HD>
-cudaError_t attn_t(const KvPagedAttnArgs &a, int type, bool pdl, cudaStream_t s) {
-    const TokPlan p = tok_plan(a.b.B, type, a.nh, a.c.nkv, HD, a.b.max_rows, a.b.max_len, a.window, a.sinks);
-    cudaError_t e = tokens_t<T, HD>(a, p, pdl, s);
-    // sequences with more columns than the token kernels take
-    if (e == cudaSuccess && static_cast<long long>(a.b.max_rows) * (a.nh / a.c.nkv) > kTokCols) e = rows_t<T, HD>(a, pdl, s);
-    return e;
-}
-
 template <typename T, int HD>
 cudaError_t configure_t() {
     return cudaFuncSetAttribute(k_paged_tokens<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -811,6 +752,7 @@ cudaError_t configure_kv_paged() {
     if (e == cudaSuccess) e = configure_t<float, 64>();
     if (e == cudaSuccess) e = configure_t<__half, 128>();
     if (e == cudaSuccess) e = configure_t<__half, 64>();
+    if (e == cudaSuccess) e = configure_kv_paged_rows();
     return e;
 }
 
@@ -819,15 +761,44 @@ cudaError_t launch_kv_paged_append(const KvPagedAppendArgs &a, int type, int hd,
     return hd == 128 ? append_t<__half, 128>(a, pdl, s) : append_t<__half, 64>(a, pdl, s);
 }
 
+namespace {
+
+// Which kernels a call needs: sequences of up to kTokCols columns are the token
+// kernels', longer ones attn_paged_tc.cu's. One sequence alone goes by max_rows.
+struct AttnPlan {
+    bool tokens, rows;
+    TokPlan tok;
+    size_t tok_bytes;
+};
+AttnPlan attn_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
+    AttnPlan p{};
+    p.rows = static_cast<long long>(max_rows) * (nh / nkv) > kTokCols;
+    p.tokens = !p.rows || B > 1;
+    if (p.tokens) {
+        p.tok = tok_plan(B, type, nh, nkv, hd, max_rows, max_len, window, sinks);
+        p.tok_bytes = (p.tok.bytes + 127) / 128 * 128;
+    }
+    return p;
+}
+
+}  // namespace
+
 size_t kv_paged_attn_workspace_bytes(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len,
                                      int window, int sinks) {
     if (B == 0 || M == 0 || max_rows == 0) return 0;
-    return tok_plan(B, type, nh, nkv, hd, max_rows, max_len, window, sinks).bytes;
+    const AttnPlan p = attn_plan(B, type, nh, nkv, hd, max_rows, max_len, window, sinks);
+    return p.tok_bytes + (p.rows ? kv_paged_rows_workspace_bytes(B, M, type, nh, nkv, hd, max_rows, max_len, window, sinks) : 0);
 }
 
 cudaError_t launch_kv_paged_attn(const KvPagedAttnArgs &a, int type, int hd, bool pdl, cudaStream_t s) {
-    if (type == QW3_F32) return hd == 128 ? attn_t<float, 128>(a, type, pdl, s) : attn_t<float, 64>(a, type, pdl, s);
-    return hd == 128 ? attn_t<__half, 128>(a, type, pdl, s) : attn_t<__half, 64>(a, type, pdl, s);
+    const AttnPlan p = attn_plan(a.b.B, type, a.nh, a.c.nkv, hd, a.b.max_rows, a.b.max_len, a.window, a.sinks);
+    cudaError_t e = cudaSuccess;
+    if (p.rows)
+        e = launch_kv_paged_rows(a, type, hd, p.tokens ? kTokCols : 0,
+                                 reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + p.tok_bytes), pdl, s);
+    if (e != cudaSuccess || !p.tokens) return e;
+    if (type == QW3_F32) return hd == 128 ? tokens_t<float, 128>(a, p.tok, pdl, s) : tokens_t<float, 64>(a, p.tok, pdl, s);
+    return hd == 128 ? tokens_t<__half, 128>(a, p.tok, pdl, s) : tokens_t<__half, 64>(a, p.tok, pdl, s);
 }
 
 }  // namespace qw3
