@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
         s_found = 0;
     }
     __syncthreads();
+    pdl_trigger();
     pdl_wait();
 
     // ---- the unit: number `pair` of the sequences' units, a sequence's last (longest) one first
@@ -736,6 +737,7 @@ __global__ void __launch_bounds__(128) k_paged_rows_join(const RwArgs r) {
     using Z = RwSizes<T, HD>;
     constexpr int E = HD / 32;
     const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5), unit = blockIdx.x;
+    pdl_trigger();
     pdl_wait();
     const RwCut cut = reinterpret_cast<const RwCut *>(r.ws)[unit];
     const int rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(128) k_paged_append(const KvPagedAppendArgs a,
     constexpr int V = PgVec<T>::V, L = HD / V, H = 32 / L;
     const int lane = threadIdx.x & 31;
     const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    pdl_trigger();
     pdl_wait();
     if (unit < units) {
         const int row = static_cast<int>(unit / per_row), pass0 = static_cast<int>(unit % per_row) * NP;
@@ -173,7 +174,6 @@ __global__ void __launch_bounds__(128) k_paged_append(const KvPagedAppendArgs a,
             if (bad) record_status(a.status, QW3_ERR_NONFINITE);
         }
     }
-    pdl_trigger();
 }
 
 template <typename T, int HD>
@@ -210,6 +210,11 @@ cudaError_t append_t(const KvPagedAppendArgs &a, bool pdl, cudaStream_t s) {
 // and reading K and V is what takes the time, not the products.
 
 constexpr int kTokWarps = 8, kTokStages = 3, kTokKeys = 16;
+// What a unit's ends cost, in steps (loading its queries, joining the warps),
+// where there are more units than CTAs: 64 sequences of 1 to 4101 take 127 us
+// with 0, 104 with 10, 93.6 with 24, 95.2 with 40. Fewer units: a CTA has two at
+// most, and shares may be short.
+constexpr int kTokUnit = 24;
 constexpr int kTokCols = 32;      // columns of a sequence's kv head that these kernels take
 
 template <typename T, int HD>
@@ -272,8 +277,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The shares are of work: a unit's is `ends` (kTokUnit or 0) and then its steps.
 // Where a CTA (or a warp's loads, ahead of it) is: unit `u` of sequence i, its
-// steps k .. end - 1 among them, and `left` steps of the share behind those.
+// steps k .. end - 1 among them, and `left` of the share behind those.
 struct TokAt {
     TokSeq s;
     int i, u, units, k, end;
@@ -285,7 +291,7 @@ __device__ __forceinline__ int tok_units(const TokSeq &s, int nkv) { return (s.c
 
 // The next unit of which the share has a step; i = -1 behind the last one.
 template <int W>
-__device__ __forceinline__ void tok_next(TokAt &t, const KvPagedAttnArgs &a, int G) {
+__device__ __forceinline__ void tok_next(TokAt &t, const KvPagedAttnArgs &a, int G, int ends) {
     while (t.left > 0) {
         if (++t.u >= t.units) {
             t.u = -1;
@@ -294,6 +300,8 @@ __device__ __forceinline__ void tok_next(TokAt &t, const KvPagedAttnArgs &a, int
             t.units = tok_units<W>(t.s, a.c.nkv);
             continue;
         }
+        t.left -= ends;
+        if (t.left <= 0) break;   // (its steps begin in the next share)
         t.k = 0;
         t.end = static_cast<int>(min(static_cast<long long>(t.s.steps), t.left));
         t.left -= t.end;
@@ -312,7 +320,7 @@ struct TokCut {
 };
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPagedAttnArgs a, int G, int max_cb, int min_share) {
+__global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPagedAttnArgs a, int G, int max_cb, int ends, int min_share) {
     using Z = TokSizes<T, HD>;
     constexpr int W = Z::W, KS = HD / 16, NT = HD / 8, CH = HD / 8;
     constexpr float kOff = 12.0f, kLazy = 3.0f;   // a weight is 2^(s - ref + 12), at most 2^15
@@ -322,15 +330,16 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     __shared__ float s_m[kTokWarps][8], s_l[kTokWarps][8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
     const int nkv = a.c.nkv;
+    pdl_trigger();
     pdl_wait();
 
-    // ---- the share of this CTA: steps x0 .. x1 - 1 of all
+    // ---- the share of this CTA: x0 .. x1 - 1 of all the work
     const int per = (a.b.B + kTokWarps * 32 - 1) / (kTokWarps * 32);
     const int i0 = min(a.b.B, tid * per), i1 = min(a.b.B, i0 + per);
     long long mine = 0;
     for (int i = i0; i < i1; ++i) {
         const TokSeq s = tok_seq(a, i, G);
-        mine += static_cast<long long>(tok_units<W>(s, nkv)) * s.steps;
+        mine += static_cast<long long>(tok_units<W>(s, nkv)) * (ends + s.steps);
     }
     long long upto = mine;
 #pragma unroll
@@ -351,11 +360,12 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
         long long at = before;
         for (int i = i0; i < i1; ++i) {
             const TokSeq s = tok_seq(a, i, G);
-            const long long n = static_cast<long long>(tok_units<W>(s, nkv)) * s.steps;
+            const int unit = ends + s.steps;
+            const long long n = static_cast<long long>(tok_units<W>(s, nkv)) * unit;
             if (x0 < at + n) {
                 s_i = i;
-                s_off_u = static_cast<int>((x0 - at) / s.steps);
-                s_off_k = static_cast<int>((x0 - at) % s.steps);
+                s_off_u = static_cast<int>((x0 - at) / unit);
+                s_off_k = static_cast<int>((x0 - at) % unit) - ends;
                 break;
             }
             at += n;
@@ -369,9 +379,11 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     t.s = tok_seq(a, t.i, G);
     t.units = tok_units<W>(t.s, nkv);
     t.u = s_off_u;
-    t.k = s_off_k;
-    t.end = static_cast<int>(min(static_cast<long long>(t.s.steps), t.k + (x1 - x0)));
-    t.left = x1 - x0 - (t.end - t.k);
+    t.k = max(0, s_off_k);
+    long long x = x0 + max(0, -s_off_k);   // where this piece's steps begin
+    if (x >= x1) return;                   // (only at the end of all the work: min_share > ends)
+    t.end = static_cast<int>(min(static_cast<long long>(t.s.steps), t.k + (x1 - x)));
+    t.left = x1 - x - (t.end - t.k);
 
     // ---- this warp's loads: the next step to fetch, its page known one step ahead
     const uint32_t ring = smem_u32(tok_smem) + warp * Z::ring;
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     uint32_t paged = 0;   // bit per stage: its step has a page
     auto settle = [&]() {   // fk to a step of the share, if there is one
         while (f.i >= 0 && fk >= f.end) {
-            tok_next<W>(f, a, G);
+            tok_next<W>(f, a, G, ends);
             fk = f.k + warp;
         }
         fpage = f.i >= 0 ? kv_page(a.b, a.c, f.i, f.s.key_step(fk) * kTokKeys) : -1;
@@ -412,7 +424,6 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     const float scale2 = a.scale * 1.4426950408889634f;   // softmax in base 2
     float *slots = static_cast<float *>(a.ws);
     TokCut *cuts = reinterpret_cast<TokCut *>(slots + static_cast<size_t>(gridDim.x) * 2 * W * Z::part);
-    long long x = x0;   // the first step of this piece
     for (int piece = 0; t.i >= 0; ++piece) {
         const int blocks = (t.s.cols + W - 1) / W, g = t.u / blocks, cb = t.u % blocks, col0 = cb * W;
         const int pmin = t.s.p0 + col0 / G, pmax = t.s.p0 + (min(t.s.cols, col0 + W) - 1) / G;
@@ -672,18 +683,21 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
             }
             __syncthreads();
         }
-        x += t.end - t.k;
-        tok_next<W>(t, a, G);
+        x += t.end - t.k + ends;
+        tok_next<W>(t, a, G, ends);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// One block to a column of a unit that was cut.
+// One block to a column of a unit that was cut: HD threads four times over, each
+// quarter a fourth of the parts.
 template <typename T, int HD>
-__global__ void __launch_bounds__(HD) k_paged_tokens_join(const KvPagedAttnArgs a, int G, int max_cb, int grid) {
+__global__ void __launch_bounds__(4 * HD) k_paged_tokens_join(const KvPagedAttnArgs a, int G, int max_cb, int grid) {
     using Z = TokSizes<T, HD>;
     constexpr int W = Z::W;
-    const int col = blockIdx.x, g = blockIdx.y, d = threadIdx.x;
+    __shared__ float s_m[4 * HD], s_l[4 * HD], s_v[3][HD];
+    const int col = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, d = tid % HD, quarter = tid / HD;
+    pdl_trigger();
     pdl_wait();
     for (int b = blockIdx.z; b < a.b.B; b += gridDim.z) {
         const TokSeq s = tok_seq(a, b, G);
@@ -692,30 +706,38 @@ __global__ void __launch_bounds__(HD) k_paged_tokens_join(const KvPagedAttnArgs 
         const TokCut *cuts = reinterpret_cast<const TokCut *>(slots + static_cast<size_t>(grid) * 2 * W * Z::part);
         const TokCut cut = cuts[(static_cast<size_t>(b) * a.c.nkv + g) * max_cb + col / W];
         if (cut.first < 0) continue;
-        const int last = static_cast<int>(cut.last & 0x7fffffffu), n = last - cut.first + 1;
-        float m = -INFINITY, l = 0.0f, v = 0.0f;
-#pragma unroll 4
-        for (int c = 0; c < n; ++c) {
+        const int last = static_cast<int>(cut.last & 0x7fffffffu), n = last - cut.first + 1;   // at most the grid: 4 HD and fewer
+        auto part = [&](int c) {
             const int slot = c == 0 && !(cut.last & 0x80000000u) ? 1 : 0;
-            const float *q = slots + ((static_cast<size_t>(cut.first + c) * 2 + slot) * W + col % W) * Z::part;
-            const float mc = q[HD], lc = q[HD + 1], vc = q[d], top = fmaxf(m, mc);
-            const float f0 = m == top ? 1.0f : ex2(m - top), f1 = mc == top ? 1.0f : ex2(mc - top);
-            l = l * f0 + lc * f1;
-            v = v * f0 + vc * f1;
-            m = top;
+            return slots + ((static_cast<size_t>(cut.first + c) * 2 + slot) * W + col % W) * Z::part;
+        };
+        if (tid < n) {
+            s_m[tid] = part(tid)[HD];
+            s_l[tid] = part(tid)[HD + 1];
         }
-        T *to = static_cast<T *>(a.out) + (s.start + col / G) * a.out_stride + static_cast<size_t>(g * G + col % G) * HD + d;
-        *to = kv_cvt<T>(l == 0.0f ? 0.0f : v / l);
+        __syncthreads();
+        float m = -INFINITY, l = 0.0f, v = 0.0f;
+        for (int c = 0; c < n; ++c) m = fmaxf(m, s_m[c]);
+#pragma unroll 8
+        for (int c = quarter; c < n; c += 4) v = fmaf(part(c)[d], s_m[c] == m ? 1.0f : ex2(s_m[c] - m), v);
+        if (quarter > 0) s_v[quarter - 1][d] = v;
+        for (int c = 0; c < n; ++c) l = fmaf(s_l[c], s_m[c] == m ? 1.0f : ex2(s_m[c] - m), l);
+        __syncthreads();
+        if (quarter == 0) {
+            v = (v + s_v[0][d]) + (s_v[1][d] + s_v[2][d]);
+            T *to = static_cast<T *>(a.out) + (s.start + col / G) * a.out_stride + static_cast<size_t>(g * G + col % G) * HD + d;
+            *to = kv_cvt<T>(l == 0.0f ? 0.0f : v / l);
+        }
+        __syncthreads();
     }
 }
 
 // How the token kernels are launched: the columns that a sequence can have, the
 // blocks of them, the CTAs.
 struct TokPlan {
-    int cols = 0, max_cb = 0, grid = 0;
+    int cols = 0, max_cb = 0, grid = 0, ends = 0, min_share = 0;
     size_t bytes = 0;
 };
-constexpr int kTokMinShare = kTokWarps;   // a step to a warp: fewer would only be more to join
 TokPlan tok_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
     TokPlan p;
     const int G = nh / nkv, W = type == QW3_F32 ? 8 : 16;
@@ -723,8 +745,11 @@ TokPlan tok_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int max
     p.max_cb = (p.cols + W - 1) / W;
     long long len = max_len;
     if (window > 0) len = std::min<long long>(len, static_cast<long long>(window) + max_rows + sinks + 3 * kTokKeys);
-    const long long steps = std::max<long long>(1, (len + kTokKeys - 1) / kTokKeys) * B * nkv * p.max_cb;
-    p.grid = static_cast<int>(std::max<long long>(1, std::min<long long>(num_sms(), (steps + kTokMinShare - 1) / kTokMinShare)));
+    const long long units = static_cast<long long>(B) * nkv * p.max_cb;
+    p.ends = units > num_sms() ? kTokUnit : 0;
+    p.min_share = p.ends + kTokWarps;   // a step to a warp: fewer would only be more to join
+    const long long work = (p.ends + std::max<long long>(1, (len + kTokKeys - 1) / kTokKeys)) * units;
+    p.grid = static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(num_sms(), 256), (work + p.min_share - 1) / p.min_share)));
     p.bytes = static_cast<size_t>(p.grid) * 2 * W * (hd + 4) * 4 + static_cast<size_t>(B) * nkv * p.max_cb * sizeof(TokCut);
     return p;
 }
@@ -733,10 +758,10 @@ template <typename T, int HD>
 cudaError_t tokens_t(const KvPagedAttnArgs &a, const TokPlan &p, bool pdl, cudaStream_t s) {
     using Z = TokSizes<T, HD>;
     const int G = a.nh / a.c.nkv;
-    cudaError_t e = launch_pdl(pdl, k_paged_tokens<T, HD>, dim3(p.grid), kTokWarps * 32, Z::smem, 1, s, a, G, p.max_cb, kTokMinShare);
+    cudaError_t e = launch_pdl(pdl, k_paged_tokens<T, HD>, dim3(p.grid), kTokWarps * 32, Z::smem, 1, s, a, G, p.max_cb, p.ends, p.min_share);
     if (e != cudaSuccess || p.grid == 1) return e;
     const dim3 grid(p.cols, a.c.nkv, std::min(a.b.B, 65535));
-    return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, HD, 0, 1, s, a, G, p.max_cb, p.grid);
+    return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, 4 * HD, 0, 1, s, a, G, p.max_cb, p.grid);
 }
 
 template <typename T, int HD>

@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobArgs a, in
     const int rank = blockIdx.x % C;
     const bool one = C == 1;
     if (!one) cluster_arrive_release();   // (completed below: peers' shared memory is there)
+    pdl_trigger();
     pdl_wait();
     const float *x = a.logits + row * a.stride;
     const int head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) / 4 & 3));

@@ -713,19 +713,27 @@ class KVCachePaged:
         self.c = Qw3KvPaged(data.data_ptr(), *sizes)
 
     def _batch(self, torch, starts, lens, table):
-        _on(self.index, torch.int32, "starts and lens", starts, lens)
+        # (written out: every call of a tensor's methods costs a short call some 0.2 of its 15 us)
+        i32, index = torch.int32, self.index
+        if (starts.dtype is not i32 or lens.dtype is not i32 or table.dtype is not i32 or starts.get_device() != index
+                or lens.get_device() != index or table.get_device() != index or not starts.is_contiguous()
+                or not lens.is_contiguous()):
+            raise Qw3Error(QW3_ERR_INVALID_ARG, f"starts, lens, table: int32 tensors on cuda:{index}, starts and lens "
+                                                "contiguous, are wanted")
         B = lens.numel()
-        if starts.numel() != B + 1 or table.dim() != 2 or table.shape[0] != B:
+        if starts.numel() != B + 1 or table.dim() != 2:
             raise Qw3Error(QW3_ERR_SHAPE, "starts holds a border more than there are sequences, table a row for each")
-        _, width, stride = _rows_of(table, "table")
-        if table.dtype is not torch.int32 or table.get_device() != self.index:
-            raise Qw3Error(QW3_ERR_INVALID_ARG, f"table: an int32 tensor on cuda:{self.index} is wanted")
-        return Qw3KvBatch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), stride, B, width)
+        rows, width = table.shape
+        stride, step = table.stride()
+        if rows != B or (width > 1 and step != 1) or width > _INT32_MAX or B > _INT32_MAX:
+            raise Qw3Error(QW3_ERR_SHAPE, "table: a row of pages, contiguous, for each sequence is wanted")
+        return Qw3KvBatch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), stride if B > 1 else width, B, width)
 
     def _type(self, torch, t, name):
-        if t.get_device() != self.index or (t.dtype is not torch.float32 and t.dtype is not torch.float16):
+        kind = QW3_F32 if t.dtype is torch.float32 else QW3_F16 if t.dtype is torch.float16 else -1
+        if kind < 0 or t.get_device() != self.index:
             raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: an f32 or f16 tensor on cuda:{self.index} is wanted")
-        return QW3_F32 if t.dtype is torch.float32 else QW3_F16
+        return kind
 
     def append(self, qkv, starts, lens, table, rope, q_norm=None, k_norm=None, eps: float = 1e-6, out=None, status=None):
         """Norm (where q_norm, k_norm: f32 [head_dim] are given), rotate and
@@ -745,18 +753,21 @@ class KVCachePaged:
         if width % hd or n_heads < 1:
             raise Qw3Error(QW3_ERR_SHAPE, "qkv: rows of n_heads + 2 n_kv_heads heads are wanted")
         _on(self.index, torch.float32, "q_norm, k_norm and rope", q_norm, k_norm, rope)
-        if any(w is not None and w.numel() != hd for w in (q_norm, k_norm)) or rope.dim() != 3 or rope.shape[1:] != (hd // 2, 2):
+        positions, half, two = rope.shape if rope.dim() == 3 else (0, 0, 0)
+        if (half * 2 != hd or two != 2 or (q_norm is not None and q_norm.numel() != hd)
+                or (k_norm is not None and k_norm.numel() != hd)):
             raise Qw3Error(QW3_ERR_SHAPE, "q_norm and k_norm hold head_dim values, rope [positions, head_dim / 2, 2]")
-        _on(self.index, torch.int32, "status", status)
+        if status is not None:
+            _on(self.index, torch.int32, "status", status)
         batch = self._batch(torch, starts, lens, table)
         if out is None:
-            out = torch.empty((M, n_heads, hd), dtype=qkv.dtype, device=self.device)
+            out = qkv.new_empty((M, n_heads, hd))
         else:
             _on(self.index, qkv.dtype, "out", out)
             if out.numel() != M * n_heads * hd:
                 raise Qw3Error(QW3_ERR_SHAPE, f"out: [{M}, {n_heads}, {hd}] is wanted")
         rc = lib().qw3_kv_paged_append(self.c, batch, kind, qkv.data_ptr(), M, stride, n_heads, _ptr(q_norm), _ptr(k_norm),
-                                       eps, rope.data_ptr(), min(rope.shape[0], _INT32_MAX), out.data_ptr(), n_heads * hd,
+                                       eps, rope.data_ptr(), min(positions, _INT32_MAX), out.data_ptr(), n_heads * hd,
                                        _ptr(status), _stream_on(torch, self.index))
         if rc:
             _check(rc)
@@ -778,13 +789,17 @@ class KVCachePaged:
             with torch.cuda.device(self.index):
                 return self.attention(q, starts, lens, table, max_rows, max_len, window, sinks, scale, out, workspace, status)
         kind = self._type(torch, q, "q")
-        if q.dim() != 3 or q.shape[2] != self.head_dim or q.shape[0] > _INT32_MAX or q.shape[1] < 1:
+        M, n_heads, hd = q.shape if q.dim() == 3 else (0, 0, 0)
+        if hd != self.head_dim or n_heads < 1 or M > _INT32_MAX:
             raise Qw3Error(QW3_ERR_SHAPE, f"q: [M, n_heads, {self.head_dim}] is wanted")
-        M, n_heads, hd = q.shape
-        _on(self.index, q.dtype, "q and out", q, out)
-        _on(self.index, torch.int32, "status", status)
-        if out is not None and out.shape != q.shape:
-            raise Qw3Error(QW3_ERR_SHAPE, "out has q's shape")
+        if not q.is_contiguous():
+            raise Qw3Error(QW3_ERR_INVALID_ARG, "q: a contiguous tensor is wanted")
+        if status is not None:
+            _on(self.index, torch.int32, "status", status)
+        if out is not None:
+            _on(self.index, q.dtype, "out", out)
+            if out.shape != q.shape:
+                raise Qw3Error(QW3_ERR_SHAPE, "out has q's shape")
         batch = self._batch(torch, starts, lens, table)
         max_rows = M if max_rows is None else min(max_rows, M)
         max_len = batch.pages_per_seq * self.page_size if max_len is None else max_len
