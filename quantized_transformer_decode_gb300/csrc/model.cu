@@ -83,7 +83,6 @@ cudaError_t configure_all() {
         if (e == cudaSuccess) e = configure_sample();
         if (e == cudaSuccess) e = configure_kv_q4();
         if (e == cudaSuccess) e = configure_kv_paged();
-        if (e == cudaSuccess) e = configure_logprobs();
         g_cfg_err[dev] = e;
         g_cfg_done[dev].store(true, std::memory_order_release);
     }
@@ -1708,7 +1707,6 @@ int qw3_logprobs(const float *logits_dev, int64_t stride, int32_t B, int32_t V, 
     if (B == 0) return QW3_OK;
     LogprobArgs a{logits_dev, stride, V, tokens_dev, T, top, logprob_dev, entropy_dev, top_id_dev, top_logprob_dev,
                   status_dev};
-    QW3_CUDA_TRY(configure_all());   // the kernel's cluster size
     QW3_CUDA_TRY(launch_logprobs(a, B, true, static_cast<cudaStream_t>(stream)));
     return QW3_OK;
 }

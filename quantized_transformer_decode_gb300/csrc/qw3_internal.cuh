@@ -422,7 +422,6 @@ struct LogprobArgs {
     float *top_lp;
     int32_t *status;
 };
-cudaError_t configure_logprobs();
 cudaError_t launch_logprobs(const LogprobArgs &a, int B, bool pdl, cudaStream_t s);
 
 }  // namespace qw3
