@@ -497,12 +497,18 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
         }
         const bool active = QT == 1 || s < row_tiles;
         int own = 0;   // tiles taken
-        for (int i = Z::split ? s : 0; active && i < NT; i += Z::split ? 2 : 1, ++own) {
+        constexpr int kStep = Z::split ? 2 : 1;
+        // which 16 positions of a tile have a page (lanes 0..7 look, a tile ahead)
+        auto look = [&](int i) {
+            const int j = tiles.key(i0 + i) + 16 * (lane & 7);
+            return j > pmax || kv_page(a.b, a.c, u.seq, j) >= 0;
+        };
+        bool there = active && NT > (Z::split ? s : 0) && look(Z::split ? s : 0);
+        for (int i = Z::split ? s : 0; active && i < NT; i += kStep, ++own) {
             const int j0 = tiles.key(i0 + i);
-            // which 16 positions have a page (lanes 0..7 look)
-            const int jl = j0 + 16 * (lane & 7);
-            const uint32_t pages = __ballot_sync(0xffffffffu, jl > pmax || kv_page(a.b, a.c, u.seq, jl) >= 0) & 0xffu;
+            const uint32_t pages = __ballot_sync(0xffffffffu, there) & 0xffu;
             const bool holes = pages != 0xffu;
+            if (i + kStep < NT) there = look(i + kStep);
             // does every row of the tile see every position?
             const bool open = !holes && j0 + kRwKeys - 1 <= smin && (a.window == 0 || smax - j0 < a.window || j0 + kRwKeys <= a.sinks);
             if (!open) {
@@ -535,9 +541,13 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             }
             wait(&b_s[s], own);
             rw_after();
-            // the row's positions j0 + k, k in [k_lo, k_hi) or [0, k_sink), of pages that are there
+            // the row's positions j0 + k, k in [k_lo, k_hi) or [0, k_sink), of pages that are there: bits of 32 positions
             const int k_hi = p - j0 + 1, k_lo = a.window > 0 ? p - a.window + 1 - j0 : 0, k_sink = a.window > 0 ? a.sinks - j0 : 0;
-            auto sees = [&](int k) { return k < k_hi && (k >= k_lo || k < k_sink) && (pages >> (k >> 4) & 1); };
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
+            auto sees = [&](int k0) {
+                const uint32_t held = (pages >> (k0 >> 4) & 1 ? 0xffffu : 0u) | (pages >> ((k0 >> 4) + 1) & 1 ? 0xffff0000u : 0u);
+                return held & below(k_hi - k0) & (~below(k_lo - k0) | below(k_sink - k0));
+            };
             if constexpr (!Z::split) {
                 uint32_t v[128];
 #pragma unroll
@@ -545,12 +555,18 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                 rw_wait_ld();
                 if (!open) {
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (!sees(k)) v[k] = 0xff800000u;
-                }
-                float mx = -INFINITY;
+                    for (int k0 = 0; k0 < 128; k0 += 32) {
+                        const uint32_t bits = sees(k0);
 #pragma unroll
-                for (int k = 0; k < 128; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+                        for (int k = 0; k < 32; ++k) v[k0 + k] = bits >> k & 1 ? v[k0 + k] : 0xff800000u;
+                    }
+                }
+                float mx8[8];   // (chains of their own)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(v[k]);
+#pragma unroll
+                for (int k = 8; k < 128; ++k) mx8[k & 7] = fmaxf(mx8[k & 7], __uint_as_float(v[k]));
+                const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])), fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
                 const bool far = m == -INFINITY ? mx > -INFINITY : (mx - m) * c > kRwLazy;
                 if (__any_sync(0xffffffffu, far)) {
                     const float mn = far ? mx : m, f = m == mn ? 1.0f : m == -INFINITY ? 0.0f : rw_ex2((m - mn) * c);
@@ -581,16 +597,27 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                 rw_st32(tS, v);
                 rw_st32(tS + 32, v + 32);
             } else {
-                float mx = -INFINITY;
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k0 = 0; k0 < 128; k0 += 32) {
-                    uint32_t v[32];
+                for (int k0 = 0; k0 < 128; k0 += 64) {
+                    uint32_t v[64];
                     rw_ld32(tS + k0, v);
+                    rw_ld32(tS + k0 + 32, v + 32);
                     rw_wait_ld();
+                    if (!open) {   // what the row does not see is -inf from here on
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (open || sees(k0 + k)) mx = fmaxf(mx, __uint_as_float(v[k]));
+                        for (int h = 0; h < 64; h += 32) {
+                            const uint32_t bits = sees(k0 + h);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[h + k] = bits >> k & 1 ? v[h + k] : 0xff800000u;
+                            rw_st32(tS + k0 + h, v + h);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[k]));
                 }
+                if (!open) rw_wait_st();
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 const float mn = fmaxf(m, mx), f = m == mn ? 1.0f : rw_ex2((m - mn) * c);
                 // the O of this warpgroup's last tile, beside the old reference
                 if (own > 0) {
@@ -614,11 +641,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                     rw_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
-                        if (!open) {
-                            x = sees(k0 + k) ? x : 0.0f;
-                            y = sees(k0 + k + 1) ? y : 0.0f;
-                        }
+                        const float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
                         sum[0] += x;
                         sum[1] += y;
                         const uint32_t hi = rw_pack(x, y);
