@@ -113,12 +113,21 @@ __device__ __forceinline__ void rw_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool rw_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Shared-memory operand with a 128-byte swizzle: K-major (rows of 128 bytes, 8-row
 // groups 1024 bytes apart) or MN-major (8-row groups along K 1024 bytes apart, 64
-// columns of N `lbo` bytes apart).
-__device__ __forceinline__ uint64_t rw_desc(uint32_t at, uint32_t lbo) {
-    return static_cast<uint64_t>((at & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// columns of N `lbo` bytes apart). at16: the address in 16-byte words.
+__device__ __forceinline__ uint64_t rw_desc(uint32_t at16, uint32_t lbo) {
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(at16 | (lbo >> 4) << 16), "r"(hi));
+    return d;
 }
 // kind::f16, f16 operands, f32 sums; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t rw_idesc(int N, bool b_mn) {
@@ -135,6 +144,16 @@ __device__ __forceinline__ void rw_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 __device__ __forceinline__ void rw_tma(uint32_t to, const CUtensorMap *map, int x, int y, uint64_t *bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+// A bounded wait that gives up with the others: *err is set by the first that ran
+// out, and looked at by those that have to wait.
+__device__ __forceinline__ void rw_wait(uint64_t *bar, int parity, volatile int *err) {
+    if (mbar_try_wait(bar, static_cast<uint32_t>(parity & 1))) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, static_cast<uint32_t>(parity & 1))) {
+        if (*err) return;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) *err = 1;
+    }
 }
 __device__ __forceinline__ void rw_bar(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 
@@ -226,7 +245,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     __shared__ RwUnit s_unit;
     __shared__ float s_c[kRwRows], s_ml[2][kRwRows];
     const KvPagedAttnArgs &a = r.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the warp's own: uniform branches)
     const uint32_t base = (smem_u32(rw_smem) + 1023) & ~1023u;
     uint8_t *const smem = rw_smem + (base - smem_u32(rw_smem));
     const int g = blockIdx.x % a.c.nkv, pair = blockIdx.x / a.c.nkv;
@@ -369,9 +389,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     };
     auto fill_of_k = [&](int i) { return Z::split ? max(0, 2 * i - 1) : 2 * i; };
     auto fill_of_v = [&](int i) { return Z::split ? min(2 * i + 2, 2 * NT - 1) : 2 * i + 1; };
-    auto wait = [&](uint64_t *bar, int parity) {
-        if (*err || !mbar_wait_bounded(bar, static_cast<uint32_t>(parity & 1))) *err = 1;
-    };
+    auto wait = [&](uint64_t *bar, int parity) { rw_wait(bar, parity, err); };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -380,15 +398,17 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             const int shift = min(a.c.shift, 7), boxes = kRwKeys >> shift;
             const uint32_t bytes = static_cast<uint32_t>(HD * 2) << shift;
             int n = 0;
-            for (; n < 2 * NT && !*err; ++n) {
+            for (; n < 2 * NT; ++n) {
                 int i;
                 bool v;
                 fill(n, i, v);
                 const int j = tiles.key(i0 + i) + (lane << shift);
                 const int page = lane < boxes && j <= pmax ? kv_page(a.b, a.c, u.seq, j) : -1;
                 const int st = n % ST;
-                if (n >= ST) wait(&b_empty[st], n / ST - 1);
-                if (__any_sync(0xffffffffu, *err != 0)) break;
+                if (n >= ST) {
+                    wait(&b_empty[st], n / ST - 1);
+                    if (__any_sync(0xffffffffu, *err != 0)) break;
+                }
                 const int held = __popc(__ballot_sync(0xffffffffu, page >= 0));
                 if (lane == 0) mbar_arrive_expect_tx(&b_full[st], held * bytes);
                 __syncwarp();
@@ -404,73 +424,73 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                 if (*err) (void)mbar_wait_bounded(&b_full[k % ST], static_cast<uint32_t>(k / ST & 1));
                 else wait(&b_empty[k % ST], k / ST);
             }
-        } else if (warp == 9 && lane == 0 && NT > 0) {
-            // ---- products
+        } else if (warp == 9 && NT > 0) {
+            // ---- products: the whole warp walks along, one lane issues
+            const uint32_t ring16 = (ring & 0x3FFFFu) >> 4, base16 = (base & 0x3FFFFu) >> 4;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const bool one = rw_elect();
             auto qk = [&](int s, int i) {
                 const int n = fill_of_k(i), st = n % ST;
                 wait(&b_full[st], n / ST);
-                if (*err) return;
                 rw_after();
-                const uint32_t k = ring + st * Z::tile, q = base + (QT == 2 ? s * Z::tile : 0);
+                const uint32_t k = ring16 + st * (Z::tile >> 4), q = base16 + (QT == 2 ? s * (Z::tile >> 4) : 0);
+                if (one) {
 #pragma unroll
-                for (int part_ = 0; part_ < (Z::split ? 2 : 1); ++part_)
+                    for (int h = 0; h < (Z::split ? 2 : 1); ++h)
 #pragma unroll
-                    for (int e = 0; e < HD / 16; ++e) {
-                        const uint32_t at = (e >> 2) * (kRwRows * 128) + (e & 3) * 32;
-                        rw_mma_ss(tmem + s * 128, rw_desc(q + part_ * Z::tile + at, 16), rw_desc(k + at, 16), rw_idesc(kRwKeys, false),
-                                  part_ + e > 0);
-                    }
+                        for (int e = 0; e < HD / 16; ++e) {
+                            const uint32_t at = (e >> 2) * (kRwRows * 128 >> 4) + (e & 3) * 2;
+                            rw_mma_ss(tm + s * 128, rw_desc(q + h * (Z::tile >> 4) + at, 16), rw_desc(k + at, 16),
+                                      rw_idesc(kRwKeys, false), h + e > 0);
+                        }
+                    rw_commit(&b_s[s]);
+                }
             };
             auto pv = [&](int s, int i, bool add) {
                 const int n = fill_of_v(i), st = n % ST;
                 wait(&b_full[st], n / ST);
                 wait(&b_p[s], Z::split ? i >> 1 : i);
-                if (*err) return;
                 rw_after();
-                const uint32_t v = ring + st * Z::tile, p = tmem + s * 128;
+                const uint32_t v = ring16 + st * (Z::tile >> 4), p = tm + s * 128;
+                if (one) {
 #pragma unroll
-                for (int e = 0; e < kRwKeys / 16; ++e) {
-                    const uint64_t d = rw_desc(v + e * 2048, kRwKeys * 128);
-                    // P: f16 [64 columns]; f32: hi and lo of 32 keys next to each other, 16 columns each
-                    const uint32_t at = p + (Z::split ? (e >> 1) * 32 + (e & 1) * 8 : e * 8);
-                    rw_mma_ts(tmem + 256 + s * HD, at, d, rw_idesc(HD, true), add || e > 0);
-                    if constexpr (Z::split) rw_mma_ts(tmem + 256 + s * HD, at + 16, d, rw_idesc(HD, true), true);
+                    for (int e = 0; e < kRwKeys / 16; ++e) {
+                        const uint64_t d = rw_desc(v + e * (2048 >> 4), kRwKeys * 128);
+                        // P: f16 [64 columns]; f32: hi and lo of 32 keys next to each other, 16 columns each
+                        const uint32_t at = p + (Z::split ? (e >> 1) * 32 + (e & 1) * 8 : e * 8);
+                        rw_mma_ts(tm + 256 + s * HD, at, d, rw_idesc(HD, true), add || e > 0);
+                        if constexpr (Z::split) rw_mma_ts(tm + 256 + s * HD, at + 16, d, rw_idesc(HD, true), true);
+                    }
                 }
             };
+            auto done = [&](uint64_t *bar) {
+                if (one) rw_commit(bar);
+            };
             if constexpr (!Z::split) {
-                for (int s = 0; s < row_tiles; ++s) {
-                    qk(s, 0);
-                    rw_commit(&b_s[s]);
-                }
-                rw_commit(&b_empty[0]);
-                for (int i = 0; i < NT && !*err; ++i) {
+                for (int s = 0; s < row_tiles; ++s) qk(s, 0);
+                done(&b_empty[0]);
+                for (int i = 0; i < NT; ++i) {
                     for (int s = 0; s < row_tiles; ++s) {
                         pv(s, i, i > 0);
-                        if (i + 1 < NT) {
-                            qk(s, i + 1);
-                            rw_commit(&b_s[s]);
-                        } else {
-                            rw_commit(&b_o[s]);
-                        }
+                        if (i + 1 < NT) qk(s, i + 1);
+                        else done(&b_o[s]);
                     }
-                    rw_commit(&b_empty[fill_of_v(i) % ST]);
-                    if (i + 1 < NT) rw_commit(&b_empty[fill_of_k(i + 1) % ST]);
+                    done(&b_empty[fill_of_v(i) % ST]);
+                    if (i + 1 < NT) done(&b_empty[fill_of_k(i + 1) % ST]);
                 }
             } else {
                 for (int i = 0; i < min(2, NT); ++i) {
                     qk(i, i);
-                    rw_commit(&b_s[i]);
-                    rw_commit(&b_empty[fill_of_k(i) % ST]);
+                    done(&b_empty[fill_of_k(i) % ST]);
                 }
-                for (int i = 0; i < NT && !*err; ++i) {
+                for (int i = 0; i < NT; ++i) {
                     pv(i & 1, i, false);
-                    rw_commit(&b_empty[fill_of_v(i) % ST]);
+                    done(&b_empty[fill_of_v(i) % ST]);
                     if (i + 2 < NT) {
                         qk(i & 1, i + 2);
-                        rw_commit(&b_s[i & 1]);
-                        rw_commit(&b_empty[fill_of_k(i + 2) % ST]);
+                        done(&b_empty[fill_of_k(i + 2) % ST]);
                     } else {
-                        rw_commit(&b_o[i & 1]);
+                        done(&b_o[i & 1]);
                     }
                 }
             }
