@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     using Z = RwSizes<T, HD>;
     constexpr int ST = Z::stages, QT = Z::QT;
     extern __shared__ uint8_t rw_smem[];
-    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2], b_o[2];
+    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2], b_o[2], b_q;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err, s_bad, s_found, s_sum[kRwThreads / 32];
     __shared__ RwUnit s_unit;
@@ -261,12 +261,23 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             mbar_init(&b_p[i], 128);
             mbar_init(&b_o[i], 1);
         }
+        mbar_init(&b_q, 256);
         fence_mbar_init();
         s_err = 0;
         s_bad = 0;
         s_found = 0;
     }
+    if (warp == 9) {   // (nothing else holds tensor memory here: no two of these CTAs fit an SM)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        rw_before();
+    }
     __syncthreads();
+    rw_after();
+    const uint32_t tmem = s_tmem;
+    auto leave = [&]() {
+        if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    };
     pdl_trigger();
     pdl_wait();
 
@@ -306,6 +317,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     RwCut *const cuts = reinterpret_cast<RwCut *>(r.ws);
     if (!s_found) {
         if (blockIdx.y == 0 && tid == 0 && r.splits > 1) cuts[blockIdx.x] = RwCut{0, 0, 0, 0};
+        leave();
         return;
     }
     const RwUnit u = s_unit;
@@ -314,67 +326,18 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     const RwTiles tiles = rw_tiles(pmin, pmax, a.window, a.sinks);
     const int parts = max(1, (tiles.n + r.split_tiles - 1) / r.split_tiles), part = blockIdx.y;
     if (part == 0 && tid == 0 && r.splits > 1) cuts[blockIdx.x] = RwCut{u.start + u.tok0, tokens, parts, 0};
-    if (part >= parts) return;
+    if (part >= parts) {
+        leave();
+        return;
+    }
     const int i0 = part * r.split_tiles, i1 = min(tiles.n, i0 + r.split_tiles), NT = i1 - i0;
     float *const dst = parts == 1 ? nullptr
                                   : r.ws + static_cast<size_t>(r.units) * 4 +
                                         (static_cast<size_t>(blockIdx.x) * r.splits + part) * (QT * kRwRows) * Z::part;
     const int row_tiles = QT == 1 ? 1 : (tokens > r.TT ? 2 : 1);
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-
-    // ---- Q to shared memory. A negative scale goes into it, so that scores are scaled by c > 0
+    // a negative scale goes into Q, so that scores are scaled by c > 0
     const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
     const float c0 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
-    {
-        constexpr int L = HD / 8, RW = 32 / L;   // lanes to a row, rows to a warp
-        const int ch = lane % L;
-#pragma unroll 4
-        for (int row = warp * RW + lane / L; row < QT * kRwRows; row += kRwThreads / 32 * RW) {
-            const int rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;
-            const bool real = rr < r.TT * r.G && tok < tokens;
-            const T *q = static_cast<const T *>(a.q) + static_cast<size_t>(u.start + u.tok0 + (real ? tok : 0)) * a.q_stride +
-                         static_cast<size_t>(g * r.G + (real ? rr % r.G : 0)) * HD + ch * 8;
-            uint8_t *to = smem + (ch >> 3) * (kRwRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-            if constexpr (Z::split) {
-                float v[8];
-                const float4 x = *reinterpret_cast<const float4 *>(q), y = *reinterpret_cast<const float4 *>(q + 4);
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-                float amax = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
-                const unsigned group = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << (lane / L * L);
-#pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
-                // the power of two that takes the row's largest into [2^14, 2^15)
-                const int ex = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23 & 0xffu));
-                const float up = pow2_f32(ex) * sign;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = real ? v[e] * up : 0.0f;
-                uint4 hi, lo;
-                split8_f16(v, hi, lo);
-                *reinterpret_cast<uint4 *>(to) = hi;
-                *reinterpret_cast<uint4 *>(to + Z::tile) = lo;
-                if (ch == 0) s_c[rr] = pow2_f32(-ex) * c0;
-            } else {
-                uint4 x = real ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
-                if (sign != 1.0f) {
-                    const __half2 f = __float2half2_rn(sign);
-                    __half2 *h = reinterpret_cast<__half2 *>(&x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
-                }
-                *reinterpret_cast<uint4 *>(to + (row / kRwRows) * Z::tile) = x;
-            }
-        }
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    rw_before();
-    __syncthreads();
-    rw_after();
-    const uint32_t tmem = s_tmem;
     const uint32_t ring = base + 2 * Z::tile;
     volatile int *err = &s_err;
     // fill n of the ring: its key tile, and whether it is V
@@ -466,6 +429,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             auto done = [&](uint64_t *bar) {
                 if (one) rw_commit(bar);
             };
+            wait(&b_q, 0);
             if constexpr (!Z::split) {
                 for (int s = 0; s < row_tiles; ++s) qk(s, 0);
                 done(&b_empty[0]);
@@ -498,6 +462,59 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---- Q to shared memory: L lanes to a row, PW rows to a warp at once, all loads of NB passes before their stores
+        {
+            constexpr int L = HD / 8, PW = 32 / L, NB = Z::split ? 4 : 8;
+            const int ch = lane % L;
+#pragma unroll 1
+            for (int row0 = warp * PW + lane / L; row0 < QT * kRwRows; row0 += 8 * PW * NB) {
+                uint4 x[NB], y[Z::split ? NB : 1];
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int row = row0 + n * 8 * PW, rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;
+                    const bool real = rr < r.TT * r.G && tok < tokens;
+                    const T *q = static_cast<const T *>(a.q) + static_cast<size_t>(u.start + u.tok0 + (real ? tok : 0)) * a.q_stride +
+                                 static_cast<size_t>(g * r.G + (real ? rr % r.G : 0)) * HD + ch * 8;
+                    x[n] = real ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
+                    if constexpr (Z::split) y[n] = real ? *reinterpret_cast<const uint4 *>(q + 4) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int row = row0 + n * 8 * PW, rr = row % kRwRows;
+                    uint8_t *to = smem + (ch >> 3) * (kRwRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+                    if constexpr (Z::split) {
+                        float v[8] = {__uint_as_float(x[n].x), __uint_as_float(x[n].y), __uint_as_float(x[n].z), __uint_as_float(x[n].w),
+                                      __uint_as_float(y[n].x), __uint_as_float(y[n].y), __uint_as_float(y[n].z), __uint_as_float(y[n].w)};
+                        float amax = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+#pragma unroll
+                        for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        // the power of two that takes the row's largest into [2^14, 2^15)
+                        const int ex = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23 & 0xffu));
+                        const float up = pow2_f32(ex) * sign;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] *= up;
+                        uint4 hi, lo;
+                        split8_f16(v, hi, lo);
+                        *reinterpret_cast<uint4 *>(to) = hi;
+                        *reinterpret_cast<uint4 *>(to + Z::tile) = lo;
+                        if (ch == 0) s_c[rr] = pow2_f32(-ex) * c0;
+                    } else {
+                        if (sign != 1.0f) {
+                            const __half2 f = __float2half2_rn(sign);
+                            __half2 *h = reinterpret_cast<__half2 *>(&x[n]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
+                        }
+                        *reinterpret_cast<uint4 *>(to + (row / kRwRows) * Z::tile) = x[n];
+                    }
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(&b_q);
+            if constexpr (Z::split) rw_bar(1);   // (s_c)
+        }
         // ---- softmax: warpgroup s, a thread to a row
         const int s = warp >> 2, rr = tid & 127;
         const int tok = (QT == 2 ? s * r.TT : 0) + rr / r.G;
@@ -768,10 +785,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     }
     __syncthreads();
     if (tid == 0 && s_err) record_status(a.status, QW3_ERR_TIMEOUT);
-    if (warp == 0) {
-        rw_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    }
+    rw_after();
+    leave();
 }
 
 // A warp to a row of a unit that was split.
@@ -811,22 +826,26 @@ struct RwPlan {
     int TT = 0, units = 0, splits = 1, split_tiles = 0;
     size_t bytes = 0;
 };
-RwPlan rw_plan(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
+RwPlan rw_plan(int B, int M, int min_cols, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
     RwPlan p;
     const int G = nh / nkv, QT = type == QW3_F32 ? 1 : 2;
     p.TT = kRwRows / G;
     const int UT = p.TT * QT;
-    const long long pairs = std::min(static_cast<long long>(B) * ((max_rows + UT - 1) / UT), (M - std::min(B, M)) / UT + static_cast<long long>(std::min(B, M)));
+    // at most so many: each sequence has more than min_cols columns, and all of them M rows
+    const long long least = min_cols / G + 1, seqs = std::min<long long>(B, M / least);
+    const long long pairs = std::max<long long>(1, std::min(seqs * ((max_rows + UT - 1) / UT), (M - seqs) / UT + seqs));
     p.units = static_cast<int>(pairs * nkv);
+    // and likely so many: beside sequences of one row (min_cols: others' are there too) the rest is in few sequences
+    const long long likely = min_cols ? std::min(pairs, (M - std::min(B, M)) / UT + 1ll) * nkv : p.units;
     long long len = max_len;
     if (window > 0) len = std::min<long long>(len, static_cast<long long>(window) + UT + 2 * kRwKeys + sinks);
     const int tiles = static_cast<int>(std::max<long long>(1, (len + kRwKeys - 1) / kRwKeys));
     // the parts that take the fewest rounds of tiles, with three tiles' time for a part's ends and four for the join
     const int sms = num_sms();
     double best = 0.0;
-    for (int s = 1; s <= std::min(tiles, 32) && (s == 1 || static_cast<long long>(p.units) * s <= 4 * sms); ++s) {
+    for (int s = 1; s <= std::min(tiles, 32) && (s == 1 || static_cast<long long>(p.units) * s <= 6 * sms); ++s) {
         const int per = (tiles + s - 1) / s;
-        const double cost = static_cast<double>((static_cast<long long>(p.units) * s + sms - 1) / sms) * (per + 3) + (s > 1 ? 4 : 0);
+        const double cost = static_cast<double>((likely * s + sms - 1) / sms) * (per + 3) + (s > 1 ? 4 : 0);
         if (s == 1 || cost < best) {
             best = cost;
             p.splits = s;
@@ -888,12 +907,13 @@ cudaError_t configure_kv_paged_rows() {
     return e;
 }
 
-size_t kv_paged_rows_workspace_bytes(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
-    return rw_plan(B, M, type, nh, nkv, hd, max_rows, max_len, window, sinks).bytes;
+size_t kv_paged_rows_workspace_bytes(int B, int M, int min_cols, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window,
+                                     int sinks) {
+    return rw_plan(B, M, min_cols, type, nh, nkv, hd, max_rows, max_len, window, sinks).bytes;
 }
 
 cudaError_t launch_kv_paged_rows(const KvPagedAttnArgs &a, int type, int hd, int min_cols, float *ws, bool pdl, cudaStream_t s) {
-    const RwPlan p = rw_plan(a.b.B, a.b.M, type, a.nh, a.c.nkv, hd, a.b.max_rows, a.b.max_len, a.window, a.sinks);
+    const RwPlan p = rw_plan(a.b.B, a.b.M, min_cols, type, a.nh, a.c.nkv, hd, a.b.max_rows, a.b.max_len, a.window, a.sinks);
     if (type == QW3_F32) return hd == 128 ? rows_t<float, 128>(a, min_cols, p, ws, pdl, s) : rows_t<float, 64>(a, min_cols, p, ws, pdl, s);
     return hd == 128 ? rows_t<__half, 128>(a, min_cols, p, ws, pdl, s) : rows_t<__half, 64>(a, min_cols, p, ws, pdl, s);
 }

@@ -812,7 +812,7 @@ size_t kv_paged_attn_workspace_bytes(int B, int M, int type, int nh, int nkv, in
                                      int window, int sinks) {
     if (B == 0 || M == 0 || max_rows == 0) return 0;
     const AttnPlan p = attn_plan(B, type, nh, nkv, hd, max_rows, max_len, window, sinks);
-    return p.tok_bytes + (p.rows ? kv_paged_rows_workspace_bytes(B, M, type, nh, nkv, hd, max_rows, max_len, window, sinks) : 0);
+    return p.tok_bytes + (p.rows ? kv_paged_rows_workspace_bytes(B, M, p.tokens ? kTokCols : 0, type, nh, nkv, hd, max_rows, max_len, window, sinks) : 0);
 }
 
 cudaError_t launch_kv_paged_attn(const KvPagedAttnArgs &a, int type, int hd, bool pdl, cudaStream_t s) {
