@@ -11,7 +11,7 @@
 //   P = 2^(S c - ref)   a thread to a row: S from tensor memory, P back over it
 //   O += P V    tcgen05.mma, P from tensor memory, V as it lies (MN-major)
 //
-// Roles: a warp loads K and V tiles by TMA (a box to a page) into a ring, a warp
+// Roles: three warps load K and V tiles by TMA (a box to a page) into a ring, a warp
 // issues the products, two warpgroups do the softmax, so that one is at work
 // while the tensor cores serve the other.
 //  * f16 activations: the warpgroups have a row tile each and share the key
@@ -53,6 +53,8 @@ struct RwSizes {
     static constexpr int stages = HD == 128 ? 5 : 8;
     static constexpr uint32_t smem = 2 * tile + stages * tile + 1024;
     static constexpr int part = HD + 4;                            // floats of a row's part: output, maximum, sum
+    // P goes to the products in parts, so that these begin before the last exponentials are there
+    static constexpr int parts = split ? 4 : 2, part_keys = kRwKeys / parts;
 };
 
 struct RwUnit {
@@ -155,7 +157,8 @@ __device__ __forceinline__ void rw_wait(uint64_t *bar, int parity, volatile int 
         if (globaltimer_ns() - t0 > kWaitLimitNs) *err = 1;
     }
 }
-__device__ __forceinline__ void rw_bar(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+template <int N>
+__device__ __forceinline__ void rw_bar(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
 
 // The key tiles of rows at pmin .. pmax: tile i is key tile i < sink ? i : i - sink + first.
 struct RwTiles {
@@ -225,21 +228,12 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
     }
 }
 
-// 16 bytes of output.
-__device__ __forceinline__ void rw_store(float *to, const float *v) {
-    *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void rw_store(__half *to, const float *v) {
-    *reinterpret_cast<uint4 *>(to) = make_uint4(rw_pack(v[0], v[1]), rw_pack(v[2], v[3]), rw_pack(v[4], v[5]), rw_pack(v[6], v[7]));
-}
-
 template <typename T, int HD>
 __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, const __grid_constant__ CUtensorMap map) {
     using Z = RwSizes<T, HD>;
     constexpr int ST = Z::stages, QT = Z::QT;
     extern __shared__ uint8_t rw_smem[];
-    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2], b_o[2], b_q;
+    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][4], b_o[2], b_q;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err, s_bad, s_found, s_sum[kRwThreads / 32];
     __shared__ RwUnit s_unit;
@@ -258,7 +252,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b_s[i], 1);
-            mbar_init(&b_p[i], 128);
+            for (int k = 0; k < 4; ++k) mbar_init(&b_p[i][k], 128);
             mbar_init(&b_o[i], 1);
         }
         mbar_init(&b_q, 256);
@@ -356,12 +350,13 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8) {
-            // ---- loads: a lane to a page of the tile
+        if (warp != 9) {
+            // ---- loads: three warps take turns, a lane to a page of the tile
+            const int turn = warp == 8 ? 0 : warp - 9;
             const int shift = min(a.c.shift, 7), boxes = kRwKeys >> shift;
             const uint32_t bytes = static_cast<uint32_t>(HD * 2) << shift;
-            int n = 0;
-            for (; n < 2 * NT; ++n) {
+            int n = turn;
+            for (; n < 2 * NT; n += 3) {
                 int i;
                 bool v;
                 fill(n, i, v);
@@ -383,11 +378,11 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                 }
             }
             // the CTA may end when every copy has landed, and every stage has been released
-            for (int k = max(0, n - ST); k < n; ++k) {
+            for (int k = n - 3; k >= 0 && k >= n - 3 * ST; k -= 3) {
                 if (*err) (void)mbar_wait_bounded(&b_full[k % ST], static_cast<uint32_t>(k / ST & 1));
-                else wait(&b_empty[k % ST], k / ST);
+                else if (k >= 2 * NT - ST) wait(&b_empty[k % ST], k / ST);
             }
-        } else if (warp == 9 && NT > 0) {
+        } else if (NT > 0) {
             // ---- products: the whole warp walks along, one lane issues
             const uint32_t ring16 = (ring & 0x3FFFFu) >> 4, base16 = (base & 0x3FFFFu) >> 4;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -412,17 +407,21 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             auto pv = [&](int s, int i, bool add) {
                 const int n = fill_of_v(i), st = n % ST;
                 wait(&b_full[st], n / ST);
-                wait(&b_p[s], Z::split ? i >> 1 : i);
-                rw_after();
                 const uint32_t v = ring16 + st * (Z::tile >> 4), p = tm + s * 128;
-                if (one) {
 #pragma unroll
-                    for (int e = 0; e < kRwKeys / 16; ++e) {
-                        const uint64_t d = rw_desc(v + e * (2048 >> 4), kRwKeys * 128);
-                        // P: f16 [64 columns]; f32: hi and lo of 32 keys next to each other, 16 columns each
-                        const uint32_t at = p + (Z::split ? (e >> 1) * 32 + (e & 1) * 8 : e * 8);
-                        rw_mma_ts(tm + 256 + s * HD, at, d, rw_idesc(HD, true), add || e > 0);
-                        if constexpr (Z::split) rw_mma_ts(tm + 256 + s * HD, at + 16, d, rw_idesc(HD, true), true);
+                for (int k = 0; k < Z::parts; ++k) {   // as the parts of P come
+                    wait(&b_p[s][k], Z::split ? i >> 1 : i);
+                    rw_after();
+                    if (one) {
+#pragma unroll
+                        for (int ee = 0; ee < Z::part_keys / 16; ++ee) {
+                            const int e = k * (Z::part_keys / 16) + ee;
+                            const uint64_t d = rw_desc(v + e * (2048 >> 4), kRwKeys * 128);
+                            // P: f16 [64 columns]; f32: hi and lo of 32 keys next to each other, 16 columns each
+                            const uint32_t at = p + (Z::split ? (e >> 1) * 32 + (e & 1) * 8 : e * 8);
+                            rw_mma_ts(tm + 256 + s * HD, at, d, rw_idesc(HD, true), add || e > 0);
+                            if constexpr (Z::split) rw_mma_ts(tm + 256 + s * HD, at + 16, d, rw_idesc(HD, true), true);
+                        }
                     }
                 }
             };
@@ -462,12 +461,12 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        // ---- Q to shared memory: L lanes to a row, PW rows to a warp at once, all loads of NB passes before their stores
+        // ---- Q to shared memory: L lanes to a row, PW rows to a warp at once, NB passes whose loads all come before the stores
         {
-            constexpr int L = HD / 8, PW = 32 / L, NB = Z::split ? 4 : 8;
+            constexpr int L = HD / 8, PW = 32 / L, NB = QT * kRwRows / (8 * PW);
             const int ch = lane % L;
-#pragma unroll 1
-            for (int row0 = warp * PW + lane / L; row0 < QT * kRwRows; row0 += 8 * PW * NB) {
+            const int row0 = warp * PW + lane / L;
+            {
                 uint4 x[NB], y[Z::split ? NB : 1];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(&b_q);
-            if constexpr (Z::split) rw_bar(1);   // (s_c)
+            if constexpr (Z::split) rw_bar<256>(1);   // (s_c)
         }
         // ---- softmax: warpgroup s, a thread to a row
         const int s = warp >> 2, rr = tid & 127;
@@ -624,15 +623,21 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                 const float b = (m == -INFINITY ? 0.0f : m * c) - kOff;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < 128; k += 2) {
-                    const float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
-                    sum[k >> 1 & 1] += x;
-                    sum[2 + (k >> 1 & 1)] += y;
-                    v[k >> 1] = rw_pack(x, y);
+                for (int h = 0; h < Z::parts; ++h) {
+#pragma unroll
+                    for (int kk = 0; kk < Z::part_keys; kk += 2) {
+                        const int k = h * Z::part_keys + kk;
+                        const float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
+                        sum[k >> 1 & 1] += x;
+                        sum[2 + (k >> 1 & 1)] += y;
+                        v[k >> 1] = rw_pack(x, y);
+                    }
+                    rw_st32(tS + 32 * h, v + 32 * h);
+                    rw_wait_st();
+                    rw_before();
+                    mbar_arrive(&b_p[s][h]);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                rw_st32(tS, v);
-                rw_st32(tS + 32, v + 32);
             } else {
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -687,53 +692,81 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                         w[16 + (k >> 1)] = rw_pack(x - h.x, y - h.y);
                     }
                     rw_st32(tS + k0, w);
+                    rw_wait_st();
+                    rw_before();
+                    mbar_arrive(&b_p[s][k0 / 32]);
                 }
                 l += sum[0] + sum[1];
             }
-            rw_wait_st();
-            rw_before();
-            mbar_arrive(&b_p[s]);
         }
         if (active && own > 0) {
             wait(&b_o[s], 0);
             rw_after();
         }
         const float m2 = m == -INFINITY ? -INFINITY : m * c;   // the reference in base 2
-        const size_t at = static_cast<size_t>(u.start + u.tok0 + tok);
-        T *const out = static_cast<T *>(a.out) + at * a.out_stride + static_cast<size_t>(g * r.G + rr % r.G) * HD;
-        float *const to = dst ? dst + static_cast<size_t>((QT == 2 ? s * kRwRows : 0) + rr) * Z::part : nullptr;
+        // Rows go out through shared memory (Q's place: every score is there), so that each is written in one run of
+        // whole lines. N threads, from t on; C chunks of 16 bytes to a row, chunk c of row x at (c ^ x) or (c + x).
+        auto row_of = [&](int x, int tile) {   // the output of row x of a row tile, or null
+            const int k = (QT == 2 ? tile * r.TT : 0) + x / r.G;
+            return x < r.TT * r.G && k < tokens ? static_cast<T *>(a.out) + static_cast<size_t>(u.start + u.tok0 + k) * a.out_stride +
+                                                      static_cast<size_t>(g * r.G + x % r.G) * HD
+                                                : nullptr;
+        };
         if constexpr (!Z::split) {
-            rw_bar(1);
-            if (!s_bad) {
+            rw_bar<256>(1);
+            if (!s_bad && active) {
+                // (NT = 0: no position, zeros)
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                if (active) {
+                uint8_t *const place = smem + s * Z::tile;
+                constexpr int C = HD / 8;
+                if (!dst) {
 #pragma unroll
                     for (int d = 0; d < HD; d += 32) {
                         uint32_t o[32];
-                        if (own > 0) rw_ld32(tO + d, o);
+                        rw_ld32(tO + d, o);
                         rw_wait_ld();
-                        float v[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = own > 0 ? __uint_as_float(o[e]) : 0.0f;
-                        if (real) {
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                if (to) {
-                                    rw_store(to + d + e, v + e);
-                                } else {
-                                    float w[8];
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k) w[k] = v[e + k] * inv;
-                                    rw_store(out + d + e, w);
-                                }
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = rw_pack(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                            const int ch = (d + e) / 8;
+                            *reinterpret_cast<uint4 *>(place + rr * (HD * 2) + ((ch ^ (rr & 7)) << 4)) =
+                                own > 0 ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
                         }
-                        __syncwarp();
                     }
-                    if (to && real) {
-                        to[HD] = m2;
-                        to[HD + 1] = l;
+                    rw_bar<128>(2 + s);
+#pragma unroll 4
+                    for (int k = rr; k < kRwRows * C; k += 128) {
+                        const int x = k / C, ch = k % C;
+                        T *to = row_of(x, s);
+                        if (to) *reinterpret_cast<uint4 *>(to + ch * 8) = *reinterpret_cast<const uint4 *>(place + x * (HD * 2) + ((ch ^ (x & 7)) << 4));
                     }
+                } else {
+                    float *const part_rows = dst + static_cast<size_t>(s * kRwRows) * Z::part;
+#pragma unroll 1
+                    for (int d0 = 0; d0 < HD; d0 += HD / 2) {   // f32: half of the dimensions at a time
+#pragma unroll
+                        for (int d = 0; d < HD / 2; d += 32) {
+                            uint32_t o[32];
+                            rw_ld32(tO + d0 + d, o);
+                            rw_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(place + rr * (HD * 2) + ((((d + e) / 4) ^ (rr & 7)) << 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
+                        rw_bar<128>(2 + s);
+#pragma unroll 4
+                        for (int k = rr; k < kRwRows * C; k += 128) {
+                            const int x = k / C, ch = k % C;
+                            *reinterpret_cast<uint4 *>(part_rows + static_cast<size_t>(x) * Z::part + d0 + ch * 4) =
+                                *reinterpret_cast<const uint4 *>(place + x * (HD * 2) + ((ch ^ (x & 7)) << 4));
+                        }
+                        rw_bar<128>(2 + s);
+                    }
+                    part_rows[static_cast<size_t>(rr) * Z::part + HD] = m2;
+                    part_rows[static_cast<size_t>(rr) * Z::part + HD + 1] = l;
                 }
             }
         } else {
@@ -747,36 +780,45 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                     for (int e = 0; e < 32; ++e) master[d + e] += __uint_as_float(o[e]);
                 }
             }
-            // the second warpgroup's part joins the first one's, through Q's place (every score is there: Q is done with)
-            float *x = reinterpret_cast<float *>(smem) + rr;
+            // the second warpgroup's part joins the first one's
+            constexpr int C = HD / 4;
+            float4 *const place = reinterpret_cast<float4 *>(smem);
             if (s == 1 && NT > 1) {
 #pragma unroll
-                for (int d = 0; d < HD; ++d) x[d * kRwRows] = master[d];
+                for (int d = 0; d < HD; d += 4)
+                    place[rr * C + ((d / 4 + rr) & (C - 1))] = make_float4(master[d], master[d + 1], master[d + 2], master[d + 3]);
                 s_ml[0][rr] = m2;
                 s_ml[1][rr] = l;
             }
-            rw_bar(1);
-            if (!s_bad && s == 0 && real) {
-                const bool two = NT > 1;
-                const float mo = two ? s_ml[0][rr] : m2, lo = two ? s_ml[1][rr] : 0.0f, top = fmaxf(m2, mo);
-                const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = mo == top ? 1.0f : rw_ex2(mo - top);
-                const float sum = l * f0 + lo * f1, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            rw_bar<256>(1);
+            if (!s_bad) {
+                if (s == 0) {
+                    const bool two = NT > 1;
+                    const float mo = two ? s_ml[0][rr] : m2, lo = two ? s_ml[1][rr] : 0.0f, top = fmaxf(m2, mo);
+                    const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = mo == top ? 1.0f : rw_ex2(mo - top);
+                    const float sum = l * f0 + lo * f1, inv = dst ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-                for (int d = 0; d < HD; d += 8) {
-                    float w[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = master[d + k] * f0 + (two ? x[(d + k) * kRwRows] * f1 : 0.0f);
-                    if (to) {
-                        rw_store(to + d, w);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) w[k] *= inv;
-                        rw_store(out + d, w);
+                    for (int d = 0; d < HD; d += 4) {
+                        float4 *at = place + rr * C + ((d / 4 + rr) & (C - 1));
+                        float4 x = two ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        const float f = two ? f1 : 0.0f;
+                        x.x = (master[d] * f0 + x.x * f) * inv;
+                        x.y = (master[d + 1] * f0 + x.y * f) * inv;
+                        x.z = (master[d + 2] * f0 + x.z * f) * inv;
+                        x.w = (master[d + 3] * f0 + x.w * f) * inv;
+                        *at = x;
+                    }
+                    if (dst) {
+                        dst[static_cast<size_t>(rr) * Z::part + HD] = top;
+                        dst[static_cast<size_t>(rr) * Z::part + HD + 1] = sum;
                     }
                 }
-                if (to) {
-                    to[HD] = top;
-                    to[HD + 1] = sum;
+                rw_bar<256>(1);
+#pragma unroll 4
+                for (int k = tid; k < kRwRows * C; k += 256) {
+                    const int x = k / C, ch = k % C;
+                    float *to = dst ? dst + static_cast<size_t>(x) * Z::part : reinterpret_cast<float *>(row_of(x, 0));
+                    if (to) *reinterpret_cast<float4 *>(to + ch * 4) = place[x * C + ((ch + x) & (C - 1))];
                 }
             }
         }
