@@ -54,7 +54,7 @@ struct RwSizes {
     static constexpr uint32_t smem = 2 * tile + stages * tile + 1024;
     static constexpr int part = HD + 4;                            // floats of a row's part: output, maximum, sum
     // P goes to the products in parts, so that these begin before the last exponentials are there
-    static constexpr int parts = split ? 4 : 2, part_keys = kRwKeys / parts;
+    static constexpr int parts = 2, part_keys = kRwKeys / parts;
 };
 
 struct RwUnit {
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     using Z = RwSizes<T, HD>;
     constexpr int ST = Z::stages, QT = Z::QT;
     extern __shared__ uint8_t rw_smem[];
-    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][4], b_o[2], b_q;
+    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err, s_bad, s_found, s_sum[kRwThreads / 32];
     __shared__ RwUnit s_unit;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b_s[i], 1);
-            for (int k = 0; k < 4; ++k) mbar_init(&b_p[i][k], 128);
+            for (int k = 0; k < Z::parts; ++k) mbar_init(&b_p[i][k], 128);
             mbar_init(&b_o[i], 1);
         }
         mbar_init(&b_q, 256);
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     auto leave = [&]() {
         if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     };
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();   // (after the wait: what is launched next may begin beside this kernel, and needs what came before it)
 
     // ---- the unit: number `pair` of the sequences' units, a sequence's last (longest) one first
     {
@@ -692,9 +692,11 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                         w[16 + (k >> 1)] = rw_pack(x - h.x, y - h.y);
                     }
                     rw_st32(tS + k0, w);
-                    rw_wait_st();
-                    rw_before();
-                    mbar_arrive(&b_p[s][k0 / 32]);
+                    if ((k0 + 32) % Z::part_keys == 0) {
+                        rw_wait_st();
+                        rw_before();
+                        mbar_arrive(&b_p[s][k0 / Z::part_keys]);
+                    }
                 }
                 l += sum[0] + sum[1];
             }
@@ -837,29 +839,31 @@ __global__ void __launch_bounds__(128) k_paged_rows_join(const RwArgs r) {
     using Z = RwSizes<T, HD>;
     constexpr int E = HD / 32;
     const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5), unit = blockIdx.x;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     const RwCut cut = reinterpret_cast<const RwCut *>(r.ws)[unit];
     const int rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;
     if (cut.parts < 2 || rr >= r.TT * r.G || tok >= cut.tokens) return;
-    const float *src = r.ws + static_cast<size_t>(r.units) * 4 + (static_cast<size_t>(unit) * r.splits * (Z::QT * kRwRows) + row) * Z::part;
-    float m = -INFINITY, l = 0.0f, o[E];
+    {
+        const float *src = r.ws + static_cast<size_t>(r.units) * 4 + (static_cast<size_t>(unit) * r.splits * (Z::QT * kRwRows) + row) * Z::part;
+        float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+        for (int e = 0; e < E; ++e) o[e] = 0.0f;
 #pragma unroll 4
-    for (int k = 0; k < cut.parts; ++k) {
-        const float *q = src + static_cast<size_t>(k) * (Z::QT * kRwRows) * Z::part;
-        const float mc = q[HD], lc = q[HD + 1], top = fmaxf(m, mc);
-        const float f0 = m == top ? 1.0f : rw_ex2(m - top), f1 = mc == top ? 1.0f : rw_ex2(mc - top);
-        l = l * f0 + lc * f1;
+        for (int k = 0; k < cut.parts; ++k) {
+            const float *q = src + static_cast<size_t>(k) * (Z::QT * kRwRows) * Z::part;
+            const float mc = q[HD], lc = q[HD + 1], top = fmaxf(m, mc);
+            const float f0 = m == top ? 1.0f : rw_ex2(m - top), f1 = mc == top ? 1.0f : rw_ex2(mc - top);
+            l = l * f0 + lc * f1;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + q[lane * E + e] * f1;
-        m = top;
+            for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + q[e * 32 + lane] * f1;
+            m = top;
+        }
+        T *to = static_cast<T *>(r.a.out) + static_cast<size_t>(cut.start + tok) * r.a.out_stride +
+                static_cast<size_t>(unit % r.a.c.nkv * r.G + rr % r.G) * HD;
+#pragma unroll
+        for (int e = 0; e < E; ++e) to[e * 32 + lane] = kv_cvt<T>(l == 0.0f ? 0.0f : o[e] / l);
     }
-    T *to = static_cast<T *>(r.a.out) + static_cast<size_t>(cut.start + tok) * r.a.out_stride +
-            static_cast<size_t>(unit % r.a.c.nkv * r.G + rr % r.G) * HD + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) to[e] = kv_cvt<T>(l == 0.0f ? 0.0f : o[e] / l);
 }
 
 // How the units are launched and split: `units` CTAs of one part each (an upper
@@ -917,8 +921,12 @@ EncodeTiled encode_tiled() {
 }
 
 template <typename T, int HD>
-cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, float *ws, bool pdl, cudaStream_t s) {
+cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, float *ws, bool join, bool pdl, cudaStream_t s) {
     using Z = RwSizes<T, HD>;
+    const RwArgs r{a, a.nh / a.c.nkv, p.TT, min_cols, p.split_tiles, p.splits, p.units, ws};
+    if (join)
+        return p.splits == 1 ? cudaSuccess
+                             : launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 4), 128, 0, 1, s, r);
     const EncodeTiled encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
     // the pool as rows of HD values; a box is 64 values of the rows of a page that lie in one key tile
@@ -928,10 +936,7 @@ cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, floa
     if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.c.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const RwArgs r{a, a.nh / a.c.nkv, p.TT, min_cols, p.split_tiles, p.splits, p.units, ws};
-    cudaError_t e = launch_pdl(pdl, k_paged_rows<T, HD>, dim3(p.units, p.splits), kRwThreads, Z::smem, 1, s, r, map);
-    if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 4), 128, 0, 1, s, r);
+    return launch_pdl(pdl, k_paged_rows<T, HD>, dim3(p.units, p.splits), kRwThreads, Z::smem, 1, s, r, map);
 }
 
 template <typename T, int HD>
@@ -954,10 +959,10 @@ size_t kv_paged_rows_workspace_bytes(int B, int M, int min_cols, int type, int n
     return rw_plan(B, M, min_cols, type, nh, nkv, hd, max_rows, max_len, window, sinks).bytes;
 }
 
-cudaError_t launch_kv_paged_rows(const KvPagedAttnArgs &a, int type, int hd, int min_cols, float *ws, bool pdl, cudaStream_t s) {
+cudaError_t launch_kv_paged_rows(const KvPagedAttnArgs &a, int type, int hd, int min_cols, float *ws, bool join, bool pdl, cudaStream_t s) {
     const RwPlan p = rw_plan(a.b.B, a.b.M, min_cols, type, a.nh, a.c.nkv, hd, a.b.max_rows, a.b.max_len, a.window, a.sinks);
-    if (type == QW3_F32) return hd == 128 ? rows_t<float, 128>(a, min_cols, p, ws, pdl, s) : rows_t<float, 64>(a, min_cols, p, ws, pdl, s);
-    return hd == 128 ? rows_t<__half, 128>(a, min_cols, p, ws, pdl, s) : rows_t<__half, 64>(a, min_cols, p, ws, pdl, s);
+    if (type == QW3_F32) return hd == 128 ? rows_t<float, 128>(a, min_cols, p, ws, join, pdl, s) : rows_t<float, 64>(a, min_cols, p, ws, join, pdl, s);
+    return hd == 128 ? rows_t<__half, 128>(a, min_cols, p, ws, join, pdl, s) : rows_t<__half, 64>(a, min_cols, p, ws, join, pdl, s);
 }
 
 }  // namespace qw3

@@ -320,7 +320,7 @@ struct TokCut {
 };
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPagedAttnArgs a, int G, int max_cb, int ends, int min_share) {
+__global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPagedAttnArgs a, int G, int max_cb, int ends, int min_share, int beside) {
     using Z = TokSizes<T, HD>;
     constexpr int W = Z::W, KS = HD / 16, NT = HD / 8, CH = HD / 8;
     constexpr float kOff = 12.0f, kLazy = 3.0f;   // a weight is 2^(s - ref + 12), at most 2^15
@@ -330,8 +330,10 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     __shared__ float s_m[kTokWarps][8], s_l[kTokWarps][8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
     const int nkv = a.c.nkv;
+    // beside: the kernel before this one works on other sequences and has waited for what came before itself; this one
+    // runs beside it, and ends after it
     pdl_trigger();
-    pdl_wait();
+    if (!beside) pdl_wait();
 
     // ---- the share of this CTA: x0 .. x1 - 1 of all the work
     const int per = (a.b.B + kTokWarps * 32 - 1) / (kTokWarps * 32);
@@ -372,7 +374,10 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
         }
     }
     __syncthreads();
-    if (x0 >= total) return;
+    if (x0 >= total) {
+        if (beside) pdl_wait();
+        return;
+    }
 
     TokAt t;   // what the CTA computes
     t.i = s_i;
@@ -381,7 +386,10 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     t.u = s_off_u;
     t.k = max(0, s_off_k);
     long long x = x0 + max(0, -s_off_k);   // where this piece's steps begin
-    if (x >= x1) return;                   // (only at the end of all the work: min_share > ends)
+    if (x >= x1) {                         // (only at the end of all the work: min_share > ends)
+        if (beside) pdl_wait();
+        return;
+    }
     t.end = static_cast<int>(min(static_cast<long long>(t.s.steps), t.k + (x1 - x)));
     t.left = x1 - x - (t.end - t.k);
 
@@ -687,49 +695,60 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
         tok_next<W>(t, a, G, ends);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (beside) pdl_wait();
 }
 
-// One block to a column of a unit that was cut: HD threads four times over, each
-// quarter a fourth of the parts.
+// One block to a unit, if it was cut: a thread to a dimension of a column, the
+// parts' weights from shared memory.
+constexpr int kTokMaxGrid = 256;   // parts that a unit can have
 template <typename T, int HD>
-__global__ void __launch_bounds__(4 * HD) k_paged_tokens_join(const KvPagedAttnArgs a, int G, int max_cb, int grid) {
+__global__ void __launch_bounds__(512) k_paged_tokens_join(const KvPagedAttnArgs a, int G, int max_cb, int grid, int beside) {
     using Z = TokSizes<T, HD>;
     constexpr int W = Z::W;
-    __shared__ float s_m[4 * HD], s_l[4 * HD], s_v[3][HD];
-    const int col = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, d = tid % HD, quarter = tid / HD;
+    __shared__ float s_f[kTokMaxGrid][W], s_sum[W];
+    const int cb = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
     pdl_trigger();
-    pdl_wait();
+    if (!beside) pdl_wait();
     for (int b = blockIdx.z; b < a.b.B; b += gridDim.z) {
         const TokSeq s = tok_seq(a, b, G);
-        if (col >= s.cols) continue;
+        if (cb * W >= s.cols) continue;
+        const int cols = min(W, s.cols - cb * W);
         const float *slots = static_cast<const float *>(a.ws);
         const TokCut *cuts = reinterpret_cast<const TokCut *>(slots + static_cast<size_t>(grid) * 2 * W * Z::part);
-        const TokCut cut = cuts[(static_cast<size_t>(b) * a.c.nkv + g) * max_cb + col / W];
+        const TokCut cut = cuts[(static_cast<size_t>(b) * a.c.nkv + g) * max_cb + cb];
         if (cut.first < 0) continue;
-        const int last = static_cast<int>(cut.last & 0x7fffffffu), n = last - cut.first + 1;   // at most the grid: 4 HD and fewer
+        const int n = static_cast<int>(cut.last & 0x7fffffffu) - cut.first + 1;
         auto part = [&](int c) {
             const int slot = c == 0 && !(cut.last & 0x80000000u) ? 1 : 0;
-            return slots + ((static_cast<size_t>(cut.first + c) * 2 + slot) * W + col % W) * Z::part;
+            return slots + (static_cast<size_t>(cut.first + c) * 2 + slot) * W * Z::part;
         };
-        if (tid < n) {
-            s_m[tid] = part(tid)[HD];
-            s_l[tid] = part(tid)[HD + 1];
+        __syncthreads();
+        // a warp to a column: its maximum, each part's factor and the sum
+        for (int c = tid >> 5; c < cols; c += 16) {
+            const int lane = tid & 31;
+            float m = -INFINITY, l = 0.0f;
+            for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)[c * Z::part + HD]);
+            m = warp_max(m);
+            for (int k = lane; k < n; k += 32) {
+                const float mk = part(k)[c * Z::part + HD], f = mk == m ? 1.0f : ex2(mk - m);
+                s_f[k][c] = f;
+                l = fmaf(part(k)[c * Z::part + HD + 1], f, l);
+            }
+            l = warp_sum(l);
+            if (lane == 0) s_sum[c] = l;
         }
         __syncthreads();
-        float m = -INFINITY, l = 0.0f, v = 0.0f;
-        for (int c = 0; c < n; ++c) m = fmaxf(m, s_m[c]);
+        for (int i = tid; i < cols * HD; i += 512) {
+            const int c = i / HD, d = i % HD;
+            float v = 0.0f;
 #pragma unroll 8
-        for (int c = quarter; c < n; c += 4) v = fmaf(part(c)[d], s_m[c] == m ? 1.0f : ex2(s_m[c] - m), v);
-        if (quarter > 0) s_v[quarter - 1][d] = v;
-        for (int c = 0; c < n; ++c) l = fmaf(s_l[c], s_m[c] == m ? 1.0f : ex2(s_m[c] - m), l);
-        __syncthreads();
-        if (quarter == 0) {
-            v = (v + s_v[0][d]) + (s_v[1][d] + s_v[2][d]);
+            for (int k = 0; k < n; ++k) v = fmaf(part(k)[c * Z::part + d], s_f[k][c], v);
+            const int col = cb * W + c;
             T *to = static_cast<T *>(a.out) + (s.start + col / G) * a.out_stride + static_cast<size_t>(g * G + col % G) * HD + d;
-            *to = kv_cvt<T>(l == 0.0f ? 0.0f : v / l);
+            *to = kv_cvt<T>(s_sum[c] == 0.0f ? 0.0f : v / s_sum[c]);
         }
-        __syncthreads();
     }
+    if (beside) pdl_wait();
 }
 
 // How the token kernels are launched: the columns that a sequence can have, the
@@ -749,19 +768,25 @@ TokPlan tok_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int max
     p.ends = units > num_sms() ? kTokUnit : 0;
     p.min_share = p.ends + kTokWarps;   // a step to a warp: fewer would only be more to join
     const long long work = (p.ends + std::max<long long>(1, (len + kTokKeys - 1) / kTokKeys)) * units;
-    p.grid = static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(num_sms(), 256), (work + p.min_share - 1) / p.min_share)));
+    p.grid = static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(num_sms(), kTokMaxGrid), (work + p.min_share - 1) / p.min_share)));
     p.bytes = static_cast<size_t>(p.grid) * 2 * W * (hd + 4) * 4 + static_cast<size_t>(B) * nkv * p.max_cb * sizeof(TokCut);
     return p;
 }
 
 template <typename T, int HD>
-cudaError_t tokens_t(const KvPagedAttnArgs &a, const TokPlan &p, bool pdl, cudaStream_t s) {
+cudaError_t tokens_t(const KvPagedAttnArgs &a, const TokPlan &p, bool join, bool beside, bool pdl, cudaStream_t s) {
     using Z = TokSizes<T, HD>;
     const int G = a.nh / a.c.nkv;
-    cudaError_t e = launch_pdl(pdl, k_paged_tokens<T, HD>, dim3(p.grid), kTokWarps * 32, Z::smem, 1, s, a, G, p.max_cb, p.ends, p.min_share);
-    if (e != cudaSuccess || p.grid == 1) return e;
-    const dim3 grid(p.cols, a.c.nkv, std::min(a.b.B, 65535));
-    return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, 4 * HD, 0, 1, s, a, G, p.max_cb, p.grid);
+    if (!join)
+        return launch_pdl(pdl, k_paged_tokens<T, HD>, dim3(p.grid), kTokWarps * 32, Z::smem, 1, s, a, G, p.max_cb, p.ends, p.min_share,
+                          static_cast<int>(beside));
+    if (p.grid == 1) return cudaSuccess;
+    const dim3 grid(p.max_cb, a.c.nkv, std::min(a.b.B, 65535));
+    return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, 512, 0, 1, s, a, G, p.max_cb, p.grid, static_cast<int>(beside));
+}
+cudaError_t launch_tokens(const KvPagedAttnArgs &a, int type, int hd, const TokPlan &p, bool join, bool beside, bool pdl, cudaStream_t s) {
+    if (type == QW3_F32) return hd == 128 ? tokens_t<float, 128>(a, p, join, beside, pdl, s) : tokens_t<float, 64>(a, p, join, beside, pdl, s);
+    return hd == 128 ? tokens_t<__half, 128>(a, p, join, beside, pdl, s) : tokens_t<__half, 64>(a, p, join, beside, pdl, s);
 }
 
 template <typename T, int HD>
@@ -791,11 +816,11 @@ namespace {
 // Which kernels a call needs: sequences of up to kTokCols columns are the token
 // kernels', longer ones attn_paged_tc.cu's. One sequence alone goes by max_rows.
 struct AttnPlan {
-    bool tokens, rows;
+    bool tokens, rows, rows_split;
     TokPlan tok;
-    size_t tok_bytes;
+    size_t tok_bytes, rows_bytes;
 };
-AttnPlan attn_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
+AttnPlan attn_plan(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len, int window, int sinks) {
     AttnPlan p{};
     p.rows = static_cast<long long>(max_rows) * (nh / nkv) > kTokCols;
     p.tokens = !p.rows || B > 1;
@@ -803,6 +828,9 @@ AttnPlan attn_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int m
         p.tok = tok_plan(B, type, nh, nkv, hd, max_rows, max_len, window, sinks);
         p.tok_bytes = (p.tok.bytes + 127) / 128 * 128;
     }
+    if (p.rows)
+        p.rows_bytes = kv_paged_rows_workspace_bytes(B, M, p.tokens ? kTokCols : 0, type, nh, nkv, hd, max_rows, max_len, window, sinks);
+    p.rows_split = p.rows_bytes > 0;
     return p;
 }
 
@@ -811,19 +839,27 @@ AttnPlan attn_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int m
 size_t kv_paged_attn_workspace_bytes(int B, int M, int type, int nh, int nkv, int hd, int max_rows, int max_len,
                                      int window, int sinks) {
     if (B == 0 || M == 0 || max_rows == 0) return 0;
-    const AttnPlan p = attn_plan(B, type, nh, nkv, hd, max_rows, max_len, window, sinks);
-    return p.tok_bytes + (p.rows ? kv_paged_rows_workspace_bytes(B, M, p.tokens ? kTokCols : 0, type, nh, nkv, hd, max_rows, max_len, window, sinks) : 0);
+    const AttnPlan p = attn_plan(B, M, type, nh, nkv, hd, max_rows, max_len, window, sinks);
+    return p.tok_bytes + p.rows_bytes;
 }
 
 cudaError_t launch_kv_paged_attn(const KvPagedAttnArgs &a, int type, int hd, bool pdl, cudaStream_t s) {
-    const AttnPlan p = attn_plan(a.b.B, type, a.nh, a.c.nkv, hd, a.b.max_rows, a.b.max_len, a.window, a.sinks);
-    cudaError_t e = cudaSuccess;
-    if (p.rows)
-        e = launch_kv_paged_rows(a, type, hd, p.tokens ? kTokCols : 0,
-                                 reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + p.tok_bytes), pdl, s);
-    if (e != cudaSuccess || !p.tokens) return e;
-    if (type == QW3_F32) return hd == 128 ? tokens_t<float, 128>(a, p.tok, pdl, s) : tokens_t<float, 64>(a, p.tok, pdl, s);
-    return hd == 128 ? tokens_t<__half, 128>(a, p.tok, pdl, s) : tokens_t<__half, 64>(a, p.tok, pdl, s);
+    const AttnPlan p = attn_plan(a.b.B, a.b.M, type, a.nh, a.c.nkv, hd, a.b.max_rows, a.b.max_len, a.window, a.sinks);
+    // the kernels first, one beside the other where there are both, then what joins their parts
+    float *const ws = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + p.tok_bytes);
+    for (const bool join : {false, true}) {
+        bool before = false;
+        if (p.rows) {
+            const cudaError_t e = launch_kv_paged_rows(a, type, hd, p.tokens ? kTokCols : 0, ws, join, pdl, s);
+            if (e != cudaSuccess) return e;
+            before = !join || p.rows_split;
+        }
+        if (p.tokens) {
+            const cudaError_t e = launch_tokens(a, type, hd, p.tok, join, before, pdl, s);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
 }
 
 }  // namespace qw3

@@ -402,11 +402,12 @@ size_t kv_paged_attn_workspace_bytes(int B, int M, int type, int nh, int nkv, in
                                      int window, int sinks);
 cudaError_t configure_kv_paged();
 // The sequences with more than min_cols rows times query heads of a kv head
-// (attn_paged_tc.cu).
+// (attn_paged_tc.cu): the kernel, then (join) what joins the units it split, if any.
 size_t kv_paged_rows_workspace_bytes(int B, int M, int min_cols, int type, int nh, int nkv, int hd, int max_rows, int max_len,
                                      int window, int sinks);
 cudaError_t configure_kv_paged_rows();
-cudaError_t launch_kv_paged_rows(const KvPagedAttnArgs &a, int type, int hd, int min_cols, float *ws, bool pdl, cudaStream_t s);
+cudaError_t launch_kv_paged_rows(const KvPagedAttnArgs &a, int type, int hd, int min_cols, float *ws, bool join, bool pdl,
+                                 cudaStream_t s);
 cudaError_t launch_kv_paged_attn(const KvPagedAttnArgs &a, int type, int hd, bool pdl, cudaStream_t s);
 
 // ---- log probabilities (logprobs.cu)
