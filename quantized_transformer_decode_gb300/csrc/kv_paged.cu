@@ -698,21 +698,22 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     if (beside) pdl_wait();
 }
 
-// One block to a unit, if it was cut: a thread to a dimension of a column, the
-// parts' weights from shared memory.
+// One block to `per` columns (all of a unit's, or one) of a unit that was cut: a
+// thread to a dimension of a column, or several that share the parts; the parts'
+// weights from shared memory.
 constexpr int kTokMaxGrid = 256;   // parts that a unit can have
 template <typename T, int HD>
-__global__ void __launch_bounds__(512) k_paged_tokens_join(const KvPagedAttnArgs a, int G, int max_cb, int grid, int beside) {
+__global__ void __launch_bounds__(512) k_paged_tokens_join(const KvPagedAttnArgs a, int G, int max_cb, int grid, int per, int beside) {
     using Z = TokSizes<T, HD>;
     constexpr int W = Z::W;
-    __shared__ float s_f[kTokMaxGrid][W], s_sum[W];
-    const int cb = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
+    __shared__ float s_f[kTokMaxGrid][W], s_sum[W], s_v[512];
+    const int cb = blockIdx.x * per / W, c0 = blockIdx.x * per % W, g = blockIdx.y, tid = threadIdx.x;
     pdl_trigger();
     if (!beside) pdl_wait();
     for (int b = blockIdx.z; b < a.b.B; b += gridDim.z) {
         const TokSeq s = tok_seq(a, b, G);
-        if (cb * W >= s.cols) continue;
-        const int cols = min(W, s.cols - cb * W);
+        if (cb * W + c0 >= s.cols) continue;
+        const int cols = min(per, s.cols - cb * W - c0);
         const float *slots = static_cast<const float *>(a.ws);
         const TokCut *cuts = reinterpret_cast<const TokCut *>(slots + static_cast<size_t>(grid) * 2 * W * Z::part);
         const TokCut cut = cuts[(static_cast<size_t>(b) * a.c.nkv + g) * max_cb + cb];
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(512) k_paged_tokens_join(const KvPagedAttnArgs
         const int n = static_cast<int>(cut.last & 0x7fffffffu) - cut.first + 1;
         auto part = [&](int c) {
             const int slot = c == 0 && !(cut.last & 0x80000000u) ? 1 : 0;
-            return slots + (static_cast<size_t>(cut.first + c) * 2 + slot) * W * Z::part;
+            return slots + ((static_cast<size_t>(cut.first + c) * 2 + slot) * W + c0) * Z::part;
         };
         __syncthreads();
         // a warp to a column: its maximum, each part's factor and the sum
@@ -738,14 +739,25 @@ __global__ void __launch_bounds__(512) k_paged_tokens_join(const KvPagedAttnArgs
             if (lane == 0) s_sum[c] = l;
         }
         __syncthreads();
-        for (int i = tid; i < cols * HD; i += 512) {
-            const int c = i / HD, d = i % HD;
+        const int values = cols * HD, shares = max(1, 512 / values);
+        for (int i0 = 0; i0 < values; i0 += 512) {
+            const int i = i0 + tid % values, share = i0 > 0 || values >= 512 ? 0 : tid / values, at = min(i, values - 1);
+            const int c = at / HD, d = at % HD;
             float v = 0.0f;
+            if (share < shares) {
 #pragma unroll 8
-            for (int k = 0; k < n; ++k) v = fmaf(part(k)[c * Z::part + d], s_f[k][c], v);
-            const int col = cb * W + c;
-            T *to = static_cast<T *>(a.out) + (s.start + col / G) * a.out_stride + static_cast<size_t>(g * G + col % G) * HD + d;
-            *to = kv_cvt<T>(s_sum[c] == 0.0f ? 0.0f : v / s_sum[c]);
+                for (int k = share; k < n; k += shares) v = fmaf(part(k)[c * Z::part + d], s_f[k][c], v);
+            }
+            if (shares > 1) {
+                s_v[tid] = v;
+                __syncthreads();
+                for (int k = 1; k < shares && share == 0; ++k) v += s_v[k * values + tid];
+            }
+            if (share == 0 && i < values) {
+                const int col = cb * W + c0 + c;
+                T *to = static_cast<T *>(a.out) + (s.start + col / G) * a.out_stride + static_cast<size_t>(g * G + col % G) * HD + d;
+                *to = kv_cvt<T>(s_sum[c] == 0.0f ? 0.0f : v / s_sum[c]);
+            }
         }
     }
     if (beside) pdl_wait();
@@ -781,8 +793,10 @@ cudaError_t tokens_t(const KvPagedAttnArgs &a, const TokPlan &p, bool join, bool
         return launch_pdl(pdl, k_paged_tokens<T, HD>, dim3(p.grid), kTokWarps * 32, Z::smem, 1, s, a, G, p.max_cb, p.ends, p.min_share,
                           static_cast<int>(beside));
     if (p.grid == 1) return cudaSuccess;
-    const dim3 grid(p.max_cb, a.c.nkv, std::min(a.b.B, 65535));
-    return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, 512, 0, 1, s, a, G, p.max_cb, p.grid, static_cast<int>(beside));
+    // few units: a block to a column (1 x 32768, 8 units in 152 parts: 34 us in all where a block to a unit makes it 38)
+    const int per = static_cast<long long>(a.b.B) * a.c.nkv * p.max_cb <= 32 ? 1 : Z::W;
+    const dim3 grid(per == 1 ? p.cols : p.max_cb, a.c.nkv, std::min(a.b.B, 65535));
+    return launch_pdl(pdl, k_paged_tokens_join<T, HD>, grid, 512, 0, 1, s, a, G, p.max_cb, p.grid, per, static_cast<int>(beside));
 }
 cudaError_t launch_tokens(const KvPagedAttnArgs &a, int type, int hd, const TokPlan &p, bool join, bool beside, bool pdl, cudaStream_t s) {
     if (type == QW3_F32) return hd == 128 ? tokens_t<float, 128>(a, p, join, beside, pdl, s) : tokens_t<float, 64>(a, p, join, beside, pdl, s);
