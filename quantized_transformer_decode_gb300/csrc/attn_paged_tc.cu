@@ -50,8 +50,11 @@ struct RwSizes {
     static constexpr bool split = sizeof(T) == 4;
     static constexpr int QT = split ? 1 : 2;                       // row tiles of a unit
     static constexpr uint32_t tile = kRwRows * HD * 2;             // bytes of a row tile, a K tile, a V tile
-    static constexpr int stages = HD == 128 ? 5 : 8;
-    static constexpr uint32_t smem = 2 * tile + stages * tile + 1024;
+    // f16: rows go out through a place of their own (per warpgroup 128 bytes of each row), so that the next unit's Q
+    // comes while this one ends; f32: through Q's
+    static constexpr int stages = HD == 128 ? (split ? 5 : 4) : 8;
+    static constexpr uint32_t out = split ? 0 : kRwRows * 128;
+    static constexpr uint32_t smem = 2 * tile + stages * tile + 2 * out + 1024;
     static constexpr int part = HD + 4;                            // floats of a row's part: output, maximum, sum
     // P goes to the products in parts, so that these begin before the last exponentials are there
     static constexpr int parts = 2, part_keys = kRwKeys / parts;
@@ -71,7 +74,7 @@ struct RwArgs {
     int G, TT;          // query heads of a kv head, tokens of a row tile
     int min_cols;       // sequences with as many columns, or fewer, are others'
     int split_tiles;    // key tiles of a part
-    int splits, units;  // parts and units that the workspace has room for
+    int splits, units;  // parts of a unit, and units, at most
     float *ws;
 };
 
@@ -157,6 +160,10 @@ __device__ __forceinline__ void rw_wait(uint64_t *bar, int parity, volatile int 
         if (globaltimer_ns() - t0 > kWaitLimitNs) *err = 1;
     }
 }
+__device__ __forceinline__ void rw_tma3(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void rw_bar(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
 
@@ -174,15 +181,16 @@ __device__ __forceinline__ RwTiles rw_tiles(int pmin, int pmax, int window, int 
     return t;
 }
 
-// The unit without matrix products, for the tiles i0 .. i1 - 1: 8 warps, a row at
-// a time. dst: the part's rows, or null for the output.
+// Rows row0 .. row1 - 1 of the unit without matrix products, for the tiles i0 .. i1
+// - 1: warp `warp` of `warps`, a row at a time. dst: the part's rows, or null for
+// the output.
 template <typename T, int HD>
-__device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwTiles &t, int i0, int i1, int g, int rows, float off,
-                                     float *dst) {
+__device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwTiles &t, int i0, int i1, int g, int row0, int row1,
+                                     int warp, int warps, float off, float *dst) {
     constexpr int E = HD / 32;
     const int lane = threadIdx.x & 31;
     const KvPagedAttnArgs &a = r.a;
-    for (int row = threadIdx.x >> 5; row < rows; row += 8) {
+    for (int row = row0 + warp; row < row1; row += warps) {
         const int tok = row / kRwRows * r.TT + row % kRwRows / r.G, h = g * r.G + row % kRwRows % r.G;
         if (row % kRwRows >= r.TT * r.G || u.tok0 + tok >= u.n) continue;
         const int p = u.p0 + u.tok0 + tok;
@@ -228,23 +236,64 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
     }
 }
 
+// The units in order: numbers that grow from call to call, so the sequences are
+// walked through once. A warp's lanes look at 32 of them; all lanes call it.
+struct RwFind {
+    int b0 = 0, before = 0;
+};
 template <typename T, int HD>
-__global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, const __grid_constant__ CUtensorMap map) {
+__device__ __forceinline__ bool rw_find(const RwArgs &r, int pair, RwFind &f, RwUnit &u) {
+    const int lane = threadIdx.x & 31, UT = r.TT * RwSizes<T, HD>::QT;
+    for (; f.b0 < r.a.b.B; f.b0 += 32) {
+        const int b = f.b0 + lane;
+        KvSeq q{0, 0, 0};
+        int mine = 0;
+        if (b < r.a.b.B) {
+            q = kv_seq(r.a.b, b);
+            if (q.n * r.G > r.min_cols) mine = (q.n + UT - 1) / UT;
+        }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int at = f.before + upto - mine, all = __shfl_sync(0xffffffffu, upto, 31);
+        if (pair < f.before + all) {
+            const int who = __ffs(__ballot_sync(0xffffffffu, pair >= at && pair < at + mine)) - 1;
+            // a sequence's last (longest) unit first
+            const int tok0 = (mine - 1 - (pair - at)) * UT;
+            u = RwUnit{f.b0 + who, __shfl_sync(0xffffffffu, q.start, who), __shfl_sync(0xffffffffu, tok0, who),
+                       __shfl_sync(0xffffffffu, q.n, who), __shfl_sync(0xffffffffu, q.p0, who)};
+            return true;
+        }
+        f.before += all;
+    }
+    return false;
+}
+
+// A part of a unit, as every role of a CTA sees it.
+struct RwItem {
+    RwUnit u;
+    RwTiles tiles;
+    int g, tokens, pmin, pmax, i0, NT, parts, part, unit;
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRwThreads, 1)
+    k_paged_rows(const RwArgs r, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
     using Z = RwSizes<T, HD>;
     constexpr int ST = Z::stages, QT = Z::QT;
     extern __shared__ uint8_t rw_smem[];
-    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q;
+    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q, b_q_free;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_err, s_bad, s_found, s_sum[kRwThreads / 32];
-    __shared__ RwUnit s_unit;
+    __shared__ int s_err, s_bad[2][3];
     __shared__ float s_c[kRwRows], s_ml[2][kRwRows];
     const KvPagedAttnArgs &a = r.a;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the warp's own: uniform branches)
     const uint32_t base = (smem_u32(rw_smem) + 1023) & ~1023u;
     uint8_t *const smem = rw_smem + (base - smem_u32(rw_smem));
-    const int g = blockIdx.x % a.c.nkv, pair = blockIdx.x / a.c.nkv;
-    const int UT = r.TT * QT;   // tokens of a unit
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&b_full[i], 1);
@@ -254,12 +303,12 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             mbar_init(&b_s[i], 1);
             for (int k = 0; k < Z::parts; ++k) mbar_init(&b_p[i][k], 128);
             mbar_init(&b_o[i], 1);
+            for (int k = 0; k < 3; ++k) s_bad[i][k] = 0;
         }
-        mbar_init(&b_q, 256);
+        mbar_init(&b_q, Z::split ? 256 : 1);
+        mbar_init(&b_q_free, 1);
         fence_mbar_init();
         s_err = 0;
-        s_bad = 0;
-        s_found = 0;
     }
     if (warp == 9) {   // (nothing else holds tensor memory here: no two of these CTAs fit an SM)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
@@ -269,73 +318,38 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
     __syncthreads();
     rw_after();
     const uint32_t tmem = s_tmem;
-    auto leave = [&]() {
-        if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    };
     pdl_wait();
     pdl_trigger();   // (after the wait: what is launched next may begin beside this kernel, and needs what came before it)
 
-    // ---- the unit: number `pair` of the sequences' units, a sequence's last (longest) one first
-    {
-        int before = 0;
-        for (int b0 = 0; b0 < a.b.B; b0 += kRwThreads) {
-            const int b = b0 + tid;
-            KvSeq q{0, 0, 0};
-            int mine = 0;
-            if (b < a.b.B) {
-                q = kv_seq(a.b, b);
-                if (q.n * r.G > r.min_cols) mine = (q.n + UT - 1) / UT;
-            }
-            int upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
-            if (lane == 31) s_sum[warp] = upto;
-            __syncthreads();
-            int at = before + upto - mine, all = 0;
-            for (int w = 0; w < kRwThreads / 32; ++w) {
-                if (w < warp) at += s_sum[w];
-                all += s_sum[w];
-            }
-            if (pair >= at && pair < at + mine) {
-                s_unit = RwUnit{b, q.start, (mine - 1 - (pair - at)) * UT, q.n, q.p0};
-                s_found = 1;
-            }
-            before += all;
-            __syncthreads();
-            if (before > pair) break;
-        }
-    }
-    RwCut *const cuts = reinterpret_cast<RwCut *>(r.ws);
-    if (!s_found) {
-        if (blockIdx.y == 0 && tid == 0 && r.splits > 1) cuts[blockIdx.x] = RwCut{0, 0, 0, 0};
-        leave();
-        return;
-    }
-    const RwUnit u = s_unit;
-    const int tokens = min(UT, u.n - u.tok0);
-    const int pmin = u.p0 + u.tok0, pmax = pmin + tokens - 1;
-    const RwTiles tiles = rw_tiles(pmin, pmax, a.window, a.sinks);
-    const int parts = max(1, (tiles.n + r.split_tiles - 1) / r.split_tiles), part = blockIdx.y;
-    if (part == 0 && tid == 0 && r.splits > 1) cuts[blockIdx.x] = RwCut{u.start + u.tok0, tokens, parts, 0};
-    if (part >= parts) {
-        leave();
-        return;
-    }
-    const int i0 = part * r.split_tiles, i1 = min(tiles.n, i0 + r.split_tiles), NT = i1 - i0;
-    float *const dst = parts == 1 ? nullptr
-                                  : r.ws + static_cast<size_t>(r.units) * 4 +
-                                        (static_cast<size_t>(blockIdx.x) * r.splits + part) * (QT * kRwRows) * Z::part;
-    const int row_tiles = QT == 1 ? 1 : (tokens > r.TT ? 2 : 1);
-    // a negative scale goes into Q, so that scores are scaled by c > 0
+    // a negative scale is taken into the scores' sign, so that they are scaled by c > 0
     const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
     const float c0 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
     const uint32_t ring = base + 2 * Z::tile;
     volatile int *err = &s_err;
-    // fill n of the ring: its key tile, and whether it is V
-    auto fill = [&](int n, int &i, bool &v) {
+    auto wait = [&](uint64_t *bar, int parity) { rw_wait(bar, parity, err); };
+    RwCut *const cuts = reinterpret_cast<RwCut *>(r.ws);
+    // Item k of this CTA: the items (parts of units, long ones first) go to the CTAs to and fro, so that the lengths
+    // add up to about the same. Every role walks through them by itself; false behind the last one.
+    const int items = r.units * r.splits;
+    auto number = [&](int k) { return k * static_cast<int>(gridDim.x) + (k & 1 ? static_cast<int>(gridDim.x - 1 - blockIdx.x) : static_cast<int>(blockIdx.x)); };
+    auto item = [&](int k, RwFind &f, RwItem &it) {
+        const int w = number(k);
+        if (w >= items) return false;
+        it.unit = w / r.splits;
+        it.part = w % r.splits;
+        it.g = it.unit % a.c.nkv;
+        if (!rw_find<T, HD>(r, it.unit / a.c.nkv, f, it.u)) return false;
+        it.tokens = min(r.TT * QT, it.u.n - it.u.tok0);
+        it.pmin = it.u.p0 + it.u.tok0;
+        it.pmax = it.pmin + it.tokens - 1;
+        it.tiles = rw_tiles(it.pmin, it.pmax, a.window, a.sinks);
+        it.parts = max(1, (it.tiles.n + r.split_tiles - 1) / r.split_tiles);
+        it.i0 = it.part * r.split_tiles;
+        it.NT = max(0, min(it.tiles.n, it.i0 + r.split_tiles) - it.i0);
+        return true;
+    };
+    // fill n of an item's in the ring: its key tile, and whether it is V
+    auto fill = [](int n, int NT, int &i, bool &v) {
         if constexpr (!Z::split) {   // K0 V0 K1 V1 ..
             v = n & 1;
             i = n >> 1;
@@ -344,51 +358,89 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
             i = n == 2 * NT - 1 ? NT - 1 : v ? (n - 2) >> 1 : (n + 1) >> 1;
         }
     };
-    auto fill_of_k = [&](int i) { return Z::split ? max(0, 2 * i - 1) : 2 * i; };
-    auto fill_of_v = [&](int i) { return Z::split ? min(2 * i + 2, 2 * NT - 1) : 2 * i + 1; };
-    auto wait = [&](uint64_t *bar, int parity) { rw_wait(bar, parity, err); };
+    auto fill_of_k = [](int i) { return Z::split ? max(0, 2 * i - 1) : 2 * i; };
+    auto fill_of_v = [](int i, int NT) { return Z::split ? min(2 * i + 2, 2 * NT - 1) : 2 * i + 1; };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        RwFind f;
+        RwItem it;
         if (warp != 9) {
-            // ---- loads: three warps take turns, a lane to a page of the tile
+            // ---- loads: three warps take turns, a lane to a page of the tile; the first one sees to Q and to the cuts
             const int turn = warp == 8 ? 0 : warp - 9;
             const int shift = min(a.c.shift, 7), boxes = kRwKeys >> shift;
             const uint32_t bytes = static_cast<uint32_t>(HD * 2) << shift;
-            int n = turn;
-            for (; n < 2 * NT; n += 3) {
-                int i;
-                bool v;
-                fill(n, i, v);
-                const int j = tiles.key(i0 + i) + (lane << shift);
-                const int page = lane < boxes && j <= pmax ? kv_page(a.b, a.c, u.seq, j) : -1;
-                const int st = n % ST;
-                if (n >= ST) {
-                    wait(&b_empty[st], n / ST - 1);
-                    if (__any_sync(0xffffffffu, *err != 0)) break;
-                }
-                const int held = __popc(__ballot_sync(0xffffffffu, page >= 0));
-                if (lane == 0) mbar_arrive_expect_tx(&b_full[st], held * bytes);
-                __syncwarp();
-                if (page >= 0) {
-                    const int y = (((page * 2 + v) * a.c.nkv + g) << a.c.shift) + (j & ((1 << a.c.shift) - 1));
-                    const uint32_t to = ring + st * Z::tile + (static_cast<uint32_t>(lane) << shift) * 128;
+            int done = 0, nq = 0;   // fills, and Qs, of the items before
+            bool ok = true;
+            for (int k = 0; ok && item(k, f, it); ++k) {
+                if (turn == 0 && lane == 0 && it.part == 0 && r.splits > 1)
+                    cuts[it.unit] = RwCut{it.u.start + it.u.tok0, it.tokens, it.parts, 0};
+                if (it.NT == 0) continue;
+                if (!Z::split && turn == 0) {
+                    if (nq > 0) wait(&b_q_free, nq - 1);
+                    if (lane == 0) {
+                        const int two = it.tokens > r.TT ? 2 : 1;
+                        mbar_arrive_expect_tx(&b_q, two * (HD * 2) * r.G * r.TT);
+                        for (int s = 0; s < two; ++s)
 #pragma unroll
-                    for (int h = 0; h < HD / 64; ++h) rw_tma(to + h * (kRwKeys * 128), &map, h * 64, y, &b_full[st]);
+                            for (int h = 0; h < HD / 64; ++h)
+                                rw_tma3(base + s * Z::tile + h * (kRwRows * 128), &qmap, h * 64, it.g * r.G,
+                                        it.u.start + it.u.tok0 + s * r.TT, &b_q);
+                    }
+                    __syncwarp();
+                    ++nq;
+                }
+                // the fills of this item that are this warp's: those whose number among all is `turn` modulo 3
+                for (int n = (turn + 3 - done % 3) % 3; n < 2 * it.NT; n += 3) {
+                    const int all = done + n, st = all % ST;
+                    int i;
+                    bool v;
+                    fill(n, it.NT, i, v);
+                    const int j = it.tiles.key(it.i0 + i) + (lane << shift);
+                    const int page = lane < boxes && j <= it.pmax ? kv_page(a.b, a.c, it.u.seq, j) : -1;
+                    if (all >= ST) wait(&b_empty[st], all / ST - 1);
+                    if (__any_sync(0xffffffffu, *err != 0)) {
+                        ok = false;
+                        break;
+                    }
+                    const int held = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                    if (lane == 0) mbar_arrive_expect_tx(&b_full[st], held * bytes);
+                    __syncwarp();
+                    if (page >= 0) {
+                        const int y = (((page * 2 + v) * a.c.nkv + it.g) << a.c.shift) + (j & ((1 << a.c.shift) - 1));
+                        const uint32_t to = ring + st * Z::tile + (static_cast<uint32_t>(lane) << shift) * 128;
+#pragma unroll
+                        for (int h = 0; h < HD / 64; ++h) rw_tma(to + h * (kRwKeys * 128), &map, h * 64, y, &b_full[st]);
+                    }
+                }
+                if (ok) done += 2 * it.NT;
+            }
+            // units that are not there
+            if (turn == 0 && lane == 0 && r.splits > 1)
+                for (int k = 0; number(k) < items; ++k)
+                    if (number(k) % r.splits == 0 && number(k) / r.splits / a.c.nkv >= f.before && f.b0 >= a.b.B)
+                        cuts[number(k) / r.splits] = RwCut{0, 0, 0, 0};
+            // the CTA may end when every copy has landed, and every stage has been released
+            if (ok) {
+                for (int n = max(0, done - ST); n < done; ++n)
+                    if (n % 3 == turn) wait(&b_empty[n % ST], n / ST);
+            } else {   // (copies in flight: as long as a second for each stage)
+                for (int st = 0; st < ST; ++st) {
+                    (void)mbar_wait_bounded(&b_full[st], 0);
+                    (void)mbar_wait_bounded(&b_full[st], 1);
                 }
             }
-            // the CTA may end when every copy has landed, and every stage has been released
-            for (int k = n - 3; k >= 0 && k >= n - 3 * ST; k -= 3) {
-                if (*err) (void)mbar_wait_bounded(&b_full[k % ST], static_cast<uint32_t>(k / ST & 1));
-                else if (k >= 2 * NT - ST) wait(&b_empty[k % ST], k / ST);
-            }
-        } else if (NT > 0) {
+        } else {
             // ---- products: the whole warp walks along, one lane issues
             const uint32_t ring16 = (ring & 0x3FFFFu) >> 4, base16 = (base & 0x3FFFFu) >> 4;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const bool one = rw_elect();
+            int done = 0, nq = 0, np[2] = {0, 0};   // fills, Qs, and tiles of P, of the items before
+            auto release = [&](int n) {
+                if (one) rw_commit(&b_empty[(done + n) % ST]);
+            };
             auto qk = [&](int s, int i) {
-                const int n = fill_of_k(i), st = n % ST;
+                const int n = done + fill_of_k(i), st = n % ST;
                 wait(&b_full[st], n / ST);
                 rw_after();
                 const uint32_t k = ring16 + st * (Z::tile >> 4), q = base16 + (QT == 2 ? s * (Z::tile >> 4) : 0);
@@ -405,12 +457,12 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                 }
             };
             auto pv = [&](int s, int i, bool add) {
-                const int n = fill_of_v(i), st = n % ST;
+                const int n = done + fill_of_v(i, it.NT), st = n % ST;
                 wait(&b_full[st], n / ST);
                 const uint32_t v = ring16 + st * (Z::tile >> 4), p = tm + s * 128;
 #pragma unroll
                 for (int k = 0; k < Z::parts; ++k) {   // as the parts of P come
-                    wait(&b_p[s][k], Z::split ? i >> 1 : i);
+                    wait(&b_p[s][k], np[s]);
                     rw_after();
                     if (one) {
 #pragma unroll
@@ -424,244 +476,370 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                         }
                     }
                 }
+                ++np[s];
             };
-            auto done = [&](uint64_t *bar) {
+            auto commit = [&](uint64_t *bar) {
                 if (one) rw_commit(bar);
             };
-            wait(&b_q, 0);
-            if constexpr (!Z::split) {
-                for (int s = 0; s < row_tiles; ++s) qk(s, 0);
-                done(&b_empty[0]);
-                for (int i = 0; i < NT; ++i) {
-                    for (int s = 0; s < row_tiles; ++s) {
-                        pv(s, i, i > 0);
-                        if (i + 1 < NT) qk(s, i + 1);
-                        else done(&b_o[s]);
+            for (int k = 0; item(k, f, it); ++k) {
+                const int NT = it.NT;
+                if (NT == 0) continue;
+                if (*err) break;
+                wait(&b_q, nq++);
+                if constexpr (!Z::split) {
+                    const int two = it.tokens > r.TT ? 2 : 1;
+                    for (int s = 0; s < two; ++s) qk(s, 0);
+                    if (NT == 1) commit(&b_q_free);
+                    release(0);
+                    for (int i = 0; i < NT; ++i) {
+                        for (int s = 0; s < two; ++s) {
+                            pv(s, i, i > 0);
+                            if (i + 1 < NT) qk(s, i + 1);
+                            else commit(&b_o[s]);
+                        }
+                        if (i + 2 == NT) commit(&b_q_free);   // (its last scores)
+                        release(fill_of_v(i, NT));
+                        if (i + 1 < NT) release(fill_of_k(i + 1));
                     }
-                    done(&b_empty[fill_of_v(i) % ST]);
-                    if (i + 1 < NT) done(&b_empty[fill_of_k(i + 1) % ST]);
-                }
-            } else {
-                for (int i = 0; i < min(2, NT); ++i) {
-                    qk(i, i);
-                    done(&b_empty[fill_of_k(i) % ST]);
-                }
-                for (int i = 0; i < NT; ++i) {
-                    pv(i & 1, i, false);
-                    done(&b_empty[fill_of_v(i) % ST]);
-                    if (i + 2 < NT) {
-                        qk(i & 1, i + 2);
-                        done(&b_empty[fill_of_k(i + 2) % ST]);
-                    } else {
-                        done(&b_o[i & 1]);
+                } else {
+                    for (int i = 0; i < min(2, NT); ++i) {
+                        qk(i, i);
+                        release(fill_of_k(i));
+                    }
+                    for (int i = 0; i < NT; ++i) {
+                        pv(i & 1, i, false);
+                        release(fill_of_v(i, NT));
+                        if (i + 2 < NT) {
+                            qk(i & 1, i + 2);
+                            release(fill_of_k(i + 2));
+                        } else {
+                            commit(&b_o[i & 1]);
+                        }
                     }
                 }
+                done += 2 * NT;
             }
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        // ---- Q to shared memory: L lanes to a row, PW rows to a warp at once, NB passes whose loads all come before the stores
-        {
-            constexpr int L = HD / 8, PW = 32 / L, NB = QT * kRwRows / (8 * PW);
-            const int ch = lane % L;
-            const int row0 = warp * PW + lane / L;
-            {
-                uint4 x[NB], y[Z::split ? NB : 1];
-#pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    const int row = row0 + n * 8 * PW, rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;
-                    const bool real = rr < r.TT * r.G && tok < tokens;
-                    const T *q = static_cast<const T *>(a.q) + static_cast<size_t>(u.start + u.tok0 + (real ? tok : 0)) * a.q_stride +
-                                 static_cast<size_t>(g * r.G + (real ? rr % r.G : 0)) * HD + ch * 8;
-                    x[n] = real ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
-                    if constexpr (Z::split) y[n] = real ? *reinterpret_cast<const uint4 *>(q + 4) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    const int row = row0 + n * 8 * PW, rr = row % kRwRows;
-                    uint8_t *to = smem + (ch >> 3) * (kRwRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-                    if constexpr (Z::split) {
-                        float v[8] = {__uint_as_float(x[n].x), __uint_as_float(x[n].y), __uint_as_float(x[n].z), __uint_as_float(x[n].w),
-                                      __uint_as_float(y[n].x), __uint_as_float(y[n].y), __uint_as_float(y[n].z), __uint_as_float(y[n].w)};
-                        float amax = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
-#pragma unroll
-                        for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                        // the power of two that takes the row's largest into [2^14, 2^15)
-                        const int ex = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23 & 0xffu));
-                        const float up = pow2_f32(ex) * sign;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= up;
-                        uint4 hi, lo;
-                        split8_f16(v, hi, lo);
-                        *reinterpret_cast<uint4 *>(to) = hi;
-                        *reinterpret_cast<uint4 *>(to + Z::tile) = lo;
-                        if (ch == 0) s_c[rr] = pow2_f32(-ex) * c0;
-                    } else {
-                        if (sign != 1.0f) {
-                            const __half2 f = __float2half2_rn(sign);
-                            __half2 *h = reinterpret_cast<__half2 *>(&x[n]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f);
-                        }
-                        *reinterpret_cast<uint4 *>(to + (row / kRwRows) * Z::tile) = x[n];
-                    }
-                }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(&b_q);
-            if constexpr (Z::split) rw_bar<256>(1);   // (s_c)
-        }
         // ---- softmax: warpgroup s, a thread to a row
         const int s = warp >> 2, rr = tid & 127;
-        const int tok = (QT == 2 ? s * r.TT : 0) + rr / r.G;
-        const bool real = rr < r.TT * r.G && tok < tokens;
-        const int p = pmin + min(tok, tokens - 1);
-        // the rows of this warpgroup's tile
-        const int smin = QT == 2 ? min(pmin + s * r.TT, pmax) : pmin, smax = QT == 2 ? min(smin + r.TT - 1, pmax) : pmax;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + s * 128, tO = tmem + lanes + 256 + s * HD;
-        const float c = Z::split ? s_c[rr] : c0;
         constexpr float kOff = Z::split ? kRwOff32 : kRwOff16;
-        float m = -INFINITY, l = 0.0f;   // reference (a score before c), sum of weights
-        float master[Z::split ? HD : 1];
-        if constexpr (Z::split) {
-#pragma unroll
-            for (int d = 0; d < HD; ++d) master[d] = 0.0f;
-        }
-        const bool active = QT == 1 || s < row_tiles;
-        int own = 0;   // tiles taken
         constexpr int kStep = Z::split ? 2 : 1;
-        // which 16 positions of a tile have a page (lanes 0..7 look, a tile ahead)
-        auto look = [&](int i) {
-            const int j = tiles.key(i0 + i) + 16 * (lane & 7);
-            return j > pmax || kv_page(a.b, a.c, u.seq, j) >= 0;
-        };
-        bool there = active && NT > (Z::split ? s : 0) && look(Z::split ? s : 0);
-        for (int i = Z::split ? s : 0; active && i < NT; i += kStep, ++own) {
-            const int j0 = tiles.key(i0 + i);
-            const uint32_t pages = __ballot_sync(0xffffffffu, there) & 0xffu;
-            const bool holes = pages != 0xffu;
-            if (i + kStep < NT) there = look(i + kStep);
-            // does every row of the tile see every position?
-            const bool open = !holes && j0 + kRwKeys - 1 <= smin && (a.window == 0 || smax - j0 < a.window || j0 + kRwKeys <= a.sinks);
-            if (!open) {
-                // V: this thread's position
-                const int n = fill_of_v(i), st = n % ST, j = j0 + rr;
-                const bool page = pages >> (rr >> 4) & 1;
-                const bool any = page && j <= pmax && kv_sees(max(j, pmin), j, a.window, a.sinks);
-                const bool all = page && j <= smin && kv_sees(smax, j, a.window, a.sinks);
-                wait(&b_full[st], n / ST);
-                uint8_t *v = smem + (2 + st) * Z::tile + rr * 128;
-                bool bad = false;
-                if (!all) {
+        RwFind f;
+        RwItem it;
+        int done = 0, ns = 0, no = 0;   // fills, tiles of S, outputs, of the items before
+        int turn = 0;                   // this item's flag
+        for (int k = 0; item(k, f, it); ++k) {
+            const int NT = it.NT, tokens = it.tokens, pmin = it.pmin, pmax = it.pmax;
+            if (it.part >= it.parts) continue;
+            // (an error ends the waits, not this loop: the barriers below need every thread)
+            int *const bad_flag = &s_bad[Z::split ? 0 : s][turn];
+            const int turn_next = turn == 2 ? 0 : turn + 1;
+            turn = turn_next;
+            float *const dst = it.parts == 1 ? nullptr
+                                             : r.ws + static_cast<size_t>(r.units) * 4 +
+                                                   (static_cast<size_t>(it.unit) * r.splits + it.part) * (QT * kRwRows) * Z::part;
+            // the output of row x of a row tile, or null
+            auto row_of = [&](int x, int tile) {
+                const int tk = (QT == 2 ? tile * r.TT : 0) + x / r.G;
+                return x < r.TT * r.G && tk < tokens ? static_cast<T *>(a.out) + static_cast<size_t>(it.u.start + it.u.tok0 + tk) * a.out_stride +
+                                                           static_cast<size_t>(it.g * r.G + x % r.G) * HD
+                                                     : nullptr;
+            };
+            if constexpr (Z::split) {
+                // ---- Q to shared memory: L lanes to a row, PW rows to a warp at once, all loads before the stores
+                constexpr int L = HD / 8, PW = 32 / L, NB = kRwRows / (8 * PW);
+                const int ch = lane % L, row0 = warp * PW + lane / L;
+                uint4 x[NB], y[NB];
 #pragma unroll
-                    for (int h = 0; h < HD / 64; ++h)
+                for (int n = 0; n < NB; ++n) {
+                    const int row = row0 + n * 8 * PW, tk = row / r.G;
+                    const bool real = row < r.TT * r.G && tk < tokens;
+                    const T *q = static_cast<const T *>(a.q) + static_cast<size_t>(it.u.start + it.u.tok0 + (real ? tk : 0)) * a.q_stride +
+                                 static_cast<size_t>(it.g * r.G + (real ? row % r.G : 0)) * HD + ch * 8;
+                    x[n] = real ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
+                    y[n] = real ? *reinterpret_cast<const uint4 *>(q + 4) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            uint4 *at = reinterpret_cast<uint4 *>(v + h * (kRwKeys * 128) + ((e ^ (lane & 7)) << 4));
-                            if (!any) {
-                                *at = make_uint4(0, 0, 0, 0);
-                            } else {
-                                const uint4 x = *at;
-                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                for (int n = 0; n < NB; ++n) {
+                    const int row = row0 + n * 8 * PW;
+                    uint8_t *to = smem + (ch >> 3) * (kRwRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+                    float v[8] = {__uint_as_float(x[n].x), __uint_as_float(x[n].y), __uint_as_float(x[n].z), __uint_as_float(x[n].w),
+                                  __uint_as_float(y[n].x), __uint_as_float(y[n].y), __uint_as_float(y[n].z), __uint_as_float(y[n].w)};
+                    float amax = 0.0f;
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7c00u) == 0x7c00u || (w[k] & 0x7c000000u) == 0x7c000000u;
+                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+#pragma unroll
+                    for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    // the power of two that takes the row's largest into [2^14, 2^15)
+                    const int ex = min(126, 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23 & 0xffu));
+                    const float up = pow2_f32(ex) * sign;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= up;
+                    uint4 hi, lo;
+                    split8_f16(v, hi, lo);
+                    *reinterpret_cast<uint4 *>(to) = hi;
+                    *reinterpret_cast<uint4 *>(to + Z::tile) = lo;
+                    if (ch == 0) s_c[row] = pow2_f32(-ex) * c0;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (NT > 0) mbar_arrive(&b_q);
+                rw_bar<256>(1);   // (s_c)
+            }
+            const int tok = (QT == 2 ? s * r.TT : 0) + rr / r.G;
+            const int p = pmin + min(tok, tokens - 1);
+            // the rows of this warpgroup's tile
+            const int smin = QT == 2 ? min(pmin + s * r.TT, pmax) : pmin, smax = QT == 2 ? min(smin + r.TT - 1, pmax) : pmax;
+            const float c = Z::split ? s_c[rr] : c0;
+            float m = -INFINITY, l = 0.0f;   // reference (a score before c), sum of weights
+            float master[Z::split ? HD : 1];
+            if constexpr (Z::split) {
+#pragma unroll
+                for (int d = 0; d < HD; ++d) master[d] = 0.0f;
+            }
+            const bool active = QT == 1 || s == 0 || tokens > r.TT;
+            // which 16 positions of a tile have a page (lanes 0..7 look, a tile ahead)
+            auto look = [&](int i) {
+                const int j = it.tiles.key(it.i0 + i) + 16 * (lane & 7);
+                return j > pmax || kv_page(a.b, a.c, it.u.seq, j) >= 0;
+            };
+            const int first = Z::split ? s : 0;
+            bool there = active && NT > first && look(first);
+            int own = 0;   // tiles taken
+            for (int i = first; active && i < NT; i += kStep, ++own) {
+                const int j0 = it.tiles.key(it.i0 + i);
+                const uint32_t pages = __ballot_sync(0xffffffffu, there) & 0xffu;
+                const bool holes = pages != 0xffu;
+                if (i + kStep < NT) there = look(i + kStep);
+                // does every row of the tile see every position?
+                const bool open = !holes && j0 + kRwKeys - 1 <= smin && (a.window == 0 || smax - j0 < a.window || j0 + kRwKeys <= a.sinks);
+                if (!open) {
+                    // V: this thread's position
+                    const int n = done + fill_of_v(i, NT), st = n % ST, j = j0 + rr;
+                    const bool page = pages >> (rr >> 4) & 1;
+                    const bool any = page && j <= pmax && kv_sees(max(j, pmin), j, a.window, a.sinks);
+                    const bool all = page && j <= smin && kv_sees(smax, j, a.window, a.sinks);
+                    wait(&b_full[st], n / ST);
+                    uint8_t *v = smem + (2 + st) * Z::tile + rr * 128;
+                    bool bad = false;
+                    if (!all) {
+#pragma unroll
+                        for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                uint4 *at = reinterpret_cast<uint4 *>(v + h * (kRwKeys * 128) + ((e ^ (lane & 7)) << 4));
+                                if (!any) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    const uint4 x = *at;
+                                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) bad |= (w[q] & 0x7c00u) == 0x7c00u || (w[q] & 0x7c000000u) == 0x7c000000u;
+                                }
+                            }
+                    }
+                    if (bad) *bad_flag = 1;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                wait(&b_s[s], ns + own);
+                rw_after();
+                // the row's positions j0 + k, k in [k_lo, k_hi) or [0, k_sink), of pages that are there: bits of 32 positions
+                const int k_hi = p - j0 + 1, k_lo = a.window > 0 ? p - a.window + 1 - j0 : 0, k_sink = a.window > 0 ? a.sinks - j0 : 0;
+                auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
+                auto sees = [&](int k0) {
+                    const uint32_t held = (pages >> (k0 >> 4) & 1 ? 0xffffu : 0u) | (pages >> ((k0 >> 4) + 1) & 1 ? 0xffff0000u : 0u);
+                    return held & below(k_hi - k0) & (~below(k_lo - k0) | below(k_sink - k0));
+                };
+                if constexpr (!Z::split) {
+                    uint32_t v[128];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) rw_ld32(tS + 32 * q, v + 32 * q);
+                    rw_wait_ld();
+                    if (sign != 1.0f) {
+#pragma unroll
+                        for (int q = 0; q < 128; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * sign);
+                    }
+                    if (!open) {
+#pragma unroll
+                        for (int k0 = 0; k0 < 128; k0 += 32) {
+                            const uint32_t bits = sees(k0);
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) v[k0 + q] = bits >> q & 1 ? v[k0 + q] : 0xff800000u;
+                        }
+                    }
+                    float mx8[8];   // (chains of their own)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) mx8[q] = __uint_as_float(v[q]);
+#pragma unroll
+                    for (int q = 8; q < 128; ++q) mx8[q & 7] = fmaxf(mx8[q & 7], __uint_as_float(v[q]));
+                    const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])), fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                    const bool far = m == -INFINITY ? mx > -INFINITY : (mx - m) * c > kRwLazy;
+                    if (__any_sync(0xffffffffu, far)) {
+                        const float mn = far ? mx : m, fac = m == mn ? 1.0f : m == -INFINITY ? 0.0f : rw_ex2((m - mn) * c);
+                        m = mn;
+                        l *= fac;
+                        if (own > 0) {
+#pragma unroll 1
+                            for (int d = 0; d < HD; d += 32) {
+                                uint32_t o[32];
+                                rw_ld32(tO + d, o);
+                                rw_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
+                                rw_st32(tO + d, o);
                             }
                         }
-                }
-                if (bad) s_bad = 1;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            wait(&b_s[s], own);
-            rw_after();
-            // the row's positions j0 + k, k in [k_lo, k_hi) or [0, k_sink), of pages that are there: bits of 32 positions
-            const int k_hi = p - j0 + 1, k_lo = a.window > 0 ? p - a.window + 1 - j0 : 0, k_sink = a.window > 0 ? a.sinks - j0 : 0;
-            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
-            auto sees = [&](int k0) {
-                const uint32_t held = (pages >> (k0 >> 4) & 1 ? 0xffffu : 0u) | (pages >> ((k0 >> 4) + 1) & 1 ? 0xffff0000u : 0u);
-                return held & below(k_hi - k0) & (~below(k_lo - k0) | below(k_sink - k0));
-            };
-            if constexpr (!Z::split) {
-                uint32_t v[128];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) rw_ld32(tS + 32 * k, v + 32 * k);
-                rw_wait_ld();
-                if (!open) {
-#pragma unroll
-                    for (int k0 = 0; k0 < 128; k0 += 32) {
-                        const uint32_t bits = sees(k0);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k0 + k] = bits >> k & 1 ? v[k0 + k] : 0xff800000u;
                     }
-                }
-                float mx8[8];   // (chains of their own)
+                    const float b = (m == -INFINITY ? 0.0f : m * c) - kOff;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(v[k]);
+                    for (int h = 0; h < Z::parts; ++h) {
 #pragma unroll
-                for (int k = 8; k < 128; ++k) mx8[k & 7] = fmaxf(mx8[k & 7], __uint_as_float(v[k]));
-                const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])), fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-                const bool far = m == -INFINITY ? mx > -INFINITY : (mx - m) * c > kRwLazy;
-                if (__any_sync(0xffffffffu, far)) {
-                    const float mn = far ? mx : m, f = m == mn ? 1.0f : m == -INFINITY ? 0.0f : rw_ex2((m - mn) * c);
-                    m = mn;
-                    l *= f;
+                        for (int kk = 0; kk < Z::part_keys; kk += 2) {
+                            const int q = h * Z::part_keys + kk;
+                            const float x = rw_ex2(fmaf(__uint_as_float(v[q]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[q + 1]), c, -b));
+                            sum[q >> 1 & 1] += x;
+                            sum[2 + (q >> 1 & 1)] += y;
+                            v[q >> 1] = rw_pack(x, y);
+                        }
+                        rw_st32(tS + 32 * h, v + 32 * h);
+                        rw_wait_st();
+                        rw_before();
+                        mbar_arrive(&b_p[s][h]);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                } else {
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k0 = 0; k0 < 128; k0 += 64) {
+                        uint32_t v[64];
+                        rw_ld32(tS + k0, v);
+                        rw_ld32(tS + k0 + 32, v + 32);
+                        rw_wait_ld();
+                        if (!open) {   // what the row does not see is -inf from here on
+#pragma unroll
+                            for (int h = 0; h < 64; h += 32) {
+                                const uint32_t bits = sees(k0 + h);
+#pragma unroll
+                                for (int q = 0; q < 32; ++q) v[h + q] = bits >> q & 1 ? v[h + q] : 0xff800000u;
+                                rw_st32(tS + k0 + h, v + h);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < 64; ++q) mx4[q & 3] = fmaxf(mx4[q & 3], __uint_as_float(v[q]));
+                    }
+                    if (!open) rw_wait_st();
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                    const float mn = fmaxf(m, mx), fac = m == mn ? 1.0f : rw_ex2((m - mn) * c);
+                    // the O of this warpgroup's last tile, beside the old reference
                     if (own > 0) {
-#pragma unroll 1
+#pragma unroll
                         for (int d = 0; d < HD; d += 32) {
                             uint32_t o[32];
                             rw_ld32(tO + d, o);
                             rw_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            rw_st32(tO + d, o);
+                            for (int e = 0; e < 32; ++e) master[d + e] = (master[d + e] + __uint_as_float(o[e])) * fac;
                         }
                     }
-                }
-                const float b = (m == -INFINITY ? 0.0f : m * c) - kOff;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    m = mn;
+                    l *= fac;
+                    const float b = (m == -INFINITY ? 0.0f : m * c) - kOff;
+                    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int h = 0; h < Z::parts; ++h) {
+                    for (int k0 = 0; k0 < 128; k0 += 32) {
+                        uint32_t v[32], w[32];
+                        rw_ld32(tS + k0, v);
+                        rw_wait_ld();
 #pragma unroll
-                    for (int kk = 0; kk < Z::part_keys; kk += 2) {
-                        const int k = h * Z::part_keys + kk;
-                        const float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
-                        sum[k >> 1 & 1] += x;
-                        sum[2 + (k >> 1 & 1)] += y;
-                        v[k >> 1] = rw_pack(x, y);
+                        for (int q = 0; q < 32; q += 2) {
+                            const float x = rw_ex2(fmaf(__uint_as_float(v[q]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[q + 1]), c, -b));
+                            sum[0] += x;
+                            sum[1] += y;
+                            const uint32_t hi = rw_pack(x, y);
+                            const float2 h = rw_unpack(hi);
+                            w[q >> 1] = hi;
+                            w[16 + (q >> 1)] = rw_pack(x - h.x, y - h.y);
+                        }
+                        rw_st32(tS + k0, w);
+                        if ((k0 + 32) % Z::part_keys == 0) {
+                            rw_wait_st();
+                            rw_before();
+                            mbar_arrive(&b_p[s][k0 / Z::part_keys]);
+                        }
                     }
-                    rw_st32(tS + 32 * h, v + 32 * h);
-                    rw_wait_st();
-                    rw_before();
-                    mbar_arrive(&b_p[s][h]);
+                    l += sum[0] + sum[1];
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            }
+            if (own > 0) {
+                wait(&b_o[s], no++);
+                rw_after();
+            }
+            ns += own;
+            done += 2 * NT;
+            const float m2 = m == -INFINITY ? -INFINITY : m * c;   // the reference in base 2
+            // Rows go out through shared memory, so that each is written in runs of whole lines.
+            if constexpr (!Z::split) {
+                // (three flags by turns: the one that is set to 0 here was read two items ago, and is next used after the barrier)
+                if (rr == 0) s_bad[s][turn_next] = 0;
+                rw_bar<128>(2 + s);
+                const bool bad = *bad_flag;
+                if (!bad && active) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    uint8_t *const place = smem + (2 + ST) * Z::tile + s * Z::out;
+                    float *const part_rows = dst ? dst + static_cast<size_t>(s * kRwRows) * Z::part : nullptr;
+                    // 128 bytes of a row at a time: 64 values of f16, 32 of a part
+                    const int width = dst ? 32 : 64;
+#pragma unroll 1
+                    for (int d0 = 0; d0 < HD; d0 += width) {
+#pragma unroll
+                        for (int d = 0; d < 64; d += 32) {
+                            if (d >= width) break;
+                            uint32_t o[32];
+                            rw_ld32(tO + d0 + d, o);
+                            rw_wait_ld();
+                            if (own == 0) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = 0;
+                            }
+                            if (dst) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<uint4 *>(place + rr * 128 + (((e / 4) ^ (rr & 7)) << 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8) {
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        w[q] = rw_pack(__uint_as_float(o[e + 2 * q]) * inv, __uint_as_float(o[e + 2 * q + 1]) * inv);
+                                    *reinterpret_cast<uint4 *>(place + rr * 128 + ((((d + e) / 8) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                        }
+                        rw_bar<128>(2 + s);
+#pragma unroll 4
+                        for (int q = rr; q < kRwRows * 8; q += 128) {
+                            const int x = q >> 3, ch = q & 7;
+                            uint8_t *to = dst ? reinterpret_cast<uint8_t *>(part_rows + static_cast<size_t>(x) * Z::part + d0)
+                                              : reinterpret_cast<uint8_t *>(row_of(x, s));
+                            if (to)
+                                *reinterpret_cast<uint4 *>(to + (dst ? 0 : d0 * 2) + ch * 16) =
+                                    *reinterpret_cast<const uint4 *>(place + x * 128 + ((ch ^ (x & 7)) << 4));
+                        }
+                        rw_bar<128>(2 + s);
+                    }
+                    if (dst) {
+                        part_rows[static_cast<size_t>(rr) * Z::part + HD] = m2;
+                        part_rows[static_cast<size_t>(rr) * Z::part + HD + 1] = l;
+                    }
+                }
+                if (bad) rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, s * kRwRows, (s + 1) * kRwRows, warp & 3, 4, kOff, dst);
             } else {
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k0 = 0; k0 < 128; k0 += 64) {
-                    uint32_t v[64];
-                    rw_ld32(tS + k0, v);
-                    rw_ld32(tS + k0 + 32, v + 32);
-                    rw_wait_ld();
-                    if (!open) {   // what the row does not see is -inf from here on
-#pragma unroll
-                        for (int h = 0; h < 64; h += 32) {
-                            const uint32_t bits = sees(k0 + h);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) v[h + k] = bits >> k & 1 ? v[h + k] : 0xff800000u;
-                            rw_st32(tS + k0 + h, v + h);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 64; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[k]));
-                }
-                if (!open) rw_wait_st();
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                const float mn = fmaxf(m, mx), f = m == mn ? 1.0f : rw_ex2((m - mn) * c);
-                // the O of this warpgroup's last tile, beside the old reference
                 if (own > 0) {
 #pragma unroll
                     for (int d = 0; d < HD; d += 32) {
@@ -669,168 +847,64 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_paged_rows(const RwArgs r, co
                         rw_ld32(tO + d, o);
                         rw_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) master[d + e] = (master[d + e] + __uint_as_float(o[e])) * f;
+                        for (int e = 0; e < 32; ++e) master[d + e] += __uint_as_float(o[e]);
                     }
                 }
-                m = mn;
-                l *= f;
-                const float b = (m == -INFINITY ? 0.0f : m * c) - kOff;
-                float sum[2] = {0.0f, 0.0f};
+                // the second warpgroup's part joins the first one's, in Q's place (every score is there: Q is done with);
+                // chunk c of 16 bytes of row x at c + x
+                constexpr int C = HD / 4;
+                float4 *const place = reinterpret_cast<float4 *>(smem);
+                if (s == 1 && NT > 1) {
 #pragma unroll
-                for (int k0 = 0; k0 < 128; k0 += 32) {
-                    uint32_t v[32], w[32];
-                    rw_ld32(tS + k0, v);
-                    rw_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const float x = rw_ex2(fmaf(__uint_as_float(v[k]), c, -b)), y = rw_ex2(fmaf(__uint_as_float(v[k + 1]), c, -b));
-                        sum[0] += x;
-                        sum[1] += y;
-                        const uint32_t hi = rw_pack(x, y);
-                        const float2 h = rw_unpack(hi);
-                        w[k >> 1] = hi;
-                        w[16 + (k >> 1)] = rw_pack(x - h.x, y - h.y);
-                    }
-                    rw_st32(tS + k0, w);
-                    if ((k0 + 32) % Z::part_keys == 0) {
-                        rw_wait_st();
-                        rw_before();
-                        mbar_arrive(&b_p[s][k0 / Z::part_keys]);
-                    }
+                    for (int d = 0; d < HD; d += 4)
+                        place[rr * C + ((d / 4 + rr) & (C - 1))] = make_float4(master[d], master[d + 1], master[d + 2], master[d + 3]);
+                    s_ml[0][rr] = m2;
+                    s_ml[1][rr] = l;
                 }
-                l += sum[0] + sum[1];
-            }
-        }
-        if (active && own > 0) {
-            wait(&b_o[s], 0);
-            rw_after();
-        }
-        const float m2 = m == -INFINITY ? -INFINITY : m * c;   // the reference in base 2
-        // Rows go out through shared memory (Q's place: every score is there), so that each is written in one run of
-        // whole lines. N threads, from t on; C chunks of 16 bytes to a row, chunk c of row x at (c ^ x) or (c + x).
-        auto row_of = [&](int x, int tile) {   // the output of row x of a row tile, or null
-            const int k = (QT == 2 ? tile * r.TT : 0) + x / r.G;
-            return x < r.TT * r.G && k < tokens ? static_cast<T *>(a.out) + static_cast<size_t>(u.start + u.tok0 + k) * a.out_stride +
-                                                      static_cast<size_t>(g * r.G + x % r.G) * HD
-                                                : nullptr;
-        };
-        if constexpr (!Z::split) {
-            rw_bar<256>(1);
-            if (!s_bad && active) {
-                // (NT = 0: no position, zeros)
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                uint8_t *const place = smem + s * Z::tile;
-                constexpr int C = HD / 8;
-                if (!dst) {
+                if (tid == 0) s_bad[0][turn_next] = 0;
+                rw_bar<256>(1);
+                const bool bad = *bad_flag;
+                if (!bad) {
+                    if (s == 0) {
+                        const bool two = NT > 1;
+                        const float mo = two ? s_ml[0][rr] : m2, lo = two ? s_ml[1][rr] : 0.0f, top = fmaxf(m2, mo);
+                        const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = mo == top ? 1.0f : rw_ex2(mo - top);
+                        const float sum = l * f0 + lo * f1, inv = dst ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-                    for (int d = 0; d < HD; d += 32) {
-                        uint32_t o[32];
-                        rw_ld32(tO + d, o);
-                        rw_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = rw_pack(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                            const int ch = (d + e) / 8;
-                            *reinterpret_cast<uint4 *>(place + rr * (HD * 2) + ((ch ^ (rr & 7)) << 4)) =
-                                own > 0 ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+                        for (int d = 0; d < HD; d += 4) {
+                            float4 *at = place + rr * C + ((d / 4 + rr) & (C - 1));
+                            float4 x = two ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            const float fo = two ? f1 : 0.0f;
+                            x.x = (master[d] * f0 + x.x * fo) * inv;
+                            x.y = (master[d + 1] * f0 + x.y * fo) * inv;
+                            x.z = (master[d + 2] * f0 + x.z * fo) * inv;
+                            x.w = (master[d + 3] * f0 + x.w * fo) * inv;
+                            *at = x;
+                        }
+                        if (dst) {
+                            dst[static_cast<size_t>(rr) * Z::part + HD] = top;
+                            dst[static_cast<size_t>(rr) * Z::part + HD + 1] = sum;
                         }
                     }
-                    rw_bar<128>(2 + s);
+                    rw_bar<256>(1);
 #pragma unroll 4
-                    for (int k = rr; k < kRwRows * C; k += 128) {
-                        const int x = k / C, ch = k % C;
-                        T *to = row_of(x, s);
-                        if (to) *reinterpret_cast<uint4 *>(to + ch * 8) = *reinterpret_cast<const uint4 *>(place + x * (HD * 2) + ((ch ^ (x & 7)) << 4));
+                    for (int q = tid; q < kRwRows * C; q += 256) {
+                        const int x = q / C, ch = q % C;
+                        float *to = dst ? dst + static_cast<size_t>(x) * Z::part : reinterpret_cast<float *>(row_of(x, 0));
+                        if (to) *reinterpret_cast<float4 *>(to + ch * 4) = place[x * C + ((ch + x) & (C - 1))];
                     }
                 } else {
-                    float *const part_rows = dst + static_cast<size_t>(s * kRwRows) * Z::part;
-#pragma unroll 1
-                    for (int d0 = 0; d0 < HD; d0 += HD / 2) {   // f32: half of the dimensions at a time
-#pragma unroll
-                        for (int d = 0; d < HD / 2; d += 32) {
-                            uint32_t o[32];
-                            rw_ld32(tO + d0 + d, o);
-                            rw_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4 *>(place + rr * (HD * 2) + ((((d + e) / 4) ^ (rr & 7)) << 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                        }
-                        rw_bar<128>(2 + s);
-#pragma unroll 4
-                        for (int k = rr; k < kRwRows * C; k += 128) {
-                            const int x = k / C, ch = k % C;
-                            *reinterpret_cast<uint4 *>(part_rows + static_cast<size_t>(x) * Z::part + d0 + ch * 4) =
-                                *reinterpret_cast<const uint4 *>(place + x * (HD * 2) + ((ch ^ (x & 7)) << 4));
-                        }
-                        rw_bar<128>(2 + s);
-                    }
-                    part_rows[static_cast<size_t>(rr) * Z::part + HD] = m2;
-                    part_rows[static_cast<size_t>(rr) * Z::part + HD + 1] = l;
+                    rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, 0, kRwRows, warp, 8, kOff, dst);
                 }
-            }
-        } else {
-            if (own > 0) {
-#pragma unroll
-                for (int d = 0; d < HD; d += 32) {
-                    uint32_t o[32];
-                    rw_ld32(tO + d, o);
-                    rw_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) master[d + e] += __uint_as_float(o[e]);
-                }
-            }
-            // the second warpgroup's part joins the first one's
-            constexpr int C = HD / 4;
-            float4 *const place = reinterpret_cast<float4 *>(smem);
-            if (s == 1 && NT > 1) {
-#pragma unroll
-                for (int d = 0; d < HD; d += 4)
-                    place[rr * C + ((d / 4 + rr) & (C - 1))] = make_float4(master[d], master[d + 1], master[d + 2], master[d + 3]);
-                s_ml[0][rr] = m2;
-                s_ml[1][rr] = l;
-            }
-            rw_bar<256>(1);
-            if (!s_bad) {
-                if (s == 0) {
-                    const bool two = NT > 1;
-                    const float mo = two ? s_ml[0][rr] : m2, lo = two ? s_ml[1][rr] : 0.0f, top = fmaxf(m2, mo);
-                    const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = mo == top ? 1.0f : rw_ex2(mo - top);
-                    const float sum = l * f0 + lo * f1, inv = dst ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-                    for (int d = 0; d < HD; d += 4) {
-                        float4 *at = place + rr * C + ((d / 4 + rr) & (C - 1));
-                        float4 x = two ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        const float f = two ? f1 : 0.0f;
-                        x.x = (master[d] * f0 + x.x * f) * inv;
-                        x.y = (master[d + 1] * f0 + x.y * f) * inv;
-                        x.z = (master[d + 2] * f0 + x.z * f) * inv;
-                        x.w = (master[d + 3] * f0 + x.w * f) * inv;
-                        *at = x;
-                    }
-                    if (dst) {
-                        dst[static_cast<size_t>(rr) * Z::part + HD] = top;
-                        dst[static_cast<size_t>(rr) * Z::part + HD + 1] = sum;
-                    }
-                }
-                rw_bar<256>(1);
-#pragma unroll 4
-                for (int k = tid; k < kRwRows * C; k += 256) {
-                    const int x = k / C, ch = k % C;
-                    float *to = dst ? dst + static_cast<size_t>(x) * Z::part : reinterpret_cast<float *>(row_of(x, 0));
-                    if (to) *reinterpret_cast<float4 *>(to + ch * 4) = place[x * C + ((ch + x) & (C - 1))];
-                }
+                rw_bar<256>(1);   // (the next item's Q comes to this place)
             }
         }
-        if (s_bad) rw_slow<T, HD>(r, u, tiles, i0, i1, g, QT * kRwRows, kOff, dst);
         rw_before();
     }
     __syncthreads();
     if (tid == 0 && s_err) record_status(a.status, QW3_ERR_TIMEOUT);
     rw_after();
-    leave();
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // A warp to a row of a unit that was split.
@@ -936,7 +1010,19 @@ cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, floa
     if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.c.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    return launch_pdl(pdl, k_paged_rows<T, HD>, dim3(p.units, p.splits), kRwThreads, Z::smem, 1, s, r, map);
+    // f16: Q of a row tile is a box, 64 values of G heads of TT tokens
+    CUtensorMap qmap = map;
+    if (!Z::split) {
+        const cuuint64_t qdims[3] = {HD, static_cast<cuuint64_t>(a.nh), static_cast<cuuint64_t>(a.b.M)};
+        const cuuint64_t qstrides[2] = {HD * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
+        const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(r.G), static_cast<cuuint32_t>(p.TT)}, qstep[3] = {1, 1, 1};
+        if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(a.q), qdims, qstrides, qbox, qstep,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const int grid = static_cast<int>(std::min<long long>(num_sms(), static_cast<long long>(p.units) * p.splits));
+    return launch_pdl(pdl, k_paged_rows<T, HD>, dim3(grid), kRwThreads, Z::smem, 1, s, r, map, qmap);
 }
 
 template <typename T, int HD>
