@@ -72,6 +72,7 @@ struct RwCut {
 struct RwArgs {
     KvPagedAttnArgs a;
     int G, TT;          // query heads of a kv head, tokens of a row tile
+    int g_inv;          // ceil(2^16 / G): x / G = x g_inv >> 16 for x < 128 (G <= 16: the error x (g_inv - 2^16 / G) 2^-16 is below 1 / G)
     int min_cols;       // sequences with as many columns, or fewer, are others'
     int split_tiles;    // key tiles of a part
     int splits, units;  // parts of a unit, and units, at most
@@ -533,9 +534,17 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         RwItem it;
         int done = 0, ns = 0, no = 0;   // fills, tiles of S, outputs, of the items before
         int turn = 0;                   // this item's flag
-        for (int k = 0; item(k, f, it); ++k) {
+        int k = 0;
+        auto next = [&](RwItem &to) {   // the next item that has a part of its unit
+            while (item(k++, f, to))
+                if (to.part < to.parts) return true;
+            return false;
+        };
+        RwItem ahead;
+        bool more = next(ahead);
+        while (more) {
+            it = ahead;
             const int NT = it.NT, tokens = it.tokens, pmin = it.pmin, pmax = it.pmax;
-            if (it.part >= it.parts) continue;
             // (an error ends the waits, not this loop: the barriers below need every thread)
             int *const bad_flag = &s_bad[Z::split ? 0 : s][turn];
             const int turn_next = turn == 2 ? 0 : turn + 1;
@@ -544,11 +553,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                                              : r.ws + static_cast<size_t>(r.units) * 4 +
                                                    (static_cast<size_t>(it.unit) * r.splits + it.part) * (QT * kRwRows) * Z::part;
             // the output of row x of a row tile, or null
+            const size_t out_row = static_cast<size_t>(a.out_stride);
+            T *const out0 = static_cast<T *>(a.out) + static_cast<size_t>(it.u.start + it.u.tok0) * out_row + static_cast<size_t>(it.g * r.G) * HD;
             auto row_of = [&](int x, int tile) {
-                const int tk = (QT == 2 ? tile * r.TT : 0) + x / r.G;
-                return x < r.TT * r.G && tk < tokens ? static_cast<T *>(a.out) + static_cast<size_t>(it.u.start + it.u.tok0 + tk) * a.out_stride +
-                                                           static_cast<size_t>(it.g * r.G + x % r.G) * HD
-                                                     : nullptr;
+                const int tx = x * r.g_inv >> 16, tk = (QT == 2 ? tile * r.TT : 0) + tx;
+                return x < r.TT * r.G && tk < tokens ? out0 + tk * out_row + (x - tx * r.G) * HD : nullptr;
             };
             if constexpr (Z::split) {
                 // ---- Q to shared memory: L lanes to a row, PW rows to a warp at once, all loads before the stores
@@ -557,10 +566,10 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 uint4 x[NB], y[NB];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const int row = row0 + n * 8 * PW, tk = row / r.G;
+                    const int row = row0 + n * 8 * PW, tk = row * r.g_inv >> 16;
                     const bool real = row < r.TT * r.G && tk < tokens;
                     const T *q = static_cast<const T *>(a.q) + static_cast<size_t>(it.u.start + it.u.tok0 + (real ? tk : 0)) * a.q_stride +
-                                 static_cast<size_t>(it.g * r.G + (real ? row % r.G : 0)) * HD + ch * 8;
+                                 static_cast<size_t>(it.g * r.G + (real ? row - tk * r.G : 0)) * HD + ch * 8;
                     x[n] = real ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
                     y[n] = real ? *reinterpret_cast<const uint4 *>(q + 4) : make_uint4(0, 0, 0, 0);
                 }
@@ -590,7 +599,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 if (NT > 0) mbar_arrive(&b_q);
                 rw_bar<256>(1);   // (s_c)
             }
-            const int tok = (QT == 2 ? s * r.TT : 0) + rr / r.G;
+            const int tok = (QT == 2 ? s * r.TT : 0) + (rr * r.g_inv >> 16);
             const int p = pmin + min(tok, tokens - 1);
             // the rows of this warpgroup's tile
             const int smin = QT == 2 ? min(pmin + s * r.TT, pmax) : pmin, smax = QT == 2 ? min(smin + r.TT - 1, pmax) : pmax;
@@ -775,6 +784,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                     l += sum[0] + sum[1];
                 }
             }
+            more = next(ahead);   // (while the last products are made)
             if (own > 0) {
                 wait(&b_o[s], no++);
                 rw_after();
@@ -997,7 +1007,8 @@ EncodeTiled encode_tiled() {
 template <typename T, int HD>
 cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, float *ws, bool join, bool pdl, cudaStream_t s) {
     using Z = RwSizes<T, HD>;
-    const RwArgs r{a, a.nh / a.c.nkv, p.TT, min_cols, p.split_tiles, p.splits, p.units, ws};
+    const int G = a.nh / a.c.nkv;
+    const RwArgs r{a, G, p.TT, (65536 + G - 1) / G, min_cols, p.split_tiles, p.splits, p.units, ws};
     if (join)
         return p.splits == 1 ? cudaSuccess
                              : launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 4), 128, 0, 1, s, r);
