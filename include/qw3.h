@@ -604,8 +604,7 @@ QW3_API int64_t qw3_kv_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t 
  * that may run at once need a workspace each). Equal calls give equal results.
  * If a bounded wait in a kernel runs out and status_dev is not NULL, *status_dev
  * becomes QW3_ERR_TIMEOUT and the outputs are not valid. q_dev, out_dev 16-byte
- * aligned, q_stride a multiple of head_dim, out_stride of 16 bytes. Asynchronous on
- * `stream`. */
+ * aligned, their strides multiples of head_dim. Asynchronous on `stream`. */
 QW3_API int qw3_kv_paged_attn(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int32_t type, const void *q_dev,
                               int32_t M, int64_t q_stride, int32_t n_heads, int32_t max_rows, int32_t max_len,
                               int32_t window, int32_t sinks, float scale, void *out_dev, int64_t out_stride,

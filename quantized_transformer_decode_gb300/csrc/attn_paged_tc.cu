@@ -165,6 +165,13 @@ __device__ __forceinline__ void rw_tma3(uint32_t to, const CUtensorMap *map, int
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                  ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void rw_tma3_out(const CUtensorMap *map, int x, int y, int z, uint32_t from) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(from) : "memory");
+}
+__device__ __forceinline__ void rw_out_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void rw_out_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }   // its source may change
+__device__ __forceinline__ void rw_out_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void rw_bar(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
 
@@ -282,14 +289,15 @@ struct RwItem {
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kRwThreads, 1)
-    k_paged_rows(const RwArgs r, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap) {
+    k_paged_rows(const RwArgs r, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap qmap,
+                 const __grid_constant__ CUtensorMap omap) {
     using Z = RwSizes<T, HD>;
     constexpr int ST = Z::stages, QT = Z::QT;
     extern __shared__ uint8_t rw_smem[];
     __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q, b_q_free;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err, s_bad[2][3];
-    __shared__ float s_c[kRwRows], s_ml[2][kRwRows];
+    __shared__ float s_c[kRwRows];
     const KvPagedAttnArgs &a = r.a;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the warp's own: uniform branches)
@@ -792,20 +800,38 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             ns += own;
             done += 2 * NT;
             const float m2 = m == -INFINITY ? -INFINITY : m * c;   // the reference in base 2
-            // Rows go out through shared memory, so that each is written in runs of whole lines.
+            // Rows go out through shared memory, 128 bytes of each at a time (chunk c of 16 bytes of row x at c ^ (x & 7),
+            // the tensor maps' swizzle): by TMA where the row tile is full, else, and to the workspace, by the threads.
+            auto copy_out = [&](const uint8_t *place, int rows_of, int d0, int thread, int threads) {
+#pragma unroll 2
+                for (int q = thread; q < kRwRows * 8; q += threads) {
+                    const int x = q >> 3, ch = q & 7;
+                    uint8_t *to = dst ? reinterpret_cast<uint8_t *>(dst + static_cast<size_t>(rows_of * kRwRows + x) * Z::part + d0)
+                                      : reinterpret_cast<uint8_t *>(row_of(x, rows_of));
+                    if (to)
+                        *reinterpret_cast<uint4 *>(to + (dst ? 0 : d0 * static_cast<int>(sizeof(T))) + ch * 16) =
+                            *reinterpret_cast<const uint4 *>(place + x * 128 + ((ch ^ (x & 7)) << 4));
+                }
+            };
             if constexpr (!Z::split) {
                 // (three flags by turns: the one that is set to 0 here was read two items ago, and is next used after the barrier)
-                if (rr == 0) s_bad[s][turn_next] = 0;
+                if (rr == 0) {
+                    s_bad[s][turn_next] = 0;
+                    rw_out_read();   // (the last item's rows have left)
+                }
                 rw_bar<128>(2 + s);
                 const bool bad = *bad_flag;
                 if (!bad && active) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    const bool full = !dst && tokens >= (s + 1) * r.TT;
                     uint8_t *const place = smem + (2 + ST) * Z::tile + s * Z::out;
-                    float *const part_rows = dst ? dst + static_cast<size_t>(s * kRwRows) * Z::part : nullptr;
-                    // 128 bytes of a row at a time: 64 values of f16, 32 of a part
-                    const int width = dst ? 32 : 64;
+                    const int width = dst ? 32 : 64;   // values in 128 bytes
 #pragma unroll 1
                     for (int d0 = 0; d0 < HD; d0 += width) {
+                        if (d0 > 0) {
+                            if (rr == 0) rw_out_read();
+                            rw_bar<128>(2 + s);
+                        }
 #pragma unroll
                         for (int d = 0; d < 64; d += 32) {
                             if (d >= width) break;
@@ -831,21 +857,19 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                                 }
                             }
                         }
+                        if (full) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         rw_bar<128>(2 + s);
-#pragma unroll 4
-                        for (int q = rr; q < kRwRows * 8; q += 128) {
-                            const int x = q >> 3, ch = q & 7;
-                            uint8_t *to = dst ? reinterpret_cast<uint8_t *>(part_rows + static_cast<size_t>(x) * Z::part + d0)
-                                              : reinterpret_cast<uint8_t *>(row_of(x, s));
-                            if (to)
-                                *reinterpret_cast<uint4 *>(to + (dst ? 0 : d0 * 2) + ch * 16) =
-                                    *reinterpret_cast<const uint4 *>(place + x * 128 + ((ch ^ (x & 7)) << 4));
+                        if (!full) {
+                            copy_out(place, s, d0, rr, 128);
+                        } else if (rr == 0) {
+                            rw_tma3_out(&omap, d0, it.g * r.G, it.u.start + it.u.tok0 + s * r.TT, smem_u32(place));
+                            rw_out_commit();
                         }
-                        rw_bar<128>(2 + s);
                     }
                     if (dst) {
-                        part_rows[static_cast<size_t>(rr) * Z::part + HD] = m2;
-                        part_rows[static_cast<size_t>(rr) * Z::part + HD + 1] = l;
+                        float *const to = dst + static_cast<size_t>(s * kRwRows + rr) * Z::part;
+                        to[HD] = m2;
+                        to[HD + 1] = l;
                     }
                 }
                 if (bad) rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, s * kRwRows, (s + 1) * kRwRows, warp & 3, 4, kOff, dst);
@@ -860,48 +884,59 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                         for (int e = 0; e < 32; ++e) master[d + e] += __uint_as_float(o[e]);
                     }
                 }
-                // the second warpgroup's part joins the first one's, in Q's place (every score is there: Q is done with);
-                // chunk c of 16 bytes of row x at c + x
-                constexpr int C = HD / 4;
-                float4 *const place = reinterpret_cast<float4 *>(smem);
-                if (s == 1 && NT > 1) {
-#pragma unroll
-                    for (int d = 0; d < HD; d += 4)
-                        place[rr * C + ((d / 4 + rr) & (C - 1))] = make_float4(master[d], master[d + 1], master[d + 2], master[d + 3]);
-                    s_ml[0][rr] = m2;
-                    s_ml[1][rr] = l;
-                }
+                // The warpgroups' parts join in Q's place: each leaves half of its dimensions to the other, and adds its
+                // other half to what it finds. (Behind the barrier: with one tile the second has waited for nothing, and
+                // Q may still be read before.)
                 if (tid == 0) s_bad[0][turn_next] = 0;
                 rw_bar<256>(1);
                 const bool bad = *bad_flag;
                 if (!bad) {
-                    if (s == 0) {
-                        const bool two = NT > 1;
-                        const float mo = two ? s_ml[0][rr] : m2, lo = two ? s_ml[1][rr] : 0.0f, top = fmaxf(m2, mo);
-                        const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = mo == top ? 1.0f : rw_ex2(mo - top);
-                        const float sum = l * f0 + lo * f1, inv = dst ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-                        for (int d = 0; d < HD; d += 4) {
-                            float4 *at = place + rr * C + ((d / 4 + rr) & (C - 1));
-                            float4 x = two ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            const float fo = two ? f1 : 0.0f;
-                            x.x = (master[d] * f0 + x.x * fo) * inv;
-                            x.y = (master[d + 1] * f0 + x.y * fo) * inv;
-                            x.z = (master[d + 2] * f0 + x.z * fo) * inv;
-                            x.w = (master[d + 3] * f0 + x.w * fo) * inv;
-                            *at = x;
-                        }
-                        if (dst) {
-                            dst[static_cast<size_t>(rr) * Z::part + HD] = top;
-                            dst[static_cast<size_t>(rr) * Z::part + HD + 1] = sum;
-                        }
-                    }
+                    float2 *const ml = reinterpret_cast<float2 *>(smem);
+                    ml[s * kRwRows + rr] = make_float2(m2, l);
                     rw_bar<256>(1);
-#pragma unroll 4
-                    for (int q = tid; q < kRwRows * C; q += 256) {
-                        const int x = q / C, ch = q % C;
-                        float *to = dst ? dst + static_cast<size_t>(x) * Z::part : reinterpret_cast<float *>(row_of(x, 0));
-                        if (to) *reinterpret_cast<float4 *>(to + ch * 4) = place[x * C + ((ch + x) & (C - 1))];
+                    const float2 other = ml[(s ^ 1) * kRwRows + rr];
+                    rw_bar<256>(1);
+                    const float top = fmaxf(m2, other.x);
+                    const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = other.x == top ? 1.0f : rw_ex2(other.x - top);
+                    const float sum = l * f0 + other.y * f1, fac = dst ? f0 : sum == 0.0f ? 0.0f : f0 / sum;
+                    auto at = [&](int d) {
+                        return reinterpret_cast<float4 *>(smem + (d >> 5) * (kRwRows * 128) + rr * 128 + (((d >> 2 & 7) ^ (rr & 7)) << 4));
+                    };
+                    auto leave = [&](int d) { *at(d) = make_float4(master[d] * fac, master[d + 1] * fac, master[d + 2] * fac, master[d + 3] * fac); };
+                    auto join = [&](int d) {
+                        const float4 x = *at(d);
+                        *at(d) = make_float4(fmaf(master[d], fac, x.x), fmaf(master[d + 1], fac, x.y), fmaf(master[d + 2], fac, x.z), fmaf(master[d + 3], fac, x.w));
+                    };
+                    if (s == 0) {
+#pragma unroll
+                        for (int d = HD / 2; d < HD; d += 4) leave(d);
+                        rw_bar<256>(1);
+#pragma unroll
+                        for (int d = 0; d < HD / 2; d += 4) join(d);
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < HD / 2; d += 4) leave(d);
+                        rw_bar<256>(1);
+#pragma unroll
+                        for (int d = HD / 2; d < HD; d += 4) join(d);
+                    }
+                    const bool full = !dst && tokens >= r.TT;
+                    if (full) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    rw_bar<256>(1);
+                    if (!full) {
+#pragma unroll 1
+                        for (int d0 = 0; d0 < HD; d0 += 32) copy_out(smem + (d0 >> 5) * (kRwRows * 128), 0, d0, tid, 256);
+                    } else if (tid == 0) {
+#pragma unroll
+                        for (int d0 = 0; d0 < HD; d0 += 32)
+                            rw_tma3_out(&omap, d0, it.g * r.G, it.u.start + it.u.tok0, base + (d0 >> 5) * (kRwRows * 128));
+                        rw_out_commit();
+                        rw_out_read();
+                    }
+                    if (dst && s == 0) {
+                        float *const to = dst + static_cast<size_t>(rr) * Z::part;
+                        to[HD] = top;
+                        to[HD + 1] = sum;
                     }
                 } else {
                     rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, 0, kRwRows, warp, 8, kOff, dst);
@@ -909,6 +944,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 rw_bar<256>(1);   // (the next item's Q comes to this place)
             }
         }
+        rw_out_done();
         rw_before();
     }
     __syncthreads();
@@ -1021,19 +1057,20 @@ cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, floa
     if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.c.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    // f16: Q of a row tile is a box, 64 values of G heads of TT tokens
-    CUtensorMap qmap = map;
-    if (!Z::split) {
-        const cuuint64_t qdims[3] = {HD, static_cast<cuuint64_t>(a.nh), static_cast<cuuint64_t>(a.b.M)};
-        const cuuint64_t qstrides[2] = {HD * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
-        const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(r.G), static_cast<cuuint32_t>(p.TT)}, qstep[3] = {1, 1, 1};
-        if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(a.q), qdims, qstrides, qbox, qstep,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
-    }
+    // rows of queries (f16) and outputs: a box is 128 bytes of G heads of TT tokens, a row tile
+    constexpr cuuint32_t size = sizeof(T);
+    const auto rows_map = [&](CUtensorMap *to, const void *from, int64_t stride) {
+        const cuuint64_t rdims[3] = {HD, static_cast<cuuint64_t>(a.nh), static_cast<cuuint64_t>(a.b.M)};
+        const cuuint64_t rstrides[2] = {HD * size, static_cast<cuuint64_t>(stride) * size};
+        const cuuint32_t rbox[3] = {128 / size, static_cast<cuuint32_t>(r.G), static_cast<cuuint32_t>(p.TT)}, rstep[3] = {1, 1, 1};
+        return encode(to, Z::split ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(from), rdims,
+                      rstrides, rbox, rstep, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUtensorMap qmap, omap;
+    if (rows_map(&qmap, a.q, a.q_stride) != CUDA_SUCCESS || rows_map(&omap, a.out, a.out_stride) != CUDA_SUCCESS) return cudaErrorInvalidValue;
     const int grid = static_cast<int>(std::min<long long>(num_sms(), static_cast<long long>(p.units) * p.splits));
-    return launch_pdl(pdl, k_paged_rows<T, HD>, dim3(grid), kRwThreads, Z::smem, 1, s, r, map, qmap);
+    return launch_pdl(pdl, k_paged_rows<T, HD>, dim3(grid), kRwThreads, Z::smem, 1, s, r, map, qmap, omap);
 }
 
 template <typename T, int HD>

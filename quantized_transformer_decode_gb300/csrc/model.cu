@@ -1671,7 +1671,8 @@ int qw3_kv_paged_attn(const qw3_kv_paged *cache, const qw3_kv_batch *batch, int3
     const int64_t qw = static_cast<int64_t>(n_heads) * cache->head_dim;
     if (int rc = check_rows(q_dev, q_stride, qw, type)) return rc;
     if (int rc = check_rows(out_dev, out_stride, qw, type)) return rc;
-    if (q_stride % cache->head_dim) return fail(nullptr, QW3_ERR_SHAPE, "q_stride must be a multiple of head_dim");
+    if (q_stride % cache->head_dim || out_stride % cache->head_dim)
+        return fail(nullptr, QW3_ERR_SHAPE, "q_stride and out_stride must be multiples of head_dim");
     if (misaligned(workspace_dev, 16) || misaligned(status_dev, 4))
         return fail(nullptr, QW3_ERR_INVALID_ARG, "the workspace must be 16-byte, the status 4-byte aligned");
     if (!(scale - scale == 0.0f)) return fail(nullptr, QW3_ERR_INVALID_ARG, "scale must be finite");
