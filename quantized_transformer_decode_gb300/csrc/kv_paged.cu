@@ -15,30 +15,31 @@ namespace {
 
 // ---------------------------------------------------------------- append
 
-// A lane holds 16 bytes of a head: V values, L = HD / V lanes to a head, 32 / L
-// heads to a warp at once. The rotation's pair (i, i + hd/2) lies L / 2 lanes
-// away.
+// A lane holds V values (16 bytes) of a head's first half and the V of its second
+// half that the rotation pairs them with: L = HD / 2 / V lanes to a head, 32 / L
+// heads to a warp at once, and no value has to change lanes.
 template <typename T>
 struct PgVec {
     static constexpr int V = 16 / sizeof(T);
 };
 
-__device__ __forceinline__ void pg_ld(float (&v)[4], const float *p) {
-    const float4 t = *reinterpret_cast<const float4 *>(p);
-    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-}
-__device__ __forceinline__ void pg_ld(float (&v)[8], const __half *p) {
-    const uint4 t = *reinterpret_cast<const uint4 *>(p);
+// 16 bytes as f32 values, and back.
+template <typename T>
+__device__ __forceinline__ void pg_cvt(float *v, uint4 t) {
     const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        if constexpr (sizeof(T) == 4) {
+            v[i] = __uint_as_float(w[i]);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
     }
 }
 template <int N>
-__device__ __forceinline__ void pg_st_half(__half *p, const float (&v)[N]) {
+__device__ __forceinline__ void pg_st_half(__half *p, const float *v) {
     uint32_t w[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
@@ -48,10 +49,8 @@ __device__ __forceinline__ void pg_st_half(__half *p, const float (&v)[N]) {
     if constexpr (N == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ void pg_st(float *p, const float (&v)[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void pg_st(__half *p, const float (&v)[8]) { pg_st_half(p, v); }
+__device__ __forceinline__ void pg_st(float *p, const float *v) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void pg_st(__half *p, const float *v) { pg_st_half<8>(p, v); }
 
 template <int L>
 __device__ __forceinline__ float pg_sum(float v) {
@@ -60,133 +59,142 @@ __device__ __forceinline__ float pg_sum(float v) {
     return v;
 }
 
-// 1 / sqrt(mean x^2 + eps) of the lane's head in f64, as a factor that takes x
-// in two steps (each a power-of-two-free f32 product could leave f32): x * a * b.
-template <int L, int V>
-__device__ __noinline__ void pg_norm_f64(const float (&x)[V], float eps, float (&y)[V]) {
+// x / sqrt(mean x^2 + eps) of the lane's head in f64.
+template <int L, int N>
+__device__ __noinline__ void pg_norm_f64(const float (&x)[N], float eps, float (&y)[N]) {
     double ss = 0.0;
 #pragma unroll
-    for (int e = 0; e < V; ++e) ss += static_cast<double>(x[e]) * x[e];
+    for (int e = 0; e < N; ++e) ss += static_cast<double>(x[e]) * x[e];
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const double r = 1.0 / sqrt(ss / (L * V) + static_cast<double>(eps));
+    const double r = 1.0 / sqrt(ss / (L * N) + static_cast<double>(eps));
 #pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = static_cast<float>(x[e] * r);
+    for (int e = 0; e < N; ++e) y[e] = static_cast<float>(x[e] * r);
 }
 
-// One warp takes NP passes (of 32 / L heads) of one row; the passes' loads are
-// issued together.
-template <typename T, int HD, int NP>
+// Warp w of a row's per_row takes passes w, w + per_row, .. (of 32 / L heads), the
+// next one's loads issued before the last one is worked on.
+template <typename T, int HD>
 __global__ void __launch_bounds__(128) k_paged_append(const KvPagedAppendArgs a, int passes, int per_row, long long units) {
-    constexpr int V = PgVec<T>::V, L = HD / V, H = 32 / L;
+    constexpr int V = PgVec<T>::V, L = HD / 2 / V, H = 32 / L;
     const int lane = threadIdx.x & 31;
     const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     pdl_trigger();
     pdl_wait();
-    if (unit < units) {
-        const int row = static_cast<int>(unit / per_row), pass0 = static_cast<int>(unit % per_row) * NP;
-        const int i = kv_seq_of(a.b, row, lane);
-        if (i >= 0) {
-            const int nkv = a.c.nkv, heads = a.nh + 2 * nkv, at = lane % L * V;
-            const T *src = static_cast<const T *>(a.qkv) + row * a.qkv_stride;
-            float x[NP][V];
+    if (unit >= units) return;
+    const int row = static_cast<int>(unit / per_row), pass0 = static_cast<int>(unit % per_row);
+    const int nkv = a.c.nkv, heads = a.nh + 2 * nkv, at = lane % L * V;
+    const T *src = static_cast<const T *>(a.qkv) + row * a.qkv_stride + at;
+    uint4 next[2];
+    auto load = [&](int pass) {
+        const int h = pass * H + lane / L;
+        next[0] = next[1] = make_uint4(0, 0, 0, 0);
+        if (h < heads) {
+            next[0] = *reinterpret_cast<const uint4 *>(src + static_cast<size_t>(h) * HD);
+            next[1] = *reinterpret_cast<const uint4 *>(src + static_cast<size_t>(h) * HD + HD / 2);
+        }
+    };
+    load(pass0);
+    const int i = kv_seq_of(a.b, row, lane);
+    if (i < 0) return;
+    // its position: row t of n rows (kv_seq's n may be cut, this one is not)
+    const int s0 = min(max(a.b.starts[i], 0), a.b.M), s1 = min(max(a.b.starts[i + 1], 0), a.b.M);
+    if (row < s0 || row >= s1) return;
+    const int p = a.b.lens[i] - (s1 - row);
+    const int page = p >= 0 && p < a.rope_len ? kv_page(a.b, a.c, i, p) : -1;
+    float2 cs[V];
 #pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                const int h = (pass0 + k) * H + lane / L;
+    for (int e = 0; e < V; ++e) cs[e] = make_float2(0.0f, 0.0f);
+    if (page >= 0) {
+        const float4 *r = reinterpret_cast<const float4 *>(a.rope + static_cast<size_t>(p) * (HD / 2) + at);
 #pragma unroll
-                for (int e = 0; e < V; ++e) x[k][e] = 0.0f;
-                if (h < heads) pg_ld(x[k], src + static_cast<size_t>(h) * HD + at);
-            }
-            // its position: row t of n rows (kv_seq's n may be cut, this one is not)
-            const int s0 = min(max(a.b.starts[i], 0), a.b.M), s1 = min(max(a.b.starts[i + 1], 0), a.b.M);
-            const int p = row < s1 ? a.b.lens[i] - (s1 - row) : -1;
-            const int page = p >= 0 && p < a.rope_len ? kv_page(a.b, a.c, i, p) : -1;
-            const bool mine = row >= s0 && row < s1;
-            float2 cs[V];
-            if (page >= 0) {
-                const float4 *r = reinterpret_cast<const float4 *>(a.rope + static_cast<size_t>(p) * (HD / 2) + at % (HD / 2));
-#pragma unroll
-                for (int e = 0; e < V / 2; ++e) {
-                    const float4 t = r[e];
-                    cs[2 * e] = make_float2(t.x, t.y);
-                    cs[2 * e + 1] = make_float2(t.z, t.w);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) cs[e] = make_float2(0.0f, 0.0f);
-            }
-            const bool first = lane % L < L / 2;   // the lane holds the pairs' first halves
-            bool bad = false;
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                const int h = (pass0 + k) * H + lane / L;
-                const bool turned = h < a.nh + nkv;
-                const float *w = h < a.nh ? a.q_norm : turned ? a.k_norm : nullptr;
-                float y[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) y[e] = x[k][e];
-                float ss = 0.0f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) ss = fmaf(y[e], y[e], ss);
-                const float mean = pg_sum<L>(ss) * (1.0f / HD) + a.eps;
-                // where the squares, or their sum, leave f32 the head is normalised in f64
-                if (__any_sync(0xffffffffu, w && !(mean > 0x1p-100f && mean < 0x1p120f))) {
-                    float z[V];
-                    pg_norm_f64<L, V>(y, a.eps, z);
-                    if (w) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) y[e] = z[e] * w[at + e];
-                    }
-                } else if (w) {
-                    const float r = rsqrtf(mean), r1 = r * fmaf(-0.5f * mean * r, r, 1.5f);   // one Newton step: within a rounding
-#pragma unroll
-                    for (int e = 0; e < V; ++e) y[e] = y[e] * r1 * w[at + e];
-                }
-                float z[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float o = __shfl_xor_sync(0xffffffffu, y[e], L / 2);
-                    z[e] = !turned ? y[e] : first ? y[e] * cs[e].x - o * cs[e].y : y[e] * cs[e].x + o * cs[e].y;
-                }
-                // a head of K or V that f16 does not hold
-                bool over = false;
-#pragma unroll
-                for (int e = 0; e < V; ++e) over |= !(fabsf(z[e]) < 65520.0f);
-                const unsigned whole = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (lane / L * L);
-                over = (__ballot_sync(0xffffffffu, over) & whole) != 0;
-                if (!mine || h >= heads) continue;
-                if (h < a.nh) {
-                    if (page < 0) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) z[e] = 0.0f;
-                    }
-                    pg_st(static_cast<T *>(a.q_out) + row * a.q_stride + static_cast<size_t>(h) * HD + at, z);
-                } else if (page >= 0) {
-                    if (over) {
-                        bad = true;
-#pragma unroll
-                        for (int e = 0; e < V; ++e) z[e] = 0.0f;
-                    }
-                    const int g = h - a.nh;
-                    pg_st_half(kv_paged_row<HD>(a.c, page, g >= nkv, g >= nkv ? g - nkv : g, p) + at, z);
-                }
-            }
-            if (bad) record_status(a.status, QW3_ERR_NONFINITE);
+        for (int e = 0; e < V / 2; ++e) {
+            const float4 t = r[e];
+            cs[2 * e] = make_float2(t.x, t.y);
+            cs[2 * e + 1] = make_float2(t.z, t.w);
         }
     }
+    bool bad = false;
+#pragma unroll 1
+    for (int pass = pass0; pass < passes; pass += per_row) {
+        float y[2 * V];   // the first half's values, then the second's
+        pg_cvt<T>(y, next[0]);
+        pg_cvt<T>(y + V, next[1]);
+        if (pass + per_row < passes) load(pass + per_row);
+        const int h = pass * H + lane / L;
+        const bool turned = h < a.nh + nkv;
+        const float *w = h < a.nh ? a.q_norm : turned ? a.k_norm : nullptr;
+        if (__any_sync(0xffffffffu, w != nullptr)) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2 * V; ++e) ss = fmaf(y[e], y[e], ss);
+            const float mean = pg_sum<L>(ss) * (1.0f / HD) + a.eps;
+            float wv[2 * V];
+#pragma unroll
+            for (int e = 0; e < 2 * V; ++e) wv[e] = w ? w[at + (e < V ? e : HD / 2 - V + e)] : 1.0f;
+            // where the squares, or their sum, leave f32 the head is normalised in f64
+            if (__any_sync(0xffffffffu, w && !(mean > 0x1p-100f && mean < 0x1p120f))) {
+                float z[2 * V];
+                pg_norm_f64<L, 2 * V>(y, a.eps, z);
+                if (w) {
+#pragma unroll
+                    for (int e = 0; e < 2 * V; ++e) y[e] = z[e] * wv[e];
+                }
+            } else if (w) {
+                const float r = rsqrtf(mean), r1 = r * fmaf(-0.5f * mean * r, r, 1.5f);   // one Newton step: within a rounding
+#pragma unroll
+                for (int e = 0; e < 2 * V; ++e) y[e] = y[e] * r1 * wv[e];
+            }
+        }
+        if (turned) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float u = y[e], v = y[V + e];
+                y[e] = u * cs[e].x - v * cs[e].y;
+                y[V + e] = v * cs[e].x + u * cs[e].y;
+            }
+        }
+        // a head of K or V that f16 does not hold
+        bool over = false;
+#pragma unroll
+        for (int e = 0; e < 2 * V; ++e) over |= !(fabsf(y[e]) < 65520.0f);
+        const unsigned head = (1u << (L & 31)) - 1;
+        over = (__ballot_sync(0xffffffffu, over) & head << (lane / L * L)) != 0;
+        if (h < a.nh) {
+            if (page < 0) {
+#pragma unroll
+                for (int e = 0; e < 2 * V; ++e) y[e] = 0.0f;
+            }
+            T *to = static_cast<T *>(a.q_out) + row * a.q_stride + static_cast<size_t>(h) * HD + at;
+            pg_st(to, y);
+            pg_st(to + HD / 2, y + V);
+        } else if (h < heads && page >= 0) {
+            if (over) {
+                bad = true;
+#pragma unroll
+                for (int e = 0; e < 2 * V; ++e) y[e] = 0.0f;
+            }
+            const int g = h - a.nh;
+            __half *to = kv_paged_row<HD>(a.c, page, g >= nkv, g >= nkv ? g - nkv : g, p) + at;
+            pg_st_half<V>(to, y);
+            pg_st_half<V>(to + HD / 2, y + V);
+        }
+        __syncwarp();
+    }
+    if (bad) record_status(a.status, QW3_ERR_NONFINITE);
 }
 
+#ifndef APR
+#define APR 8
+#endif
 template <typename T, int HD>
 cudaError_t append_t(const KvPagedAppendArgs &a, bool pdl, cudaStream_t s) {
-    constexpr int V = PgVec<T>::V, H = 32 / (HD / V);
+    constexpr int V = PgVec<T>::V, H = 32 / (HD / 2 / V);
     const int passes = (a.nh + 2 * a.c.nkv + H - 1) / H;
-    // few rows: a warp to a pass; many: four passes' loads in flight to a warp
-    const bool few = static_cast<long long>(a.b.M) * passes <= 152 * 32;
-    const int np = few ? 1 : 4, per_row = (passes + np - 1) / np;
+    // few rows: a warp to a pass; many: four to a row
+    const int per_row = static_cast<long long>(a.b.M) * passes <= 152 * 32 ? passes : std::min(passes, APR);
     const long long units = static_cast<long long>(a.b.M) * per_row;
-    const dim3 grid(static_cast<unsigned>((units + 3) / 4));
-    return few ? launch_pdl(pdl, k_paged_append<T, HD, 1>, grid, 128, 0, 1, s, a, passes, per_row, units)
-               : launch_pdl(pdl, k_paged_append<T, HD, 4>, grid, 128, 0, 1, s, a, passes, per_row, units);
+    return launch_pdl(pdl, k_paged_append<T, HD>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0, 1, s, a, passes, per_row, units);
 }
 
 // ---------------------------------------------------------------- attention of few rows
@@ -215,6 +223,9 @@ constexpr int kTokWarps = 8, kTokStages = 3, kTokKeys = 16;
 // with 0, 104 with 10, 93.6 with 24, 95.2 with 40. Fewer units: a CTA has two at
 // most, and shares may be short.
 constexpr int kTokUnit = 24;
+// Few short units: a CTA to each, and nothing to join. (One token of one sequence,
+// 16/8 heads: 517 positions 9.9 us instead of 12.2, 1000 positions 13.3 instead of 12.5.)
+constexpr int kTokWhole = 48;
 constexpr int kTokCols = 32;      // columns of a sequence's kv head that these kernels take
 
 template <typename T, int HD>
@@ -277,7 +288,8 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// The shares are of work: a unit's is `ends` (kTokUnit or 0) and then its steps.
+// The shares are of work: a unit's is `ends` (kTokUnit or 0) and then its steps; or
+// (ends < 0) one, and a CTA has one unit.
 // Where a CTA (or a warp's loads, ahead of it) is: unit `u` of sequence i, its
 // steps k .. end - 1 among them, and `left` of the share behind those.
 struct TokAt {
@@ -341,7 +353,7 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
     long long mine = 0;
     for (int i = i0; i < i1; ++i) {
         const TokSeq s = tok_seq(a, i, G);
-        mine += static_cast<long long>(tok_units<W>(s, nkv)) * (ends + s.steps);
+        mine += static_cast<long long>(tok_units<W>(s, nkv)) * (ends < 0 ? 1 : ends + s.steps);
     }
     long long upto = mine;
 #pragma unroll
@@ -362,12 +374,12 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
         long long at = before;
         for (int i = i0; i < i1; ++i) {
             const TokSeq s = tok_seq(a, i, G);
-            const int unit = ends + s.steps;
+            const int unit = ends < 0 ? 1 : ends + s.steps;
             const long long n = static_cast<long long>(tok_units<W>(s, nkv)) * unit;
             if (x0 < at + n) {
                 s_i = i;
                 s_off_u = static_cast<int>((x0 - at) / unit);
-                s_off_k = static_cast<int>((x0 - at) % unit) - ends;
+                s_off_k = ends < 0 ? 0 : static_cast<int>((x0 - at) % unit) - ends;
                 break;
             }
             at += n;
@@ -390,8 +402,8 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
         if (beside) pdl_wait();
         return;
     }
-    t.end = static_cast<int>(min(static_cast<long long>(t.s.steps), t.k + (x1 - x)));
-    t.left = x1 - x - (t.end - t.k);
+    t.end = ends < 0 ? t.s.steps : static_cast<int>(min(static_cast<long long>(t.s.steps), t.k + (x1 - x)));
+    t.left = ends < 0 ? 0 : x1 - x - (t.end - t.k);
 
     // ---- this warp's loads: the next step to fetch, its page known one step ahead
     const uint32_t ring = smem_u32(tok_smem) + warp * Z::ring;
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
         // ---- the warps' parts joined, 8 columns at a time
         const bool whole = t.k == 0 && t.end == t.s.steps;
         float *const dst = slots + (static_cast<size_t>(blockIdx.x) * 2 + (piece > 0)) * W * Z::part;
-        if (t.k == 0 && tid == 0) {
+        if (t.k == 0 && tid == 0 && ends >= 0) {
             // the first of the unit's CTAs says where the others are
             TokCut c{-1, 0u};
             if (!whole) c = {static_cast<int>(blockIdx.x), static_cast<uint32_t>((x + t.s.steps - 1) / share) | (piece == 0 ? 0x80000000u : 0u)};
@@ -777,9 +789,16 @@ TokPlan tok_plan(int B, int type, int nh, int nkv, int hd, int max_rows, int max
     long long len = max_len;
     if (window > 0) len = std::min<long long>(len, static_cast<long long>(window) + max_rows + sinks + 3 * kTokKeys);
     const long long units = static_cast<long long>(B) * nkv * p.max_cb;
+    const long long most = std::max<long long>(1, (len + kTokKeys - 1) / kTokKeys);   // steps of a unit
+    if (units <= num_sms() && most <= kTokWhole) {
+        p.ends = -1;
+        p.min_share = 1;
+        p.grid = static_cast<int>(units);
+        return p;
+    }
     p.ends = units > num_sms() ? kTokUnit : 0;
     p.min_share = p.ends + kTokWarps;   // a step to a warp: fewer would only be more to join
-    const long long work = (p.ends + std::max<long long>(1, (len + kTokKeys - 1) / kTokKeys)) * units;
+    const long long work = (p.ends + most) * units;
     p.grid = static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(num_sms(), kTokMaxGrid), (work + p.min_share - 1) / p.min_share)));
     p.bytes = static_cast<size_t>(p.grid) * 2 * W * (hd + 4) * 4 + static_cast<size_t>(B) * nkv * p.max_cb * sizeof(TokCut);
     return p;
@@ -792,7 +811,7 @@ cudaError_t tokens_t(const KvPagedAttnArgs &a, const TokPlan &p, bool join, bool
     if (!join)
         return launch_pdl(pdl, k_paged_tokens<T, HD>, dim3(p.grid), kTokWarps * 32, Z::smem, 1, s, a, G, p.max_cb, p.ends, p.min_share,
                           static_cast<int>(beside));
-    if (p.grid == 1) return cudaSuccess;
+    if (p.grid == 1 || p.ends < 0) return cudaSuccess;
     // few units: a block to a column (1 x 32768, 8 units in 152 parts: 34 us in all where a block to a unit makes it 38)
     const int per = static_cast<long long>(a.b.B) * a.c.nkv * p.max_cb <= 32 ? 1 : Z::W;
     const dim3 grid(per == 1 ? p.cols : p.max_cb, a.c.nkv, std::min(a.b.B, 65535));
