@@ -72,29 +72,38 @@ __device__ __noinline__ void pg_norm_f64(const float (&x)[N], float eps, float (
     for (int e = 0; e < N; ++e) y[e] = static_cast<float>(x[e] * r);
 }
 
-// Warp w of a row's per_row takes passes w, w + per_row, .. (of 32 / L heads), the
-// next one's loads issued before the last one is worked on.
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) k_paged_append(const KvPagedAppendArgs a, int passes, int per_row, long long units) {
+// Bound by reads that wait for the ones before them: 4096 rows of 32/8 heads (186
+// MB) take 42 us, 0.65 of the copy rate; one row of 16/8 heads 2.6 us.
+//
+// Warp w of a row's per_row takes passes w, w + per_row, .. (of 32 / L heads), NP at
+// most, whose loads are all issued before the row's place is looked up.
+template <typename T, int HD, int NP>
+__global__ void __launch_bounds__(128) k_paged_append(const KvPagedAppendArgs a, int per_row, long long units) {
     constexpr int V = PgVec<T>::V, L = HD / 2 / V, H = 32 / L;
     const int lane = threadIdx.x & 31;
     const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    __shared__ __align__(16) float s_w[2][HD];   // the norms' weights (4-byte loads for every head were what bounded this)
     pdl_trigger();
     pdl_wait();
+    for (int e = threadIdx.x; e < HD; e += 128) {
+        s_w[0][e] = a.q_norm ? a.q_norm[e] : 1.0f;
+        s_w[1][e] = a.k_norm ? a.k_norm[e] : 1.0f;
+    }
+    __syncthreads();
     if (unit >= units) return;
     const int row = static_cast<int>(unit / per_row), pass0 = static_cast<int>(unit % per_row);
     const int nkv = a.c.nkv, heads = a.nh + 2 * nkv, at = lane % L * V;
     const T *src = static_cast<const T *>(a.qkv) + row * a.qkv_stride + at;
-    uint4 next[2];
-    auto load = [&](int pass) {
-        const int h = pass * H + lane / L;
-        next[0] = next[1] = make_uint4(0, 0, 0, 0);
+    uint4 raw[NP][2];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int h = (pass0 + k * per_row) * H + lane / L;
+        raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
         if (h < heads) {
-            next[0] = *reinterpret_cast<const uint4 *>(src + static_cast<size_t>(h) * HD);
-            next[1] = *reinterpret_cast<const uint4 *>(src + static_cast<size_t>(h) * HD + HD / 2);
+            raw[k][0] = __ldcs(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(h) * HD));
+            raw[k][1] = __ldcs(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(h) * HD + HD / 2));
         }
-    };
-    load(pass0);
+    }
     const int i = kv_seq_of(a.b, row, lane);
     if (i < 0) return;
     // its position: row t of n rows (kv_seq's n may be cut, this one is not)
@@ -115,23 +124,27 @@ __global__ void __launch_bounds__(128) k_paged_append(const KvPagedAppendArgs a,
         }
     }
     bool bad = false;
-#pragma unroll 1
-    for (int pass = pass0; pass < passes; pass += per_row) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int h = (pass0 + k * per_row) * H + lane / L;
+        if ((pass0 + k * per_row) * H >= heads) break;
         float y[2 * V];   // the first half's values, then the second's
-        pg_cvt<T>(y, next[0]);
-        pg_cvt<T>(y + V, next[1]);
-        if (pass + per_row < passes) load(pass + per_row);
-        const int h = pass * H + lane / L;
+        pg_cvt<T>(y, raw[k][0]);
+        pg_cvt<T>(y + V, raw[k][1]);
         const bool turned = h < a.nh + nkv;
-        const float *w = h < a.nh ? a.q_norm : turned ? a.k_norm : nullptr;
-        if (__any_sync(0xffffffffu, w != nullptr)) {
+        const bool w = h < a.nh ? a.q_norm != nullptr : turned && a.k_norm;
+        if (__any_sync(0xffffffffu, w)) {
             float ss = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e) ss = fmaf(y[e], y[e], ss);
             const float mean = pg_sum<L>(ss) * (1.0f / HD) + a.eps;
             float wv[2 * V];
+            const float *sw = s_w[h < a.nh ? 0 : 1] + at;
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) wv[e] = w ? w[at + (e < V ? e : HD / 2 - V + e)] : 1.0f;
+            for (int e = 0; e < 2 * V; e += 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(sw + (e < V ? e : HD / 2 - V + e));
+                wv[e] = t.x; wv[e + 1] = t.y; wv[e + 2] = t.z; wv[e + 3] = t.w;
+            }
             // where the squares, or their sum, leave f32 the head is normalised in f64
             if (__any_sync(0xffffffffu, w && !(mean > 0x1p-100f && mean < 0x1p120f))) {
                 float z[2 * V];
@@ -184,17 +197,18 @@ __global__ void __launch_bounds__(128) k_paged_append(const KvPagedAppendArgs a,
     if (bad) record_status(a.status, QW3_ERR_NONFINITE);
 }
 
-#ifndef APR
-#define APR 8
-#endif
 template <typename T, int HD>
 cudaError_t append_t(const KvPagedAppendArgs &a, bool pdl, cudaStream_t s) {
     constexpr int V = PgVec<T>::V, H = 32 / (HD / 2 / V);
+    constexpr int NP = 2;   // 4096 rows of 32/8 heads, f32: 46 us with 1, 42 with 2, 47 with 4 (floor 28)
     const int passes = (a.nh + 2 * a.c.nkv + H - 1) / H;
-    // few rows: a warp to a pass; many: four to a row
-    const int per_row = static_cast<long long>(a.b.M) * passes <= 152 * 32 ? passes : std::min(passes, APR);
+    // few rows: a warp to a pass
+    const bool few = static_cast<long long>(a.b.M) * passes <= 152 * 32;
+    const int per_row = few ? passes : (passes + NP - 1) / NP;
     const long long units = static_cast<long long>(a.b.M) * per_row;
-    return launch_pdl(pdl, k_paged_append<T, HD>, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0, 1, s, a, passes, per_row, units);
+    const dim3 grid(static_cast<unsigned>((units + 3) / 4));
+    return few ? launch_pdl(pdl, k_paged_append<T, HD, 1>, grid, 128, 0, 1, s, a, per_row, units)
+               : launch_pdl(pdl, k_paged_append<T, HD, NP>, grid, 128, 0, 1, s, a, per_row, units);
 }
 
 // ---------------------------------------------------------------- attention of few rows

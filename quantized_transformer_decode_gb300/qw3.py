@@ -956,6 +956,19 @@ class Qw3Model:
             qw3_forward_all_logits(self.h, seq, tokens.data_ptr(), n, logits.data_ptr(), am.data_ptr())
         return logits, am
 
+    def score(self, seq: int, tokens, top: int = 0):
+        """Append tokens (CUDA int32 tensor [n]) to sequence seq as
+        forward_all_logits does, and return what the model makes of them: (log
+        probabilities f32 [n - 1] of tokens[1:], each after the tokens before it,
+        entropies f32 [n] of every row, its `top` most likely tokens int32
+        [n, top] and their log probabilities f32 [n, top])."""
+        torch = _torch()
+        tokens = tokens.to(torch.int32).contiguous()
+        logits, _ = self.forward_all_logits(seq, tokens)
+        after = torch.cat((tokens[1:], tokens.new_full((1,), -1)))   # (nothing is known to follow the last one)
+        lp, entropy, top_id, top_lp = logprobs(logits, after, top=top)
+        return lp[:-1], entropy, top_id, top_lp
+
     def decode(self, tokens, pos: Sequence[int], seqs: Optional[Sequence[int]] = None, want_logits: bool = True):
         """One decode step for B = len(pos) sequences; tokens CUDA int32 [B]."""
         torch = _torch()

@@ -383,6 +383,39 @@ def test_large_scores(torch, rows, dtype):
         b.check(b.attend(scale=scale), scale=np.float64(np.float32(scale)))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_queries_and_outputs_inside_wider_rows(torch, dtype):
+    """Through the C entry: queries where the projections lie, outputs in rows of another width; what lies beside them stays."""
+    b = Batch(torch, [(1, 70), (90, 200), (3, 3), (64, 64)], nh=4, nkv=2, hd=64, dtype=dtype, lead=1, tail=2)
+    qw3, c = b.qw3, b.cache()
+    starts, lens, table = b.where()
+    batch = qw3.Qw3KvBatch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], 4, table.shape[1])
+    wide = torch.full((b.M, 8, b.hd), 5.0, dtype=b.dtype, device="cuda")
+    wide[:, 2:6] = b.dev(b.q)
+    out = torch.full((b.M, 7, b.hd), 9.0, dtype=b.dtype, device="cuda")
+    need = qw3.qw3_kv_paged_attn_workspace_bytes(4, b.M, int(b.f16), 4, 2, 64, 90, 208)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda").fill_(255)
+    stream = torch.cuda.current_stream().cuda_stream
+    size = wide.element_size() * b.hd
+    for src, dst, first in ((wide, out, 1), (wide, wide, 2)):
+        qw3.qw3_kv_paged_attn(c.c, batch, int(b.f16), wide.data_ptr() + 2 * size, b.M, 8 * b.hd, 4, 90, 208, 0, 0, b.hd ** -0.5,
+                              dst.data_ptr() + first * size, dst.shape[1] * b.hd, ws.data_ptr(), need, 0, stream)
+        b.check(dst[:, first:first + 4])
+        keep = torch.ones(dst.shape[:2], dtype=torch.bool, device="cuda")
+        keep[1:-2, first:first + 4] = False
+        assert (dst[keep] == (9 if dst is out else torch.cat((torch.full_like(wide[:, :2], 5.0), b.dev(b.q), torch.full_like(wide[:, 6:], 5.0)), 1)[keep])).all()
+
+
+def test_queries_of_any_size(torch):
+    """f32 queries up to the type's largest values, and scores that leave f32."""
+    for rows in (1, 70):
+        b = Batch(torch, [(rows, 150)], nh=4, nkv=2, hd=64)
+        b.q = (b.q.astype(np.float64) / 8 * 3e38).clip(-3.3e38, 3.3e38).astype(np.float32)
+        b.check(b.attend(scale=1e-38), scale=np.float64(np.float32(1e-38)))
+        b.q = (b.rng.standard_normal(b.q.shape) * 1e-38).astype(np.float32)
+        b.check(b.attend(scale=1e38), scale=np.float64(np.float32(1e38)))
+
+
 def test_offsets_past_32_bits(torch):
     """Pages beyond 2^32 bytes of the pool."""
     from quantized_transformer_decode_gb300 import qw3
