@@ -55,7 +55,9 @@ struct RwSizes {
     static constexpr int stages = HD == 128 ? (split ? 5 : 4) : 8;
     static constexpr uint32_t out = split ? 0 : kRwRows * 128;
     static constexpr uint32_t smem = 2 * tile + stages * tile + 2 * out + 1024;
-    static constexpr int part = HD + 4;                            // floats of a row's part: output, maximum, sum
+    // a warpgroup's part in the workspace: [HD outputs, maximum, sum][128 rows] floats, so that a warp's rows are written
+    // and read side by side; two of them to a unit's part (f16: of its row tiles, f32: of its warpgroups)
+    static constexpr int part = (HD + 2) * kRwRows;
     // P goes to the products in parts, so that these begin before the last exponentials are there
     static constexpr int parts = 2, part_keys = kRwKeys / parts;
 };
@@ -190,8 +192,8 @@ __device__ __forceinline__ RwTiles rw_tiles(int pmin, int pmax, int window, int 
 }
 
 // Rows row0 .. row1 - 1 of the unit without matrix products, for the tiles i0 .. i1
-// - 1: warp `warp` of `warps`, a row at a time. dst: the part's rows, or null for
-// the output.
+// - 1: warp `warp` of `warps`, a row at a time. dst: the part, or null for the
+// output.
 template <typename T, int HD>
 __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwTiles &t, int i0, int i1, int g, int row0, int row1,
                                      int warp, int warps, float off, float *dst) {
@@ -229,12 +231,12 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
             }
         }
         if (dst) {
-            float *to = dst + static_cast<size_t>(row) * RwSizes<T, HD>::part;
+            float *to = dst + row % kRwRows;
 #pragma unroll
-            for (int e = 0; e < E; ++e) to[lane * E + e] = o[e];
+            for (int e = 0; e < E; ++e) to[(lane * E + e) * kRwRows] = o[e];
             if (lane == 0) {
-                to[HD] = m;
-                to[HD + 1] = l;
+                to[HD * kRwRows] = m;
+                to[(HD + 1) * kRwRows] = l;
             }
         } else {
             T *to = static_cast<T *>(a.out) + at * a.out_stride + static_cast<size_t>(h) * HD + lane * E;
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             turn = turn_next;
             float *const dst = it.parts == 1 ? nullptr
                                              : r.ws + static_cast<size_t>(r.units) * 4 +
-                                                   (static_cast<size_t>(it.unit) * r.splits + it.part) * (QT * kRwRows) * Z::part;
+                                                   ((static_cast<size_t>(it.unit) * r.splits + it.part) * 2 + s) * Z::part;
             // the output of row x of a row tile, or null
             const size_t out_row = static_cast<size_t>(a.out_stride);
             T *const out0 = static_cast<T *>(a.out) + static_cast<size_t>(it.u.start + it.u.tok0) * out_row + static_cast<size_t>(it.g * r.G) * HD;
@@ -801,15 +803,15 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             done += 2 * NT;
             const float m2 = m == -INFINITY ? -INFINITY : m * c;   // the reference in base 2
             // Rows go out through shared memory, 128 bytes of each at a time (chunk c of 16 bytes of row x at c ^ (x & 7),
-            // the tensor maps' swizzle): by TMA where the row tile is full, else, and to the workspace, by the threads.
-            auto copy_out = [&](const uint8_t *place, int rows_of, int d0, int thread, int threads) {
+            // the tensor maps' swizzle): by TMA where the row tile is full, else by the threads. Parts go to the workspace
+            // as they are.
+            auto copy_out = [&](const uint8_t *place, int tile, int d0, int thread, int threads) {
 #pragma unroll 2
                 for (int q = thread; q < kRwRows * 8; q += threads) {
                     const int x = q >> 3, ch = q & 7;
-                    uint8_t *to = dst ? reinterpret_cast<uint8_t *>(dst + static_cast<size_t>(rows_of * kRwRows + x) * Z::part + d0)
-                                      : reinterpret_cast<uint8_t *>(row_of(x, rows_of));
+                    T *to = row_of(x, tile);
                     if (to)
-                        *reinterpret_cast<uint4 *>(to + (dst ? 0 : d0 * static_cast<int>(sizeof(T))) + ch * 16) =
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(to + d0) + ch * 16) =
                             *reinterpret_cast<const uint4 *>(place + x * 128 + ((ch ^ (x & 7)) << 4));
                 }
             };
@@ -821,20 +823,29 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 }
                 rw_bar<128>(2 + s);
                 const bool bad = *bad_flag;
-                if (!bad && active) {
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    const bool full = !dst && tokens >= (s + 1) * r.TT;
-                    uint8_t *const place = smem + (2 + ST) * Z::tile + s * Z::out;
-                    const int width = dst ? 32 : 64;   // values in 128 bytes
+                if (!bad && active && dst) {
 #pragma unroll 1
-                    for (int d0 = 0; d0 < HD; d0 += width) {
+                    for (int d = 0; d < HD; d += 32) {
+                        uint32_t o[32];
+                        rw_ld32(tO + d, o);
+                        rw_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) dst[(d + e) * kRwRows + rr] = own > 0 ? __uint_as_float(o[e]) : 0.0f;
+                    }
+                    dst[HD * kRwRows + rr] = m2;
+                    dst[(HD + 1) * kRwRows + rr] = l;
+                } else if (!bad && active) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    const bool full = tokens >= (s + 1) * r.TT;
+                    uint8_t *const place = smem + (2 + ST) * Z::tile + s * Z::out;
+#pragma unroll 1
+                    for (int d0 = 0; d0 < HD; d0 += 64) {
                         if (d0 > 0) {
                             if (rr == 0) rw_out_read();
                             rw_bar<128>(2 + s);
                         }
 #pragma unroll
                         for (int d = 0; d < 64; d += 32) {
-                            if (d >= width) break;
                             uint32_t o[32];
                             rw_ld32(tO + d0 + d, o);
                             rw_wait_ld();
@@ -842,19 +853,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) o[e] = 0;
                             }
-                            if (dst) {
 #pragma unroll
-                                for (int e = 0; e < 32; e += 4)
-                                    *reinterpret_cast<uint4 *>(place + rr * 128 + (((e / 4) ^ (rr & 7)) << 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                            } else {
+                            for (int e = 0; e < 32; e += 8) {
+                                uint32_t w[4];
 #pragma unroll
-                                for (int e = 0; e < 32; e += 8) {
-                                    uint32_t w[4];
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q)
-                                        w[q] = rw_pack(__uint_as_float(o[e + 2 * q]) * inv, __uint_as_float(o[e + 2 * q + 1]) * inv);
-                                    *reinterpret_cast<uint4 *>(place + rr * 128 + ((((d + e) / 8) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
+                                for (int q = 0; q < 4; ++q)
+                                    w[q] = rw_pack(__uint_as_float(o[e + 2 * q]) * inv, __uint_as_float(o[e + 2 * q + 1]) * inv);
+                                *reinterpret_cast<uint4 *>(place + rr * 128 + ((((d + e) / 8) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         }
                         if (full) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -865,11 +870,6 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                             rw_tma3_out(&omap, d0, it.g * r.G, it.u.start + it.u.tok0 + s * r.TT, smem_u32(place));
                             rw_out_commit();
                         }
-                    }
-                    if (dst) {
-                        float *const to = dst + static_cast<size_t>(s * kRwRows + rr) * Z::part;
-                        to[HD] = m2;
-                        to[HD + 1] = l;
                     }
                 }
                 if (bad) rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, s * kRwRows, (s + 1) * kRwRows, warp & 3, 4, kOff, dst);
@@ -890,7 +890,12 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 if (tid == 0) s_bad[0][turn_next] = 0;
                 rw_bar<256>(1);
                 const bool bad = *bad_flag;
-                if (!bad) {
+                if (!bad && dst) {
+#pragma unroll
+                    for (int d = 0; d < HD; ++d) dst[d * kRwRows + rr] = master[d];
+                    dst[HD * kRwRows + rr] = m2;
+                    dst[(HD + 1) * kRwRows + rr] = l;
+                } else if (!bad) {
                     float2 *const ml = reinterpret_cast<float2 *>(smem);
                     ml[s * kRwRows + rr] = make_float2(m2, l);
                     rw_bar<256>(1);
@@ -898,7 +903,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                     rw_bar<256>(1);
                     const float top = fmaxf(m2, other.x);
                     const float f0 = m2 == top ? 1.0f : rw_ex2(m2 - top), f1 = other.x == top ? 1.0f : rw_ex2(other.x - top);
-                    const float sum = l * f0 + other.y * f1, fac = dst ? f0 : sum == 0.0f ? 0.0f : f0 / sum;
+                    const float sum = l * f0 + other.y * f1, fac = sum == 0.0f ? 0.0f : f0 / sum;
                     auto at = [&](int d) {
                         return reinterpret_cast<float4 *>(smem + (d >> 5) * (kRwRows * 128) + rr * 128 + (((d >> 2 & 7) ^ (rr & 7)) << 4));
                     };
@@ -920,7 +925,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
 #pragma unroll
                         for (int d = HD / 2; d < HD; d += 4) join(d);
                     }
-                    const bool full = !dst && tokens >= r.TT;
+                    const bool full = tokens >= r.TT;
                     if (full) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     rw_bar<256>(1);
                     if (!full) {
@@ -933,13 +938,12 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                         rw_out_commit();
                         rw_out_read();
                     }
-                    if (dst && s == 0) {
-                        float *const to = dst + static_cast<size_t>(rr) * Z::part;
-                        to[HD] = top;
-                        to[HD + 1] = sum;
-                    }
                 } else {
-                    rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, 0, kRwRows, warp, 8, kOff, dst);
+                    if (dst && s == 1) {   // the first warpgroup's part is the whole, this one is nothing
+#pragma unroll 1
+                        for (int d = 0; d < HD + 2; ++d) dst[d * kRwRows + rr] = d == HD ? -INFINITY : 0.0f;
+                    }
+                    rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, 0, kRwRows, warp, 8, kOff, dst ? dst - s * Z::part : nullptr);
                 }
                 rw_bar<256>(1);   // (the next item's Q comes to this place)
             }
@@ -953,36 +957,43 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// A warp to a row of a unit that was split.
+// 32 rows of a unit that was split to a block: a lane to a row, a warp to a fourth
+// of the dimensions.
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) k_paged_rows_join(const RwArgs r) {
     using Z = RwSizes<T, HD>;
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5), unit = blockIdx.x;
+    constexpr int D = HD / 4, per = Z::split ? 2 : 1;
+    const int row = blockIdx.y * 32 + (threadIdx.x & 31), d0 = (threadIdx.x >> 5) * D, unit = blockIdx.x;
     pdl_wait();
     pdl_trigger();
     const RwCut cut = reinterpret_cast<const RwCut *>(r.ws)[unit];
-    const int rr = row % kRwRows, tok = row / kRwRows * r.TT + rr / r.G;
+    const int rr = row % kRwRows, tk = rr * r.g_inv >> 16, tok = row / kRwRows * r.TT + tk;
     if (cut.parts < 2 || rr >= r.TT * r.G || tok >= cut.tokens) return;
-    {
-        const float *src = r.ws + static_cast<size_t>(r.units) * 4 + (static_cast<size_t>(unit) * r.splits * (Z::QT * kRwRows) + row) * Z::part;
-        float m = -INFINITY, l = 0.0f, o[E];
+    const float *src = r.ws + static_cast<size_t>(r.units) * 4 + (static_cast<size_t>(unit) * r.splits * 2 + row / kRwRows) * Z::part + rr;
+    auto part = [&](int k) { return src + static_cast<size_t>(Z::split ? k : 2 * k) * Z::part; };
+    const int n = cut.parts * per;
+    float m = -INFINITY, l = 0.0f, o[D];
+    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[HD * kRwRows]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < cut.parts; ++k) {
-            const float *q = src + static_cast<size_t>(k) * (Z::QT * kRwRows) * Z::part;
-            const float mc = q[HD], lc = q[HD + 1], top = fmaxf(m, mc);
-            const float f0 = m == top ? 1.0f : rw_ex2(m - top), f1 = mc == top ? 1.0f : rw_ex2(mc - top);
-            l = l * f0 + lc * f1;
+    for (int e = 0; e < D; ++e) o[e] = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        const float *q = part(k);
+        const float mk = q[HD * kRwRows], f = mk == m ? 1.0f : rw_ex2(mk - m);
+        l = fmaf(q[(HD + 1) * kRwRows], f, l);
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + q[e * 32 + lane] * f1;
-            m = top;
-        }
-        T *to = static_cast<T *>(r.a.out) + static_cast<size_t>(cut.start + tok) * r.a.out_stride +
-                static_cast<size_t>(unit % r.a.c.nkv * r.G + rr % r.G) * HD;
+        for (int e = 0; e < D; ++e) o[e] = fmaf(q[(d0 + e) * kRwRows], f, o[e]);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T *to = static_cast<T *>(r.a.out) + static_cast<size_t>(cut.start + tok) * r.a.out_stride +
+            static_cast<size_t>(unit % r.a.c.nkv * r.G + rr - tk * r.G) * HD + d0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) to[e * 32 + lane] = kv_cvt<T>(l == 0.0f ? 0.0f : o[e] / l);
+    for (int e = 0; e < D; e += 16 / sizeof(T)) {
+        if constexpr (Z::split)
+            *reinterpret_cast<float4 *>(to + e) = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+        else
+            *reinterpret_cast<uint4 *>(to + e) = make_uint4(rw_pack(o[e] * inv, o[e + 1] * inv), rw_pack(o[e + 2] * inv, o[e + 3] * inv),
+                                                            rw_pack(o[e + 4] * inv, o[e + 5] * inv), rw_pack(o[e + 6] * inv, o[e + 7] * inv));
     }
 }
 
@@ -1020,7 +1031,7 @@ RwPlan rw_plan(int B, int M, int min_cols, int type, int nh, int nkv, int hd, in
     }
     if (p.splits > 1)
         p.bytes = static_cast<size_t>(p.units) * sizeof(RwCut) +
-                  static_cast<size_t>(p.units) * p.splits * (QT * kRwRows) * (hd + 4) * sizeof(float);
+                  static_cast<size_t>(p.units) * p.splits * 2 * (hd + 2) * kRwRows * sizeof(float);
     return p;
 }
 
@@ -1047,7 +1058,7 @@ cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, floa
     const RwArgs r{a, G, p.TT, (65536 + G - 1) / G, min_cols, p.split_tiles, p.splits, p.units, ws};
     if (join)
         return p.splits == 1 ? cudaSuccess
-                             : launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 4), 128, 0, 1, s, r);
+                             : launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 32), 128, 0, 1, s, r);
     const EncodeTiled encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
     // the pool as rows of HD values; a box is 64 values of the rows of a page that lie in one key tile
