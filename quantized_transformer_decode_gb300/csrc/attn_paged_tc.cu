@@ -957,43 +957,60 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// 32 rows of a unit that was split to a block: a lane to a row, a warp to a fourth
-// of the dimensions.
+// 32 rows and 32 dimensions of a unit that was split to a block: a lane to a row, a
+// warp to a fourth of the parts.
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) k_paged_rows_join(const RwArgs r) {
     using Z = RwSizes<T, HD>;
-    constexpr int D = HD / 4, per = Z::split ? 2 : 1;
-    const int row = blockIdx.y * 32 + (threadIdx.x & 31), d0 = (threadIdx.x >> 5) * D, unit = blockIdx.x;
+    __shared__ float s_o[4][33][32];   // the warps' outputs, and sums
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + lane, d0 = blockIdx.z * 32, unit = blockIdx.x;
     pdl_wait();
     pdl_trigger();
     const RwCut cut = reinterpret_cast<const RwCut *>(r.ws)[unit];
+    if (cut.parts < 2) return;
     const int rr = row % kRwRows, tk = rr * r.g_inv >> 16, tok = row / kRwRows * r.TT + tk;
-    if (cut.parts < 2 || rr >= r.TT * r.G || tok >= cut.tokens) return;
+    const bool real = rr < r.TT * r.G && tok < cut.tokens;
+    if (__all_sync(0xffffffffu, !real)) return;   // (the same in every warp)
     const float *src = r.ws + static_cast<size_t>(r.units) * 4 + (static_cast<size_t>(unit) * r.splits * 2 + row / kRwRows) * Z::part + rr;
     auto part = [&](int k) { return src + static_cast<size_t>(Z::split ? k : 2 * k) * Z::part; };
-    const int n = cut.parts * per;
-    float m = -INFINITY, l = 0.0f, o[D];
-    for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[HD * kRwRows]);
-#pragma unroll
-    for (int e = 0; e < D; ++e) o[e] = 0.0f;
-#pragma unroll 1
-    for (int k = 0; k < n; ++k) {
-        const float *q = part(k);
-        const float mk = q[HD * kRwRows], f = mk == m ? 1.0f : rw_ex2(mk - m);
-        l = fmaf(q[(HD + 1) * kRwRows], f, l);
-#pragma unroll
-        for (int e = 0; e < D; ++e) o[e] = fmaf(q[(d0 + e) * kRwRows], f, o[e]);
+    const int n = cut.parts * (Z::split ? 2 : 1);
+    float m = -INFINITY, l = 0.0f, o[32];
+    if (real) {
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) m = fmaxf(m, part(k)[HD * kRwRows]);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T *to = static_cast<T *>(r.a.out) + static_cast<size_t>(cut.start + tok) * r.a.out_stride +
-            static_cast<size_t>(unit % r.a.c.nkv * r.G + rr - tk * r.G) * HD + d0;
 #pragma unroll
-    for (int e = 0; e < D; e += 16 / sizeof(T)) {
-        if constexpr (Z::split)
-            *reinterpret_cast<float4 *>(to + e) = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
-        else
-            *reinterpret_cast<uint4 *>(to + e) = make_uint4(rw_pack(o[e] * inv, o[e + 1] * inv), rw_pack(o[e + 2] * inv, o[e + 3] * inv),
-                                                            rw_pack(o[e + 4] * inv, o[e + 5] * inv), rw_pack(o[e + 6] * inv, o[e + 7] * inv));
+    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+    if (real) {
+#pragma unroll 2
+        for (int k = warp; k < n; k += 4) {
+            const float *q = part(k);
+            const float mk = q[HD * kRwRows], f = mk == m ? 1.0f : rw_ex2(mk - m);
+            l = fmaf(q[(HD + 1) * kRwRows], f, l);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(q[(d0 + e) * kRwRows], f, o[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s_o[warp][e][lane] = o[e];
+    s_o[warp][32][lane] = l;
+    __syncthreads();
+    if (!real) return;
+    l = (s_o[0][32][lane] + s_o[1][32][lane]) + (s_o[2][32][lane] + s_o[3][32][lane]);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float v[8];   // a warp to 8 dimensions
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int d = warp * 8 + e;
+        v[e] = ((s_o[0][d][lane] + s_o[1][d][lane]) + (s_o[2][d][lane] + s_o[3][d][lane])) * inv;
+    }
+    T *to = static_cast<T *>(r.a.out) + static_cast<size_t>(cut.start + tok) * r.a.out_stride +
+            static_cast<size_t>(unit % r.a.c.nkv * r.G + rr - tk * r.G) * HD + d0 + warp * 8;
+    if constexpr (Z::split) {
+        *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(rw_pack(v[0], v[1]), rw_pack(v[2], v[3]), rw_pack(v[4], v[5]), rw_pack(v[6], v[7]));
     }
 }
 
@@ -1058,7 +1075,7 @@ cudaError_t rows_t(const KvPagedAttnArgs &a, int min_cols, const RwPlan &p, floa
     const RwArgs r{a, G, p.TT, (65536 + G - 1) / G, min_cols, p.split_tiles, p.splits, p.units, ws};
     if (join)
         return p.splits == 1 ? cudaSuccess
-                             : launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 32), 128, 0, 1, s, r);
+                             : launch_pdl(pdl, k_paged_rows_join<T, HD>, dim3(p.units, Z::QT * kRwRows / 32, HD / 32), 128, 0, 1, s, r);
     const EncodeTiled encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
     // the pool as rows of HD values; a box is 64 values of the rows of a page that lie in one key tile
