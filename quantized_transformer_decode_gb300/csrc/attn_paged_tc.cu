@@ -636,8 +636,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 if (i + kStep < NT) there = look(i + kStep);
                 // does every row of the tile see every position?
                 const bool open = !holes && j0 + kRwKeys - 1 <= smin && (a.window == 0 || smax - j0 < a.window || j0 + kRwKeys <= a.sinks);
+                wait(&b_s[s], ns + own);
+                rw_after();
                 if (!open) {
-                    // V: this thread's position
+                    // V: this thread's position. (Behind the wait for the scores: they say that every fill before their K
+                    // has come, and only then does the parity of V's barrier tell this fill from the one before the last.)
                     const int n = done + fill_of_v(i, NT), st = n % ST, j = j0 + rr;
                     const bool page = pages >> (rr >> 4) & 1;
                     const bool any = page && j <= pmax && kv_sees(max(j, pmin), j, a.window, a.sinks);
@@ -664,8 +667,6 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                     if (bad) *bad_flag = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                wait(&b_s[s], ns + own);
-                rw_after();
                 // the row's positions j0 + k, k in [k_lo, k_hi) or [0, k_sink), of pages that are there: bits of 32 positions
                 const int k_hi = p - j0 + 1, k_lo = a.window > 0 ? p - a.window + 1 - j0 : 0, k_sink = a.window > 0 ? a.sinks - j0 : 0;
                 auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
