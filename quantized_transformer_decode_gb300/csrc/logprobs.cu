@@ -301,12 +301,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LogprobArgs a,
                     __shfl_xor_sync(0xffffffffu, part.w, o));
     if (lane == 0) s.warp[tid >> 5] = part;
     __syncthreads();
-    part = s.warp[lane % kLpWarps];
-#pragma unroll
-    for (int o = kLpWarps / 2; o > 0; o >>= 1)
-        lp_join_all(part, __shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.r, o),
-                    __shfl_xor_sync(0xffffffffu, part.w, o));
-    if (part.r < 1.25f && part.r > 0.0f) {   // (all threads: they have joined the same parts)
+    part = s.warp[0];
+    for (int i = 1; i < kLpWarps; ++i) lp_join_all(part, s.warp[i].m, s.warp[i].r, s.warp[i].w);
+    // (every thread has joined the same parts in the same order: to the last bit all of them go the same way)
+    if (part.r < 1.25f && part.r > 0.0f) {
         float rest = own.m == part.m ? 0.0f : own.r * lp_exp(own.m - part.m);
         if (__any_sync(0xffffffffu, own.m == part.m)) {
             // the thread with the maximum (there is one: a second would make the sum 2): its logits, a lane to a word
