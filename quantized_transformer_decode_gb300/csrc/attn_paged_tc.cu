@@ -28,8 +28,15 @@
 // one that only some rows see is not finite the unit is done again without
 // matrix products (k_rows' slow path).
 //
-// Bound by the tensor cores for long prompts. Few units are split along the keys
-// and joined by a second kernel.
+// CTAs stay and take the units to and fro, longest first; the next unit's Q comes
+// by TMA while the last one's rows go out by TMA. Few units are split along the
+// keys and joined by a second kernel.
+//
+// Bound by the tensor cores, and nearly as much by shared memory, which holds both
+// operands of the first product and one of the second: a 128 x 128 x 16 product
+// takes 83 cycles (plain library products 79, the peak rate 64). A prompt of 4096
+// tokens with 32 query and 8 kv heads of 128, f16: 107 us, 1.28 PFLOP/s. 509 rows
+// behind 7680 positions, f32 (twice the products, 128 units on 152 SMs): 99 us.
 #include <algorithm>
 #include <cstdint>
 

@@ -230,11 +230,15 @@ cudaError_t append_t(const KvPagedAppendArgs &a, bool pdl, cudaStream_t s) {
 // setting pairs of positions side by side (one byte permutation to a register).
 // tcgen05.mma has no part here: a tile of 128 rows would be filled by 2 to 16,
 // and reading K and V is what takes the time, not the products.
+//
+// Bound by HBM: 64 sequences of 1 to 4101, 16/8 heads of 128, f32 (537 MB) take 98
+// us, 0.81 of the copy rate; one of 32768, 32/8 heads, f16 (134 MB) 34 us with its
+// join, 0.58. Short ones by the latency of a warp's steps: 517 positions 9.9 us.
 
 constexpr int kTokWarps = 8, kTokStages = 3, kTokKeys = 16;
 // What a unit's ends cost, in steps (loading its queries, joining the warps),
-// where there are more units than CTAs: 64 sequences of 1 to 4101 take 127 us
-// with 0, 104 with 10, 93.6 with 24, 95.2 with 40. Fewer units: a CTA has two at
+// where there are more units than CTAs: 64 sequences of 1 to 4101 take 135 us
+// with 0, 112 with 10, 98 with 24, 99 with 40. Fewer units: a CTA has two at
 // most, and shares may be short.
 constexpr int kTokUnit = 24;
 // Few short units: a CTA to each, and nothing to join. (One token of one sequence,

@@ -97,6 +97,7 @@ def attn(L, c, b, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(type=5), ARG), (dict(q=None), ARG), (dict(q=8), ARG), (dict(out=None), ARG), (dict(out=4), ARG), (dict(M=-1), ARG),
     (dict(stride=252), SHAPE), (dict(stride=258), ARG), (dict(ostride=255), SHAPE), (dict(type=1, ostride=260), ARG),
+    (dict(stride=260), SHAPE), (dict(ostride=260), SHAPE), (dict(type=1, stride=264), SHAPE),  # not whole heads
     (dict(nh=5), SHAPE), (dict(max_rows=5), ARG), (dict(max_rows=-1), ARG), (dict(max_len=65), OVERFLOW), (dict(max_len=-1), ARG),
     (dict(window=-1), ARG), (dict(sinks=-2), ARG), (dict(scale=float("inf")), ARG), (dict(scale=float("nan")), ARG),
     (dict(ws=8), ARG), (dict(status=6), ARG), (dict(M=2 ** 30, max_rows=1), SHAPE),
