@@ -166,7 +166,9 @@ __device__ __forceinline__ void lp_push(LpShared &s, float x, int i) {
 
 // Row blockIdx.x / C in C slices. Slices begin at whole 16-byte words of the
 // row's memory; the up to 3 logits before the first and after the last word are
-// taken one by one by rank 0.
+// taken one by one by rank 0, behind its slice: no bound for the slice may come
+// from them. (A logit that equals the bound is left out because what set the bound
+// has lower indices, and the row's last ones have the highest.)
 __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LogprobArgs a, int C) {
     __shared__ LpShared s;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LogprobArgs a,
         for (int k = 0; k < N; ++k) v[k] = next[k];
         load(next, base + kLpThreads * kLpChunk);
         const bool begin = base == w0;
-        float mx = begin ? lone_x : -INFINITY;
+        float mx = -INFINITY;
 #pragma unroll
         for (int k = 0; k < N; ++k) mx = fmaxf(mx, v[k]);
         {
@@ -231,23 +233,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LogprobArgs a,
                 r[k & 1] += e;
                 w[k & 1] = fmaf(e, fmaxf(dk, -1000.0f), w[k & 1]);   // (0 * -inf is no part of the sum; NaN: e keeps it)
             }
-            if (begin) {
-                const float dk = lone_x - m, e = lp_ex2(dk * kLog2e);
-                r[0] += e;
-                w[0] = fmaf(e, fmaxf(dk, -1000.0f), w[0]);
-            }
             part = {m, r[0] + r[1], w[0] + w[1]};
         }
         if (a.top > 0) {
             if (begin) {
-                int id = lone >= 0 && lone_x == mx ? lone : 0x7fffffff;
+                int id = 0x7fffffff;
 #pragma unroll
                 for (int k = N - 1; k >= 0; --k)
                     if (v[k] == mx) id = min(id, head + 4 * (base + (k >> 2) * kLpThreads + tid) + (k & 3));
                 const unsigned long long least = lp_bound(s, a.top, mx > -INFINITY ? lp_key(mx, id) : 0, turn);
                 turn ^= 1;
                 bound = least ? lp_value(least) : -INFINITY;
-                if (lone_x > -INFINITY && lp_key(lone_x, lone) >= least) lp_push(s, lone_x, lone);
                 if (mx >= bound) {
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
@@ -267,6 +263,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LogprobArgs a,
         }
     }
 
+    if (lone >= 0) {
+        const float m = fmaxf(part.m, lone_x), d = fmaxf(part.m - m, -1000.0f), f = lp_ex2(d * kLog2e);
+        const float dk = lone_x - m, e = lp_ex2(dk * kLog2e);
+        part = {m, fmaf(part.r, f, e), fmaf(e, fmaxf(dk, -1000.0f), f * (part.w + d * part.r))};
+        if (a.top > 0 && lone_x > -INFINITY && lone_x >= bound) lp_push(s, lone_x, lone);
+    }
     if (!one) cluster_wait_acquire();
     if (a.top > 0) {
         if (chunk > 1) raise();

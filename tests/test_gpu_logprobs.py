@@ -225,3 +225,39 @@ def test_refusals(torch):
                  lambda: qw3.logprobs(x[:, :0], t), lambda: qw3.logprobs(x, t.view(3, 1, 1))):
         with pytest.raises(qw3.Qw3Error):
             call()
+
+
+@pytest.mark.parametrize("top", [1, 5, 64])
+@pytest.mark.parametrize("first", [0, 1, 2, 3])
+@pytest.mark.parametrize("B,V", [(1, 50257), (2, 50258), (3, 50259), (300, 9001), (301, 9002), (302, 9003)])
+def test_equal_logits_at_a_rows_end(torch, B, V, first, top):
+    """The last of the alternatives is one of several equal logits, the row's last three among them: the lowest index, in
+    one CTA to a row and in several, wherever the row begins in a 16-byte word."""
+    g = np.random.default_rng(B + first)
+    x = np.full((B, V), -9.0) - g.random((B, V))
+    for i, r in enumerate(x):
+        # (behind what a CTA reads at first, and, with several of them to a row, within the first one's slice)
+        inner = g.choice(np.arange(4200, min(V - 3, 6200)), 3 + i % 2, replace=False)
+        r[[1, 700, 4199]] = 7.0, 6.5, 6.0
+        r[g.choice(np.arange(2000, 4000), 80, replace=False)[:max(0, top - 4)]] = 6.25
+        r[inner] = 5.0
+        r[V - 3 + i % 3:] = 5.0
+    if top == 1:
+        x[:, [1, 700, 4199]] = -9.0
+    x = x.astype(np.float32)
+    wide = torch.full((B + 1, V + 1), float("nan"), device="cuda")
+    view = wide.flatten()[first:first + B * (V + 1)].as_strided((B, V), (V + 1, 1))   # (each row begins 4 bytes further in a word)
+    view.copy_(torch.from_numpy(x))
+    check(torch, x, tokens=np.full((B, 1), V - 1, np.int32), top=top, dev=view)
+
+
+@pytest.mark.parametrize("B,V", [(1, 151937), (1, 30003), (300, 20002)])
+def test_ties_of_coarse_logits(torch, B, V):
+    """Logits in steps of 1/4, as from a narrower type: every place of the list is tied; and rising ones, whose list overflows,
+    with the row's end as large as the ones before it."""
+    x = np.round(rows(B, V, V) * 4) / 4
+    x[:, -2:] = np.sort(x, -1)[:, -20:-19]
+    check(torch, x, top=20)
+    x = np.tile(np.arange(V) // 50 * 0.01, (B, 1)).astype(np.float32)
+    x[:, -1] = x[:, -70]
+    check(torch, x, tokens=np.full((B, 1), V - 1, np.int32), top=64)
