@@ -610,7 +610,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                     split8_f16(v, hi, lo);
                     *reinterpret_cast<uint4 *>(to) = hi;
                     *reinterpret_cast<uint4 *>(to + Z::tile) = lo;
-                    if (ch == 0) s_c[row] = pow2_f32(-ex) * c0;
+                    // (never 0: -inf times it has to stay -inf. At 2^-126 every score is 0 to the last bit: they are below 2^38.)
+                    if (ch == 0) s_c[row] = fmaxf(pow2_f32(-ex) * c0, 0x1p-126f);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 if (NT > 0) mbar_arrive(&b_q);

@@ -416,6 +416,17 @@ def test_queries_of_any_size(torch):
         b.check(b.attend(scale=1e38), scale=np.float64(np.float32(1e38)))
 
 
+def test_rows_of_zeros_at_any_scale(torch):
+    """A query row of zeros (as append leaves one) has equal scores, however small the scale."""
+    for rows in (1, 70):
+        for kw in ({}, dict(window=40, sinks=2)):
+            b = Batch(torch, [(rows, 150), (rows, rows)], nh=4, nkv=2, hd=64)
+            b.q[0] = 0
+            b.q[rows // 2 + rows:] = 0
+            for scale in (1e-38, 1e-20, 1e-8, 1.0):
+                b.check(b.attend(scale=scale, **kw), scale=np.float64(np.float32(scale)), **kw)
+
+
 def test_offsets_past_32_bits(torch):
     """Pages beyond 2^32 bytes of the pool."""
     from quantized_transformer_decode_gb300 import qw3
