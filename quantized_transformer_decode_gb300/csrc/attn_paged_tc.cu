@@ -216,7 +216,7 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
         float x[E], o[E], m = -INFINITY, l = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            x[e] = kv_f32(q[e]);
+            x[e] = kv_f32(q[e]) * (a.scale * 1.4426950408889634f);   // (before the sum, which large queries would take out of f32)
             o[e] = 0.0f;
         }
         for (int i = i0; i < i1; ++i) {
@@ -229,7 +229,7 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
                 float d = 0.0f;
 #pragma unroll
                 for (int e = 0; e < E; ++e) d = fmaf(x[e], kv_f32(k[e]), d);
-                d = warp_sum(d) * (a.scale * 1.4426950408889634f);
+                d = warp_sum(d);
                 const float mn = d > m ? d : m, c = m == mn ? 1.0f : rw_ex2(m - mn), w = rw_ex2(d - mn + off);
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[e] = fmaf(w, kv_f32(v[e]), o[e] * c);

@@ -416,6 +416,15 @@ def test_queries_of_any_size(torch):
         b.check(b.attend(scale=1e38), scale=np.float64(np.float32(1e38)))
 
 
+def test_queries_of_any_size_beside_infinities(torch):
+    """f32 queries at the type's ends, where what rows see is not finite and they are done without matrix products."""
+    for size, scale in ((3e38, 1e-38), (1e-38, 1e38)):
+        b = Batch(torch, [(90, 200)], nh=4, nkv=2, hd=64, seed=13)
+        b.q = (b.q.astype(np.float64) / 8 * size).clip(-3.3e38, 3.3e38).astype(np.float32)
+        b.data[b.table[0, 150 // 16], 1, 0, 150 % 16, 9] = np.inf      # rows 40 .. 89 see it
+        b.check(b.attend(scale=scale), scale=np.float64(np.float32(scale)))
+
+
 def test_rows_of_zeros_at_any_scale(torch):
     """A query row of zeros (as append leaves one) has equal scores, however small the scale."""
     for rows in (1, 70):
