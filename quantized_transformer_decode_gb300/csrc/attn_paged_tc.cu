@@ -26,7 +26,7 @@
 // What a row does not see must not reach it, and 0 * NaN would: in a tile that
 // is not seen whole, V rows that no row of the unit sees are set to zero, and if
 // one that only some rows see is not finite the unit is done again without
-// matrix products (k_rows' slow path).
+// matrix products (rw_slow).
 //
 // CTAs stay and take the units to and fro, longest first; the next unit's Q comes
 // by TMA while the last one's rows go out by TMA. Few units are split along the
@@ -161,13 +161,23 @@ __device__ __forceinline__ void rw_tma(uint32_t to, const CUtensorMap *map, int 
                  ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
 // A bounded wait that gives up with the others: *err is set by the first that ran
-// out, and looked at by those that have to wait.
-__device__ __forceinline__ void rw_wait(uint64_t *bar, int parity, volatile int *err) {
+// out, and looked at by those that have to wait. A warpgroup that does its rows
+// without matrix products may be long about it: while *beat grows the wait's time
+// begins anew (Beat: where the wait may be for such a warpgroup).
+template <bool Beat>
+__device__ __forceinline__ void rw_wait(uint64_t *bar, int parity, volatile int *err, volatile int *beat) {
     if (mbar_try_wait(bar, static_cast<uint32_t>(parity & 1))) return;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
+    int heard = Beat ? *beat : 0;
     while (!mbar_try_wait(bar, static_cast<uint32_t>(parity & 1))) {
         if (*err) return;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) *err = 1;
+        const int now = Beat ? *beat : 0;
+        if (now != heard) {
+            heard = now;
+            t0 = globaltimer_ns();
+        } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *err = 1;
+        }
     }
 }
 __device__ __forceinline__ void rw_tma3(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
@@ -199,12 +209,14 @@ __device__ __forceinline__ RwTiles rw_tiles(int pmin, int pmax, int window, int 
 }
 
 // Rows row0 .. row1 - 1 of the unit without matrix products, for the tiles i0 .. i1
-// - 1: warp `warp` of `warps`, a row at a time. dst: the part, or null for the
-// output.
+// - 1: warp `warp` of `warps`, a row at a time, 4 positions at once (8 would cost the
+// f32 kernel, which keeps its registers over the call, 130 bytes of spills). dst: the
+// part, or null for the output. *beat grows with every tile of a row (the other
+// roles' waits go on as long as it does).
 template <typename T, int HD>
 __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwTiles &t, int i0, int i1, int g, int row0, int row1,
-                                     int warp, int warps, float off, float *dst) {
-    constexpr int E = HD / 32;
+                                     int warp, int warps, float off, float *dst, int *beat) {
+    constexpr int E = HD / 32, N = 4;
     const int lane = threadIdx.x & 31;
     const KvPagedAttnArgs &a = r.a;
     for (int row = row0 + warp; row < row1; row += warps) {
@@ -219,21 +231,51 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
             x[e] = kv_f32(q[e]) * (a.scale * 1.4426950408889634f);   // (before the sum, which large queries would take out of f32)
             o[e] = 0.0f;
         }
+        auto halves = [](float (&y)[E], const __half *src) {   // E values, as one word or two
+            if constexpr (E == 4) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                const float2 f = rw_unpack(w.x), z = rw_unpack(w.y);
+                y[0] = f.x; y[1] = f.y; y[2] = z.x; y[3] = z.y;
+            } else {
+                const float2 f = rw_unpack(*reinterpret_cast<const uint32_t *>(src));
+                y[0] = f.x; y[1] = f.y;
+            }
+        };
         for (int i = i0; i < i1; ++i) {
-            const int j0 = t.key(i);
-            for (int j = j0; j < j0 + kRwKeys; ++j) {
-                if (!kv_sees(p, j, a.window, a.sinks)) continue;
-                const int page = kv_page(a.b, a.c, u.seq, j);
+            if (lane == 0) atomicAdd(beat, 1);
+            const int end = min(t.key(i) + kRwKeys - 1, p);
+            int page = -1;
+#pragma unroll 1
+            for (int j0 = t.key(i); j0 <= end; j0 += N) {
+                if (j0 % 16 == 0) page = kv_page(a.b, a.c, u.seq, j0);   // (16 positions lie in one)
                 if (page < 0) continue;
-                const __half *k = kv_paged_row<HD>(a.c, page, 0, g, j) + lane * E, *v = kv_paged_row<HD>(a.c, page, 1, g, j) + lane * E;
-                float d = 0.0f;
+                const __half *k = kv_paged_row<HD>(a.c, page, 0, g, j0) + lane * E, *v = kv_paged_row<HD>(a.c, page, 1, g, j0) + lane * E;
+                float d[N], mn = m;
 #pragma unroll
-                for (int e = 0; e < E; ++e) d = fmaf(x[e], kv_f32(k[e]), d);
-                d = warp_sum(d);
-                const float mn = d > m ? d : m, c = m == mn ? 1.0f : rw_ex2(m - mn), w = rw_ex2(d - mn + off);
+                for (int n = 0; n < N; ++n) {
+                    float y[E];
+                    halves(y, k + n * HD);
+                    d[n] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(w, kv_f32(v[e]), o[e] * c);
-                l = fmaf(l, c, w);
+                    for (int e = 0; e < E; ++e) d[n] = fmaf(x[e], y[e], d[n]);
+                    d[n] = warp_sum(d[n]);
+                    if (!kv_sees(p, j0 + n, a.window, a.sinks)) d[n] = -INFINITY;
+                    mn = d[n] > mn ? d[n] : mn;
+                }
+                const float c = m == mn ? 1.0f : rw_ex2(m - mn);
+                l *= c;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] *= c;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    float y[E];
+                    halves(y, v + n * HD);
+                    if (!kv_sees(p, j0 + n, a.window, a.sinks)) continue;   // (whatever y is)
+                    const float w = rw_ex2(d[n] - mn + off);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = fmaf(w, y[e], o[e]);
+                    l += w;
+                }
                 m = mn;
             }
         }
@@ -305,7 +347,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     extern __shared__ uint8_t rw_smem[];
     __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q, b_q_free;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_err, s_bad[2][3];
+    __shared__ int s_err, s_beat, s_bad[2][3];
     __shared__ float s_c[kRwRows];
     const KvPagedAttnArgs &a = r.a;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -326,7 +368,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         mbar_init(&b_q, Z::split ? 256 : 1);
         mbar_init(&b_q_free, 1);
         fence_mbar_init();
-        s_err = 0;
+        s_err = s_beat = 0;
     }
     if (warp == 9) {   // (nothing else holds tensor memory here: no two of these CTAs fit an SM)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
@@ -344,7 +386,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     const float c0 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
     const uint32_t ring = base + 2 * Z::tile;
     volatile int *err = &s_err;
-    auto wait = [&](uint64_t *bar, int parity) { rw_wait(bar, parity, err); };
+    auto wait = [&](uint64_t *bar, int parity) { rw_wait<true>(bar, parity, err, &s_beat); };
     RwCut *const cuts = reinterpret_cast<RwCut *>(r.ws);
     // Item k of this CTA: the items (parts of units, long ones first) go to the CTAs to and fro, so that the lengths
     // add up to about the same. Every role walks through them by itself; false behind the last one.
@@ -547,6 +589,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         const uint32_t tS = tmem + lanes + s * 128, tO = tmem + lanes + 256 + s * HD;
         constexpr float kOff = Z::split ? kRwOff32 : kRwOff16;
         constexpr int kStep = Z::split ? 2 : 1;
+        // (f32: the warpgroups go the long way together, and what they wait for is not each other)
+        auto wait = [&](uint64_t *bar, int parity) { rw_wait<!Z::split>(bar, parity, err, &s_beat); };
         RwFind f;
         RwItem it;
         int done = 0, ns = 0, no = 0;   // fills, tiles of S, outputs, of the items before
@@ -881,7 +925,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                         }
                     }
                 }
-                if (bad) rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, s * kRwRows, (s + 1) * kRwRows, warp & 3, 4, kOff, dst);
+                if (bad) rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, s * kRwRows, (s + 1) * kRwRows, warp & 3, 4, kOff, dst, &s_beat);
             } else {
                 if (own > 0) {
 #pragma unroll
@@ -952,7 +996,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
 #pragma unroll 1
                         for (int d = 0; d < HD + 2; ++d) dst[d * kRwRows + rr] = d == HD ? -INFINITY : 0.0f;
                     }
-                    rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, 0, kRwRows, warp, 8, kOff, dst ? dst - s * Z::part : nullptr);
+                    rw_slow<T, HD>(r, it.u, it.tiles, it.i0, it.i0 + NT, it.g, 0, kRwRows, warp, 8, kOff, dst ? dst - s * Z::part : nullptr, &s_beat);
                 }
                 rw_bar<256>(1);   // (the next item's Q comes to this place)
             }

@@ -344,6 +344,48 @@ def test_what_is_not_seen_has_no_part(torch, seqs, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_long_rows_beside_what_is_not_finite(torch, dtype):
+    """Rows that are done without matrix products, for longer than a wait in the kernel may last that nothing ends: no
+    status, and the right outputs. (304 units, two to a CTA, so that the CTA's other warps wait for the first one's rows, some
+    1.6 s where the limit is 1 s.)"""
+    from quantized_transformer_decode_gb300 import qw3
+    f16 = dtype == "f16"
+    B, rows, nh, hd, page, pages = 304, 16 if f16 else 8, 16, 64, 256, 384 if f16 else 768
+    n = pages * page - 7
+    g = torch.Generator(device="cuda").manual_seed(1)
+    data = torch.randn(pages, 2, 1, page, hd, generator=g, device="cuda").half()
+    hole = n - rows // 2            # the first half of the rows does not see it
+    data[hole // page, 1, 0, hole % page, 9] = float("inf")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(B, 1)          # every sequence holds the same
+    q1 = torch.randn(rows, nh, hd, generator=g, device="cuda").to(torch.float16 if f16 else torch.float32)
+    starts = torch.arange(B + 1, dtype=torch.int32, device="cuda") * rows
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = qw3.KVCachePaged(pages, page, 1, hd, data=data)
+    q = q1.repeat(B, 1, 1)
+    out = cache.attention(q, starts, lens, table, max_rows=rows, max_len=n, status=status)
+    assert int(status) == 0
+    out = out.view(B, rows, nh, hd).double()
+    assert (out == out[:1]).logical_or(out.isnan() & out[:1].isnan()).all()
+    k, v = data[:, 0, 0].reshape(-1, hd)[:n].double(), data[:, 1, 0].reshape(-1, hd)[:n].double()
+    v[hole, 9] = 0
+    for r in range(rows):
+        seen = n - rows + r + 1
+        s = q1[r].double() @ k[:seen].T * hd ** -0.5
+        p = torch.softmax(s, -1)
+        want = p @ v[:seen]
+        err = {"pv": (p @ v[:seen].abs()).cpu().numpy(), "qk": (q1[r].double().abs() @ k[:seen].abs().T).amax(-1, keepdim=True).cpu().numpy() * hd ** -0.5,
+               "vmax": float(v.abs().max()), "n": np.float64(16)}
+        # (a row's sums are chains of n roundings of 2^-24, random in sign: 16 sqrt(n) of them with room)
+        lim = ref.bound(err, want.cpu().numpy(), hd, f16) + 16 * n ** 0.5 * 2.0 ** -24 * err["pv"]
+        got = out[0, r].cpu().numpy()
+        if n - rows + r >= hole:
+            assert np.isposinf(got[:, 9]).all()
+            got[:, 9] = want[:, 9].cpu().numpy()
+        assert (np.abs(got - want.cpu().numpy()) <= lim).all(), (r, np.abs(got - want.cpu().numpy()).max(), lim.min())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
 def test_rows_outside_the_batch_stay(torch, dtype):
     b = Batch(torch, [(3, 40), (70, 90), (1, 5)], dtype=dtype, lead=2, tail=5)
     out = torch.full((b.M, b.nh, b.hd), 9.0, dtype=b.dtype, device="cuda")
