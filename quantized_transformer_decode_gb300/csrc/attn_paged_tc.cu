@@ -426,15 +426,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         RwFind f;
         RwItem it;
         if (warp != 9) {
-            // ---- loads: three warps take turns, a lane to a page of the tile; the first one sees to Q and to the cuts
+            // ---- loads: three warps take turns, a lane to a page of the tile; the first one sees to Q, and at last to the cuts
             const int turn = warp == 8 ? 0 : warp - 9;
             const int shift = min(a.c.shift, 7), boxes = kRwKeys >> shift;
             const uint32_t bytes = static_cast<uint32_t>(HD * 2) << shift;
             int done = 0, nq = 0;   // fills, and Qs, of the items before
             bool ok = true;
             for (int k = 0; ok && item(k, f, it); ++k) {
-                if (turn == 0 && lane == 0 && it.part == 0 && r.splits > 1)
-                    cuts[it.unit] = RwCut{it.u.start + it.u.tok0, it.tokens, it.parts, 0};
                 if (it.NT == 0) continue;
                 if (!Z::split && turn == 0) {
                     if (nq > 0) wait(&b_q_free, nq - 1);
@@ -475,11 +473,16 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 }
                 if (ok) done += 2 * it.NT;
             }
-            // units that are not there
-            if (turn == 0 && lane == 0 && r.splits > 1)
-                for (int k = 0; number(k) < items; ++k)
-                    if (number(k) % r.splits == 0 && number(k) / r.splits / a.c.nkv >= f.before && f.b0 >= a.b.B)
-                        cuts[number(k) / r.splits] = RwCut{0, 0, 0, 0};
+            // the cuts, of units that are not there too: all of them, whatever has become of the loads, because the join
+            // goes by them
+            if (turn == 0 && r.splits > 1) {
+                RwFind all;
+                int k = 0;
+                for (; item(k, all, it); ++k)
+                    if (lane == 0 && it.part == 0) cuts[it.unit] = RwCut{it.u.start + it.u.tok0, it.tokens, it.parts, 0};
+                for (; number(k) < items; ++k)
+                    if (lane == 0 && number(k) % r.splits == 0) cuts[number(k) / r.splits] = RwCut{0, 0, 0, 0};
+            }
             // the CTA may end when every copy has landed, and every stage has been released
             if (ok) {
                 for (int n = max(0, done - ST); n < done; ++n)

@@ -547,6 +547,26 @@ def test_units_of_one_row_tile_among_longer_ones(torch, dtype):
         assert int(differ) == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("seqs,tail", [([(100, 6000)], 300), ([(100, 6000), (1, 300)], 300), ([(0, 40), (70, 5000), (0, 0)], 500)])
+def test_units_that_are_not_there(torch, seqs, tail, dtype):
+    """Bounds of more rows than the sequences have, in a call that is split: what the join reads of the units that could be is
+    written, whatever the workspace held."""
+    from quantized_transformer_decode_gb300 import qw3
+    b = Batch(torch, seqs, nh=4, nkv=2, hd=64, dtype=dtype, tail=tail)
+    n = max(n for _, n in seqs)
+    need = qw3.qw3_kv_paged_attn_workspace_bytes(len(seqs), b.M, int(b.f16), 4, 2, 64, b.M, n)
+    assert need > 1 << 20       # (units are split)
+    first = None
+    for fill in (0, 1, 0x7F):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.full((b.M, 4, 64), 9.0, dtype=b.dtype, device="cuda")
+        _, written = b.check(b.attend(out=out, max_rows=b.M, max_len=n, workspace=ws))
+        assert (out[~torch.from_numpy(written).cuda()] == 9).all()
+        assert first is None or torch.equal(out, first)
+        first = out
+
+
 def test_two_at_once(torch):
     """Calls on two streams, each with its own workspace."""
     bs = [Batch(torch, [(1, 4000), (200, 1500)], nh=16, nkv=8, hd=128, dtype="f16", seed=i) for i in range(2)]
