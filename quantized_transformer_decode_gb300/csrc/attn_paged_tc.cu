@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     using Z = RwSizes<T, HD>;
     constexpr int ST = Z::stages, QT = Z::QT;
     extern __shared__ uint8_t rw_smem[];
-    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q, b_q_free;
+    __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q, b_q_free, b_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_err, s_beat, s_bad[2][3];
     __shared__ float s_c[kRwRows];
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         }
         mbar_init(&b_q, Z::split ? 256 : 1);
         mbar_init(&b_q_free, 1);
+        mbar_init(&b_end, 1);
         fence_mbar_init();
         s_err = s_beat = 0;
     }
@@ -431,11 +432,16 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             const int shift = min(a.c.shift, 7), boxes = kRwKeys >> shift;
             const uint32_t bytes = static_cast<uint32_t>(HD * 2) << shift;
             int done = 0, nq = 0;   // fills, and Qs, of the items before
+            int last = -1;          // this warp's last fill
             bool ok = true;
             for (int k = 0; ok && item(k, f, it); ++k) {
                 if (it.NT == 0) continue;
                 if (!Z::split && turn == 0) {
                     if (nq > 0) wait(&b_q_free, nq - 1);
+                    if (__any_sync(0xffffffffu, *err != 0)) {
+                        ok = false;
+                        break;
+                    }
                     if (lane == 0) {
                         const int two = it.tokens > r.TT ? 2 : 1;
                         mbar_arrive_expect_tx(&b_q, two * (HD * 2) * r.G * r.TT);
@@ -462,6 +468,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                         break;
                     }
                     const int held = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                    last = all;
                     if (lane == 0) mbar_arrive_expect_tx(&b_full[st], held * bytes);
                     __syncwarp();
                     if (page >= 0) {
@@ -487,11 +494,10 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             if (ok) {
                 for (int n = max(0, done - ST); n < done; ++n)
                     if (n % 3 == turn) wait(&b_empty[n % ST], n / ST);
-            } else {   // (copies in flight: as long as a second for each stage)
-                for (int st = 0; st < ST; ++st) {
-                    (void)mbar_wait_bounded(&b_full[st], 0);
-                    (void)mbar_wait_bounded(&b_full[st], 1);
-                }
+            }
+            if (__any_sync(0xffffffffu, *err != 0)) {   // (given up, here or elsewhere: then for a second at most to a copy)
+                for (int n = last; n >= 0 && n > last - 3 * ST; n -= 3) (void)mbar_wait_bounded(&b_full[n % ST], n / ST & 1);
+                if (nq > 0) (void)mbar_wait_bounded(&b_q, nq - 1 & 1);
             }
         } else {
             // ---- products: the whole warp walks along, one lane issues
@@ -1009,6 +1015,10 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     }
     __syncthreads();
     if (tid == 0 && s_err) record_status(a.status, QW3_ERR_TIMEOUT);
+    if (warp == 9 && s_err) {   // products that nobody has waited for end before their memory is given back
+        if (rw_elect()) rw_commit(&b_end);
+        (void)mbar_wait_bounded(&b_end, 0);
+    }
     rw_after();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
