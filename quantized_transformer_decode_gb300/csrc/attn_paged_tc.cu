@@ -162,22 +162,16 @@ __device__ __forceinline__ void rw_tma(uint32_t to, const CUtensorMap *map, int 
 }
 // A bounded wait that gives up with the others: *err is set by the first that ran
 // out, and looked at by those that have to wait. A warpgroup that does its rows
-// without matrix products may be long about it: while *beat grows the wait's time
-// begins anew (Beat: where the wait may be for such a warpgroup).
+// without matrix products may be long about it: the limit counts from the last time
+// that it wrote to *beat (Beat: where the wait may be for such a warpgroup).
 template <bool Beat>
-__device__ __forceinline__ void rw_wait(uint64_t *bar, int parity, volatile int *err, volatile int *beat) {
+__device__ __forceinline__ void rw_wait(uint64_t *bar, int parity, volatile int *err, volatile int64_t *beat) {
     if (mbar_try_wait(bar, static_cast<uint32_t>(parity & 1))) return;
-    uint64_t t0 = globaltimer_ns();
-    int heard = Beat ? *beat : 0;
+    const int64_t t0 = static_cast<int64_t>(globaltimer_ns());
     while (!mbar_try_wait(bar, static_cast<uint32_t>(parity & 1))) {
         if (*err) return;
-        const int now = Beat ? *beat : 0;
-        if (now != heard) {
-            heard = now;
-            t0 = globaltimer_ns();
-        } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            *err = 1;
-        }
+        const int64_t since = Beat ? max(t0, *beat) : t0;
+        if (static_cast<int64_t>(globaltimer_ns()) - since > static_cast<int64_t>(kWaitLimitNs)) *err = 1;
     }
 }
 __device__ __forceinline__ void rw_tma3(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
@@ -211,11 +205,11 @@ __device__ __forceinline__ RwTiles rw_tiles(int pmin, int pmax, int window, int 
 // Rows row0 .. row1 - 1 of the unit without matrix products, for the tiles i0 .. i1
 // - 1: warp `warp` of `warps`, a row at a time, 4 positions at once (8 would cost the
 // f32 kernel, which keeps its registers over the call, 130 bytes of spills). dst: the
-// part, or null for the output. *beat grows with every tile of a row (the other
-// roles' waits go on as long as it does).
+// part, or null for the output. *beat is the time of the last tile of a row (the
+// other roles' waits count from it).
 template <typename T, int HD>
 __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwTiles &t, int i0, int i1, int g, int row0, int row1,
-                                     int warp, int warps, float off, float *dst, int *beat) {
+                                     int warp, int warps, float off, float *dst, volatile int64_t *beat) {
     constexpr int E = HD / 32, N = 4;
     const int lane = threadIdx.x & 31;
     const KvPagedAttnArgs &a = r.a;
@@ -242,7 +236,7 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
             }
         };
         for (int i = i0; i < i1; ++i) {
-            if (lane == 0) atomicAdd(beat, 1);
+            if (lane == 0) *beat = static_cast<int64_t>(globaltimer_ns());
             const int end = min(t.key(i) + kRwKeys - 1, p);
             int page = -1;
 #pragma unroll 1
@@ -347,7 +341,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     extern __shared__ uint8_t rw_smem[];
     __shared__ uint64_t b_full[ST], b_empty[ST], b_s[2], b_p[2][Z::parts], b_o[2], b_q, b_q_free, b_end;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_err, s_beat, s_bad[2][3];
+    __shared__ int64_t s_beat;
+    __shared__ int s_err, s_bad[2][3];
     __shared__ float s_c[kRwRows];
     const KvPagedAttnArgs &a = r.a;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -369,7 +364,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         mbar_init(&b_q_free, 1);
         mbar_init(&b_end, 1);
         fence_mbar_init();
-        s_err = s_beat = 0;
+        s_err = 0;
+        s_beat = 0;
     }
     if (warp == 9) {   // (nothing else holds tensor memory here: no two of these CTAs fit an SM)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
@@ -387,7 +383,10 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     const float c0 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
     const uint32_t ring = base + 2 * Z::tile;
     volatile int *err = &s_err;
-    auto wait = [&](uint64_t *bar, int parity) { rw_wait<true>(bar, parity, err, &s_beat); };
+    auto wait = [&](uint64_t *bar, int parity) { rw_wait<false>(bar, parity, err, &s_beat); };
+    // for what a warpgroup without matrix products may hold up: in f16 its P, and with it the other one; in f32, where both go
+    // that way together, the next Q; the ring's places
+    auto wait_long = [&](uint64_t *bar, int parity) { rw_wait<true>(bar, parity, err, &s_beat); };
     RwCut *const cuts = reinterpret_cast<RwCut *>(r.ws);
     // Item k of this CTA: the items (parts of units, long ones first) go to the CTAs to and fro, so that the lengths
     // add up to about the same. Every role walks through them by itself; false behind the last one.
@@ -432,12 +431,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             const int shift = min(a.c.shift, 7), boxes = kRwKeys >> shift;
             const uint32_t bytes = static_cast<uint32_t>(HD * 2) << shift;
             int done = 0, nq = 0;   // fills, and Qs, of the items before
-            int last = -1;          // this warp's last fill
             bool ok = true;
             for (int k = 0; ok && item(k, f, it); ++k) {
                 if (it.NT == 0) continue;
                 if (!Z::split && turn == 0) {
-                    if (nq > 0) wait(&b_q_free, nq - 1);
+                    if (nq > 0) wait_long(&b_q_free, nq - 1);
                     if (__any_sync(0xffffffffu, *err != 0)) {
                         ok = false;
                         break;
@@ -462,13 +460,12 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                     fill(n, it.NT, i, v);
                     const int j = it.tiles.key(it.i0 + i) + (lane << shift);
                     const int page = lane < boxes && j <= it.pmax ? kv_page(a.b, a.c, it.u.seq, j) : -1;
-                    if (all >= ST) wait(&b_empty[st], all / ST - 1);
+                    if (all >= ST) wait_long(&b_empty[st], all / ST - 1);
                     if (__any_sync(0xffffffffu, *err != 0)) {
                         ok = false;
                         break;
                     }
                     const int held = __popc(__ballot_sync(0xffffffffu, page >= 0));
-                    last = all;
                     if (lane == 0) mbar_arrive_expect_tx(&b_full[st], held * bytes);
                     __syncwarp();
                     if (page >= 0) {
@@ -493,11 +490,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             // the CTA may end when every copy has landed, and every stage has been released
             if (ok) {
                 for (int n = max(0, done - ST); n < done; ++n)
-                    if (n % 3 == turn) wait(&b_empty[n % ST], n / ST);
-            }
-            if (__any_sync(0xffffffffu, *err != 0)) {   // (given up, here or elsewhere: then for a second at most to a copy)
-                for (int n = last; n >= 0 && n > last - 3 * ST; n -= 3) (void)mbar_wait_bounded(&b_full[n % ST], n / ST & 1);
-                if (nq > 0) (void)mbar_wait_bounded(&b_q, nq - 1 & 1);
+                    if (n % 3 == turn) wait_long(&b_empty[n % ST], n / ST);
             }
         } else {
             // ---- products: the whole warp walks along, one lane issues
@@ -531,7 +524,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 const uint32_t v = ring16 + st * (Z::tile >> 4), p = tm + s * 128;
 #pragma unroll
                 for (int k = 0; k < Z::parts; ++k) {   // as the parts of P come
-                    wait(&b_p[s][k], np[s]);
+                    rw_wait<!Z::split>(&b_p[s][k], np[s], err, &s_beat);
                     rw_after();
                     if (one) {
 #pragma unroll
@@ -554,7 +547,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 const int NT = it.NT;
                 if (NT == 0) continue;
                 if (*err) break;
-                wait(&b_q, nq++);
+                rw_wait<Z::split>(&b_q, nq++, err, &s_beat);
                 if constexpr (!Z::split) {
                     const int two = it.tokens > r.TT ? 2 : 1;
                     for (int s = 0; s < two; ++s) qk(s, 0);
@@ -598,7 +591,6 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         const uint32_t tS = tmem + lanes + s * 128, tO = tmem + lanes + 256 + s * HD;
         constexpr float kOff = Z::split ? kRwOff32 : kRwOff16;
         constexpr int kStep = Z::split ? 2 : 1;
-        // (f32: the warpgroups go the long way together, and what they wait for is not each other)
         auto wait = [&](uint64_t *bar, int parity) { rw_wait<!Z::split>(bar, parity, err, &s_beat); };
         RwFind f;
         RwItem it;
@@ -1015,9 +1007,14 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     }
     __syncthreads();
     if (tid == 0 && s_err) record_status(a.status, QW3_ERR_TIMEOUT);
-    if (warp == 9 && s_err) {   // products that nobody has waited for end before their memory is given back
-        if (rw_elect()) rw_commit(&b_end);
-        (void)mbar_wait_bounded(&b_end, 0);
+    if (s_err) {   // given up: copies and products that nobody has waited for end first (both parities: no phase is open then, or a second is over)
+        if (warp == 9 && rw_elect()) rw_commit(&b_end);
+        if (tid < ST + 2) {
+            uint64_t *const bar = tid < ST ? &b_full[tid] : tid == ST ? &b_q : &b_end;
+            (void)mbar_wait_bounded(bar, 0);
+            if (tid <= ST) (void)mbar_wait_bounded(bar, 1);
+        }
+        __syncthreads();
     }
     rw_after();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
