@@ -592,6 +592,10 @@ QW3_API int64_t qw3_kv_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t 
  *     out = sum_j softmax_j(scale * q . K[j]) V[j].
  * A row that attends to nothing (p < 0 among them) is zeros. Nothing that a row
  * does not attend to has a part in it, be it NaN or infinite.
+ * An infinite value that a row attends to comes out as infinite (opposite ones, and
+ * one whose weight is below 2^-30 of the row's largest, may be NaN). The keys that a
+ * row attends to have to be finite, as qw3_kv_paged_append leaves them: a row that
+ * attends to one that is not has no answer (NaN, or any value).
  * Row counts and lengths are read on the device, and taken as at most max_rows
  * (a sequence's rows past it are left as they were) and max_len (at most
  * pages_per_seq * page_size; QW3_ERR_KV_OVERFLOW), which decide how the work is

@@ -26,7 +26,8 @@
 // What a row does not see must not reach it, and 0 * NaN would: in a tile that
 // is not seen whole, V rows that no row of the unit sees are set to zero, and if
 // one that only some rows see is not finite the unit is done again without
-// matrix products (rw_slow).
+// matrix products (rw_slow); in f32 also where one that is seen has made a NaN of
+// two infinite parts.
 //
 // CTAs stay and take the units to and fro, longest first; the next unit's Q comes
 // by TMA while the last one's rows go out by TMA. Few units are split along the
@@ -937,6 +938,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) master[d + e] += __uint_as_float(o[e]);
                     }
+                    // an infinite value times a weight's low part, which is 0 or of either sign, is NaN: the unit is done again
+                    bool nan = false;
+#pragma unroll
+                    for (int d = 0; d < HD; ++d) nan |= master[d] != master[d];
+                    if (nan && l == l) *bad_flag = 1;
                 }
                 // The warpgroups' parts join in Q's place: each leaves half of its dimensions to the other, and adds its
                 // other half to what it finds. (Behind the barrier: with one tile the second has waited for nothing, and

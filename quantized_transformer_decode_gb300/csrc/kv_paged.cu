@@ -689,8 +689,12 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1) k_paged_tokens(const KvPage
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    o[(((n >> 3) * 2 + e) * 8 + (n & 7)) * 4] = Z::split ? acc[n][e] + acc[n][2 + e] : acc[n][2 * h + e];
+                for (int e = 0; e < 2; ++e) {
+                    float v = acc[n][Z::split ? e : 2 * h + e];
+                    // (an infinite value: the weights' low parts are 0 or of either sign, and would make it NaN)
+                    if constexpr (Z::split) v = fabsf(v) == INFINITY ? v : v + acc[n][2 + e];
+                    o[(((n >> 3) * 2 + e) * 8 + (n & 7)) * 4] = v;
+                }
             __syncthreads();
             const int here = min(8, t.s.cols - col0 - 8 * h);
             for (int n = tid; n < here * HD; n += kTokWarps * 32) {

@@ -343,6 +343,35 @@ def test_what_is_not_seen_has_no_part(torch, seqs, dtype):
                 assert (np.abs(got[i, h] - want[i, h]) <= lim[i, h]).all()
 
 
+def check_infinities(b, got, **kw):
+    """Infinite values come out as they are, opposite ones as NaN, and the other outputs within their bound."""
+    want, err, written = ref.attend(b.q, b.data.astype(np.float64), b.starts, b.lens, b.table, **kw)
+    got = got.cpu().numpy().astype(np.float64)
+    assert np.array_equal(np.isnan(got[written]), np.isnan(want[written]))
+    inf = np.isinf(want) & written[:, None, None]
+    assert np.array_equal(got[inf], want[inf])
+    fine = np.isfinite(want) & written[:, None, None]
+    want = np.where(fine, want, 0)
+    assert (np.abs(got - want)[fine] <= ref.bound(err, want, b.hd, b.f16)[fine]).all()
+    return inf.any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("seqs", [[(1, 200), (1, 90)], [(6, 200), (3, 90)], [(150, 200), (40, 90)], [(1, 3000), (2, 70)],
+                                  [(100, 2500)], [(300, 400), (1, 900)]])
+def test_infinities_that_are_seen(torch, seqs, dtype):
+    """In values that every row sees and in ones that some rows see, in units that are split and in whole ones, in place too."""
+    b = Batch(torch, seqs, dtype=dtype, nh=4, nkv=2, hd=64, seed=11)
+    b.q *= b.np_type(0.25)      # (no weight below 2^-30 of its row's largest)
+    for i, (rows, n) in enumerate(seqs):
+        for p, d, bad in ((3, 5, np.inf), (3, 6, -np.inf), (17, 7, np.inf), (n - rows // 2 - 1, 7, -np.inf), (n - 1, 9, np.inf)):
+            b.data[b.table[i, p // 16], 1, i % 2, p % 16, d] = bad
+    assert check_infinities(b, b.attend())
+    check_infinities(b, b.attend(window=60, sinks=4), window=60, sinks=4)
+    q = b.dev(b.q)
+    check_infinities(b, b.attend(q=q, out=q))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 def test_long_rows_beside_what_is_not_finite(torch, dtype):
     """Rows that are done without matrix products, for longer than a wait in the kernel may last that nothing ends: no
