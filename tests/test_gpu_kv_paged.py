@@ -682,6 +682,30 @@ def test_refusals(torch):
     b.check(c.attention(q, starts, lens, table))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("seqs", [[(1, 3000)], [(100, 6000)], [(100, 3000), (1, 2500)]])
+def test_workspaces_of_the_exact_size(torch, seqs, dtype):
+    """What is too small by a byte, or missing, is refused; what lies behind the workspace stays as it was."""
+    from quantized_transformer_decode_gb300 import qw3
+    b = Batch(torch, seqs, nh=4, nkv=2, hd=64, dtype=dtype)
+    rows, n = max(r for r, _ in seqs), max(n for _, n in seqs)
+    need = qw3.qw3_kv_paged_attn_workspace_bytes(len(seqs), b.M, int(b.f16), 4, 2, 64, rows, n)
+    assert need > 16
+    room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    kw = dict(max_rows=rows, max_len=n)
+    b.check(b.attend(workspace=room[:need], **kw))
+    assert (room[need:] == 0xA5).all()
+    q, out = b.dev(b.q), torch.full((b.M, 4, 64), 9.0, dtype=b.dtype, device="cuda")
+    with pytest.raises(qw3.Qw3Error):
+        b.attend(q=q, out=out, workspace=room[:need - 1], **kw)
+    c, (starts, lens, table) = b.cache(), b.where()
+    batch = qw3.Qw3KvBatch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], len(seqs), table.shape[1])
+    with pytest.raises(qw3.Qw3Error):
+        qw3.qw3_kv_paged_attn(c.c, batch, int(b.f16), q.data_ptr(), b.M, 256, 4, rows, n, 0, 0, 0.125, out.data_ptr(), 256, 0, need,
+                              0, torch.cuda.current_stream().cuda_stream)
+    assert (out == 9).all()
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
