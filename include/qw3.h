@@ -575,8 +575,8 @@ QW3_API int qw3_kv_paged_append(const qw3_kv_paged *cache, const qw3_kv_batch *b
                                 int32_t rope_len, void *q_out_dev, int64_t q_stride, int32_t *status_dev,
                                 void *stream);
 
-/* Workspace bytes of qw3_kv_paged_attn for these sizes (may be 0), or -1 if one
- * of them cannot be taken. */
+/* Workspace bytes of qw3_kv_paged_attn for these sizes (may be 0) on the current
+ * device, which has to be the call's, or -1 if one of them cannot be taken. */
 QW3_API int64_t qw3_kv_paged_attn_workspace_bytes(int32_t B, int32_t M, int32_t type, int32_t n_heads,
                                                   int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
                                                   int32_t max_len, int32_t window, int32_t sinks);

@@ -682,7 +682,12 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stat
 
 
 _kv_paged_bytes = functools.lru_cache(maxsize=256)(qw3_kv_paged_bytes)
-_kv_paged_attn_workspace_bytes = functools.lru_cache(maxsize=1024)(qw3_kv_paged_attn_workspace_bytes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_paged_attn_workspace_bytes(device: int, *sizes: int) -> int:
+    """The bytes on the current device, `device` (they go by its number of SMs)."""
+    return qw3_kv_paged_attn_workspace_bytes(*sizes)
 
 
 class KVCachePaged:
@@ -808,8 +813,8 @@ class KVCachePaged:
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
-            need = _kv_paged_attn_workspace_bytes(batch.B, M, kind, n_heads, self.n_kv_heads, hd, max_rows, max_len, window,
-                                                  sinks)
+            need = _kv_paged_attn_workspace_bytes(self.index, batch.B, M, kind, n_heads, self.n_kv_heads, hd, max_rows,
+                                                  max_len, window, sinks)
             if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         else:

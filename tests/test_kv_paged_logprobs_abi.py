@@ -150,3 +150,34 @@ def test_logprob_refusals(L, kw, want):
 
 def test_logprobs_of_no_rows(L):
     assert logprobs(L, B=0, x=None, tokens=None, lp=None, ids=None, alts=None) == OK
+
+
+def test_workspaces_go_by_the_device(monkeypatch):
+    """A call's workspace has the size that its own device asks for, whatever another one asked for before."""
+    torch = pytest.importorskip("torch")
+    needs, got, current = {0: 4096, 1: 8192}, [], [0]
+
+    class Lib:      # a library that sees two devices
+        def qw3_kv_paged_attn_workspace_bytes(self, *sizes):
+            return needs[current[0]]
+
+        def qw3_kv_paged_attn(self, *args):
+            got.append((args[14], args[15]))
+            return OK
+
+    class On(torch.Tensor):      # host tensors that say they lie on the current device
+        def get_device(self):
+            return current[0]
+
+    monkeypatch.setattr(qw3, "lib", Lib)
+    monkeypatch.setattr(qw3, "_elsewhere", lambda torch, index: False)
+    monkeypatch.setattr(qw3, "_stream_on", lambda torch, index: 0)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32).as_subclass(On)  # noqa: E731
+    for device in (0, 1, 0):
+        current[0] = device
+        c = object.__new__(qw3.KVCachePaged)
+        c.data, c.device, c.index = None, torch.device("cpu"), device
+        c.n_pages, c.page_size, c.n_kv_heads, c.head_dim = 10, 16, 2, 64
+        c.c = cache()
+        c.attention(torch.zeros(3, 4, 64).as_subclass(On), ints(0, 3), ints(9), ints(1).view(1, 1))
+        assert got[-1][0] and got[-1][1] == needs[device]
