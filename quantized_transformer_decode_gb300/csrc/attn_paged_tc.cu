@@ -508,13 +508,15 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 rw_after();
                 const uint32_t k = ring16 + st * (Z::tile >> 4), q = base16 + (QT == 2 ? s * (Z::tile >> 4) : 0);
                 if (one) {
+                    // f32: the low parts first, whose sums are small, so that half as many steps are truncated beside large ones
+                    constexpr int parts = Z::split ? 2 : 1;
 #pragma unroll
-                    for (int h = 0; h < (Z::split ? 2 : 1); ++h)
+                    for (int h = parts - 1; h >= 0; --h)
 #pragma unroll
                         for (int e = 0; e < HD / 16; ++e) {
                             const uint32_t at = (e >> 2) * (kRwRows * 128 >> 4) + (e & 3) * 2;
                             rw_mma_ss(tm + s * 128, rw_desc(q + h * (Z::tile >> 4) + at, 16), rw_desc(k + at, 16),
-                                      rw_idesc(kRwKeys, false), h + e > 0);
+                                      rw_idesc(kRwKeys, false), e > 0 || h < parts - 1);
                         }
                     rw_commit(&b_s[s]);
                 }
@@ -529,14 +531,15 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                     rw_after();
                     if (one) {
 #pragma unroll
-                        for (int ee = 0; ee < Z::part_keys / 16; ++ee) {
-                            const int e = k * (Z::part_keys / 16) + ee;
-                            const uint64_t d = rw_desc(v + e * (2048 >> 4), kRwKeys * 128);
-                            // P: f16 [64 columns]; f32: hi and lo of 32 keys next to each other, 16 columns each
-                            const uint32_t at = p + (Z::split ? (e >> 1) * 32 + (e & 1) * 8 : e * 8);
-                            rw_mma_ts(tm + 256 + s * HD, at, d, rw_idesc(HD, true), add || e > 0);
-                            if constexpr (Z::split) rw_mma_ts(tm + 256 + s * HD, at + 16, d, rw_idesc(HD, true), true);
-                        }
+                        for (int lo = Z::split ? 1 : 0; lo >= 0; --lo)
+#pragma unroll
+                            for (int ee = 0; ee < Z::part_keys / 16; ++ee) {
+                                const int e = k * (Z::part_keys / 16) + ee;
+                                // P: f16 [64 columns]; f32: hi and lo of 32 keys next to each other, 16 columns each (low parts first here too)
+                                const uint32_t at = p + (Z::split ? (e >> 1) * 32 + (e & 1) * 8 + lo * 16 : e * 8);
+                                rw_mma_ts(tm + 256 + s * HD, at, rw_desc(v + e * (2048 >> 4), kRwKeys * 128), rw_idesc(HD, true),
+                                          add || e > 0 || (Z::split && lo == 0));
+                            }
                     }
                 }
                 ++np[s];

@@ -283,6 +283,30 @@ def test_long_contexts(torch, dtype):
         b.check(b.attend(**kw), **kw)
 
 
+@pytest.mark.parametrize("seqs,kw", [([(404, 1831)], {}), ([(31, 1799), (90, 800)], dict(window=172)), ([(253, 2197)], dict(window=1148, sinks=3)),
+                                     ([(290, 837)], {})])
+@pytest.mark.parametrize("nh,nkv,hd", [(16, 8, 128), (8, 4, 64)])
+def test_as_exact_as_products_in_32_bits(torch, seqs, kw, nh, nkv, hd):
+    """f32 activations, many rows: no farther from 64 bits than matrix products, exponentials and sums in f32 are. (A score's sum
+    is truncated at each of hd / 16 steps, half a step of f32 on average and always downwards, where f32 rounds hd times, to
+    nearest: for 64 and 128 both come to 2 to 4 half steps. A quarter is left for where the two fall together.)"""
+    b = Batch(torch, seqs, nh=nh, nkv=nkv, hd=hd, page=32, seed=21)
+    got = b.attend(**kw).cpu().numpy().astype(np.float64)
+    want, _, _ = ref.attend(b.q, b.data.astype(np.float64), b.starts, b.lens, b.table, **kw)
+    plain = np.zeros_like(want)
+    for i, (rows, n) in enumerate(seqs):
+        a, j = int(b.starts[i]), np.arange(n)
+        k, v = (b.dev(b.data[b.table[i, j // 32], s, :, j % 32]).float().repeat_interleave(nh // nkv, 1) for s in (0, 1))
+        p = n - rows + np.arange(rows)[:, None]
+        sees = b.dev((j <= p) & ((j > p - kw.get("window", n)) | (j < kw.get("sinks", 0))))
+        s = torch.einsum("rhd,jhd->hrj", b.dev(b.q[a:a + rows]), k) * hd ** -0.5
+        s = torch.where(sees, s, -torch.inf)
+        e = torch.exp(s - s.amax(-1, keepdim=True))
+        plain[a:a + rows] = (torch.einsum("hrj,jhd->hrd", e, v) / e.sum(-1, keepdim=True)).transpose(0, 1).cpu().numpy()
+    off, of32 = np.linalg.norm(got - want), np.linalg.norm(plain - want)
+    assert off <= 1.25 * of32, (off / np.linalg.norm(want), of32 / np.linalg.norm(want))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 @pytest.mark.parametrize("seqs", [[(4, 2), (1, 0), (3, 0), (2, 20)], [(60, 20), (1, 40), (200, 100)]])
 def test_rows_that_see_nothing(torch, seqs, dtype):
