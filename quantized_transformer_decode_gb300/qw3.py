@@ -510,7 +510,7 @@ def _rows_of(t, name: str):
         raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a 2-d tensor with contiguous rows is wanted")
     rows, width = t.shape
     stride, step = t.stride()
-    if width > 1 and step != 1:
+    if rows and width > 1 and step != 1:     # (of no rows any strides will do)
         raise Qw3Error(QW3_ERR_INVALID_ARG, f"{name}: a 2-d tensor with contiguous rows is wanted")
     if rows > _INT32_MAX or width > _INT32_MAX:
         raise Qw3Error(QW3_ERR_SHAPE, f"{name}: more rows or columns than 31 bits count")

@@ -181,3 +181,13 @@ def test_workspaces_go_by_the_device(monkeypatch):
         c.c = cache()
         c.attention(torch.zeros(3, 4, 64).as_subclass(On), ints(0, 3), ints(9), ints(1).view(1, 1))
         assert got[-1][0] and got[-1][1] == needs[device]
+
+
+def test_no_rows_of_any_strides():
+    """A tensor of no rows has no strides to keep to (numpy's come with others than torch's)."""
+    torch = pytest.importorskip("torch")
+    for t in (torch.empty(0, 8), torch.empty_strided((0, 8), (1, 0)), torch.empty_strided((0, 8), (0, 3))):
+        rows, width, stride = qw3._rows_of(t, "t")
+        assert (rows, width) == (0, 8) and stride >= 8
+    with pytest.raises(qw3.Qw3Error):
+        qw3._rows_of(torch.empty(4, 16)[:, ::2], "t")
