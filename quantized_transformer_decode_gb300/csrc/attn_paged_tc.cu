@@ -16,12 +16,19 @@
 // while the tensor cores serve the other.
 //  * f16 activations: the warpgroups have a row tile each and share the key
 //    tiles. O stays in tensor memory; a row's reference maximum moves only when
-//    it is passed by 2^8, and the row is then rescaled in place. P is f16.
+//    it is passed by 2^8, and the row is then rescaled in place. P is rounded to
+//    f16, once (an operand of the product with V has V's type; what it adds, 2^-11
+//    of a weight at most, is less than what the output's own rounding to f16 does:
+//    2.6e-4 of 64 bits in all, 2.0e-4 with P in 32 bits). Sums of P are of the
+//    weights before it.
 //  * f32 activations: Q and P in two f16 parts (hi + lo), two products each. The
 //    warpgroups take alternate key tiles of the same rows, and each adds its
 //    tile's O to a master in registers (f32, round to nearest): the tensor core
 //    truncates its sums, a relative 1.6e-8 for every step of a chain, and a chain
-//    of one tile has 16. The two masters are joined at the end.
+//    of one tile has 16. The low parts' products come first, while the sum is small
+//    (the other way round outputs are twice as far from 64 bits: 1.2e-6 instead of
+//    0.57e-6 for 3 x 946 rows with a window of 1208). The two masters are joined at
+//    the end.
 //
 // What a row does not see must not reach it, and 0 * NaN would: in a tile that
 // is not seen whole, V rows that no row of the unit sees are set to zero, and if
@@ -36,8 +43,9 @@
 // Bound by the tensor cores, and nearly as much by shared memory, which holds both
 // operands of the first product and one of the second: a 128 x 128 x 16 product
 // takes 83 cycles (plain library products 79, the peak rate 64). A prompt of 4096
-// tokens with 32 query and 8 kv heads of 128, f16: 107 us, 1.28 PFLOP/s. 509 rows
-// behind 7680 positions, f32 (twice the products, 128 units on 152 SMs): 99 us.
+// tokens with 32 query and 8 kv heads of 128, f16: 105 us, 1.31 PFLOP/s; f32 (twice
+// the products): 222 us. 509 rows behind 7680 positions, f32 (128 units on 152 SMs):
+// 99 us.
 #include <algorithm>
 #include <cstdint>
 
@@ -508,7 +516,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 rw_after();
                 const uint32_t k = ring16 + st * (Z::tile >> 4), q = base16 + (QT == 2 ? s * (Z::tile >> 4) : 0);
                 if (one) {
-                    // f32: the low parts first, whose sums are small, so that half as many steps are truncated beside large ones
+                    // f32: the low parts first
                     constexpr int parts = Z::split ? 2 : 1;
 #pragma unroll
                     for (int h = parts - 1; h >= 0; --h)
@@ -1086,8 +1094,8 @@ __global__ void __launch_bounds__(128) k_paged_rows_join(const RwArgs r) {
     }
 }
 
-// How the units are launched and split: `units` CTAs of one part each (an upper
-// bound: starts are on the device), times `splits`.
+// How the units are launched and split: `units` (an upper bound: starts are on the
+// device) in `splits` parts each at most, which up to one CTA to an SM take in turn.
 struct RwPlan {
     int TT = 0, units = 0, splits = 1, split_tiles = 0;
     size_t bytes = 0;

@@ -73,7 +73,7 @@ __device__ __noinline__ void pg_norm_f64(const float (&x)[N], float eps, float (
 }
 
 // Bound by reads that wait for the ones before them: 4096 rows of 32/8 heads (186
-// MB) take 42 us, 0.65 of the copy rate; one row of 16/8 heads 2.6 us.
+// MB) take 41 us, 0.68 of the copy rate; one row of 16/8 heads 2.5 us.
 //
 // Warp w of a row's per_row takes passes w, w + per_row, .. (of 32 / L heads), NP at
 // most, whose loads are all issued before the row's place is looked up.
@@ -228,6 +228,9 @@ cudaError_t append_t(const KvPagedAppendArgs &a, bool pdl, cudaStream_t s) {
 // columns (f16), K is B as it lies (8 positions x 16 dimensions, the dimensions
 // in an order that gives a thread 16 contiguous bytes), and so is V after
 // setting pairs of positions side by side (one byte permutation to a register).
+// f16 activations: a weight is rounded to f16, once, as the product with V asks
+// (2^-11 of it at most beside the output's own rounding; sums are of the weights
+// before it).
 // tcgen05.mma has no part here: a tile of 128 rows would be filled by 2 to 16,
 // and reading K and V is what takes the time, not the products.
 //

@@ -22,9 +22,9 @@
 // is put in order by counting for each how many are before it. A list that
 // overflows raises the bound and the slice is read again.
 //
-// Bound by HBM for many rows (512 x 151936 is 311 MB, 46 us of copying: 51 us
-// without alternatives, 55 with one, 62 with 20), by latency for one (4.7 us
-// without, 14.4 with 20).
+// Bound by HBM for many rows (512 x 151936 is 311 MB, 46 us of copying: 50 us
+// without alternatives, 54 with one, 62 with 20), by latency for one (4.6 us
+// without, 11 with five, 14.4 with 20).
 #include <algorithm>
 #include <cstdint>
 
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LogprobArgs a,
 
 cudaError_t launch_logprobs(const LogprobArgs &a, int B, bool pdl, cudaStream_t s) {
     // a row's CTAs: as many as give each SM two, while a slice is worth a CTA. 512 rows of 151936 with 20
-    // alternatives take 61 us with one CTA to a row, 73 with two, 152 rows 38 and 31, 64 rows 28 with four, 25 with
+    // alternatives take 61 us with one CTA to a row, 78 with two, 152 rows 36 and 29, 64 rows 28 with four, 23 with
     // eight (what a row's end costs against SMs without work)
     int C = 1;
     while (C < kLpMaxCluster && static_cast<long long>(B) * C < 300 && a.V / C > 4 * kLpThreads * kLpChunk) C *= 2;

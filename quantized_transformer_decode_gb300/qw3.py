@@ -785,7 +785,10 @@ class KVCachePaged:
         a row sees its `window` newest positions and the sequence's first `sinks`.
         max_rows, max_len: upper bounds of a sequence's rows and length (M and
         what the table has pages for where they are not given); rows past
-        max_rows are not written, nor are those outside the batch. scale:
+        max_rows are not written, nor are those outside the batch. They decide
+        which kernels run and how the work is split: give them where they are
+        known (max_rows 1 in a step of single tokens; else one sequence may have
+        all the rows, and the kernel for prompts runs beside). scale:
         1 / sqrt(head_dim) where it is not given. out: where the result goes (q
         itself, or apart from it). workspace: a uint8 tensor to use in place of a
         new one."""
