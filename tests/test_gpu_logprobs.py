@@ -261,3 +261,35 @@ def test_ties_of_coarse_logits(torch, B, V):
     x = np.tile(np.arange(V) // 50 * 0.01, (B, 1)).astype(np.float32)
     x[:, -1] = x[:, -70]
     check(torch, x, tokens=np.full((B, 1), V - 1, np.int32), top=64)
+
+
+@pytest.mark.parametrize("B", [1, 512])
+def test_rows_that_rise_take_a_few_readings(torch, B):
+    """A row in which every logit is larger than the ones before overflows the list of alternatives: its slice is read once or
+    twice more, not until the list fits by itself. (Half a row rises: the list is full either way.)"""
+    from quantized_transformer_decode_gb300 import qw3
+    V = 151936
+    rising = torch.arange(V, device="cuda") * 1e-3
+    half = torch.cat((rising[:V // 2], -rising[V // 2:]))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    usual = torch.randn(V, generator=g, device="cuda") * 3
+    tokens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    took = []
+    for row in (usual, rising, half):
+        x = row.repeat(B, 1)
+        for top in (5, 64):
+            _, _, ids, _ = qw3.logprobs(x, tokens, top=top)
+            want = torch.sort(row, descending=True, stable=True).indices[:top].int()
+            assert (ids == want).all()
+        best = 1e9
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            qw3.logprobs(x, tokens, top=20)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        took.append(best)
+    # (three readings where one is usual, a place in the list asked for by every logit, and what a list of 2048 costs to put in
+    # order: 5 to 7 times as long; seventy readings are 300 times)
+    assert max(took[1:]) < 20 * took[0], took
