@@ -212,14 +212,17 @@ __device__ __forceinline__ RwTiles rw_tiles(int pmin, int pmax, int window, int 
 }
 
 // Rows row0 .. row1 - 1 of the unit without matrix products, for the tiles i0 .. i1
-// - 1: warp `warp` of `warps`, a row at a time, 4 positions at once (8 would cost the
-// f32 kernel, which keeps its registers over the call, 130 bytes of spills). dst: the
-// part, or null for the output. *beat is the time of the last tile of a row (the
-// other roles' waits count from it).
+// - 1: warp `warp` of `warps`, a row at a time. Scores: a lane to a position, which
+// reads its K row whole, 32 at once; outputs: a lane to E dimensions, 16 V rows on
+// their way. dst: the part, or null for the output. *beat is the time of the last tile
+// of a row (the other roles' waits count from it). Bound by the latency of its loads:
+// 509 rows behind 7680 positions, 32/8 heads, f32, every unit: 23 ms; 256 rows x 98
+// thousand positions 0.37 s (a position at a time, a lane to E dimensions for the
+// scores too: 4.5 times as long).
 template <typename T, int HD>
 __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwTiles &t, int i0, int i1, int g, int row0, int row1,
                                      int warp, int warps, float off, float *dst, volatile int64_t *beat) {
-    constexpr int E = HD / 32, N = 4;
+    constexpr int E = HD / 32;
     const int lane = threadIdx.x & 31;
     const KvPagedAttnArgs &a = r.a;
     for (int row = row0 + warp; row < row1; row += warps) {
@@ -228,60 +231,64 @@ __device__ __noinline__ void rw_slow(const RwArgs &r, const RwUnit &u, const RwT
         const int p = u.p0 + u.tok0 + tok;
         const size_t at = static_cast<size_t>(u.start + u.tok0 + tok);
         const T *q = static_cast<const T *>(a.q) + at * a.q_stride + static_cast<size_t>(h) * HD + lane * E;
-        float x[E], o[E], m = -INFINITY, l = 0.0f;
+        float x[E], o[E], m = -INFINITY, l = 0.0f;   // (l: of this lane's positions)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             x[e] = kv_f32(q[e]) * (a.scale * 1.4426950408889634f);   // (before the sum, which large queries would take out of f32)
             o[e] = 0.0f;
         }
-        auto halves = [](float (&y)[E], const __half *src) {   // E values, as one word or two
-            if constexpr (E == 4) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                const float2 f = rw_unpack(w.x), z = rw_unpack(w.y);
-                y[0] = f.x; y[1] = f.y; y[2] = z.x; y[3] = z.y;
-            } else {
-                const float2 f = rw_unpack(*reinterpret_cast<const uint32_t *>(src));
-                y[0] = f.x; y[1] = f.y;
-            }
-        };
         for (int i = i0; i < i1; ++i) {
             if (lane == 0) *beat = static_cast<int64_t>(globaltimer_ns());
             const int end = min(t.key(i) + kRwKeys - 1, p);
-            int page = -1;
 #pragma unroll 1
-            for (int j0 = t.key(i); j0 <= end; j0 += N) {
-                if (j0 % 16 == 0) page = kv_page(a.b, a.c, u.seq, j0);   // (16 positions lie in one)
-                if (page < 0) continue;
-                const __half *k = kv_paged_row<HD>(a.c, page, 0, g, j0) + lane * E, *v = kv_paged_row<HD>(a.c, page, 1, g, j0) + lane * E;
-                float d[N], mn = m;
+            for (int j0 = t.key(i); j0 <= end; j0 += 32) {
+                const int j = j0 + lane, page = j <= end ? kv_page(a.b, a.c, u.seq, j) : -1;
+                const bool sees = page >= 0 && kv_sees(p, j, a.window, a.sinks);
+                const uint32_t seen = __ballot_sync(0xffffffffu, sees);
+                if (seen == 0) continue;
+                const __half *k = kv_paged_row<HD>(a.c, max(page, 0), 0, g, j);
+                float d = 0.0f;
+#pragma unroll 4
+                for (int c = 0; c < HD; c += 8) {
+                    const uint4 y = sees ? *reinterpret_cast<const uint4 *>(k + c) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    float y[E];
-                    halves(y, k + n * HD);
-                    d[n] = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) d[n] = fmaf(x[e], y[e], d[n]);
-                    d[n] = warp_sum(d[n]);
-                    if (!kv_sees(p, j0 + n, a.window, a.sinks)) d[n] = -INFINITY;
-                    mn = d[n] > mn ? d[n] : mn;
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = rw_unpack(w[e]);
+                        d = fmaf(__shfl_sync(0xffffffffu, x[2 * e % E], (c + 2 * e) / E), f.x, d);
+                        d = fmaf(__shfl_sync(0xffffffffu, x[(2 * e + 1) % E], (c + 2 * e + 1) / E), f.y, d);
+                    }
                 }
-                const float c = m == mn ? 1.0f : rw_ex2(m - mn);
-                l *= c;
+                const float mn = fmaxf(m, warp_max(sees ? d : -INFINITY)), c = m == mn ? 1.0f : rw_ex2(m - mn);
+                const float w = sees ? rw_ex2(d - mn + off) : 0.0f;
+                m = mn;
+                l = fmaf(l, c, w);
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[e] *= c;
+#pragma unroll 1
+                for (int n0 = 0; n0 < 32; n0 += 16) {   // (16 positions lie in one page)
+                    const int pg = __shfl_sync(0xffffffffu, page, n0);
+                    if ((seen >> n0 & 0xffffu) == 0) continue;
+                    const __half *v = kv_paged_row<HD>(a.c, max(pg, 0), 1, g, j0 + n0) + lane * E;
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    float y[E];
-                    halves(y, v + n * HD);
-                    if (!kv_sees(p, j0 + n, a.window, a.sinks)) continue;   // (whatever y is)
-                    const float w = rw_ex2(d[n] - mn + off);
+                    for (int n = 0; n < 16; ++n) {
+                        float y[E];
+                        if constexpr (E == 4) {
+                            const uint2 b = *reinterpret_cast<const uint2 *>(v + n * HD);
+                            const float2 f = rw_unpack(b.x), s = rw_unpack(b.y);
+                            y[0] = f.x; y[1] = f.y; y[2] = s.x; y[3] = s.y;
+                        } else {
+                            const float2 f = rw_unpack(*reinterpret_cast<const uint32_t *>(v + n * HD));
+                            y[0] = f.x; y[1] = f.y;
+                        }
+                        const float wn = __shfl_sync(0xffffffffu, w, n0 + n);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = fmaf(w, y[e], o[e]);
-                    l += w;
+                        for (int e = 0; e < E; ++e) o[e] = seen >> (n0 + n) & 1 ? fmaf(wn, y[e], o[e]) : o[e];   // (whatever y is)
+                    }
                 }
-                m = mn;
             }
         }
+        l = warp_sum(l);
         if (dst) {
             float *to = dst + row % kRwRows;
 #pragma unroll

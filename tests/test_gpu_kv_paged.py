@@ -403,7 +403,7 @@ def test_long_rows_beside_what_is_not_finite(torch, dtype):
     1.6 s where the limit is 1 s.)"""
     from quantized_transformer_decode_gb300 import qw3
     f16 = dtype == "f16"
-    B, rows, nh, hd, page, pages = 304, 16 if f16 else 8, 16, 64, 256, 384 if f16 else 768
+    B, rows, nh, hd, page, pages = 304, 16 if f16 else 8, 16, 64, 256, 1728 if f16 else 3712
     n = pages * page - 7
     g = torch.Generator(device="cuda").manual_seed(1)
     data = torch.randn(pages, 2, 1, page, hd, generator=g, device="cuda").half()
